@@ -460,6 +460,159 @@ int pgg_unpermute_grad_apply(const void* permuted, const void* d_out, const void
                              pgg_dtype probs_grad_dtype, void* workspace, size_t workspace_bytes,
                              void* perm_grad, void* probs_grad, pgg_stream_t stream);
 
+/*
+ * ---------------------------------------------------------------------------
+ * Router: the top-k choice of experts from router logits, the routing weights,
+ * and the expanded order that the grouped products of this file read.
+ *
+ *     key[b, e]  = logits[b, e] + bias[e]        (bias takes part in the choice only)
+ *     experts[b] = the topK largest keys in decreasing order, the lowest index
+ *                  first among equals
+ *     s          = softmax(logits[b]) over all G experts, or sigmoid(logits[b])
+ *     probs[b,j] = scale * s[experts[b,j]], or with `renormalize`
+ *                  scale * s[experts[b,j]] / sum over the chosen of s
+ *     expandedRowIdx, groupList: the pairs p = b * topK + j sorted by
+ *                  (experts[b,j], p), in the rowIdxType form, and the experts' counts
+ *
+ *   logits   device, [batch, G] of `dtype`; -inf masks an expert (weight 0). A
+ *            token whose experts are all masked takes the lowest indices with
+ *            weights 0. A NaN key sorts below every other; a NaN or +inf logit
+ *            gives NaN weights, as IEEE arithmetic does; the order stays valid.
+ *   bias     device, fp32 [G], or NULL
+ *   G <= 1024, topK <= min(G, 32), else PGG_ERR_SHAPE
+ *   workspace at least pgg_route_workspace_size bytes, 256-byte aligned; the
+ *            status word at offset 0 is 0 after the call
+ *   probs    device, fp32 [batch, topK];  experts device, int64 [batch, topK]
+ *   expandedRowIdx device, int64 [batch * topK];  groupList device, int64 [G]
+ *
+ * Weights are computed in fp32; the order depends on no atomic's order.
+ */
+typedef enum { PGG_SCORE_SOFTMAX = 0, PGG_SCORE_SIGMOID = 1 } pgg_score;
+
+int pgg_route_workspace_size(int64_t batch, int64_t G, int64_t topK, size_t* workspace_bytes);
+
+int pgg_route_execute(const void* logits, const float* bias, int64_t batch, int64_t G,
+                      int64_t topK, int rowIdxType, pgg_dtype dtype, pgg_score score,
+                      int renormalize, float scale, void* workspace, size_t workspace_bytes,
+                      float* probs, int64_t* experts, int64_t* expandedRowIdx,
+                      int64_t* groupList, pgg_stream_t stream);
+
+/*
+ * Gradient of probs for the logits (bias gets none: the choice is piecewise
+ * constant). d_logits [batch, G] of `dtype` is written whole; needs no
+ * workspace. A token whose `experts` hold an index outside [0, G) or one
+ * twice gets NaN. Aliasing d_logits with logits is not allowed.
+ */
+int pgg_route_grad(const float* d_probs, const void* logits, const int64_t* experts,
+                   int64_t batch, int64_t G, int64_t topK, pgg_dtype dtype, pgg_score score,
+                   int renormalize, float scale, void* d_logits, pgg_stream_t stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * Gated expert product (the first half of an expert's feed-forward part):
+ *
+ *     [gate | up][i, :] = x[batch(i), :] weight[g(i), :, :]
+ *     h[i, f] = prob * silu(gate[i, f]) * up[i, f],  silu(t) = t / (1 + exp(-t))
+ *
+ * with prob = probs[original position of row i], or 1 when probs is NULL. The
+ * second half with the weighted combination of a token's experts is
+ * pgg_dx_execute(h, w_down [G, H, F]), whose output is [batch, H].
+ *
+ *   x        device, [batch, K] of `dtype`, original token order
+ *   weight   device, [G, K, 2F] of `dtype`: F gate columns, then F up columns
+ *   probs    device, fp32 [batch, topK], or NULL
+ *   expandedRowIdx, groupList, M, G, L, batch, topK, rowIdxType: as for
+ *            pgg_dx_execute
+ *   h        device, [M, F] of `dtype`, expanded order
+ *   gate_up  device, [M, 2F] of `dtype` (what pgg_swiglu_grad reads), or NULL
+ *   workspace at least pgg_swiglu_workspace_size bytes, 256-byte aligned; status
+ *            word at offset 0. When the routing is not valid both outputs are
+ *            zero-filled.
+ *
+ * Accumulation, activation and weight are fp32; each output is rounded once.
+ * Bitwise repeatable.
+ */
+int pgg_swiglu_workspace_size(int64_t M, int64_t F, int64_t K, int64_t G, int64_t L,
+                              int64_t batch, int64_t topK, int rowIdxType, pgg_dtype dtype,
+                              size_t* workspace_bytes);
+
+int pgg_swiglu_execute(const void* x, const void* weight, const int64_t* expandedRowIdx,
+                       const int64_t* groupList, const float* probs, int64_t M, int64_t F,
+                       int64_t K, int64_t G, int64_t L, int64_t batch, int64_t topK,
+                       int rowIdxType, pgg_dtype dtype, void* workspace, size_t workspace_bytes,
+                       void* h, void* gate_up, pgg_stream_t stream);
+
+/*
+ * Gradient of the gate, from d_h and the kept gate_up:
+ *
+ *     d_up = prob d_h silu(gate);  d_gate = prob d_h up silu'(gate)
+ *     d_probs[original position of i] = sum over f of d_h silu(gate) up
+ *     h = prob silu(gate) up
+ *
+ * d_gate_up [M, 2F] is the gradY of pgg_dx_execute and pgg_dw_execute with the
+ * gate's weight; h [M, F] that of pgg_dw_execute with the down projection's.
+ *   probs    fp32 [batch, topK] or NULL;  d_probs fp32 [batch, topK] or NULL
+ *            (not without probs: PGG_ERR_NULL);  h may be NULL
+ *   workspace pgg_swiglu_grad_workspace_size bytes, 256-byte aligned; status word
+ *            at offset 0 (an index that is not a permutation zero-fills the outputs)
+ */
+int pgg_swiglu_grad_workspace_size(int64_t M, int64_t batch, int64_t topK,
+                                   size_t* workspace_bytes);
+
+int pgg_swiglu_grad(const void* d_h, const void* gate_up, const float* probs,
+                    const int64_t* expandedRowIdx, int64_t M, int64_t F, int64_t batch,
+                    int64_t topK, int rowIdxType, pgg_dtype dtype, void* workspace,
+                    size_t workspace_bytes, void* d_gate_up, float* d_probs, void* h,
+                    pgg_stream_t stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * A shared projection with one low-rank adapter per token:
+ *
+ *     y[t, :] = x[t, :] weight + scale[ad] (x[t, :] a[ad]) b[ad]^T,  ad = adapter[t]
+ *
+ *   x        device, [T, K] of `dtype`;  weight device, [K, N] of `dtype`
+ *   a        device, [A, K, R] of `dtype`;  b device, [A, N, R] of `dtype` (the
+ *            rank is innermost in both); an adapter of a smaller rank is stored
+ *            with zero columns
+ *   adapter  device, int64 [T], -1 = no adapter; another value outside [0, A)
+ *            sets PGG_ERR_INDEX and zero-fills the outputs
+ *   scale    device, fp32 [A], or NULL (1)
+ *   A <= 1023, R <= 256, T < 2^30, else PGG_ERR_SHAPE
+ *   workspace at least pgg_adapters_workspace_size bytes, 256-byte aligned; status
+ *            word at offset 0
+ *   y        device, [T, N] of `dtype`
+ *
+ * Tokens may be in any order. What one adapter's weights hold (infinities, NaN)
+ * does not reach the tokens of another.
+ */
+int pgg_adapters_workspace_size(int64_t T, int64_t K, int64_t N, int64_t R, int64_t A,
+                                pgg_dtype dtype, size_t* workspace_bytes);
+
+int pgg_adapters_execute(const void* x, const void* weight, const void* a, const void* b,
+                         const int64_t* adapter, const float* scale, int64_t T, int64_t K,
+                         int64_t N, int64_t R, int64_t A, pgg_dtype dtype, void* workspace,
+                         size_t workspace_bytes, void* y, pgg_stream_t stream);
+
+/*
+ * Its gradient with the projection frozen:
+ *
+ *     v = scale (d_y b[ad]),  d_x = d_y weight^T + v a[ad]^T  [T, K], may be NULL
+ *     d_a[ad] = sum over its tokens of x^T v                  [A, K, R]
+ *     d_b[ad] = sum over its tokens of d_y^T (scale x a[ad])  [A, N, R]
+ *
+ * all of `dtype`; an adapter without tokens gets zeros. Sums are fp32; v and
+ * scale x a[ad] are rounded once to `dtype` before the second product.
+ */
+int pgg_adapters_grad_workspace_size(int64_t T, int64_t K, int64_t N, int64_t R, int64_t A,
+                                     pgg_dtype dtype, size_t* workspace_bytes);
+
+int pgg_adapters_grad(const void* d_y, const void* x, const void* weight, const void* a,
+                      const void* b, const int64_t* adapter, const float* scale, int64_t T,
+                      int64_t K, int64_t N, int64_t R, int64_t A, pgg_dtype dtype,
+                      void* workspace, size_t workspace_bytes, void* d_x, void* d_a, void* d_b,
+                      pgg_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

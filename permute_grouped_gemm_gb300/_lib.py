@@ -12,6 +12,7 @@ import threading
 from . import build as _build
 
 PGG_F32, PGG_F16, PGG_BF16 = 0, 1, 2
+PGG_SCORE_SOFTMAX, PGG_SCORE_SIGMOID = 0, 1
 
 STATUS = {
     0: "PGG_OK", 1: "PGG_ERR_NULL", 2: "PGG_ERR_SHAPE", 3: "PGG_ERR_ATTR", 4: "PGG_ERR_DTYPE",
@@ -93,6 +94,26 @@ def load(path: str | None = None):
                       "pgg_dx_grouped_gemm", "pgg_dx_route_prep", "pgg_dx_execute_static_scratch",
                       "pgg_dw_workspace_size", "pgg_dw_plan", "pgg_dw_execute",
                       "pgg_dw_grouped_gemm"):
+                getattr(lib, f).restype = ctypes.c_int
+            i64, f32 = ctypes.c_int64, ctypes.c_float
+            lib.pgg_route_workspace_size.argtypes = [i64] * 3 + [ctypes.POINTER(sz)]
+            lib.pgg_route_execute.argtypes = [vp, vp, i64, i64, i64, i32, i32, i32, i32, f32, vp,
+                                              sz, vp, vp, vp, vp, vp]
+            lib.pgg_route_grad.argtypes = [vp, vp, vp, i64, i64, i64, i32, i32, i32, f32, vp, vp]
+            lib.pgg_swiglu_workspace_size.argtypes = [*_SIZES, i32, i32, ctypes.POINTER(sz)]
+            lib.pgg_swiglu_execute.argtypes = [vp] * 5 + [*_SIZES, i32, i32, vp, sz, vp, vp, vp]
+            lib.pgg_swiglu_grad_workspace_size.argtypes = [i64] * 3 + [ctypes.POINTER(sz)]
+            lib.pgg_swiglu_grad.argtypes = [vp] * 4 + [i64] * 4 + [i32, i32, vp, sz, vp, vp, vp,
+                                                                   vp]
+            lib.pgg_adapters_workspace_size.argtypes = [i64] * 5 + [i32, ctypes.POINTER(sz)]
+            lib.pgg_adapters_execute.argtypes = [vp] * 6 + [i64] * 5 + [i32, vp, sz, vp, vp]
+            lib.pgg_adapters_grad_workspace_size.argtypes = [i64] * 5 + [i32, ctypes.POINTER(sz)]
+            lib.pgg_adapters_grad.argtypes = [vp] * 7 + [i64] * 5 + [i32, vp, sz, vp, vp, vp, vp]
+            for f in ("pgg_route_workspace_size", "pgg_route_execute", "pgg_route_grad",
+                      "pgg_swiglu_workspace_size", "pgg_swiglu_execute",
+                      "pgg_swiglu_grad_workspace_size", "pgg_swiglu_grad",
+                      "pgg_adapters_workspace_size", "pgg_adapters_execute",
+                      "pgg_adapters_grad_workspace_size", "pgg_adapters_grad"):
                 getattr(lib, f).restype = ctypes.c_int
             lib.pgg_status_string.argtypes = [ctypes.c_int]
             lib.pgg_status_string.restype = ctypes.c_char_p
@@ -257,6 +278,87 @@ def pgg_unpermute_grad_apply(permuted, d_out, probs, expandedRowIdx, M, H, batch
                                            expandedRowIdx, M, H, batch, topK, rowIdxType, dtype,
                                            probs_grad_dtype, workspace, workspace_bytes,
                                            perm_grad, probs_grad or None, stream)
+
+
+def pgg_route_workspace_size(batch, G, topK) -> int:
+    out = ctypes.c_size_t(0)
+    _check(load().pgg_route_workspace_size(batch, G, topK, ctypes.byref(out)),
+           "pgg_route_workspace_size")
+    return out.value
+
+
+def pgg_route_execute(logits, bias, batch, G, topK, rowIdxType, dtype, score, renormalize, scale,
+                      workspace, workspace_bytes, probs, experts, expandedRowIdx, groupList,
+                      stream) -> int:
+    """Raw call with integer device addresses (0 for an absent bias)."""
+    return load().pgg_route_execute(logits, bias or None, batch, G, topK, rowIdxType, dtype, score,
+                                    renormalize, scale, workspace, workspace_bytes, probs, experts,
+                                    expandedRowIdx, groupList, stream)
+
+
+def pgg_route_grad(d_probs, logits, experts, batch, G, topK, dtype, score, renormalize, scale,
+                   d_logits, stream) -> int:
+    return load().pgg_route_grad(d_probs, logits, experts, batch, G, topK, dtype, score,
+                                 renormalize, scale, d_logits, stream)
+
+
+def pgg_swiglu_workspace_size(M, F, K, G, L, batch, topK, rowIdxType, dtype) -> int:
+    out = ctypes.c_size_t(0)
+    _check(load().pgg_swiglu_workspace_size(M, F, K, G, L, batch, topK, rowIdxType, dtype,
+                                            ctypes.byref(out)), "pgg_swiglu_workspace_size")
+    return out.value
+
+
+def pgg_swiglu_execute(x, weight, expandedRowIdx, groupList, probs, M, F, K, G, L, batch, topK,
+                       rowIdxType, dtype, workspace, workspace_bytes, h, gate_up, stream) -> int:
+    """Raw call with integer device addresses (0 for absent probs or gate_up)."""
+    return load().pgg_swiglu_execute(x, weight, expandedRowIdx, groupList, probs or None, M, F, K,
+                                     G, L, batch, topK, rowIdxType, dtype, workspace,
+                                     workspace_bytes, h, gate_up or None, stream)
+
+
+def pgg_swiglu_grad_workspace_size(M, batch, topK) -> int:
+    out = ctypes.c_size_t(0)
+    _check(load().pgg_swiglu_grad_workspace_size(M, batch, topK, ctypes.byref(out)),
+           "pgg_swiglu_grad_workspace_size")
+    return out.value
+
+
+def pgg_swiglu_grad(d_h, gate_up, probs, expandedRowIdx, M, F, batch, topK, rowIdxType, dtype,
+                    workspace, workspace_bytes, d_gate_up, d_probs, h, stream) -> int:
+    """Raw call with integer device addresses (0 for absent probs, d_probs or h)."""
+    return load().pgg_swiglu_grad(d_h, gate_up, probs or None, expandedRowIdx, M, F, batch, topK,
+                                  rowIdxType, dtype, workspace, workspace_bytes, d_gate_up,
+                                  d_probs or None, h or None, stream)
+
+
+def pgg_adapters_workspace_size(T, K, N, R, A, dtype) -> int:
+    out = ctypes.c_size_t(0)
+    _check(load().pgg_adapters_workspace_size(T, K, N, R, A, dtype, ctypes.byref(out)),
+           "pgg_adapters_workspace_size")
+    return out.value
+
+
+def pgg_adapters_execute(x, weight, a, b, adapter, scale, T, K, N, R, A, dtype, workspace,
+                         workspace_bytes, y, stream) -> int:
+    """Raw call with integer device addresses (0 for an absent scale)."""
+    return load().pgg_adapters_execute(x, weight, a, b, adapter, scale or None, T, K, N, R, A,
+                                       dtype, workspace, workspace_bytes, y, stream)
+
+
+def pgg_adapters_grad_workspace_size(T, K, N, R, A, dtype) -> int:
+    out = ctypes.c_size_t(0)
+    _check(load().pgg_adapters_grad_workspace_size(T, K, N, R, A, dtype, ctypes.byref(out)),
+           "pgg_adapters_grad_workspace_size")
+    return out.value
+
+
+def pgg_adapters_grad(d_y, x, weight, a, b, adapter, scale, T, K, N, R, A, dtype, workspace,
+                      workspace_bytes, d_x, d_a, d_b, stream) -> int:
+    """Raw call with integer device addresses (0 for an absent scale or d_x)."""
+    return load().pgg_adapters_grad(d_y, x, weight, a, b, adapter, scale or None, T, K, N, R, A,
+                                    dtype, workspace, workspace_bytes, d_x or None, d_a, d_b,
+                                    stream)
 
 
 def pgg_status_string(code: int) -> str:

@@ -1,0 +1,500 @@
+// C ABI of the router, the gated product and the adapters (include/pgg.h):
+// argument validation, workspace layouts, the choice of kernel and the launches.
+
+#include <cstdint>
+#include <cstring>
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "pgg.h"
+#include "pgg_internal.h"
+#include "pgg_ops.h"
+
+namespace pgg {
+namespace {
+
+constexpr int64_t kInt32Max = 2147483647;
+constexpr int kVariantSimt = 3;
+
+size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
+bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+bool known_dtype(int d) { return d == PGG_F32 || d == PGG_F16 || d == PGG_BF16; }
+int64_t elem_size(int d) { return d == PGG_F32 ? 4 : 2; }
+int status_of(cudaError_t e) { return e == cudaSuccess ? PGG_OK : PGG_ERR_CUDA; }
+
+// Takes pieces of a workspace, each aligned to 256 bytes.
+struct Carver {
+  size_t used = 0;
+  size_t take(int64_t bytes) {
+    const size_t at = used;
+    used = align_up(used + static_cast<size_t>(bytes), 256);
+    return at;
+  }
+};
+
+// ---------------------------------------------------------------- router
+
+int check_route(int64_t batch, int64_t G, int64_t topK) {
+  if (batch <= 0 || topK <= 0) return PGG_ERR_ATTR;
+  if (G <= 0 || G > kMaxRouteExperts || topK > G || topK > kMaxRouteTopK) return PGG_ERR_SHAPE;
+  if (batch > kInt32Max / topK) return PGG_ERR_SHAPE;
+  return PGG_OK;
+}
+
+size_t route_workspace(int64_t batch, int64_t G, int64_t topK) {
+  int blocks, per;
+  route_blocks(batch, G, topK, &blocks, &per);
+  return 256 + align_up(static_cast<size_t>(G) * static_cast<size_t>(blocks) * 4, 256);
+}
+
+// ---------------------------------------------------------------- gated product
+
+struct GatedPlan {
+  int variant;
+  int rows_per_block;
+  int64_t max_row_blocks;
+  size_t rblist, rowinfo, inv, total;
+};
+
+int check_gated(int64_t M, int64_t F, int64_t K, int64_t G, int64_t L, int64_t batch,
+                int64_t topK, int rowIdxType, int dtype) {
+  if (!known_dtype(dtype)) return PGG_ERR_DTYPE;
+  if (batch <= 0 || topK <= 0 || (rowIdxType != 0 && rowIdxType != 1)) return PGG_ERR_ATTR;
+  if (M <= 0 || F <= 0 || K <= 0 || G <= 0) return PGG_ERR_SHAPE;
+  if (M > kInt32Max || F > kInt32Max / 2 || K > kInt32Max || G > kInt32Max) return PGG_ERR_SHAPE;
+  if (L != M || batch > M || topK > M || batch * topK != M) return PGG_ERR_SHAPE;
+  return PGG_OK;
+}
+
+int gated_plan(int64_t M, int64_t F, int64_t G, GatedPlan* p) {
+  p->variant = kVariantSimt;
+  p->rows_per_block = 64;
+  p->max_row_blocks = (M + p->rows_per_block - 1) / p->rows_per_block + (G < M ? G : M);
+  if (p->max_row_blocks * ((F + 63) / 64) > kInt32Max) return PGG_ERR_SHAPE;  // 32-bit tile numbers
+  Carver c;
+  c.take(sizeof(WsHeader));
+  p->rblist = c.take(static_cast<int64_t>(sizeof(int4)) * p->max_row_blocks);
+  p->rowinfo = c.take(static_cast<int64_t>(sizeof(RowInfo)) * M);
+  p->inv = c.take(4 * M);
+  p->total = c.used;
+  return PGG_OK;
+}
+
+// ---------------------------------------------------------------- adapters
+
+struct AdapterPlan {
+  int variant;
+  int rb;        // rows per low-rank row block
+  int padded;
+  int64_t max_row_blocks, rows_u;
+  int blocks, tokens_per_block;
+  size_t off, order, padrow, rblist, segs, blkseg, counts, u, v, total;
+};
+
+int check_adapters(int64_t T, int64_t K, int64_t N, int64_t R, int64_t A, int dtype) {
+  if (!known_dtype(dtype)) return PGG_ERR_DTYPE;
+  if (T <= 0) return PGG_ERR_ATTR;
+  if (K <= 0 || N <= 0 || R <= 0 || A <= 0) return PGG_ERR_SHAPE;
+  if (R > kMaxRank || A > kMaxAdapters) return PGG_ERR_SHAPE;
+  if (T > kInt32Max / 2 || K > kInt32Max || N > kInt32Max) return PGG_ERR_SHAPE;
+  return PGG_OK;
+}
+
+int adapter_plan(int64_t T, int64_t K, int64_t N, int64_t R, int64_t A, int dtype, bool grad,
+                 AdapterPlan* p) {
+  p->variant = kVariantSimt;
+  p->rb = 64;
+  p->padded = grad ? 1 : 0;
+  const int64_t groups = A + 1 < T ? A + 1 : T;
+  p->max_row_blocks = (T + p->rb - 1) / p->rb + groups;
+  p->rows_u = grad ? T + 63 * groups : T;
+  const int64_t widest = N > K ? N : K;
+  if (p->max_row_blocks * ((widest + 63) / 64) > kInt32Max) return PGG_ERR_SHAPE;
+  adapter_blocks(T, &p->blocks, &p->tokens_per_block);
+  Carver c;
+  c.take(sizeof(WsHeader));
+  p->off = c.take(8 * (A + 2));
+  p->order = c.take(static_cast<int64_t>(sizeof(RowInfo)) * T);
+  p->padrow = c.take(grad ? static_cast<int64_t>(sizeof(RowInfo)) * p->rows_u : 0);
+  p->rblist = c.take(static_cast<int64_t>(sizeof(int4)) * p->max_row_blocks);
+  p->segs = c.take(static_cast<int64_t>(sizeof(int4)) * A);
+  p->blkseg = c.take(static_cast<int64_t>(sizeof(int2)) * ((T + 255) / 256));
+  p->counts = c.take(p->blocks > 1 ? 4 * (A + 1) * (p->blocks + 2) : 0);
+  p->u = c.take(p->rows_u * R * elem_size(dtype));
+  p->v = c.take(grad ? p->rows_u * R * elem_size(dtype) : 0);
+  p->total = c.used;
+  return PGG_OK;
+}
+
+AdapterTables tables_of(const AdapterPlan& p, void* ws) {
+  char* w = static_cast<char*>(ws);
+  AdapterTables t;
+  t.hdr = reinterpret_cast<WsHeader*>(w);
+  t.off = reinterpret_cast<int64_t*>(w + p.off);
+  t.order = reinterpret_cast<RowInfo*>(w + p.order);
+  t.padrow = reinterpret_cast<RowInfo*>(w + p.padrow);
+  t.rblist = reinterpret_cast<int4*>(w + p.rblist);
+  t.segs = reinterpret_cast<int4*>(w + p.segs);
+  t.blkseg = reinterpret_cast<int2*>(w + p.blkseg);
+  t.counts = reinterpret_cast<uint32_t*>(w + p.counts);
+  return t;
+}
+
+int run_adapter_prep(const AdapterPlan& p, const AdapterTables& t, const int64_t* adapter,
+                     int64_t T, int64_t A, cudaStream_t stream) {
+  AdapterPrepArgs a;
+  a.adapter = adapter;
+  a.t = t;
+  a.T = T;
+  a.A = static_cast<int32_t>(A);
+  a.rb = p.rb;
+  a.padded = p.padded;
+  a.blocks = p.blocks;
+  a.tokens_per_block = p.tokens_per_block;
+  return status_of(launch_adapter_prep(a, stream));
+}
+
+// u = scale * x f[adapter] for f [A, K, R], into rows of `u`.
+int run_shrink(const AdapterPlan& p, const AdapterTables& t, const HostEnv& env, const void* x,
+               const void* f, const float* scale, void* u, int64_t T, int64_t K, int64_t R,
+               int64_t A, int dtype, cudaStream_t stream) {
+  RowsArgs a;
+  std::memset(&a, 0, sizeof(a));
+  a.x = x;
+  a.w = f;
+  a.scale = scale;
+  a.rblist = t.rblist;
+  a.rowinfo = t.order;
+  a.hdr = t.hdr;
+  a.out = u;
+  a.M = T;
+  a.N = R;
+  a.K = K;
+  a.G = A;
+  a.batch = T;
+  a.max_row_blocks = p.max_row_blocks;
+  a.padded = p.padded;
+  a.wait_limit_ns = env.wait_limit_ns;
+  return status_of(launch_rows_simt(dtype, kShrink, a, env.num_sms, stream));
+}
+
+// y = x W + u f[adapter]^T for W [K, N] (transposed: [N, K]) and f [A, N, R].
+int run_adapt(const AdapterPlan& p, const AdapterTables& t, const HostEnv& env, bool transposed,
+              const void* x, const void* w, const void* u, const void* f, void* y, int64_t T,
+              int64_t K, int64_t N, int64_t R, int64_t A, int dtype, cudaStream_t stream) {
+  RowsArgs a;
+  std::memset(&a, 0, sizeof(a));
+  a.x = x;
+  a.w = w;
+  a.u = u;
+  a.b = f;
+  a.rblist = t.rblist;
+  a.rowinfo = t.order;
+  a.segs = t.segs;
+  a.blkseg = t.blkseg;
+  a.hdr = t.hdr;
+  a.out = y;
+  a.M = T;
+  a.N = N;
+  a.K = K;
+  a.G = A;
+  a.R = static_cast<int32_t>(R);
+  a.batch = T;
+  a.max_row_blocks = p.max_row_blocks;
+  a.hold_release = env.hold_release;
+  a.wait_limit_ns = env.wait_limit_ns;
+  return status_of(
+      launch_rows_simt(dtype, transposed ? kAdaptT : kAdapt, a, env.num_sms, stream));
+}
+
+}  // namespace
+}  // namespace pgg
+
+using namespace pgg;
+
+extern "C" {
+
+int pgg_route_workspace_size(int64_t batch, int64_t G, int64_t topK, size_t* workspace_bytes) {
+  if (!workspace_bytes) return PGG_ERR_NULL;
+  const int rc = check_route(batch, G, topK);
+  if (rc != PGG_OK) return rc;
+  *workspace_bytes = route_workspace(batch, G, topK);
+  return PGG_OK;
+}
+
+int pgg_route_execute(const void* logits, const float* bias, int64_t batch, int64_t G,
+                      int64_t topK, int rowIdxType, pgg_dtype dtype, pgg_score score,
+                      int renormalize, float scale, void* workspace, size_t workspace_bytes,
+                      float* probs, int64_t* experts, int64_t* expandedRowIdx, int64_t* groupList,
+                      pgg_stream_t stream) {
+  if (!logits || !workspace || !probs || !experts || !expandedRowIdx || !groupList)
+    return PGG_ERR_NULL;
+  if (!known_dtype(dtype)) return PGG_ERR_DTYPE;
+  if (rowIdxType != 0 && rowIdxType != 1) return PGG_ERR_ATTR;
+  if (score != PGG_SCORE_SOFTMAX && score != PGG_SCORE_SIGMOID) return PGG_ERR_ATTR;
+  const int rc = check_route(batch, G, topK);
+  if (rc != PGG_OK) return rc;
+  if (!aligned(logits, static_cast<uintptr_t>(elem_size(dtype))) || !aligned(bias, 4) ||
+      !aligned(probs, 4) || !aligned(experts, 8) || !aligned(expandedRowIdx, 8) ||
+      !aligned(groupList, 8) || !aligned(workspace, 256))
+    return PGG_ERR_ALIGN;
+  if (workspace_bytes < route_workspace(batch, G, topK)) return PGG_ERR_WORKSPACE;
+  RouteArgs a;
+  a.logits = logits;
+  a.bias = bias;
+  a.probs = probs;
+  a.experts = experts;
+  a.idx = expandedRowIdx;
+  a.groups = groupList;
+  a.counts = reinterpret_cast<uint32_t*>(static_cast<char*>(workspace) + 256);
+  a.T = batch;
+  a.scale = scale;
+  a.G = static_cast<int32_t>(G);
+  a.k = static_cast<int32_t>(topK);
+  a.row_idx_type = rowIdxType;
+  a.sigmoid = score == PGG_SCORE_SIGMOID ? 1 : 0;
+  a.renormalize = renormalize != 0 ? 1 : 0;
+  a.hdr = static_cast<WsHeader*>(workspace);
+  route_blocks(batch, G, topK, &a.blocks, &a.tokens_per_block);
+  return status_of(launch_route(dtype, a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int pgg_route_grad(const float* d_probs, const void* logits, const int64_t* experts,
+                   int64_t batch, int64_t G, int64_t topK, pgg_dtype dtype, pgg_score score,
+                   int renormalize, float scale, void* d_logits, pgg_stream_t stream) {
+  if (!d_probs || !logits || !experts || !d_logits) return PGG_ERR_NULL;
+  if (!known_dtype(dtype)) return PGG_ERR_DTYPE;
+  if (score != PGG_SCORE_SOFTMAX && score != PGG_SCORE_SIGMOID) return PGG_ERR_ATTR;
+  const int rc = check_route(batch, G, topK);
+  if (rc != PGG_OK) return rc;
+  const uintptr_t es = static_cast<uintptr_t>(elem_size(dtype));
+  if (!aligned(logits, es) || !aligned(d_logits, es) || !aligned(d_probs, 4) ||
+      !aligned(experts, 8))
+    return PGG_ERR_ALIGN;
+  HostEnv env;
+  if (host_env(&env) != PGG_OK) return PGG_ERR_CUDA;
+  RouteGradArgs a;
+  a.d_probs = d_probs;
+  a.logits = logits;
+  a.experts = experts;
+  a.d_logits = d_logits;
+  a.T = batch;
+  a.scale = scale;
+  a.G = static_cast<int32_t>(G);
+  a.k = static_cast<int32_t>(topK);
+  a.sigmoid = score == PGG_SCORE_SIGMOID ? 1 : 0;
+  a.renormalize = renormalize != 0 ? 1 : 0;
+  return status_of(launch_route_grad(dtype, a, env.num_sms,
+                                     reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int pgg_swiglu_workspace_size(int64_t M, int64_t F, int64_t K, int64_t G, int64_t L,
+                              int64_t batch, int64_t topK, int rowIdxType, pgg_dtype dtype,
+                              size_t* workspace_bytes) {
+  if (!workspace_bytes) return PGG_ERR_NULL;
+  int rc = check_gated(M, F, K, G, L, batch, topK, rowIdxType, dtype);
+  if (rc != PGG_OK) return rc;
+  GatedPlan p;
+  rc = gated_plan(M, F, G, &p);
+  if (rc != PGG_OK) return rc;
+  *workspace_bytes = p.total;
+  return PGG_OK;
+}
+
+int pgg_swiglu_execute(const void* x, const void* weight, const int64_t* expandedRowIdx,
+                       const int64_t* groupList, const float* probs, int64_t M, int64_t F,
+                       int64_t K, int64_t G, int64_t L, int64_t batch, int64_t topK,
+                       int rowIdxType, pgg_dtype dtype, void* workspace, size_t workspace_bytes,
+                       void* h, void* gate_up, pgg_stream_t stream) {
+  if (!x || !weight || !expandedRowIdx || !groupList || !workspace || !h) return PGG_ERR_NULL;
+  int rc = check_gated(M, F, K, G, L, batch, topK, rowIdxType, dtype);
+  if (rc != PGG_OK) return rc;
+  GatedPlan p;
+  rc = gated_plan(M, F, G, &p);
+  if (rc != PGG_OK) return rc;
+  const uintptr_t es = static_cast<uintptr_t>(elem_size(dtype));
+  if (!aligned(workspace, 256) || !aligned(expandedRowIdx, 8) || !aligned(groupList, 8) ||
+      !aligned(probs, 4) || !aligned(x, es) || !aligned(weight, es) || !aligned(h, es) ||
+      !aligned(gate_up, es))
+    return PGG_ERR_ALIGN;
+  if (workspace_bytes < p.total) return PGG_ERR_WORKSPACE;
+  HostEnv env;
+  if (host_env(&env) != PGG_OK) return PGG_ERR_CUDA;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  char* w = static_cast<char*>(workspace);
+  RowsPrepArgs pr;
+  pr.idx = expandedRowIdx;
+  pr.groups = groupList;
+  pr.hdr = reinterpret_cast<WsHeader*>(w);
+  pr.rblist = reinterpret_cast<int4*>(w + p.rblist);
+  pr.rowinfo = reinterpret_cast<RowInfo*>(w + p.rowinfo);
+  pr.inv = reinterpret_cast<int32_t*>(w + p.inv);
+  pr.M = M;
+  pr.G = G;
+  pr.top_k = static_cast<int32_t>(topK);
+  pr.row_idx_type = rowIdxType;
+  pr.rows_per_block = p.rows_per_block;
+  rc = status_of(launch_rows_prep(pr, env.num_sms, s));
+  if (rc != PGG_OK) return rc;
+  RowsArgs a;
+  std::memset(&a, 0, sizeof(a));
+  a.x = x;
+  a.w = weight;
+  a.probs = probs;
+  a.rblist = pr.rblist;
+  a.rowinfo = pr.rowinfo;
+  a.hdr = pr.hdr;
+  a.out = h;
+  a.gate_up = gate_up;
+  a.M = M;
+  a.N = F;
+  a.K = K;
+  a.G = G;
+  a.batch = batch;
+  a.max_row_blocks = p.max_row_blocks;
+  a.hold_release = env.hold_release;
+  a.wait_limit_ns = env.wait_limit_ns;
+  return status_of(launch_rows_simt(dtype, kGated, a, env.num_sms, s));
+}
+
+int pgg_swiglu_grad_workspace_size(int64_t M, int64_t batch, int64_t topK,
+                                   size_t* workspace_bytes) {
+  return pgg_unpermute_grad_workspace_size(M, batch, topK, workspace_bytes);
+}
+
+int pgg_swiglu_grad(const void* d_h, const void* gate_up, const float* probs,
+                    const int64_t* expandedRowIdx, int64_t M, int64_t F, int64_t batch,
+                    int64_t topK, int rowIdxType, pgg_dtype dtype, void* workspace,
+                    size_t workspace_bytes, void* d_gate_up, float* d_probs, void* h,
+                    pgg_stream_t stream) {
+  if (!d_h || !gate_up || !expandedRowIdx || !workspace || !d_gate_up) return PGG_ERR_NULL;
+  if (d_probs && !probs) return PGG_ERR_NULL;
+  if (!known_dtype(dtype)) return PGG_ERR_DTYPE;
+  if (rowIdxType != 0 && rowIdxType != 1) return PGG_ERR_ATTR;
+  size_t need = 0;
+  int rc = pgg_swiglu_grad_workspace_size(M, batch, topK, &need);
+  if (rc != PGG_OK) return rc;
+  if (F <= 0 || F > kInt32Max / 2) return PGG_ERR_SHAPE;
+  const uintptr_t es = static_cast<uintptr_t>(elem_size(dtype));
+  if (!aligned(workspace, 256) || !aligned(expandedRowIdx, 8) || !aligned(probs, 4) ||
+      !aligned(d_probs, 4) || !aligned(d_h, es) || !aligned(gate_up, es) ||
+      !aligned(d_gate_up, es) || !aligned(h, es))
+    return PGG_ERR_ALIGN;
+  if (workspace_bytes < need) return PGG_ERR_WORKSPACE;
+  HostEnv env;
+  if (host_env(&env) != PGG_OK) return PGG_ERR_CUDA;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  char* w = static_cast<char*>(workspace);
+  WsHeader* hdr = reinterpret_cast<WsHeader*>(w);
+  rc = status_of(launch_index_prep(expandedRowIdx, M, rowIdxType,
+                                   reinterpret_cast<int32_t*>(w + 256), hdr, env.num_sms, s));
+  if (rc != PGG_OK) return rc;
+  GatedGradArgs a;
+  a.d_h = d_h;
+  a.gate_up = gate_up;
+  a.probs = probs;
+  a.idx = expandedRowIdx;
+  a.hdr = hdr;
+  a.d_gate_up = d_gate_up;
+  a.h = h;
+  a.d_probs = d_probs;
+  a.M = M;
+  a.F = F;
+  a.row_idx_type = rowIdxType;
+  const bool vec = (F * static_cast<int64_t>(es)) % 16 == 0 && aligned(d_h, 16) &&
+                   aligned(gate_up, 16) && aligned(d_gate_up, 16) && aligned(h, 16);
+  return status_of(launch_gated_grad(dtype, a, vec, env.num_sms, s));
+}
+
+int pgg_adapters_workspace_size(int64_t T, int64_t K, int64_t N, int64_t R, int64_t A,
+                                pgg_dtype dtype, size_t* workspace_bytes) {
+  if (!workspace_bytes) return PGG_ERR_NULL;
+  int rc = check_adapters(T, K, N, R, A, dtype);
+  if (rc != PGG_OK) return rc;
+  AdapterPlan p;
+  rc = adapter_plan(T, K, N, R, A, dtype, false, &p);
+  if (rc != PGG_OK) return rc;
+  *workspace_bytes = p.total;
+  return PGG_OK;
+}
+
+int pgg_adapters_execute(const void* x, const void* weight, const void* a, const void* b,
+                         const int64_t* adapter, const float* scale, int64_t T, int64_t K,
+                         int64_t N, int64_t R, int64_t A, pgg_dtype dtype, void* workspace,
+                         size_t workspace_bytes, void* y, pgg_stream_t stream) {
+  if (!x || !weight || !a || !b || !adapter || !workspace || !y) return PGG_ERR_NULL;
+  int rc = check_adapters(T, K, N, R, A, dtype);
+  if (rc != PGG_OK) return rc;
+  AdapterPlan p;
+  rc = adapter_plan(T, K, N, R, A, dtype, false, &p);
+  if (rc != PGG_OK) return rc;
+  const uintptr_t es = static_cast<uintptr_t>(elem_size(dtype));
+  if (!aligned(workspace, 256) || !aligned(adapter, 8) || !aligned(scale, 4) || !aligned(x, es) ||
+      !aligned(weight, es) || !aligned(a, es) || !aligned(b, es) || !aligned(y, es))
+    return PGG_ERR_ALIGN;
+  if (workspace_bytes < p.total) return PGG_ERR_WORKSPACE;
+  HostEnv env;
+  if (host_env(&env) != PGG_OK) return PGG_ERR_CUDA;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const AdapterTables t = tables_of(p, workspace);
+  void* u = static_cast<char*>(workspace) + p.u;
+  rc = run_adapter_prep(p, t, adapter, T, A, s);
+  if (rc != PGG_OK) return rc;
+  rc = run_shrink(p, t, env, x, a, scale, u, T, K, R, A, dtype, s);
+  if (rc != PGG_OK) return rc;
+  return run_adapt(p, t, env, false, x, weight, u, b, y, T, K, N, R, A, dtype, s);
+}
+
+int pgg_adapters_grad_workspace_size(int64_t T, int64_t K, int64_t N, int64_t R, int64_t A,
+                                     pgg_dtype dtype, size_t* workspace_bytes) {
+  if (!workspace_bytes) return PGG_ERR_NULL;
+  int rc = check_adapters(T, K, N, R, A, dtype);
+  if (rc != PGG_OK) return rc;
+  AdapterPlan p;
+  rc = adapter_plan(T, K, N, R, A, dtype, true, &p);
+  if (rc != PGG_OK) return rc;
+  *workspace_bytes = p.total;
+  return PGG_OK;
+}
+
+int pgg_adapters_grad(const void* d_y, const void* x, const void* weight, const void* a,
+                      const void* b, const int64_t* adapter, const float* scale, int64_t T,
+                      int64_t K, int64_t N, int64_t R, int64_t A, pgg_dtype dtype,
+                      void* workspace, size_t workspace_bytes, void* d_x, void* d_a, void* d_b,
+                      pgg_stream_t stream) {
+  if (!d_y || !x || !weight || !a || !b || !adapter || !workspace || !d_a || !d_b)
+    return PGG_ERR_NULL;
+  int rc = check_adapters(T, K, N, R, A, dtype);
+  if (rc != PGG_OK) return rc;
+  AdapterPlan p;
+  rc = adapter_plan(T, K, N, R, A, dtype, true, &p);
+  if (rc != PGG_OK) return rc;
+  const uintptr_t es = static_cast<uintptr_t>(elem_size(dtype));
+  if (!aligned(workspace, 256) || !aligned(adapter, 8) || !aligned(scale, 4) ||
+      !aligned(d_y, es) || !aligned(x, es) || !aligned(weight, es) || !aligned(a, es) ||
+      !aligned(b, es) || !aligned(d_x, es) || !aligned(d_a, es) || !aligned(d_b, es))
+    return PGG_ERR_ALIGN;
+  if (workspace_bytes < p.total) return PGG_ERR_WORKSPACE;
+  HostEnv env;
+  if (host_env(&env) != PGG_OK) return PGG_ERR_CUDA;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const AdapterTables t = tables_of(p, workspace);
+  void* u = static_cast<char*>(workspace) + p.u;
+  void* v = static_cast<char*>(workspace) + p.v;
+  rc = run_adapter_prep(p, t, adapter, T, A, s);
+  if (rc != PGG_OK) return rc;
+  rc = run_shrink(p, t, env, x, a, scale, u, T, K, R, A, dtype, s);
+  if (rc != PGG_OK) return rc;
+  rc = run_shrink(p, t, env, d_y, b, scale, v, T, N, R, A, dtype, s);
+  if (rc != PGG_OK) return rc;
+  if (d_x) {
+    rc = run_adapt(p, t, env, true, d_y, weight, v, a, d_x, T, N, K, R, A, dtype, s);
+    if (rc != PGG_OK) return rc;
+  }
+  rc = run_dw_tables(x, v, t.off, t.padrow, t.hdr, p.rows_u, R, K, A, T, dtype, d_a, s);
+  if (rc != PGG_OK) return rc;
+  return run_dw_tables(d_y, u, t.off, t.padrow, t.hdr, p.rows_u, R, N, A, T, dtype, d_b, s);
+}
+
+}  // extern "C"

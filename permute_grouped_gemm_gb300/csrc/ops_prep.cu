@@ -1,0 +1,398 @@
+// Preparation launches of the gated product and of the adapters: the tables
+// that the products walk, and the validation of what the caller gave.
+//
+// Gated product (rows_prep): the row blocks of every expert from groupList,
+// {token, original position} of every expanded row from expandedRowIdx, and
+// the checks that groupList sums to M and expandedRowIdx is a permutation.
+// Few rows: one block, one launch (a bit per position finds a repetition).
+// Many: two launches (the inverse is written, then compared).
+//
+// Adapters (adapter_prep): a stable counting sort of the tokens by adapter
+// (tokens without one last), the list of live adapters, which of them each 256
+// rows meet, and the row blocks of the low-rank factors. One block up to
+// kSmallTokens tokens; beyond that counting, prefix sums, placement and the
+// lists are four launches.
+//
+// All of it is integer work on a few bytes per row: latency is what it costs,
+// so what counts is the number of launches.
+
+#include <cstdint>
+
+#include "pgg_ops.h"
+#include "pgg_ptx.cuh"
+#include "pgg_sort.cuh"
+
+namespace pgg {
+namespace {
+
+constexpr int kSmallRows = 8192;     // gated product: one block up to here
+constexpr int kSmallGroups = 4096;
+constexpr int kSmallTokens = 16384;  // adapters: one block up to here
+
+__device__ __forceinline__ RowInfo row_info(int64_t p, int top_k) {
+  RowInfo r;
+  r.token = static_cast<int32_t>(static_cast<uint32_t>(p) / static_cast<uint32_t>(top_k));
+  r.rank = static_cast<int32_t>(p);
+  return r;
+}
+
+// The whole block: expert offsets and row blocks; returns whether groupList is
+// right. Writes n_row_blocks (0 when it is not).
+__device__ bool build_row_blocks(const RowsPrepArgs& a) {
+  __shared__ uint32_t s_scan[33];
+  __shared__ int s_bad;
+  if (threadIdx.x == 0) s_bad = 0;
+  __syncthreads();
+  // 64-bit sum of the counts beside the 32-bit scan: counts are at most M < 2^31
+  // each, so a wrong list is noticed before a scan could wrap
+  __shared__ unsigned long long s_sum;
+  if (threadIdx.x == 0) s_sum = 0;
+  __syncthreads();
+  for (int64_t g = threadIdx.x; g < a.G; g += blockDim.x) {
+    const int64_t c = a.groups[g];
+    if (c < 0 || c > a.M)
+      s_bad = 1;
+    else
+      atomicAdd(&s_sum, static_cast<unsigned long long>(c));
+  }
+  __syncthreads();
+  const bool ok = !s_bad && s_sum == static_cast<unsigned long long>(a.M);
+  uint32_t rows = 0, blocks = 0;
+  for (int64_t g0 = 0; ok && g0 < a.G; g0 += blockDim.x) {
+    const int64_t g = g0 + threadIdx.x;
+    const uint32_t c = g < a.G ? static_cast<uint32_t>(a.groups[g]) : 0u;
+    const uint32_t rpb = static_cast<uint32_t>(a.rows_per_block);
+    const uint32_t nb = (c + rpb - 1) / rpb;
+    uint32_t tot_c, tot_b;
+    const uint32_t row0 = rows + block_scan_u32(c, s_scan, &tot_c);
+    const uint32_t b0 = blocks + block_scan_u32(nb, s_scan, &tot_b);
+    for (uint32_t j = 0; j < nb; ++j) {
+      const uint32_t left = c - j * rpb;
+      a.rblist[b0 + j] = make_int4(static_cast<int>(g), static_cast<int>(row0 + j * rpb),
+                                   static_cast<int>(left < rpb ? left : rpb), 0);
+    }
+    rows += tot_c;
+    blocks += tot_b;
+  }
+  if (threadIdx.x == 0) {
+    a.hdr->n_row_blocks = blocks;
+    a.hdr->sched_next = 0;
+    a.hdr->timeout_site = 0;
+    a.hdr->unsorted = 0;
+  }
+  return ok;
+}
+
+__global__ void __launch_bounds__(1024) rows_prep_small_kernel(const RowsPrepArgs a) {
+  __shared__ uint32_t s_seen[kSmallRows / 32];
+  __shared__ uint32_t s_status;
+  ptx::griddep_wait();
+  const int M = static_cast<int>(a.M);
+  for (int i = threadIdx.x; i < (M + 31) / 32; i += blockDim.x) s_seen[i] = 0;
+  if (threadIdx.x == 0) s_status = 0;
+  const bool ok = build_row_blocks(a);  // (has barriers)
+  for (int q = threadIdx.x; q < M; q += blockDim.x) {
+    const int64_t v = a.idx[q];
+    if (v < 0 || v >= a.M) {
+      atomicCAS(&s_status, 0u, kStIndex);
+      continue;
+    }
+    const uint32_t bit = 1u << (v & 31);
+    if (atomicOr(&s_seen[v >> 5], bit) & bit) atomicCAS(&s_status, 0u, kStNotPerm);
+    const int64_t row = a.row_idx_type == 0 ? q : v;
+    const int64_t pos = a.row_idx_type == 0 ? v : q;
+    a.rowinfo[row] = row_info(pos, a.top_k);
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) a.hdr->status = ok ? s_status : kStGroupSum;
+}
+
+// Many rows, first launch: block 0 builds the row blocks, the others the rows'
+// records and the inverse index.
+__global__ void __launch_bounds__(512) rows_prep_fill_kernel(const RowsPrepArgs a) {
+  ptx::griddep_wait();
+  if (blockIdx.x == 0) {
+    const bool ok = build_row_blocks(a);
+    if (threadIdx.x == 0) a.hdr->status = ok ? 0u : kStGroupSum;
+    return;
+  }
+  const int64_t stride = static_cast<int64_t>(gridDim.x - 1) * blockDim.x;
+  for (int64_t q = static_cast<int64_t>(blockIdx.x - 1) * blockDim.x + threadIdx.x; q < a.M;
+       q += stride) {
+    const int64_t v = a.idx[q];
+    if (v < 0 || v >= a.M) {
+      // the record stays readable: whoever reads it before the status is seen is in bounds
+      if (a.row_idx_type == 0) a.rowinfo[q] = row_info(0, a.top_k);
+      continue;
+    }
+    a.inv[v] = static_cast<int32_t>(q);
+    const int64_t row = a.row_idx_type == 0 ? q : v;
+    const int64_t pos = a.row_idx_type == 0 ? v : q;
+    a.rowinfo[row] = row_info(pos, a.top_k);
+  }
+}
+
+// Second launch: every entry must find itself in the inverse. (What earlier
+// calls left in inv cannot pass for this call's: inv[idx[q]] was written by
+// this call, by q or by another entry with the same value.)
+__global__ void __launch_bounds__(512) rows_prep_check_kernel(const RowsPrepArgs a) {
+  ptx::griddep_wait();
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * blockDim.x;
+  for (int64_t q = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; q < a.M;
+       q += stride) {
+    const int64_t v = a.idx[q];
+    if (v < 0 || v >= a.M)
+      atomicCAS(&a.hdr->status, 0u, kStIndex);
+    else if (a.inv[v] != q)
+      atomicCAS(&a.hdr->status, 0u, kStNotPerm);
+  }
+}
+
+// ------------------------------------------------------------------ adapters
+
+// Key of a token: its adapter, A without one; an id outside [-1, A) counts as none.
+__device__ __forceinline__ int adapter_key(int64_t id, int A) {
+  return id >= 0 && id < A ? static_cast<int>(id) : A;
+}
+
+// Block-wide, blockDim.x > A (one thread per adapter and one for the group without): the lists
+// from the groups' sizes. Thread g holds group g's count and first compact row.
+__device__ void build_adapter_lists(const AdapterPrepArgs& a, uint32_t count, uint32_t start,
+                                    uint32_t* s_scan, uint32_t* s_start, uint32_t* s_ustart,
+                                    uint32_t* s_seg_end) {
+  const int g = threadIdx.x;
+  const bool group = g <= a.A;
+  if (!group) count = 0;
+  const uint32_t room = a.padded ? (count + 63u) / 64u * 64u : count;
+  uint32_t total, n_seg, n_rb;
+  const uint32_t ustart = block_scan_u32(room, s_scan, &total);
+  const bool live = g < a.A && count > 0;
+  const uint32_t seg = block_scan_u32(live ? 1u : 0u, s_scan, &n_seg);
+  const uint32_t nb = group ? (count + a.rb - 1) / a.rb : 0u;
+  const uint32_t rb0 = block_scan_u32(nb, s_scan, &n_rb);
+  if (group) {
+    a.t.off[g] = ustart;
+    s_start[g] = start;
+    s_ustart[g] = ustart;
+    for (uint32_t j = 0; j < nb; ++j) {
+      const uint32_t left = count - j * a.rb;
+      a.t.rblist[rb0 + j] = make_int4(
+          g, static_cast<int>(start + j * a.rb),
+          static_cast<int>(left < static_cast<uint32_t>(a.rb) ? left : a.rb),
+          static_cast<int>(ustart + j * a.rb));
+    }
+  }
+  if (live) {
+    a.t.segs[seg] = make_int4(g, static_cast<int>(start), static_cast<int>(start + count),
+                              static_cast<int>(ustart));
+    s_seg_end[seg] = start + count;
+  }
+  if (g == 0) a.t.hdr->n_row_blocks = n_rb;
+  __syncthreads();
+  // segments that rows [256 b, 256 b + 256) meet: they are in row order and leave no gaps
+  for (int64_t b = threadIdx.x; b < (a.T + 255) / 256; b += blockDim.x) {
+    const uint32_t r0 = static_cast<uint32_t>(256 * b);
+    const uint32_t r1 = static_cast<uint32_t>(256 * b + 256 < a.T ? 256 * b + 256 : a.T);
+    uint32_t lo = 0, hi = n_seg;  // first segment that ends past r0
+    while (lo < hi) {
+      const uint32_t mid = (lo + hi) >> 1;
+      if (s_seg_end[mid] > r0) hi = mid; else lo = mid + 1;
+    }
+    uint32_t e = lo;
+    uint32_t top = n_seg;  // first segment that ends at r1 or past it
+    while (e < top) {
+      const uint32_t mid = (e + top) >> 1;
+      if (s_seg_end[mid] >= r1) top = mid; else e = mid + 1;
+    }
+    const uint32_t end = e < n_seg ? e + 1 : n_seg;
+    a.t.blkseg[b] = make_int2(static_cast<int>(lo), static_cast<int>(end > lo ? end - lo : 0));
+  }
+}
+
+// Records of one sorted token; the last token of a padded adapter also fills up its last 64 rows.
+__device__ __forceinline__ void put_token(const AdapterPrepArgs& a, int64_t token, int g,
+                                          uint32_t where, uint32_t start, uint32_t ustart,
+                                          uint32_t count) {
+  RowInfo r;
+  r.token = static_cast<int32_t>(token);
+  r.rank = g;
+  a.t.order[where] = r;
+  if (!a.padded) return;
+  const uint32_t i = where - start;
+  r.rank = 0;
+  a.t.padrow[ustart + i] = r;
+  if (i + 1 == count)
+    for (uint32_t j = count; j < (count + 63u) / 64u * 64u; ++j) a.t.padrow[ustart + j] = r;
+}
+
+__global__ void __launch_bounds__(1024) adapter_prep_small_kernel(const AdapterPrepArgs a) {
+  extern __shared__ uint32_t s_cnt[];  // [warps][A + 1], then 4 x [A + 1]
+  __shared__ uint32_t s_scan[33];
+  __shared__ int s_bad;
+  ptx::griddep_wait();
+  const int G = a.A + 1, warps = blockDim.x >> 5;
+  uint32_t* s_start = s_cnt + warps * G;
+  uint32_t *s_ustart = s_start + G, *s_seg = s_ustart + G, *s_count = s_seg + G;
+  if (threadIdx.x == 0) s_bad = 0;
+  __syncthreads();
+  const int n = static_cast<int>(a.T);
+  for (int e = threadIdx.x; e < n; e += blockDim.x) {
+    const int64_t id = a.adapter[e];
+    if (id < -1 || id >= a.A) s_bad = 1;
+  }
+  const int run = ((n + warps - 1) / warps + 31) / 32 * 32;
+  auto key = [&](int e) { return adapter_key(a.adapter[e], a.A); };
+  sort_count(s_cnt, G, n, run, key);
+  const int g = threadIdx.x;
+  uint32_t c = 0, total;
+  if (g < G) {
+    for (int w = 0; w < warps; ++w) c += s_cnt[w * G + g];
+    s_count[g] = c;
+  }
+  const uint32_t start = block_scan_u32(c, s_scan, &total);
+  build_adapter_lists(a, c, start, s_scan, s_start, s_ustart, s_seg);
+  __syncthreads();
+  sort_place(
+      s_cnt, G, n, run, key, [&](int) { return start; },
+      [&](int e, uint32_t where) {
+        const int k = key(e);
+        put_token(a, e, k, where, s_start[k], s_ustart[k], s_count[k]);
+      });
+  if (threadIdx.x == 0) {
+    a.t.hdr->status = s_bad ? kStIndex : 0u;
+    a.t.hdr->sched_next = 0;
+    a.t.hdr->timeout_site = 0;
+    a.t.hdr->unsorted = 0;
+  }
+}
+
+constexpr int kSortThreads = 256;
+
+// Many tokens, first launch: the block's count of every adapter.
+__global__ void __launch_bounds__(kSortThreads) adapter_count_kernel(const AdapterPrepArgs a) {
+  extern __shared__ uint32_t s_cnt[];  // [A + 1]
+  ptx::griddep_wait();
+  const int G = a.A + 1;
+  for (int g = threadIdx.x; g < G; g += blockDim.x) s_cnt[g] = 0;
+  __syncthreads();
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * a.tokens_per_block;
+  const int64_t t1 = t0 + a.tokens_per_block < a.T ? t0 + a.tokens_per_block : a.T;
+  for (int64_t t = t0 + threadIdx.x; t < t1; t += blockDim.x)
+    atomicAdd(&s_cnt[adapter_key(a.adapter[t], a.A)], 1u);
+  __syncthreads();
+  for (int g = threadIdx.x; g < G; g += blockDim.x)
+    a.t.counts[static_cast<int64_t>(g) * a.blocks + blockIdx.x] = s_cnt[g];
+}
+
+// Third launch (one block), after the prefix sums: the lists. The totals arrive in off.
+__global__ void __launch_bounds__(1024) adapter_lists_kernel(const AdapterPrepArgs a) {
+  extern __shared__ uint32_t s_lists[];  // 3 x [A + 1]
+  __shared__ uint32_t s_scan[33];
+  ptx::griddep_wait();
+  const int G = a.A + 1, g = threadIdx.x;
+  const uint32_t c = g < G ? static_cast<uint32_t>(a.t.off[g]) : 0u;
+  uint32_t total;
+  const uint32_t start = block_scan_u32(c, s_scan, &total);
+  build_adapter_lists(a, c, start, s_scan, s_lists, s_lists + G, s_lists + 2 * G);
+  // [blocks of this group's prefix sums become first rows]
+  __syncthreads();
+  if (g < G) {
+    // starts and counts for the placement, after the counts: counts [G][blocks], then 2 x [G]
+    uint32_t* tail = a.t.counts + static_cast<int64_t>(G) * a.blocks;
+    tail[g] = start;
+    tail[G + g] = c;
+  }
+  if (g == 0) {
+    a.t.hdr->status = 0;
+    a.t.hdr->sched_next = 0;
+    a.t.hdr->timeout_site = 0;
+    a.t.hdr->unsorted = 0;
+  }
+}
+
+// Fourth launch: placement, and the check of the ids.
+__global__ void __launch_bounds__(kSortThreads) adapter_place_kernel(const AdapterPrepArgs a) {
+  extern __shared__ uint32_t s_cnt[];  // [warps][A + 1]
+  ptx::griddep_wait();
+  const int G = a.A + 1;
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * a.tokens_per_block;
+  const int64_t left = a.T - t0;
+  const int n = left < a.tokens_per_block ? static_cast<int>(left) : a.tokens_per_block;
+  constexpr int kW = kSortThreads / 32;
+  const int run = ((n + kW - 1) / kW + 31) / 32 * 32;
+  const uint32_t* tail = a.t.counts + static_cast<int64_t>(G) * a.blocks;
+  auto key = [&](int e) { return adapter_key(a.adapter[t0 + e], a.A); };
+  for (int e = threadIdx.x; e < n; e += blockDim.x) {
+    const int64_t id = a.adapter[t0 + e];
+    if (id < -1 || id >= a.A) atomicCAS(&a.t.hdr->status, 0u, kStIndex);
+  }
+  sort_count(s_cnt, G, n, run, key);
+  sort_place(
+      s_cnt, G, n, run, key,
+      [&](int g) {
+        return tail[g] + a.t.counts[static_cast<int64_t>(g) * a.blocks + blockIdx.x];
+      },
+      [&](int e, uint32_t where) {
+        const int k = key(e);
+        put_token(a, t0 + e, k, where, tail[k], static_cast<uint32_t>(a.t.off[k]), tail[G + k]);
+      });
+}
+
+}  // namespace
+
+cudaError_t launch_rows_prep(const RowsPrepArgs& a, int num_sms, cudaStream_t stream) {
+  if (a.M <= kSmallRows && a.G <= kSmallGroups) {
+    int64_t threads = (a.M > a.G ? a.M : a.G);
+    threads = (threads + 31) / 32 * 32;
+    if (threads > 1024) threads = 1024;
+    return launch_pdl(rows_prep_small_kernel, dim3(1), dim3(static_cast<unsigned>(threads)), 0,
+                      stream, 1, a);
+  }
+  int64_t blocks = (a.M + 511) / 512;
+  const int64_t cap = static_cast<int64_t>(num_sms) * 4;
+  if (blocks > cap) blocks = cap;
+  cudaError_t err = launch_pdl(rows_prep_fill_kernel, dim3(static_cast<unsigned>(blocks + 1)),
+                               dim3(512), 0, stream, 1, a);
+  if (err != cudaSuccess) return err;
+  return launch_pdl(rows_prep_check_kernel, dim3(static_cast<unsigned>(blocks)), dim3(512), 0,
+                    stream, 1, a);
+}
+
+// Blocks of the counting and placement launches; 1: one launch does everything.
+void adapter_blocks(int64_t T, int* blocks, int* tokens_per_block) {
+  if (T <= kSmallTokens) {
+    *blocks = 1;
+    *tokens_per_block = static_cast<int>(T);
+    return;
+  }
+  int64_t per = (T + 511) / 512;
+  per = (per + kSortThreads - 1) / kSortThreads * kSortThreads;
+  *tokens_per_block = static_cast<int>(per);
+  *blocks = static_cast<int>((T + per - 1) / per);
+}
+
+cudaError_t launch_adapter_prep(const AdapterPrepArgs& a, cudaStream_t stream) {
+  const int G = a.A + 1;
+  if (a.blocks == 1) {
+    int threads = static_cast<int>((a.T > G ? a.T : G) + 31) / 32 * 32;
+    if (threads > 1024) threads = 1024;
+    const size_t smem = static_cast<size_t>(threads / 32 + 4) * G * 4;
+    cudaError_t err = cudaFuncSetAttribute(
+        adapter_prep_small_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        static_cast<int>(smem));
+    if (err != cudaSuccess) return err;
+    return launch_pdl(adapter_prep_small_kernel, dim3(1), dim3(threads), smem, stream, 1, a);
+  }
+  cudaError_t err = launch_pdl(adapter_count_kernel, dim3(a.blocks), dim3(kSortThreads),
+                               static_cast<size_t>(G) * 4, stream, 1, a);
+  if (err != cudaSuccess) return err;
+  err = launch_count_scan(a.t.counts, G, a.blocks, a.t.off, stream);
+  if (err != cudaSuccess) return err;
+  err = launch_pdl(adapter_lists_kernel, dim3(1), dim3(1024), static_cast<size_t>(3) * G * 4,
+                   stream, 1, a);
+  if (err != cudaSuccess) return err;
+  return launch_pdl(adapter_place_kernel, dim3(a.blocks), dim3(kSortThreads),
+                    static_cast<size_t>(kSortThreads / 32) * G * 4, stream, 1, a);
+}
+
+}  // namespace pgg

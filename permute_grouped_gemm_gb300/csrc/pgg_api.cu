@@ -13,6 +13,7 @@
 
 #include "pgg.h"
 #include "pgg_internal.h"
+#include "pgg_ops.h"
 
 namespace pgg {
 
@@ -52,8 +53,6 @@ int owner_stages(bool wide);
 int owner_threads();
 cudaError_t launch_owner(int dtype, const OwnerMaps& m, const OwnerArgs& a, int num_sms,
                          cudaStream_t stream);
-cudaError_t launch_index_prep(const int64_t* idx, int64_t M, int row_idx_type, int32_t* inv,
-                              WsHeader* hdr, int num_sms, cudaStream_t stream);
 cudaError_t launch_unpermute_grad(int dtype, const UnpermArgs& a, bool vec, bool pairs,
                                   int num_sms, cudaStream_t stream);
 
@@ -721,6 +720,57 @@ int run_fwd(const Plan& plan, const void* x, const void* weight, void* ws, void*
 }
 
 }  // namespace
+
+// ---------------------------------------------------------------- shared with ops_api.cu
+
+int host_env(HostEnv* env) {
+  DeviceInfo di;
+  const int rc = device_info(&di);
+  if (rc != PGG_OK) return rc;
+  env->num_sms = di.num_sms;
+  env->force_variant = g_force_variant.load();
+  env->hold_release = g_hold_release.load() != 0 ? 1 : 0;
+  env->wait_limit_ns = g_wait_limit_ns.load();
+  return PGG_OK;
+}
+
+int forced_variant() { return g_force_variant.load(); }
+
+bool encode_map_3d(CUtensorMap* m, int dtype, const void* base, int64_t d0, int64_t d1, int64_t d2,
+                   int box1) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return false;
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(d0), static_cast<cuuint64_t>(d1),
+                        static_cast<cuuint64_t>(d2)};
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(d0) * 2,
+                           static_cast<cuuint64_t>(d0) * static_cast<cuuint64_t>(d1) * 2};
+  cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box1), 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return enc(m, tmap_type(dtype), 3, const_cast<void*>(base), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+         CUDA_SUCCESS;
+}
+
+// run_dw reads sizes and three table offsets of its plan; the tables here lie anywhere.
+int run_dw_tables(const void* x, const void* dy, const int64_t* off, const RowInfo* rowinfo,
+                  WsHeader* hdr, int64_t rows, int64_t N, int64_t K, int64_t G, int64_t batch,
+                  int dtype, void* out, cudaStream_t stream) {
+  Plan p;
+  std::memset(&p, 0, sizeof(p));
+  p.dtype = dtype;
+  p.M = rows;
+  p.N = N;
+  p.K = K;
+  p.G = G;
+  p.batch = batch;
+  char* base = reinterpret_cast<char*>(hdr);
+  p.layout.hdr = 0;
+  p.layout.off = static_cast<size_t>(reinterpret_cast<const char*>(off) - base);
+  p.layout.rowinfo = static_cast<size_t>(reinterpret_cast<const char*>(rowinfo) - base);
+  return run_dw(p, x, dy, base, out, dtype, stream);
+}
+
 }  // namespace pgg
 
 using namespace pgg;

@@ -1,0 +1,172 @@
+// Internal definitions of the router, gated-product and adapter operators:
+// the tables their preparation kernels build in the workspace, the kernels'
+// arguments, and the host helpers they share with the other entry points.
+#pragma once
+
+#include "pgg_internal.h"
+
+namespace pgg {
+
+// ------------------------------------------------------------ shared host helpers (pgg_api.cu)
+
+struct HostEnv {
+  int num_sms;             // of the current device
+  int force_variant;       // test hook, -1 = automatic
+  int hold_release;        // test hook
+  uint64_t wait_limit_ns;  // bound of every wait inside a kernel
+};
+int host_env(HostEnv* env);  // pgg_status
+int forced_variant();        // test hook, -1 = automatic
+// Tensor map of a row-major 16-bit [d2][d1][d0] array (d0 innermost) with boxes of 64 x box1 x 1
+// elements and the 128-byte swizzle; reads outside it give zeros. False when it cannot be encoded.
+bool encode_map_3d(CUtensorMap* m, int dtype, const void* base, int64_t d0, int64_t d1, int64_t d2,
+                   int box1);
+// The weight-gradient kernels on tables already in memory: out[g] = sum over rows i in
+// [off[g], off[g + 1]) of x[token(i)]^T dy[i], g < G. dy has `rows` rows.
+int run_dw_tables(const void* x, const void* dy, const int64_t* off, const RowInfo* rowinfo,
+                  WsHeader* hdr, int64_t rows, int64_t N, int64_t K, int64_t G, int64_t batch,
+                  int dtype, void* out, cudaStream_t stream);
+
+// ------------------------------------------------------------ limits
+
+constexpr int64_t kMaxRouteExperts = 1024;  // a token's logits sit in one warp's registers
+constexpr int64_t kMaxRouteTopK = 32;       // one lane per choice
+constexpr int64_t kMaxAdapters = 1023;      // + the group of tokens without one: one thread each
+constexpr int64_t kMaxRank = 256;
+
+// ------------------------------------------------------------ router
+
+struct RouteArgs {
+  const void* logits;   // [T, G]
+  const float* bias;    // [G] or null
+  float* probs;         // [T, k]
+  int64_t* experts;     // [T, k]
+  int64_t* idx;         // [T * k]
+  int64_t* groups;      // [G]
+  uint32_t* counts;     // [G][blocks]: entries of each block per expert, then their prefix sums
+  WsHeader* hdr;
+  int64_t T;
+  float scale;
+  int32_t G, k;
+  int32_t row_idx_type;
+  int32_t sigmoid, renormalize;
+  int32_t blocks;            // blocks of the choice and placement launches
+  int32_t tokens_per_block;  // tokens of each
+};
+
+struct RouteGradArgs {
+  const float* d_probs;    // [T, k]
+  const void* logits;      // [T, G]
+  const int64_t* experts;  // [T, k]
+  void* d_logits;          // [T, G]
+  int64_t T;
+  float scale;
+  int32_t G, k;
+  int32_t sigmoid, renormalize;
+};
+
+// counts [G][blocks] -> their exclusive prefix sums over the blocks, and the totals.
+cudaError_t launch_count_scan(uint32_t* counts, int G, int blocks, int64_t* groups,
+                              cudaStream_t stream);
+void route_blocks(int64_t T, int64_t G, int64_t k, int* blocks, int* tokens_per_block);
+cudaError_t launch_route(int dtype, const RouteArgs& a, cudaStream_t stream);
+cudaError_t launch_route_grad(int dtype, const RouteGradArgs& a, int num_sms, cudaStream_t stream);
+
+// ------------------------------------------------------------ tables of the gated product
+
+struct RowsPrepArgs {
+  const int64_t* idx;     // expandedRowIdx [M]
+  const int64_t* groups;  // groupList [G]
+  WsHeader* hdr;
+  int4* rblist;      // {expert, first row, rows, 0}
+  RowInfo* rowinfo;  // [M] {token, original position} of each expanded row
+  int32_t* inv;      // [M]
+  int64_t M, G;
+  int32_t top_k, row_idx_type, rows_per_block;
+};
+cudaError_t launch_rows_prep(const RowsPrepArgs& a, int num_sms, cudaStream_t stream);
+
+// ------------------------------------------------------------ tables of the adapters
+
+// Tokens are put in order of their adapter (stable; tokens without one last, as group A). That
+// compact order of T rows is what the projection walks. The low-rank factors u and v are stored in
+// a second order, in which (padded = 1) every adapter starts at a multiple of 64 rows and is
+// filled up with zero rows: the weight-gradient kernel reads 64 rows at a time, and what it reads
+// past an adapter's rows must not be another adapter's.
+struct AdapterTables {
+  WsHeader* hdr;
+  int64_t* off;       // [A + 1] first row of each adapter in the order of u and v
+  RowInfo* order;     // [T] compact order: {token, adapter}
+  RowInfo* padrow;    // [P] order of u and v: {token, 0}; a filled-up row repeats a token
+  int4* rblist;       // {adapter, first compact row, rows, first row of u}: at most rb rows each
+  int4* segs;         // {adapter, first compact row, end, first row of u} of each live adapter
+  int2* blkseg;       // [ceil(T / 256)] {first segment, segments} of each 256 compact rows
+  uint32_t* counts;   // [A + 1][blocks], for many tokens
+};
+
+struct AdapterPrepArgs {
+  const int64_t* adapter;  // [T]
+  AdapterTables t;
+  int64_t T;
+  int32_t A;
+  int32_t rb;      // rows per entry of rblist, a multiple of 64 when padded
+  int32_t padded;
+  int32_t blocks, tokens_per_block;  // of the counting and placement launches
+};
+void adapter_blocks(int64_t T, int* blocks, int* tokens_per_block);
+cudaError_t launch_adapter_prep(const AdapterPrepArgs& a, cudaStream_t stream);
+
+// ------------------------------------------------------------ products over ragged rows
+
+enum RowsMode {
+  kGated = 0,    // h and gate_up from x [batch, K] and weight [G, K, 2F]
+  kShrink = 1,   // u [rows, R] = scale[ad] * x a[ad], a [A, K, R]
+  kAdapt = 2,    // y [T, N] = x W + u b[ad]^T, W [K, N], b [A, N, R]
+  kAdaptT = 3,   // the same with W given as [N, K]: the gradient of x
+};
+
+struct RowsArgs {
+  const void* x;           // rows gathered by token, K elements each
+  const void* w;           // kGated [G, K, 2 N]; kShrink [G, K, N]; kAdapt [K, N]; kAdaptT [N, K]
+  const void* u;           // kAdapt*: [*, R] low-rank rows, scale applied
+  const void* b;           // kAdapt*: [A, N, R]
+  const float* probs;      // kGated: [M] weight of each original position, or null
+  const float* scale;      // kShrink: [A] or null
+  const int4* rblist;      // row blocks (kAdapt*: of the FP32-pipe kernel only)
+  const RowInfo* rowinfo;  // kGated {token, position}; else {token, adapter}
+  const int4* segs;        // kAdapt*
+  const int2* blkseg;      // kAdapt*
+  WsHeader* hdr;
+  void* out;               // h [M, N], u [*, N], y [T, N] (rows in token order)
+  void* gate_up;           // kGated: [M, 2 N] or null
+  int64_t M, N, K, G, batch, max_row_blocks;
+  int32_t R;
+  int32_t n_blocks;
+  int32_t padded;          // kShrink: fill the last row block of an adapter with zeros to 64 rows
+  int32_t hold_release;
+  uint64_t wait_limit_ns;
+};
+
+cudaError_t launch_rows_simt(int dtype, RowsMode mode, RowsArgs a, int num_sms,
+                             cudaStream_t stream);
+
+// ------------------------------------------------------------ gradient of the gate
+
+struct GatedGradArgs {
+  const void* d_h;      // [M, F]
+  const void* gate_up;  // [M, 2F]
+  const float* probs;   // [M] by original position, or null
+  const int64_t* idx;   // [M]
+  WsHeader* hdr;
+  void* d_gate_up;      // [M, 2F]
+  void* h;              // [M, F] or null
+  float* d_probs;       // [M] by original position, or null
+  int64_t M, F;
+  int32_t row_idx_type;
+};
+cudaError_t launch_gated_grad(int dtype, const GatedGradArgs& a, bool vec, int num_sms,
+                              cudaStream_t stream);
+cudaError_t launch_index_prep(const int64_t* idx, int64_t M, int row_idx_type, int32_t* inv,
+                              WsHeader* hdr, int num_sms, cudaStream_t stream);
+
+}  // namespace pgg
