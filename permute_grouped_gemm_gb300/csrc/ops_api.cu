@@ -15,7 +15,8 @@ namespace pgg {
 namespace {
 
 constexpr int64_t kInt32Max = 2147483647;
-constexpr int kVariantSimt = 3;
+constexpr int kVariantWide = 0;  // tensor cores, row blocks of up to 256 rows on CTA pairs
+constexpr int kVariantSimt = 3;  // FP32 pipes: any dtype, size and alignment
 
 size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
@@ -67,9 +68,21 @@ int check_gated(int64_t M, int64_t F, int64_t K, int64_t G, int64_t L, int64_t b
   return PGG_OK;
 }
 
-int gated_plan(int64_t M, int64_t F, int64_t G, GatedPlan* p) {
+// 16-bit rows that the tensor-memory-access unit can stream, x rows (K elements) that 32-bit
+// offsets in 16-byte units can address.
+bool tensor_sizes(int dtype, int64_t rows, int64_t K, int64_t N) {
+  return dtype != PGG_F32 && K % 8 == 0 && N % 8 == 0 && rows * (K / 8) < 0xFFFFFFFFll;
+}
+
+int gated_plan(int64_t M, int64_t F, int64_t K, int64_t G, int64_t batch, int dtype,
+               GatedPlan* p) {
+  const int forced = forced_variant();
   p->variant = kVariantSimt;
   p->rows_per_block = 64;
+  if (forced != kVariantSimt && tensor_sizes(dtype, batch, K, F)) {
+    p->variant = kVariantWide;
+    p->rows_per_block = rows_wide_block();
+  }
   p->max_row_blocks = (M + p->rows_per_block - 1) / p->rows_per_block + (G < M ? G : M);
   if (p->max_row_blocks * ((F + 63) / 64) > kInt32Max) return PGG_ERR_SHAPE;  // 32-bit tile numbers
   Carver c;
@@ -104,6 +117,9 @@ int check_adapters(int64_t T, int64_t K, int64_t N, int64_t R, int64_t A, int dt
 int adapter_plan(int64_t T, int64_t K, int64_t N, int64_t R, int64_t A, int dtype, bool grad,
                  AdapterPlan* p) {
   p->variant = kVariantSimt;
+  if (forced_variant() != kVariantSimt && R % 8 == 0 && tensor_sizes(dtype, T, K, N) &&
+      tensor_sizes(dtype, T, N, K))
+    p->variant = kVariantWide;
   p->rb = 64;
   p->padded = grad ? 1 : 0;
   const int64_t groups = A + 1 < T ? A + 1 : T;
@@ -204,8 +220,11 @@ int run_adapt(const AdapterPlan& p, const AdapterTables& t, const HostEnv& env, 
   a.max_row_blocks = p.max_row_blocks;
   a.hold_release = env.hold_release;
   a.wait_limit_ns = env.wait_limit_ns;
-  return status_of(
-      launch_rows_simt(dtype, transposed ? kAdaptT : kAdapt, a, env.num_sms, stream));
+  const RowsMode mode = transposed ? kAdaptT : kAdapt;
+  if (p.variant == kVariantWide && aligned(x, 16) && aligned(w, 16) && aligned(f, 16) &&
+      aligned(y, 16))
+    return status_of(launch_rows_wide(dtype, mode, a, env.num_sms, stream));
+  return status_of(launch_rows_simt(dtype, mode, a, env.num_sms, stream));
 }
 
 }  // namespace
@@ -296,7 +315,7 @@ int pgg_swiglu_workspace_size(int64_t M, int64_t F, int64_t K, int64_t G, int64_
   int rc = check_gated(M, F, K, G, L, batch, topK, rowIdxType, dtype);
   if (rc != PGG_OK) return rc;
   GatedPlan p;
-  rc = gated_plan(M, F, G, &p);
+  rc = gated_plan(M, F, K, G, batch, dtype, &p);
   if (rc != PGG_OK) return rc;
   *workspace_bytes = p.total;
   return PGG_OK;
@@ -311,7 +330,7 @@ int pgg_swiglu_execute(const void* x, const void* weight, const int64_t* expande
   int rc = check_gated(M, F, K, G, L, batch, topK, rowIdxType, dtype);
   if (rc != PGG_OK) return rc;
   GatedPlan p;
-  rc = gated_plan(M, F, G, &p);
+  rc = gated_plan(M, F, K, G, batch, dtype, &p);
   if (rc != PGG_OK) return rc;
   const uintptr_t es = static_cast<uintptr_t>(elem_size(dtype));
   if (!aligned(workspace, 256) || !aligned(expandedRowIdx, 8) || !aligned(groupList, 8) ||
@@ -355,6 +374,11 @@ int pgg_swiglu_execute(const void* x, const void* weight, const int64_t* expande
   a.max_row_blocks = p.max_row_blocks;
   a.hold_release = env.hold_release;
   a.wait_limit_ns = env.wait_limit_ns;
+  // the tensor cores need 16-byte aligned rows; the FP32 pipes take any row blocks
+  const bool rows16 = aligned(x, 16) && aligned(weight, 16) && aligned(h, 16) &&
+                      aligned(gate_up, 16);
+  if (p.variant == kVariantWide && rows16)
+    return status_of(launch_rows_wide(dtype, kGated, a, env.num_sms, s));
   return status_of(launch_rows_simt(dtype, kGated, a, env.num_sms, s));
 }
 

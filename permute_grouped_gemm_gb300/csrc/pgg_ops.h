@@ -150,6 +150,14 @@ struct RowsArgs {
 cudaError_t launch_rows_simt(int dtype, RowsMode mode, RowsArgs a, int num_sms,
                              cudaStream_t stream);
 
+// Tensor cores, many rows per group (16-bit, every width a multiple of 8, 16-byte aligned).
+cudaError_t launch_rows_wide(int dtype, RowsMode mode, RowsArgs a, int num_sms,
+                             cudaStream_t stream);
+int rows_wide_block();
+int rows_wide_smem();
+int rows_wide_threads();
+int rows_wide_stages();
+
 // ------------------------------------------------------------ gradient of the gate
 
 struct GatedGradArgs {

@@ -1,0 +1,57 @@
+// Device pieces shared by the tensor-core kernels of the gated product and the adapters.
+#pragma once
+
+#include <cstdint>
+
+#include "pgg_ops.h"
+#include "pgg_ptx.cuh"
+
+namespace pgg {
+
+__device__ __forceinline__ void raise_status(WsHeader* hdr, uint32_t code, uint32_t site) {
+  if (atomicCAS(&hdr->status, 0u, code) == 0u) hdr->timeout_site = site;
+}
+
+// The preparation found the caller's routing or adapter ids not valid.
+__device__ __forceinline__ bool routing_failed(const WsHeader* hdr) {
+  const uint32_t st = hdr->status;
+  return st == kStIndex || st == kStGroupSum || st == kStNotPerm;
+}
+
+// Zeros to every element of the 16-bit outputs (the whole grid).
+__device__ __forceinline__ void zero_rows16(const RowsArgs& a) {
+  const int64_t n = a.M * a.N;
+  for (int64_t q = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; q < n;
+       q += static_cast<int64_t>(gridDim.x) * blockDim.x) {
+    static_cast<uint16_t*>(a.out)[q] = 0;
+    if (a.gate_up) {
+      static_cast<uint16_t*>(a.gate_up)[2 * q] = 0;
+      static_cast<uint16_t*>(a.gate_up)[2 * q + 1] = 0;
+    }
+  }
+}
+
+// p * silu(g) * u for a 16-bit output: the fast exponential and reciprocal, whose error (a few
+// 2^-21) is far below the one rounding of the result.
+__device__ __forceinline__ float gate(float g, float u, float p) {
+  return p * (g * __fdividef(1.0f, 1.0f + __expf(-g)) * u);
+}
+
+// Pair MMA (see ptx::mma_f16_pair) that leaves the accumulator lanes of the set mask bits as they
+// are: bit b of word i is lane 32 i + b of the pair's 256.
+__device__ __forceinline__ void mma_f16_pair_lanes(uint32_t d_tmem, uint64_t a_desc,
+                                                   uint64_t b_desc, uint32_t idesc,
+                                                   const uint32_t (&m)[8], uint32_t accumulate) {
+  asm volatile(
+      "{\n"
+      ".reg .pred p;\n"
+      "setp.ne.b32 p, %4, 0;\n"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3,"
+      " {%5, %6, %7, %8, %9, %10, %11, %12}, p;\n"
+      "}\n" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(m[0]), "r"(m[1]), "r"(m[2]),
+      "r"(m[3]), "r"(m[4]), "r"(m[5]), "r"(m[6]), "r"(m[7])
+      : "memory");
+}
+
+}  // namespace pgg

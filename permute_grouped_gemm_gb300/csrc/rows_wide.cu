@@ -1,0 +1,631 @@
+// Products over many ragged rows on tcgen05 tensor cores:
+//
+//     gated    [gate | up][i, :] = x[token(i), :] W[g(i)],  h = prob * silu(gate) * up
+//     adapt    y[t, :] = x[t, :] W + u[t, :] b[ad(t)]^T          (W [K, N], b [A, N, R])
+//     adaptT   the same with W given as [N, K]                   (the gradient of x)
+//
+// Tile: 256 rows x 256 accumulator columns on a pair of CTAs (cta_group::2),
+// reduced 64 at a time through six or seven stage slots; CTA r owns rows
+// 128 r .. 128 r + 127, whose fp32 accumulators (two buffers) sit in its tensor
+// memory. The rows of x are gathered by token with 16-byte cp.async, one warp
+// per stage slot; the weights come by TMA.
+//
+// gated: 128 of the accumulator's columns are gates and the other 128 the ups
+// that belong to them (each CTA loads one of the two operands), so a thread of
+// the epilogue finds both of its pair in its own lane, and neither is written
+// unless the caller keeps them: h alone is a third of what a product of
+// [M, 2F] and an activation over it would move.
+//
+// adapt: rows are taken in the order of their adapters, 256 at a time whatever
+// the adapters' borders, so that no row of the shared product is padding. The
+// low-rank part is more steps of the same reduction: for each adapter the tile
+// meets, the A operand is u and the B operand b[ad], and the MMA writes only
+// that adapter's accumulator lanes (disable-output-lane). Masking the output
+// and not the operand keeps what another adapter's weights hold (infinities,
+// NaN) out of the row: 0 * inf never happens. u is rounded to the dtype once
+// (it is an operand of the tensor cores), its sums are fp32.
+//
+// Warp roles per CTA: 0 TMA; 1 tensor-memory allocation and (even CTA) MMA
+// issue; one gather warp per stage slot; four epilogue warps. Tiles are
+// statically interleaved over the clusters. Waits are bounded; when one runs
+// out the kernel records PGG_ERR_TIMEOUT, drains its copies and MMAs, frees
+// tensor memory and returns.
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <cstdint>
+#include <cstring>
+
+#include "pgg_epilogue.cuh"
+#include "pgg_ops.h"
+#include "pgg_ops_mma.cuh"
+#include "pgg_ptx.cuh"
+
+namespace pgg {
+namespace {
+
+constexpr int kFM = 128;   // rows per CTA (the pair's MMA M is 256)
+constexpr int kFN = 256;   // accumulator columns per tile (MMA N)
+constexpr int kFK = 64;    // reduction per stage: one 128-byte row of A
+constexpr int kStages = 7;
+constexpr int kPanel = kFK * 128;   // MN-major B panel: 64 k rows x 128 bytes (64 n)
+constexpr int kABytes = kFM * 128;  // A: 128 rows x 128 bytes
+constexpr int kBBytes = 2 * kPanel; // B: this CTA's 128 columns, either major
+constexpr int kStageBytes = kABytes + kBBytes;
+constexpr int kGatherWarps = kStages;
+constexpr int kEpiWarps = 4;
+constexpr int kEpiWarp0 = 2 + kGatherWarps;
+constexpr int kThreads = 32 * (kEpiWarp0 + kEpiWarps);
+constexpr int kTmemCols = 512;
+constexpr int kAccCols = 256;
+
+struct WideCtl {
+  uint64_t full[kStages];   // even CTA: weight bytes of both CTAs + rows gathered in both
+  uint64_t empty[kStages];  // each CTA: MMAs of the stage done (multicast commit)
+  uint64_t tfull[2];        // each CTA: accumulator ready
+  uint64_t tempty[2];       // even CTA: accumulator drained (epilogue warps x 2 CTAs)
+  uint64_t drain;
+  uint32_t tmem_base;
+  int abort;
+};
+
+constexpr int kSmemBytes = kStages * kStageBytes + static_cast<int>(sizeof(WideCtl)) + 1024;
+static_assert(kSmemBytes <= 227 * 1024, "shared memory per CTA");
+
+__device__ __forceinline__ uint32_t cluster_id() { return blockIdx.x >> 1; }
+__device__ __forceinline__ uint32_t n_clusters() { return gridDim.x >> 1; }
+
+struct Tile {
+  int64_t g, row0, n0;  // row0: this CTA's first row; n0: first output column
+  int rows;             // this CTA's rows of the block (0 .. 128)
+  int steps;            // reduction steps, the low-rank ones included
+  int seg0;             // adapt: first adapter segment of the tile
+};
+
+template <int MODE>
+struct Shape {
+  static constexpr int kTileN = MODE == kGated ? 128 : 256;  // output columns of a tile
+};
+
+// Steps of the x W part, and per adapter segment.
+__device__ __forceinline__ int main_steps(const RowsArgs& a) {
+  return static_cast<int>((a.K + kFK - 1) / kFK);
+}
+__device__ __forceinline__ int rank_steps(const RowsArgs& a) { return (a.R + kFK - 1) / kFK; }
+
+template <int MODE>
+__device__ __forceinline__ Tile tile_of(uint32_t t, const RowsArgs& a, uint32_t rank) {
+  const uint32_t rb = t / static_cast<uint32_t>(a.n_blocks);
+  Tile x;
+  x.n0 = static_cast<int64_t>(t - rb * static_cast<uint32_t>(a.n_blocks)) * Shape<MODE>::kTileN;
+  x.steps = main_steps(a);
+  x.seg0 = 0;
+  int left;
+  if constexpr (MODE == kGated) {
+    int4 e = a.rblist[check_index(a.hdr, rb, a.max_row_blocks, 80)];
+    if (!check_ok(a.hdr,
+                  e.x >= 0 && e.x < a.G && e.y >= 0 && e.z >= 0 &&
+                      static_cast<int64_t>(e.y) + e.z <= a.M,
+                  81))
+      e = make_int4(0, 0, 0, 0);
+    x.g = e.x;
+    x.row0 = static_cast<int64_t>(e.y) + kFM * rank;
+    left = e.z - kFM * static_cast<int>(rank);
+  } else {
+    x.g = 0;
+    x.row0 = static_cast<int64_t>(rb) * (2 * kFM) + kFM * rank;
+    const int64_t l = a.M - x.row0;
+    left = l > kFM ? kFM : static_cast<int>(l);
+    const int2 s = a.blkseg[rb];
+    x.seg0 = s.x;
+    x.steps += s.y * rank_steps(a);
+  }
+  x.rows = left < 0 ? 0 : (left > kFM ? kFM : left);
+  return x;
+}
+
+// Segment and first rank of low-rank step e of a tile.
+__device__ __forceinline__ int4 segment_of(const RowsArgs& a, const Tile& x, int e, int* r0) {
+  const int rs = rank_steps(a);
+  const int s = e / rs;
+  *r0 = (e - s * rs) * kFK;
+  return a.segs[x.seg0 + s];
+}
+
+// Weight bytes that CTA `rank` loads for one main or low-rank step of a tile.
+template <int MODE>
+__device__ __forceinline__ uint32_t w_bytes(const RowsArgs& a, int64_t n0, uint32_t rank,
+                                            bool low_rank) {
+  if constexpr (MODE == kGated) {
+    return n0 + 64 < a.N ? 2u * kPanel : static_cast<uint32_t>(kPanel);
+  } else {
+    const int64_t nc = n0 + 128 * rank;
+    if (MODE == kAdaptT || low_rank) return nc < a.N ? static_cast<uint32_t>(kBBytes) : 0u;
+    uint32_t b = 0;
+    for (int j = 0; j < 2; ++j) b += (nc + 64 * j < a.N) ? static_cast<uint32_t>(kPanel) : 0u;
+    return b;
+  }
+}
+
+template <int MODE>
+__device__ void w_producer(uint8_t* smem, WideCtl* ctl, const CUtensorMap* tm_w,
+                           const CUtensorMap* tm_b, const RowsArgs& a, uint32_t total,
+                           uint32_t rank) {
+  const uint64_t lim = a.wait_limit_ns;
+  volatile int* abort = &ctl->abort;
+  const bool leader = rank == 0;
+  const int nks = main_steps(a);
+  int stage = 0;
+  uint32_t phase = 0, outstanding = 0, last_parity = 0;
+  bool failed = false;
+  for (uint32_t t = cluster_id(); t < total && !failed; t += n_clusters()) {
+    const Tile x = tile_of<MODE>(t, a, rank);
+    const int64_t nc = x.n0 + 128 * rank;
+    for (int ks = 0; ks < x.steps; ++ks) {
+      const bool low = MODE != kGated && ks >= nks;
+      int4 seg = make_int4(0, 0, 0, 0);
+      int r0 = 0;
+      if (low) seg = segment_of(a, x, ks - nks, &r0);
+      if (!ptx::mbar_wait_cluster(&ctl->empty[stage], phase ^ 1u, lim, abort)) {
+        failed = true;
+        break;
+      }
+      uint8_t* sb = smem + stage * kStageBytes + kABytes;
+      const uint32_t fb = ptx::mapa(&ctl->full[stage], 0);
+      if (leader)
+        ptx::mbar_arrive_expect_tx(
+            &ctl->full[stage], w_bytes<MODE>(a, x.n0, 0, low) + w_bytes<MODE>(a, x.n0, 1, low));
+      if constexpr (MODE == kGated) {
+        // the even CTA loads the gates' columns, the odd one the ups'
+        const int32_t c0 = static_cast<int32_t>(x.n0 + (rank ? a.N : 0));
+        for (int j = 0; j < 2; ++j)
+          if (x.n0 + 64 * j < a.N)
+            ptx::tma_load_3d_pair(sb + j * kPanel, tm_w, fb, c0 + 64 * j, ks * kFK,
+                                  static_cast<int32_t>(x.g));
+      } else if (low) {
+        if (nc < a.N)
+          ptx::tma_load_3d_pair(sb, tm_b, fb, r0, static_cast<int32_t>(nc), seg.x);
+      } else if constexpr (MODE == kAdaptT) {
+        if (nc < a.N)
+          ptx::tma_load_3d_pair(sb, tm_w, fb, ks * kFK, static_cast<int32_t>(nc), 0);
+      } else {
+        for (int j = 0; j < 2; ++j)
+          if (nc + 64 * j < a.N)
+            ptx::tma_load_3d_pair(sb + j * kPanel, tm_w, fb, static_cast<int32_t>(nc + 64 * j),
+                                  ks * kFK, 0);
+      }
+      outstanding |= 1u << stage;
+      last_parity = (last_parity & ~(1u << stage)) | (phase << stage);
+      if (++stage == kStages) {
+        stage = 0;
+        phase ^= 1u;
+      }
+    }
+  }
+  if (failed) {
+    ctl->abort = 1;
+    raise_status(a.hdr, kStTimeout, 32);
+  }
+  if (leader) {
+    int no_abort = 0;
+    for (int s = 0; s < kStages; ++s)
+      if (outstanding & (1u << s))
+        ptx::mbar_wait_cluster(&ctl->full[s], (last_parity >> s) & 1u, lim, &no_abort);
+  }
+}
+
+// Gather warp w fills stage slot w: the CTA's stages w, w + S, ... in the
+// sequence of all steps of all its tiles. Rows lane >> 3 + 4 q, 16-byte chunk lane & 7.
+template <int MODE>
+__device__ void x_gatherer(uint8_t* smem, WideCtl* ctl, const RowsArgs& a, uint32_t total,
+                           uint32_t rank) {
+  const uint64_t lim = a.wait_limit_ns;
+  volatile int* abort = &ctl->abort;
+  const int w = (threadIdx.x >> 5) - 2;
+  const int lane = threadIdx.x & 31;
+  const int c = lane & 7;
+  const char* xb = static_cast<const char*>(a.x);
+  const uint32_t sa_slot = ptx::smem_addr(smem + w * kStageBytes);
+  const uint32_t full = ptx::mapa(&ctl->full[w], 0);
+  const int nks = main_steps(a);
+  uint32_t phase = 0;
+  bool failed = false;
+  int kb = w;  // the warp's next step, counted from the start of tile t
+  // this lane's rows (lane >> 3) + 4 q of the tile: the x row's offset in
+  // 16-byte units, or kNoRow past the block
+  constexpr uint32_t kNoRow = 0xFFFFFFFFu;
+  const uint32_t row_units = static_cast<uint32_t>(a.K / 8);
+  uint32_t row16[kFM / 4];
+  for (uint32_t t = cluster_id(); t < total && !failed; t += n_clusters()) {
+    const Tile x = tile_of<MODE>(t, a, rank);
+    if (kb < x.steps) {
+      int32_t tok[4];
+#pragma unroll
+      for (int h = 0; h < 4; ++h) {
+        const int r = lane + 32 * h;
+        tok[h] = r < x.rows ? static_cast<int32_t>(check_index(
+                                  a.hdr, a.rowinfo[check_index(a.hdr, x.row0 + r, a.M, 82)].token,
+                                  a.batch, 83))
+                            : -1;
+      }
+#pragma unroll
+      for (int q = 0; q < kFM / 4; ++q) {
+        const int rr = (lane >> 3) + 4 * q;
+        const int32_t tk = __shfl_sync(0xFFFFFFFFu, tok[rr >> 5], rr & 31);
+        row16[q] = tk >= 0 ? static_cast<uint32_t>(tk) * row_units : kNoRow;
+      }
+    }
+    for (; kb < x.steps; kb += kStages) {
+      if (!ptx::mbar_wait_cluster(&ctl->empty[w], phase ^ 1u, lim, abort)) {
+        failed = true;
+        break;
+      }
+      if (MODE == kGated || kb < nks) {
+        const int64_t k = static_cast<int64_t>(kb) * kFK + c * 8;
+        const bool k_ok = k < a.K;
+        const char* xk = xb + k * 2;
+#pragma unroll
+        for (int q = 0; q < kFM / 4; ++q) {
+          const int rr = (lane >> 3) + 4 * q;
+          const bool ok = k_ok && row16[q] != kNoRow;
+          const void* src = ok ? static_cast<const void*>(
+                                     xk + (static_cast<uint64_t>(row16[q]) << 4))
+                               : static_cast<const void*>(xb);
+          ptx::cp_async_16(sa_slot + rr * 128 + ((c ^ (rr & 7)) << 4), src, ok ? 16u : 0u);
+        }
+      } else {
+        // rows of u that belong to the step's adapter; zeros elsewhere
+        int r0;
+        const int4 seg = segment_of(a, x, kb - nks, &r0);
+        const int64_t r = r0 + c * 8;
+        const char* ub = static_cast<const char*>(a.u);
+#pragma unroll 4
+        for (int q = 0; q < kFM / 4; ++q) {
+          const int rr = (lane >> 3) + 4 * q;
+          const int64_t row = x.row0 + rr;
+          const bool ok = r < a.R && rr < x.rows && row >= seg.y && row < seg.z;
+          const void* src = ok ? static_cast<const void*>(
+                                     ub + ((seg.w + (row - seg.y)) * a.R + r) * 2)
+                               : static_cast<const void*>(ub);
+          ptx::cp_async_16(sa_slot + rr * 128 + ((c ^ (rr & 7)) << 4), src, ok ? 16u : 0u);
+        }
+      }
+      ptx::cp_async_commit();
+      ptx::cp_async_wait<0>();
+      ptx::fence_proxy_async_smem();
+      __syncwarp();
+      // the even CTA's own rows go to its own MMA thread: CTA scope suffices
+      if (lane == 0) {
+        if (rank == 0)
+          ptx::mbar_arrive(&ctl->full[w]);
+        else
+          ptx::mbar_arrive_remote(full);
+      }
+      phase ^= 1u;
+    }
+    kb -= x.steps;
+  }
+  ptx::cp_async_wait<0>();
+  if (failed) {
+    ctl->abort = 1;
+    if (lane == 0) raise_status(a.hdr, kStTimeout, 33);
+  }
+}
+
+// Lanes of the pair's 256 that lie outside rows [lo, hi) of the tile, as the eight words of a
+// disable-output-lane mask.
+__device__ __forceinline__ void lane_mask(int lo, int hi, uint32_t (&m)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int l = lo - 32 * i, h = hi - 32 * i;
+    const uint32_t below = l <= 0 ? 0u : (l >= 32 ? 0xFFFFFFFFu : (1u << l) - 1u);
+    const uint32_t upto = h <= 0 ? 0u : (h >= 32 ? 0xFFFFFFFFu : (1u << h) - 1u);
+    m[i] = ~(upto & ~below);
+  }
+}
+
+template <int DT, int MODE>
+__device__ void mma_issuer(uint8_t* smem, WideCtl* ctl, uint32_t tmem_base, const RowsArgs& a,
+                           uint32_t total) {
+  constexpr uint32_t kFmt = DT == PGG_BF16 ? 1u : 0u;
+  constexpr uint32_t idesc_k = ptx::idesc_make(kFmt, 2 * kFM, kFN);  // both operands K-major
+  constexpr uint32_t idesc_mn = idesc_k | (1u << 16);                // B MN-major
+  const uint64_t lim = a.wait_limit_ns;
+  volatile int* abort = &ctl->abort;
+  const int nks = main_steps(a);
+  int stage = 0, acc = 0;
+  uint32_t phase = 0, aph = 0;
+  bool issued = false, failed = false;
+  for (uint32_t t = cluster_id(); t < total && !failed; t += n_clusters()) {
+    const Tile x = tile_of<MODE>(t, a, 0);
+    if (!ptx::mbar_wait_cluster(&ctl->tempty[acc], aph ^ 1u, lim, abort)) {
+      failed = true;
+      break;
+    }
+    ptx::tc_fence_after_sync();
+    const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * kAccCols);
+    for (int ks = 0; ks < x.steps; ++ks) {
+      const bool low = MODE != kGated && ks >= nks;
+      int4 seg = make_int4(0, 0, 0, 0);
+      int r0 = 0;
+      if (low) seg = segment_of(a, x, ks - nks, &r0);
+      if (!ptx::mbar_wait_cluster(&ctl->full[stage], phase, lim, abort)) {
+        failed = true;
+        break;
+      }
+      ptx::tc_fence_after_sync();
+      const uint32_t sa = ptx::smem_addr(smem + stage * kStageBytes);
+      const uint64_t da = ptx::sdesc_sw128(sa);
+      if (low) {
+        const uint64_t db = ptx::sdesc_sw128(sa + kABytes);
+        uint32_t m[8];
+        lane_mask(static_cast<int>(seg.y - x.row0), static_cast<int>(seg.z - x.row0), m);
+#pragma unroll
+        for (int kk = 0; kk < kFK / 16; ++kk)
+          if (r0 + 16 * kk < a.R) {
+            const uint64_t off = static_cast<uint64_t>((kk * 32) >> 4);
+            mma_f16_pair_lanes(d_tmem, da + off, db + off, idesc_k, m, 1u);
+          }
+      } else if constexpr (MODE == kAdaptT) {
+        const uint64_t db = ptx::sdesc_sw128(sa + kABytes);
+#pragma unroll
+        for (int kk = 0; kk < kFK / 16; ++kk) {
+          const uint64_t off = static_cast<uint64_t>((kk * 32) >> 4);
+          ptx::mma_f16_pair(d_tmem, da + off, db + off, idesc_k, (ks > 0 || kk > 0) ? 1u : 0u);
+        }
+      } else {
+        const uint64_t db = ptx::sdesc_sw128_mn(sa + kABytes, kPanel);
+#pragma unroll
+        for (int kk = 0; kk < kFK / 16; ++kk) {
+          const uint64_t a_off = static_cast<uint64_t>((kk * 32) >> 4);        // 16 k: 32 bytes
+          const uint64_t b_off = static_cast<uint64_t>((kk * 16 * 128) >> 4);  // 16 k rows
+          ptx::mma_f16_pair(d_tmem, da + a_off, db + b_off, idesc_mn,
+                            (ks > 0 || kk > 0) ? 1u : 0u);
+        }
+      }
+      issued = true;
+      ptx::mma_commit_pair(&ctl->empty[stage], 0x3);
+      if (++stage == kStages) {
+        stage = 0;
+        phase ^= 1u;
+      }
+    }
+    if (failed) break;
+    ptx::mma_commit_pair(&ctl->tfull[acc], 0x3);
+    acc ^= 1;
+    if (acc == 0) aph ^= 1u;
+  }
+  if (failed) {
+    ctl->abort = 1;
+    raise_status(a.hdr, kStTimeout, 34);
+  }
+  if (issued) {
+    int no_abort = 0;
+    ptx::mma_commit_pair(&ctl->drain, 0x1);
+    ptx::mbar_wait(&ctl->drain, 0u, lim, &no_abort);
+  }
+}
+
+// 32 lanes' rows x 64 columns of 16-bit values (b: each lane its own row's 128 bytes) to rows
+// `row` (each lane's own, -1 = not written) of a row-major [*, ld] output, columns col ..
+// col + 63 below `ncols`: after the transpose every warp store covers four rows' full segments.
+__device__ __forceinline__ void store_rows(uint4 (&b)[8], void* out, int64_t row, int64_t ld,
+                                           int64_t base, int64_t col, int64_t ncols, int lane) {
+  transpose8(b, lane);
+  const int bg = lane >> 3;
+  const int64_t c = col + (lane & 7) * 8;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const int64_t r = __shfl_sync(0xFFFFFFFFu, row, 8 * bg + j);
+    if (r >= 0 && c < ncols)
+      *reinterpret_cast<uint4*>(static_cast<char*>(out) + (r * ld + base + c) * 2) = b[j];
+  }
+}
+
+template <int DT, int MODE>
+__device__ void epilogue(WideCtl* ctl, uint32_t tmem_base, const RowsArgs& a, uint32_t total,
+                         uint32_t rank) {
+  const uint64_t lim = a.wait_limit_ns;
+  volatile int* abort = &ctl->abort;
+  const int lane = threadIdx.x & 31;
+  const int quarter = (threadIdx.x >> 5) & 3;  // accumulator lanes (rows) 32 q .. 32 q + 31
+  const uint32_t tempty0 = ptx::mapa(&ctl->tempty[0], 0);
+  const uint32_t tempty1 = ptx::mapa(&ctl->tempty[1], 0);
+  int acc = 0;
+  uint32_t aph = 0;
+  bool held = a.hold_release != 0;  // (test hook: the first release is withheld)
+  for (uint32_t t = cluster_id(); t < total; t += n_clusters()) {
+    const Tile x = tile_of<MODE>(t, a, rank);
+    const int valid = x.rows - 32 * quarter;  // rows of this warp's 32 that exist
+    int64_t row = -1;                         // output row of this lane
+    float p = 1.0f;
+    if (lane < valid) {
+      row = x.row0 + 32 * quarter + lane;
+      const RowInfo ri = a.rowinfo[check_index(a.hdr, row, a.M, 84)];
+      if constexpr (MODE == kGated) {
+        if (a.probs) p = a.probs[check_index(a.hdr, ri.rank, a.M, 85)];
+      } else {
+        row = check_index(a.hdr, ri.token, a.batch, 86);
+      }
+    }
+    const bool ok = ptx::mbar_wait_cluster(&ctl->tfull[acc], aph, lim, abort);
+    if (!__all_sync(0xFFFFFFFFu, ok)) {
+      if (lane == 0) {
+        ctl->abort = 1;
+        raise_status(a.hdr, kStTimeout, 35);
+      }
+      break;
+    }
+    ptx::tc_fence_after_sync();
+    const uint32_t t_lane = tmem_base + (static_cast<uint32_t>(32 * quarter) << 16) +
+                            static_cast<uint32_t>(acc * kAccCols);
+#pragma unroll 1
+    for (int c0 = 0; c0 < Shape<MODE>::kTileN && x.n0 + c0 < a.N && valid > 0; c0 += 64) {
+      uint4 b[8];
+      if constexpr (MODE == kGated) {
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          uint32_t g[32], u[32];
+          ptx::tmem_ld_32x32b_x32(t_lane + static_cast<uint32_t>(c0 + 32 * half), g);
+          ptx::tmem_ld_32x32b_x32(t_lane + static_cast<uint32_t>(128 + c0 + 32 * half), u);
+          ptx::tmem_ld_wait_regs(g);
+          ptx::tmem_ld_wait_regs(u);
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            u[i] = __float_as_uint(gate(__uint_as_float(g[i]), __uint_as_float(u[i]), p));
+#pragma unroll
+          for (int q = 0; q < 4; ++q) b[4 * half + q] = pack8<DT>(u + 8 * q);
+        }
+        store_rows(b, a.out, row, a.N, 0, x.n0 + c0, a.N, lane);
+        if (a.gate_up) {
+          chunk_blocks<DT>(t_lane + static_cast<uint32_t>(c0), false, b);
+          store_rows(b, a.gate_up, row, 2 * a.N, 0, x.n0 + c0, a.N, lane);
+          chunk_blocks<DT>(t_lane + static_cast<uint32_t>(128 + c0), false, b);
+          store_rows(b, a.gate_up, row, 2 * a.N, a.N, x.n0 + c0, a.N, lane);
+        }
+      } else {
+        chunk_blocks<DT>(t_lane + static_cast<uint32_t>(c0), false, b);
+        store_rows(b, a.out, row, a.N, 0, x.n0 + c0, a.N, lane);
+      }
+    }
+    ptx::tc_fence_before_sync();
+    __syncwarp();
+    // tensor memory changes hands (the output goes out through global memory,
+    // not to the MMA thread): CTA scope
+    if (lane == 0 && !held) ptx::mbar_arrive_remote_cta(acc ? tempty1 : tempty0);
+    held = false;
+    acc ^= 1;
+    if (acc == 0) aph ^= 1u;
+  }
+}
+
+template <int DT, int MODE>
+__global__ void __launch_bounds__(kThreads, 1)
+    rows_wide_kernel(const __grid_constant__ CUtensorMap tm_w,
+                     const __grid_constant__ CUtensorMap tm_b, const RowsArgs a) {
+  ptx::griddep_wait();  // launched with programmatic serialization: predecessors done
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  auto* ctl = reinterpret_cast<WideCtl*>(smem + kStages * kStageBytes);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = ptx::cluster_ctarank();
+
+  if (routing_failed(a.hdr)) {  // the result is defined as zeros
+    zero_rows16(a);
+    return;
+  }
+  const uint32_t row_blocks = MODE == kGated
+                                  ? a.hdr->n_row_blocks
+                                  : static_cast<uint32_t>((a.M + 2 * kFM - 1) / (2 * kFM));
+  const uint32_t total = row_blocks * static_cast<uint32_t>(a.n_blocks);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      ptx::mbar_init(&ctl->full[s], 3);
+      ptx::mbar_init(&ctl->empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      ptx::mbar_init(&ctl->tfull[b], 1);
+      ptx::mbar_init(&ctl->tempty[b], 2 * kEpiWarps);
+    }
+    ptx::mbar_init(&ctl->drain, 1);
+    ctl->abort = 0;
+    ptx::fence_mbar_init();
+  }
+  if (warp == 0 && lane == 0) {
+    ptx::tma_prefetch_desc(&tm_w);
+    if (MODE != kGated) ptx::tma_prefetch_desc(&tm_b);
+  }
+  if (warp == 1) {
+    ptx::tmem_alloc_pair(&ctl->tmem_base, kTmemCols);
+    ptx::tmem_relinquish_pair();
+  }
+  ptx::tc_fence_before_sync();
+  __syncthreads();
+  ptx::cluster_sync();
+  ptx::tc_fence_after_sync();
+  const uint32_t tmem_base = ctl->tmem_base;
+
+  if (warp == 0) {
+    if (lane == 0) w_producer<MODE>(smem, ctl, &tm_w, &tm_b, a, total, rank);
+  } else if (warp == 1) {
+    if (lane == 0 && rank == 0) mma_issuer<DT, MODE>(smem, ctl, tmem_base, a, total);
+  } else if (warp < kEpiWarp0) {
+    x_gatherer<MODE>(smem, ctl, a, total, rank);
+  } else {
+    epilogue<DT, MODE>(ctl, tmem_base, a, total, rank);
+  }
+
+  ptx::tc_fence_before_sync();
+  __syncthreads();
+  ptx::cluster_sync();
+  if (warp == 1) {
+    ptx::tc_fence_after_sync();
+    ptx::tmem_dealloc_pair(tmem_base, kTmemCols);
+  }
+}
+
+template <int DT>
+cudaError_t launch_t(RowsMode mode, const CUtensorMap& tm_w, const CUtensorMap& tm_b,
+                     const RowsArgs& a, int64_t max_tiles, int num_sms, cudaStream_t stream) {
+  using K = void (*)(const CUtensorMap, const CUtensorMap, const RowsArgs);
+  const K kern = mode == kGated   ? K(rows_wide_kernel<DT, kGated>)
+                 : mode == kAdapt ? K(rows_wide_kernel<DT, kAdapt>)
+                                  : K(rows_wide_kernel<DT, kAdaptT>);
+  cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         kSmemBytes);
+  if (err != cudaSuccess) return err;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.dynamicSmemBytes = kSmemBytes;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int64_t want = max_tiles < num_sms / 2 ? max_tiles : num_sms / 2;
+  if (want < 1) want = 1;
+  cfg.gridDim = dim3(static_cast<unsigned>(2 * want), 1, 1);
+  int clusters = 0;
+  err = cudaOccupancyMaxActiveClusters(&clusters, kern, &cfg);
+  if (err != cudaSuccess) return err;
+  if (clusters < 1) return cudaErrorInvalidConfiguration;
+  return launch_pdl(kern, dim3(static_cast<unsigned>(2 * (clusters < want ? clusters : want))),
+                    dim3(kThreads), static_cast<size_t>(kSmemBytes), stream, 2, tm_w, tm_b, a);
+}
+
+}  // namespace
+
+cudaError_t launch_rows_wide(int dtype, RowsMode mode, RowsArgs a, int num_sms,
+                             cudaStream_t stream) {
+  const int64_t tile_n = mode == kGated ? 128 : 256;
+  a.n_blocks = static_cast<int32_t>((a.N + tile_n - 1) / tile_n);
+  CUtensorMap tm_w, tm_b;
+  std::memset(&tm_b, 0, sizeof(tm_b));
+  bool ok;
+  if (mode == kGated)
+    ok = encode_map_3d(&tm_w, dtype, a.w, 2 * a.N, a.K, a.G, kFK);
+  else if (mode == kAdapt)
+    ok = encode_map_3d(&tm_w, dtype, a.w, a.N, a.K, 1, kFK);
+  else
+    ok = encode_map_3d(&tm_w, dtype, a.w, a.K, a.N, 1, 128);
+  if (ok && mode != kGated) ok = encode_map_3d(&tm_b, dtype, a.b, a.R, a.N, a.G, 128);
+  if (!ok) return cudaErrorInvalidValue;
+  const int64_t row_blocks = mode == kGated ? a.max_row_blocks : (a.M + 2 * kFM - 1) / (2 * kFM);
+  const int64_t tiles = row_blocks * a.n_blocks;
+  if (dtype == PGG_BF16) return launch_t<PGG_BF16>(mode, tm_w, tm_b, a, tiles, num_sms, stream);
+  if (dtype == PGG_F16) return launch_t<PGG_F16>(mode, tm_w, tm_b, a, tiles, num_sms, stream);
+  return cudaErrorInvalidValue;
+}
+
+int rows_wide_block() { return 2 * kFM; }
+int rows_wide_smem() { return kSmemBytes; }
+int rows_wide_threads() { return kThreads; }
+int rows_wide_stages() { return kStages; }
+
+}  // namespace pgg
