@@ -1,6 +1,7 @@
 // C ABI of the router, the gated product and the adapters (include/pgg.h):
 // argument validation, workspace layouts, the choice of kernel and the launches.
 
+#include <cmath>
 #include <cstdint>
 #include <cstring>
 
@@ -16,7 +17,14 @@ namespace {
 
 constexpr int64_t kInt32Max = 2147483647;
 constexpr int kVariantWide = 0;  // tensor cores, row blocks of up to 256 rows on CTA pairs
+constexpr int kVariantSkinny = 1;  // tensor cores, few rows per block, the weight streamed
 constexpr int kVariantSimt = 3;  // FP32 pipes: any dtype, size and alignment
+
+// Gated product: up to this many rows per live expert the weights bound it and are streamed once
+// per block of rows; beyond, the tensor cores do.
+constexpr double kSkinnyRows = 64.0;
+// Adapters: up to this many tokens the shared weight is streamed once for all of them.
+constexpr int64_t kSkinnyTokens = 64;
 
 size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
@@ -55,6 +63,7 @@ struct GatedPlan {
   int variant;
   int rows_per_block;
   int64_t max_row_blocks;
+  int64_t live_blocks;  // about how many row blocks an even routing gives
   size_t rblist, rowinfo, inv, total;
 };
 
@@ -79,9 +88,22 @@ int gated_plan(int64_t M, int64_t F, int64_t K, int64_t G, int64_t batch, int dt
   const int forced = forced_variant();
   p->variant = kVariantSimt;
   p->rows_per_block = 64;
+  p->live_blocks = 0;
   if (forced != kVariantSimt && tensor_sizes(dtype, batch, K, F)) {
-    p->variant = kVariantWide;
+    const double topK = static_cast<double>(M) / static_cast<double>(batch);
+    const double miss = topK >= G ? 0.0 : 1.0 - topK / static_cast<double>(G);
+    const double live = G * (1.0 - std::pow(miss, static_cast<double>(batch)));
+    const double rows = M / live;  // per live expert, if the routing is even
+    p->variant = forced == kVariantWide || (forced != kVariantSkinny && rows > kSkinnyRows)
+                     ? kVariantWide
+                     : kVariantSkinny;
     p->rows_per_block = rows_wide_block();
+    if (p->variant == kVariantSkinny) {
+      // room for twice the even share, but an expert has at most one row of a token
+      const double want = 2.0 * rows < static_cast<double>(batch) ? 2.0 * rows : batch;
+      p->rows_per_block = want <= 16 ? 16 : want <= 32 ? 32 : want <= 64 ? 64 : 128;
+      p->live_blocks = static_cast<int64_t>(live * std::ceil(rows / p->rows_per_block) + 0.5);
+    }
   }
   p->max_row_blocks = (M + p->rows_per_block - 1) / p->rows_per_block + (G < M ? G : M);
   if (p->max_row_blocks * ((F + 63) / 64) > kInt32Max) return PGG_ERR_SHAPE;  // 32-bit tile numbers
@@ -117,12 +139,18 @@ int check_adapters(int64_t T, int64_t K, int64_t N, int64_t R, int64_t A, int dt
 int adapter_plan(int64_t T, int64_t K, int64_t N, int64_t R, int64_t A, int dtype, bool grad,
                  AdapterPlan* p) {
   p->variant = kVariantSimt;
-  if (forced_variant() != kVariantSimt && R % 8 == 0 && tensor_sizes(dtype, T, K, N) &&
-      tensor_sizes(dtype, T, N, K))
-    p->variant = kVariantWide;
-  p->rb = 64;
-  p->padded = grad ? 1 : 0;
+  const int forced = forced_variant();
   const int64_t groups = A + 1 < T ? A + 1 : T;
+  p->rb = 64;
+  if (forced != kVariantSimt && R % 8 == 0 && tensor_sizes(dtype, T, K, N) &&
+      tensor_sizes(dtype, T, N, K)) {
+    p->variant = !grad && (forced == kVariantSkinny || (forced != kVariantWide && T <= kSkinnyTokens))
+                     ? kVariantSkinny
+                     : kVariantWide;
+    // low-rank rows: blocks of 16 when adapters have about that many tokens
+    p->rb = !grad && T <= 16 * groups ? 16 : 128;
+  }
+  p->padded = grad ? 1 : 0;
   p->max_row_blocks = (T + p->rb - 1) / p->rb + groups;
   p->rows_u = grad ? T + 63 * groups : T;
   const int64_t widest = N > K ? N : K;
@@ -137,7 +165,7 @@ int adapter_plan(int64_t T, int64_t K, int64_t N, int64_t R, int64_t A, int dtyp
   p->segs = c.take(static_cast<int64_t>(sizeof(int4)) * A);
   p->blkseg = c.take(static_cast<int64_t>(sizeof(int2)) * ((T + 255) / 256));
   p->counts = c.take(p->blocks > 1 ? 4 * (A + 1) * (p->blocks + 2) : 0);
-  p->u = c.take(p->rows_u * R * elem_size(dtype));
+  p->u = c.take(p->rows_u * R * (p->variant == kVariantSkinny ? 4 : elem_size(dtype)));
   p->v = c.take(grad ? p->rows_u * R * elem_size(dtype) : 0);
   p->total = c.used;
   return PGG_OK;
@@ -171,10 +199,11 @@ int run_adapter_prep(const AdapterPlan& p, const AdapterTables& t, const int64_t
   return status_of(launch_adapter_prep(a, stream));
 }
 
-// u = scale * x f[adapter] for f [A, K, R], into rows of `u`.
+// u = scale * x f[adapter] for f [A, K, R], into rows of `u`: of the dtype in the adapters' order,
+// or (by_token) fp32 in the tokens' order.
 int run_shrink(const AdapterPlan& p, const AdapterTables& t, const HostEnv& env, const void* x,
                const void* f, const float* scale, void* u, int64_t T, int64_t K, int64_t R,
-               int64_t A, int dtype, cudaStream_t stream) {
+               int64_t A, int dtype, bool by_token, cudaStream_t stream) {
   RowsArgs a;
   std::memset(&a, 0, sizeof(a));
   a.x = x;
@@ -191,13 +220,20 @@ int run_shrink(const AdapterPlan& p, const AdapterTables& t, const HostEnv& env,
   a.batch = T;
   a.max_row_blocks = p.max_row_blocks;
   a.padded = p.padded;
+  a.u_by_token = by_token ? 1 : 0;
+  a.hold_release = env.hold_release;
   a.wait_limit_ns = env.wait_limit_ns;
+  if (p.variant != kVariantSimt && aligned(x, 16) && aligned(f, 16)) {
+    const int64_t live = (T + p.rb - 1) / p.rb + (A < T ? A : T) / 2;
+    return status_of(launch_rows_skinny(dtype, kShrink, p.rb, a, live, env.num_sms, stream));
+  }
   return status_of(launch_rows_simt(dtype, kShrink, a, env.num_sms, stream));
 }
 
-// y = x W + u f[adapter]^T for W [K, N] (transposed: [N, K]) and f [A, N, R].
+// y = x W + u f[adapter]^T for W [K, N] (transposed: [N, K]) and f [A, N, R]. by_token: the
+// adapter ids when u is fp32 in the tokens' order, else null.
 int run_adapt(const AdapterPlan& p, const AdapterTables& t, const HostEnv& env, bool transposed,
-              const void* x, const void* w, const void* u, const void* f, void* y, int64_t T,
+              const int64_t* by_token, const void* x, const void* w, const void* u, const void* f, void* y, int64_t T,
               int64_t K, int64_t N, int64_t R, int64_t A, int dtype, cudaStream_t stream) {
   RowsArgs a;
   std::memset(&a, 0, sizeof(a));
@@ -221,7 +257,13 @@ int run_adapt(const AdapterPlan& p, const AdapterTables& t, const HostEnv& env, 
   a.hold_release = env.hold_release;
   a.wait_limit_ns = env.wait_limit_ns;
   const RowsMode mode = transposed ? kAdaptT : kAdapt;
-  if (p.variant == kVariantWide && aligned(x, 16) && aligned(w, 16) && aligned(f, 16) &&
+  if (by_token) {
+    a.adapter = by_token;
+    const int nr = T <= 16 ? 16 : 64;
+    return status_of(launch_rows_skinny(dtype, mode, nr, a, (T + nr - 1) / nr, env.num_sms,
+                                        stream));
+  }
+  if (p.variant != kVariantSimt && aligned(x, 16) && aligned(w, 16) && aligned(f, 16) &&
       aligned(y, 16))
     return status_of(launch_rows_wide(dtype, mode, a, env.num_sms, stream));
   return status_of(launch_rows_simt(dtype, mode, a, env.num_sms, stream));
@@ -377,6 +419,9 @@ int pgg_swiglu_execute(const void* x, const void* weight, const int64_t* expande
   // the tensor cores need 16-byte aligned rows; the FP32 pipes take any row blocks
   const bool rows16 = aligned(x, 16) && aligned(weight, 16) && aligned(h, 16) &&
                       aligned(gate_up, 16);
+  if (p.variant == kVariantSkinny && rows16)
+    return status_of(launch_rows_skinny(dtype, kGated, p.rows_per_block, a, p.live_blocks,
+                                        env.num_sms, s));
   if (p.variant == kVariantWide && rows16)
     return status_of(launch_rows_wide(dtype, kGated, a, env.num_sms, s));
   return status_of(launch_rows_simt(dtype, kGated, a, env.num_sms, s));
@@ -465,9 +510,12 @@ int pgg_adapters_execute(const void* x, const void* weight, const void* a, const
   void* u = static_cast<char*>(workspace) + p.u;
   rc = run_adapter_prep(p, t, adapter, T, A, s);
   if (rc != PGG_OK) return rc;
-  rc = run_shrink(p, t, env, x, a, scale, u, T, K, R, A, dtype, s);
+  const bool by_token = p.variant == kVariantSkinny && aligned(x, 16) && aligned(weight, 16) &&
+                        aligned(a, 16) && aligned(b, 16) && aligned(y, 2);
+  rc = run_shrink(p, t, env, x, a, scale, u, T, K, R, A, dtype, by_token, s);
   if (rc != PGG_OK) return rc;
-  return run_adapt(p, t, env, false, x, weight, u, b, y, T, K, N, R, A, dtype, s);
+  return run_adapt(p, t, env, false, by_token ? adapter : nullptr, x, weight, u, b, y, T, K, N, R,
+                   A, dtype, s);
 }
 
 int pgg_adapters_grad_workspace_size(int64_t T, int64_t K, int64_t N, int64_t R, int64_t A,
@@ -508,12 +556,12 @@ int pgg_adapters_grad(const void* d_y, const void* x, const void* weight, const 
   void* v = static_cast<char*>(workspace) + p.v;
   rc = run_adapter_prep(p, t, adapter, T, A, s);
   if (rc != PGG_OK) return rc;
-  rc = run_shrink(p, t, env, x, a, scale, u, T, K, R, A, dtype, s);
+  rc = run_shrink(p, t, env, x, a, scale, u, T, K, R, A, dtype, false, s);
   if (rc != PGG_OK) return rc;
-  rc = run_shrink(p, t, env, d_y, b, scale, v, T, N, R, A, dtype, s);
+  rc = run_shrink(p, t, env, d_y, b, scale, v, T, N, R, A, dtype, false, s);
   if (rc != PGG_OK) return rc;
   if (d_x) {
-    rc = run_adapt(p, t, env, true, d_y, weight, v, a, d_x, T, N, K, R, A, dtype, s);
+    rc = run_adapt(p, t, env, true, nullptr, d_y, weight, v, a, d_x, T, N, K, R, A, dtype, s);
     if (rc != PGG_OK) return rc;
   }
   rc = run_dw_tables(x, v, t.off, t.padrow, t.hdr, p.rows_u, R, K, A, T, dtype, d_a, s);

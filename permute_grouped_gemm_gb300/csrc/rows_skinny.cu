@@ -1,0 +1,683 @@
+// Products over few rows per group on tcgen05 tensor cores: what is streamed is
+// the weight, so the weight is the MMA's M operand and the rows are its N.
+//
+//     gated    [gate | up][i, :] = x[token(i), :] W[g(i)],  h = prob * silu(gate) * up
+//     shrink   u[i, :] = scale[ad] * x[token(i), :] a[ad]
+//     adapt    y[t, :] = x[t, :] W + u[t, :] b[ad(t)]^T
+//
+// Tile: a block of at most NR rows x 128 weight columns (gated: 64 gates and
+// their 64 ups) whose transposed fp32 accumulator, 128 lanes x NR columns, sits
+// in tensor memory (two buffers). A cluster of S CTAs shares a tile: each
+// reduces its part of K, then every CTA receives from the others, through
+// distributed shared memory, the partial sums of its NR / S rows and adds them
+// in the order of the CTAs: split-K without a second launch, atomics or
+// workspace, bitwise repeatable. S = 1 when the tiles alone fill the GPU.
+//
+// A stage is 64 of k: two 64-column panels of the weight by TMA (16 KB) and NR
+// x rows gathered by token with cp.async. With NR = 16 eleven stages are in
+// flight per SM, 176 KB of weight, which is what keeps HBM busy.
+//
+// adapt with few tokens: rows stay in the caller's order, and the low-rank part
+// is added in the epilogue in fp32 (a row's u and its adapter's b, read once per
+// row: the bytes the operator needs anyway). A row meets no adapter but its own.
+// Its weight stream needs nothing from the launches before it, so it starts
+// while they run (see launch_dependents in the shrink mode).
+//
+// Warp roles per CTA: 0 TMA, 1 tensor memory and MMA issue, one gather warp per
+// stage slot, four epilogue warps. Waits are bounded as everywhere.
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <cstdint>
+#include <cstring>
+
+#include "pgg_ops.h"
+#include "pgg_ops_mma.cuh"
+#include "pgg_ptx.cuh"
+
+namespace pgg {
+namespace {
+
+constexpr int kM = 128;            // weight columns per tile: accumulator lanes
+constexpr int kFK = 64;            // reduction per stage
+constexpr int kPanel = kFK * 128;  // 64 k rows x 128 bytes (64 columns)
+constexpr int kEpiWarps = 4;
+constexpr int kMaxSplit = 8;
+
+template <int NR, int PANELS>
+struct Cfg {
+  static constexpr int kABytes = PANELS * kPanel;
+  static constexpr int kBBytes = NR * 128;
+  static constexpr int kStageBytes = kABytes + kBBytes;
+  static constexpr int kRedBytes = NR * kM * 4;  // S slots of NR / S rows x 128 lanes
+  static constexpr int kFit = (226 * 1024 - 2048 - kRedBytes) / kStageBytes;
+  static constexpr int kStages = kFit < 11 ? kFit : 11;
+  static constexpr int kThreads = 32 * (2 + kStages + kEpiWarps);
+  static constexpr int kTmemCols = 2 * NR < 32 ? 32 : 2 * NR;
+  static_assert(kBBytes % 1024 == 0, "operand alignment");
+};
+
+template <int STAGES>
+struct Ctl {
+  uint64_t full[STAGES];   // weight bytes + the gather warp's arrival
+  uint64_t empty[STAGES];  // MMAs of the stage done
+  uint64_t tfull[2], tempty[2];
+  uint64_t rfull, rempty;  // partial sums of all CTAs received here / mine read by all CTAs
+  uint64_t drain;
+  uint32_t tmem_base;
+  int abort;
+};
+
+template <int NR, int PANELS>
+constexpr int smem_bytes() {
+  using C = Cfg<NR, PANELS>;
+  return C::kStages * C::kStageBytes + C::kRedBytes +
+         static_cast<int>(sizeof(Ctl<C::kStages>)) + 1024;
+}
+
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(r));
+  return r;
+}
+
+__device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+
+__device__ __forceinline__ void launch_dependents() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+struct Tile {
+  int64_t g, row0, n0;  // n0: first output column (gated: of h)
+  int rows, urow;
+};
+
+template <int MODE, int NR>
+__device__ __forceinline__ Tile tile_of(uint32_t t, const RowsArgs& a) {
+  const uint32_t rb = t / static_cast<uint32_t>(a.n_blocks);
+  Tile x;
+  x.n0 = static_cast<int64_t>(t - rb * static_cast<uint32_t>(a.n_blocks)) *
+         (MODE == kGated ? 64 : kM);
+  if constexpr (MODE == kAdapt) {
+    x.g = 0;
+    x.row0 = static_cast<int64_t>(rb) * NR;
+    x.rows = a.M - x.row0 < NR ? static_cast<int>(a.M - x.row0) : NR;
+    x.urow = 0;
+  } else {
+    int4 e = a.rblist[check_index(a.hdr, rb, a.max_row_blocks, 90)];
+    if (!check_ok(a.hdr,
+                  e.x >= 0 && e.x <= a.G && e.y >= 0 && e.z >= 0 && e.z <= NR &&
+                      static_cast<int64_t>(e.y) + e.z <= a.M,
+                  91))
+      e = make_int4(0, 0, 0, 0);
+    x.g = e.x;
+    x.row0 = e.y;
+    x.rows = e.z;
+    x.urow = e.w;
+  }
+  return x;
+}
+
+// The tiles that this CTA walks, and its part of the reduction.
+struct Walk {
+  uint32_t first, step, total;
+  int ks0, ks1;
+};
+
+// Rows of tokens without an adapter have nothing to shrink.
+template <int MODE>
+__device__ __forceinline__ bool skipped(const RowsArgs& a, const Tile& x) {
+  return MODE == kShrink && x.g >= a.G;
+}
+
+template <int MODE, int NR, int PANELS>
+__device__ void w_producer(uint8_t* smem, Ctl<Cfg<NR, PANELS>::kStages>* ctl,
+                           const CUtensorMap* tm_w, const RowsArgs& a, const Walk& k) {
+  using C = Cfg<NR, PANELS>;
+  const uint64_t lim = a.wait_limit_ns;
+  volatile int* abort = &ctl->abort;
+  int stage = 0;
+  uint32_t phase = 0, outstanding = 0, last_parity = 0;
+  bool failed = false;
+  for (uint32_t t = k.first; t < k.total && !failed; t += k.step) {
+    const Tile x = tile_of<MODE, NR>(t, a);
+    if (skipped<MODE>(a, x)) continue;
+    int32_t col[2];
+    bool on[2];
+    for (int j = 0; j < 2; ++j) {
+      col[j] = static_cast<int32_t>(MODE == kGated ? x.n0 + (j ? a.N : 0) : x.n0 + 64 * j);
+      on[j] = j < PANELS && (MODE == kGated || x.n0 + 64 * j < a.N);
+    }
+    const uint32_t bytes = (on[0] ? kPanel : 0) + (on[1] ? kPanel : 0);
+    for (int ks = k.ks0; ks < k.ks1; ++ks) {
+      if (!ptx::mbar_wait(&ctl->empty[stage], phase ^ 1u, lim, abort)) {
+        failed = true;
+        break;
+      }
+      uint8_t* sa = smem + stage * C::kStageBytes;
+      ptx::mbar_arrive_expect_tx(&ctl->full[stage], bytes);
+      for (int j = 0; j < PANELS; ++j)
+        if (on[j])
+          ptx::tma_load_3d(sa + j * kPanel, tm_w, &ctl->full[stage], col[j], ks * kFK,
+                           static_cast<int32_t>(x.g));
+      outstanding |= 1u << stage;
+      last_parity = (last_parity & ~(1u << stage)) | (phase << stage);
+      if (++stage == C::kStages) {
+        stage = 0;
+        phase ^= 1u;
+      }
+    }
+  }
+  if (failed) {
+    ctl->abort = 1;
+    raise_status(a.hdr, kStTimeout, 42);
+  }
+  int no_abort = 0;
+  for (int s = 0; s < C::kStages; ++s)
+    if (outstanding & (1u << s)) ptx::mbar_wait(&ctl->full[s], (last_parity >> s) & 1u, lim, &no_abort);
+}
+
+// Gather warp w fills stage slot w: rows (lane >> 3) + 4 q, 16-byte chunk lane & 7.
+template <int MODE, int NR, int PANELS>
+__device__ void x_gatherer(uint8_t* smem, Ctl<Cfg<NR, PANELS>::kStages>* ctl, const RowsArgs& a,
+                           const Walk& k) {
+  using C = Cfg<NR, PANELS>;
+  const uint64_t lim = a.wait_limit_ns;
+  volatile int* abort = &ctl->abort;
+  const int w = (threadIdx.x >> 5) - 2;
+  const int lane = threadIdx.x & 31, c = lane & 7;
+  const char* xb = static_cast<const char*>(a.x);
+  const uint32_t sb = ptx::smem_addr(smem + w * C::kStageBytes + C::kABytes);
+  const int steps = k.ks1 - k.ks0;
+  constexpr uint32_t kNoRow = 0xFFFFFFFFu;
+  const uint32_t row_units = static_cast<uint32_t>(a.K / 8);
+  uint32_t row16[NR / 4];
+  uint32_t phase = 0;
+  bool failed = false;
+  int kb = w;  // the warp's next step, counted from the start of tile t
+  for (uint32_t t = k.first; t < k.total && !failed; t += k.step) {
+    const Tile x = tile_of<MODE, NR>(t, a);
+    if (skipped<MODE>(a, x)) continue;
+    if (kb < steps) {
+#pragma unroll
+      for (int q = 0; q < NR / 4; ++q) {
+        const int rr = (lane >> 3) + 4 * q;
+        row16[q] = kNoRow;
+        if (rr < x.rows) {
+          const int64_t row = x.row0 + rr;
+          const int64_t tok =
+              MODE == kAdapt
+                  ? row
+                  : check_index(a.hdr, a.rowinfo[check_index(a.hdr, row, a.M, 92)].token, a.batch,
+                                93);
+          row16[q] = static_cast<uint32_t>(tok) * row_units;
+        }
+      }
+    }
+    for (; kb < steps; kb += C::kStages) {
+      if (!ptx::mbar_wait(&ctl->empty[w], phase ^ 1u, lim, abort)) {
+        failed = true;
+        break;
+      }
+      const int64_t kk = static_cast<int64_t>(k.ks0 + kb) * kFK + c * 8;
+      const bool k_ok = kk < a.K;
+      const char* xk = xb + kk * 2;
+#pragma unroll
+      for (int q = 0; q < NR / 4; ++q) {
+        const int rr = (lane >> 3) + 4 * q;
+        const bool ok = k_ok && row16[q] != kNoRow;
+        const void* src = ok ? static_cast<const void*>(xk + (static_cast<uint64_t>(row16[q]) << 4))
+                             : static_cast<const void*>(xb);
+        ptx::cp_async_16(sb + rr * 128 + ((c ^ (rr & 7)) << 4), src, ok ? 16u : 0u);
+      }
+      ptx::cp_async_commit();
+      ptx::cp_async_wait<0>();
+      ptx::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(&ctl->full[w]);
+      phase ^= 1u;
+    }
+    kb -= steps;
+  }
+  ptx::cp_async_wait<0>();
+  if (failed) {
+    ctl->abort = 1;
+    if (lane == 0) raise_status(a.hdr, kStTimeout, 43);
+  }
+}
+
+template <int DT, int MODE, int NR, int PANELS>
+__device__ void mma_issuer(uint8_t* smem, Ctl<Cfg<NR, PANELS>::kStages>* ctl, uint32_t tmem_base,
+                           const RowsArgs& a, const Walk& k) {
+  using C = Cfg<NR, PANELS>;
+  constexpr uint32_t kFmt = DT == PGG_BF16 ? 1u : 0u;
+  constexpr uint32_t idesc = ptx::idesc_make(kFmt, kM, NR) | (1u << 15);  // A MN-major
+  const uint64_t lim = a.wait_limit_ns;
+  volatile int* abort = &ctl->abort;
+  int stage = 0, acc = 0;
+  uint32_t phase = 0, aph = 0;
+  bool issued = false, failed = false;
+  for (uint32_t t = k.first; t < k.total && !failed; t += k.step) {
+    if (skipped<MODE>(a, tile_of<MODE, NR>(t, a))) continue;
+    if (!ptx::mbar_wait(&ctl->tempty[acc], aph ^ 1u, lim, abort)) {
+      failed = true;
+      break;
+    }
+    ptx::tc_fence_after_sync();
+    const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * NR);
+    for (int ks = k.ks0; ks < k.ks1; ++ks) {
+      if (!ptx::mbar_wait(&ctl->full[stage], phase, lim, abort)) {
+        failed = true;
+        break;
+      }
+      ptx::tc_fence_after_sync();
+      const uint32_t sa = ptx::smem_addr(smem + stage * C::kStageBytes);
+      const uint64_t da = ptx::sdesc_sw128_mn(sa, kPanel);
+      const uint64_t db = ptx::sdesc_sw128(sa + C::kABytes);
+#pragma unroll
+      for (int kk = 0; kk < kFK / 16; ++kk)
+        ptx::mma_f16(d_tmem, da + static_cast<uint64_t>((kk * 16 * 128) >> 4),
+                     db + static_cast<uint64_t>((kk * 32) >> 4), idesc,
+                     (ks > k.ks0 || kk > 0) ? 1u : 0u);
+      issued = true;
+      ptx::mma_commit(&ctl->empty[stage]);
+      if (++stage == C::kStages) {
+        stage = 0;
+        phase ^= 1u;
+      }
+    }
+    if (failed) break;
+    ptx::mma_commit(&ctl->tfull[acc]);
+    acc ^= 1;
+    if (acc == 0) aph ^= 1u;
+  }
+  if (failed) {
+    ctl->abort = 1;
+    raise_status(a.hdr, kStTimeout, 44);
+  }
+  if (issued) {
+    int no_abort = 0;
+    ptx::mma_commit(&ctl->drain);
+    ptx::mbar_wait(&ctl->drain, 0u, lim, &no_abort);
+  }
+}
+
+template <int DT>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  if constexpr (DT == PGG_BF16) {
+    const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&p);
+  } else {
+    const __half2 p = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&p);
+  }
+}
+
+template <int DT>
+__device__ __forceinline__ float2 unpack2(uint32_t w) {
+  if constexpr (DT == PGG_BF16)
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+  else
+    return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+
+template <int DT>
+__device__ __forceinline__ void store16(void* out, int64_t i, float v) {
+  const uint32_t p = pack2<DT>(v, 0.0f);
+  static_cast<uint16_t*>(out)[i] = static_cast<uint16_t>(p & 0xFFFFu);
+}
+
+// Output of tile rows j, j + 4, ... < n (j: this warp's), whose first row is tile row j0: red
+// holds S slots of `slot` floats, rows of 128 lanes each.
+template <int DT, int MODE>
+__device__ __forceinline__ void write_rows(const float* red, int slot, uint32_t S, const RowsArgs& a,
+                                           const Tile& x, int j0, int n, bool failed) {
+  const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 3;
+#pragma unroll 1
+  for (int j = warp; j < n; j += kEpiWarps) {
+    const int64_t row = x.row0 + j0 + j;
+    const float* r = red + j * kM;
+    if constexpr (MODE == kGated) {
+      const float2* r2 = reinterpret_cast<const float2*>(r) + lane;
+      float2 g = make_float2(0.0f, 0.0f), u = g;
+      for (uint32_t s = 0; s < S; ++s) {
+        const float2 pg = r2[s * slot / 2], pu = r2[s * slot / 2 + 32];
+        g.x += pg.x;
+        g.y += pg.y;
+        u.x += pu.x;
+        u.y += pu.y;
+      }
+      const int64_t f = x.n0 + 2 * lane;
+      if (f >= a.N) continue;  // (N is even)
+      const float p =
+          a.probs ? a.probs[check_index(a.hdr, a.rowinfo[row].rank, a.M, 94)] : 1.0f;
+      *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + row * a.N + f) =
+          pack2<DT>(gate(g.x, u.x, p), gate(g.y, u.y, p));
+      if (a.gate_up) {
+        uint16_t* gu = static_cast<uint16_t*>(a.gate_up) + row * 2 * a.N + f;
+        *reinterpret_cast<uint32_t*>(gu) = pack2<DT>(g.x, g.y);
+        *reinterpret_cast<uint32_t*>(gu + a.N) = pack2<DT>(u.x, u.y);
+      }
+    } else {
+      float v[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[i] = 0.0f;
+        for (uint32_t s = 0; s < S; ++s) v[i] += r[s * slot + lane + 32 * i];
+      }
+      if constexpr (MODE == kShrink) {
+        const float sc = a.scale ? a.scale[x.g] : 1.0f;
+        const int64_t token = a.rowinfo[check_index(a.hdr, row, a.M, 95)].token;
+        const int64_t orow = a.u_by_token ? token : static_cast<int64_t>(x.urow) + j0 + j;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int64_t c = x.n0 + lane + 32 * i;
+          if (c >= a.N) continue;
+          if (a.u_by_token)
+            static_cast<float*>(a.out)[orow * a.N + c] = v[i] * sc;
+          else
+            store16<DT>(a.out, orow * a.N + c, v[i] * sc);
+        }
+      } else {
+        // the row's own adapter, in fp32: u [R] against b [n][R]
+        const int64_t ad = a.adapter[row];
+        if (ad >= 0 && ad < a.G && !failed) {
+          const float* u = static_cast<const float*>(a.u) + row * a.R;
+          const char* b = static_cast<const char*>(a.b) + ((ad * a.N + x.n0) * a.R) * 2;
+#pragma unroll 1
+          for (int r0 = 0; r0 < a.R; r0 += 8) {
+            const float4 ua = __ldcg(reinterpret_cast<const float4*>(u + r0));
+            const float4 ub = __ldcg(reinterpret_cast<const float4*>(u + r0 + 4));
+            uint4 q[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              q[i] = make_uint4(0, 0, 0, 0);
+              if (x.n0 + lane + 32 * i < a.N)
+                q[i] = __ldg(reinterpret_cast<const uint4*>(
+                    b + (static_cast<int64_t>(lane + 32 * i) * a.R + r0) * 2));
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float2 b0 = unpack2<DT>(q[i].x), b1 = unpack2<DT>(q[i].y);
+              const float2 b2 = unpack2<DT>(q[i].z), b3 = unpack2<DT>(q[i].w);
+              v[i] = fmaf(ua.x, b0.x, v[i]);
+              v[i] = fmaf(ua.y, b0.y, v[i]);
+              v[i] = fmaf(ua.z, b1.x, v[i]);
+              v[i] = fmaf(ua.w, b1.y, v[i]);
+              v[i] = fmaf(ub.x, b2.x, v[i]);
+              v[i] = fmaf(ub.y, b2.y, v[i]);
+              v[i] = fmaf(ub.z, b3.x, v[i]);
+              v[i] = fmaf(ub.w, b3.y, v[i]);
+            }
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int64_t c = x.n0 + lane + 32 * i;
+          if (c < a.N) store16<DT>(a.out, row * a.N + c, failed ? 0.0f : v[i]);
+        }
+      }
+    }
+  }
+}
+
+template <int DT, int MODE, int NR, int PANELS>
+__device__ void epilogue(Ctl<Cfg<NR, PANELS>::kStages>* ctl, float* red, uint32_t tmem_base,
+                         const RowsArgs& a, const Walk& k, uint32_t rank, uint32_t S) {
+  const uint64_t lim = a.wait_limit_ns;
+  volatile int* abort = &ctl->abort;
+  const int lane = threadIdx.x & 31;
+  const int quarter = (threadIdx.x >> 5) & 3;
+  const int per = NR / static_cast<int>(S);  // rows that each CTA of the cluster finishes
+  const int slot = per * kM;
+  int acc = 0;
+  uint32_t aph = 0, rph = 0;
+  bool failed_input = false;
+  if constexpr (MODE == kAdapt) {
+    ptx::griddep_wait();  // u and the ids' check; the weight stream is under way already
+    failed_input = routing_failed(a.hdr);
+  }
+  bool held = a.hold_release != 0;
+  for (uint32_t t = k.first; t < k.total; t += k.step) {
+    const Tile x = tile_of<MODE, NR>(t, a);
+    if (skipped<MODE>(a, x)) {
+      // (fills of padded rows belong to adapters only)
+      continue;
+    }
+    bool ok = ptx::mbar_wait(&ctl->tfull[acc], aph, lim, abort);
+    // the others have read what they got from this CTA for the tile before
+    ok = ok && ptx::mbar_wait_cluster(&ctl->rempty, rph ^ 1u, lim, abort);
+    if (!__all_sync(0xFFFFFFFFu, ok)) {
+      if (lane == 0) {
+        ctl->abort = 1;
+        raise_status(a.hdr, kStTimeout, 45);
+      }
+      break;
+    }
+    ptx::tc_fence_after_sync();
+    const uint32_t t_lane = tmem_base + (static_cast<uint32_t>(32 * quarter) << 16) +
+                            static_cast<uint32_t>(acc * NR);
+    const uint32_t mine = 32 * quarter + lane;
+#pragma unroll 1
+    for (int c0 = 0; c0 < NR && c0 < x.rows; c0 += 16) {
+      uint32_t v[16];
+      ptx::tmem_ld_32x32b_x16(t_lane + static_cast<uint32_t>(c0), v);
+      ptx::tmem_ld_wait();
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int j = c0 + i;
+        if (j >= x.rows) break;
+        const int dst = j / per;
+        // slot `rank` of the CTA that finishes row j
+        float* where = red + rank * slot + (j - dst * per) * kM + mine;
+        if (S == 1)
+          *where = __uint_as_float(v[i]);
+        else
+          st_cluster_f32(ptx::mapa(where, static_cast<uint32_t>(dst)), __uint_as_float(v[i]));
+      }
+    }
+    ptx::tc_fence_before_sync();
+    __syncwarp();
+    if (lane == 0 && !held) ptx::mbar_arrive(&ctl->tempty[acc]);
+    held = false;
+    if (lane < static_cast<int>(S)) ptx::mbar_arrive_remote(ptx::mapa(&ctl->rfull, lane));
+    ok = ptx::mbar_wait_cluster(&ctl->rfull, rph, lim, abort);
+    if (!__all_sync(0xFFFFFFFFu, ok)) {
+      if (lane == 0) {
+        ctl->abort = 1;
+        raise_status(a.hdr, kStTimeout, 46);
+      }
+      break;
+    }
+    const int j0 = static_cast<int>(rank) * per;
+    const int n = x.rows - j0 < per ? x.rows - j0 : per;
+    write_rows<DT, MODE>(red, slot, S, a, x, j0, n, failed_input);
+    if constexpr (MODE == kShrink) {
+      if (a.padded) {  // rows that fill the adapter up to a multiple of 64
+        const int end = (x.rows + 63) / 64 * 64;
+        for (int j = x.rows + static_cast<int>(rank) * kEpiWarps + quarter; j < end;
+             j += static_cast<int>(S) * kEpiWarps)
+          for (int64_t c = x.n0 + lane; c < a.N && c < x.n0 + kM; c += 32)
+            static_cast<uint16_t*>(a.out)[(static_cast<int64_t>(x.urow) + j) * a.N + c] = 0;
+      }
+    }
+    __syncwarp();
+    if (lane < static_cast<int>(S)) ptx::mbar_arrive_remote(ptx::mapa(&ctl->rempty, lane));
+    rph ^= 1u;
+    acc ^= 1;
+    if (acc == 0) aph ^= 1u;
+  }
+}
+
+template <int DT, int MODE, int NR, int PANELS>
+__global__ void __launch_bounds__(Cfg<NR, PANELS>::kThreads, 1)
+    rows_skinny_kernel(const __grid_constant__ CUtensorMap tm_w, const RowsArgs a) {
+  using C = Cfg<NR, PANELS>;
+  if (MODE != kAdapt) {
+    ptx::griddep_wait();
+    // everything before this launch has completed: the adapt launch behind it, which reads only
+    // the caller's x and weight until its own wait, may start
+    if (MODE == kShrink && a.u_by_token) launch_dependents();
+  }
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  float* red = reinterpret_cast<float*>(smem + C::kStages * C::kStageBytes);
+  auto* ctl = reinterpret_cast<Ctl<C::kStages>*>(smem + C::kStages * C::kStageBytes + C::kRedBytes);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = ptx::cluster_ctarank(), S = cluster_size();
+
+  if (MODE != kAdapt && routing_failed(a.hdr)) {
+    if (MODE == kGated) zero_rows16(a);
+    return;
+  }
+  Walk k;
+  const uint32_t row_blocks = MODE == kAdapt ? static_cast<uint32_t>((a.M + NR - 1) / NR)
+                                             : a.hdr->n_row_blocks;
+  k.total = row_blocks * static_cast<uint32_t>(a.n_blocks);
+  k.first = blockIdx.x / S;
+  k.step = gridDim.x / S;
+  const int nks = static_cast<int>((a.K + kFK - 1) / kFK);
+  k.ks0 = nks * static_cast<int>(rank) / static_cast<int>(S);
+  k.ks1 = nks * (static_cast<int>(rank) + 1) / static_cast<int>(S);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::kStages; ++s) {
+      ptx::mbar_init(&ctl->full[s], 2);
+      ptx::mbar_init(&ctl->empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      ptx::mbar_init(&ctl->tfull[b], 1);
+      ptx::mbar_init(&ctl->tempty[b], kEpiWarps);
+    }
+    ptx::mbar_init(&ctl->rfull, kEpiWarps * S);
+    ptx::mbar_init(&ctl->rempty, kEpiWarps * S);
+    ptx::mbar_init(&ctl->drain, 1);
+    ctl->abort = 0;
+    ptx::fence_mbar_init();
+  }
+  if (warp == 0 && lane == 0) ptx::tma_prefetch_desc(&tm_w);
+  if (warp == 1) {
+    ptx::tmem_alloc(&ctl->tmem_base, C::kTmemCols);
+    ptx::tmem_relinquish();
+  }
+  ptx::tc_fence_before_sync();
+  __syncthreads();
+  ptx::cluster_sync();  // the others' barriers are ready before anything arrives there
+  ptx::tc_fence_after_sync();
+  const uint32_t tmem_base = ctl->tmem_base;
+
+  if (warp == 0) {
+    if (lane == 0) w_producer<MODE, NR, PANELS>(smem, ctl, &tm_w, a, k);
+  } else if (warp == 1) {
+    if (lane == 0) mma_issuer<DT, MODE, NR, PANELS>(smem, ctl, tmem_base, a, k);
+  } else if (warp < 2 + C::kStages) {
+    x_gatherer<MODE, NR, PANELS>(smem, ctl, a, k);
+  } else {
+    epilogue<DT, MODE, NR, PANELS>(ctl, red, tmem_base, a, k, rank, S);
+  }
+
+  ptx::tc_fence_before_sync();
+  __syncthreads();
+  ptx::cluster_sync();  // no CTA leaves while another may still write to it
+  if (warp == 1) {
+    ptx::tc_fence_after_sync();
+    ptx::tmem_dealloc(tmem_base, C::kTmemCols);
+  }
+}
+
+// CTAs per tile: the split of K that leaves the fewest steps on the critical path for about
+// `tiles` tiles, counting kTileCost steps per tile for its epilogue and exchange.
+int choose_split(int64_t tiles, int nks, int NR, int num_sms) {
+  constexpr int kTileCost = 8;
+  int best = 1;
+  int64_t best_cost = 0;
+  for (int s = 1; s <= kMaxSplit && s <= nks && s <= NR; s *= 2) {
+    const int64_t clusters = num_sms / s;
+    const int64_t waves = (tiles + clusters - 1) / clusters;
+    const int64_t cost = waves * ((nks + s - 1) / s + kTileCost);
+    if (s == 1 || cost < best_cost) {
+      best = s;
+      best_cost = cost;
+    }
+  }
+  return best;
+}
+
+template <int DT, int MODE, int NR, int PANELS>
+cudaError_t launch_t(const CUtensorMap& tm_w, const RowsArgs& a, int64_t tiles, int num_sms,
+                     cudaStream_t stream) {
+  using C = Cfg<NR, PANELS>;
+  constexpr int smem = smem_bytes<NR, PANELS>();
+  static_assert(smem <= 227 * 1024, "shared memory per CTA");
+  auto kern = rows_skinny_kernel<DT, MODE, NR, PANELS>;
+  cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (err != cudaSuccess) return err;
+  const int nks = static_cast<int>((a.K + kFK - 1) / kFK);
+  const int S = choose_split(tiles, nks, NR, num_sms);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(S);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(C::kThreads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int64_t want = num_sms / S;
+  const int64_t most = (MODE == kAdapt ? (a.M + NR - 1) / NR : a.max_row_blocks) * a.n_blocks;
+  if (most < want) want = most;
+  cfg.gridDim = dim3(static_cast<unsigned>(S * want), 1, 1);
+  int clusters = 0;
+  err = cudaOccupancyMaxActiveClusters(&clusters, kern, &cfg);
+  if (err != cudaSuccess) return err;
+  if (clusters < 1) return cudaErrorInvalidConfiguration;
+  if (clusters < want) want = clusters;
+  return launch_pdl(kern, dim3(static_cast<unsigned>(S * want)), dim3(C::kThreads),
+                    static_cast<size_t>(smem), stream, static_cast<unsigned>(S), tm_w, a);
+}
+
+template <int DT>
+cudaError_t launch_mode(RowsMode mode, int NR, const CUtensorMap& m, const RowsArgs& a,
+                        int64_t tiles, int sms, cudaStream_t st) {
+  if (mode == kGated) {
+    if (NR == 16) return launch_t<DT, kGated, 16, 2>(m, a, tiles, sms, st);
+    if (NR == 32) return launch_t<DT, kGated, 32, 2>(m, a, tiles, sms, st);
+    if (NR == 64) return launch_t<DT, kGated, 64, 2>(m, a, tiles, sms, st);
+    if (NR == 128) return launch_t<DT, kGated, 128, 2>(m, a, tiles, sms, st);
+  } else if (mode == kShrink) {
+    if (NR == 16) return launch_t<DT, kShrink, 16, 2>(m, a, tiles, sms, st);
+    if (NR == 128 && a.N <= 64) return launch_t<DT, kShrink, 128, 1>(m, a, tiles, sms, st);
+    if (NR == 128) return launch_t<DT, kShrink, 128, 2>(m, a, tiles, sms, st);
+  } else if (mode == kAdapt) {
+    if (NR == 16) return launch_t<DT, kAdapt, 16, 2>(m, a, tiles, sms, st);
+    if (NR == 64) return launch_t<DT, kAdapt, 64, 2>(m, a, tiles, sms, st);
+  }
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace
+
+// live_blocks: about how many row blocks there will be (the launch's shape goes by it, nothing
+// else).
+cudaError_t launch_rows_skinny(int dtype, RowsMode mode, int NR, RowsArgs a, int64_t live_blocks,
+                               int num_sms, cudaStream_t stream) {
+  const int64_t tile_n = mode == kGated ? 64 : kM;
+  a.n_blocks = static_cast<int32_t>((a.N + tile_n - 1) / tile_n);
+  CUtensorMap tm_w;
+  const int64_t cols = mode == kGated ? 2 * a.N : a.N;
+  if (!encode_map_3d(&tm_w, dtype, a.w, cols, a.K, mode == kAdapt ? 1 : a.G, kFK))
+    return cudaErrorInvalidValue;
+  const int64_t tiles = live_blocks * a.n_blocks;
+  if (dtype == PGG_BF16)
+    return launch_mode<PGG_BF16>(mode, NR, tm_w, a, tiles, num_sms, stream);
+  if (dtype == PGG_F16) return launch_mode<PGG_F16>(mode, NR, tm_w, a, tiles, num_sms, stream);
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace pgg
