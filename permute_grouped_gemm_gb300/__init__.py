@@ -199,6 +199,14 @@ def _score_code(score: str) -> int:
     return _SCORES[score]
 
 
+def _stream_of(stream, device) -> int:
+    """Address of ``stream``, or of torch's current stream on ``device``."""
+    if stream is not None:
+        return stream.cuda_stream
+    import torch
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
 def _dense(*tensors):
     for t in tensors:
         if t is not None and not (t.is_cuda and t.is_contiguous()):
@@ -230,9 +238,9 @@ def route(logits, top_k: int, row_idx_type: int = 0, bias=None, score: str = "so
     _is("experts", experts, (batch, top_k), torch.int64)
     _is("expanded_row_idx", expanded_row_idx, (M,), torch.int64)
     _is("group_list", group_list, (G,), torch.int64)
-    need = pgg_route_workspace_size(batch, G, top_k)
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        workspace = torch.empty(pgg_route_workspace_size(batch, G, top_k),
+                                dtype=torch.uint8, device=dev)
     if probs is None:
         probs = torch.empty(batch, top_k, dtype=torch.float32, device=dev)
     if experts is None:
@@ -241,14 +249,13 @@ def route(logits, top_k: int, row_idx_type: int = 0, bias=None, score: str = "so
         expanded_row_idx = torch.empty(M, dtype=torch.int64, device=dev)
     if group_list is None:
         group_list = torch.empty(G, dtype=torch.int64, device=dev)
-    if stream is None:
-        stream = torch.cuda.current_stream(dev)
+    stream = _stream_of(stream, dev)
     rc = pgg_route_execute(logits.data_ptr(), bias.data_ptr() if bias is not None else 0, batch, G,
                            top_k, row_idx_type, dtype_code(logits.dtype), _score_code(score),
                            int(renormalize), scale, workspace.data_ptr(),
                            workspace.numel() * workspace.element_size(), probs.data_ptr(),
                            experts.data_ptr(), expanded_row_idx.data_ptr(), group_list.data_ptr(),
-                           stream.cuda_stream)
+                           stream)
     if rc != 0:
         raise PggError(rc, "pgg_route_execute")
     return probs, experts, expanded_row_idx, group_list, workspace
@@ -267,11 +274,10 @@ def route_grad(d_probs, logits, experts, score: str = "softmax", renormalize: bo
     _is("out", out, (batch, G), logits.dtype)
     if out is None:
         out = torch.empty_like(logits)
-    if stream is None:
-        stream = torch.cuda.current_stream(logits.device)
+    stream = _stream_of(stream, logits.device)
     rc = pgg_route_grad(d_probs.data_ptr(), logits.data_ptr(), experts.data_ptr(), batch, G, top_k,
                         dtype_code(logits.dtype), _score_code(score), int(renormalize), scale,
-                        out.data_ptr(), stream.cuda_stream)
+                        out.data_ptr(), stream)
     if rc != 0:
         raise PggError(rc, "pgg_route_grad")
     return out
@@ -299,20 +305,19 @@ def swiglu(x, weight, expanded_row_idx, group_list, batch: int, top_k: int, row_
     _is("out", out, (M, F), x.dtype)
     _is("gate_up", gate_up, (M, F2), x.dtype)
     dt = dtype_code(x.dtype)
-    need = pgg_swiglu_workspace_size(M, F, K, G, M, batch, top_k, row_idx_type, dt)
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        workspace = torch.empty(pgg_swiglu_workspace_size(M, F, K, G, M, batch, top_k, row_idx_type, dt),
+                                dtype=torch.uint8, device=dev)
     if out is None:
         out = torch.empty(M, F, dtype=x.dtype, device=dev)
     if keep and gate_up is None:
         gate_up = torch.empty(M, F2, dtype=x.dtype, device=dev)
-    if stream is None:
-        stream = torch.cuda.current_stream(dev)
+    stream = _stream_of(stream, dev)
     rc = pgg_swiglu_execute(x.data_ptr(), weight.data_ptr(), expanded_row_idx.data_ptr(),
                             group_list.data_ptr(), probs.data_ptr() if probs is not None else 0,
                             M, F, K, G, M, batch, top_k, row_idx_type, dt, workspace.data_ptr(),
                             workspace.numel() * workspace.element_size(), out.data_ptr(),
-                            gate_up.data_ptr() if gate_up is not None else 0, stream.cuda_stream)
+                            gate_up.data_ptr() if gate_up is not None else 0, stream)
     if rc != 0:
         raise PggError(rc, "pgg_swiglu_execute")
     return out, gate_up, workspace
@@ -339,24 +344,23 @@ def swiglu_grad(d_h, gate_up, expanded_row_idx, top_k: int, row_idx_type: int, p
     _is("d_gate_up", d_gate_up, (M, 2 * F), d_h.dtype)
     _is("d_probs", d_probs, (batch, top_k), torch.float32)
     _is("h", h, (M, F), d_h.dtype)
-    need = pgg_swiglu_grad_workspace_size(M, batch, top_k)
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        workspace = torch.empty(pgg_swiglu_grad_workspace_size(M, batch, top_k),
+                                dtype=torch.uint8, device=dev)
     if d_gate_up is None:
         d_gate_up = torch.empty_like(gate_up)
     if probs is not None and d_probs is None:
         d_probs = torch.empty_like(probs)
     if h is None:
         h = torch.empty_like(d_h)
-    if stream is None:
-        stream = torch.cuda.current_stream(dev)
+    stream = _stream_of(stream, dev)
     rc = pgg_swiglu_grad(d_h.data_ptr(), gate_up.data_ptr(),
                          probs.data_ptr() if probs is not None else 0,
                          expanded_row_idx.data_ptr(), M, F, batch, top_k, row_idx_type,
                          dtype_code(d_h.dtype), workspace.data_ptr(),
                          workspace.numel() * workspace.element_size(), d_gate_up.data_ptr(),
                          d_probs.data_ptr() if probs is not None else 0, h.data_ptr(),
-                         stream.cuda_stream)
+                         stream)
     if rc != 0:
         raise PggError(rc, "pgg_swiglu_grad")
     return d_gate_up, (d_probs if probs is not None else None), h, workspace
@@ -391,18 +395,17 @@ def adapters(x, weight, a, b, adapter, scale=None, out=None, workspace=None, str
     T, K, N, R, A = _adapter_sizes("adapters", x, weight, a, b, adapter, scale)
     _is("out", out, (T, N), x.dtype)
     dt = dtype_code(x.dtype)
-    need = pgg_adapters_workspace_size(T, K, N, R, A, dt)
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+        workspace = torch.empty(pgg_adapters_workspace_size(T, K, N, R, A, dt),
+                                dtype=torch.uint8, device=x.device)
     if out is None:
         out = torch.empty(T, N, dtype=x.dtype, device=x.device)
-    if stream is None:
-        stream = torch.cuda.current_stream(x.device)
+    stream = _stream_of(stream, x.device)
     rc = pgg_adapters_execute(x.data_ptr(), weight.data_ptr(), a.data_ptr(), b.data_ptr(),
                               adapter.data_ptr(), scale.data_ptr() if scale is not None else 0,
                               T, K, N, R, A, dt, workspace.data_ptr(),
                               workspace.numel() * workspace.element_size(), out.data_ptr(),
-                              stream.cuda_stream)
+                              stream)
     if rc != 0:
         raise PggError(rc, "pgg_adapters_execute")
     return out, workspace
@@ -420,23 +423,22 @@ def adapters_grad(d_y, x, weight, a, b, adapter, scale=None, need_x: bool = True
     _is("d_a", d_a, (A, K, R), x.dtype)
     _is("d_b", d_b, (A, N, R), x.dtype)
     dt = dtype_code(x.dtype)
-    need = pgg_adapters_grad_workspace_size(T, K, N, R, A, dt)
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+        workspace = torch.empty(pgg_adapters_grad_workspace_size(T, K, N, R, A, dt),
+                                dtype=torch.uint8, device=x.device)
     if need_x and d_x is None:
         d_x = torch.empty_like(x)
     if d_a is None:
         d_a = torch.empty_like(a)
     if d_b is None:
         d_b = torch.empty_like(b)
-    if stream is None:
-        stream = torch.cuda.current_stream(x.device)
+    stream = _stream_of(stream, x.device)
     rc = pgg_adapters_grad(d_y.data_ptr(), x.data_ptr(), weight.data_ptr(), a.data_ptr(),
                            b.data_ptr(), adapter.data_ptr(),
                            scale.data_ptr() if scale is not None else 0, T, K, N, R, A, dt,
                            workspace.data_ptr(), workspace.numel() * workspace.element_size(),
                            d_x.data_ptr() if need_x else 0, d_a.data_ptr(), d_b.data_ptr(),
-                           stream.cuda_stream)
+                           stream)
     if rc != 0:
         raise PggError(rc, "pgg_adapters_grad")
     return (d_x if need_x else None), d_a, d_b, workspace

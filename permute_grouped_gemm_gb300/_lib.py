@@ -51,6 +51,8 @@ _SIZES = [ctypes.c_int64] * 7  # M, N, K, G, L, batch, topK
 def load(path: str | None = None):
     """The loaded library (ctypes.CDLL). Raises if it has not been built."""
     global _handle
+    if _handle is not None:
+        return _handle
     with _lock:
         if _handle is None:
             lib_path = path or _build.LIB

@@ -148,7 +148,7 @@ int adapter_plan(int64_t T, int64_t K, int64_t N, int64_t R, int64_t A, int dtyp
                      ? kVariantSkinny
                      : kVariantWide;
     // low-rank rows: blocks of 16 when adapters have about that many tokens
-    p->rb = !grad && T <= 16 * groups ? 16 : 128;
+    p->rb = !grad && T <= 16 * groups ? 16 : 64;
   }
   p->padded = grad ? 1 : 0;
   p->max_row_blocks = (T + p->rb - 1) / p->rb + groups;
@@ -164,7 +164,7 @@ int adapter_plan(int64_t T, int64_t K, int64_t N, int64_t R, int64_t A, int dtyp
   p->rblist = c.take(static_cast<int64_t>(sizeof(int4)) * p->max_row_blocks);
   p->segs = c.take(static_cast<int64_t>(sizeof(int4)) * A);
   p->blkseg = c.take(static_cast<int64_t>(sizeof(int2)) * ((T + 255) / 256));
-  p->counts = c.take(p->blocks > 1 ? 4 * (A + 1) * (p->blocks + 2) : 0);
+  p->counts = c.take(p->blocks > 8 ? 4 * (A + 1) * (p->blocks + 2) : 0);
   p->u = c.take(p->rows_u * R * (p->variant == kVariantSkinny ? 4 : elem_size(dtype)));
   p->v = c.take(grad ? p->rows_u * R * elem_size(dtype) : 0);
   p->total = c.used;
@@ -199,11 +199,10 @@ int run_adapter_prep(const AdapterPlan& p, const AdapterTables& t, const int64_t
   return status_of(launch_adapter_prep(a, stream));
 }
 
-// u = scale * x f[adapter] for f [A, K, R], into rows of `u`: of the dtype in the adapters' order,
-// or (by_token) fp32 in the tokens' order.
+// u = scale * x f[adapter] for f [A, K, R], into rows of `u`, in the adapters' order.
 int run_shrink(const AdapterPlan& p, const AdapterTables& t, const HostEnv& env, const void* x,
                const void* f, const float* scale, void* u, int64_t T, int64_t K, int64_t R,
-               int64_t A, int dtype, bool by_token, cudaStream_t stream) {
+               int64_t A, int dtype, cudaStream_t stream) {
   RowsArgs a;
   std::memset(&a, 0, sizeof(a));
   a.x = x;
@@ -220,7 +219,6 @@ int run_shrink(const AdapterPlan& p, const AdapterTables& t, const HostEnv& env,
   a.batch = T;
   a.max_row_blocks = p.max_row_blocks;
   a.padded = p.padded;
-  a.u_by_token = by_token ? 1 : 0;
   a.hold_release = env.hold_release;
   a.wait_limit_ns = env.wait_limit_ns;
   if (p.variant != kVariantSimt && aligned(x, 16) && aligned(f, 16)) {
@@ -228,6 +226,25 @@ int run_shrink(const AdapterPlan& p, const AdapterTables& t, const HostEnv& env,
     return status_of(launch_rows_skinny(dtype, kShrink, p.rb, a, live, env.num_sms, stream));
   }
   return status_of(launch_rows_simt(dtype, kShrink, a, env.num_sms, stream));
+}
+
+// The same for a few tokens, fp32 in the tokens' order; checks the ids too.
+int run_few_shrink(const AdapterTables& t, const void* x, const void* f, const int64_t* adapter,
+                   const float* scale, void* u, int64_t T, int64_t K, int64_t R, int64_t A,
+                   int dtype, cudaStream_t stream) {
+  RowsArgs a;
+  std::memset(&a, 0, sizeof(a));
+  a.x = x;
+  a.w = f;
+  a.adapter = adapter;
+  a.scale = scale;
+  a.hdr = t.hdr;
+  a.out = u;
+  a.M = T;
+  a.N = R;
+  a.K = K;
+  a.G = A;
+  return status_of(launch_few_shrink(dtype, a, stream));
 }
 
 // y = x W + u f[adapter]^T for W [K, N] (transposed: [N, K]) and f [A, N, R]. by_token: the
@@ -508,14 +525,17 @@ int pgg_adapters_execute(const void* x, const void* weight, const void* a, const
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const AdapterTables t = tables_of(p, workspace);
   void* u = static_cast<char*>(workspace) + p.u;
+  if (p.variant == kVariantSkinny && aligned(x, 16) && aligned(weight, 16) && aligned(a, 16) &&
+      aligned(b, 16)) {
+    rc = run_few_shrink(t, x, a, adapter, scale, u, T, K, R, A, dtype, s);
+    if (rc != PGG_OK) return rc;
+    return run_adapt(p, t, env, false, adapter, x, weight, u, b, y, T, K, N, R, A, dtype, s);
+  }
   rc = run_adapter_prep(p, t, adapter, T, A, s);
   if (rc != PGG_OK) return rc;
-  const bool by_token = p.variant == kVariantSkinny && aligned(x, 16) && aligned(weight, 16) &&
-                        aligned(a, 16) && aligned(b, 16) && aligned(y, 2);
-  rc = run_shrink(p, t, env, x, a, scale, u, T, K, R, A, dtype, by_token, s);
+  rc = run_shrink(p, t, env, x, a, scale, u, T, K, R, A, dtype, s);
   if (rc != PGG_OK) return rc;
-  return run_adapt(p, t, env, false, by_token ? adapter : nullptr, x, weight, u, b, y, T, K, N, R,
-                   A, dtype, s);
+  return run_adapt(p, t, env, false, nullptr, x, weight, u, b, y, T, K, N, R, A, dtype, s);
 }
 
 int pgg_adapters_grad_workspace_size(int64_t T, int64_t K, int64_t N, int64_t R, int64_t A,
@@ -556,9 +576,9 @@ int pgg_adapters_grad(const void* d_y, const void* x, const void* weight, const 
   void* v = static_cast<char*>(workspace) + p.v;
   rc = run_adapter_prep(p, t, adapter, T, A, s);
   if (rc != PGG_OK) return rc;
-  rc = run_shrink(p, t, env, x, a, scale, u, T, K, R, A, dtype, false, s);
+  rc = run_shrink(p, t, env, x, a, scale, u, T, K, R, A, dtype, s);
   if (rc != PGG_OK) return rc;
-  rc = run_shrink(p, t, env, d_y, b, scale, v, T, N, R, A, dtype, false, s);
+  rc = run_shrink(p, t, env, d_y, b, scale, v, T, N, R, A, dtype, s);
   if (rc != PGG_OK) return rc;
   if (d_x) {
     rc = run_adapt(p, t, env, true, nullptr, d_y, weight, v, a, d_x, T, N, K, R, A, dtype, s);

@@ -9,9 +9,11 @@
 //
 // Adapters (adapter_prep): a stable counting sort of the tokens by adapter
 // (tokens without one last), the list of live adapters, which of them each 256
-// rows meet, and the row blocks of the low-rank factors. One block up to
-// kSmallTokens tokens; beyond that counting, prefix sums, placement and the
-// lists are four launches.
+// rows meet, and the row blocks of the low-rank factors. Up to kSmallTokens
+// tokens one cluster of eight blocks does it, an eighth of the tokens each, with
+// the counts exchanged through distributed shared memory (one block alone took
+// 13 us for 8192 tokens: the matches inside 32 keys are what it waits for);
+// beyond that counting, prefix sums, placement and the lists are four launches.
 //
 // All of it is integer work on a few bytes per row: latency is what it costs,
 // so what counts is the number of launches.
@@ -27,7 +29,13 @@ namespace {
 
 constexpr int kSmallRows = 8192;     // gated product: one block up to here
 constexpr int kSmallGroups = 4096;
-constexpr int kSmallTokens = 16384;  // adapters: one block up to here
+constexpr int64_t kSmallTokens = 65536;  // adapters: one cluster up to here
+constexpr int kCluster = 8;
+
+// A word into the shared memory of a block of the cluster (address from ptx::mapa).
+__device__ __forceinline__ void st_cluster_u32(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
 
 __device__ __forceinline__ RowInfo row_info(int64_t p, int top_k) {
   RowInfo r;
@@ -156,9 +164,10 @@ __device__ __forceinline__ int adapter_key(int64_t id, int A) {
 }
 
 // Block-wide, blockDim.x > A (one thread per adapter and one for the group without): the lists
-// from the groups' sizes. Thread g holds group g's count and first compact row.
-__device__ void build_adapter_lists(const AdapterPrepArgs& a, uint32_t count, uint32_t start,
-                                    uint32_t* s_scan, uint32_t* s_start, uint32_t* s_ustart,
+// from the groups' sizes, into memory if `write`, and s_start, s_ustart in any case. Thread g
+// holds group g's count and first compact row.
+__device__ void build_adapter_lists(const AdapterPrepArgs& a, bool write, uint32_t count,
+                                    uint32_t start, uint32_t* s_scan, uint32_t* s_start, uint32_t* s_ustart,
                                     uint32_t* s_seg_end) {
   const int g = threadIdx.x;
   const bool group = g <= a.A;
@@ -171,9 +180,12 @@ __device__ void build_adapter_lists(const AdapterPrepArgs& a, uint32_t count, ui
   const uint32_t nb = group ? (count + a.rb - 1) / a.rb : 0u;
   const uint32_t rb0 = block_scan_u32(nb, s_scan, &n_rb);
   if (group) {
-    a.t.off[g] = ustart;
     s_start[g] = start;
     s_ustart[g] = ustart;
+  }
+  if (!write) return;
+  if (group) {
+    a.t.off[g] = ustart;
     for (uint32_t j = 0; j < nb; ++j) {
       const uint32_t left = count - j * a.rb;
       a.t.rblist[rb0 + j] = make_int4(
@@ -226,40 +238,63 @@ __device__ __forceinline__ void put_token(const AdapterPrepArgs& a, int64_t toke
 }
 
 __global__ void __launch_bounds__(1024) adapter_prep_small_kernel(const AdapterPrepArgs a) {
-  extern __shared__ uint32_t s_cnt[];  // [warps][A + 1], then 4 x [A + 1]
+  // [warps][A + 1] counters, [kCluster][A + 1] counts of every block, 4 x [A + 1], the block's keys
+  extern __shared__ uint32_t s_cnt[];
   __shared__ uint32_t s_scan[33];
-  __shared__ int s_bad;
+  __shared__ int s_bad[kCluster];
   ptx::griddep_wait();
   const int G = a.A + 1, warps = blockDim.x >> 5;
-  uint32_t* s_start = s_cnt + warps * G;
+  const int C = static_cast<int>(gridDim.x), rank = static_cast<int>(blockIdx.x);  // one cluster
+  uint32_t* s_all = s_cnt + warps * G;
+  uint32_t* s_start = s_all + kCluster * G;
   uint32_t *s_ustart = s_start + G, *s_seg = s_ustart + G, *s_count = s_seg + G;
-  if (threadIdx.x == 0) s_bad = 0;
-  __syncthreads();
-  const int n = static_cast<int>(a.T);
+  uint16_t* s_key = reinterpret_cast<uint16_t*>(s_count + G);
+  const int64_t t0 = static_cast<int64_t>(rank) * a.tokens_per_block;
+  const int64_t left = a.T - t0;
+  const int n = left < 0 ? 0
+                         : (left < a.tokens_per_block ? static_cast<int>(left)
+                                                      : a.tokens_per_block);
+  bool bad = false;
+#pragma unroll 8
   for (int e = threadIdx.x; e < n; e += blockDim.x) {
-    const int64_t id = a.adapter[e];
-    if (id < -1 || id >= a.A) s_bad = 1;
+    const int64_t id = a.adapter[t0 + e];
+    bad = bad || id < -1 || id >= a.A;
+    s_key[e] = static_cast<uint16_t>(adapter_key(id, a.A));
   }
+  bad = __syncthreads_or(bad);
   const int run = ((n + warps - 1) / warps + 31) / 32 * 32;
-  auto key = [&](int e) { return adapter_key(a.adapter[e], a.A); };
+  auto key = [&](int e) { return static_cast<int>(s_key[e]); };
   sort_count(s_cnt, G, n, run, key);
   const int g = threadIdx.x;
-  uint32_t c = 0, total;
+  // every block's counts to every block
   if (g < G) {
+    uint32_t c = 0;
     for (int w = 0; w < warps; ++w) c += s_cnt[w * G + g];
+    for (int d = 0; d < C; ++d) st_cluster_u32(ptx::mapa(&s_all[rank * G + g], d), c);
+  }
+  if (g == 0) st_cluster_u32(ptx::mapa(&s_bad[rank], 0), bad ? 1u : 0u);
+  ptx::cluster_sync();
+  uint32_t c = 0, mine = 0, total;
+  if (g < G) {
+    for (int d = 0; d < C; ++d) {
+      if (d == rank) mine = c;
+      c += s_all[d * G + g];
+    }
     s_count[g] = c;
   }
   const uint32_t start = block_scan_u32(c, s_scan, &total);
-  build_adapter_lists(a, c, start, s_scan, s_start, s_ustart, s_seg);
+  build_adapter_lists(a, rank == 0, c, start, s_scan, s_start, s_ustart, s_seg);
   __syncthreads();
   sort_place(
-      s_cnt, G, n, run, key, [&](int) { return start; },
+      s_cnt, G, n, run, key, [&](int) { return start + mine; },
       [&](int e, uint32_t where) {
         const int k = key(e);
-        put_token(a, e, k, where, s_start[k], s_ustart[k], s_count[k]);
+        put_token(a, t0 + e, k, where, s_start[k], s_ustart[k], s_count[k]);
       });
-  if (threadIdx.x == 0) {
-    a.t.hdr->status = s_bad ? kStIndex : 0u;
+  if (rank == 0 && threadIdx.x == 0) {
+    int any = 0;
+    for (int d = 0; d < C; ++d) any |= s_bad[d];
+    a.t.hdr->status = any ? kStIndex : 0u;
     a.t.hdr->sched_next = 0;
     a.t.hdr->timeout_site = 0;
     a.t.hdr->unsorted = 0;
@@ -293,7 +328,7 @@ __global__ void __launch_bounds__(1024) adapter_lists_kernel(const AdapterPrepAr
   const uint32_t c = g < G ? static_cast<uint32_t>(a.t.off[g]) : 0u;
   uint32_t total;
   const uint32_t start = block_scan_u32(c, s_scan, &total);
-  build_adapter_lists(a, c, start, s_scan, s_lists, s_lists + G, s_lists + 2 * G);
+  build_adapter_lists(a, true, c, start, s_scan, s_lists, s_lists + G, s_lists + 2 * G);
   // [blocks of this group's prefix sums become first rows]
   __syncthreads();
   if (g < G) {
@@ -358,30 +393,32 @@ cudaError_t launch_rows_prep(const RowsPrepArgs& a, int num_sms, cudaStream_t st
                     stream, 1, a);
 }
 
-// Blocks of the counting and placement launches; 1: one launch does everything.
+// Blocks of the counting and placement launches, and the tokens of each; at most kCluster blocks:
+// one launch, one cluster.
 void adapter_blocks(int64_t T, int* blocks, int* tokens_per_block) {
-  if (T <= kSmallTokens) {
-    *blocks = 1;
-    *tokens_per_block = static_cast<int>(T);
-    return;
-  }
-  int64_t per = (T + 511) / 512;
-  per = (per + kSortThreads - 1) / kSortThreads * kSortThreads;
+  int64_t n = T <= 512 ? 1 : T <= kSmallTokens ? kCluster : 512;  // (count_scan takes up to 608)
+  int64_t per = (T + n - 1) / n;
+  if (n > kCluster) per = (per + kSortThreads - 1) / kSortThreads * kSortThreads;
   *tokens_per_block = static_cast<int>(per);
-  *blocks = static_cast<int>((T + per - 1) / per);
+  *blocks = static_cast<int>(n > kCluster ? (T + per - 1) / per : n);
 }
 
 cudaError_t launch_adapter_prep(const AdapterPrepArgs& a, cudaStream_t stream) {
   const int G = a.A + 1;
-  if (a.blocks == 1) {
-    int threads = static_cast<int>((a.T > G ? a.T : G) + 31) / 32 * 32;
-    if (threads > 1024) threads = 1024;
-    const size_t smem = static_cast<size_t>(threads / 32 + 4) * G * 4;
-    cudaError_t err = cudaFuncSetAttribute(
-        adapter_prep_small_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-        static_cast<int>(smem));
-    if (err != cudaSuccess) return err;
-    return launch_pdl(adapter_prep_small_kernel, dim3(1), dim3(threads), smem, stream, 1, a);
+  if (a.blocks <= kCluster) {
+    int threads = a.tokens_per_block > G ? a.tokens_per_block : G;
+    if (threads > 512) threads = G > 512 ? G : 512;
+    threads = (threads + 31) / 32 * 32;
+    const size_t smem = static_cast<size_t>(threads / 32 + kCluster + 4) * G * 4 +
+                        static_cast<size_t>(a.tokens_per_block) * 2;
+    if (smem > 32 * 1024) {
+      cudaError_t err = cudaFuncSetAttribute(
+          adapter_prep_small_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+          static_cast<int>(smem));
+      if (err != cudaSuccess) return err;
+    }
+    return launch_pdl(adapter_prep_small_kernel, dim3(a.blocks), dim3(threads), smem, stream,
+                      static_cast<unsigned>(a.blocks), a);
   }
   cudaError_t err = launch_pdl(adapter_count_kernel, dim3(a.blocks), dim3(kSortThreads),
                                static_cast<size_t>(G) * 4, stream, 1, a);

@@ -143,8 +143,7 @@ struct RowsArgs {
   int32_t R;
   int32_t n_blocks;
   int32_t padded;          // kShrink: fill the last row block of an adapter with zeros to 64 rows
-  int32_t u_by_token;      // kShrink: u is fp32 in token order (few-token kAdapt reads it so)
-  const int64_t* adapter;  // few-token kAdapt: [T]
+  const int64_t* adapter;  // few tokens: [T]; u is fp32 in token order then
   int32_t hold_release;
   uint64_t wait_limit_ns;
 };
@@ -160,9 +159,12 @@ int rows_wide_smem();
 int rows_wide_threads();
 int rows_wide_stages();
 
-// Tensor cores, at most NR rows per block (kGated 16, 32, 64, 128; kShrink 16, 128; kAdapt 16, 64).
+// Tensor cores, at most NR rows per block (kGated 16, 32, 64, 128; kShrink and kAdapt 16, 64).
 cudaError_t launch_rows_skinny(int dtype, RowsMode mode, int NR, RowsArgs a, int64_t live_blocks,
                                int num_sms, cudaStream_t stream);
+
+// Few tokens: u [T, R] fp32 in token order (R and K multiples of 8), and the ids' check.
+cudaError_t launch_few_shrink(int dtype, const RowsArgs& a, cudaStream_t stream);
 
 // ------------------------------------------------------------ gradient of the gate
 

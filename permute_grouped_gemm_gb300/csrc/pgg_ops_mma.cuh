@@ -1,6 +1,9 @@
 // Device pieces shared by the tensor-core kernels of the gated product and the adapters.
 #pragma once
 
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
 #include <cstdint>
 
 #include "pgg_ops.h"
@@ -29,6 +32,36 @@ __device__ __forceinline__ void zero_rows16(const RowsArgs& a) {
       static_cast<uint16_t*>(a.gate_up)[2 * q + 1] = 0;
     }
   }
+}
+
+// Two 16-bit values of a 32-bit word <-> fp32 (round to nearest even).
+template <int DT>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  if constexpr (DT == PGG_BF16) {
+    const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&p);
+  } else {
+    const __half2 p = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&p);
+  }
+}
+
+template <int DT>
+__device__ __forceinline__ float2 unpack2(uint32_t w) {
+  if constexpr (DT == PGG_BF16)
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+  else
+    return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+
+// A float into the shared memory of a CTA of the cluster (address from ptx::mapa).
+__device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+
+// Programmatic dependent launch: the launch behind this one may start.
+__device__ __forceinline__ void launch_dependents() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
 // p * silu(g) * u for a 16-bit output: the fast exponential and reciprocal, whose error (a few

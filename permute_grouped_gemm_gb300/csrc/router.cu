@@ -9,8 +9,7 @@
 //     rows     = the pairs (token, j) sorted by (expert, token * k + j)
 //
 // A warp takes one token: its logits sit in registers (G / 32 a lane) as
-// sortable integers, and each of the k rounds is a lane-local maximum, one
-// warp-wide integer maximum of the keys and one minimum of the index. A NaN key
+// sortable integers; see choose_and_write. A NaN key
 // sorts below everything (the choice stays a valid one); scores follow IEEE
 // arithmetic, so a NaN or +inf logit gives NaN weights. A masked expert
 // (-inf) has weight 0; a token whose experts are all masked takes the lowest
@@ -37,6 +36,7 @@ namespace {
 constexpr int kWarps = 8;           // of the choice, placement and gradient blocks
 constexpr int kSmallEntries = 2048; // one block does it all up to this many (token, j) pairs
 constexpr int kSmallThreads = 1024;
+constexpr int kMaxBlocks = 608;     // of the choice and placement launches: four a multiprocessor
 
 template <int DT>
 __device__ __forceinline__ float load_logit(const void* p, int64_t i) {
@@ -45,12 +45,11 @@ __device__ __forceinline__ float load_logit(const void* p, int64_t i) {
   if constexpr (DT == PGG_BF16) return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
 }
 
-// Order-preserving map of a float to an integer: NaN -> 0, -inf -> 1 or more,
-// -0 and +0 to the same.
+// Order-preserving map of a float (not -0) to an integer: NaN -> 1, -inf far above it.
 __device__ __forceinline__ uint32_t sort_key(float f) {
-  if (f != f) return 0u;
-  const uint32_t u = __float_as_uint(f + 0.0f);
-  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+  const int32_t u = __float_as_int(f);
+  const uint32_t k = static_cast<uint32_t>(u ^ ((u >> 31) | static_cast<int32_t>(0x80000000)));
+  return f != f ? 1u : k;
 }
 
 __device__ __forceinline__ float warp_sum(float v) {
@@ -72,92 +71,181 @@ __device__ __forceinline__ float soft_exp(float l, float m) {
 
 __device__ __forceinline__ float sigmoid(float l) { return 1.0f / (1.0f + expf(-l)); }
 
-// Chooses token t's experts with one warp: lane j < k returns expert and weight j.
-template <int DT, int V>
-__device__ __forceinline__ void choose(const RouteArgs& a, int64_t t, int lane, int* expert,
-                                       float* prob) {
-  float l[V];
-  uint32_t key[V];
-  float m = -INFINITY;
-  const int64_t row = t * a.G;
-#pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int e = lane + 32 * i;
-    l[i] = e < a.G ? load_logit<DT>(a.logits, row + e) : -INFINITY;
-  }
-#pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int e = lane + 32 * i;
-    m = fmaxf(m, l[i]);
-    // keys are shifted up by one (NaN 1), so that 0 marks what is taken or not there
-    key[i] = e < a.G ? sort_key(a.bias ? l[i] + a.bias[e] : l[i]) : 0u;
-    if (e < a.G && key[i] == 0u) key[i] = 1u;
-  }
-  // what was chosen: lane j keeps round j's expert and logit
-  int my_e = 0;
-  float my_l = -INFINITY;
-  for (int j = 0; j < a.k; ++j) {
-    uint32_t best = 0;
-    int slot = 0;
+// Where value i of a lane sits in a row: VL neighbouring values a load, 32 VL a warp.
+template <int VL>
+__device__ __forceinline__ int expert_at(int i, int lane) {
+  return (i / VL) * (32 * VL) + lane * VL + i % VL;
+}
+
+// A row's logits, V a lane; -inf past the end. VL > 1: 4 VL or 2 VL bytes a load (G is a multiple
+// of VL and the rows are aligned to it).
+template <int DT, int V, int VL>
+__device__ __forceinline__ void load_row(const void* logits, int64_t row, int G, int lane,
+                                         float (&l)[V]) {
+  constexpr int kBytes = VL * (DT == PGG_F32 ? 4 : 2);
+  if constexpr (VL == 1) {
 #pragma unroll
     for (int i = 0; i < V; ++i)
-      if (key[i] > best) {
-        best = key[i];
-        slot = i;
-      }
-    const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, best);
-    const uint32_t idx = __reduce_min_sync(
-        0xFFFFFFFFu, best == top ? static_cast<uint32_t>(lane + 32 * slot) : 0xFFFFFFFFu);
-    const int owner = static_cast<int>(idx & 31u), oslot = static_cast<int>(idx >> 5);
-    float v = 0.0f;
+      l[i] = expert_at<1>(i, lane) < G ? load_logit<DT>(logits, row + expert_at<1>(i, lane))
+                                       : -INFINITY;
+  } else {
 #pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (i == oslot) {
-        v = l[i];
-        if (lane == owner) key[i] = 0u;
+    for (int i = 0; i < V; i += VL) {
+      const int e = expert_at<VL>(i, lane);
+      uint32_t w[4] = {0, 0, 0, 0};
+      if (e < G) {
+        const char* p = static_cast<const char*>(logits) + (row + e) * (kBytes / VL);
+        if constexpr (kBytes == 16) {
+          const uint4 q = *reinterpret_cast<const uint4*>(p);
+          w[0] = q.x, w[1] = q.y, w[2] = q.z, w[3] = q.w;
+        } else if constexpr (kBytes == 8) {
+          const uint2 q = *reinterpret_cast<const uint2*>(p);
+          w[0] = q.x, w[1] = q.y;
+        } else {
+          w[0] = *reinterpret_cast<const uint32_t*>(p);
+        }
       }
-    v = __shfl_sync(0xFFFFFFFFu, v, owner);
-    if (lane == j) {
-      my_e = static_cast<int>(idx);
-      my_l = v;
+#pragma unroll
+      for (int c = 0; c < VL; ++c) {
+        float f;
+        if constexpr (DT == PGG_F32)
+          f = __uint_as_float(w[c]);
+        else if constexpr (DT == PGG_BF16)
+          f = __uint_as_float(c % 2 ? w[c / 2] & 0xFFFF0000u : w[c / 2] << 16);
+        else
+          f = __half2float(__ushort_as_half(
+              static_cast<unsigned short>(c % 2 ? w[c / 2] >> 16 : w[c / 2] & 0xFFFFu)));
+        l[i + c] = e < G ? f : -INFINITY;
+      }
     }
   }
+}
+
+template <int V, int VL>
+__device__ __forceinline__ void load_bias(const float* bias, int G, int lane, float (&b)[V]) {
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int e = expert_at<VL>(i, lane);
+    b[i] = (bias && e < G ? bias[e] : 0.0f) + 0.0f;  // (-0 becomes +0)
+  }
+}
+
+// Token t's choice with one warp, written to probs, experts and s_expert [k].
+//
+// The k-th largest of the lanes' maxima is at most the k-th largest key, so
+// the chosen are among the keys that reach it: rarely more than k plus a
+// few. They are collected, one a lane, and each finds its rank by counting
+// those before it. Only when equal keys leave more than 32 of them the k
+// rounds of a warp-wide maximum are done instead. About 400 instructions a
+// token at 256 experts and k = 8, half of what the rounds take.
+template <int DT, int V, int VL>
+__device__ __forceinline__ void choose_and_write(const RouteArgs& a, int64_t t, int lane,
+                                                 const float (&bias)[V], uint64_t* s_cand,
+                                                 int* s_expert) {
+  float l[V];
+  uint32_t key[V];
+  const int64_t row = t * a.G;
+  load_row<DT, V, VL>(a.logits, row, a.G, lane, l);
+  uint32_t best = 0;
+#pragma unroll
+  for (int i = 0; i < V; i += VL) {
+    // 0: not there (a whole load is, or is not)
+    const bool there = expert_at<VL>(i, lane) < a.G;
+#pragma unroll
+    for (int c = i; c < i + VL; ++c) {
+      // (the bias is +0 without one, so a sum is never -0)
+      key[c] = there ? sort_key(l[c] + bias[c]) : 0u;
+      best = key[c] > best ? key[c] : best;
+    }
+  }
+  uint32_t floor_key = 0;
+  for (int seen = 0; seen < a.k;) {
+    floor_key = __reduce_max_sync(0xFFFFFFFFu, best);
+    if (floor_key == 0) break;  // (fewer lanes than k hold anything: all that is there)
+    const bool top = best == floor_key;
+    seen += __popc(__ballot_sync(0xFFFFFFFFu, top));
+    if (top) best = 0;
+  }
+  if (floor_key == 0) floor_key = 1;
+  int mine_n = 0;  // candidates of this lane, and of the lanes up to it
+#pragma unroll
+  for (int i = 0; i < V; ++i) mine_n += key[i] >= floor_key ? 1 : 0;
+  int upto = mine_n;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int y = __shfl_up_sync(0xFFFFFFFFu, upto, d);
+    if (lane >= d) upto += y;
+  }
+  const int n = __shfl_sync(0xFFFFFFFFu, upto, 31);
+  int e = 0, rank = 32;
+  if (n <= 32) {
+    // key above, the index's complement below: a larger number comes first
+    uint64_t* at = s_cand + (upto - mine_n);
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (key[i] >= floor_key)
+        *at++ = static_cast<uint64_t>(key[i]) << 32 |
+                static_cast<uint32_t>(~expert_at<VL>(i, lane));
+    __syncwarp();
+    const uint64_t mine = lane < n ? s_cand[lane] : 0u;
+    int before = 0;
+#pragma unroll 4
+    for (int j = 0; j < n; ++j) before += s_cand[j] > mine ? 1 : 0;
+    __syncwarp();
+    if (lane < n && before < a.k) {
+      rank = before;
+      e = static_cast<int>(~static_cast<uint32_t>(mine));
+    }
+  } else {
+    for (int j = 0; j < a.k; ++j) {
+      uint32_t top = 0, where = 0xFFFFFFFFu;
+#pragma unroll
+      for (int i = 0; i < V; ++i) top = key[i] > top ? key[i] : top;
+      top = __reduce_max_sync(0xFFFFFFFFu, top);
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const uint32_t x = static_cast<uint32_t>(expert_at<VL>(i, lane));
+        if (key[i] == top && x < where) where = x;
+      }
+      where = __reduce_min_sync(0xFFFFFFFFu, where);
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (static_cast<uint32_t>(expert_at<VL>(i, lane)) == where) key[i] = 0;
+      if (lane == j) {
+        e = static_cast<int>(where);
+        rank = j;
+      }
+    }
+  }
+  const bool on = rank < 32;
+  const float my_l = on ? load_logit<DT>(a.logits, row + e) : -INFINITY;
   float p;
   if (a.sigmoid) {
-    p = lane < a.k ? sigmoid(my_l) : 0.0f;
+    p = on ? sigmoid(my_l) : 0.0f;
     if (a.renormalize) {
       const float z = warp_sum(p);
       p = z == 0.0f ? 0.0f : p / z;
     }
   } else if (a.renormalize) {
     // softmax over the chosen alone: the others' part cancels
-    const float mc = warp_max(lane < a.k ? my_l : -INFINITY);
-    p = lane < a.k ? soft_exp(my_l, mc) : 0.0f;
+    const float m = warp_max(my_l);
+    p = on ? soft_exp(my_l, m) : 0.0f;
     const float z = warp_sum(p);
-    p = mc == -INFINITY && z == 0.0f ? 0.0f : p / z;
+    p = m == -INFINITY && z == 0.0f ? 0.0f : p / z;
   } else {
-    m = warp_max(m);
-    float z = 0.0f;
+    float m = -INFINITY, z = 0.0f;
 #pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (lane + 32 * i < a.G) z += soft_exp(l[i], m);
+    for (int i = 0; i < V; ++i) m = fmaxf(m, l[i]);
+    m = warp_max(m);
+#pragma unroll
+    for (int i = 0; i < V; ++i) z += soft_exp(l[i], m);  // (0 past the end)
     z = warp_sum(z);
     p = m == -INFINITY && z == 0.0f ? 0.0f : soft_exp(my_l, m) / z;
   }
-  *expert = my_e;
-  *prob = p * a.scale;
-}
-
-template <int DT, int V>
-__device__ __forceinline__ void choose_and_write(const RouteArgs& a, int64_t t, int lane,
-                                                 int* s_expert) {
-  int e;
-  float p;
-  choose<DT, V>(a, t, lane, &e, &p);
-  if (lane < a.k) {
-    a.experts[t * a.k + lane] = e;
-    a.probs[t * a.k + lane] = p;
-    s_expert[lane] = e;
+  if (on) {
+    a.experts[t * a.k + rank] = e;
+    a.probs[t * a.k + rank] = p * a.scale;
+    s_expert[rank] = e;
   }
 }
 
@@ -169,15 +257,19 @@ __device__ __forceinline__ void write_place(const RouteArgs& a, int64_t p, int64
 }
 
 // Everything in one block.
-template <int DT, int V>
+template <int DT, int V, int VL>
 __global__ void __launch_bounds__(kSmallThreads) route_small_kernel(const RouteArgs a) {
   extern __shared__ uint32_t s_cnt[];  // [warps][G], then the entries' experts
   __shared__ uint32_t s_scan[33];
+  __shared__ uint64_t s_cand[kSmallThreads / 32][32];
   ptx::griddep_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   int* s_expert = reinterpret_cast<int*>(s_cnt + warps * a.G);
   const int T = static_cast<int>(a.T), n = T * a.k;
-  for (int t = warp; t < T; t += warps) choose_and_write<DT, V>(a, t, lane, s_expert + t * a.k);
+  float bias[V];
+  load_bias<V, VL>(a.bias, a.G, lane, bias);
+  for (int t = warp; t < T; t += warps)
+    choose_and_write<DT, V, VL>(a, t, lane, bias, s_cand[warp], s_expert + t * a.k);
   __syncthreads();
   const int run = ((n + warps - 1) / warps + 31) / 32 * 32;
   auto key = [&](int e) { return s_expert[e]; };
@@ -198,9 +290,10 @@ __global__ void __launch_bounds__(kSmallThreads) route_small_kernel(const RouteA
 }
 
 // (1) Choice, and the block's count of every expert.
-template <int DT, int V>
-__global__ void __launch_bounds__(32 * kWarps) route_choose_kernel(const RouteArgs a) {
+template <int DT, int V, int VL>
+__global__ void __launch_bounds__(32 * kWarps, V <= 8 ? 4 : 2) route_choose_kernel(const RouteArgs a) {
   extern __shared__ uint32_t s_cnt[];  // [G]
+  __shared__ uint64_t s_cand[kWarps][32];
   __shared__ int s_expert[kWarps][kMaxRouteTopK];
   ptx::griddep_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -209,8 +302,10 @@ __global__ void __launch_bounds__(32 * kWarps) route_choose_kernel(const RouteAr
   __syncthreads();
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * a.tokens_per_block;
   const int64_t t1 = t0 + a.tokens_per_block < a.T ? t0 + a.tokens_per_block : a.T;
+  float bias[V];
+  load_bias<V, VL>(a.bias, a.G, lane, bias);
   for (int64_t t = t0 + warp; t < t1; t += kWarps) {
-    choose_and_write<DT, V>(a, t, lane, s_expert[warp]);
+    choose_and_write<DT, V, VL>(a, t, lane, bias, s_cand[warp], s_expert[warp]);
     __syncwarp();
     // (integer counts: the order of these additions changes nothing)
     if (lane < a.k) atomicAdd(&s_cnt[s_expert[warp][lane]], 1u);
@@ -229,17 +324,23 @@ __global__ void __launch_bounds__(32 * kWarps) count_scan_kernel(uint32_t* count
   const int g = blockIdx.x * kWarps + (threadIdx.x >> 5);
   if (g >= G) return;
   uint32_t* row = counts + static_cast<int64_t>(g) * blocks;
+  uint32_t v[kMaxBlocks / 32];  // all loads at once: their latency is what this launch costs
+#pragma unroll
+  for (int i = 0; i < kMaxBlocks / 32; ++i) {
+    const int b = 32 * i + lane;
+    v[i] = b < blocks ? row[b] : 0u;
+  }
   uint32_t sum = 0;
-  for (int b0 = 0; b0 < blocks; b0 += 32) {
-    const int b = b0 + lane;
-    const uint32_t v = b < blocks ? row[b] : 0u;
-    uint32_t x = v;
+#pragma unroll
+  for (int i = 0; i < kMaxBlocks / 32; ++i) {
+    if (32 * i >= blocks) break;
+    uint32_t x = v[i];
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
       const uint32_t y = __shfl_up_sync(0xFFFFFFFFu, x, d);
       if (lane >= d) x += y;
     }
-    if (b < blocks) row[b] = sum + x - v;
+    if (32 * i + lane < blocks) row[32 * i + lane] = sum + x - v[i];
     sum += __shfl_sync(0xFFFFFFFFu, x, 31);
   }
   if (lane == 0) groups[g] = sum;
@@ -292,33 +393,39 @@ __global__ void __launch_bounds__(32 * kWarps) route_grad_kernel(const RouteGrad
   for (int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + warp; t < a.T;
        t += static_cast<int64_t>(gridDim.x) * kWarps) {
     const int64_t row = t * a.G;
-    for (int e = lane; e < a.G; e += 32) ds[e] = 0.0f;
     const bool on = lane < a.k;
     const int64_t e64 = on ? a.experts[t * a.k + lane] : 0;
+    const float dp = on ? a.d_probs[t * a.k + lane] * a.scale : 0.0f;
+    float l[V];
+    if (!a.sigmoid && !a.renormalize) {
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        l[i] = lane + 32 * i < a.G ? load_logit<DT>(a.logits, row + lane + 32 * i) : -INFINITY;
+    }
+    for (int e = lane; e < a.G; e += 32) ds[e] = 0.0f;
     const bool in = e64 >= 0 && e64 < a.G;
     const int e = in ? static_cast<int>(e64) : 0;
     const uint32_t same = __match_any_sync(0xFFFFFFFFu, on ? e : -1 - lane);
     const bool bad = __any_sync(0xFFFFFFFFu, on && (!in || __popc(same) > 1));
-    const float dp = on ? a.d_probs[t * a.k + lane] * a.scale : 0.0f;
     __syncwarp();
     if (bad) {
       for (int i = lane; i < a.G; i += 32) ds[i] = NAN;
     } else if (a.sigmoid || a.renormalize) {
-      const float l = on ? load_logit<DT>(a.logits, row + e) : -INFINITY;
+      const float lj = on ? load_logit<DT>(a.logits, row + e) : -INFINITY;
       float p, w;  // normalised weight, and d(weight before normalising) / d(logit) over the sum
       if (a.sigmoid) {
-        const float s = on ? sigmoid(l) : 0.0f;
+        const float s = on ? sigmoid(lj) : 0.0f;
         if (a.renormalize) {
           const float z = warp_sum(s);
           p = z == 0.0f ? 0.0f : s / z;
-          w = p * sigmoid(-l);  // 1 - s without its cancellation
+          w = p * sigmoid(-lj);  // 1 - s without its cancellation
         } else {
           p = 0.0f;
-          w = s * sigmoid(-l);
+          w = s * sigmoid(-lj);
         }
       } else {
-        const float m = warp_max(l);
-        p = on ? soft_exp(l, m) : 0.0f;
+        const float m = warp_max(lj);
+        p = on ? soft_exp(lj, m) : 0.0f;
         const float z = warp_sum(p);
         p = m == -INFINITY && z == 0.0f ? 0.0f : p / z;
         w = p;
@@ -326,10 +433,7 @@ __global__ void __launch_bounds__(32 * kWarps) route_grad_kernel(const RouteGrad
       const float dot = a.renormalize ? warp_sum(on ? dp * p : 0.0f) : 0.0f;
       if (on) ds[e] = w * (dp - dot);
     } else {
-      float l[V], m = -INFINITY, z = 0.0f, dot = 0.0f;
-#pragma unroll
-      for (int i = 0; i < V; ++i)
-        l[i] = lane + 32 * i < a.G ? load_logit<DT>(a.logits, row + lane + 32 * i) : -INFINITY;
+      float m = -INFINITY, z = 0.0f, dot = 0.0f;
       if (on) ds[e] = dp;
       __syncwarp();
 #pragma unroll
@@ -370,34 +474,54 @@ int log2_slots(int G) {
   return i;
 }
 
-template <int DT>
-cudaError_t launch_route_t(const RouteArgs& a, cudaStream_t stream) {
-  using K = void (*)(const RouteArgs);
-  static const K small[6] = {route_small_kernel<DT, 1>, route_small_kernel<DT, 2>,
-                             route_small_kernel<DT, 4>, route_small_kernel<DT, 8>,
-                             route_small_kernel<DT, 16>, route_small_kernel<DT, 32>};
-  static const K many[6] = {route_choose_kernel<DT, 1>, route_choose_kernel<DT, 2>,
-                            route_choose_kernel<DT, 4>, route_choose_kernel<DT, 8>,
-                            route_choose_kernel<DT, 16>, route_choose_kernel<DT, 32>};
-  const int v = log2_slots(a.G);
+// Widest load of a row's logits: VL values, when the rows are a multiple of it and aligned to it.
+template <int DT, int V>
+constexpr int load_width() {
+  return V < (DT == PGG_F32 ? 4 : 8) ? V : (DT == PGG_F32 ? 4 : 8);
+}
+
+template <int DT, int V, int VL>
+cudaError_t launch_route_v(const RouteArgs& a, cudaStream_t stream) {
   if (a.blocks == 1) {
     // threads for the tokens and for the experts' scan, no more: fewer counters to clear
     int threads = static_cast<int>(a.T < 32 ? a.T : 32) * 32;
     const int for_scan = (a.G + 31) / 32 * 32;
     if (threads < for_scan) threads = for_scan;
     const size_t smem = (static_cast<size_t>(threads / 32) * a.G + a.T * a.k) * 4;
-    cudaError_t err = cudaFuncSetAttribute(small[v], cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                           static_cast<int>(smem));
-    if (err != cudaSuccess) return err;
-    return launch_pdl(small[v], dim3(1), dim3(threads), smem, stream, 1, a);
+    auto kern = route_small_kernel<DT, V, VL>;
+    if (smem > 32 * 1024) {
+      cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             static_cast<int>(smem));
+      if (err != cudaSuccess) return err;
+    }
+    return launch_pdl(kern, dim3(1), dim3(threads), smem, stream, 1, a);
   }
-  cudaError_t err = launch_pdl(many[v], dim3(a.blocks), dim3(32 * kWarps),
+  cudaError_t err = launch_pdl(route_choose_kernel<DT, V, VL>, dim3(a.blocks), dim3(32 * kWarps),
                                static_cast<size_t>(a.G) * 4, stream, 1, a);
   if (err != cudaSuccess) return err;
   err = launch_count_scan(a.counts, a.G, a.blocks, a.groups, stream);
   if (err != cudaSuccess) return err;
   return launch_pdl(route_place_kernel, dim3(a.blocks), dim3(32 * kWarps),
                     static_cast<size_t>(kWarps + 1) * a.G * 4, stream, 1, a);
+}
+
+template <int DT, int V>
+cudaError_t launch_route_t(const RouteArgs& a, cudaStream_t stream) {
+  constexpr int kVL = load_width<DT, V>();
+  constexpr uintptr_t kAlign = kVL * (DT == PGG_F32 ? 4 : 2);
+  if (kVL > 1 && a.G % kVL == 0 && reinterpret_cast<uintptr_t>(a.logits) % kAlign == 0)
+    return launch_route_v<DT, V, kVL>(a, stream);
+  return launch_route_v<DT, V, 1>(a, stream);
+}
+
+template <int DT>
+cudaError_t launch_route_d(const RouteArgs& a, cudaStream_t stream) {
+  if (a.G <= 32) return launch_route_t<DT, 1>(a, stream);
+  if (a.G <= 64) return launch_route_t<DT, 2>(a, stream);
+  if (a.G <= 128) return launch_route_t<DT, 4>(a, stream);
+  if (a.G <= 256) return launch_route_t<DT, 8>(a, stream);
+  if (a.G <= 512) return launch_route_t<DT, 16>(a, stream);
+  return launch_route_t<DT, 32>(a, stream);
 }
 
 }  // namespace
@@ -409,23 +533,23 @@ cudaError_t launch_count_scan(uint32_t* counts, int G, int blocks, int64_t* grou
 }
 
 // Blocks of the choice and placement launches: one when all the pairs fit one
-// block, else at most 1024 with a multiple of the block's warps of tokens each.
+// block, else at most kMaxBlocks with a multiple of the block's warps of tokens each.
 void route_blocks(int64_t T, int64_t G, int64_t k, int* blocks, int* tokens_per_block) {
   if (T * k <= kSmallEntries && T <= 256) {
     *blocks = 1;
     *tokens_per_block = static_cast<int>(T);
     return;
   }
-  int64_t per = (T + 1023) / 1024;
+  int64_t per = (T + kMaxBlocks - 1) / kMaxBlocks;
   per = (per + kWarps - 1) / kWarps * kWarps;
   *tokens_per_block = static_cast<int>(per);
   *blocks = static_cast<int>((T + per - 1) / per);
 }
 
 cudaError_t launch_route(int dtype, const RouteArgs& a, cudaStream_t stream) {
-  if (dtype == PGG_F32) return launch_route_t<PGG_F32>(a, stream);
-  if (dtype == PGG_F16) return launch_route_t<PGG_F16>(a, stream);
-  if (dtype == PGG_BF16) return launch_route_t<PGG_BF16>(a, stream);
+  if (dtype == PGG_F32) return launch_route_d<PGG_F32>(a, stream);
+  if (dtype == PGG_F16) return launch_route_d<PGG_F16>(a, stream);
+  if (dtype == PGG_BF16) return launch_route_d<PGG_BF16>(a, stream);
   return cudaErrorInvalidValue;
 }
 

@@ -14,14 +14,14 @@
 // workspace, bitwise repeatable. S = 1 when the tiles alone fill the GPU.
 //
 // A stage is 64 of k: two 64-column panels of the weight by TMA (16 KB) and NR
-// x rows gathered by token with cp.async. With NR = 16 eleven stages are in
-// flight per SM, 176 KB of weight, which is what keeps HBM busy.
+// x rows gathered by token with cp.async. With NR = 16 twelve stages are in
+// flight per SM, 192 KB of weight, which is what keeps HBM busy.
 //
 // adapt with few tokens: rows stay in the caller's order, and the low-rank part
-// is added in the epilogue in fp32 (a row's u and its adapter's b, read once per
-// row: the bytes the operator needs anyway). A row meets no adapter but its own.
-// Its weight stream needs nothing from the launches before it, so it starts
-// while they run (see launch_dependents in the shrink mode).
+// is added in fp32 by the epilogue warps, which work it out from a row's u and
+// its adapter's b (the bytes the operator needs anyway) while the weight still
+// streams. A row meets no adapter but its own. The stream needs nothing from the
+// launch before it (adapters_few.cu), so it starts while that one runs.
 //
 // Warp roles per CTA: 0 TMA, 1 tensor memory and MMA issue, one gather warp per
 // stage slot, four epilogue warps. Waits are bounded as everywhere.
@@ -33,6 +33,7 @@
 #include <cstring>
 
 #include "pgg_ops.h"
+#include "pgg_ops_launch.h"
 #include "pgg_ops_mma.cuh"
 #include "pgg_ptx.cuh"
 
@@ -52,7 +53,7 @@ struct Cfg {
   static constexpr int kStageBytes = kABytes + kBBytes;
   static constexpr int kRedBytes = NR * kM * 4;  // S slots of NR / S rows x 128 lanes
   static constexpr int kFit = (226 * 1024 - 2048 - kRedBytes) / kStageBytes;
-  static constexpr int kStages = kFit < 11 ? kFit : 11;
+  static constexpr int kStages = kFit < 12 ? kFit : 12;
   static constexpr int kThreads = 32 * (2 + kStages + kEpiWarps);
   static constexpr int kTmemCols = 2 * NR < 32 ? 32 : 2 * NR;
   static_assert(kBBytes % 1024 == 0, "operand alignment");
@@ -80,14 +81,6 @@ __device__ __forceinline__ uint32_t cluster_size() {
   uint32_t r;
   asm volatile("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(r));
   return r;
-}
-
-__device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
-  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
-}
-
-__device__ __forceinline__ void launch_dependents() {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
 struct Tile {
@@ -306,25 +299,6 @@ __device__ void mma_issuer(uint8_t* smem, Ctl<Cfg<NR, PANELS>::kStages>* ctl, ui
 }
 
 template <int DT>
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-  if constexpr (DT == PGG_BF16) {
-    const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&p);
-  } else {
-    const __half2 p = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&p);
-  }
-}
-
-template <int DT>
-__device__ __forceinline__ float2 unpack2(uint32_t w) {
-  if constexpr (DT == PGG_BF16)
-    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
-  else
-    return __half22float2(*reinterpret_cast<const __half2*>(&w));
-}
-
-template <int DT>
 __device__ __forceinline__ void store16(void* out, int64_t i, float v) {
   const uint32_t p = pack2<DT>(v, 0.0f);
   static_cast<uint16_t*>(out)[i] = static_cast<uint16_t>(p & 0xFFFFu);
@@ -332,9 +306,10 @@ __device__ __forceinline__ void store16(void* out, int64_t i, float v) {
 
 // Output of tile rows j, j + 4, ... < n (j: this warp's), whose first row is tile row j0: red
 // holds S slots of `slot` floats, rows of 128 lanes each.
-template <int DT, int MODE>
+template <int DT, int MODE, int LR>
 __device__ __forceinline__ void write_rows(const float* red, int slot, uint32_t S, const RowsArgs& a,
-                                           const Tile& x, int j0, int n, bool failed) {
+                                           const Tile& x, int j0, int n, bool failed,
+                                           const float (&lr)[LR][4]) {
   const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 3;
 #pragma unroll 1
   for (int j = warp; j < n; j += kEpiWarps) {
@@ -366,59 +341,76 @@ __device__ __forceinline__ void write_rows(const float* red, int slot, uint32_t 
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         v[i] = 0.0f;
+        if (MODE == kShrink && x.n0 + lane + 32 * i >= a.N) continue;
         for (uint32_t s = 0; s < S; ++s) v[i] += r[s * slot + lane + 32 * i];
       }
       if constexpr (MODE == kShrink) {
         const float sc = a.scale ? a.scale[x.g] : 1.0f;
-        const int64_t token = a.rowinfo[check_index(a.hdr, row, a.M, 95)].token;
-        const int64_t orow = a.u_by_token ? token : static_cast<int64_t>(x.urow) + j0 + j;
+        const int64_t orow = static_cast<int64_t>(x.urow) + j0 + j;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int64_t c = x.n0 + lane + 32 * i;
-          if (c >= a.N) continue;
-          if (a.u_by_token)
-            static_cast<float*>(a.out)[orow * a.N + c] = v[i] * sc;
-          else
-            store16<DT>(a.out, orow * a.N + c, v[i] * sc);
+          if (c < a.N) store16<DT>(a.out, orow * a.N + c, v[i] * sc);
         }
       } else {
-        // the row's own adapter, in fp32: u [R] against b [n][R]
-        const int64_t ad = a.adapter[row];
-        if (ad >= 0 && ad < a.G && !failed) {
-          const float* u = static_cast<const float*>(a.u) + row * a.R;
-          const char* b = static_cast<const char*>(a.b) + ((ad * a.N + x.n0) * a.R) * 2;
-#pragma unroll 1
-          for (int r0 = 0; r0 < a.R; r0 += 8) {
-            const float4 ua = __ldcg(reinterpret_cast<const float4*>(u + r0));
-            const float4 ub = __ldcg(reinterpret_cast<const float4*>(u + r0 + 4));
-            uint4 q[4];
+        // (a loop over constants: lr stays in registers)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              q[i] = make_uint4(0, 0, 0, 0);
-              if (x.n0 + lane + 32 * i < a.N)
-                q[i] = __ldg(reinterpret_cast<const uint4*>(
-                    b + (static_cast<int64_t>(lane + 32 * i) * a.R + r0) * 2));
-            }
+        for (int q = 0; q < LR; ++q)
+          if (j == warp + kEpiWarps * q) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float2 b0 = unpack2<DT>(q[i].x), b1 = unpack2<DT>(q[i].y);
-              const float2 b2 = unpack2<DT>(q[i].z), b3 = unpack2<DT>(q[i].w);
-              v[i] = fmaf(ua.x, b0.x, v[i]);
-              v[i] = fmaf(ua.y, b0.y, v[i]);
-              v[i] = fmaf(ua.z, b1.x, v[i]);
-              v[i] = fmaf(ua.w, b1.y, v[i]);
-              v[i] = fmaf(ub.x, b2.x, v[i]);
-              v[i] = fmaf(ub.y, b2.y, v[i]);
-              v[i] = fmaf(ub.z, b3.x, v[i]);
-              v[i] = fmaf(ub.w, b3.y, v[i]);
-            }
+            for (int i = 0; i < 4; ++i) v[i] += lr[q][i];
           }
-        }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int64_t c = x.n0 + lane + 32 * i;
           if (c < a.N) store16<DT>(a.out, row * a.N + c, failed ? 0.0f : v[i]);
         }
+      }
+    }
+  }
+}
+
+// Low-rank part of tile rows j0 + j, j = warp, warp + 4, ... < n: each row's u [R] against its own
+// adapter's b [n][R], 8 ranks (16 bytes of b) at a time, in fp32; lane l takes columns l + 32 i.
+template <int DT, int LR>
+__device__ __forceinline__ void low_rank(const RowsArgs& a, const Tile& x, int j0, int n,
+                                         float (&lr)[LR][4]) {
+  const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 3;
+#pragma unroll
+  for (int q = 0; q < LR; ++q) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) lr[q][i] = 0.0f;
+    const int j = warp + kEpiWarps * q;
+    if (j >= n) continue;
+    const int64_t row = x.row0 + j0 + j;
+    const int64_t ad = a.adapter[row];
+    if (ad < 0 || ad >= a.G) continue;
+    const float* u = static_cast<const float*>(a.u) + row * a.R;
+    const char* b = static_cast<const char*>(a.b) + ((ad * a.N + x.n0) * a.R) * 2;
+#pragma unroll 2
+    for (int r0 = 0; r0 < a.R; r0 += 8) {
+      const float4 ua = __ldcg(reinterpret_cast<const float4*>(u + r0));
+      const float4 ub = __ldcg(reinterpret_cast<const float4*>(u + r0 + 4));
+      uint4 w[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        w[i] = make_uint4(0, 0, 0, 0);
+        if (x.n0 + lane + 32 * i < a.N)
+          w[i] = __ldg(reinterpret_cast<const uint4*>(
+              b + (static_cast<int64_t>(lane + 32 * i) * a.R + r0) * 2));
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 b0 = unpack2<DT>(w[i].x), b1 = unpack2<DT>(w[i].y);
+        const float2 b2 = unpack2<DT>(w[i].z), b3 = unpack2<DT>(w[i].w);
+        lr[q][i] = fmaf(ua.x, b0.x, lr[q][i]);
+        lr[q][i] = fmaf(ua.y, b0.y, lr[q][i]);
+        lr[q][i] = fmaf(ua.z, b1.x, lr[q][i]);
+        lr[q][i] = fmaf(ua.w, b1.y, lr[q][i]);
+        lr[q][i] = fmaf(ub.x, b2.x, lr[q][i]);
+        lr[q][i] = fmaf(ub.y, b2.y, lr[q][i]);
+        lr[q][i] = fmaf(ub.z, b3.x, lr[q][i]);
+        lr[q][i] = fmaf(ub.w, b3.y, lr[q][i]);
       }
     }
   }
@@ -447,6 +439,13 @@ __device__ void epilogue(Ctl<Cfg<NR, PANELS>::kStages>* ctl, float* red, uint32_
       // (fills of padded rows belong to adapters only)
       continue;
     }
+    const int j0 = static_cast<int>(rank) * per;  // this CTA finishes rows j0 .. j0 + n - 1
+    const int n = x.rows - j0 < per ? x.rows - j0 : per;
+    constexpr int kLR = MODE == kAdapt ? NR / kEpiWarps : 1;
+    float lr[kLR][4];
+    if constexpr (MODE == kAdapt) {
+      if (!failed_input) low_rank<DT, kLR>(a, x, j0, n, lr);
+    }
     bool ok = ptx::mbar_wait(&ctl->tfull[acc], aph, lim, abort);
     // the others have read what they got from this CTA for the tile before
     ok = ok && ptx::mbar_wait_cluster(&ctl->rempty, rph ^ 1u, lim, abort);
@@ -461,8 +460,10 @@ __device__ void epilogue(Ctl<Cfg<NR, PANELS>::kStages>* ctl, float* red, uint32_
     const uint32_t t_lane = tmem_base + (static_cast<uint32_t>(32 * quarter) << 16) +
                             static_cast<uint32_t>(acc * NR);
     const uint32_t mine = 32 * quarter + lane;
+    // (lanes past the rank hold nothing)
+    const int cols = MODE == kShrink && x.n0 + 32 * quarter >= a.N ? 0 : x.rows;
 #pragma unroll 1
-    for (int c0 = 0; c0 < NR && c0 < x.rows; c0 += 16) {
+    for (int c0 = 0; c0 < NR && c0 < cols; c0 += 16) {
       uint32_t v[16];
       ptx::tmem_ld_32x32b_x16(t_lane + static_cast<uint32_t>(c0), v);
       ptx::tmem_ld_wait();
@@ -492,9 +493,7 @@ __device__ void epilogue(Ctl<Cfg<NR, PANELS>::kStages>* ctl, float* red, uint32_
       }
       break;
     }
-    const int j0 = static_cast<int>(rank) * per;
-    const int n = x.rows - j0 < per ? x.rows - j0 : per;
-    write_rows<DT, MODE>(red, slot, S, a, x, j0, n, failed_input);
+    write_rows<DT, MODE, kLR>(red, slot, S, a, x, j0, n, failed_input, lr);
     if constexpr (MODE == kShrink) {
       if (a.padded) {  // rows that fill the adapter up to a multiple of 64
         const int end = (x.rows + 63) / 64 * 64;
@@ -516,12 +515,7 @@ template <int DT, int MODE, int NR, int PANELS>
 __global__ void __launch_bounds__(Cfg<NR, PANELS>::kThreads, 1)
     rows_skinny_kernel(const __grid_constant__ CUtensorMap tm_w, const RowsArgs a) {
   using C = Cfg<NR, PANELS>;
-  if (MODE != kAdapt) {
-    ptx::griddep_wait();
-    // everything before this launch has completed: the adapt launch behind it, which reads only
-    // the caller's x and weight until its own wait, may start
-    if (MODE == kShrink && a.u_by_token) launch_dependents();
-  }
+  if (MODE != kAdapt) ptx::griddep_wait();
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
@@ -614,29 +608,16 @@ cudaError_t launch_t(const CUtensorMap& tm_w, const RowsArgs& a, int64_t tiles, 
   constexpr int smem = smem_bytes<NR, PANELS>();
   static_assert(smem <= 227 * 1024, "shared memory per CTA");
   auto kern = rows_skinny_kernel<DT, MODE, NR, PANELS>;
-  cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (err != cudaSuccess) return err;
   const int nks = static_cast<int>((a.K + kFK - 1) / kFK);
   const int S = choose_split(tiles, nks, NR, num_sms);
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = static_cast<unsigned>(S);
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.blockDim = dim3(C::kThreads, 1, 1);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  static ClusterLimits limits;
+  int clusters = 0;
+  const cudaError_t err =
+      clusters_that_fit(&limits, kern, C::kThreads, smem, S, num_sms, &clusters);
+  if (err != cudaSuccess) return err;
   int64_t want = num_sms / S;
   const int64_t most = (MODE == kAdapt ? (a.M + NR - 1) / NR : a.max_row_blocks) * a.n_blocks;
   if (most < want) want = most;
-  cfg.gridDim = dim3(static_cast<unsigned>(S * want), 1, 1);
-  int clusters = 0;
-  err = cudaOccupancyMaxActiveClusters(&clusters, kern, &cfg);
-  if (err != cudaSuccess) return err;
-  if (clusters < 1) return cudaErrorInvalidConfiguration;
   if (clusters < want) want = clusters;
   return launch_pdl(kern, dim3(static_cast<unsigned>(S * want)), dim3(C::kThreads),
                     static_cast<size_t>(smem), stream, static_cast<unsigned>(S), tm_w, a);
@@ -651,9 +632,11 @@ cudaError_t launch_mode(RowsMode mode, int NR, const CUtensorMap& m, const RowsA
     if (NR == 64) return launch_t<DT, kGated, 64, 2>(m, a, tiles, sms, st);
     if (NR == 128) return launch_t<DT, kGated, 128, 2>(m, a, tiles, sms, st);
   } else if (mode == kShrink) {
+    // ranks up to 64 fit one panel of the factor: more stages in flight
+    if (NR == 16 && a.N <= 64) return launch_t<DT, kShrink, 16, 1>(m, a, tiles, sms, st);
     if (NR == 16) return launch_t<DT, kShrink, 16, 2>(m, a, tiles, sms, st);
-    if (NR == 128 && a.N <= 64) return launch_t<DT, kShrink, 128, 1>(m, a, tiles, sms, st);
-    if (NR == 128) return launch_t<DT, kShrink, 128, 2>(m, a, tiles, sms, st);
+    if (NR == 64 && a.N <= 64) return launch_t<DT, kShrink, 64, 1>(m, a, tiles, sms, st);
+    if (NR == 64) return launch_t<DT, kShrink, 64, 2>(m, a, tiles, sms, st);
   } else if (mode == kAdapt) {
     if (NR == 16) return launch_t<DT, kAdapt, 16, 2>(m, a, tiles, sms, st);
     if (NR == 64) return launch_t<DT, kAdapt, 64, 2>(m, a, tiles, sms, st);

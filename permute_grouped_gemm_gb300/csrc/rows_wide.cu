@@ -39,6 +39,7 @@
 
 #include "pgg_epilogue.cuh"
 #include "pgg_ops.h"
+#include "pgg_ops_launch.h"
 #include "pgg_ops_mma.cuh"
 #include "pgg_ptx.cuh"
 
@@ -574,27 +575,12 @@ cudaError_t launch_t(RowsMode mode, const CUtensorMap& tm_w, const CUtensorMap& 
   const K kern = mode == kGated   ? K(rows_wide_kernel<DT, kGated>)
                  : mode == kAdapt ? K(rows_wide_kernel<DT, kAdapt>)
                                   : K(rows_wide_kernel<DT, kAdaptT>);
-  cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         kSmemBytes);
-  if (err != cudaSuccess) return err;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.blockDim = dim3(kThreads, 1, 1);
-  cfg.dynamicSmemBytes = kSmemBytes;
-  cfg.stream = stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  int64_t want = max_tiles < num_sms / 2 ? max_tiles : num_sms / 2;
-  if (want < 1) want = 1;
-  cfg.gridDim = dim3(static_cast<unsigned>(2 * want), 1, 1);
+  static ClusterLimits limits[3];
   int clusters = 0;
-  err = cudaOccupancyMaxActiveClusters(&clusters, kern, &cfg);
+  const cudaError_t err = clusters_that_fit(&limits[mode == kGated ? 0 : mode == kAdapt ? 1 : 2],
+                                            kern, kThreads, kSmemBytes, 2, num_sms, &clusters);
   if (err != cudaSuccess) return err;
-  if (clusters < 1) return cudaErrorInvalidConfiguration;
+  const int64_t want = max_tiles < num_sms / 2 ? max_tiles : num_sms / 2;
   return launch_pdl(kern, dim3(static_cast<unsigned>(2 * (clusters < want ? clusters : want))),
                     dim3(kThreads), static_cast<size_t>(kSmemBytes), stream, 2, tm_w, tm_b, a);
 }

@@ -131,12 +131,14 @@ def test_infinite_weights_of_one_adapter_stay_with_its_tokens(T):
     assert torch.equal(y2[rest].view(torch.int16), clean[rest].view(torch.int16))
 
 
-def test_more_tokens_than_one_block_sorts():
+def test_more_tokens_than_one_block_or_one_cluster_sorts():
     check(inputs(17000, 64, 72, 8, 200, seed=50))
     check(inputs(20000, 64, 64, 8, 1023, seed=51))
+    check(inputs(66000, 64, 72, 8, 1023, seed=55))
+    check(inputs(70000, 64, 64, 8, 3, ids="runs", seed=56))
 
 
-@pytest.mark.parametrize("T", [20, 900, 17000])
+@pytest.mark.parametrize("T", [20, 900, 17000, 66000])
 def test_an_unknown_adapter_zeroes_the_output(T):
     s = inputs(T, 64, 64, 8, 4, seed=52)
     for bad in (4, -2, 1 << 40):
@@ -214,6 +216,7 @@ def test_gradient(size, dtype, ids):
 
 def test_gradient_of_many_tokens():
     check_grad(inputs(17000, 64, 72, 8, 30, seed=61))
+    check_grad(inputs(66000, 64, 72, 8, 30, seed=65))
 
 
 def test_gradient_against_differences():
