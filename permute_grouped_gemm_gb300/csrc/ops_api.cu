@@ -124,7 +124,7 @@ struct AdapterPlan {
   int padded;
   int64_t max_row_blocks, rows_u;
   int blocks, tokens_per_block;
-  size_t off, order, padrow, rblist, segs, blkseg, counts, u, v, total;
+  size_t off, range, order, padrow, rblist, segs, blkseg, box, counts, u, v, total;
 };
 
 int check_adapters(int64_t T, int64_t K, int64_t N, int64_t R, int64_t A, int dtype) {
@@ -158,13 +158,15 @@ int adapter_plan(int64_t T, int64_t K, int64_t N, int64_t R, int64_t A, int dtyp
   adapter_blocks(T, &p->blocks, &p->tokens_per_block);
   Carver c;
   c.take(sizeof(WsHeader));
-  p->off = c.take(8 * (A + 2));
+  p->off = c.take(8 * (A + 1));
+  p->range = c.take(static_cast<int64_t>(sizeof(int4)) * (A + 1));
   p->order = c.take(static_cast<int64_t>(sizeof(RowInfo)) * T);
   p->padrow = c.take(grad ? static_cast<int64_t>(sizeof(RowInfo)) * p->rows_u : 0);
   p->rblist = c.take(static_cast<int64_t>(sizeof(int4)) * p->max_row_blocks);
   p->segs = c.take(static_cast<int64_t>(sizeof(int4)) * A);
   p->blkseg = c.take(static_cast<int64_t>(sizeof(int2)) * ((T + 255) / 256));
-  p->counts = c.take(p->blocks > 8 ? 4 * (A + 1) * (p->blocks + 2) : 0);
+  p->box = c.take(8 * ((T + 255) / 256));
+  p->counts = c.take(p->blocks > 8 ? 4 * (A + 1) * p->blocks : 0);
   p->u = c.take(p->rows_u * R * (p->variant == kVariantSkinny ? 4 : elem_size(dtype)));
   p->v = c.take(grad ? p->rows_u * R * elem_size(dtype) : 0);
   p->total = c.used;
@@ -176,17 +178,19 @@ AdapterTables tables_of(const AdapterPlan& p, void* ws) {
   AdapterTables t;
   t.hdr = reinterpret_cast<WsHeader*>(w);
   t.off = reinterpret_cast<int64_t*>(w + p.off);
+  t.range = reinterpret_cast<int4*>(w + p.range);
   t.order = reinterpret_cast<RowInfo*>(w + p.order);
   t.padrow = reinterpret_cast<RowInfo*>(w + p.padrow);
   t.rblist = reinterpret_cast<int4*>(w + p.rblist);
   t.segs = reinterpret_cast<int4*>(w + p.segs);
   t.blkseg = reinterpret_cast<int2*>(w + p.blkseg);
+  t.box = reinterpret_cast<int32_t*>(w + p.box);
   t.counts = reinterpret_cast<uint32_t*>(w + p.counts);
   return t;
 }
 
-int run_adapter_prep(const AdapterPlan& p, const AdapterTables& t, const int64_t* adapter,
-                     int64_t T, int64_t A, cudaStream_t stream) {
+int run_adapter_prep(const AdapterPlan& p, const AdapterTables& t, bool by_first,
+                     const int64_t* adapter, int64_t T, int64_t A, cudaStream_t stream) {
   AdapterPrepArgs a;
   a.adapter = adapter;
   a.t = t;
@@ -194,6 +198,7 @@ int run_adapter_prep(const AdapterPlan& p, const AdapterTables& t, const int64_t
   a.A = static_cast<int32_t>(A);
   a.rb = p.rb;
   a.padded = p.padded;
+  a.by_first = by_first ? 1 : 0;
   a.blocks = p.blocks;
   a.tokens_per_block = p.tokens_per_block;
   return status_of(launch_adapter_prep(a, stream));
@@ -262,6 +267,7 @@ int run_adapt(const AdapterPlan& p, const AdapterTables& t, const HostEnv& env, 
   a.rowinfo = t.order;
   a.segs = t.segs;
   a.blkseg = t.blkseg;
+  a.box = t.box;
   a.hdr = t.hdr;
   a.out = y;
   a.M = T;
@@ -531,7 +537,7 @@ int pgg_adapters_execute(const void* x, const void* weight, const void* a, const
     if (rc != PGG_OK) return rc;
     return run_adapt(p, t, env, false, adapter, x, weight, u, b, y, T, K, N, R, A, dtype, s);
   }
-  rc = run_adapter_prep(p, t, adapter, T, A, s);
+  rc = run_adapter_prep(p, t, true, adapter, T, A, s);
   if (rc != PGG_OK) return rc;
   rc = run_shrink(p, t, env, x, a, scale, u, T, K, R, A, dtype, s);
   if (rc != PGG_OK) return rc;
@@ -574,7 +580,13 @@ int pgg_adapters_grad(const void* d_y, const void* x, const void* weight, const 
   const AdapterTables t = tables_of(p, workspace);
   void* u = static_cast<char*>(workspace) + p.u;
   void* v = static_cast<char*>(workspace) + p.v;
-  rc = run_adapter_prep(p, t, adapter, T, A, s);
+  // on the tensor cores throughout, or, for what they cannot take, on the FP32 pipes and with the
+  // weight-gradient kernels (which want the groups by id)
+  const bool tensor = p.variant != kVariantSimt && aligned(x, 16) && aligned(d_y, 16) &&
+                      aligned(a, 16) && aligned(b, 16) && aligned(d_a, 16) && aligned(d_b, 16) &&
+                      static_cast<int64_t>(A) * ((K + 127) / 128 + (N + 127) / 128) <
+                          kInt32Max / 4;
+  rc = run_adapter_prep(p, t, tensor, adapter, T, A, s);
   if (rc != PGG_OK) return rc;
   rc = run_shrink(p, t, env, x, a, scale, u, T, K, R, A, dtype, s);
   if (rc != PGG_OK) return rc;
@@ -583,6 +595,29 @@ int pgg_adapters_grad(const void* d_y, const void* x, const void* weight, const 
   if (d_x) {
     rc = run_adapt(p, t, env, true, nullptr, d_y, weight, v, a, d_x, T, N, K, R, A, dtype, s);
     if (rc != PGG_OK) return rc;
+  }
+  if (tensor) {
+    OuterArgs o;
+    std::memset(&o, 0, sizeof(o));
+    o.left[0] = x;
+    o.left[1] = d_y;
+    o.right[0] = v;
+    o.right[1] = u;
+    o.out[0] = d_a;
+    o.out[1] = d_b;
+    o.range = t.range;
+    o.order = t.order;
+    o.padrow = t.padrow;
+    o.hdr = t.hdr;
+    o.cols[0] = K;
+    o.cols[1] = N;
+    o.T = T;
+    o.right_rows = p.rows_u;
+    o.A = static_cast<int32_t>(A);
+    o.R = static_cast<int32_t>(R);
+    o.hold_release = env.hold_release;
+    o.wait_limit_ns = env.wait_limit_ns;
+    return status_of(launch_rows_outer(dtype, o, env.num_sms, s));
   }
   rc = run_dw_tables(x, v, t.off, t.padrow, t.hdr, p.rows_u, R, K, A, T, dtype, d_a, s);
   if (rc != PGG_OK) return rc;

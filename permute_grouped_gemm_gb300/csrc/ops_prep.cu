@@ -13,7 +13,8 @@
 // tokens one cluster of eight blocks does it, an eighth of the tokens each, with
 // the counts exchanged through distributed shared memory (one block alone took
 // 13 us for 8192 tokens: the matches inside 32 keys are what it waits for);
-// beyond that counting, prefix sums, placement and the lists are four launches.
+// beyond that counting, prefix sums, the lists, placement and the search for
+// neighbouring rows are five launches.
 //
 // All of it is integer work on a few bytes per row: latency is what it costs,
 // so what counts is the number of launches.
@@ -164,60 +165,82 @@ __device__ __forceinline__ int adapter_key(int64_t id, int A) {
 }
 
 // Block-wide, blockDim.x > A (one thread per adapter and one for the group without): the lists
-// from the groups' sizes, into memory if `write`, and s_start, s_ustart in any case. Thread g
-// holds group g's count and first compact row.
+// from the groups' sizes, into memory if `write`, and s_start, s_ustart (by id) in any case.
+// Thread g holds group g's count and first token; s_work is 3 x [A + 1].
 __device__ void build_adapter_lists(const AdapterPrepArgs& a, bool write, uint32_t count,
-                                    uint32_t start, uint32_t* s_scan, uint32_t* s_start, uint32_t* s_ustart,
-                                    uint32_t* s_seg_end) {
-  const int g = threadIdx.x;
-  const bool group = g <= a.A;
-  if (!group) count = 0;
-  const uint32_t room = a.padded ? (count + 63u) / 64u * 64u : count;
-  uint32_t total, n_seg, n_rb;
-  const uint32_t ustart = block_scan_u32(room, s_scan, &total);
-  const bool live = g < a.A && count > 0;
-  const uint32_t seg = block_scan_u32(live ? 1u : 0u, s_scan, &n_seg);
-  const uint32_t nb = group ? (count + a.rb - 1) / a.rb : 0u;
-  const uint32_t rb0 = block_scan_u32(nb, s_scan, &n_rb);
-  if (group) {
-    s_start[g] = start;
-    s_ustart[g] = ustart;
-  }
-  if (!write) return;
-  if (group) {
-    a.t.off[g] = ustart;
-    for (uint32_t j = 0; j < nb; ++j) {
-      const uint32_t left = count - j * a.rb;
-      a.t.rblist[rb0 + j] = make_int4(
-          g, static_cast<int>(start + j * a.rb),
-          static_cast<int>(left < static_cast<uint32_t>(a.rb) ? left : a.rb),
-          static_cast<int>(ustart + j * a.rb));
+                                    uint32_t first, uint32_t* s_scan, uint32_t* s_start,
+                                    uint32_t* s_ustart, uint32_t* s_work) {
+  const int G = a.A + 1, g = threadIdx.x;
+  const bool group = g < G;
+  uint32_t *s_first = s_work, *s_by = s_work + G, *s_end = s_work + 2 * G;
+  // place of the group among the groups: its id, or how many have an earlier first token (empty
+  // groups last, by id)
+  int place = g;
+  if (a.by_first) {
+    if (group) s_first[g] = count > 0 ? first : 0x80000000u + static_cast<uint32_t>(g);
+    __syncthreads();
+    if (group) {
+      const uint32_t mine = s_first[g];
+      place = 0;
+      for (int i = 0; i < G; ++i) place += s_first[i] < mine ? 1 : 0;
     }
   }
-  if (live) {
-    a.t.segs[seg] = make_int4(g, static_cast<int>(start), static_cast<int>(start + count),
-                              static_cast<int>(ustart));
-    s_seg_end[seg] = start + count;
-  }
-  if (g == 0) a.t.hdr->n_row_blocks = n_rb;
+  if (group) s_by[place] = static_cast<uint32_t>(g) | (count > 0 ? 0x80000000u : 0u);
+  if (group) s_start[place] = count;  // (by place for now)
   __syncthreads();
-  // segments that rows [256 b, 256 b + 256) meet: they are in row order and leave no gaps
+  // from here on thread i stands for the group in place i
+  const uint32_t id = group ? s_by[g] & 0x7FFFFFFFu : 0u;
+  const uint32_t n = group ? s_start[g] : 0u;
+  uint32_t total, n_seg, n_rb;
+  const uint32_t start = block_scan_u32(n, s_scan, &total);
+  const uint32_t ustart =
+      block_scan_u32(a.padded ? (n + 63u) / 64u * 64u : n, s_scan, &total);
+  const bool live = group && n > 0 && static_cast<int>(id) < a.A;
+  const uint32_t seg = block_scan_u32(live ? 1u : 0u, s_scan, &n_seg);
+  const uint32_t nb = (n + a.rb - 1) / a.rb;
+  const uint32_t rb0 = block_scan_u32(nb, s_scan, &n_rb);
+  if (group) {
+    s_start[id] = start;
+    s_ustart[id] = ustart;
+  }
+  if (write) {
+    if (group) {
+      a.t.off[id] = ustart;
+      a.t.range[id] = make_int4(static_cast<int>(start), static_cast<int>(n),
+                                static_cast<int>(ustart), 0);
+      for (uint32_t j = 0; j < nb; ++j) {
+        const uint32_t left = n - j * a.rb;
+        a.t.rblist[rb0 + j] = make_int4(
+            static_cast<int>(id), static_cast<int>(start + j * a.rb),
+            static_cast<int>(left < static_cast<uint32_t>(a.rb) ? left : a.rb),
+            static_cast<int>(ustart + j * a.rb));
+      }
+    }
+    if (live) {
+      a.t.segs[seg] = make_int4(static_cast<int>(id), static_cast<int>(start),
+                                static_cast<int>(start + n), static_cast<int>(ustart));
+      s_end[seg] = start + n;
+      s_first[seg] = start;
+    }
+    if (g == 0) a.t.hdr->n_row_blocks = n_rb;
+  }
+  __syncthreads();
+  if (!write) return;
+  // segments that rows [256 b, 256 b + 256) meet: they are in row order
   for (int64_t b = threadIdx.x; b < (a.T + 255) / 256; b += blockDim.x) {
     const uint32_t r0 = static_cast<uint32_t>(256 * b);
     const uint32_t r1 = static_cast<uint32_t>(256 * b + 256 < a.T ? 256 * b + 256 : a.T);
     uint32_t lo = 0, hi = n_seg;  // first segment that ends past r0
     while (lo < hi) {
       const uint32_t mid = (lo + hi) >> 1;
-      if (s_seg_end[mid] > r0) hi = mid; else lo = mid + 1;
+      if (s_end[mid] > r0) hi = mid; else lo = mid + 1;
     }
-    uint32_t e = lo;
-    uint32_t top = n_seg;  // first segment that ends at r1 or past it
+    uint32_t e = lo, top = n_seg;  // first segment from there that starts at r1 or past it
     while (e < top) {
       const uint32_t mid = (e + top) >> 1;
-      if (s_seg_end[mid] >= r1) top = mid; else e = mid + 1;
+      if (s_first[mid] >= r1) top = mid; else e = mid + 1;
     }
-    const uint32_t end = e < n_seg ? e + 1 : n_seg;
-    a.t.blkseg[b] = make_int2(static_cast<int>(lo), static_cast<int>(end > lo ? end - lo : 0));
+    a.t.blkseg[b] = make_int2(static_cast<int>(lo), static_cast<int>(e - lo));
   }
 }
 
@@ -237,8 +260,26 @@ __device__ __forceinline__ void put_token(const AdapterPrepArgs& a, int64_t toke
     for (uint32_t j = count; j < (count + 63u) / 64u * 64u; ++j) a.t.padrow[ustart + j] = r;
 }
 
+// Warps w, w + warps, ...: whether each 128 compact rows are neighbours in token order.
+__device__ __forceinline__ void find_boxes(const AdapterPrepArgs& a, int64_t w, int64_t warps) {
+  const int lane = threadIdx.x & 31;
+  for (int64_t b = w; b < 2 * ((a.T + 255) / 256); b += warps) {
+    const int64_t r0 = 128 * b;
+    const int32_t t0 = r0 < a.T ? a.t.order[r0].token : -1;
+    bool same = r0 < a.T;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int64_t r = r0 + lane + 32 * i;
+      if (r < a.T) same = same && a.t.order[r].token - t0 == r - r0;
+    }
+    same = __all_sync(0xFFFFFFFFu, same);
+    if (lane == 0) a.t.box[b] = same ? t0 : -1;
+  }
+}
+
 __global__ void __launch_bounds__(1024) adapter_prep_small_kernel(const AdapterPrepArgs a) {
-  // [warps][A + 1] counters, [kCluster][A + 1] counts of every block, 4 x [A + 1], the block's keys
+  // [warps][A + 1] counters, [kCluster][A + 1] counts of every block and their first tokens,
+  // 6 x [A + 1], the block's keys
   extern __shared__ uint32_t s_cnt[];
   __shared__ uint32_t s_scan[33];
   __shared__ int s_bad[kCluster];
@@ -246,9 +287,10 @@ __global__ void __launch_bounds__(1024) adapter_prep_small_kernel(const AdapterP
   const int G = a.A + 1, warps = blockDim.x >> 5;
   const int C = static_cast<int>(gridDim.x), rank = static_cast<int>(blockIdx.x);  // one cluster
   uint32_t* s_all = s_cnt + warps * G;
-  uint32_t* s_start = s_all + kCluster * G;
-  uint32_t *s_ustart = s_start + G, *s_seg = s_ustart + G, *s_count = s_seg + G;
-  uint16_t* s_key = reinterpret_cast<uint16_t*>(s_count + G);
+  uint32_t* s_allf = s_all + kCluster * G;
+  uint32_t* s_start = s_all + (a.by_first ? 2 : 1) * kCluster * G;  // (no s_allf otherwise)
+  uint32_t *s_ustart = s_start + G, *s_count = s_ustart + G, *s_work = s_count + G;
+  uint16_t* s_key = reinterpret_cast<uint16_t*>(s_work + 3 * G);
   const int64_t t0 = static_cast<int64_t>(rank) * a.tokens_per_block;
   const int64_t left = a.T - t0;
   const int n = left < 0 ? 0
@@ -261,7 +303,11 @@ __global__ void __launch_bounds__(1024) adapter_prep_small_kernel(const AdapterP
     bad = bad || id < -1 || id >= a.A;
     s_key[e] = static_cast<uint16_t>(adapter_key(id, a.A));
   }
+  for (int i = threadIdx.x; i < G; i += blockDim.x) s_work[i] = 0xFFFFFFFFu;
   bad = __syncthreads_or(bad);
+  for (int e = threadIdx.x; a.by_first && e < n; e += blockDim.x)
+    if (e == 0 || s_key[e] != s_key[e - 1])  // (starts of runs are enough)
+      atomicMin(&s_work[s_key[e]], static_cast<uint32_t>(t0 + e));
   const int run = ((n + warps - 1) / warps + 31) / 32 * 32;
   auto key = [&](int e) { return static_cast<int>(s_key[e]); };
   sort_count(s_cnt, G, n, run, key);
@@ -270,27 +316,32 @@ __global__ void __launch_bounds__(1024) adapter_prep_small_kernel(const AdapterP
   if (g < G) {
     uint32_t c = 0;
     for (int w = 0; w < warps; ++w) c += s_cnt[w * G + g];
-    for (int d = 0; d < C; ++d) st_cluster_u32(ptx::mapa(&s_all[rank * G + g], d), c);
+    for (int d = 0; d < C; ++d) {
+      st_cluster_u32(ptx::mapa(&s_all[rank * G + g], d), c);
+      if (a.by_first) st_cluster_u32(ptx::mapa(&s_allf[rank * G + g], d), s_work[g]);
+    }
   }
   if (g == 0) st_cluster_u32(ptx::mapa(&s_bad[rank], 0), bad ? 1u : 0u);
   ptx::cluster_sync();
-  uint32_t c = 0, mine = 0, total;
+  uint32_t c = 0, mine = 0, first = 0xFFFFFFFFu;
   if (g < G) {
     for (int d = 0; d < C; ++d) {
       if (d == rank) mine = c;
       c += s_all[d * G + g];
+      if (a.by_first && s_allf[d * G + g] < first) first = s_allf[d * G + g];
     }
     s_count[g] = c;
   }
-  const uint32_t start = block_scan_u32(c, s_scan, &total);
-  build_adapter_lists(a, rank == 0, c, start, s_scan, s_start, s_ustart, s_seg);
+  build_adapter_lists(a, rank == 0, c, first, s_scan, s_start, s_ustart, s_work);
   __syncthreads();
   sort_place(
-      s_cnt, G, n, run, key, [&](int) { return start + mine; },
+      s_cnt, G, n, run, key, [&](int k) { return s_start[k] + mine; },
       [&](int e, uint32_t where) {
         const int k = key(e);
         put_token(a, t0 + e, k, where, s_start[k], s_ustart[k], s_count[k]);
       });
+  ptx::cluster_sync();  // every block's part of the order is there
+  find_boxes(a, rank * warps + (threadIdx.x >> 5), static_cast<int64_t>(C) * warps);
   if (rank == 0 && threadIdx.x == 0) {
     int any = 0;
     for (int d = 0; d < C; ++d) any |= s_bad[d];
@@ -321,22 +372,13 @@ __global__ void __launch_bounds__(kSortThreads) adapter_count_kernel(const Adapt
 
 // Third launch (one block), after the prefix sums: the lists. The totals arrive in off.
 __global__ void __launch_bounds__(1024) adapter_lists_kernel(const AdapterPrepArgs a) {
-  extern __shared__ uint32_t s_lists[];  // 3 x [A + 1]
+  extern __shared__ uint32_t s_lists[];  // 5 x [A + 1]
   __shared__ uint32_t s_scan[33];
   ptx::griddep_wait();
   const int G = a.A + 1, g = threadIdx.x;
   const uint32_t c = g < G ? static_cast<uint32_t>(a.t.off[g]) : 0u;
-  uint32_t total;
-  const uint32_t start = block_scan_u32(c, s_scan, &total);
-  build_adapter_lists(a, true, c, start, s_scan, s_lists, s_lists + G, s_lists + 2 * G);
-  // [blocks of this group's prefix sums become first rows]
-  __syncthreads();
-  if (g < G) {
-    // starts and counts for the placement, after the counts: counts [G][blocks], then 2 x [G]
-    uint32_t* tail = a.t.counts + static_cast<int64_t>(G) * a.blocks;
-    tail[g] = start;
-    tail[G + g] = c;
-  }
+  // (groups by id: the first tokens would be one more launch's work)
+  build_adapter_lists(a, true, c, 0, s_scan, s_lists, s_lists + G, s_lists + 2 * G);
   if (g == 0) {
     a.t.hdr->status = 0;
     a.t.hdr->sched_next = 0;
@@ -355,7 +397,6 @@ __global__ void __launch_bounds__(kSortThreads) adapter_place_kernel(const Adapt
   const int n = left < a.tokens_per_block ? static_cast<int>(left) : a.tokens_per_block;
   constexpr int kW = kSortThreads / 32;
   const int run = ((n + kW - 1) / kW + 31) / 32 * 32;
-  const uint32_t* tail = a.t.counts + static_cast<int64_t>(G) * a.blocks;
   auto key = [&](int e) { return adapter_key(a.adapter[t0 + e], a.A); };
   for (int e = threadIdx.x; e < n; e += blockDim.x) {
     const int64_t id = a.adapter[t0 + e];
@@ -365,12 +406,21 @@ __global__ void __launch_bounds__(kSortThreads) adapter_place_kernel(const Adapt
   sort_place(
       s_cnt, G, n, run, key,
       [&](int g) {
-        return tail[g] + a.t.counts[static_cast<int64_t>(g) * a.blocks + blockIdx.x];
+        return static_cast<uint32_t>(a.t.range[g].x) +
+               a.t.counts[static_cast<int64_t>(g) * a.blocks + blockIdx.x];
       },
       [&](int e, uint32_t where) {
         const int k = key(e);
-        put_token(a, t0 + e, k, where, tail[k], static_cast<uint32_t>(a.t.off[k]), tail[G + k]);
+        const int4 r = a.t.range[k];
+        put_token(a, t0 + e, k, where, r.x, r.z, r.y);
       });
+}
+
+// Fifth launch.
+__global__ void __launch_bounds__(kSortThreads) adapter_boxes_kernel(const AdapterPrepArgs a) {
+  ptx::griddep_wait();
+  const int64_t per = kSortThreads / 32;
+  find_boxes(a, blockIdx.x * per + (threadIdx.x >> 5), gridDim.x * per);
 }
 
 }  // namespace
@@ -409,8 +459,11 @@ cudaError_t launch_adapter_prep(const AdapterPrepArgs& a, cudaStream_t stream) {
     int threads = a.tokens_per_block > G ? a.tokens_per_block : G;
     if (threads > 512) threads = G > 512 ? G : 512;
     threads = (threads + 31) / 32 * 32;
-    const size_t smem = static_cast<size_t>(threads / 32 + kCluster + 4) * G * 4 +
-                        static_cast<size_t>(a.tokens_per_block) * 2;
+    AdapterPrepArgs q = a;
+    if (G > 512) q.by_first = 0;  // (their tables would not fit beside the counters)
+    const size_t smem =
+        static_cast<size_t>(threads / 32 + (q.by_first ? 2 : 1) * kCluster + 6) * G * 4 +
+        static_cast<size_t>(a.tokens_per_block) * 2;
     if (smem > 32 * 1024) {
       cudaError_t err = cudaFuncSetAttribute(
           adapter_prep_small_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -418,18 +471,22 @@ cudaError_t launch_adapter_prep(const AdapterPrepArgs& a, cudaStream_t stream) {
       if (err != cudaSuccess) return err;
     }
     return launch_pdl(adapter_prep_small_kernel, dim3(a.blocks), dim3(threads), smem, stream,
-                      static_cast<unsigned>(a.blocks), a);
+                      static_cast<unsigned>(a.blocks), q);
   }
   cudaError_t err = launch_pdl(adapter_count_kernel, dim3(a.blocks), dim3(kSortThreads),
                                static_cast<size_t>(G) * 4, stream, 1, a);
   if (err != cudaSuccess) return err;
   err = launch_count_scan(a.t.counts, G, a.blocks, a.t.off, stream);
   if (err != cudaSuccess) return err;
-  err = launch_pdl(adapter_lists_kernel, dim3(1), dim3(1024), static_cast<size_t>(3) * G * 4,
-                   stream, 1, a);
+  AdapterPrepArgs by_id = a;
+  by_id.by_first = 0;
+  err = launch_pdl(adapter_lists_kernel, dim3(1), dim3(1024), static_cast<size_t>(5) * G * 4,
+                   stream, 1, by_id);
   if (err != cudaSuccess) return err;
-  return launch_pdl(adapter_place_kernel, dim3(a.blocks), dim3(kSortThreads),
-                    static_cast<size_t>(kSortThreads / 32) * G * 4, stream, 1, a);
+  err = launch_pdl(adapter_place_kernel, dim3(a.blocks), dim3(kSortThreads),
+                   static_cast<size_t>(kSortThreads / 32) * G * 4, stream, 1, a);
+  if (err != cudaSuccess) return err;
+  return launch_pdl(adapter_boxes_kernel, dim3(152), dim3(kSortThreads), 0, stream, 1, a);
 }
 
 }  // namespace pgg

@@ -752,6 +752,20 @@ bool encode_map_3d(CUtensorMap* m, int dtype, const void* base, int64_t d0, int6
          CUDA_SUCCESS;
 }
 
+bool encode_map_rows(CUtensorMap* m, int dtype, const void* base, int64_t d0, int64_t d1,
+                     int box1) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return false;
+  cuuint64_t dims[2] = {static_cast<cuuint64_t>(d0), static_cast<cuuint64_t>(d1)};
+  cuuint64_t strides[1] = {static_cast<cuuint64_t>(d0) * 2};
+  cuuint32_t box[2] = {64, static_cast<cuuint32_t>(box1)};
+  cuuint32_t estr[2] = {1, 1};
+  return enc(m, tmap_type(dtype), 2, const_cast<void*>(base), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+         CUDA_SUCCESS;
+}
+
 // run_dw reads sizes and three table offsets of its plan; the tables here lie anywhere.
 int run_dw_tables(const void* x, const void* dy, const int64_t* off, const RowInfo* rowinfo,
                   WsHeader* hdr, int64_t rows, int64_t N, int64_t K, int64_t G, int64_t batch,

@@ -21,6 +21,9 @@ int forced_variant();        // test hook, -1 = automatic
 // elements and the 128-byte swizzle; reads outside it give zeros. False when it cannot be encoded.
 bool encode_map_3d(CUtensorMap* m, int dtype, const void* base, int64_t d0, int64_t d1, int64_t d2,
                    int box1);
+// The same of a row-major 16-bit [d1][d0] array with boxes of 64 x box1 elements.
+bool encode_map_rows(CUtensorMap* m, int dtype, const void* base, int64_t d0, int64_t d1,
+                     int box1);
 // The weight-gradient kernels on tables already in memory: out[g] = sum over rows i in
 // [off[g], off[g + 1]) of x[token(i)]^T dy[i], g < G. dy has `rows` rows.
 int run_dw_tables(const void* x, const void* dy, const int64_t* off, const RowInfo* rowinfo,
@@ -88,18 +91,24 @@ cudaError_t launch_rows_prep(const RowsPrepArgs& a, int num_sms, cudaStream_t st
 
 // ------------------------------------------------------------ tables of the adapters
 
-// Tokens are put in order of their adapter (stable; tokens without one last, as group A). That
-// compact order of T rows is what the projection walks. The low-rank factors u and v are stored in
-// a second order, in which (padded = 1) every adapter starts at a multiple of 64 rows and is
-// filled up with zero rows: the weight-gradient kernel reads 64 rows at a time, and what it reads
-// past an adapter's rows must not be another adapter's.
+// Tokens are put in order of their adapter (stable; tokens without one are group A). The groups
+// stand in the order of their first token (by_first), so that a batch of requests one after
+// another stays as it is and its rows can be copied in boxes; or in the order of their ids (the
+// weight-gradient kernels that take off[] need that). That compact order of T rows is what the
+// projection walks. The low-rank factors u and v are stored in a second order, in which
+// (padded = 1) every group starts at a multiple of 64 rows and is filled up with zero rows: the
+// reduction over an adapter's rows reads 64 at a time, and what it reads past them must not be
+// another adapter's.
 struct AdapterTables {
   WsHeader* hdr;
-  int64_t* off;       // [A + 1] first row of each adapter in the order of u and v
+  int64_t* off;       // [A + 1] first row of each group in the order of u and v, groups by id
+  int4* range;        // [A + 1] {first compact row, rows, first row of u, 0} by id
   RowInfo* order;     // [T] compact order: {token, adapter}
   RowInfo* padrow;    // [P] order of u and v: {token, 0}; a filled-up row repeats a token
   int4* rblist;       // {adapter, first compact row, rows, first row of u}: at most rb rows each
   int4* segs;         // {adapter, first compact row, end, first row of u} of each live adapter
+  int32_t* box;       // [2 ceil(T / 256)] first token of each 128 compact rows if they are neighbours
+                      // in token order, else -1
   int2* blkseg;       // [ceil(T / 256)] {first segment, segments} of each 256 compact rows
   uint32_t* counts;   // [A + 1][blocks], for many tokens
 };
@@ -110,7 +119,7 @@ struct AdapterPrepArgs {
   int64_t T;
   int32_t A;
   int32_t rb;      // rows per entry of rblist, a multiple of 64 when padded
-  int32_t padded;
+  int32_t padded, by_first;
   int32_t blocks, tokens_per_block;  // of the counting and placement launches
 };
 void adapter_blocks(int64_t T, int* blocks, int* tokens_per_block);
@@ -136,6 +145,7 @@ struct RowsArgs {
   const RowInfo* rowinfo;  // kGated {token, position}; else {token, adapter}
   const int4* segs;        // kAdapt*
   const int2* blkseg;      // kAdapt*
+  const int32_t* box;      // kAdapt*
   WsHeader* hdr;
   void* out;               // h [M, N], u [*, N], y [T, N] (rows in token order)
   void* gate_up;           // kGated: [M, 2 N] or null
@@ -165,6 +175,26 @@ cudaError_t launch_rows_skinny(int dtype, RowsMode mode, int NR, RowsArgs a, int
 
 // Few tokens: u [T, R] fp32 in token order (R and K multiples of 8), and the ids' check.
 cudaError_t launch_few_shrink(int dtype, const RowsArgs& a, cudaStream_t stream);
+
+// Both factors' gradients, for tables in the padded order (16-bit, widths multiples of 8, 16-byte
+// aligned): out[w] [A, cols[w], R] = sum over an adapter's rows of left[w]^T right[w].
+struct OuterArgs {
+  const void* left[2];   // x [T, cols[0]], d_y [T, cols[1]]: rows by token
+  const void* right[2];  // v, u [right_rows, R]: rows in the padded order
+  void* out[2];
+  const int4* range;     // [A + 1]
+  const RowInfo* order;
+  const RowInfo* padrow;
+  WsHeader* hdr;
+  int64_t cols[2];
+  int64_t T, right_rows;
+  int32_t A, R;
+  int32_t blocks0, blocks1;  // 128-column blocks of each (set by the launch)
+  uint32_t r_blocks;
+  int32_t hold_release;
+  uint64_t wait_limit_ns;
+};
+cudaError_t launch_rows_outer(int dtype, OuterArgs a, int num_sms, cudaStream_t stream);
 
 // ------------------------------------------------------------ gradient of the gate
 

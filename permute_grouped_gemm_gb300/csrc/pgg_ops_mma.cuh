@@ -34,6 +34,14 @@ __device__ __forceinline__ void zero_rows16(const RowsArgs& a) {
   }
 }
 
+// First token of `rows` compact rows of one adapter from row0 if they are neighbouring tokens, else
+// -1. (An adapter's rows are in token order, so the ends tell.)
+__device__ __forceinline__ int32_t box_of_rows(const RowInfo* order, int64_t row0, int rows) {
+  if (rows <= 0) return -1;
+  const int32_t t0 = order[row0].token;
+  return order[row0 + rows - 1].token - t0 == rows - 1 ? t0 : -1;
+}
+
 // Two 16-bit values of a 32-bit word <-> fp32 (round to nearest even).
 template <int DT>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {

@@ -14,7 +14,8 @@
 // workspace, bitwise repeatable. S = 1 when the tiles alone fill the GPU.
 //
 // A stage is 64 of k: two 64-column panels of the weight by TMA (16 KB) and NR
-// x rows gathered by token with cp.async. With NR = 16 twelve stages are in
+// x rows, gathered by token with cp.async or, where they are neighbours, as one
+// TMA box. With NR = 16 twelve stages are in
 // flight per SM, 192 KB of weight, which is what keeps HBM busy.
 //
 // adapt with few tokens: rows stay in the caller's order, and the low-rank part
@@ -120,6 +121,14 @@ struct Walk {
   int ks0, ks1;
 };
 
+// First token of the tile's rows if they are neighbours (they come as one TMA box then), else -1.
+template <int MODE>
+__device__ __forceinline__ int32_t box_of(const RowsArgs& a, const Tile& x) {
+  if (MODE == kAdapt) return static_cast<int32_t>(x.row0);
+  if (MODE == kShrink) return box_of_rows(a.rowinfo, x.row0, x.rows);
+  return -1;
+}
+
 // Rows of tokens without an adapter have nothing to shrink.
 template <int MODE>
 __device__ __forceinline__ bool skipped(const RowsArgs& a, const Tile& x) {
@@ -128,7 +137,8 @@ __device__ __forceinline__ bool skipped(const RowsArgs& a, const Tile& x) {
 
 template <int MODE, int NR, int PANELS>
 __device__ void w_producer(uint8_t* smem, Ctl<Cfg<NR, PANELS>::kStages>* ctl,
-                           const CUtensorMap* tm_w, const RowsArgs& a, const Walk& k) {
+                           const CUtensorMap* tm_w, const CUtensorMap* tm_x, const RowsArgs& a,
+                           const Walk& k) {
   using C = Cfg<NR, PANELS>;
   const uint64_t lim = a.wait_limit_ns;
   volatile int* abort = &ctl->abort;
@@ -144,7 +154,9 @@ __device__ void w_producer(uint8_t* smem, Ctl<Cfg<NR, PANELS>::kStages>* ctl,
       col[j] = static_cast<int32_t>(MODE == kGated ? x.n0 + (j ? a.N : 0) : x.n0 + 64 * j);
       on[j] = j < PANELS && (MODE == kGated || x.n0 + 64 * j < a.N);
     }
-    const uint32_t bytes = (on[0] ? kPanel : 0) + (on[1] ? kPanel : 0);
+    const int32_t box = box_of<MODE>(a, x);
+    const uint32_t bytes =
+        (on[0] ? kPanel : 0) + (on[1] ? kPanel : 0) + (box >= 0 ? C::kBBytes : 0);
     for (int ks = k.ks0; ks < k.ks1; ++ks) {
       if (!ptx::mbar_wait(&ctl->empty[stage], phase ^ 1u, lim, abort)) {
         failed = true;
@@ -152,6 +164,7 @@ __device__ void w_producer(uint8_t* smem, Ctl<Cfg<NR, PANELS>::kStages>* ctl,
       }
       uint8_t* sa = smem + stage * C::kStageBytes;
       ptx::mbar_arrive_expect_tx(&ctl->full[stage], bytes);
+      if (box >= 0) ptx::tma_load_2d(sa + C::kABytes, tm_x, &ctl->full[stage], ks * kFK, box);
       for (int j = 0; j < PANELS; ++j)
         if (on[j])
           ptx::tma_load_3d(sa + j * kPanel, tm_w, &ctl->full[stage], col[j], ks * kFK,
@@ -194,19 +207,17 @@ __device__ void x_gatherer(uint8_t* smem, Ctl<Cfg<NR, PANELS>::kStages>* ctl, co
   for (uint32_t t = k.first; t < k.total && !failed; t += k.step) {
     const Tile x = tile_of<MODE, NR>(t, a);
     if (skipped<MODE>(a, x)) continue;
-    if (kb < steps) {
+    const int32_t box = box_of<MODE>(a, x);
+    if (kb < steps && box < 0) {
 #pragma unroll
       for (int q = 0; q < NR / 4; ++q) {
         const int rr = (lane >> 3) + 4 * q;
         row16[q] = kNoRow;
         if (rr < x.rows) {
-          const int64_t row = x.row0 + rr;
-          const int64_t tok =
-              MODE == kAdapt
-                  ? row
-                  : check_index(a.hdr, a.rowinfo[check_index(a.hdr, row, a.M, 92)].token, a.batch,
-                                93);
-          row16[q] = static_cast<uint32_t>(tok) * row_units;
+          const int64_t row = check_index(a.hdr, x.row0 + rr, a.M, 92);
+          row16[q] = static_cast<uint32_t>(
+                         check_index(a.hdr, a.rowinfo[row].token, a.batch, 93)) *
+                     row_units;
         }
       }
     }
@@ -215,21 +226,24 @@ __device__ void x_gatherer(uint8_t* smem, Ctl<Cfg<NR, PANELS>::kStages>* ctl, co
         failed = true;
         break;
       }
-      const int64_t kk = static_cast<int64_t>(k.ks0 + kb) * kFK + c * 8;
-      const bool k_ok = kk < a.K;
-      const char* xk = xb + kk * 2;
+      if (box < 0) {
+        const int64_t kk = static_cast<int64_t>(k.ks0 + kb) * kFK + c * 8;
+        const bool k_ok = kk < a.K;
+        const char* xk = xb + kk * 2;
 #pragma unroll
-      for (int q = 0; q < NR / 4; ++q) {
-        const int rr = (lane >> 3) + 4 * q;
-        const bool ok = k_ok && row16[q] != kNoRow;
-        const void* src = ok ? static_cast<const void*>(xk + (static_cast<uint64_t>(row16[q]) << 4))
-                             : static_cast<const void*>(xb);
-        ptx::cp_async_16(sb + rr * 128 + ((c ^ (rr & 7)) << 4), src, ok ? 16u : 0u);
+        for (int q = 0; q < NR / 4; ++q) {
+          const int rr = (lane >> 3) + 4 * q;
+          const bool ok = k_ok && row16[q] != kNoRow;
+          const void* src = ok ? static_cast<const void*>(
+                                     xk + (static_cast<uint64_t>(row16[q]) << 4))
+                               : static_cast<const void*>(xb);
+          ptx::cp_async_16(sb + rr * 128 + ((c ^ (rr & 7)) << 4), src, ok ? 16u : 0u);
+        }
+        ptx::cp_async_commit();
+        ptx::cp_async_wait<0>();
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
       }
-      ptx::cp_async_commit();
-      ptx::cp_async_wait<0>();
-      ptx::fence_proxy_async_smem();
-      __syncwarp();
       if (lane == 0) ptx::mbar_arrive(&ctl->full[w]);
       phase ^= 1u;
     }
@@ -309,7 +323,7 @@ __device__ __forceinline__ void store16(void* out, int64_t i, float v) {
 template <int DT, int MODE, int LR>
 __device__ __forceinline__ void write_rows(const float* red, int slot, uint32_t S, const RowsArgs& a,
                                            const Tile& x, int j0, int n, bool failed,
-                                           const float (&lr)[LR][4]) {
+                                           const float (&lr)[LR][4], float row_scale) {
   const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 3;
 #pragma unroll 1
   for (int j = warp; j < n; j += kEpiWarps) {
@@ -326,9 +340,8 @@ __device__ __forceinline__ void write_rows(const float* red, int slot, uint32_t 
         u.y += pu.y;
       }
       const int64_t f = x.n0 + 2 * lane;
+      const float p = __shfl_sync(0xFFFFFFFFu, row_scale, (j - warp) / kEpiWarps);
       if (f >= a.N) continue;  // (N is even)
-      const float p =
-          a.probs ? a.probs[check_index(a.hdr, a.rowinfo[row].rank, a.M, 94)] : 1.0f;
       *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + row * a.N + f) =
           pack2<DT>(gate(g.x, u.x, p), gate(g.y, u.y, p));
       if (a.gate_up) {
@@ -345,12 +358,11 @@ __device__ __forceinline__ void write_rows(const float* red, int slot, uint32_t 
         for (uint32_t s = 0; s < S; ++s) v[i] += r[s * slot + lane + 32 * i];
       }
       if constexpr (MODE == kShrink) {
-        const float sc = a.scale ? a.scale[x.g] : 1.0f;
         const int64_t orow = static_cast<int64_t>(x.urow) + j0 + j;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int64_t c = x.n0 + lane + 32 * i;
-          if (c < a.N) store16<DT>(a.out, orow * a.N + c, v[i] * sc);
+          if (c < a.N) store16<DT>(a.out, orow * a.N + c, v[i] * row_scale);
         }
       } else {
         // (a loop over constants: lr stays in registers)
@@ -376,14 +388,17 @@ template <int DT, int LR>
 __device__ __forceinline__ void low_rank(const RowsArgs& a, const Tile& x, int j0, int n,
                                          float (&lr)[LR][4]) {
   const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 3;
+  // lane i loads the adapter of this warp's i-th row
+  int ids = -1;
+  if (lane < LR && warp + kEpiWarps * lane < n)
+    ids = static_cast<int>(a.adapter[x.row0 + j0 + warp + kEpiWarps * lane]);
 #pragma unroll
   for (int q = 0; q < LR; ++q) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) lr[q][i] = 0.0f;
     const int j = warp + kEpiWarps * q;
-    if (j >= n) continue;
     const int64_t row = x.row0 + j0 + j;
-    const int64_t ad = a.adapter[row];
+    const int64_t ad = __shfl_sync(0xFFFFFFFFu, ids, q);
     if (ad < 0 || ad >= a.G) continue;
     const float* u = static_cast<const float*>(a.u) + row * a.R;
     const char* b = static_cast<const char*>(a.b) + ((ad * a.N + x.n0) * a.R) * 2;
@@ -423,7 +438,8 @@ __device__ void epilogue(Ctl<Cfg<NR, PANELS>::kStages>* ctl, float* red, uint32_
   volatile int* abort = &ctl->abort;
   const int lane = threadIdx.x & 31;
   const int quarter = (threadIdx.x >> 5) & 3;
-  const int per = NR / static_cast<int>(S);  // rows that each CTA of the cluster finishes
+  const int shift = 31 - __clz(NR / static_cast<int>(S));
+  const int per = 1 << shift;  // rows that each CTA of the cluster finishes
   const int slot = per * kM;
   int acc = 0;
   uint32_t aph = 0, rph = 0;
@@ -441,6 +457,16 @@ __device__ void epilogue(Ctl<Cfg<NR, PANELS>::kStages>* ctl, float* red, uint32_
     }
     const int j0 = static_cast<int>(rank) * per;  // this CTA finishes rows j0 .. j0 + n - 1
     const int n = x.rows - j0 < per ? x.rows - j0 : per;
+    // what the rows are scaled by is loaded ahead: lane i holds the weight of this warp's i-th row
+    float row_scale = 1.0f;
+    if constexpr (MODE == kGated) {
+      const int j = quarter + kEpiWarps * lane;
+      if (a.probs && j < n)
+        row_scale = a.probs[check_index(
+            a.hdr, a.rowinfo[check_index(a.hdr, x.row0 + j0 + j, a.M, 94)].rank, a.M, 95)];
+    } else if constexpr (MODE == kShrink) {
+      if (a.scale) row_scale = a.scale[x.g];
+    }
     constexpr int kLR = MODE == kAdapt ? NR / kEpiWarps : 1;
     float lr[kLR][4];
     if constexpr (MODE == kAdapt) {
@@ -471,9 +497,9 @@ __device__ void epilogue(Ctl<Cfg<NR, PANELS>::kStages>* ctl, float* red, uint32_
       for (int i = 0; i < 16; ++i) {
         const int j = c0 + i;
         if (j >= x.rows) break;
-        const int dst = j / per;
+        const int dst = j >> shift;
         // slot `rank` of the CTA that finishes row j
-        float* where = red + rank * slot + (j - dst * per) * kM + mine;
+        float* where = red + rank * slot + (j & (per - 1)) * kM + mine;
         if (S == 1)
           *where = __uint_as_float(v[i]);
         else
@@ -493,7 +519,7 @@ __device__ void epilogue(Ctl<Cfg<NR, PANELS>::kStages>* ctl, float* red, uint32_
       }
       break;
     }
-    write_rows<DT, MODE, kLR>(red, slot, S, a, x, j0, n, failed_input, lr);
+    write_rows<DT, MODE, kLR>(red, slot, S, a, x, j0, n, failed_input, lr, row_scale);
     if constexpr (MODE == kShrink) {
       if (a.padded) {  // rows that fill the adapter up to a multiple of 64
         const int end = (x.rows + 63) / 64 * 64;
@@ -513,7 +539,8 @@ __device__ void epilogue(Ctl<Cfg<NR, PANELS>::kStages>* ctl, float* red, uint32_
 
 template <int DT, int MODE, int NR, int PANELS>
 __global__ void __launch_bounds__(Cfg<NR, PANELS>::kThreads, 1)
-    rows_skinny_kernel(const __grid_constant__ CUtensorMap tm_w, const RowsArgs a) {
+    rows_skinny_kernel(const __grid_constant__ CUtensorMap tm_w,
+                       const __grid_constant__ CUtensorMap tm_x, const RowsArgs a) {
   using C = Cfg<NR, PANELS>;
   if (MODE != kAdapt) ptx::griddep_wait();
   extern __shared__ uint8_t smem_raw[];
@@ -553,7 +580,10 @@ __global__ void __launch_bounds__(Cfg<NR, PANELS>::kThreads, 1)
     ctl->abort = 0;
     ptx::fence_mbar_init();
   }
-  if (warp == 0 && lane == 0) ptx::tma_prefetch_desc(&tm_w);
+  if (warp == 0 && lane == 0) {
+    ptx::tma_prefetch_desc(&tm_w);
+    if (MODE != kGated) ptx::tma_prefetch_desc(&tm_x);
+  }
   if (warp == 1) {
     ptx::tmem_alloc(&ctl->tmem_base, C::kTmemCols);
     ptx::tmem_relinquish();
@@ -565,7 +595,7 @@ __global__ void __launch_bounds__(Cfg<NR, PANELS>::kThreads, 1)
   const uint32_t tmem_base = ctl->tmem_base;
 
   if (warp == 0) {
-    if (lane == 0) w_producer<MODE, NR, PANELS>(smem, ctl, &tm_w, a, k);
+    if (lane == 0) w_producer<MODE, NR, PANELS>(smem, ctl, &tm_w, &tm_x, a, k);
   } else if (warp == 1) {
     if (lane == 0) mma_issuer<DT, MODE, NR, PANELS>(smem, ctl, tmem_base, a, k);
   } else if (warp < 2 + C::kStages) {
@@ -602,7 +632,7 @@ int choose_split(int64_t tiles, int nks, int NR, int num_sms) {
 }
 
 template <int DT, int MODE, int NR, int PANELS>
-cudaError_t launch_t(const CUtensorMap& tm_w, const RowsArgs& a, int64_t tiles, int num_sms,
+cudaError_t launch_t(const CUtensorMap (&tm)[2], const RowsArgs& a, int64_t tiles, int num_sms,
                      cudaStream_t stream) {
   using C = Cfg<NR, PANELS>;
   constexpr int smem = smem_bytes<NR, PANELS>();
@@ -620,11 +650,11 @@ cudaError_t launch_t(const CUtensorMap& tm_w, const RowsArgs& a, int64_t tiles, 
   if (most < want) want = most;
   if (clusters < want) want = clusters;
   return launch_pdl(kern, dim3(static_cast<unsigned>(S * want)), dim3(C::kThreads),
-                    static_cast<size_t>(smem), stream, static_cast<unsigned>(S), tm_w, a);
+                    static_cast<size_t>(smem), stream, static_cast<unsigned>(S), tm[0], tm[1], a);
 }
 
 template <int DT>
-cudaError_t launch_mode(RowsMode mode, int NR, const CUtensorMap& m, const RowsArgs& a,
+cudaError_t launch_mode(RowsMode mode, int NR, const CUtensorMap (&m)[2], const RowsArgs& a,
                         int64_t tiles, int sms, cudaStream_t st) {
   if (mode == kGated) {
     if (NR == 16) return launch_t<DT, kGated, 16, 2>(m, a, tiles, sms, st);
@@ -652,14 +682,17 @@ cudaError_t launch_rows_skinny(int dtype, RowsMode mode, int NR, RowsArgs a, int
                                int num_sms, cudaStream_t stream) {
   const int64_t tile_n = mode == kGated ? 64 : kM;
   a.n_blocks = static_cast<int32_t>((a.N + tile_n - 1) / tile_n);
-  CUtensorMap tm_w;
+  CUtensorMap tm[2];  // weight, x
+  std::memset(tm, 0, sizeof(tm));
   const int64_t cols = mode == kGated ? 2 * a.N : a.N;
-  if (!encode_map_3d(&tm_w, dtype, a.w, cols, a.K, mode == kAdapt ? 1 : a.G, kFK))
+  if (!encode_map_3d(&tm[0], dtype, a.w, cols, a.K, mode == kAdapt ? 1 : a.G, kFK))
+    return cudaErrorInvalidValue;
+  if (mode != kGated && !encode_map_rows(&tm[1], dtype, a.x, a.K, a.batch, NR))
     return cudaErrorInvalidValue;
   const int64_t tiles = live_blocks * a.n_blocks;
   if (dtype == PGG_BF16)
-    return launch_mode<PGG_BF16>(mode, NR, tm_w, a, tiles, num_sms, stream);
-  if (dtype == PGG_F16) return launch_mode<PGG_F16>(mode, NR, tm_w, a, tiles, num_sms, stream);
+    return launch_mode<PGG_BF16>(mode, NR, tm, a, tiles, num_sms, stream);
+  if (dtype == PGG_F16) return launch_mode<PGG_F16>(mode, NR, tm, a, tiles, num_sms, stream);
   return cudaErrorInvalidValue;
 }
 

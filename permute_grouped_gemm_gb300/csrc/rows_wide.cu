@@ -5,10 +5,14 @@
 //     adaptT   the same with W given as [N, K]                   (the gradient of x)
 //
 // Tile: 256 rows x 256 accumulator columns on a pair of CTAs (cta_group::2),
-// reduced 64 at a time through six or seven stage slots; CTA r owns rows
-// 128 r .. 128 r + 127, whose fp32 accumulators (two buffers) sit in its tensor
-// memory. The rows of x are gathered by token with 16-byte cp.async, one warp
-// per stage slot; the weights come by TMA.
+// reduced 64 at a time through seven stage slots; CTA r owns rows 128 r .. 128 r
+// + 127, whose fp32 accumulators (two buffers) sit in its tensor memory. The
+// weights come by TMA. The rows of x are gathered by token with 16-byte
+// cp.async, one warp per stage slot; where a CTA's rows are neighbouring tokens
+// (adapt: requests one after another) they come as one TMA box instead, which
+// does not share the gathers' limit (a multiprocessor keeps about 30 KB of
+// cp.async in flight whatever the slots: 0.39 us a step against 0.27). TMA's own
+// gather of four rows is no way out: 75 cycles an instruction, 1.2 us a step.
 //
 // gated: 128 of the accumulator's columns are gates and the other 128 the ups
 // that belong to them (each CTA loads one of the two operands), so a thread of
@@ -82,6 +86,7 @@ struct Tile {
   int rows;             // this CTA's rows of the block (0 .. 128)
   int steps;            // reduction steps, the low-rank ones included
   int seg0;             // adapt: first adapter segment of the tile
+  int32_t box[2];       // adapt: first token of each CTA's rows if they are neighbours, else -1
 };
 
 template <int MODE>
@@ -102,6 +107,7 @@ __device__ __forceinline__ Tile tile_of(uint32_t t, const RowsArgs& a, uint32_t 
   x.n0 = static_cast<int64_t>(t - rb * static_cast<uint32_t>(a.n_blocks)) * Shape<MODE>::kTileN;
   x.steps = main_steps(a);
   x.seg0 = 0;
+  x.box[0] = x.box[1] = -1;
   int left;
   if constexpr (MODE == kGated) {
     int4 e = a.rblist[check_index(a.hdr, rb, a.max_row_blocks, 80)];
@@ -120,6 +126,8 @@ __device__ __forceinline__ Tile tile_of(uint32_t t, const RowsArgs& a, uint32_t 
     left = l > kFM ? kFM : static_cast<int>(l);
     const int2 s = a.blkseg[rb];
     x.seg0 = s.x;
+    x.box[0] = a.box[2 * rb];
+    x.box[1] = a.box[2 * rb + 1];
     x.steps += s.y * rank_steps(a);
   }
   x.rows = left < 0 ? 0 : (left > kFM ? kFM : left);
@@ -151,7 +159,7 @@ __device__ __forceinline__ uint32_t w_bytes(const RowsArgs& a, int64_t n0, uint3
 
 template <int MODE>
 __device__ void w_producer(uint8_t* smem, WideCtl* ctl, const CUtensorMap* tm_w,
-                           const CUtensorMap* tm_b, const RowsArgs& a, uint32_t total,
+                           const CUtensorMap* tm_b, const CUtensorMap* tm_x, const RowsArgs& a, uint32_t total,
                            uint32_t rank) {
   const uint64_t lim = a.wait_limit_ns;
   volatile int* abort = &ctl->abort;
@@ -174,9 +182,14 @@ __device__ void w_producer(uint8_t* smem, WideCtl* ctl, const CUtensorMap* tm_w,
       }
       uint8_t* sb = smem + stage * kStageBytes + kABytes;
       const uint32_t fb = ptx::mapa(&ctl->full[stage], 0);
-      if (leader)
-        ptx::mbar_arrive_expect_tx(
-            &ctl->full[stage], w_bytes<MODE>(a, x.n0, 0, low) + w_bytes<MODE>(a, x.n0, 1, low));
+      if (leader) {
+        uint32_t bytes = w_bytes<MODE>(a, x.n0, 0, low) + w_bytes<MODE>(a, x.n0, 1, low);
+        if (MODE != kGated && !low)
+          bytes += (x.box[0] >= 0 ? kABytes : 0) + (x.box[1] >= 0 ? kABytes : 0);
+        ptx::mbar_arrive_expect_tx(&ctl->full[stage], bytes);
+      }
+      if (MODE != kGated && !low && x.box[rank] >= 0)
+        ptx::tma_load_2d_pair(sb - kABytes, tm_x, fb, ks * kFK, x.box[rank]);
       if constexpr (MODE == kGated) {
         // the even CTA loads the gates' columns, the odd one the ups'
         const int32_t c0 = static_cast<int32_t>(x.n0 + (rank ? a.N : 0));
@@ -262,7 +275,9 @@ __device__ void x_gatherer(uint8_t* smem, WideCtl* ctl, const RowsArgs& a, uint3
         failed = true;
         break;
       }
-      if (MODE == kGated || kb < nks) {
+      if (MODE != kGated && kb < nks && x.box[rank] >= 0) {
+        // neighbouring rows: the weight's producer copies them as one box
+      } else if (MODE == kGated || kb < nks) {
         const int64_t k = static_cast<int64_t>(kb) * kFK + c * 8;
         const bool k_ok = k < a.K;
         const char* xk = xb + k * 2;
@@ -504,7 +519,8 @@ __device__ void epilogue(WideCtl* ctl, uint32_t tmem_base, const RowsArgs& a, ui
 template <int DT, int MODE>
 __global__ void __launch_bounds__(kThreads, 1)
     rows_wide_kernel(const __grid_constant__ CUtensorMap tm_w,
-                     const __grid_constant__ CUtensorMap tm_b, const RowsArgs a) {
+                     const __grid_constant__ CUtensorMap tm_b,
+                     const __grid_constant__ CUtensorMap tm_x, const RowsArgs a) {
   ptx::griddep_wait();  // launched with programmatic serialization: predecessors done
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -538,6 +554,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 0 && lane == 0) {
     ptx::tma_prefetch_desc(&tm_w);
     if (MODE != kGated) ptx::tma_prefetch_desc(&tm_b);
+    if (MODE != kGated) ptx::tma_prefetch_desc(&tm_x);
   }
   if (warp == 1) {
     ptx::tmem_alloc_pair(&ctl->tmem_base, kTmemCols);
@@ -550,7 +567,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem_base = ctl->tmem_base;
 
   if (warp == 0) {
-    if (lane == 0) w_producer<MODE>(smem, ctl, &tm_w, &tm_b, a, total, rank);
+    if (lane == 0) w_producer<MODE>(smem, ctl, &tm_w, &tm_b, &tm_x, a, total, rank);
   } else if (warp == 1) {
     if (lane == 0 && rank == 0) mma_issuer<DT, MODE>(smem, ctl, tmem_base, a, total);
   } else if (warp < kEpiWarp0) {
@@ -569,9 +586,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <int DT>
-cudaError_t launch_t(RowsMode mode, const CUtensorMap& tm_w, const CUtensorMap& tm_b,
-                     const RowsArgs& a, int64_t max_tiles, int num_sms, cudaStream_t stream) {
-  using K = void (*)(const CUtensorMap, const CUtensorMap, const RowsArgs);
+cudaError_t launch_t(RowsMode mode, const CUtensorMap (&tm)[3], const RowsArgs& a,
+                     int64_t max_tiles, int num_sms, cudaStream_t stream) {
+  using K = void (*)(const CUtensorMap, const CUtensorMap, const CUtensorMap, const RowsArgs);
   const K kern = mode == kGated   ? K(rows_wide_kernel<DT, kGated>)
                  : mode == kAdapt ? K(rows_wide_kernel<DT, kAdapt>)
                                   : K(rows_wide_kernel<DT, kAdaptT>);
@@ -582,7 +599,8 @@ cudaError_t launch_t(RowsMode mode, const CUtensorMap& tm_w, const CUtensorMap& 
   if (err != cudaSuccess) return err;
   const int64_t want = max_tiles < num_sms / 2 ? max_tiles : num_sms / 2;
   return launch_pdl(kern, dim3(static_cast<unsigned>(2 * (clusters < want ? clusters : want))),
-                    dim3(kThreads), static_cast<size_t>(kSmemBytes), stream, 2, tm_w, tm_b, a);
+                    dim3(kThreads), static_cast<size_t>(kSmemBytes), stream, 2, tm[0], tm[1], tm[2],
+                    a);
 }
 
 }  // namespace
@@ -591,21 +609,23 @@ cudaError_t launch_rows_wide(int dtype, RowsMode mode, RowsArgs a, int num_sms,
                              cudaStream_t stream) {
   const int64_t tile_n = mode == kGated ? 128 : 256;
   a.n_blocks = static_cast<int32_t>((a.N + tile_n - 1) / tile_n);
-  CUtensorMap tm_w, tm_b;
-  std::memset(&tm_b, 0, sizeof(tm_b));
+  CUtensorMap tm[3];  // weight, b, x
+  std::memset(tm, 0, sizeof(tm));
   bool ok;
   if (mode == kGated)
-    ok = encode_map_3d(&tm_w, dtype, a.w, 2 * a.N, a.K, a.G, kFK);
+    ok = encode_map_3d(&tm[0], dtype, a.w, 2 * a.N, a.K, a.G, kFK);
   else if (mode == kAdapt)
-    ok = encode_map_3d(&tm_w, dtype, a.w, a.N, a.K, 1, kFK);
+    ok = encode_map_3d(&tm[0], dtype, a.w, a.N, a.K, 1, kFK);
   else
-    ok = encode_map_3d(&tm_w, dtype, a.w, a.K, a.N, 1, 128);
-  if (ok && mode != kGated) ok = encode_map_3d(&tm_b, dtype, a.b, a.R, a.N, a.G, 128);
+    ok = encode_map_3d(&tm[0], dtype, a.w, a.K, a.N, 1, 128);
+  if (mode != kGated)
+    ok = ok && encode_map_3d(&tm[1], dtype, a.b, a.R, a.N, a.G, 128) &&
+         encode_map_rows(&tm[2], dtype, a.x, a.K, a.batch, kFM);
   if (!ok) return cudaErrorInvalidValue;
   const int64_t row_blocks = mode == kGated ? a.max_row_blocks : (a.M + 2 * kFM - 1) / (2 * kFM);
   const int64_t tiles = row_blocks * a.n_blocks;
-  if (dtype == PGG_BF16) return launch_t<PGG_BF16>(mode, tm_w, tm_b, a, tiles, num_sms, stream);
-  if (dtype == PGG_F16) return launch_t<PGG_F16>(mode, tm_w, tm_b, a, tiles, num_sms, stream);
+  if (dtype == PGG_BF16) return launch_t<PGG_BF16>(mode, tm, a, tiles, num_sms, stream);
+  if (dtype == PGG_F16) return launch_t<PGG_F16>(mode, tm, a, tiles, num_sms, stream);
   return cudaErrorInvalidValue;
 }
 

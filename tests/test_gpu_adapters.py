@@ -271,3 +271,17 @@ def test_gradient_with_an_unknown_adapter_is_zero():
     torch.cuda.synchronize()
     assert pgg.STATUS[pgg.status(ws)] == "PGG_ERR_INDEX"
     assert all(torch.count_nonzero(o) == 0 for o in outs.values())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_neighbouring_and_scattered_rows_in_one_call(dtype):
+    # runs of requests (copied as boxes) broken by tokens that change places, block by block
+    s = inputs(1500, 264, 200, 16, 6, dtype=dtype, ids="runs", seed=66)
+    ad = s["adapter"]
+    ad[100:110] = -1
+    ad[300], ad[301] = ad[900].clone(), ad[0].clone()
+    ad[640:768] = torch.arange(128, device="cuda") % 6
+    check(s)
+    check_grad(s)
+    s["adapter"] = ad.flip(0).contiguous()
+    check(s)
