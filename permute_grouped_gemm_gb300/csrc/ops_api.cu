@@ -152,7 +152,7 @@ int adapter_plan(int64_t T, int64_t K, int64_t N, int64_t R, int64_t A, int dtyp
   }
   p->padded = grad ? 1 : 0;
   p->max_row_blocks = (T + p->rb - 1) / p->rb + groups;
-  p->rows_u = grad ? T + 63 * groups : T;
+  p->rows_u = grad ? T + (kRowPad - 1) * groups : T;
   const int64_t widest = N > K ? N : K;
   if (p->max_row_blocks * ((widest + 63) / 64) > kInt32Max) return PGG_ERR_SHAPE;
   adapter_blocks(T, &p->blocks, &p->tokens_per_block);
@@ -224,6 +224,7 @@ int run_shrink(const AdapterPlan& p, const AdapterTables& t, const HostEnv& env,
   a.batch = T;
   a.max_row_blocks = p.max_row_blocks;
   a.padded = p.padded;
+  a.range = t.range;
   a.hold_release = env.hold_release;
   a.wait_limit_ns = env.wait_limit_ns;
   if (p.variant != kVariantSimt && aligned(x, 16) && aligned(f, 16)) {

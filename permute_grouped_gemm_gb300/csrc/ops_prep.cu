@@ -194,7 +194,7 @@ __device__ void build_adapter_lists(const AdapterPrepArgs& a, bool write, uint32
   uint32_t total, n_seg, n_rb;
   const uint32_t start = block_scan_u32(n, s_scan, &total);
   const uint32_t ustart =
-      block_scan_u32(a.padded ? (n + 63u) / 64u * 64u : n, s_scan, &total);
+      block_scan_u32(a.padded ? (n + kRowPad - 1) / kRowPad * kRowPad : n, s_scan, &total);
   const bool live = group && n > 0 && static_cast<int>(id) < a.A;
   const uint32_t seg = block_scan_u32(live ? 1u : 0u, s_scan, &n_seg);
   const uint32_t nb = (n + a.rb - 1) / a.rb;
@@ -244,7 +244,7 @@ __device__ void build_adapter_lists(const AdapterPrepArgs& a, bool write, uint32
   }
 }
 
-// Records of one sorted token; the last token of a padded adapter also fills up its last 64 rows.
+// Records of one sorted token; the last token of a padded adapter also fills up its last rows.
 __device__ __forceinline__ void put_token(const AdapterPrepArgs& a, int64_t token, int g,
                                           uint32_t where, uint32_t start, uint32_t ustart,
                                           uint32_t count) {
@@ -257,7 +257,7 @@ __device__ __forceinline__ void put_token(const AdapterPrepArgs& a, int64_t toke
   r.rank = 0;
   a.t.padrow[ustart + i] = r;
   if (i + 1 == count)
-    for (uint32_t j = count; j < (count + 63u) / 64u * 64u; ++j) a.t.padrow[ustart + j] = r;
+    for (uint32_t j = count; j < (count + kRowPad - 1) / kRowPad * kRowPad; ++j) a.t.padrow[ustart + j] = r;
 }
 
 // Warps w, w + warps, ...: whether each 128 compact rows are neighbours in token order.

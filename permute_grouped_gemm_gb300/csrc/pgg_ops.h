@@ -36,6 +36,7 @@ constexpr int64_t kMaxRouteExperts = 1024;  // a token's logits sit in one warp'
 constexpr int64_t kMaxRouteTopK = 32;       // one lane per choice
 constexpr int64_t kMaxAdapters = 1023;      // + the group of tokens without one: one thread each
 constexpr int64_t kMaxRank = 256;
+constexpr int kRowPad = 128;  // rows of the factors' gradients reduced at a time
 
 // ------------------------------------------------------------ router
 
@@ -96,8 +97,8 @@ cudaError_t launch_rows_prep(const RowsPrepArgs& a, int num_sms, cudaStream_t st
 // another stays as it is and its rows can be copied in boxes; or in the order of their ids (the
 // weight-gradient kernels that take off[] need that). That compact order of T rows is what the
 // projection walks. The low-rank factors u and v are stored in a second order, in which
-// (padded = 1) every group starts at a multiple of 64 rows and is filled up with zero rows: the
-// reduction over an adapter's rows reads 64 at a time, and what it reads past them must not be
+// (padded = 1) every group starts at a multiple of kRowPad rows and is filled up with zero rows: the
+// reduction over an adapter's rows reads that many at a time, and what it reads past them must not be
 // another adapter's.
 struct AdapterTables {
   WsHeader* hdr;
@@ -118,7 +119,7 @@ struct AdapterPrepArgs {
   AdapterTables t;
   int64_t T;
   int32_t A;
-  int32_t rb;      // rows per entry of rblist, a multiple of 64 when padded
+  int32_t rb;      // rows per entry of rblist, a divisor of kRowPad when padded
   int32_t padded, by_first;
   int32_t blocks, tokens_per_block;  // of the counting and placement launches
 };
@@ -145,6 +146,7 @@ struct RowsArgs {
   const RowInfo* rowinfo;  // kGated {token, position}; else {token, adapter}
   const int4* segs;        // kAdapt*
   const int2* blkseg;      // kAdapt*
+  const int4* range;       // kShrink, padded: see AdapterTables
   const int32_t* box;      // kAdapt*
   WsHeader* hdr;
   void* out;               // h [M, N], u [*, N], y [T, N] (rows in token order)
@@ -152,11 +154,20 @@ struct RowsArgs {
   int64_t M, N, K, G, batch, max_row_blocks;
   int32_t R;
   int32_t n_blocks;
-  int32_t padded;          // kShrink: fill the last row block of an adapter with zeros to 64 rows
+  int32_t padded;          // kShrink: fill up an adapter's rows with zeros to a multiple of kRowPad
   const int64_t* adapter;  // few tokens: [T]; u is fp32 in token order then
   int32_t hold_release;
   uint64_t wait_limit_ns;
 };
+
+// Rows of zeros behind a row block of an adapter (none but behind its last).
+#ifdef __CUDACC__
+__device__ __forceinline__ int rows_to_fill(const RowsArgs& a, const int4& block) {
+  const int4 r = a.range[block.x];
+  if (block.y + block.z != r.x + r.y) return 0;
+  return (r.y + kRowPad - 1) / kRowPad * kRowPad - r.y;
+}
+#endif
 
 cudaError_t launch_rows_simt(int dtype, RowsMode mode, RowsArgs a, int num_sms,
                              cudaStream_t stream);

@@ -7,10 +7,10 @@
 // of one adapter, so what they cost is reading x and d_y once (R multiply-adds
 // a byte). Tile: one adapter, 128 of the K (N) columns as accumulator lanes and
 // 64 ranks as accumulator columns, fp32 in tensor memory (two buffers); both
-// operands are MN-major. A stage is 64 rows: 128 columns of x, by TMA where
-// the 64 rows are neighbouring tokens, else gathered by token with cp.async
+// operands are MN-major. A stage is 128 rows: 128 columns of x, by TMA where
+// the 128 rows are neighbouring tokens, else gathered by token with cp.async
 // (one warp per stage slot), and the rows' ranks of v by TMA. v is stored so
-// that an adapter's rows end on a multiple of 64 with rows of zeros, whose x row
+// that an adapter's rows end on a multiple of 128 with rows of zeros, whose x row
 // repeats the adapter's last: another adapter's rows, whatever they hold, never
 // take part.
 //
@@ -35,19 +35,21 @@ namespace {
 
 constexpr int kM = 128;            // columns of x (d_y) per tile: accumulator lanes
 constexpr int kNR = 64;            // ranks per tile: accumulator columns
-constexpr int kRows = 64;          // reduction per stage
+constexpr int kRows = 128;         // reduction per stage
 constexpr int kPanel = kRows * 128;
 constexpr int kABytes = 2 * kPanel;
 constexpr int kBBytes = kPanel;
 constexpr int kStageBytes = kABytes + kBBytes;
-constexpr int kStages = 7;
+constexpr int kStages = 4;
 constexpr int kRedBytes = kM * kNR * 4;
 constexpr int kEpiWarps = 4;
-constexpr int kThreads = 32 * (2 + kStages + kEpiWarps);
+constexpr int kGatherWarps = 2 * kStages;  // two per stage slot
+constexpr int kEpiWarp0 = 12;              // (a multiple of four: tensor-memory lanes)
+constexpr int kThreads = 32 * (kEpiWarp0 + kEpiWarps);
 constexpr int kTmemCols = 2 * kNR;
 
 struct Ctl {
-  uint64_t full[kStages];   // bytes + the gather warp's arrival
+  uint64_t full[kStages];   // bytes + the two gather warps' arrivals
   uint64_t empty[kStages];  // MMAs of the stage done
   uint64_t tfull[2], tempty[2];
   uint64_t rfull, rempty;   // partial sums of all CTAs received here / mine read by all CTAs
@@ -71,7 +73,7 @@ struct Tile {
   int ad, r0;
   int64_t c0;              // first column
   int4 range;              // {first compact row, rows, first row of v, 0}
-  int s0, s1;              // this CTA's steps of 64 rows
+  int s0, s1;              // this CTA's steps of 128 rows
   int steps;               // all steps of the adapter
 };
 
@@ -93,7 +95,7 @@ __device__ __forceinline__ Tile tile_of(uint32_t t, const OuterArgs& a, uint32_t
   return x;
 }
 
-// First token of the 64 rows of step s if all 64 are the adapter's and neighbouring tokens.
+// First token of the 128 rows of step s if all of them are the adapter's and neighbouring tokens.
 __device__ __forceinline__ int32_t box_of(const OuterArgs& a, const Tile& x, int s) {
   if (kRows * (s + 1) > x.range.y) return -1;
   return box_of_rows(a.order, static_cast<int64_t>(x.range.x) + kRows * s, kRows);
@@ -146,13 +148,13 @@ __device__ void producer(uint8_t* smem, Ctl* ctl, const CUtensorMap* tm, const O
       ptx::mbar_wait(&ctl->full[s], (last_parity >> s) & 1u, lim, &no_abort);
 }
 
-// Gather warp w fills stage slot w where its rows are not neighbours: row (lane >> 4) + 2 q,
-// 16-byte chunk lane & 15 of its 256 bytes.
+// Gather warps 2 w and 2 w + 1 fill half of stage slot w each where its rows are not neighbours:
+// row (lane >> 4) + 2 q, 16-byte chunk lane & 15 of its 256 bytes.
 __device__ void gatherer(uint8_t* smem, Ctl* ctl, const OuterArgs& a, uint32_t total,
                          uint32_t first, uint32_t step, uint32_t rank, uint32_t S) {
   const uint64_t lim = a.wait_limit_ns;
   volatile int* abort = &ctl->abort;
-  const int w = (threadIdx.x >> 5) - 2;
+  const int w = ((threadIdx.x >> 5) - 2) >> 1, half = ((threadIdx.x >> 5) - 2) & 1;
   const int lane = threadIdx.x & 31, c = lane & 15;
   const uint32_t sa = ptx::smem_addr(smem + w * kStageBytes + (c >> 3) * kPanel);
   uint32_t phase = 0;
@@ -168,21 +170,22 @@ __device__ void gatherer(uint8_t* smem, Ctl* ctl, const OuterArgs& a, uint32_t t
     for (; kb < steps; kb += kStages) {
       const int s = x.s0 + kb;
       const int32_t box = box_of(a, x, s);
-      int32_t tok[2];  // rows lane and lane + 32 of the step
+      int32_t tok[2];  // rows 64 half + lane + 32 h of the step
       if (box < 0) {
 #pragma unroll
         for (int h = 0; h < 2; ++h)
-          tok[h] = a.padrow[static_cast<int64_t>(x.range.z) + kRows * s + lane + 32 * h].token;
+          tok[h] = a.padrow[static_cast<int64_t>(x.range.z) + kRows * s + 64 * half + lane + 32 * h]
+                       .token;
       }
       if (!ptx::mbar_wait(&ctl->empty[w], phase ^ 1u, lim, abort)) {
         failed = true;
         break;
       }
       if (box < 0) {
-#pragma unroll 8
-        for (int q = 0; q < kRows / 2; ++q) {
-          const int rr = (lane >> 4) + 2 * q;
-          const int32_t tk = __shfl_sync(0xFFFFFFFFu, q < 16 ? tok[0] : tok[1], rr & 31);
+#pragma unroll
+        for (int q = 0; q < kRows / 4; ++q) {
+          const int rq = (lane >> 4) + 2 * q, rr = 64 * half + rq;
+          const int32_t tk = __shfl_sync(0xFFFFFFFFu, tok[q / 16], rq & 31);
           const void* src = in ? static_cast<const void*>(
                                      base + (static_cast<int64_t>(tk) * C + col) * 2)
                                : static_cast<const void*>(base);
@@ -374,7 +377,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
-      ptx::mbar_init(&ctl->full[s], 2);
+      ptx::mbar_init(&ctl->full[s], 3);
       ptx::mbar_init(&ctl->empty[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
@@ -402,9 +405,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) producer(smem, ctl, maps.m, a, total, first, step, rank, S);
   } else if (warp == 1) {
     if (lane == 0) mma_issuer<DT>(smem, ctl, tmem_base, a, total, first, step, rank, S);
-  } else if (warp < 2 + kStages) {
+  } else if (warp < 2 + kGatherWarps) {
     gatherer(smem, ctl, a, total, first, step, rank, S);
-  } else {
+  } else if (warp >= kEpiWarp0) {
     epilogue<DT>(ctl, red, tmem_base, a, total, first, step, rank, S);
   }
 
@@ -429,20 +432,20 @@ cudaError_t launch_rows_outer(int dtype, OuterArgs a, int num_sms, cudaStream_t 
         !encode_map_rows(&maps.m[2 * w + 1], dtype, a.right[w], a.R, a.right_rows, kRows))
       return cudaErrorInvalidValue;
   const auto kern = dtype == PGG_BF16 ? rows_outer_kernel<PGG_BF16> : rows_outer_kernel<PGG_F16>;
-  // Four CTAs a tile: adapters have unequal numbers of rows, and the finer the pieces the less one
-  // of them holds up the rest. (Two a tile measured the same, one 20% slower, with six adapters of
-  // 8192 tokens.)
-  constexpr int S = 4;
+  // Two CTAs a tile while there are few tiles for the SMs, so that one long adapter does not hold up
+  // the rest; with many the exchange costs more than it evens out (8192 tokens, K 4096, N 2048, of
+  // one adapter: 204 us alone, 190 in two; of 48: 227 alone, 264 in two).
+  const int64_t all_tiles =
+      static_cast<int64_t>(a.A) * a.r_blocks * (a.blocks0 + a.blocks1);
+  const int S = all_tiles < 4 * num_sms ? 2 : 1;
   static ClusterLimits limits[2];
   int clusters = 0;
   const cudaError_t err = clusters_that_fit(&limits[dtype == PGG_BF16 ? 0 : 1], kern, kThreads,
                                             kSmemBytes, S, num_sms, &clusters);
   if (err != cudaSuccess) return err;
-  const int64_t tiles =
-      static_cast<int64_t>(a.A) * a.r_blocks * (a.blocks0 + a.blocks1);
-  if (tiles < clusters) clusters = static_cast<int>(tiles);
+  if (all_tiles < clusters) clusters = static_cast<int>(all_tiles);
   return launch_pdl(kern, dim3(static_cast<unsigned>(S * clusters)), dim3(kThreads),
-                    static_cast<size_t>(kSmemBytes), stream, S, maps, a);
+                    static_cast<size_t>(kSmemBytes), stream, static_cast<unsigned>(S), maps, a);
 }
 
 }  // namespace pgg

@@ -13,10 +13,12 @@
 // in the order of the CTAs: split-K without a second launch, atomics or
 // workspace, bitwise repeatable. S = 1 when the tiles alone fill the GPU.
 //
-// A stage is 64 of k: two 64-column panels of the weight by TMA (16 KB) and NR
-// x rows, gathered by token with cp.async or, where they are neighbours, as one
-// TMA box. With NR = 16 twelve stages are in
-// flight per SM, 192 KB of weight, which is what keeps HBM busy.
+// A stage is 128 of k (64 for NR = 128): two 64-column panels of the weight by
+// TMA (32 KB) and NR x rows, gathered by token with cp.async or, where they are
+// neighbours, as TMA boxes. With NR = 16 six stages are in flight per SM, 192 KB
+// of weight. The one thread that issues the MMAs is the limit otherwise: a wait,
+// four MMAs and a commit took it 0.33 us a 64 of k, everything present; with
+// eight MMAs to a wait and a commit it is 0.2.
 //
 // adapt with few tokens: rows stay in the caller's order, and the low-rank part
 // is added in fp32 by the epilogue warps, which work it out from a row's u and
@@ -42,22 +44,24 @@ namespace pgg {
 namespace {
 
 constexpr int kM = 128;            // weight columns per tile: accumulator lanes
-constexpr int kFK = 64;            // reduction per stage
-constexpr int kPanel = kFK * 128;  // 64 k rows x 128 bytes (64 columns)
+constexpr int kFK = 64;            // reduction of one 128-byte row of x
 constexpr int kEpiWarps = 4;
 constexpr int kMaxSplit = 8;
 
 template <int NR, int PANELS>
 struct Cfg {
+  static constexpr int kSub = NR <= 64 ? 2 : 1;       // 64s of k per stage
+  static constexpr int kPanel = kSub * kFK * 128;     // k rows x 128 bytes (64 columns)
   static constexpr int kABytes = PANELS * kPanel;
-  static constexpr int kBBytes = NR * 128;
+  static constexpr int kSubBytes = NR * 128;          // rows x 64 of k
+  static constexpr int kBBytes = kSub * kSubBytes;
   static constexpr int kStageBytes = kABytes + kBBytes;
   static constexpr int kRedBytes = NR * kM * 4;  // S slots of NR / S rows x 128 lanes
   static constexpr int kFit = (226 * 1024 - 2048 - kRedBytes) / kStageBytes;
   static constexpr int kStages = kFit < 12 ? kFit : 12;
   static constexpr int kThreads = 32 * (2 + kStages + kEpiWarps);
   static constexpr int kTmemCols = 2 * NR < 32 ? 32 : 2 * NR;
-  static_assert(kBBytes % 1024 == 0, "operand alignment");
+  static_assert(kSubBytes % 1024 == 0, "operand alignment");
 };
 
 template <int STAGES>
@@ -156,7 +160,7 @@ __device__ void w_producer(uint8_t* smem, Ctl<Cfg<NR, PANELS>::kStages>* ctl,
     }
     const int32_t box = box_of<MODE>(a, x);
     const uint32_t bytes =
-        (on[0] ? kPanel : 0) + (on[1] ? kPanel : 0) + (box >= 0 ? C::kBBytes : 0);
+        (on[0] ? C::kPanel : 0) + (on[1] ? C::kPanel : 0) + (box >= 0 ? C::kBBytes : 0);
     for (int ks = k.ks0; ks < k.ks1; ++ks) {
       if (!ptx::mbar_wait(&ctl->empty[stage], phase ^ 1u, lim, abort)) {
         failed = true;
@@ -164,11 +168,13 @@ __device__ void w_producer(uint8_t* smem, Ctl<Cfg<NR, PANELS>::kStages>* ctl,
       }
       uint8_t* sa = smem + stage * C::kStageBytes;
       ptx::mbar_arrive_expect_tx(&ctl->full[stage], bytes);
-      if (box >= 0) ptx::tma_load_2d(sa + C::kABytes, tm_x, &ctl->full[stage], ks * kFK, box);
+      for (int j = 0; j < C::kSub && box >= 0; ++j)
+        ptx::tma_load_2d(sa + C::kABytes + j * C::kSubBytes, tm_x, &ctl->full[stage],
+                         (ks * C::kSub + j) * kFK, box);
       for (int j = 0; j < PANELS; ++j)
         if (on[j])
-          ptx::tma_load_3d(sa + j * kPanel, tm_w, &ctl->full[stage], col[j], ks * kFK,
-                           static_cast<int32_t>(x.g));
+          ptx::tma_load_3d(sa + j * C::kPanel, tm_w, &ctl->full[stage], col[j],
+                           ks * C::kSub * kFK, static_cast<int32_t>(x.g));
       outstanding |= 1u << stage;
       last_parity = (last_parity & ~(1u << stage)) | (phase << stage);
       if (++stage == C::kStages) {
@@ -227,17 +233,21 @@ __device__ void x_gatherer(uint8_t* smem, Ctl<Cfg<NR, PANELS>::kStages>* ctl, co
         break;
       }
       if (box < 0) {
-        const int64_t kk = static_cast<int64_t>(k.ks0 + kb) * kFK + c * 8;
-        const bool k_ok = kk < a.K;
-        const char* xk = xb + kk * 2;
 #pragma unroll
-        for (int q = 0; q < NR / 4; ++q) {
-          const int rr = (lane >> 3) + 4 * q;
-          const bool ok = k_ok && row16[q] != kNoRow;
-          const void* src = ok ? static_cast<const void*>(
-                                     xk + (static_cast<uint64_t>(row16[q]) << 4))
-                               : static_cast<const void*>(xb);
-          ptx::cp_async_16(sb + rr * 128 + ((c ^ (rr & 7)) << 4), src, ok ? 16u : 0u);
+        for (int j = 0; j < C::kSub; ++j) {
+          const int64_t kk = static_cast<int64_t>((k.ks0 + kb) * C::kSub + j) * kFK + c * 8;
+          const bool k_ok = kk < a.K;
+          const char* xk = xb + kk * 2;
+#pragma unroll
+          for (int q = 0; q < NR / 4; ++q) {
+            const int rr = (lane >> 3) + 4 * q;
+            const bool ok = k_ok && row16[q] != kNoRow;
+            const void* src = ok ? static_cast<const void*>(
+                                       xk + (static_cast<uint64_t>(row16[q]) << 4))
+                                 : static_cast<const void*>(xb);
+            ptx::cp_async_16(sb + j * C::kSubBytes + rr * 128 + ((c ^ (rr & 7)) << 4), src,
+                             ok ? 16u : 0u);
+          }
         }
         ptx::cp_async_commit();
         ptx::cp_async_wait<0>();
@@ -282,13 +292,13 @@ __device__ void mma_issuer(uint8_t* smem, Ctl<Cfg<NR, PANELS>::kStages>* ctl, ui
       }
       ptx::tc_fence_after_sync();
       const uint32_t sa = ptx::smem_addr(smem + stage * C::kStageBytes);
-      const uint64_t da = ptx::sdesc_sw128_mn(sa, kPanel);
+      const uint64_t da = ptx::sdesc_sw128_mn(sa, C::kPanel);
       const uint64_t db = ptx::sdesc_sw128(sa + C::kABytes);
 #pragma unroll
-      for (int kk = 0; kk < kFK / 16; ++kk)
+      for (int kk = 0; kk < C::kSub * kFK / 16; ++kk)
         ptx::mma_f16(d_tmem, da + static_cast<uint64_t>((kk * 16 * 128) >> 4),
-                     db + static_cast<uint64_t>((kk * 32) >> 4), idesc,
-                     (ks > k.ks0 || kk > 0) ? 1u : 0u);
+                     db + static_cast<uint64_t>(((kk / 4) * C::kSubBytes + (kk % 4) * 32) >> 4),
+                     idesc, (ks > k.ks0 || kk > 0) ? 1u : 0u);
       issued = true;
       ptx::mma_commit(&ctl->empty[stage]);
       if (++stage == C::kStages) {
@@ -521,8 +531,10 @@ __device__ void epilogue(Ctl<Cfg<NR, PANELS>::kStages>* ctl, float* red, uint32_
     }
     write_rows<DT, MODE, kLR>(red, slot, S, a, x, j0, n, failed_input, lr, row_scale);
     if constexpr (MODE == kShrink) {
-      if (a.padded) {  // rows that fill the adapter up to a multiple of 64
-        const int end = (x.rows + 63) / 64 * 64;
+      if (a.padded) {  // the adapter's last block: rows that fill it up
+        const int end = x.rows + rows_to_fill(a, make_int4(static_cast<int>(x.g),
+                                                           static_cast<int>(x.row0), x.rows,
+                                                           x.urow));
         for (int j = x.rows + static_cast<int>(rank) * kEpiWarps + quarter; j < end;
              j += static_cast<int>(S) * kEpiWarps)
           for (int64_t c = x.n0 + lane; c < a.N && c < x.n0 + kM; c += 32)
@@ -561,7 +573,7 @@ __global__ void __launch_bounds__(Cfg<NR, PANELS>::kThreads, 1)
   k.total = row_blocks * static_cast<uint32_t>(a.n_blocks);
   k.first = blockIdx.x / S;
   k.step = gridDim.x / S;
-  const int nks = static_cast<int>((a.K + kFK - 1) / kFK);
+  const int nks = static_cast<int>((a.K + C::kSub * kFK - 1) / (C::kSub * kFK));
   k.ks0 = nks * static_cast<int>(rank) / static_cast<int>(S);
   k.ks1 = nks * (static_cast<int>(rank) + 1) / static_cast<int>(S);
 
@@ -616,7 +628,7 @@ __global__ void __launch_bounds__(Cfg<NR, PANELS>::kThreads, 1)
 // CTAs per tile: the split of K that leaves the fewest steps on the critical path for about
 // `tiles` tiles, counting kTileCost steps per tile for its epilogue and exchange.
 int choose_split(int64_t tiles, int nks, int NR, int num_sms) {
-  constexpr int kTileCost = 8;
+  constexpr int kTileCost = 5;
   int best = 1;
   int64_t best_cost = 0;
   for (int s = 1; s <= kMaxSplit && s <= nks && s <= NR; s *= 2) {
@@ -638,7 +650,7 @@ cudaError_t launch_t(const CUtensorMap (&tm)[2], const RowsArgs& a, int64_t tile
   constexpr int smem = smem_bytes<NR, PANELS>();
   static_assert(smem <= 227 * 1024, "shared memory per CTA");
   auto kern = rows_skinny_kernel<DT, MODE, NR, PANELS>;
-  const int nks = static_cast<int>((a.K + kFK - 1) / kFK);
+  const int nks = static_cast<int>((a.K + C::kSub * kFK - 1) / (C::kSub * kFK));
   const int S = choose_split(tiles, nks, NR, num_sms);
   static ClusterLimits limits;
   int clusters = 0;
@@ -685,7 +697,8 @@ cudaError_t launch_rows_skinny(int dtype, RowsMode mode, int NR, RowsArgs a, int
   CUtensorMap tm[2];  // weight, x
   std::memset(tm, 0, sizeof(tm));
   const int64_t cols = mode == kGated ? 2 * a.N : a.N;
-  if (!encode_map_3d(&tm[0], dtype, a.w, cols, a.K, mode == kAdapt ? 1 : a.G, kFK))
+  if (!encode_map_3d(&tm[0], dtype, a.w, cols, a.K, mode == kAdapt ? 1 : a.G,
+                     NR <= 64 ? 2 * kFK : kFK))
     return cudaErrorInvalidValue;
   if (mode != kGated && !encode_map_rows(&tm[1], dtype, a.x, a.K, a.batch, NR))
     return cudaErrorInvalidValue;
