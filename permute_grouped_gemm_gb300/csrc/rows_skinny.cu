@@ -322,78 +322,83 @@ __device__ void mma_issuer(uint8_t* smem, Ctl<Cfg<NR, PANELS>::kStages>* ctl, ui
   }
 }
 
-template <int DT>
-__device__ __forceinline__ void store16(void* out, int64_t i, float v) {
-  const uint32_t p = pack2<DT>(v, 0.0f);
-  static_cast<uint16_t*>(out)[i] = static_cast<uint16_t>(p & 0xFFFFu);
+// Sums of the S CTAs' partial sums for four neighbouring lanes (weight columns) of a row: red holds
+// S slots of `slot` floats, rows of 128.
+__device__ __forceinline__ float4 sum4(const float* red, int slot, uint32_t S, int at) {
+  float4 v = *reinterpret_cast<const float4*>(red + at);
+  for (uint32_t s = 1; s < S; ++s) {
+    const float4 p = *reinterpret_cast<const float4*>(red + s * slot + at);
+    v.x += p.x;
+    v.y += p.y;
+    v.z += p.z;
+    v.w += p.w;
+  }
+  return v;
 }
 
-// Output of tile rows j, j + 4, ... < n (j: this warp's), whose first row is tile row j0: red
-// holds S slots of `slot` floats, rows of 128 lanes each.
+template <int DT>
+__device__ __forceinline__ uint2 pack4(const float4& v) {
+  return make_uint2(pack2<DT>(v.x, v.y), pack2<DT>(v.z, v.w));
+}
+
+// Output of tile rows j0 .. j0 + n - 1, four columns a thread (N is a multiple of 8, so all four
+// are there or none is). One warp at a time would be bound by its own latency here: the rows are
+// spread over all the epilogue's threads.
 template <int DT, int MODE, int LR>
 __device__ __forceinline__ void write_rows(const float* red, int slot, uint32_t S, const RowsArgs& a,
                                            const Tile& x, int j0, int n, bool failed,
                                            const float (&lr)[LR][4], float row_scale) {
   const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 3;
-#pragma unroll 1
-  for (int j = warp; j < n; j += kEpiWarps) {
-    const int64_t row = x.row0 + j0 + j;
-    const float* r = red + j * kM;
-    if constexpr (MODE == kGated) {
-      const float2* r2 = reinterpret_cast<const float2*>(r) + lane;
-      float2 g = make_float2(0.0f, 0.0f), u = g;
-      for (uint32_t s = 0; s < S; ++s) {
-        const float2 pg = r2[s * slot / 2], pu = r2[s * slot / 2 + 32];
-        g.x += pg.x;
-        g.y += pg.y;
-        u.x += pu.x;
-        u.y += pu.y;
-      }
-      const int64_t f = x.n0 + 2 * lane;
-      const float p = __shfl_sync(0xFFFFFFFFu, row_scale, (j - warp) / kEpiWarps);
-      if (f >= a.N) continue;  // (N is even)
-      *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + row * a.N + f) =
-          pack2<DT>(gate(g.x, u.x, p), gate(g.y, u.y, p));
+  if constexpr (MODE == kGated) {
+    // 16 threads a row, two rows a warp: gates in lanes 0 .. 63 of the tile, ups in 64 .. 127
+    const int f4 = 4 * (lane & 15);
+    const int64_t f = x.n0 + f4;
+#pragma unroll 2
+    for (int j = 2 * warp + (lane >> 4); j < (n + 1) / 2 * 2; j += 2 * kEpiWarps) {
+      // (both rows of a pair take part in the shuffle)
+      const float p = __shfl_sync(0xFFFFFFFFu, row_scale, 2 * ((j - 2 * warp) / 8) + (j & 1));
+      if (j >= n || f >= a.N) continue;
+      const int64_t row = x.row0 + j0 + j;
+      const float4 g = sum4(red, slot, S, j * kM + f4);
+      const float4 u = sum4(red, slot, S, j * kM + 64 + f4);
+      const float4 h = make_float4(gate(g.x, u.x, p), gate(g.y, u.y, p), gate(g.z, u.z, p),
+                                   gate(g.w, u.w, p));
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + row * a.N + f) = pack4<DT>(h);
       if (a.gate_up) {
         uint16_t* gu = static_cast<uint16_t*>(a.gate_up) + row * 2 * a.N + f;
-        *reinterpret_cast<uint32_t*>(gu) = pack2<DT>(g.x, g.y);
-        *reinterpret_cast<uint32_t*>(gu + a.N) = pack2<DT>(u.x, u.y);
+        *reinterpret_cast<uint2*>(gu) = pack4<DT>(g);
+        *reinterpret_cast<uint2*>(gu + a.N) = pack4<DT>(u);
       }
-    } else {
-      float v[4];
+    }
+  } else if constexpr (MODE == kShrink) {
+    const int left = static_cast<int>(a.N - x.n0 < kM ? a.N - x.n0 : kM);
+    const int groups = left / 4;  // of four columns
+#pragma unroll 2
+    for (int i = 32 * warp + lane; i < n * groups; i += 32 * kEpiWarps) {
+      const int j = i / groups, c = 4 * (i - j * groups);
+      float4 v = sum4(red, slot, S, j * kM + c);
+      v = make_float4(v.x * row_scale, v.y * row_scale, v.z * row_scale, v.w * row_scale);
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) +
+                                (static_cast<int64_t>(x.urow) + j0 + j) * a.N + x.n0 + c) =
+          pack4<DT>(v);
+    }
+  } else {
+    const int64_t c = x.n0 + 4 * lane;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        v[i] = 0.0f;
-        if (MODE == kShrink && x.n0 + lane + 32 * i >= a.N) continue;
-        for (uint32_t s = 0; s < S; ++s) v[i] += r[s * slot + lane + 32 * i];
-      }
-      if constexpr (MODE == kShrink) {
-        const int64_t orow = static_cast<int64_t>(x.urow) + j0 + j;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int64_t c = x.n0 + lane + 32 * i;
-          if (c < a.N) store16<DT>(a.out, orow * a.N + c, v[i] * row_scale);
-        }
-      } else {
-        // (a loop over constants: lr stays in registers)
-#pragma unroll
-        for (int q = 0; q < LR; ++q)
-          if (j == warp + kEpiWarps * q) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] += lr[q][i];
-          }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int64_t c = x.n0 + lane + 32 * i;
-          if (c < a.N) store16<DT>(a.out, row * a.N + c, failed ? 0.0f : v[i]);
-        }
-      }
+    for (int q = 0; q < LR; ++q) {
+      const int j = warp + kEpiWarps * q;
+      if (j >= n || c >= a.N) continue;
+      float4 v = sum4(red, slot, S, j * kM + 4 * lane);
+      v = failed ? make_float4(0.0f, 0.0f, 0.0f, 0.0f)
+                 : make_float4(v.x + lr[q][0], v.y + lr[q][1], v.z + lr[q][2], v.w + lr[q][3]);
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + (x.row0 + j0 + j) * a.N + c) =
+          pack4<DT>(v);
     }
   }
 }
 
 // Low-rank part of tile rows j0 + j, j = warp, warp + 4, ... < n: each row's u [R] against its own
-// adapter's b [n][R], 8 ranks (16 bytes of b) at a time, in fp32; lane l takes columns l + 32 i.
+// adapter's b [n][R], 8 ranks (16 bytes of b) at a time, in fp32; lane l takes columns 4 l + i.
 template <int DT, int LR>
 __device__ __forceinline__ void low_rank(const RowsArgs& a, const Tile& x, int j0, int n,
                                          float (&lr)[LR][4]) {
@@ -420,9 +425,9 @@ __device__ __forceinline__ void low_rank(const RowsArgs& a, const Tile& x, int j
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         w[i] = make_uint4(0, 0, 0, 0);
-        if (x.n0 + lane + 32 * i < a.N)
+        if (x.n0 + 4 * lane < a.N)
           w[i] = __ldg(reinterpret_cast<const uint4*>(
-              b + (static_cast<int64_t>(lane + 32 * i) * a.R + r0) * 2));
+              b + (static_cast<int64_t>(4 * lane + i) * a.R + r0) * 2));
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -467,10 +472,11 @@ __device__ void epilogue(Ctl<Cfg<NR, PANELS>::kStages>* ctl, float* red, uint32_
     }
     const int j0 = static_cast<int>(rank) * per;  // this CTA finishes rows j0 .. j0 + n - 1
     const int n = x.rows - j0 < per ? x.rows - j0 : per;
-    // what the rows are scaled by is loaded ahead: lane i holds the weight of this warp's i-th row
+    // what the rows are scaled by is loaded ahead: lane i holds the weight of this warp's i-th row,
+    // rows 2 q, 2 q + 1, 2 q + 8, 2 q + 9, ... for warp q
     float row_scale = 1.0f;
     if constexpr (MODE == kGated) {
-      const int j = quarter + kEpiWarps * lane;
+      const int j = 2 * quarter + (lane & 1) + 8 * (lane >> 1);
       if (a.probs && j < n)
         row_scale = a.probs[check_index(
             a.hdr, a.rowinfo[check_index(a.hdr, x.row0 + j0 + j, a.M, 94)].rank, a.M, 95)];
@@ -498,22 +504,24 @@ __device__ void epilogue(Ctl<Cfg<NR, PANELS>::kStages>* ctl, float* red, uint32_
     const uint32_t mine = 32 * quarter + lane;
     // (lanes past the rank hold nothing)
     const int cols = MODE == kShrink && x.n0 + 32 * quarter >= a.N ? 0 : x.rows;
+    // (whole groups of 16 rows: what lies past the tile's rows is sent and not read)
 #pragma unroll 1
     for (int c0 = 0; c0 < NR && c0 < cols; c0 += 16) {
       uint32_t v[16];
       ptx::tmem_ld_32x32b_x16(t_lane + static_cast<uint32_t>(c0), v);
       ptx::tmem_ld_wait();
+      if (S == 1) {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const int j = c0 + i;
-        if (j >= x.rows) break;
-        const int dst = j >> shift;
-        // slot `rank` of the CTA that finishes row j
-        float* where = red + rank * slot + (j & (per - 1)) * kM + mine;
-        if (S == 1)
-          *where = __uint_as_float(v[i]);
-        else
-          st_cluster_f32(ptx::mapa(where, static_cast<uint32_t>(dst)), __uint_as_float(v[i]));
+        for (int i = 0; i < 16; ++i) red[(c0 + i) * kM + mine] = __uint_as_float(v[i]);
+      } else {
+        // row j goes to slot `rank` of the CTA that finishes it
+        const uint32_t base = ptx::smem_addr(red + rank * slot + mine);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int j = c0 + i;
+          st_cluster_f32(mapa_addr(base + (j & (per - 1)) * kM * 4, j >> shift),
+                         __uint_as_float(v[i]));
+        }
       }
     }
     ptx::tc_fence_before_sync();
