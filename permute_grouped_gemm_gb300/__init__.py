@@ -215,7 +215,7 @@ def _dense(*tensors):
 
 def _is(what: str, t, shape, dtype):
     """An optional tensor of the given shape and dtype."""
-    if t is not None and (tuple(t.shape) != shape or t.dtype != dtype):
+    if t is not None and (t.shape != shape or t.dtype != dtype):
         raise ValueError(f"{what} must be {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
 
 
@@ -298,7 +298,7 @@ def swiglu(x, weight, expanded_row_idx, group_list, batch: int, top_k: int, row_
     if x.dtype != weight.dtype:
         raise PggError(CODES["PGG_ERR_DTYPE"], "swiglu")
     G, K, F2 = weight.shape
-    if F2 % 2 or tuple(x.shape) != (batch, K) or tuple(group_list.shape) != (G,):
+    if F2 % 2 or x.shape != (batch, K) or group_list.shape != (G,):
         raise PggError(CODES["PGG_ERR_SHAPE"], "swiglu")
     M, F, dev = expanded_row_idx.shape[0], F2 // 2, x.device
     _is("probs", probs, (batch, top_k), torch.float32)
@@ -336,8 +336,8 @@ def swiglu_grad(d_h, gate_up, expanded_row_idx, top_k: int, row_idx_type: int, p
     if d_h.dtype != gate_up.dtype:
         raise PggError(CODES["PGG_ERR_DTYPE"], "swiglu_grad")
     M, F = d_h.shape
-    if tuple(gate_up.shape) != (M, 2 * F) or tuple(expanded_row_idx.shape) != (M,) \
-            or top_k <= 0 or M % top_k:
+    if gate_up.shape != (M, 2 * F) or expanded_row_idx.shape != (M,) or top_k <= 0 \
+            or M % top_k:
         raise PggError(CODES["PGG_ERR_SHAPE"], "swiglu_grad")
     batch, dev = M // top_k, d_h.device
     _is("probs", probs, (batch, top_k), torch.float32)
@@ -372,8 +372,8 @@ def _adapter_sizes(where, x, weight, a, b, adapter, scale):
     T, K = x.shape
     N = weight.shape[1]
     A, _, R = a.shape
-    if tuple(weight.shape) != (K, N) or tuple(a.shape) != (A, K, R) \
-            or tuple(b.shape) != (A, N, R) or tuple(adapter.shape) != (T,):
+    if weight.shape != (K, N) or a.shape != (A, K, R) or b.shape != (A, N, R) \
+            or adapter.shape != (T,):
         raise PggError(CODES["PGG_ERR_SHAPE"], where)
     if not x.dtype == weight.dtype == a.dtype == b.dtype:
         raise PggError(CODES["PGG_ERR_DTYPE"], where)

@@ -8,8 +8,8 @@
 //     prob[j]  = scale * score[chosen_j]  (/ sum over the chosen when renormalised)
 //     rows     = the pairs (token, j) sorted by (expert, token * k + j)
 //
-// A warp takes one token: its logits sit in registers (G / 32 a lane) as
-// sortable integers; see choose_and_write. A NaN key
+// A warp takes two tokens (or one): the logits sit in registers, G / 16 a lane,
+// as sortable integers; see choose_and_write. A NaN key
 // sorts below everything (the choice stays a valid one); scores follow IEEE
 // arithmetic, so a NaN or +inf logit gives NaN weights. A masked expert
 // (-inf) has weight 0; a token whose experts are all masked takes the lowest
@@ -35,7 +35,7 @@ namespace {
 
 constexpr int kWarps = 8;           // of the choice, placement and gradient blocks
 constexpr int kSmallEntries = 2048; // one block does it all up to this many (token, j) pairs
-constexpr int kSmallThreads = 1024;
+constexpr int kSmallThreads = 512;
 constexpr int kMaxBlocks = 608;     // of the choice and placement launches: four a multiprocessor
 
 template <int DT>
@@ -50,6 +50,35 @@ __device__ __forceinline__ uint32_t sort_key(float f) {
   const int32_t u = __float_as_int(f);
   const uint32_t k = static_cast<uint32_t>(u ^ ((u >> 31) | static_cast<int32_t>(0x80000000)));
   return f != f ? 1u : k;
+}
+
+// Sum and maximum over groups of LPT lanes.
+template <int LPT>
+__device__ __forceinline__ float group_sum(float v) {
+#pragma unroll
+  for (int d = LPT / 2; d > 0; d >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, d);
+  return v;
+}
+
+template <int LPT>
+__device__ __forceinline__ float group_max(float v) {
+#pragma unroll
+  for (int d = LPT / 2; d > 0; d >>= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, d));
+  return v;
+}
+
+template <int LPT>
+__device__ __forceinline__ uint32_t group_max_u32(uint32_t v) {
+  if constexpr (LPT == 32) {
+    return __reduce_max_sync(0xFFFFFFFFu, v);
+  } else {
+#pragma unroll
+    for (int d = LPT / 2; d > 0; d >>= 1) {
+      const uint32_t o = __shfl_xor_sync(0xFFFFFFFFu, v, d);
+      v = o > v ? o : v;
+    }
+    return v;
+  }
 }
 
 __device__ __forceinline__ float warp_sum(float v) {
@@ -71,27 +100,28 @@ __device__ __forceinline__ float soft_exp(float l, float m) {
 
 __device__ __forceinline__ float sigmoid(float l) { return 1.0f / (1.0f + expf(-l)); }
 
-// Where value i of a lane sits in a row: VL neighbouring values a load, 32 VL a warp.
-template <int VL>
-__device__ __forceinline__ int expert_at(int i, int lane) {
-  return (i / VL) * (32 * VL) + lane * VL + i % VL;
+// Where value i of lane sl of a token's LPT lanes sits in its row: VL neighbouring values a load,
+// LPT VL a group of lanes.
+template <int VL, int LPT>
+__device__ __forceinline__ int expert_at(int i, int sl) {
+  return (i / VL) * (LPT * VL) + sl * VL + i % VL;
 }
 
 // A row's logits, V a lane; -inf past the end. VL > 1: 4 VL or 2 VL bytes a load (G is a multiple
 // of VL and the rows are aligned to it).
-template <int DT, int V, int VL>
-__device__ __forceinline__ void load_row(const void* logits, int64_t row, int G, int lane,
+template <int DT, int V, int VL, int LPT>
+__device__ __forceinline__ void load_row(const void* logits, int64_t row, int G, int sl,
                                          float (&l)[V]) {
   constexpr int kBytes = VL * (DT == PGG_F32 ? 4 : 2);
   if constexpr (VL == 1) {
 #pragma unroll
     for (int i = 0; i < V; ++i)
-      l[i] = expert_at<1>(i, lane) < G ? load_logit<DT>(logits, row + expert_at<1>(i, lane))
+      l[i] = expert_at<1, LPT>(i, sl) < G ? load_logit<DT>(logits, row + expert_at<1, LPT>(i, sl))
                                        : -INFINITY;
   } else {
 #pragma unroll
     for (int i = 0; i < V; i += VL) {
-      const int e = expert_at<VL>(i, lane);
+      const int e = expert_at<VL, LPT>(i, sl);
       uint32_t w[4] = {0, 0, 0, 0};
       if (e < G) {
         const char* p = static_cast<const char*>(logits) + (row + e) * (kBytes / VL);
@@ -121,131 +151,143 @@ __device__ __forceinline__ void load_row(const void* logits, int64_t row, int G,
   }
 }
 
-template <int V, int VL>
-__device__ __forceinline__ void load_bias(const float* bias, int G, int lane, float (&b)[V]) {
+template <int V, int VL, int LPT>
+__device__ __forceinline__ void load_bias(const float* bias, int G, int sl, float (&b)[V]) {
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    const int e = expert_at<VL>(i, lane);
+    const int e = expert_at<VL, LPT>(i, sl);
     b[i] = (bias && e < G ? bias[e] : 0.0f) + 0.0f;  // (-0 becomes +0)
   }
 }
 
-// Token t's choice with one warp, written to probs, experts and s_expert [k].
+// The choice of 32 / LPT tokens from t0 on with one warp, LPT lanes each, written to probs,
+// experts and s_expert [k] (a token at or past T writes nothing).
 //
-// The k-th largest of the lanes' maxima is at most the k-th largest key, so
-// the chosen are among the keys that reach it: rarely more than k plus a
-// few. They are collected, one a lane, and each finds its rank by counting
-// those before it. Only when equal keys leave more than 32 of them the k
-// rounds of a warp-wide maximum are done instead. About 400 instructions a
-// token at 256 experts and k = 8, half of what the rounds take.
-template <int DT, int V, int VL>
-__device__ __forceinline__ void choose_and_write(const RouteArgs& a, int64_t t, int lane,
-                                                 const float (&bias)[V], uint64_t* s_cand,
-                                                 int* s_expert) {
+// The k-th largest of the lanes' maxima is at most the k-th largest key, so the chosen are among
+// the keys that reach it: rarely more than k plus a few. They are collected in shared memory and
+// each finds its rank by counting those before it. Only when equal keys leave more than 32 of them
+// the k rounds of a group-wide maximum are done instead. With two tokens a warp (k <= 16, at most
+// 512 experts) everything but the keys themselves is shared by two tokens.
+template <int DT, int V, int VL, int LPT>
+__device__ __forceinline__ void choose_and_write(const RouteArgs& a, int64_t t0, int64_t t1,
+                                                 int lane, const float (&bias)[V],
+                                                 uint64_t* s_cand, int* s_expert) {
+  const int sl = lane % LPT, sub = lane / LPT;
+  const uint32_t group = LPT == 32 ? 0xFFFFFFFFu : 0xFFFFu << (16 * sub);
+  const int64_t t = t0 + sub < t1 ? t0 + sub : t1 - 1;  // (the last one again, not written)
+  const bool there = t0 + sub < t1;
+  s_cand += 32 * sub;
+  s_expert += a.k * sub;
   float l[V];
   uint32_t key[V];
   const int64_t row = t * a.G;
-  load_row<DT, V, VL>(a.logits, row, a.G, lane, l);
+  load_row<DT, V, VL, LPT>(a.logits, row, a.G, sl, l);
+  float m = -INFINITY, z = 0.0f;
+  if (!a.sigmoid && !a.renormalize) {  // softmax over all
+#pragma unroll
+    for (int i = 0; i < V; ++i) m = fmaxf(m, l[i]);
+    m = group_max<LPT>(m);
+#pragma unroll
+    for (int i = 0; i < V; ++i) z += soft_exp(l[i], m);  // (0 past the end)
+    z = group_sum<LPT>(z);
+  }
   uint32_t best = 0;
 #pragma unroll
   for (int i = 0; i < V; i += VL) {
     // 0: not there (a whole load is, or is not)
-    const bool there = expert_at<VL>(i, lane) < a.G;
+    const bool in = expert_at<VL, LPT>(i, sl) < a.G;
 #pragma unroll
     for (int c = i; c < i + VL; ++c) {
       // (the bias is +0 without one, so a sum is never -0)
-      key[c] = there ? sort_key(l[c] + bias[c]) : 0u;
+      key[c] = in ? sort_key(l[c] + bias[c]) : 0u;
       best = key[c] > best ? key[c] : best;
     }
   }
   uint32_t floor_key = 0;
-  for (int seen = 0; seen < a.k;) {
-    floor_key = __reduce_max_sync(0xFFFFFFFFu, best);
-    if (floor_key == 0) break;  // (fewer lanes than k hold anything: all that is there)
-    const bool top = best == floor_key;
-    seen += __popc(__ballot_sync(0xFFFFFFFFu, top));
+  for (int seen = 0;;) {
+    const uint32_t top_key = group_max_u32<LPT>(best);
+    const bool more = seen < a.k;
+    const bool top = more && best == top_key;
+    const int n = __popc(__ballot_sync(0xFFFFFFFFu, top) & group);
+    if (more) {
+      // 0: fewer lanes than k hold anything, so all that is there is looked at
+      floor_key = top_key > 0 ? top_key : 1u;
+      seen = top_key > 0 ? seen + n : a.k;
+    }
     if (top) best = 0;
+    if (!__any_sync(0xFFFFFFFFu, seen < a.k)) break;
   }
-  if (floor_key == 0) floor_key = 1;
-  int mine_n = 0;  // candidates of this lane, and of the lanes up to it
+  int mine = 0;  // candidates of this lane, then of the lanes up to it
 #pragma unroll
-  for (int i = 0; i < V; ++i) mine_n += key[i] >= floor_key ? 1 : 0;
-  int upto = mine_n;
+  for (int i = 0; i < V; ++i) mine += key[i] >= floor_key ? 1 : 0;
+  int upto = mine;
 #pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const int y = __shfl_up_sync(0xFFFFFFFFu, upto, d);
-    if (lane >= d) upto += y;
+  for (int d = 1; d < LPT; d <<= 1) {
+    const int y = __shfl_up_sync(0xFFFFFFFFu, upto, d, LPT);
+    if (sl >= d) upto += y;
   }
-  const int n = __shfl_sync(0xFFFFFFFFu, upto, 31);
-  int e = 0, rank = 32;
+  const int n = __shfl_sync(0xFFFFFFFFu, upto, LPT - 1, LPT);
   if (n <= 32) {
     // key above, the index's complement below: a larger number comes first
-    uint64_t* at = s_cand + (upto - mine_n);
+    uint64_t* at = s_cand + (upto - mine);
 #pragma unroll
     for (int i = 0; i < V; ++i)
       if (key[i] >= floor_key)
         *at++ = static_cast<uint64_t>(key[i]) << 32 |
-                static_cast<uint32_t>(~expert_at<VL>(i, lane));
-    __syncwarp();
-    const uint64_t mine = lane < n ? s_cand[lane] : 0u;
-    int before = 0;
-#pragma unroll 4
-    for (int j = 0; j < n; ++j) before += s_cand[j] > mine ? 1 : 0;
-    __syncwarp();
-    if (lane < n && before < a.k) {
-      rank = before;
-      e = static_cast<int>(~static_cast<uint32_t>(mine));
-    }
-  } else {
+                static_cast<uint32_t>(~expert_at<VL, LPT>(i, sl));
+  }
+  __syncwarp();
+  if (__any_sync(0xFFFFFFFFu, n > 32)) {
     for (int j = 0; j < a.k; ++j) {
-      uint32_t top = 0, where = 0xFFFFFFFFu;
+      uint32_t top = 0, where = 0;
 #pragma unroll
       for (int i = 0; i < V; ++i) top = key[i] > top ? key[i] : top;
-      top = __reduce_max_sync(0xFFFFFFFFu, top);
+      top = group_max_u32<LPT>(top);
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const uint32_t x = static_cast<uint32_t>(expert_at<VL>(i, lane));
-        if (key[i] == top && x < where) where = x;
+      for (int i = 0; i < V; ++i) {  // the lowest index: the largest complement
+        const uint32_t x = ~static_cast<uint32_t>(expert_at<VL, LPT>(i, sl));
+        if (key[i] == top && x > where) where = x;
       }
-      where = __reduce_min_sync(0xFFFFFFFFu, where);
+      where = ~group_max_u32<LPT>(where);
 #pragma unroll
       for (int i = 0; i < V; ++i)
-        if (static_cast<uint32_t>(expert_at<VL>(i, lane)) == where) key[i] = 0;
-      if (lane == j) {
-        e = static_cast<int>(where);
-        rank = j;
-      }
+        if (static_cast<uint32_t>(expert_at<VL, LPT>(i, sl)) == where) key[i] = 0;
+      if (n > 32 && sl == 0) s_expert[j] = static_cast<int>(where);
     }
   }
-  const bool on = rank < 32;
+  for (int c0 = 0; c0 < 32; c0 += LPT) {
+    if (!__any_sync(0xFFFFFFFFu, n <= 32 && c0 < n)) break;
+    if (n <= 32 && c0 + sl < n) {
+      const uint64_t own = s_cand[c0 + sl];
+      int before = 0;
+#pragma unroll 4
+      for (int j = 0; j < n; ++j) before += s_cand[j] > own ? 1 : 0;
+      if (before < a.k) s_expert[before] = static_cast<int>(~static_cast<uint32_t>(own));
+    }
+  }
+  __syncwarp();
+  const bool on = sl < a.k;
+  const int e = on ? s_expert[sl] : 0;
   const float my_l = on ? load_logit<DT>(a.logits, row + e) : -INFINITY;
   float p;
   if (a.sigmoid) {
     p = on ? sigmoid(my_l) : 0.0f;
     if (a.renormalize) {
-      const float z = warp_sum(p);
+      z = group_sum<LPT>(p);
       p = z == 0.0f ? 0.0f : p / z;
     }
   } else if (a.renormalize) {
     // softmax over the chosen alone: the others' part cancels
-    const float m = warp_max(my_l);
+    m = group_max<LPT>(my_l);
     p = on ? soft_exp(my_l, m) : 0.0f;
-    const float z = warp_sum(p);
+    z = group_sum<LPT>(p);
     p = m == -INFINITY && z == 0.0f ? 0.0f : p / z;
   } else {
-    float m = -INFINITY, z = 0.0f;
-#pragma unroll
-    for (int i = 0; i < V; ++i) m = fmaxf(m, l[i]);
-    m = warp_max(m);
-#pragma unroll
-    for (int i = 0; i < V; ++i) z += soft_exp(l[i], m);  // (0 past the end)
-    z = warp_sum(z);
     p = m == -INFINITY && z == 0.0f ? 0.0f : soft_exp(my_l, m) / z;
   }
-  if (on) {
-    a.experts[t * a.k + rank] = e;
-    a.probs[t * a.k + rank] = p * a.scale;
-    s_expert[rank] = e;
+  if (on && there) {
+    a.experts[t * a.k + sl] = e;
+    a.probs[t * a.k + sl] = p * a.scale;
   }
 }
 
@@ -257,44 +299,49 @@ __device__ __forceinline__ void write_place(const RouteArgs& a, int64_t p, int64
 }
 
 // Everything in one block.
-template <int DT, int V, int VL>
+template <int DT, int V, int VL, int LPT>
 __global__ void __launch_bounds__(kSmallThreads) route_small_kernel(const RouteArgs a) {
-  extern __shared__ uint32_t s_cnt[];  // [warps][G], then the entries' experts
+  extern __shared__ uint32_t s_cnt[];  // [warps][G], the entries' experts, [G] bases
   __shared__ uint32_t s_scan[33];
-  __shared__ uint64_t s_cand[kSmallThreads / 32][32];
+  __shared__ uint64_t s_cand[kSmallThreads / 32][64];
   ptx::griddep_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   int* s_expert = reinterpret_cast<int*>(s_cnt + warps * a.G);
   const int T = static_cast<int>(a.T), n = T * a.k;
   float bias[V];
-  load_bias<V, VL>(a.bias, a.G, lane, bias);
-  for (int t = warp; t < T; t += warps)
-    choose_and_write<DT, V, VL>(a, t, lane, bias, s_cand[warp], s_expert + t * a.k);
+  load_bias<V, VL, LPT>(a.bias, a.G, lane % LPT, bias);
+  constexpr int kTok = 32 / LPT;  // tokens of a warp at a time
+  for (int t = kTok * warp; t < T; t += kTok * warps)
+    choose_and_write<DT, V, VL, LPT>(a, t, T, lane, bias, s_cand[warp], s_expert + t * a.k);
   __syncthreads();
   const int run = ((n + warps - 1) / warps + 31) / 32 * 32;
   auto key = [&](int e) { return s_expert[e]; };
   sort_count(s_cnt, a.G, n, run, key);
-  const int g = threadIdx.x;
-  if (g == 0) a.hdr->status = 0;
-  uint32_t c = 0;
-  if (g < a.G) {
-    for (int w = 0; w < warps; ++w) c += s_cnt[w * a.G + g];
-    a.groups[g] = c;
+  if (threadIdx.x == 0) a.hdr->status = 0;
+  uint32_t* s_base = reinterpret_cast<uint32_t*>(s_expert + n);
+  uint32_t before = 0;
+  for (int g0 = 0; g0 < a.G; g0 += blockDim.x) {
+    const int g = g0 + threadIdx.x;
+    uint32_t c = 0, total;
+    if (g < a.G) {
+      for (int w = 0; w < warps; ++w) c += s_cnt[w * a.G + g];
+      a.groups[g] = c;
+    }
+    const uint32_t at = block_scan_u32(c, s_scan, &total);
+    if (g < a.G) s_base[g] = before + at;
+    before += total;
   }
-  uint32_t total;
-  const uint32_t at = block_scan_u32(c, s_scan, &total);
-  // blockDim >= G: thread g is the one that asks for key g's base
   sort_place(
-      s_cnt, a.G, n, run, key, [&](int) { return at; },
+      s_cnt, a.G, n, run, key, [&](int g) { return s_base[g]; },
       [&](int e, uint32_t where) { write_place(a, e, where); });
 }
 
 // (1) Choice, and the block's count of every expert.
-template <int DT, int V, int VL>
-__global__ void __launch_bounds__(32 * kWarps, V <= 8 ? 4 : 2) route_choose_kernel(const RouteArgs a) {
+template <int DT, int V, int VL, int LPT>
+__global__ void __launch_bounds__(32 * kWarps, V <= 16 ? 4 : 2) route_choose_kernel(const RouteArgs a) {
   extern __shared__ uint32_t s_cnt[];  // [G]
-  __shared__ uint64_t s_cand[kWarps][32];
-  __shared__ int s_expert[kWarps][kMaxRouteTopK];
+  __shared__ uint64_t s_cand[kWarps][64];
+  __shared__ int s_expert[kWarps][kMaxRouteTopK];  // (two tokens of at most 16 or one)
   ptx::griddep_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   for (int g = threadIdx.x; g < a.G; g += blockDim.x) s_cnt[g] = 0;
@@ -303,12 +350,13 @@ __global__ void __launch_bounds__(32 * kWarps, V <= 8 ? 4 : 2) route_choose_kern
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * a.tokens_per_block;
   const int64_t t1 = t0 + a.tokens_per_block < a.T ? t0 + a.tokens_per_block : a.T;
   float bias[V];
-  load_bias<V, VL>(a.bias, a.G, lane, bias);
-  for (int64_t t = t0 + warp; t < t1; t += kWarps) {
-    choose_and_write<DT, V, VL>(a, t, lane, bias, s_cand[warp], s_expert[warp]);
-    __syncwarp();
+  load_bias<V, VL, LPT>(a.bias, a.G, lane % LPT, bias);
+  constexpr int kTok = 32 / LPT;  // tokens of a warp at a time
+  for (int64_t t = t0 + kTok * warp; t < t1; t += kTok * kWarps) {
+    choose_and_write<DT, V, VL, LPT>(a, t, t1, lane, bias, s_cand[warp], s_expert[warp]);
     // (integer counts: the order of these additions changes nothing)
-    if (lane < a.k) atomicAdd(&s_cnt[s_expert[warp][lane]], 1u);
+    const int n = t + kTok <= t1 ? kTok * a.k : static_cast<int>(t1 - t) * a.k;
+    if (lane < n) atomicAdd(&s_cnt[s_expert[warp][lane]], 1u);
     __syncwarp();
   }
   __syncthreads();
@@ -480,15 +528,14 @@ constexpr int load_width() {
   return V < (DT == PGG_F32 ? 4 : 8) ? V : (DT == PGG_F32 ? 4 : 8);
 }
 
-template <int DT, int V, int VL>
+template <int DT, int V, int VL, int LPT>
 cudaError_t launch_route_v(const RouteArgs& a, cudaStream_t stream) {
   if (a.blocks == 1) {
-    // threads for the tokens and for the experts' scan, no more: fewer counters to clear
-    int threads = static_cast<int>(a.T < 32 ? a.T : 32) * 32;
-    const int for_scan = (a.G + 31) / 32 * 32;
-    if (threads < for_scan) threads = for_scan;
-    const size_t smem = (static_cast<size_t>(threads / 32) * a.G + a.T * a.k) * 4;
-    auto kern = route_small_kernel<DT, V, VL>;
+    // threads for the tokens, no more: fewer counters to clear
+    const int64_t warps = (a.T * LPT + 31) / 32;
+    const int threads = static_cast<int>(warps < kSmallThreads / 32 ? warps : kSmallThreads / 32) * 32;
+    const size_t smem = (static_cast<size_t>(threads / 32 + 1) * a.G + a.T * a.k) * 4;
+    auto kern = route_small_kernel<DT, V, VL, LPT>;
     if (smem > 32 * 1024) {
       cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              static_cast<int>(smem));
@@ -496,7 +543,7 @@ cudaError_t launch_route_v(const RouteArgs& a, cudaStream_t stream) {
     }
     return launch_pdl(kern, dim3(1), dim3(threads), smem, stream, 1, a);
   }
-  cudaError_t err = launch_pdl(route_choose_kernel<DT, V, VL>, dim3(a.blocks), dim3(32 * kWarps),
+  cudaError_t err = launch_pdl(route_choose_kernel<DT, V, VL, LPT>, dim3(a.blocks), dim3(32 * kWarps),
                                static_cast<size_t>(a.G) * 4, stream, 1, a);
   if (err != cudaSuccess) return err;
   err = launch_count_scan(a.counts, a.G, a.blocks, a.groups, stream);
@@ -505,23 +552,26 @@ cudaError_t launch_route_v(const RouteArgs& a, cudaStream_t stream) {
                     static_cast<size_t>(kWarps + 1) * a.G * 4, stream, 1, a);
 }
 
-template <int DT, int V>
+template <int DT, int V, int LPT>
 cudaError_t launch_route_t(const RouteArgs& a, cudaStream_t stream) {
   constexpr int kVL = load_width<DT, V>();
   constexpr uintptr_t kAlign = kVL * (DT == PGG_F32 ? 4 : 2);
   if (kVL > 1 && a.G % kVL == 0 && reinterpret_cast<uintptr_t>(a.logits) % kAlign == 0)
-    return launch_route_v<DT, V, kVL>(a, stream);
-  return launch_route_v<DT, V, 1>(a, stream);
+    return launch_route_v<DT, V, kVL, LPT>(a, stream);
+  return launch_route_v<DT, V, 1, LPT>(a, stream);
 }
 
 template <int DT>
 cudaError_t launch_route_d(const RouteArgs& a, cudaStream_t stream) {
-  if (a.G <= 32) return launch_route_t<DT, 1>(a, stream);
-  if (a.G <= 64) return launch_route_t<DT, 2>(a, stream);
-  if (a.G <= 128) return launch_route_t<DT, 4>(a, stream);
-  if (a.G <= 256) return launch_route_t<DT, 8>(a, stream);
-  if (a.G <= 512) return launch_route_t<DT, 16>(a, stream);
-  return launch_route_t<DT, 32>(a, stream);
+  // two tokens a warp where a half's lanes are enough for the choices and the logits
+  if (a.k <= 16 && a.G <= 512) {
+    if (a.G <= 32) return launch_route_t<DT, 2, 16>(a, stream);
+    if (a.G <= 64) return launch_route_t<DT, 4, 16>(a, stream);
+    if (a.G <= 128) return launch_route_t<DT, 8, 16>(a, stream);
+    if (a.G <= 256) return launch_route_t<DT, 16, 16>(a, stream);
+    return launch_route_t<DT, 32, 16>(a, stream);
+  }
+  return launch_route_t<DT, 32, 32>(a, stream);
 }
 
 }  // namespace
