@@ -102,8 +102,8 @@ int gated_plan(int64_t M, int64_t F, int64_t K, int64_t G, int64_t batch, int dt
       // room for twice the even share, but an expert has at most one row of a token
       const double want = 2.0 * rows < static_cast<double>(batch) ? 2.0 * rows : batch;
       p->rows_per_block = want <= 16 ? 16 : want <= 32 ? 32 : want <= 64 ? 64 : 128;
-      p->live_blocks = static_cast<int64_t>(live * std::ceil(rows / p->rows_per_block) + 0.5);
     }
+    p->live_blocks = static_cast<int64_t>(live * std::ceil(rows / p->rows_per_block) + 0.5);
   }
   p->max_row_blocks = (M + p->rows_per_block - 1) / p->rows_per_block + (G < M ? G : M);
   if (p->max_row_blocks * ((F + 63) / 64) > kInt32Max) return PGG_ERR_SHAPE;  // 32-bit tile numbers
@@ -289,7 +289,7 @@ int run_adapt(const AdapterPlan& p, const AdapterTables& t, const HostEnv& env, 
   }
   if (p.variant != kVariantSimt && aligned(x, 16) && aligned(w, 16) && aligned(f, 16) &&
       aligned(y, 16))
-    return status_of(launch_rows_wide(dtype, mode, a, env.num_sms, stream));
+    return status_of(launch_rows_wide(dtype, mode, a, (T + 255) / 256, env.num_sms, stream));
   return status_of(launch_rows_simt(dtype, mode, a, env.num_sms, stream));
 }
 
@@ -447,7 +447,7 @@ int pgg_swiglu_execute(const void* x, const void* weight, const int64_t* expande
     return status_of(launch_rows_skinny(dtype, kGated, p.rows_per_block, a, p.live_blocks,
                                         env.num_sms, s));
   if (p.variant == kVariantWide && rows16)
-    return status_of(launch_rows_wide(dtype, kGated, a, env.num_sms, s));
+    return status_of(launch_rows_wide(dtype, kGated, a, p.live_blocks, env.num_sms, s));
   return status_of(launch_rows_simt(dtype, kGated, a, env.num_sms, s));
 }
 

@@ -173,12 +173,9 @@ cudaError_t launch_rows_simt(int dtype, RowsMode mode, RowsArgs a, int num_sms,
                              cudaStream_t stream);
 
 // Tensor cores, many rows per group (16-bit, every width a multiple of 8, 16-byte aligned).
-cudaError_t launch_rows_wide(int dtype, RowsMode mode, RowsArgs a, int num_sms,
-                             cudaStream_t stream);
+cudaError_t launch_rows_wide(int dtype, RowsMode mode, RowsArgs a, int64_t live_blocks,
+                             int num_sms, cudaStream_t stream);
 int rows_wide_block();
-int rows_wide_smem();
-int rows_wide_threads();
-int rows_wide_stages();
 
 // Tensor cores, at most NR rows per block (kGated 16, 32, 64, 128; kShrink and kAdapt 16, 64).
 cudaError_t launch_rows_skinny(int dtype, RowsMode mode, int NR, RowsArgs a, int64_t live_blocks,

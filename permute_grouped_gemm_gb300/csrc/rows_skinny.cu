@@ -292,7 +292,9 @@ __device__ void mma_issuer(uint8_t* smem, Ctl<Cfg<NR, PANELS>::kStages>* ctl, ui
       }
       ptx::tc_fence_after_sync();
       const uint32_t sa = ptx::smem_addr(smem + stage * C::kStageBytes);
-      const uint64_t da = ptx::sdesc_sw128_mn(sa, C::kPanel);
+      // with one panel the upper 64 lanes read it again (and are not looked at): the operand stays
+      // inside its stage
+      const uint64_t da = ptx::sdesc_sw128_mn(sa, PANELS == 1 ? 0 : C::kPanel);
       const uint64_t db = ptx::sdesc_sw128(sa + C::kABytes);
 #pragma unroll
       for (int kk = 0; kk < C::kSub * kFK / 16; ++kk)

@@ -30,7 +30,7 @@
 // (it is an operand of the tensor cores), its sums are fp32.
 //
 // Warp roles per CTA: 0 TMA; 1 tensor-memory allocation and (even CTA) MMA
-// issue; one gather warp per stage slot; four epilogue warps. Tiles are
+// issue; one gather warp per stage slot; eight epilogue warps an MMA. Tiles are
 // statically interleaved over the clusters. Waits are bounded; when one runs
 // out the kernel records PGG_ERR_TIMEOUT, drains its copies and MMAs, frees
 // tensor memory and returns.
@@ -40,6 +40,7 @@
 
 #include <cstdint>
 #include <cstring>
+#include <cstdlib>
 
 #include "pgg_epilogue.cuh"
 #include "pgg_ops.h"
@@ -51,32 +52,44 @@ namespace pgg {
 namespace {
 
 constexpr int kFM = 128;   // rows per CTA (the pair's MMA M is 256)
-constexpr int kFN = 256;   // accumulator columns per tile (MMA N)
+constexpr int kFN = 256;   // MMA N
 constexpr int kFK = 64;    // reduction per stage: one 128-byte row of A
-constexpr int kStages = 7;
 constexpr int kPanel = kFK * 128;   // MN-major B panel: 64 k rows x 128 bytes (64 n)
 constexpr int kABytes = kFM * 128;  // A: 128 rows x 128 bytes
-constexpr int kBBytes = 2 * kPanel; // B: this CTA's 128 columns, either major
-constexpr int kStageBytes = kABytes + kBBytes;
-constexpr int kGatherWarps = kStages;
-constexpr int kEpiWarps = 4;
-constexpr int kEpiWarp0 = 2 + kGatherWarps;
-constexpr int kThreads = 32 * (kEpiWarp0 + kEpiWarps);
+constexpr int kHalfBytes = 2 * kPanel;  // B of one MMA: this CTA's 128 of the 256 columns
 constexpr int kTmemCols = 512;
-constexpr int kAccCols = 256;
+constexpr int kMaxStages = 7;
+
+// H = 1: tiles of 256 accumulator columns, two accumulators. H = 2: 512 columns, one accumulator.
+template <int H>
+struct Cfg {
+  static constexpr int kBBytes = H * kHalfBytes;
+  static constexpr int kStageBytes = kABytes + kBBytes;
+  static constexpr int kStages = H == 1 ? 7 : 4;
+  static constexpr int kGatherWarps = kStages;
+  // Eight epilogue warps an MMA: two share its lanes' quarter, each half of the columns. (They wait
+  // for their own loads most of the time; with four, the drain of a tile took 19,000 cycles.)
+  static constexpr int kEpiWarps = 8 * H;
+  static constexpr int kEpiWarp0 = 2 + kGatherWarps;
+  static constexpr int kThreads = 32 * (kEpiWarp0 + kEpiWarps);
+};
 
 struct WideCtl {
-  uint64_t full[kStages];   // even CTA: weight bytes of both CTAs + rows gathered in both
-  uint64_t empty[kStages];  // each CTA: MMAs of the stage done (multicast commit)
-  uint64_t tfull[2];        // each CTA: accumulator ready
-  uint64_t tempty[2];       // even CTA: accumulator drained (epilogue warps x 2 CTAs)
+  uint64_t full[kMaxStages];   // even CTA: weight bytes of both CTAs + rows gathered in both
+  uint64_t empty[kMaxStages];  // each CTA: MMAs of the stage done (multicast commit)
+  uint64_t tfull[2];           // each CTA: accumulator ready
+  uint64_t tempty[2];          // even CTA: accumulator drained (epilogue warps x 2 CTAs)
   uint64_t drain;
   uint32_t tmem_base;
   int abort;
 };
 
-constexpr int kSmemBytes = kStages * kStageBytes + static_cast<int>(sizeof(WideCtl)) + 1024;
-static_assert(kSmemBytes <= 227 * 1024, "shared memory per CTA");
+template <int H>
+constexpr int smem_bytes() {
+  return Cfg<H>::kStages * Cfg<H>::kStageBytes + static_cast<int>(sizeof(WideCtl)) + 1024;
+}
+static_assert(smem_bytes<1>() <= 227 * 1024 && smem_bytes<2>() <= 227 * 1024,
+              "shared memory per CTA");
 
 __device__ __forceinline__ uint32_t cluster_id() { return blockIdx.x >> 1; }
 __device__ __forceinline__ uint32_t n_clusters() { return gridDim.x >> 1; }
@@ -89,9 +102,10 @@ struct Tile {
   int32_t box[2];       // adapt: first token of each CTA's rows if they are neighbours, else -1
 };
 
-template <int MODE>
+template <int MODE, int H>
 struct Shape {
-  static constexpr int kTileN = MODE == kGated ? 128 : 256;  // output columns of a tile
+  static constexpr int kHalfN = MODE == kGated ? 128 : 256;  // output columns of one MMA
+  static constexpr int kTileN = H * kHalfN;
 };
 
 // Steps of the x W part, and per adapter segment.
@@ -100,11 +114,11 @@ __device__ __forceinline__ int main_steps(const RowsArgs& a) {
 }
 __device__ __forceinline__ int rank_steps(const RowsArgs& a) { return (a.R + kFK - 1) / kFK; }
 
-template <int MODE>
+template <int MODE, int H>
 __device__ __forceinline__ Tile tile_of(uint32_t t, const RowsArgs& a, uint32_t rank) {
   const uint32_t rb = t / static_cast<uint32_t>(a.n_blocks);
   Tile x;
-  x.n0 = static_cast<int64_t>(t - rb * static_cast<uint32_t>(a.n_blocks)) * Shape<MODE>::kTileN;
+  x.n0 = static_cast<int64_t>(t - rb * static_cast<uint32_t>(a.n_blocks)) * Shape<MODE, H>::kTileN;
   x.steps = main_steps(a);
   x.seg0 = 0;
   x.box[0] = x.box[1] = -1;
@@ -142,25 +156,36 @@ __device__ __forceinline__ int4 segment_of(const RowsArgs& a, const Tile& x, int
   return a.segs[x.seg0 + s];
 }
 
-// Weight bytes that CTA `rank` loads for one main or low-rank step of a tile.
+// First weight column of panel j (64 columns) of MMA h that CTA `rank` loads, as the output column
+// it belongs to (gated: both CTAs' panels belong to the same outputs).
 template <int MODE>
-__device__ __forceinline__ uint32_t w_bytes(const RowsArgs& a, int64_t n0, uint32_t rank,
-                                            bool low_rank) {
-  if constexpr (MODE == kGated) {
-    return n0 + 64 < a.N ? 2u * kPanel : static_cast<uint32_t>(kPanel);
-  } else {
-    const int64_t nc = n0 + 128 * rank;
-    if (MODE == kAdaptT || low_rank) return nc < a.N ? static_cast<uint32_t>(kBBytes) : 0u;
-    uint32_t b = 0;
-    for (int j = 0; j < 2; ++j) b += (nc + 64 * j < a.N) ? static_cast<uint32_t>(kPanel) : 0u;
-    return b;
-  }
+__device__ __forceinline__ int64_t panel_column(int64_t n0, int h, int j, uint32_t rank) {
+  return MODE == kGated ? n0 + 128 * h + 64 * j : n0 + 256 * h + 128 * rank + 64 * j;
 }
 
-template <int MODE>
+// Weight bytes that CTA `rank` loads for one main or low-rank step of a tile.
+template <int MODE, int H>
+__device__ __forceinline__ uint32_t w_bytes(const RowsArgs& a, int64_t n0, uint32_t rank,
+                                            bool low_rank) {
+  uint32_t b = 0;
+#pragma unroll
+  for (int h = 0; h < H; ++h) {
+    if (MODE == kAdaptT || low_rank) {
+      b += panel_column<MODE>(n0, h, 0, rank) < a.N ? static_cast<uint32_t>(kHalfBytes) : 0u;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        b += panel_column<MODE>(n0, h, j, rank) < a.N ? static_cast<uint32_t>(kPanel) : 0u;
+    }
+  }
+  return b;
+}
+
+template <int MODE, int H>
 __device__ void w_producer(uint8_t* smem, WideCtl* ctl, const CUtensorMap* tm_w,
                            const CUtensorMap* tm_b, const CUtensorMap* tm_x, const RowsArgs& a, uint32_t total,
                            uint32_t rank) {
+  using C = Cfg<H>;
   const uint64_t lim = a.wait_limit_ns;
   volatile int* abort = &ctl->abort;
   const bool leader = rank == 0;
@@ -169,8 +194,7 @@ __device__ void w_producer(uint8_t* smem, WideCtl* ctl, const CUtensorMap* tm_w,
   uint32_t phase = 0, outstanding = 0, last_parity = 0;
   bool failed = false;
   for (uint32_t t = cluster_id(); t < total && !failed; t += n_clusters()) {
-    const Tile x = tile_of<MODE>(t, a, rank);
-    const int64_t nc = x.n0 + 128 * rank;
+    const Tile x = tile_of<MODE, H>(t, a, rank);
     for (int ks = 0; ks < x.steps; ++ks) {
       const bool low = MODE != kGated && ks >= nks;
       int4 seg = make_int4(0, 0, 0, 0);
@@ -180,38 +204,38 @@ __device__ void w_producer(uint8_t* smem, WideCtl* ctl, const CUtensorMap* tm_w,
         failed = true;
         break;
       }
-      uint8_t* sb = smem + stage * kStageBytes + kABytes;
+      uint8_t* sb = smem + stage * C::kStageBytes + kABytes;
       const uint32_t fb = ptx::mapa(&ctl->full[stage], 0);
       if (leader) {
-        uint32_t bytes = w_bytes<MODE>(a, x.n0, 0, low) + w_bytes<MODE>(a, x.n0, 1, low);
+        uint32_t bytes = w_bytes<MODE, H>(a, x.n0, 0, low) + w_bytes<MODE, H>(a, x.n0, 1, low);
         if (MODE != kGated && !low)
           bytes += (x.box[0] >= 0 ? kABytes : 0) + (x.box[1] >= 0 ? kABytes : 0);
         ptx::mbar_arrive_expect_tx(&ctl->full[stage], bytes);
       }
-      if (MODE != kGated && !low && x.box[rank] >= 0)
-        ptx::tma_load_2d_pair(sb - kABytes, tm_x, fb, ks * kFK, x.box[rank]);
-      if constexpr (MODE == kGated) {
-        // the even CTA loads the gates' columns, the odd one the ups'
-        const int32_t c0 = static_cast<int32_t>(x.n0 + (rank ? a.N : 0));
-        for (int j = 0; j < 2; ++j)
-          if (x.n0 + 64 * j < a.N)
-            ptx::tma_load_3d_pair(sb + j * kPanel, tm_w, fb, c0 + 64 * j, ks * kFK,
-                                  static_cast<int32_t>(x.g));
-      } else if (low) {
-        if (nc < a.N)
-          ptx::tma_load_3d_pair(sb, tm_b, fb, r0, static_cast<int32_t>(nc), seg.x);
-      } else if constexpr (MODE == kAdaptT) {
-        if (nc < a.N)
-          ptx::tma_load_3d_pair(sb, tm_w, fb, ks * kFK, static_cast<int32_t>(nc), 0);
-      } else {
-        for (int j = 0; j < 2; ++j)
-          if (nc + 64 * j < a.N)
-            ptx::tma_load_3d_pair(sb + j * kPanel, tm_w, fb, static_cast<int32_t>(nc + 64 * j),
-                                  ks * kFK, 0);
+      if (MODE != kGated && !low && (rank ? x.box[1] : x.box[0]) >= 0)
+        ptx::tma_load_2d_pair(sb - kABytes, tm_x, fb, ks * kFK, (rank ? x.box[1] : x.box[0]));
+#pragma unroll
+      for (int h = 0; h < H; ++h) {
+        uint8_t* sh = sb + h * kHalfBytes;
+        const int64_t nc = panel_column<MODE>(x.n0, h, 0, rank);
+        if (low) {
+          if (nc < a.N) ptx::tma_load_3d_pair(sh, tm_b, fb, r0, static_cast<int32_t>(nc), seg.x);
+        } else if (MODE == kAdaptT) {
+          if (nc < a.N)
+            ptx::tma_load_3d_pair(sh, tm_w, fb, ks * kFK, static_cast<int32_t>(nc), 0);
+        } else {
+          // gated: the even CTA loads the gates' columns, the odd one the ups'
+          const int64_t shift = MODE == kGated && rank ? a.N : 0;
+          for (int j = 0; j < 2; ++j)
+            if (nc + 64 * j < a.N)
+              ptx::tma_load_3d_pair(sh + j * kPanel, tm_w, fb,
+                                    static_cast<int32_t>(nc + 64 * j + shift), ks * kFK,
+                                    static_cast<int32_t>(x.g));
+        }
       }
       outstanding |= 1u << stage;
       last_parity = (last_parity & ~(1u << stage)) | (phase << stage);
-      if (++stage == kStages) {
+      if (++stage == C::kStages) {
         stage = 0;
         phase ^= 1u;
       }
@@ -223,7 +247,7 @@ __device__ void w_producer(uint8_t* smem, WideCtl* ctl, const CUtensorMap* tm_w,
   }
   if (leader) {
     int no_abort = 0;
-    for (int s = 0; s < kStages; ++s)
+    for (int s = 0; s < C::kStages; ++s)
       if (outstanding & (1u << s))
         ptx::mbar_wait_cluster(&ctl->full[s], (last_parity >> s) & 1u, lim, &no_abort);
   }
@@ -231,16 +255,17 @@ __device__ void w_producer(uint8_t* smem, WideCtl* ctl, const CUtensorMap* tm_w,
 
 // Gather warp w fills stage slot w: the CTA's stages w, w + S, ... in the
 // sequence of all steps of all its tiles. Rows lane >> 3 + 4 q, 16-byte chunk lane & 7.
-template <int MODE>
+template <int MODE, int H>
 __device__ void x_gatherer(uint8_t* smem, WideCtl* ctl, const RowsArgs& a, uint32_t total,
                            uint32_t rank) {
+  using C = Cfg<H>;
   const uint64_t lim = a.wait_limit_ns;
   volatile int* abort = &ctl->abort;
   const int w = (threadIdx.x >> 5) - 2;
   const int lane = threadIdx.x & 31;
   const int c = lane & 7;
   const char* xb = static_cast<const char*>(a.x);
-  const uint32_t sa_slot = ptx::smem_addr(smem + w * kStageBytes);
+  const uint32_t sa_slot = ptx::smem_addr(smem + w * C::kStageBytes);
   const uint32_t full = ptx::mapa(&ctl->full[w], 0);
   const int nks = main_steps(a);
   uint32_t phase = 0;
@@ -252,7 +277,7 @@ __device__ void x_gatherer(uint8_t* smem, WideCtl* ctl, const RowsArgs& a, uint3
   const uint32_t row_units = static_cast<uint32_t>(a.K / 8);
   uint32_t row16[kFM / 4];
   for (uint32_t t = cluster_id(); t < total && !failed; t += n_clusters()) {
-    const Tile x = tile_of<MODE>(t, a, rank);
+    const Tile x = tile_of<MODE, H>(t, a, rank);
     if (kb < x.steps) {
       int32_t tok[4];
 #pragma unroll
@@ -270,12 +295,12 @@ __device__ void x_gatherer(uint8_t* smem, WideCtl* ctl, const RowsArgs& a, uint3
         row16[q] = tk >= 0 ? static_cast<uint32_t>(tk) * row_units : kNoRow;
       }
     }
-    for (; kb < x.steps; kb += kStages) {
+    for (; kb < x.steps; kb += C::kStages) {
       if (!ptx::mbar_wait_cluster(&ctl->empty[w], phase ^ 1u, lim, abort)) {
         failed = true;
         break;
       }
-      if (MODE != kGated && kb < nks && x.box[rank] >= 0) {
+      if (MODE != kGated && kb < nks && (rank ? x.box[1] : x.box[0]) >= 0) {
         // neighbouring rows: the weight's producer copies them as one box
       } else if (MODE == kGated || kb < nks) {
         const int64_t k = static_cast<int64_t>(kb) * kFK + c * 8;
@@ -341,9 +366,10 @@ __device__ __forceinline__ void lane_mask(int lo, int hi, uint32_t (&m)[8]) {
   }
 }
 
-template <int DT, int MODE>
+template <int DT, int MODE, int H>
 __device__ void mma_issuer(uint8_t* smem, WideCtl* ctl, uint32_t tmem_base, const RowsArgs& a,
                            uint32_t total) {
+  using C = Cfg<H>;
   constexpr uint32_t kFmt = DT == PGG_BF16 ? 1u : 0u;
   constexpr uint32_t idesc_k = ptx::idesc_make(kFmt, 2 * kFM, kFN);  // both operands K-major
   constexpr uint32_t idesc_mn = idesc_k | (1u << 16);                // B MN-major
@@ -354,13 +380,13 @@ __device__ void mma_issuer(uint8_t* smem, WideCtl* ctl, uint32_t tmem_base, cons
   uint32_t phase = 0, aph = 0;
   bool issued = false, failed = false;
   for (uint32_t t = cluster_id(); t < total && !failed; t += n_clusters()) {
-    const Tile x = tile_of<MODE>(t, a, 0);
+    const Tile x = tile_of<MODE, H>(t, a, 0);
     if (!ptx::mbar_wait_cluster(&ctl->tempty[acc], aph ^ 1u, lim, abort)) {
       failed = true;
       break;
     }
     ptx::tc_fence_after_sync();
-    const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * kAccCols);
+    const bool both = H == 2 && x.n0 + Shape<MODE, H>::kHalfN < a.N;  // any column in the second
     for (int ks = 0; ks < x.steps; ++ks) {
       const bool low = MODE != kGated && ks >= nks;
       int4 seg = make_int4(0, 0, 0, 0);
@@ -371,45 +397,51 @@ __device__ void mma_issuer(uint8_t* smem, WideCtl* ctl, uint32_t tmem_base, cons
         break;
       }
       ptx::tc_fence_after_sync();
-      const uint32_t sa = ptx::smem_addr(smem + stage * kStageBytes);
+      const uint32_t sa = ptx::smem_addr(smem + stage * C::kStageBytes);
       const uint64_t da = ptx::sdesc_sw128(sa);
-      if (low) {
-        const uint64_t db = ptx::sdesc_sw128(sa + kABytes);
-        uint32_t m[8];
-        lane_mask(static_cast<int>(seg.y - x.row0), static_cast<int>(seg.z - x.row0), m);
+      uint32_t m[8];
+      if (low) lane_mask(static_cast<int>(seg.y - x.row0), static_cast<int>(seg.z - x.row0), m);
 #pragma unroll
-        for (int kk = 0; kk < kFK / 16; ++kk)
-          if (r0 + 16 * kk < a.R) {
+      for (int h = 0; h < H; ++h) {
+        if (h == 1 && !both) continue;
+        const uint32_t d_tmem = tmem_base + static_cast<uint32_t>((H == 1 ? acc : h) * kFN);
+        const uint32_t sb = sa + kABytes + h * kHalfBytes;
+        if (low) {
+          const uint64_t db = ptx::sdesc_sw128(sb);
+#pragma unroll
+          for (int kk = 0; kk < kFK / 16; ++kk)
+            if (r0 + 16 * kk < a.R) {
+              const uint64_t off = static_cast<uint64_t>((kk * 32) >> 4);
+              mma_f16_pair_lanes(d_tmem, da + off, db + off, idesc_k, m, 1u);
+            }
+        } else if constexpr (MODE == kAdaptT) {
+          const uint64_t db = ptx::sdesc_sw128(sb);
+#pragma unroll
+          for (int kk = 0; kk < kFK / 16; ++kk) {
             const uint64_t off = static_cast<uint64_t>((kk * 32) >> 4);
-            mma_f16_pair_lanes(d_tmem, da + off, db + off, idesc_k, m, 1u);
+            ptx::mma_f16_pair(d_tmem, da + off, db + off, idesc_k, (ks > 0 || kk > 0) ? 1u : 0u);
           }
-      } else if constexpr (MODE == kAdaptT) {
-        const uint64_t db = ptx::sdesc_sw128(sa + kABytes);
+        } else {
+          const uint64_t db = ptx::sdesc_sw128_mn(sb, kPanel);
 #pragma unroll
-        for (int kk = 0; kk < kFK / 16; ++kk) {
-          const uint64_t off = static_cast<uint64_t>((kk * 32) >> 4);
-          ptx::mma_f16_pair(d_tmem, da + off, db + off, idesc_k, (ks > 0 || kk > 0) ? 1u : 0u);
-        }
-      } else {
-        const uint64_t db = ptx::sdesc_sw128_mn(sa + kABytes, kPanel);
-#pragma unroll
-        for (int kk = 0; kk < kFK / 16; ++kk) {
-          const uint64_t a_off = static_cast<uint64_t>((kk * 32) >> 4);        // 16 k: 32 bytes
-          const uint64_t b_off = static_cast<uint64_t>((kk * 16 * 128) >> 4);  // 16 k rows
-          ptx::mma_f16_pair(d_tmem, da + a_off, db + b_off, idesc_mn,
-                            (ks > 0 || kk > 0) ? 1u : 0u);
+          for (int kk = 0; kk < kFK / 16; ++kk) {
+            const uint64_t a_off = static_cast<uint64_t>((kk * 32) >> 4);        // 16 k: 32 bytes
+            const uint64_t b_off = static_cast<uint64_t>((kk * 16 * 128) >> 4);  // 16 k rows
+            ptx::mma_f16_pair(d_tmem, da + a_off, db + b_off, idesc_mn,
+                              (ks > 0 || kk > 0) ? 1u : 0u);
+          }
         }
       }
       issued = true;
       ptx::mma_commit_pair(&ctl->empty[stage], 0x3);
-      if (++stage == kStages) {
+      if (++stage == C::kStages) {
         stage = 0;
         phase ^= 1u;
       }
     }
     if (failed) break;
     ptx::mma_commit_pair(&ctl->tfull[acc], 0x3);
-    acc ^= 1;
+    if (H == 1) acc ^= 1;
     if (acc == 0) aph ^= 1u;
   }
   if (failed) {
@@ -420,6 +452,37 @@ __device__ void mma_issuer(uint8_t* smem, WideCtl* ctl, uint32_t tmem_base, cons
     int no_abort = 0;
     ptx::mma_commit_pair(&ctl->drain, 0x1);
     ptx::mbar_wait(&ctl->drain, 0u, lim, &no_abort);
+  }
+}
+
+// Each lane's own row, 64 columns from `taddr` on, as 128 bytes of 16-bit values. (16 columns at a
+// time: the epilogue's threads have 80 registers.)
+template <int DT>
+__device__ __forceinline__ void plain_blocks(uint32_t taddr, uint4 (&b)[8]) {
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    uint32_t v[16];
+    ptx::tmem_ld_32x32b_x16(taddr + 16u * q, v);
+    ptx::tmem_ld_wait();
+    b[2 * q] = pack8<DT>(v);
+    b[2 * q + 1] = pack8<DT>(v + 8);
+  }
+}
+
+// The same of the gated product of the columns from `taddr` on and those 128 further.
+template <int DT>
+__device__ __forceinline__ void gated_blocks(uint32_t taddr, float p, uint4 (&b)[8]) {
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    uint32_t g[16], u[16];
+    ptx::tmem_ld_32x32b_x16(taddr + 16u * q, g);
+    ptx::tmem_ld_32x32b_x16(taddr + 128u + 16u * q, u);
+    ptx::tmem_ld_wait();
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      u[i] = __float_as_uint(gate(__uint_as_float(g[i]), __uint_as_float(u[i]), p));
+    b[2 * q] = pack8<DT>(u);
+    b[2 * q + 1] = pack8<DT>(u + 8);
   }
 }
 
@@ -439,20 +502,25 @@ __device__ __forceinline__ void store_rows(uint4 (&b)[8], void* out, int64_t row
   }
 }
 
-template <int DT, int MODE>
+template <int DT, int MODE, int H>
 __device__ void epilogue(WideCtl* ctl, uint32_t tmem_base, const RowsArgs& a, uint32_t total,
                          uint32_t rank) {
   const uint64_t lim = a.wait_limit_ns;
   volatile int* abort = &ctl->abort;
   const int lane = threadIdx.x & 31;
   const int quarter = (threadIdx.x >> 5) & 3;  // accumulator lanes (rows) 32 q .. 32 q + 31
+  const int part = ((threadIdx.x >> 5) - Cfg<H>::kEpiWarp0) / 4;
+  const int h = part >> 1;  // H == 2: the MMA it drains
+  constexpr int kSpan = Shape<MODE, H>::kHalfN / 2;
+  const int col0 = (part & 1) * kSpan;  // its columns of that MMA's outputs
   const uint32_t tempty0 = ptx::mapa(&ctl->tempty[0], 0);
   const uint32_t tempty1 = ptx::mapa(&ctl->tempty[1], 0);
   int acc = 0;
   uint32_t aph = 0;
   bool held = a.hold_release != 0;  // (test hook: the first release is withheld)
   for (uint32_t t = cluster_id(); t < total; t += n_clusters()) {
-    const Tile x = tile_of<MODE>(t, a, rank);
+    const Tile x = tile_of<MODE, H>(t, a, rank);
+    const int64_t n0 = x.n0 + h * Shape<MODE, H>::kHalfN;
     const int valid = x.rows - 32 * quarter;  // rows of this warp's 32 that exist
     int64_t row = -1;                         // output row of this lane
     float p = 1.0f;
@@ -475,34 +543,22 @@ __device__ void epilogue(WideCtl* ctl, uint32_t tmem_base, const RowsArgs& a, ui
     }
     ptx::tc_fence_after_sync();
     const uint32_t t_lane = tmem_base + (static_cast<uint32_t>(32 * quarter) << 16) +
-                            static_cast<uint32_t>(acc * kAccCols);
+                            static_cast<uint32_t>((H == 1 ? acc : h) * kFN);
 #pragma unroll 1
-    for (int c0 = 0; c0 < Shape<MODE>::kTileN && x.n0 + c0 < a.N && valid > 0; c0 += 64) {
+    for (int c0 = col0; c0 < col0 + kSpan && n0 + c0 < a.N && valid > 0; c0 += 64) {
       uint4 b[8];
       if constexpr (MODE == kGated) {
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          uint32_t g[32], u[32];
-          ptx::tmem_ld_32x32b_x32(t_lane + static_cast<uint32_t>(c0 + 32 * half), g);
-          ptx::tmem_ld_32x32b_x32(t_lane + static_cast<uint32_t>(128 + c0 + 32 * half), u);
-          ptx::tmem_ld_wait_regs(g);
-          ptx::tmem_ld_wait_regs(u);
-#pragma unroll
-          for (int i = 0; i < 32; ++i)
-            u[i] = __float_as_uint(gate(__uint_as_float(g[i]), __uint_as_float(u[i]), p));
-#pragma unroll
-          for (int q = 0; q < 4; ++q) b[4 * half + q] = pack8<DT>(u + 8 * q);
-        }
-        store_rows(b, a.out, row, a.N, 0, x.n0 + c0, a.N, lane);
+        gated_blocks<DT>(t_lane + static_cast<uint32_t>(c0), p, b);
+        store_rows(b, a.out, row, a.N, 0, n0 + c0, a.N, lane);
         if (a.gate_up) {
-          chunk_blocks<DT>(t_lane + static_cast<uint32_t>(c0), false, b);
-          store_rows(b, a.gate_up, row, 2 * a.N, 0, x.n0 + c0, a.N, lane);
-          chunk_blocks<DT>(t_lane + static_cast<uint32_t>(128 + c0), false, b);
-          store_rows(b, a.gate_up, row, 2 * a.N, a.N, x.n0 + c0, a.N, lane);
+          plain_blocks<DT>(t_lane + static_cast<uint32_t>(c0), b);
+          store_rows(b, a.gate_up, row, 2 * a.N, 0, n0 + c0, a.N, lane);
+          plain_blocks<DT>(t_lane + static_cast<uint32_t>(128 + c0), b);
+          store_rows(b, a.gate_up, row, 2 * a.N, a.N, n0 + c0, a.N, lane);
         }
       } else {
-        chunk_blocks<DT>(t_lane + static_cast<uint32_t>(c0), false, b);
-        store_rows(b, a.out, row, a.N, 0, x.n0 + c0, a.N, lane);
+        plain_blocks<DT>(t_lane + static_cast<uint32_t>(c0), b);
+        store_rows(b, a.out, row, a.N, 0, n0 + c0, a.N, lane);
       }
     }
     ptx::tc_fence_before_sync();
@@ -511,21 +567,22 @@ __device__ void epilogue(WideCtl* ctl, uint32_t tmem_base, const RowsArgs& a, ui
     // not to the MMA thread): CTA scope
     if (lane == 0 && !held) ptx::mbar_arrive_remote_cta(acc ? tempty1 : tempty0);
     held = false;
-    acc ^= 1;
+    if (H == 1) acc ^= 1;
     if (acc == 0) aph ^= 1u;
   }
 }
 
-template <int DT, int MODE>
-__global__ void __launch_bounds__(kThreads, 1)
+template <int DT, int MODE, int H>
+__global__ void __launch_bounds__(Cfg<H>::kThreads, 1)
     rows_wide_kernel(const __grid_constant__ CUtensorMap tm_w,
                      const __grid_constant__ CUtensorMap tm_b,
                      const __grid_constant__ CUtensorMap tm_x, const RowsArgs a) {
+  using C = Cfg<H>;
   ptx::griddep_wait();  // launched with programmatic serialization: predecessors done
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
-  auto* ctl = reinterpret_cast<WideCtl*>(smem + kStages * kStageBytes);
+  auto* ctl = reinterpret_cast<WideCtl*>(smem + C::kStages * C::kStageBytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = ptx::cluster_ctarank();
 
@@ -539,13 +596,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t total = row_blocks * static_cast<uint32_t>(a.n_blocks);
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kStages; ++s) {
+    for (int s = 0; s < C::kStages; ++s) {
       ptx::mbar_init(&ctl->full[s], 3);
       ptx::mbar_init(&ctl->empty[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
       ptx::mbar_init(&ctl->tfull[b], 1);
-      ptx::mbar_init(&ctl->tempty[b], 2 * kEpiWarps);
+      ptx::mbar_init(&ctl->tempty[b], 2 * C::kEpiWarps);
     }
     ptx::mbar_init(&ctl->drain, 1);
     ctl->abort = 0;
@@ -567,13 +624,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem_base = ctl->tmem_base;
 
   if (warp == 0) {
-    if (lane == 0) w_producer<MODE>(smem, ctl, &tm_w, &tm_b, &tm_x, a, total, rank);
+    if (lane == 0) w_producer<MODE, H>(smem, ctl, &tm_w, &tm_b, &tm_x, a, total, rank);
   } else if (warp == 1) {
-    if (lane == 0 && rank == 0) mma_issuer<DT, MODE>(smem, ctl, tmem_base, a, total);
-  } else if (warp < kEpiWarp0) {
-    x_gatherer<MODE>(smem, ctl, a, total, rank);
-  } else {
-    epilogue<DT, MODE>(ctl, tmem_base, a, total, rank);
+    if (lane == 0 && rank == 0) mma_issuer<DT, MODE, H>(smem, ctl, tmem_base, a, total);
+  } else if (warp < 2 + C::kGatherWarps) {
+    x_gatherer<MODE, H>(smem, ctl, a, total, rank);
+  } else if (warp >= C::kEpiWarp0) {
+    epilogue<DT, MODE, H>(ctl, tmem_base, a, total, rank);
   }
 
   ptx::tc_fence_before_sync();
@@ -585,30 +642,35 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <int DT>
+template <int DT, int H>
 cudaError_t launch_t(RowsMode mode, const CUtensorMap (&tm)[3], const RowsArgs& a,
                      int64_t max_tiles, int num_sms, cudaStream_t stream) {
   using K = void (*)(const CUtensorMap, const CUtensorMap, const CUtensorMap, const RowsArgs);
-  const K kern = mode == kGated   ? K(rows_wide_kernel<DT, kGated>)
-                 : mode == kAdapt ? K(rows_wide_kernel<DT, kAdapt>)
-                                  : K(rows_wide_kernel<DT, kAdaptT>);
+  const K kern = mode == kGated   ? K(rows_wide_kernel<DT, kGated, H>)
+                 : mode == kAdapt ? K(rows_wide_kernel<DT, kAdapt, H>)
+                                  : K(rows_wide_kernel<DT, kAdaptT, H>);
   static ClusterLimits limits[3];
   int clusters = 0;
-  const cudaError_t err = clusters_that_fit(&limits[mode == kGated ? 0 : mode == kAdapt ? 1 : 2],
-                                            kern, kThreads, kSmemBytes, 2, num_sms, &clusters);
+  const cudaError_t err =
+      clusters_that_fit(&limits[mode == kGated ? 0 : mode == kAdapt ? 1 : 2], kern,
+                        Cfg<H>::kThreads, smem_bytes<H>(), 2, num_sms, &clusters);
   if (err != cudaSuccess) return err;
   const int64_t want = max_tiles < num_sms / 2 ? max_tiles : num_sms / 2;
   return launch_pdl(kern, dim3(static_cast<unsigned>(2 * (clusters < want ? clusters : want))),
-                    dim3(kThreads), static_cast<size_t>(kSmemBytes), stream, 2, tm[0], tm[1], tm[2],
-                    a);
+                    dim3(Cfg<H>::kThreads), static_cast<size_t>(smem_bytes<H>()), stream, 2, tm[0],
+                    tm[1], tm[2], a);
 }
 
 }  // namespace
 
-cudaError_t launch_rows_wide(int dtype, RowsMode mode, RowsArgs a, int num_sms,
-                             cudaStream_t stream) {
-  const int64_t tile_n = mode == kGated ? 128 : 256;
-  a.n_blocks = static_cast<int32_t>((a.N + tile_n - 1) / tile_n);
+// live_blocks: about how many row blocks there will be (the choice of the tile goes by it, nothing
+// else).
+cudaError_t launch_rows_wide(int dtype, RowsMode mode, RowsArgs a, int64_t live_blocks,
+                             int num_sms, cudaStream_t stream) {
+  const int64_t half_n = mode == kGated ? 128 : 256;
+  const int64_t row_blocks = mode == kGated ? a.max_row_blocks : (a.M + 2 * kFM - 1) / (2 * kFM);
+  int H = getenv("PGG_H") ? atoi(getenv("PGG_H")) : 2;
+  a.n_blocks = static_cast<int32_t>((a.N + H * half_n - 1) / (H * half_n));
   CUtensorMap tm[3];  // weight, b, x
   std::memset(tm, 0, sizeof(tm));
   bool ok;
@@ -622,16 +684,16 @@ cudaError_t launch_rows_wide(int dtype, RowsMode mode, RowsArgs a, int num_sms,
     ok = ok && encode_map_3d(&tm[1], dtype, a.b, a.R, a.N, a.G, 128) &&
          encode_map_rows(&tm[2], dtype, a.x, a.K, a.batch, kFM);
   if (!ok) return cudaErrorInvalidValue;
-  const int64_t row_blocks = mode == kGated ? a.max_row_blocks : (a.M + 2 * kFM - 1) / (2 * kFM);
   const int64_t tiles = row_blocks * a.n_blocks;
-  if (dtype == PGG_BF16) return launch_t<PGG_BF16>(mode, tm, a, tiles, num_sms, stream);
-  if (dtype == PGG_F16) return launch_t<PGG_F16>(mode, tm, a, tiles, num_sms, stream);
+  if (dtype == PGG_BF16)
+    return H == 2 ? launch_t<PGG_BF16, 2>(mode, tm, a, tiles, num_sms, stream)
+                  : launch_t<PGG_BF16, 1>(mode, tm, a, tiles, num_sms, stream);
+  if (dtype == PGG_F16)
+    return H == 2 ? launch_t<PGG_F16, 2>(mode, tm, a, tiles, num_sms, stream)
+                  : launch_t<PGG_F16, 1>(mode, tm, a, tiles, num_sms, stream);
   return cudaErrorInvalidValue;
 }
 
 int rows_wide_block() { return 2 * kFM; }
-int rows_wide_smem() { return kSmemBytes; }
-int rows_wide_threads() { return kThreads; }
-int rows_wide_stages() { return kStages; }
 
 }  // namespace pgg

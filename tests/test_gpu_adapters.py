@@ -83,7 +83,7 @@ def check(s):
 # (T, K, N, R, A): a single token, a decode batch, odd and ragged sizes, several row blocks
 SIZES = [(1, 64, 64, 8, 1), (1, 1024, 512, 16, 8), (7, 200, 136, 16, 3), (48, 512, 264, 16, 64),
          (65, 128, 256, 64, 5), (300, 264, 520, 24, 4), (513, 192, 192, 32, 20),
-         (40, 100, 50, 5, 6), (600, 321, 77, 7, 9), (33, 64, 128, 256, 4), (1000, 96, 72, 1, 1)]
+         (200, 4096, 264, 16, 24), (90, 2048, 136, 72, 30), (40, 100, 50, 5, 6), (600, 321, 77, 7, 9), (33, 64, 128, 256, 4), (1000, 96, 72, 1, 1)]
 
 
 @pytest.mark.parametrize("ids", ["mixed", "runs"])
