@@ -21,10 +21,20 @@ constexpr int kVariantSkinny = 1;  // tensor cores, few rows per block, the weig
 constexpr int kVariantSimt = 3;  // FP32 pipes: any dtype, size and alignment
 
 // Gated product: up to this many rows per live expert the weights bound it and are streamed once
-// per block of rows; beyond, the tensor cores do.
-constexpr double kSkinnyRows = 64.0;
-// Adapters: up to this many tokens the shared weight is streamed once for all of them.
-constexpr int64_t kSkinnyTokens = 64;
+// per block of rows; beyond, the tensor cores do. (60 experts, K 4096, F 1024: 96 rows each take
+// 185 us this way and 210 in blocks of 256 rows, 128 rows 230 and 214; 32 experts, K 7168, F 2048:
+// 302 and 363, 411 and 366.)
+constexpr double kSkinnyRows = 104.0;
+
+// Adapters: whether the shared weight is streamed for blocks of 64 tokens in the caller's order,
+// with the low-rank part on the FP32 pipes (its cost grows with T R). (64 adapters mixed; K 7168,
+// N 4096, R 16: 256 tokens take 52 us this way and 111 in sorted blocks of 256; K = N = 4096, R 64:
+// 128 tokens 62 and 86, 192 tokens 95 and 90.) Beyond one block of tokens only while the tiles of 64
+// tokens x 128 columns fit the 152 SMs at once (K 2048, N 5120: 192 tokens 35 and 36, 256 53 and 37).
+bool few_tokens(int64_t T, int64_t N, int64_t R) {
+  return T <= 256 && T * R <= 8192 &&
+         (T <= 64 || (T + 63) / 64 * ((N + 127) / 128) <= 152);
+}
 
 size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
@@ -144,7 +154,7 @@ int adapter_plan(int64_t T, int64_t K, int64_t N, int64_t R, int64_t A, int dtyp
   p->rb = 64;
   if (forced != kVariantSimt && R % 8 == 0 && tensor_sizes(dtype, T, K, N) &&
       tensor_sizes(dtype, T, N, K)) {
-    p->variant = !grad && (forced == kVariantSkinny || (forced != kVariantWide && T <= kSkinnyTokens))
+    p->variant = !grad && (forced == kVariantSkinny || (forced != kVariantWide && few_tokens(T, N, R)))
                      ? kVariantSkinny
                      : kVariantWide;
     // low-rank rows: blocks of 16 when adapters have about that many tokens
@@ -283,7 +293,7 @@ int run_adapt(const AdapterPlan& p, const AdapterTables& t, const HostEnv& env, 
   const RowsMode mode = transposed ? kAdaptT : kAdapt;
   if (by_token) {
     a.adapter = by_token;
-    const int nr = T <= 16 ? 16 : 64;
+    const int nr = T <= 16 ? 16 : T <= 32 ? 32 : 64;
     return status_of(launch_rows_skinny(dtype, mode, nr, a, (T + nr - 1) / nr, env.num_sms,
                                         stream));
   }

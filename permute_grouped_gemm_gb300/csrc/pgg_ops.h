@@ -177,7 +177,7 @@ cudaError_t launch_rows_wide(int dtype, RowsMode mode, RowsArgs a, int64_t live_
                              int num_sms, cudaStream_t stream);
 int rows_wide_block();
 
-// Tensor cores, at most NR rows per block (kGated 16, 32, 64, 128; kShrink and kAdapt 16, 64).
+// Tensor cores, at most NR rows per block (kGated 16, 32, 64, 128; kShrink 16, 64; kAdapt 16, 32, 64).
 cudaError_t launch_rows_skinny(int dtype, RowsMode mode, int NR, RowsArgs a, int64_t live_blocks,
                                int num_sms, cudaStream_t stream);
 

@@ -409,40 +409,54 @@ __device__ __forceinline__ void low_rank(const RowsArgs& a, const Tile& x, int j
   int ids = -1;
   if (lane < LR && warp + kEpiWarps * lane < n)
     ids = static_cast<int>(a.adapter[x.row0 + j0 + warp + kEpiWarps * lane]);
+  const bool col = x.n0 + 4 * lane < a.N;
 #pragma unroll
-  for (int q = 0; q < LR; ++q) {
+  for (int q0 = 0; q0 < LR; q0 += 2) {  // two rows' loads at a time: latency is what this costs
 #pragma unroll
-    for (int i = 0; i < 4; ++i) lr[q][i] = 0.0f;
-    const int j = warp + kEpiWarps * q;
-    const int64_t row = x.row0 + j0 + j;
-    const int64_t ad = __shfl_sync(0xFFFFFFFFu, ids, q);
-    if (ad < 0 || ad >= a.G) continue;
-    const float* u = static_cast<const float*>(a.u) + row * a.R;
-    const char* b = static_cast<const char*>(a.b) + ((ad * a.N + x.n0) * a.R) * 2;
+    for (int q = q0; q < q0 + 2; ++q)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) lr[q][i] = 0.0f;
+    if (warp + kEpiWarps * q0 >= n) continue;
+    const float* u[2];
+    const char* b[2];
+    bool on[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int64_t ad = __shfl_sync(0xFFFFFFFFu, ids, q0 + e);
+      on[e] = ad >= 0 && ad < a.G;  // (-1 past the rows)
+      u[e] = static_cast<const float*>(a.u) + (x.row0 + j0 + warp + kEpiWarps * (q0 + e)) * a.R;
+      b[e] = static_cast<const char*>(a.b) + (((on[e] ? ad : 0) * a.N + x.n0 + 4 * lane) * a.R) * 2;
+    }
 #pragma unroll 2
     for (int r0 = 0; r0 < a.R; r0 += 8) {
-      const float4 ua = __ldcg(reinterpret_cast<const float4*>(u + r0));
-      const float4 ub = __ldcg(reinterpret_cast<const float4*>(u + r0 + 4));
-      uint4 w[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        w[i] = make_uint4(0, 0, 0, 0);
-        if (x.n0 + 4 * lane < a.N)
-          w[i] = __ldg(reinterpret_cast<const uint4*>(
-              b + (static_cast<int64_t>(4 * lane + i) * a.R + r0) * 2));
-      }
+      for (int e = 0; e < 2; ++e) {
+        float4 ua = make_float4(0.0f, 0.0f, 0.0f, 0.0f), ub = ua;
+        uint4 w[4];
+        if (on[e]) {
+          ua = __ldcg(reinterpret_cast<const float4*>(u[e] + r0));
+          ub = __ldcg(reinterpret_cast<const float4*>(u[e] + r0 + 4));
+        }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 b0 = unpack2<DT>(w[i].x), b1 = unpack2<DT>(w[i].y);
-        const float2 b2 = unpack2<DT>(w[i].z), b3 = unpack2<DT>(w[i].w);
-        lr[q][i] = fmaf(ua.x, b0.x, lr[q][i]);
-        lr[q][i] = fmaf(ua.y, b0.y, lr[q][i]);
-        lr[q][i] = fmaf(ua.z, b1.x, lr[q][i]);
-        lr[q][i] = fmaf(ua.w, b1.y, lr[q][i]);
-        lr[q][i] = fmaf(ub.x, b2.x, lr[q][i]);
-        lr[q][i] = fmaf(ub.y, b2.y, lr[q][i]);
-        lr[q][i] = fmaf(ub.z, b3.x, lr[q][i]);
-        lr[q][i] = fmaf(ub.w, b3.y, lr[q][i]);
+        for (int i = 0; i < 4; ++i) {
+          w[i] = make_uint4(0, 0, 0, 0);
+          if (on[e] && col)
+            w[i] = __ldg(reinterpret_cast<const uint4*>(b[e] + (i * a.R + r0) * 2));
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float& v = lr[q0 + e][i];
+          const float2 b0 = unpack2<DT>(w[i].x), b1 = unpack2<DT>(w[i].y);
+          const float2 b2 = unpack2<DT>(w[i].z), b3 = unpack2<DT>(w[i].w);
+          v = fmaf(ua.x, b0.x, v);
+          v = fmaf(ua.y, b0.y, v);
+          v = fmaf(ua.z, b1.x, v);
+          v = fmaf(ua.w, b1.y, v);
+          v = fmaf(ub.x, b2.x, v);
+          v = fmaf(ub.y, b2.y, v);
+          v = fmaf(ub.z, b3.x, v);
+          v = fmaf(ub.w, b3.y, v);
+        }
       }
     }
   }
@@ -691,6 +705,7 @@ cudaError_t launch_mode(RowsMode mode, int NR, const CUtensorMap (&m)[2], const 
     if (NR == 64) return launch_t<DT, kShrink, 64, 2>(m, a, tiles, sms, st);
   } else if (mode == kAdapt) {
     if (NR == 16) return launch_t<DT, kAdapt, 16, 2>(m, a, tiles, sms, st);
+    if (NR == 32) return launch_t<DT, kAdapt, 32, 2>(m, a, tiles, sms, st);
     if (NR == 64) return launch_t<DT, kAdapt, 64, 2>(m, a, tiles, sms, st);
   }
   return cudaErrorInvalidValue;

@@ -6,13 +6,13 @@
 //
 // Tile: 256 rows x 256 accumulator columns on a pair of CTAs (cta_group::2),
 // reduced 64 at a time through seven stage slots; CTA r owns rows 128 r .. 128 r
-// + 127, whose fp32 accumulators (two buffers) sit in its tensor memory. The
+// + 127, whose fp32 accumulators (two buffers) sit in its tensor memory. (Or 512
+// columns, four slots and one accumulator: see choose_halves.) The
 // weights come by TMA. The rows of x are gathered by token with 16-byte
 // cp.async, one warp per stage slot; where a CTA's rows are neighbouring tokens
-// (adapt: requests one after another) they come as one TMA box instead, which
-// does not share the gathers' limit (a multiprocessor keeps about 30 KB of
-// cp.async in flight whatever the slots: 0.39 us a step against 0.27). TMA's own
-// gather of four rows is no way out: 75 cycles an instruction, 1.2 us a step.
+// (adapt: requests one after another) they come as one TMA box instead (714
+// cycles a step against 753). TMA's own gather of four rows is no way out: 75
+// cycles an instruction, 2.5 times the whole product's time.
 //
 // gated: 128 of the accumulator's columns are gates and the other 128 the ups
 // that belong to them (each CTA loads one of the two operands), so a thread of
@@ -40,7 +40,6 @@
 
 #include <cstdint>
 #include <cstring>
-#include <cstdlib>
 
 #include "pgg_epilogue.cuh"
 #include "pgg_ops.h"
@@ -642,6 +641,24 @@ __global__ void __launch_bounds__(Cfg<H>::kThreads, 1)
   }
 }
 
+// Tiles of 256 or of 512 accumulator columns: the form whose busiest pair of CTAs has the fewer
+// cycles. A 64-k step takes about 720 with 256 columns and 1180 with 512 (measured; the wider tile
+// reads a quarter less per product, and what L2 delivers, 40 to 45 bytes a cycle and SM, is the
+// limit in both). With 512 columns there is one accumulator, so nothing hides a tile's output:
+// 13,000 cycles with gate_up, 7,300 for h alone, 5,200 for y. Both sides: 13,500 tokens x 8, 60
+// experts, K 7168, F 2048: 4.45 ms and 4.13; 4096 x 8, 16 experts, K 2048, F 1024: 198 us and 238;
+// adapters, K = N = 4096, 2048 tokens: 79 and 71 us, 8191: 203 and 206.
+int choose_halves(RowsMode mode, const RowsArgs& a, int64_t row_blocks, int pairs) {
+  const int64_t half_n = mode == kGated ? 128 : 256;
+  const int64_t steps = (a.K + kFK - 1) / kFK;
+  const int64_t drain = mode != kGated ? 5200 : a.gate_up ? 13000 : 7300;
+  const int64_t n1 = row_blocks * ((a.N + half_n - 1) / half_n);
+  const int64_t n2 = row_blocks * ((a.N + 2 * half_n - 1) / (2 * half_n));
+  const int64_t one = (n1 + pairs - 1) / pairs * (steps * 720 > drain ? steps * 720 : drain);
+  const int64_t two = (n2 + pairs - 1) / pairs * (steps * 1180 + drain);
+  return two < one ? 2 : 1;
+}
+
 template <int DT, int H>
 cudaError_t launch_t(RowsMode mode, const CUtensorMap (&tm)[3], const RowsArgs& a,
                      int64_t max_tiles, int num_sms, cudaStream_t stream) {
@@ -669,7 +686,7 @@ cudaError_t launch_rows_wide(int dtype, RowsMode mode, RowsArgs a, int64_t live_
                              int num_sms, cudaStream_t stream) {
   const int64_t half_n = mode == kGated ? 128 : 256;
   const int64_t row_blocks = mode == kGated ? a.max_row_blocks : (a.M + 2 * kFM - 1) / (2 * kFM);
-  int H = getenv("PGG_H") ? atoi(getenv("PGG_H")) : 2;
+  const int H = choose_halves(mode, a, mode == kGated ? live_blocks : row_blocks, num_sms / 2);
   a.n_blocks = static_cast<int32_t>((a.N + H * half_n - 1) / (H * half_n));
   CUtensorMap tm[3];  // weight, b, x
   std::memset(tm, 0, sizeof(tm));
