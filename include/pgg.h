@@ -543,6 +543,17 @@ int pgg_swiglu_execute(const void* x, const void* weight, const int64_t* expande
                        void* h, void* gate_up, pgg_stream_t stream);
 
 /*
+ * How pgg_swiglu_execute runs these sizes with 16-byte aligned tensors (16-bit
+ * dtypes with K and F multiples of 8, else, and for other tensors, variant 3):
+ * variant 0 (tensor cores, row blocks of up to 256 rows on CTA pairs), 1
+ * (tensor cores, row blocks of up to 16 .. 128 rows, the weight streamed: few
+ * rows per expert) or 3 (FP32 pipes: any dtype, size and alignment). The
+ * fields not named here are 0. Host only, no CUDA call.
+ */
+int pgg_swiglu_plan(int64_t M, int64_t F, int64_t K, int64_t G, int64_t L, int64_t batch,
+                    int64_t topK, int rowIdxType, pgg_dtype dtype, pgg_plan_info* info);
+
+/*
  * Gradient of the gate, from d_h and the kept gate_up:
  *
  *     d_up = prob d_h silu(gate);  d_gate = prob d_h up silu'(gate)
@@ -593,6 +604,16 @@ int pgg_adapters_execute(const void* x, const void* weight, const void* a, const
                          const int64_t* adapter, const float* scale, int64_t T, int64_t K,
                          int64_t N, int64_t R, int64_t A, pgg_dtype dtype, void* workspace,
                          size_t workspace_bytes, void* y, pgg_stream_t stream);
+
+/*
+ * How pgg_adapters_execute runs these sizes with 16-byte aligned tensors:
+ * variant 0 (tensor cores, tokens sorted by adapter, blocks of 256), 1 (tensor
+ * cores, blocks of up to 64 tokens in the caller's order, the weight streamed
+ * and the low-rank part on the FP32 pipes) or 3 (FP32 pipes); rows_per_block is
+ * that of the projection, max_row_blocks counts the low-rank rows' blocks.
+ */
+int pgg_adapters_plan(int64_t T, int64_t K, int64_t N, int64_t R, int64_t A, pgg_dtype dtype,
+                      pgg_plan_info* info);
 
 /*
  * Its gradient with the projection frozen:

@@ -12,9 +12,9 @@ from __future__ import annotations
 from ._lib import (  # noqa: F401
     CODES, PGG_BF16, PGG_F16, PGG_F32, PGG_SCORE_SIGMOID, PGG_SCORE_SOFTMAX, STATUS, PggError,
     load, pgg_adapters_execute, pgg_adapters_grad, pgg_adapters_grad_workspace_size,
-    pgg_adapters_workspace_size, pgg_route_execute, pgg_route_grad, pgg_route_workspace_size,
+    pgg_adapters_plan, pgg_adapters_workspace_size, pgg_route_execute, pgg_route_grad, pgg_route_workspace_size,
     pgg_swiglu_execute, pgg_swiglu_grad, pgg_swiglu_grad_workspace_size,
-    pgg_swiglu_workspace_size,
+    pgg_swiglu_plan, pgg_swiglu_workspace_size,
     pgg_debug_force_variant, pgg_debug_set_band_k_blocks, pgg_debug_set_hold_release,
     pgg_debug_set_ticket_bias, pgg_debug_set_wait_limit_ns,
     pgg_dw_execute, pgg_dw_grouped_gemm, pgg_dw_plan, pgg_dw_workspace_size,
@@ -306,8 +306,8 @@ def swiglu(x, weight, expanded_row_idx, group_list, batch: int, top_k: int, row_
     _is("gate_up", gate_up, (M, F2), x.dtype)
     dt = dtype_code(x.dtype)
     if workspace is None:
-        workspace = torch.empty(pgg_swiglu_workspace_size(M, F, K, G, M, batch, top_k, row_idx_type, dt),
-                                dtype=torch.uint8, device=dev)
+        need = pgg_swiglu_workspace_size(M, F, K, G, M, batch, top_k, row_idx_type, dt)
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     if out is None:
         out = torch.empty(M, F, dtype=x.dtype, device=dev)
     if keep and gate_up is None:

@@ -103,18 +103,20 @@ def load(path: str | None = None):
                                               sz, vp, vp, vp, vp, vp]
             lib.pgg_route_grad.argtypes = [vp, vp, vp, i64, i64, i64, i32, i32, i32, f32, vp, vp]
             lib.pgg_swiglu_workspace_size.argtypes = [*_SIZES, i32, i32, ctypes.POINTER(sz)]
+            lib.pgg_swiglu_plan.argtypes = [*_SIZES, i32, i32, ctypes.POINTER(PlanInfo)]
             lib.pgg_swiglu_execute.argtypes = [vp] * 5 + [*_SIZES, i32, i32, vp, sz, vp, vp, vp]
             lib.pgg_swiglu_grad_workspace_size.argtypes = [i64] * 3 + [ctypes.POINTER(sz)]
             lib.pgg_swiglu_grad.argtypes = [vp] * 4 + [i64] * 4 + [i32, i32, vp, sz, vp, vp, vp,
                                                                    vp]
             lib.pgg_adapters_workspace_size.argtypes = [i64] * 5 + [i32, ctypes.POINTER(sz)]
+            lib.pgg_adapters_plan.argtypes = [i64] * 5 + [i32, ctypes.POINTER(PlanInfo)]
             lib.pgg_adapters_execute.argtypes = [vp] * 6 + [i64] * 5 + [i32, vp, sz, vp, vp]
             lib.pgg_adapters_grad_workspace_size.argtypes = [i64] * 5 + [i32, ctypes.POINTER(sz)]
             lib.pgg_adapters_grad.argtypes = [vp] * 7 + [i64] * 5 + [i32, vp, sz, vp, vp, vp, vp]
             for f in ("pgg_route_workspace_size", "pgg_route_execute", "pgg_route_grad",
-                      "pgg_swiglu_workspace_size", "pgg_swiglu_execute",
+                      "pgg_swiglu_workspace_size", "pgg_swiglu_plan", "pgg_swiglu_execute",
                       "pgg_swiglu_grad_workspace_size", "pgg_swiglu_grad",
-                      "pgg_adapters_workspace_size", "pgg_adapters_execute",
+                      "pgg_adapters_workspace_size", "pgg_adapters_plan", "pgg_adapters_execute",
                       "pgg_adapters_grad_workspace_size", "pgg_adapters_grad"):
                 getattr(lib, f).restype = ctypes.c_int
             lib.pgg_status_string.argtypes = [ctypes.c_int]
@@ -311,6 +313,13 @@ def pgg_swiglu_workspace_size(M, F, K, G, L, batch, topK, rowIdxType, dtype) -> 
     return out.value
 
 
+def pgg_swiglu_plan(M, F, K, G, L, batch, topK, rowIdxType, dtype) -> dict:
+    info = PlanInfo()
+    _check(load().pgg_swiglu_plan(M, F, K, G, L, batch, topK, rowIdxType, dtype,
+                                  ctypes.byref(info)), "pgg_swiglu_plan")
+    return info.as_dict()
+
+
 def pgg_swiglu_execute(x, weight, expandedRowIdx, groupList, probs, M, F, K, G, L, batch, topK,
                        rowIdxType, dtype, workspace, workspace_bytes, h, gate_up, stream) -> int:
     """Raw call with integer device addresses (0 for absent probs or gate_up)."""
@@ -339,6 +348,13 @@ def pgg_adapters_workspace_size(T, K, N, R, A, dtype) -> int:
     _check(load().pgg_adapters_workspace_size(T, K, N, R, A, dtype, ctypes.byref(out)),
            "pgg_adapters_workspace_size")
     return out.value
+
+
+def pgg_adapters_plan(T, K, N, R, A, dtype) -> dict:
+    info = PlanInfo()
+    _check(load().pgg_adapters_plan(T, K, N, R, A, dtype, ctypes.byref(info)),
+           "pgg_adapters_plan")
+    return info.as_dict()
 
 
 def pgg_adapters_execute(x, weight, a, b, adapter, scale, T, K, N, R, A, dtype, workspace,

@@ -36,6 +36,8 @@ bool few_tokens(int64_t T, int64_t N, int64_t R) {
          (T <= 64 || (T + 63) / 64 * ((N + 127) / 128) <= 152);
 }
 
+int few_token_block(int64_t T) { return T <= 16 ? 16 : T <= 32 ? 32 : 64; }
+
 size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 bool known_dtype(int d) { return d == PGG_F32 || d == PGG_F16 || d == PGG_BF16; }
@@ -109,8 +111,10 @@ int gated_plan(int64_t M, int64_t F, int64_t K, int64_t G, int64_t batch, int dt
                      : kVariantSkinny;
     p->rows_per_block = rows_wide_block();
     if (p->variant == kVariantSkinny) {
-      // room for twice the even share, but an expert has at most one row of a token
-      const double want = 2.0 * rows < static_cast<double>(batch) ? 2.0 * rows : batch;
+      // room for the even share and what an even draw adds to it in all but 0.3% of the experts
+      // (their rows take a second block), but an expert has at most one row of a token
+      const double most = rows + 2.8 * std::sqrt(rows);
+      const double want = most < static_cast<double>(batch) ? most : static_cast<double>(batch);
       p->rows_per_block = want <= 16 ? 16 : want <= 32 ? 32 : want <= 64 ? 64 : 128;
     }
     p->live_blocks = static_cast<int64_t>(live * std::ceil(rows / p->rows_per_block) + 0.5);
@@ -293,7 +297,7 @@ int run_adapt(const AdapterPlan& p, const AdapterTables& t, const HostEnv& env, 
   const RowsMode mode = transposed ? kAdaptT : kAdapt;
   if (by_token) {
     a.adapter = by_token;
-    const int nr = T <= 16 ? 16 : T <= 32 ? 32 : 64;
+    const int nr = few_token_block(T);
     return status_of(launch_rows_skinny(dtype, mode, nr, a, (T + nr - 1) / nr, env.num_sms,
                                         stream));
   }
@@ -394,6 +398,23 @@ int pgg_swiglu_workspace_size(int64_t M, int64_t F, int64_t K, int64_t G, int64_
   rc = gated_plan(M, F, K, G, batch, dtype, &p);
   if (rc != PGG_OK) return rc;
   *workspace_bytes = p.total;
+  return PGG_OK;
+}
+
+int pgg_swiglu_plan(int64_t M, int64_t F, int64_t K, int64_t G, int64_t L, int64_t batch,
+                    int64_t topK, int rowIdxType, pgg_dtype dtype, pgg_plan_info* info) {
+  if (!info) return PGG_ERR_NULL;
+  int rc = check_gated(M, F, K, G, L, batch, topK, rowIdxType, dtype);
+  if (rc != PGG_OK) return rc;
+  GatedPlan p;
+  rc = gated_plan(M, F, K, G, batch, dtype, &p);
+  if (rc != PGG_OK) return rc;
+  std::memset(info, 0, sizeof(*info));
+  info->variant = p.variant;
+  info->rows_per_block = p.rows_per_block;
+  info->max_row_blocks = p.max_row_blocks;
+  info->workspace_bytes = p.total;
+  info->cta_pair = p.variant == kVariantWide ? 1 : 0;
   return PGG_OK;
 }
 
@@ -519,6 +540,25 @@ int pgg_adapters_workspace_size(int64_t T, int64_t K, int64_t N, int64_t R, int6
   rc = adapter_plan(T, K, N, R, A, dtype, false, &p);
   if (rc != PGG_OK) return rc;
   *workspace_bytes = p.total;
+  return PGG_OK;
+}
+
+int pgg_adapters_plan(int64_t T, int64_t K, int64_t N, int64_t R, int64_t A, pgg_dtype dtype,
+                      pgg_plan_info* info) {
+  if (!info) return PGG_ERR_NULL;
+  int rc = check_adapters(T, K, N, R, A, dtype);
+  if (rc != PGG_OK) return rc;
+  AdapterPlan p;
+  rc = adapter_plan(T, K, N, R, A, dtype, false, &p);
+  if (rc != PGG_OK) return rc;
+  std::memset(info, 0, sizeof(*info));
+  info->variant = p.variant;
+  info->rows_per_block = p.variant == kVariantWide     ? rows_wide_block()
+                         : p.variant == kVariantSkinny ? few_token_block(T)
+                                                       : p.rb;
+  info->max_row_blocks = p.max_row_blocks;
+  info->workspace_bytes = p.total;
+  info->cta_pair = p.variant == kVariantWide ? 1 : 0;
   return PGG_OK;
 }
 

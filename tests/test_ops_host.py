@@ -141,3 +141,31 @@ def test_wrappers_refuse_host_tensors():
     with pytest.raises(ValueError):
         pgg.adapters(x, torch.zeros(8, 4), torch.zeros(1, 8, 2), torch.zeros(1, 4, 2),
                      torch.zeros(4, dtype=torch.int64))
+
+
+def test_plans():
+    def gated(tokens, k, G, K, F, dt):
+        return pgg.pgg_swiglu_plan(tokens * k, F, K, G, tokens * k, tokens, k, 0, dt)
+
+    p = gated(13500, 8, 60, 7168, 2048, pgg.PGG_BF16)
+    assert p["variant"] == 0 and p["rows_per_block"] == 256 and p["cta_pair"] == 1
+    p = gated(1, 8, 60, 7168, 2048, pgg.PGG_BF16)       # one row an expert
+    assert p["variant"] == 1 and p["rows_per_block"] == 16
+    p = gated(256, 8, 256, 7168, 2048, pgg.PGG_F16)     # eight on average
+    assert p["variant"] == 1 and p["rows_per_block"] == 16
+    p = gated(700, 8, 60, 7168, 2048, pgg.PGG_BF16)     # 93 on average
+    assert p["variant"] == 1 and p["rows_per_block"] == 128
+    assert gated(900, 8, 60, 7168, 2048, pgg.PGG_BF16)["variant"] == 0
+    for K, F, dt in ((7168, 2048, pgg.PGG_F32), (7167, 2048, pgg.PGG_BF16), (64, 36, pgg.PGG_F16)):
+        assert gated(64, 4, 8, K, F, dt)["variant"] == 3
+
+    def adapters(T, K=4096, N=4096, R=16, A=8, dt=pgg.PGG_BF16):
+        return pgg.pgg_adapters_plan(T, K, N, R, A, dt)
+
+    assert [adapters(T)["rows_per_block"] for T in (1, 16, 17, 33, 256, 257)] == \
+        [16, 16, 32, 64, 64, 256]
+    assert adapters(256)["variant"] == 1 and adapters(257)["variant"] == 0
+    assert adapters(256, N=5120)["variant"] == 0 and adapters(256, R=64)["variant"] == 0
+    for kw in (dict(R=12), dict(K=100), dict(N=77), dict(dt=pgg.PGG_F32)):
+        assert adapters(64, **kw)["variant"] == 3
+    assert refused(pgg.pgg_adapters_plan, 1, 1, 1, 1, 0, 0) == "PGG_ERR_SHAPE"
