@@ -63,10 +63,12 @@ int check_route(int64_t batch, int64_t G, int64_t topK) {
   return PGG_OK;
 }
 
-size_t route_workspace(int64_t batch, int64_t G, int64_t topK) {
+// Header, the blocks' counts, and (several blocks only) every pair's rank.
+size_t route_workspace(int64_t batch, int64_t G, int64_t topK, size_t* rank) {
   int blocks, per;
   route_blocks(batch, G, topK, &blocks, &per);
-  return 256 + align_up(static_cast<size_t>(G) * static_cast<size_t>(blocks) * 4, 256);
+  *rank = 256 + align_up(static_cast<size_t>(G) * static_cast<size_t>(blocks) * 4, 256);
+  return *rank + (blocks > 1 ? align_up(static_cast<size_t>(batch * topK) * 4, 256) : 0);
 }
 
 // ---------------------------------------------------------------- gated product
@@ -318,7 +320,8 @@ int pgg_route_workspace_size(int64_t batch, int64_t G, int64_t topK, size_t* wor
   if (!workspace_bytes) return PGG_ERR_NULL;
   const int rc = check_route(batch, G, topK);
   if (rc != PGG_OK) return rc;
-  *workspace_bytes = route_workspace(batch, G, topK);
+  size_t rank;
+  *workspace_bytes = route_workspace(batch, G, topK, &rank);
   return PGG_OK;
 }
 
@@ -338,7 +341,8 @@ int pgg_route_execute(const void* logits, const float* bias, int64_t batch, int6
       !aligned(probs, 4) || !aligned(experts, 8) || !aligned(expandedRowIdx, 8) ||
       !aligned(groupList, 8) || !aligned(workspace, 256))
     return PGG_ERR_ALIGN;
-  if (workspace_bytes < route_workspace(batch, G, topK)) return PGG_ERR_WORKSPACE;
+  size_t rank;
+  if (workspace_bytes < route_workspace(batch, G, topK, &rank)) return PGG_ERR_WORKSPACE;
   RouteArgs a;
   a.logits = logits;
   a.bias = bias;
@@ -347,6 +351,7 @@ int pgg_route_execute(const void* logits, const float* bias, int64_t batch, int6
   a.idx = expandedRowIdx;
   a.groups = groupList;
   a.counts = reinterpret_cast<uint32_t*>(static_cast<char*>(workspace) + 256);
+  a.rank = reinterpret_cast<uint32_t*>(static_cast<char*>(workspace) + rank);
   a.T = batch;
   a.scale = scale;
   a.G = static_cast<int32_t>(G);

@@ -48,6 +48,7 @@ struct RouteArgs {
   int64_t* idx;         // [T * k]
   int64_t* groups;      // [G]
   uint32_t* counts;     // [G][blocks]: entries of each block per expert, then their prefix sums
+  uint32_t* rank;       // [T * k] rank of a pair among its block's pairs of its expert
   WsHeader* hdr;
   int64_t T;
   float scale;

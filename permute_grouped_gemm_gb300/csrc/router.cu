@@ -15,11 +15,11 @@
 // (-inf) has weight 0; a token whose experts are all masked takes the lowest
 // indices with weights 0. Everything is computed in 32 bits.
 //
-// Few tokens: one block does everything in one launch. Many: (1) choice and
-// the block's count of every expert, (2) prefix sums of the counts over the
+// Few tokens: one block does everything in one launch. Many: (1) choice, ranks
+// and the block's count of every expert, (2) prefix sums of the counts over the
 // blocks, (3) placement. The order is a stable counting sort, so the result
 // depends on no atomic's order. What bounds the large case is instruction
-// issue in the k rounds of the choice, not the 2 or 4 bytes read per logit.
+// issue in the choice, not the 2 or 4 bytes read per logit.
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -168,8 +168,9 @@ __device__ __forceinline__ void load_bias(const float* bias, int G, int sl, floa
 // each finds its rank by counting those before it. Only when equal keys leave more than 32 of them
 // the k rounds of a group-wide maximum are done instead. With two tokens a warp (k <= 16, at most
 // 512 experts) everything but the keys themselves is shared by two tokens.
+// Returns this lane's choice (its token's sl-th), -1 without one.
 template <int DT, int V, int VL, int LPT>
-__device__ __forceinline__ void choose_and_write(const RouteArgs& a, int64_t t0, int64_t t1,
+__device__ __forceinline__ int choose_and_write(const RouteArgs& a, int64_t t0, int64_t t1,
                                                  int lane, const float (&bias)[V],
                                                  uint64_t* s_cand, int* s_expert) {
   const int sl = lane % LPT, sub = lane / LPT;
@@ -289,6 +290,7 @@ __device__ __forceinline__ void choose_and_write(const RouteArgs& a, int64_t t0,
     a.experts[t * a.k + sl] = e;
     a.probs[t * a.k + sl] = p * a.scale;
   }
+  return on && there ? e : -1;
 }
 
 __device__ __forceinline__ void write_place(const RouteArgs& a, int64_t p, int64_t row) {
@@ -336,32 +338,56 @@ __global__ void __launch_bounds__(kSmallThreads) route_small_kernel(const RouteA
       [&](int e, uint32_t where) { write_place(a, e, where); });
 }
 
-// (1) Choice, and the block's count of every expert.
+// (1) Choice, every pair's rank among the block's pairs of its expert, and the block's count of
+// every expert. A warp takes its tokens one after another and a token's choices are distinct, so a
+// counter per warp and expert gives the ranks in order, without atomics; the warps' counts are then
+// added up in their order.
 template <int DT, int V, int VL, int LPT>
 __global__ void __launch_bounds__(32 * kWarps, V <= 16 ? 4 : 2) route_choose_kernel(const RouteArgs a) {
-  extern __shared__ uint32_t s_cnt[];  // [G]
+  extern __shared__ uint32_t s_cnt[];  // [warps][G]
   __shared__ uint64_t s_cand[kWarps][64];
   __shared__ int s_expert[kWarps][kMaxRouteTopK];  // (two tokens of at most 16 or one)
   ptx::griddep_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  for (int g = threadIdx.x; g < a.G; g += blockDim.x) s_cnt[g] = 0;
+  for (int i = threadIdx.x; i < kWarps * a.G; i += blockDim.x) s_cnt[i] = 0;
   if (blockIdx.x == 0 && threadIdx.x == 0) a.hdr->status = 0;
   __syncthreads();
-  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * a.tokens_per_block;
-  const int64_t t1 = t0 + a.tokens_per_block < a.T ? t0 + a.tokens_per_block : a.T;
+  constexpr int kTok = 32 / LPT;  // tokens of a warp at a time
+  const int64_t b0 = static_cast<int64_t>(blockIdx.x) * a.tokens_per_block;
+  const int64_t b1 = b0 + a.tokens_per_block < a.T ? b0 + a.tokens_per_block : a.T;
+  const int64_t run = a.tokens_per_block / kWarps;  // (a multiple of the warps, see route_blocks)
+  const int64_t t0 = b0 + warp * run < b1 ? b0 + warp * run : b1;
+  const int64_t t1 = t0 + run < b1 ? t0 + run : b1;
+  uint32_t* mine = s_cnt + warp * a.G;
   float bias[V];
   load_bias<V, VL, LPT>(a.bias, a.G, lane % LPT, bias);
-  constexpr int kTok = 32 / LPT;  // tokens of a warp at a time
-  for (int64_t t = t0 + kTok * warp; t < t1; t += kTok * kWarps) {
-    choose_and_write<DT, V, VL, LPT>(a, t, t1, lane, bias, s_cand[warp], s_expert[warp]);
-    // (integer counts: the order of these additions changes nothing)
-    const int n = t + kTok <= t1 ? kTok * a.k : static_cast<int>(t1 - t) * a.k;
-    if (lane < n) atomicAdd(&s_cnt[s_expert[warp][lane]], 1u);
-    __syncwarp();
+  for (int64_t t = t0; t < t1; t += kTok) {
+    const int e =
+        choose_and_write<DT, V, VL, LPT>(a, t, t1, lane, bias, s_cand[warp], s_expert[warp]);
+    uint32_t r = 0;
+#pragma unroll
+    for (int s = 0; s < kTok; ++s) {
+      if (e >= 0 && lane / LPT == s) r = mine[e]++;
+      __syncwarp();
+    }
+    if (e >= 0) a.rank[(t + lane / LPT) * a.k + lane % LPT] = r;
   }
   __syncthreads();
-  for (int g = threadIdx.x; g < a.G; g += blockDim.x)
-    a.counts[static_cast<int64_t>(g) * a.blocks + blockIdx.x] = s_cnt[g];
+  for (int g = threadIdx.x; g < a.G; g += blockDim.x) {
+    uint32_t at = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const uint32_t c = s_cnt[w * a.G + g];
+      s_cnt[w * a.G + g] = at;
+      at += c;
+    }
+    a.counts[static_cast<int64_t>(g) * a.blocks + blockIdx.x] = at;
+  }
+  __syncthreads();
+  if (warp > 0)
+#pragma unroll 4
+    for (int64_t p = t0 * a.k + lane; p < t1 * a.k; p += 32)
+      a.rank[p] += mine[a.experts[p]];
 }
 
 // (2) One warp per expert: exclusive prefix sums over the blocks, and the total.
@@ -394,32 +420,29 @@ __global__ void __launch_bounds__(32 * kWarps) count_scan_kernel(uint32_t* count
   if (lane == 0) groups[g] = sum;
 }
 
-// (3) Placement of the block's entries.
+// (3) Placement of the block's pairs: the expert's first row, the pairs of the blocks before, the
+// rank in the block.
 __global__ void __launch_bounds__(32 * kWarps) route_place_kernel(const RouteArgs a) {
-  extern __shared__ uint32_t s_cnt[];  // [warps][G], then [G] bases
+  extern __shared__ uint32_t s_base[];  // [G]
   __shared__ uint32_t s_scan[33];
   ptx::griddep_wait();
-  uint32_t* s_base = s_cnt + kWarps * a.G;
   uint32_t before = 0;
   for (int g0 = 0; g0 < a.G; g0 += blockDim.x) {
     const int g = g0 + threadIdx.x;
     const uint32_t c = g < a.G ? static_cast<uint32_t>(a.groups[g]) : 0u;
+    const uint32_t here =
+        g < a.G ? a.counts[static_cast<int64_t>(g) * a.blocks + blockIdx.x] : 0u;
     uint32_t total;
     const uint32_t at = block_scan_u32(c, s_scan, &total);
-    if (g < a.G)
-      s_base[g] = before + at + a.counts[static_cast<int64_t>(g) * a.blocks + blockIdx.x];
+    if (g < a.G) s_base[g] = before + at + here;
     before += total;
   }
+  __syncthreads();
   const int64_t p0 = static_cast<int64_t>(blockIdx.x) * a.tokens_per_block * a.k;
-  const int64_t left = a.T * a.k - p0;
-  const int most = a.tokens_per_block * a.k;
-  const int n = left < most ? static_cast<int>(left) : most;
-  const int run = ((n + kWarps - 1) / kWarps + 31) / 32 * 32;
-  auto key = [&](int e) { return static_cast<int>(a.experts[p0 + e]); };
-  sort_count(s_cnt, a.G, n, run, key);
-  sort_place(
-      s_cnt, a.G, n, run, key, [&](int g) { return s_base[g]; },
-      [&](int e, uint32_t where) { write_place(a, p0 + e, where); });
+  const int64_t p1 = p0 + static_cast<int64_t>(a.tokens_per_block) * a.k;
+#pragma unroll 4
+  for (int64_t p = p0 + threadIdx.x; p < (p1 < a.T * a.k ? p1 : a.T * a.k); p += blockDim.x)
+    write_place(a, p, s_base[a.experts[p]] + a.rank[p]);
 }
 
 // ------------------------------------------------------------------ gradient
@@ -544,12 +567,12 @@ cudaError_t launch_route_v(const RouteArgs& a, cudaStream_t stream) {
     return launch_pdl(kern, dim3(1), dim3(threads), smem, stream, 1, a);
   }
   cudaError_t err = launch_pdl(route_choose_kernel<DT, V, VL, LPT>, dim3(a.blocks), dim3(32 * kWarps),
-                               static_cast<size_t>(a.G) * 4, stream, 1, a);
+                               static_cast<size_t>(kWarps) * a.G * 4, stream, 1, a);
   if (err != cudaSuccess) return err;
   err = launch_count_scan(a.counts, a.G, a.blocks, a.groups, stream);
   if (err != cudaSuccess) return err;
   return launch_pdl(route_place_kernel, dim3(a.blocks), dim3(32 * kWarps),
-                    static_cast<size_t>(kWarps + 1) * a.G * 4, stream, 1, a);
+                    static_cast<size_t>(a.G) * 4, stream, 1, a);
 }
 
 template <int DT, int V, int LPT>
@@ -583,7 +606,7 @@ cudaError_t launch_count_scan(uint32_t* counts, int G, int blocks, int64_t* grou
 }
 
 // Blocks of the choice and placement launches: one when all the pairs fit one
-// block, else at most kMaxBlocks with a multiple of the block's warps of tokens each.
+// block, else at most kMaxBlocks.
 void route_blocks(int64_t T, int64_t G, int64_t k, int* blocks, int* tokens_per_block) {
   if (T * k <= kSmallEntries && T <= 256) {
     *blocks = 1;
@@ -591,7 +614,8 @@ void route_blocks(int64_t T, int64_t G, int64_t k, int* blocks, int* tokens_per_
     return;
   }
   int64_t per = (T + kMaxBlocks - 1) / kMaxBlocks;
-  per = (per + kWarps - 1) / kWarps * kWarps;
+  // whole warps of two tokens each
+  per = (per + 2 * kWarps - 1) / (2 * kWarps) * (2 * kWarps);
   *tokens_per_block = static_cast<int>(per);
   *blocks = static_cast<int>((T + per - 1) / per);
 }

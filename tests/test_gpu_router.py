@@ -135,6 +135,19 @@ def test_repeats_bitwise_and_on_another_stream():
         assert torch.equal(a, b)
 
 
+def test_more_pairs_per_block_than_it_sorts_at_a_time():
+    l = logits_of(250000, 40, "bf16", 7)
+    probs, experts, idx, groups, _ = pgg.route(l, 6)
+    flat = experts.reshape(-1)
+    want = torch.sort(flat, stable=True).indices
+    assert torch.equal(idx, want)
+    assert torch.equal(groups, torch.bincount(flat, minlength=40))
+    rows = torch.randperm(250000)[:500].cuda()
+    check(l[rows].contiguous(), 6)
+    assert torch.equal(experts[rows], torch.sort(l[rows].float(), dim=1, descending=True,
+                                                 stable=True).indices[:, :6])
+
+
 def test_the_order_is_what_the_grouped_products_take():
     l = logits_of(500, 12, "fp32", 6)
     probs, experts, idx, groups, _ = pgg.route(l, 3, 1)
