@@ -81,6 +81,20 @@ __device__ __forceinline__ uint32_t group_max_u32(uint32_t v) {
   }
 }
 
+// The group's values in decreasing order, one a lane (a bitonic network).
+template <int LPT>
+__device__ __forceinline__ uint32_t sort_lanes(uint32_t v, int sl) {
+#pragma unroll
+  for (int size = 2; size <= LPT; size <<= 1)
+#pragma unroll
+    for (int d = size >> 1; d > 0; d >>= 1) {
+      const uint32_t o = __shfl_xor_sync(0xFFFFFFFFu, v, d);
+      const bool larger = ((sl & d) == 0) == ((sl & size) == 0);
+      v = larger ? (o > v ? o : v) : (o < v ? o : v);
+    }
+  return v;
+}
+
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, d);
@@ -174,10 +188,9 @@ __device__ __forceinline__ int choose_and_write(const RouteArgs& a, int64_t t0, 
                                                  int lane, const float (&bias)[V],
                                                  uint64_t* s_cand, int* s_expert) {
   const int sl = lane % LPT, sub = lane / LPT;
-  const uint32_t group = LPT == 32 ? 0xFFFFFFFFu : 0xFFFFu << (16 * sub);
   const int64_t t = t0 + sub < t1 ? t0 + sub : t1 - 1;  // (the last one again, not written)
   const bool there = t0 + sub < t1;
-  s_cand += 32 * sub;
+  s_cand += 33 * sub;
   s_expert += a.k * sub;
   float l[V];
   uint32_t key[V];
@@ -204,20 +217,11 @@ __device__ __forceinline__ int choose_and_write(const RouteArgs& a, int64_t t0, 
       best = key[c] > best ? key[c] : best;
     }
   }
-  uint32_t floor_key = 0;
-  for (int seen = 0;;) {
-    const uint32_t top_key = group_max_u32<LPT>(best);
-    const bool more = seen < a.k;
-    const bool top = more && best == top_key;
-    const int n = __popc(__ballot_sync(0xFFFFFFFFu, top) & group);
-    if (more) {
-      // 0: fewer lanes than k hold anything, so all that is there is looked at
-      floor_key = top_key > 0 ? top_key : 1u;
-      seen = top_key > 0 ? seen + n : a.k;
-    }
-    if (top) best = 0;
-    if (!__any_sync(0xFFFFFFFFu, seen < a.k)) break;
-  }
+  // the k-th largest of the lanes' maxima (0: fewer lanes than k hold anything, so all that is
+  // there is looked at)
+  uint32_t floor_key =
+      __shfl_sync(0xFFFFFFFFu, sort_lanes<LPT>(best, sl), a.k - 1, LPT);
+  if (floor_key == 0) floor_key = 1;
   int mine = 0;  // candidates of this lane, then of the lanes up to it
 #pragma unroll
   for (int i = 0; i < V; ++i) mine += key[i] >= floor_key ? 1 : 0;
@@ -228,14 +232,17 @@ __device__ __forceinline__ int choose_and_write(const RouteArgs& a, int64_t t0, 
     if (sl >= d) upto += y;
   }
   const int n = __shfl_sync(0xFFFFFFFFu, upto, LPT - 1, LPT);
-  if (n <= 32) {
-    // key above, the index's complement below: a larger number comes first
-    uint64_t* at = s_cand + (upto - mine);
+  {
+    // key above, the index's complement below: a larger number comes first. What is no candidate, or
+    // past the 32nd, goes to the last word, so that no lane branches.
+    int at = upto - mine;
 #pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (key[i] >= floor_key)
-        *at++ = static_cast<uint64_t>(key[i]) << 32 |
-                static_cast<uint32_t>(~expert_at<VL, LPT>(i, sl));
+    for (int i = 0; i < V; ++i) {
+      const bool in = key[i] >= floor_key;
+      s_cand[in && at < 32 ? at : 32] = static_cast<uint64_t>(key[i]) << 32 |
+                                        static_cast<uint32_t>(~expert_at<VL, LPT>(i, sl));
+      at += in ? 1 : 0;
+    }
   }
   __syncwarp();
   if (__any_sync(0xFFFFFFFFu, n > 32)) {
@@ -305,7 +312,7 @@ template <int DT, int V, int VL, int LPT>
 __global__ void __launch_bounds__(kSmallThreads) route_small_kernel(const RouteArgs a) {
   extern __shared__ uint32_t s_cnt[];  // [warps][G], the entries' experts, [G] bases
   __shared__ uint32_t s_scan[33];
-  __shared__ uint64_t s_cand[kSmallThreads / 32][64];
+  __shared__ uint64_t s_cand[kSmallThreads / 32][66];
   ptx::griddep_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   int* s_expert = reinterpret_cast<int*>(s_cnt + warps * a.G);
@@ -345,7 +352,7 @@ __global__ void __launch_bounds__(kSmallThreads) route_small_kernel(const RouteA
 template <int DT, int V, int VL, int LPT>
 __global__ void __launch_bounds__(32 * kWarps, V <= 16 ? 4 : 2) route_choose_kernel(const RouteArgs a) {
   extern __shared__ uint32_t s_cnt[];  // [warps][G]
-  __shared__ uint64_t s_cand[kWarps][64];
+  __shared__ uint64_t s_cand[kWarps][66];
   __shared__ int s_expert[kWarps][kMaxRouteTopK];  // (two tokens of at most 16 or one)
   ptx::griddep_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
