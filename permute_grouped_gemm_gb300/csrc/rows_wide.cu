@@ -98,6 +98,7 @@ struct Tile {
   int rows;             // this CTA's rows of the block (0 .. 128)
   int steps;            // reduction steps, the low-rank ones included
   int seg0;             // adapt: first adapter segment of the tile
+  bool both;            // H == 2: the second MMA's columns are this tile's too
   int32_t box[2];       // adapt: first token of each CTA's rows if they are neighbours, else -1
 };
 
@@ -113,11 +114,31 @@ __device__ __forceinline__ int main_steps(const RowsArgs& a) {
 }
 __device__ __forceinline__ int rank_steps(const RowsArgs& a) { return (a.R + kFK - 1) / kFK; }
 
+// The tiles' numbers: `full` whole ones, then (H == 2) the two halves of each of the others, so that
+// a last round that would leave most pairs of CTAs idle takes half the time.
+struct Schedule {
+  uint32_t full, total;
+};
+
+template <int H>
+__device__ __forceinline__ Schedule schedule_of(uint32_t tiles) {
+  const uint32_t pairs = n_clusters(), rest = tiles % pairs;
+  Schedule s;
+  s.full = H == 2 && 2 * rest <= pairs ? tiles - rest : tiles;
+  s.total = s.full + 2 * (tiles - s.full);
+  return s;
+}
+
 template <int MODE, int H>
-__device__ __forceinline__ Tile tile_of(uint32_t t, const RowsArgs& a, uint32_t rank) {
-  const uint32_t rb = t / static_cast<uint32_t>(a.n_blocks);
+__device__ __forceinline__ Tile tile_of(uint32_t t, const Schedule& s, const RowsArgs& a,
+                                        uint32_t rank) {
+  const bool part = H == 2 && t >= s.full;
+  const uint32_t f = part ? s.full + (t - s.full) / 2 : t;
+  const uint32_t rb = f / static_cast<uint32_t>(a.n_blocks);
   Tile x;
-  x.n0 = static_cast<int64_t>(t - rb * static_cast<uint32_t>(a.n_blocks)) * Shape<MODE, H>::kTileN;
+  x.n0 = static_cast<int64_t>(f - rb * static_cast<uint32_t>(a.n_blocks)) * Shape<MODE, H>::kTileN;
+  if (part && ((t - s.full) & 1)) x.n0 += Shape<MODE, H>::kHalfN;
+  x.both = H == 2 && !part && x.n0 + Shape<MODE, H>::kHalfN < a.N;
   x.steps = main_steps(a);
   x.seg0 = 0;
   x.box[0] = x.box[1] = -1;
@@ -164,11 +185,13 @@ __device__ __forceinline__ int64_t panel_column(int64_t n0, int h, int j, uint32
 
 // Weight bytes that CTA `rank` loads for one main or low-rank step of a tile.
 template <int MODE, int H>
-__device__ __forceinline__ uint32_t w_bytes(const RowsArgs& a, int64_t n0, uint32_t rank,
+__device__ __forceinline__ uint32_t w_bytes(const RowsArgs& a, const Tile& x, uint32_t rank,
                                             bool low_rank) {
+  const int64_t n0 = x.n0;
   uint32_t b = 0;
 #pragma unroll
   for (int h = 0; h < H; ++h) {
+    if (h == 1 && !x.both) continue;
     if (MODE == kAdaptT || low_rank) {
       b += panel_column<MODE>(n0, h, 0, rank) < a.N ? static_cast<uint32_t>(kHalfBytes) : 0u;
     } else {
@@ -182,7 +205,7 @@ __device__ __forceinline__ uint32_t w_bytes(const RowsArgs& a, int64_t n0, uint3
 
 template <int MODE, int H>
 __device__ void w_producer(uint8_t* smem, WideCtl* ctl, const CUtensorMap* tm_w,
-                           const CUtensorMap* tm_b, const CUtensorMap* tm_x, const RowsArgs& a, uint32_t total,
+                           const CUtensorMap* tm_b, const CUtensorMap* tm_x, const RowsArgs& a, const Schedule& sc,
                            uint32_t rank) {
   using C = Cfg<H>;
   const uint64_t lim = a.wait_limit_ns;
@@ -192,8 +215,8 @@ __device__ void w_producer(uint8_t* smem, WideCtl* ctl, const CUtensorMap* tm_w,
   int stage = 0;
   uint32_t phase = 0, outstanding = 0, last_parity = 0;
   bool failed = false;
-  for (uint32_t t = cluster_id(); t < total && !failed; t += n_clusters()) {
-    const Tile x = tile_of<MODE, H>(t, a, rank);
+  for (uint32_t t = cluster_id(); t < sc.total && !failed; t += n_clusters()) {
+    const Tile x = tile_of<MODE, H>(t, sc, a, rank);
     for (int ks = 0; ks < x.steps; ++ks) {
       const bool low = MODE != kGated && ks >= nks;
       int4 seg = make_int4(0, 0, 0, 0);
@@ -206,7 +229,7 @@ __device__ void w_producer(uint8_t* smem, WideCtl* ctl, const CUtensorMap* tm_w,
       uint8_t* sb = smem + stage * C::kStageBytes + kABytes;
       const uint32_t fb = ptx::mapa(&ctl->full[stage], 0);
       if (leader) {
-        uint32_t bytes = w_bytes<MODE, H>(a, x.n0, 0, low) + w_bytes<MODE, H>(a, x.n0, 1, low);
+        uint32_t bytes = w_bytes<MODE, H>(a, x, 0, low) + w_bytes<MODE, H>(a, x, 1, low);
         if (MODE != kGated && !low)
           bytes += (x.box[0] >= 0 ? kABytes : 0) + (x.box[1] >= 0 ? kABytes : 0);
         ptx::mbar_arrive_expect_tx(&ctl->full[stage], bytes);
@@ -215,6 +238,7 @@ __device__ void w_producer(uint8_t* smem, WideCtl* ctl, const CUtensorMap* tm_w,
         ptx::tma_load_2d_pair(sb - kABytes, tm_x, fb, ks * kFK, (rank ? x.box[1] : x.box[0]));
 #pragma unroll
       for (int h = 0; h < H; ++h) {
+        if (h == 1 && !x.both) continue;
         uint8_t* sh = sb + h * kHalfBytes;
         const int64_t nc = panel_column<MODE>(x.n0, h, 0, rank);
         if (low) {
@@ -255,7 +279,7 @@ __device__ void w_producer(uint8_t* smem, WideCtl* ctl, const CUtensorMap* tm_w,
 // Gather warp w fills stage slot w: the CTA's stages w, w + S, ... in the
 // sequence of all steps of all its tiles. Rows lane >> 3 + 4 q, 16-byte chunk lane & 7.
 template <int MODE, int H>
-__device__ void x_gatherer(uint8_t* smem, WideCtl* ctl, const RowsArgs& a, uint32_t total,
+__device__ void x_gatherer(uint8_t* smem, WideCtl* ctl, const RowsArgs& a, const Schedule& sc,
                            uint32_t rank) {
   using C = Cfg<H>;
   const uint64_t lim = a.wait_limit_ns;
@@ -275,8 +299,8 @@ __device__ void x_gatherer(uint8_t* smem, WideCtl* ctl, const RowsArgs& a, uint3
   constexpr uint32_t kNoRow = 0xFFFFFFFFu;
   const uint32_t row_units = static_cast<uint32_t>(a.K / 8);
   uint32_t row16[kFM / 4];
-  for (uint32_t t = cluster_id(); t < total && !failed; t += n_clusters()) {
-    const Tile x = tile_of<MODE, H>(t, a, rank);
+  for (uint32_t t = cluster_id(); t < sc.total && !failed; t += n_clusters()) {
+    const Tile x = tile_of<MODE, H>(t, sc, a, rank);
     if (kb < x.steps) {
       int32_t tok[4];
 #pragma unroll
@@ -300,7 +324,12 @@ __device__ void x_gatherer(uint8_t* smem, WideCtl* ctl, const RowsArgs& a, uint3
         break;
       }
       if (MODE != kGated && kb < nks && (rank ? x.box[1] : x.box[0]) >= 0) {
-        // neighbouring rows: the weight's producer copies them as one box
+        // neighbouring rows: the weight's producer copies them as one box. This warp has written
+        // nothing, so its arrival need not release anything across the cluster (which costs the
+        // odd CTA's warp up to 1,500 cycles).
+        if (lane == 0) ptx::mbar_arrive_remote_cta(full);
+        phase ^= 1u;
+        continue;
       } else if (MODE == kGated || kb < nks) {
         const int64_t k = static_cast<int64_t>(kb) * kFK + c * 8;
         const bool k_ok = k < a.K;
@@ -367,7 +396,7 @@ __device__ __forceinline__ void lane_mask(int lo, int hi, uint32_t (&m)[8]) {
 
 template <int DT, int MODE, int H>
 __device__ void mma_issuer(uint8_t* smem, WideCtl* ctl, uint32_t tmem_base, const RowsArgs& a,
-                           uint32_t total) {
+                           const Schedule& sc) {
   using C = Cfg<H>;
   constexpr uint32_t kFmt = DT == PGG_BF16 ? 1u : 0u;
   constexpr uint32_t idesc_k = ptx::idesc_make(kFmt, 2 * kFM, kFN);  // both operands K-major
@@ -378,14 +407,13 @@ __device__ void mma_issuer(uint8_t* smem, WideCtl* ctl, uint32_t tmem_base, cons
   int stage = 0, acc = 0;
   uint32_t phase = 0, aph = 0;
   bool issued = false, failed = false;
-  for (uint32_t t = cluster_id(); t < total && !failed; t += n_clusters()) {
-    const Tile x = tile_of<MODE, H>(t, a, 0);
+  for (uint32_t t = cluster_id(); t < sc.total && !failed; t += n_clusters()) {
+    const Tile x = tile_of<MODE, H>(t, sc, a, 0);
     if (!ptx::mbar_wait_cluster(&ctl->tempty[acc], aph ^ 1u, lim, abort)) {
       failed = true;
       break;
     }
     ptx::tc_fence_after_sync();
-    const bool both = H == 2 && x.n0 + Shape<MODE, H>::kHalfN < a.N;  // any column in the second
     for (int ks = 0; ks < x.steps; ++ks) {
       const bool low = MODE != kGated && ks >= nks;
       int4 seg = make_int4(0, 0, 0, 0);
@@ -402,7 +430,7 @@ __device__ void mma_issuer(uint8_t* smem, WideCtl* ctl, uint32_t tmem_base, cons
       if (low) lane_mask(static_cast<int>(seg.y - x.row0), static_cast<int>(seg.z - x.row0), m);
 #pragma unroll
       for (int h = 0; h < H; ++h) {
-        if (h == 1 && !both) continue;
+        if (h == 1 && !x.both) continue;
         const uint32_t d_tmem = tmem_base + static_cast<uint32_t>((H == 1 ? acc : h) * kFN);
         const uint32_t sb = sa + kABytes + h * kHalfBytes;
         if (low) {
@@ -502,7 +530,7 @@ __device__ __forceinline__ void store_rows(uint4 (&b)[8], void* out, int64_t row
 }
 
 template <int DT, int MODE, int H>
-__device__ void epilogue(WideCtl* ctl, uint32_t tmem_base, const RowsArgs& a, uint32_t total,
+__device__ void epilogue(WideCtl* ctl, uint32_t tmem_base, const RowsArgs& a, const Schedule& sc,
                          uint32_t rank) {
   const uint64_t lim = a.wait_limit_ns;
   volatile int* abort = &ctl->abort;
@@ -517,8 +545,8 @@ __device__ void epilogue(WideCtl* ctl, uint32_t tmem_base, const RowsArgs& a, ui
   int acc = 0;
   uint32_t aph = 0;
   bool held = a.hold_release != 0;  // (test hook: the first release is withheld)
-  for (uint32_t t = cluster_id(); t < total; t += n_clusters()) {
-    const Tile x = tile_of<MODE, H>(t, a, rank);
+  for (uint32_t t = cluster_id(); t < sc.total; t += n_clusters()) {
+    const Tile x = tile_of<MODE, H>(t, sc, a, rank);
     const int64_t n0 = x.n0 + h * Shape<MODE, H>::kHalfN;
     const int valid = x.rows - 32 * quarter;  // rows of this warp's 32 that exist
     int64_t row = -1;                         // output row of this lane
@@ -544,7 +572,8 @@ __device__ void epilogue(WideCtl* ctl, uint32_t tmem_base, const RowsArgs& a, ui
     const uint32_t t_lane = tmem_base + (static_cast<uint32_t>(32 * quarter) << 16) +
                             static_cast<uint32_t>((H == 1 ? acc : h) * kFN);
 #pragma unroll 1
-    for (int c0 = col0; c0 < col0 + kSpan && n0 + c0 < a.N && valid > 0; c0 += 64) {
+    for (int c0 = col0; c0 < col0 + kSpan && n0 + c0 < a.N && valid > 0 && (h == 0 || x.both);
+         c0 += 64) {
       uint4 b[8];
       if constexpr (MODE == kGated) {
         gated_blocks<DT>(t_lane + static_cast<uint32_t>(c0), p, b);
@@ -592,7 +621,7 @@ __global__ void __launch_bounds__(Cfg<H>::kThreads, 1)
   const uint32_t row_blocks = MODE == kGated
                                   ? a.hdr->n_row_blocks
                                   : static_cast<uint32_t>((a.M + 2 * kFM - 1) / (2 * kFM));
-  const uint32_t total = row_blocks * static_cast<uint32_t>(a.n_blocks);
+  const Schedule sc = schedule_of<H>(row_blocks * static_cast<uint32_t>(a.n_blocks));
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
@@ -623,13 +652,13 @@ __global__ void __launch_bounds__(Cfg<H>::kThreads, 1)
   const uint32_t tmem_base = ctl->tmem_base;
 
   if (warp == 0) {
-    if (lane == 0) w_producer<MODE, H>(smem, ctl, &tm_w, &tm_b, &tm_x, a, total, rank);
+    if (lane == 0) w_producer<MODE, H>(smem, ctl, &tm_w, &tm_b, &tm_x, a, sc, rank);
   } else if (warp == 1) {
-    if (lane == 0 && rank == 0) mma_issuer<DT, MODE, H>(smem, ctl, tmem_base, a, total);
+    if (lane == 0 && rank == 0) mma_issuer<DT, MODE, H>(smem, ctl, tmem_base, a, sc);
   } else if (warp < 2 + C::kGatherWarps) {
-    x_gatherer<MODE, H>(smem, ctl, a, total, rank);
+    x_gatherer<MODE, H>(smem, ctl, a, sc, rank);
   } else if (warp >= C::kEpiWarp0) {
-    epilogue<DT, MODE, H>(ctl, tmem_base, a, total, rank);
+    epilogue<DT, MODE, H>(ctl, tmem_base, a, sc, rank);
   }
 
   ptx::tc_fence_before_sync();
@@ -642,9 +671,9 @@ __global__ void __launch_bounds__(Cfg<H>::kThreads, 1)
 }
 
 // Tiles of 256 or of 512 accumulator columns: the form whose busiest pair of CTAs has the fewer
-// cycles. A 64-k step takes about 720 with 256 columns and 1180 with 512 (measured; the wider tile
-// reads a quarter less per product, and what L2 delivers, 40 to 45 bytes a cycle and SM, is the
-// limit in both). With 512 columns there is one accumulator, so nothing hides a tile's output:
+// cycles. A 64-k step takes about 720 with 256 columns and 1230 with 512 (1113 where the rows come
+// as boxes): the wider tile reads a quarter less per product and has eight MMAs to a wait and a
+// commit. With 512 columns there is one accumulator, so nothing hides a tile's output:
 // 13,000 cycles with gate_up, 7,300 for h alone, 5,200 for y. Both sides: 13,500 tokens x 8, 60
 // experts, K 7168, F 2048: 4.45 ms and 4.13; 4096 x 8, 16 experts, K 2048, F 1024: 198 us and 238;
 // adapters, K = N = 4096, 2048 tokens: 79 and 71 us, 8191: 203 and 206.
@@ -652,10 +681,15 @@ int choose_halves(RowsMode mode, const RowsArgs& a, int64_t row_blocks, int pair
   const int64_t half_n = mode == kGated ? 128 : 256;
   const int64_t steps = (a.K + kFK - 1) / kFK;
   const int64_t drain = mode != kGated ? 5200 : a.gate_up ? 13000 : 7300;
+  const int64_t step2 = mode != kGated ? 1113 : 1230;
   const int64_t n1 = row_blocks * ((a.N + half_n - 1) / half_n);
   const int64_t n2 = row_blocks * ((a.N + 2 * half_n - 1) / (2 * half_n));
   const int64_t one = (n1 + pairs - 1) / pairs * (steps * 720 > drain ? steps * 720 : drain);
-  const int64_t two = (n2 + pairs - 1) / pairs * (steps * 1180 + drain);
+  const int64_t rest = n2 % pairs;  // as halves when they are few (see schedule_of)
+  const int64_t tail = rest == 0           ? 0
+                       : 2 * rest <= pairs ? steps * 720 + drain
+                                           : steps * step2 + drain;
+  const int64_t two = n2 / pairs * (steps * step2 + drain) + tail;
   return two < one ? 2 : 1;
 }
 
