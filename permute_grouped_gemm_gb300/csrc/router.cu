@@ -8,8 +8,8 @@
 //     prob[j]  = scale * score[chosen_j]  (/ sum over the chosen when renormalised)
 //     rows     = the pairs (token, j) sorted by (expert, token * k + j)
 //
-// A warp takes two tokens (or one): the logits sit in registers, G / 16 a lane,
-// as sortable integers; see choose_and_write. A NaN key
+// A warp takes four tokens (or two, or one): the logits sit in registers, G / 8 a lane,
+// see choose_and_write. A NaN key
 // sorts below everything (the choice stays a valid one); scores follow IEEE
 // arithmetic, so a NaN or +inf logit gives NaN weights. A masked expert
 // (-inf) has weight 0; a token whose experts are all masked takes the lowest
@@ -81,18 +81,40 @@ __device__ __forceinline__ uint32_t group_max_u32(uint32_t v) {
   }
 }
 
-// The group's values in decreasing order, one a lane (a bitonic network).
+// The group's values (no NaN) in decreasing order, one a lane (a bitonic network).
 template <int LPT>
-__device__ __forceinline__ uint32_t sort_lanes(uint32_t v, int sl) {
+__device__ __forceinline__ float sort_lanes(float v, int sl) {
 #pragma unroll
   for (int size = 2; size <= LPT; size <<= 1)
 #pragma unroll
     for (int d = size >> 1; d > 0; d >>= 1) {
-      const uint32_t o = __shfl_xor_sync(0xFFFFFFFFu, v, d);
+      const float o = __shfl_xor_sync(0xFFFFFFFFu, v, d);
       const bool larger = ((sl & d) == 0) == ((sl & size) == 0);
-      v = larger ? (o > v ? o : v) : (o < v ? o : v);
+      v = larger ? fmaxf(v, o) : fminf(v, o);
     }
   return v;
+}
+
+// The same of two values a lane: 2 LPT in all, the 2 sl-th and the next in v0 and v1.
+template <int LPT>
+__device__ __forceinline__ void sort_lanes_two(float& v0, float& v1, int sl) {
+#pragma unroll
+  for (int size = 2; size <= 2 * LPT; size <<= 1)
+#pragma unroll
+    for (int d = size >> 1; d > 0; d >>= 1) {
+      const bool down = (2 * sl & size) == 0;
+      if (d == 1) {
+        const float hi = fmaxf(v0, v1), lo = fminf(v0, v1);
+        v0 = down ? hi : lo;
+        v1 = down ? lo : hi;
+      } else {
+        const float o0 = __shfl_xor_sync(0xFFFFFFFFu, v0, d / 2);
+        const float o1 = __shfl_xor_sync(0xFFFFFFFFu, v1, d / 2);
+        const bool larger = ((2 * sl & d) == 0) == down;
+        v0 = larger ? fmaxf(v0, o0) : fminf(v0, o0);
+        v1 = larger ? fmaxf(v1, o1) : fminf(v1, o1);
+      }
+    }
 }
 
 __device__ __forceinline__ float warp_sum(float v) {
@@ -136,7 +158,9 @@ __device__ __forceinline__ void load_row(const void* logits, int64_t row, int G,
 #pragma unroll
     for (int i = 0; i < V; i += VL) {
       const int e = expert_at<VL, LPT>(i, sl);
-      uint32_t w[4] = {0, 0, 0, 0};
+      constexpr uint32_t kNone = DT == PGG_F32 ? 0xFF800000u : DT == PGG_BF16 ? 0xFF80FF80u
+                                                                              : 0xFC00FC00u;
+      uint32_t w[4] = {kNone, kNone, kNone, kNone};  // -inf
       if (e < G) {
         const char* p = static_cast<const char*>(logits) + (row + e) * (kBytes / VL);
         if constexpr (kBytes == 16) {
@@ -159,41 +183,69 @@ __device__ __forceinline__ void load_row(const void* logits, int64_t row, int G,
         else
           f = __half2float(__ushort_as_half(
               static_cast<unsigned short>(c % 2 ? w[c / 2] >> 16 : w[c / 2] & 0xFFFFu)));
-        l[i + c] = e < G ? f : -INFINITY;
+        l[i + c] = f;
       }
     }
   }
 }
 
+// The bias in shared memory, in the order in which the lanes read it (value i of lane sl at
+// i / 4 * 4 LPT + 4 sl + i % 4); 0 past the end.
 template <int V, int VL, int LPT>
-__device__ __forceinline__ void load_bias(const float* bias, int G, int sl, float (&b)[V]) {
-#pragma unroll
-  for (int i = 0; i < V; ++i) {
+__device__ __forceinline__ void stage_bias(const RouteArgs& a, float* s_bias) {
+  for (int j = threadIdx.x; j < V * LPT; j += blockDim.x) {
+    const int c = V < 4 ? V : 4;
+    const int i = j / (c * LPT) * c + j % c, sl = j / c % LPT;
     const int e = expert_at<VL, LPT>(i, sl);
-    b[i] = (bias && e < G ? bias[e] : 0.0f) + 0.0f;  // (-0 becomes +0)
+    s_bias[j] = a.bias && e < a.G ? a.bias[e] : 0.0f;
   }
 }
+
+template <int V, int LPT>
+__device__ __forceinline__ void add_bias(const float* s_bias, int sl, float (&l)[V]) {
+  if constexpr (V < 4) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) l[i] += s_bias[V * sl + i];
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; i += 4) {
+      const float4 b = *reinterpret_cast<const float4*>(s_bias + i * LPT + 4 * sl);
+      l[i] += b.x, l[i + 1] += b.y, l[i + 2] += b.z, l[i + 3] += b.w;
+    }
+  }
+}
+
+// A warp's scratch memory of the choice: the candidates of up to four tokens. (34 words apart, so
+// that the tokens' broadcast reads of 16 bytes meet in different banks.)
+constexpr int kCand = 32;
+template <int LPT>
+struct alignas(16) ChoiceScratch {
+  uint64_t word[32 / LPT][kCand + 2];  // key above, the index's complement below: larger is first
+  int expert[32 / LPT][kCand];
+};
 
 // The choice of 32 / LPT tokens from t0 on with one warp, LPT lanes each, written to probs,
 // experts and s_expert [k] (a token at or past T writes nothing).
 //
-// The k-th largest of the lanes' maxima is at most the k-th largest key, so the chosen are among
-// the keys that reach it: rarely more than k plus a few. They are collected in shared memory and
-// each finds its rank by counting those before it. Only when equal keys leave more than 32 of them
-// the k rounds of a group-wide maximum are done instead. With two tokens a warp (k <= 16, at most
-// 512 experts) everything but the keys themselves is shared by two tokens.
+// The k-th largest of the lanes' maxima (of two halves each with 8 lanes) is at most the k-th largest
+// key, so the chosen are among the keys that reach it: rarely more than k plus a few. Their indices are collected in shared
+// memory, and the lanes, one a candidate, find each one's rank by counting those before it. Up to
+// there the keys are floats (the maximum of two passes over a NaN, and no NaN reaches a
+// threshold); only the few candidates become integers. Where too few lanes hold a key above -inf,
+// or equal keys leave more than 32 candidates, the k rounds of a group-wide maximum are done
+// instead. With two or four tokens a warp everything but the logits themselves is shared by them.
 // Returns this lane's choice (its token's sl-th), -1 without one.
 template <int DT, int V, int VL, int LPT>
 __device__ __forceinline__ int choose_and_write(const RouteArgs& a, int64_t t0, int64_t t1,
-                                                 int lane, const float (&bias)[V],
-                                                 uint64_t* s_cand, int* s_expert) {
+                                                 int lane, const float* s_bias,
+                                                 ChoiceScratch<LPT>* scratch, int* s_expert) {
   const int sl = lane % LPT, sub = lane / LPT;
   const int64_t t = t0 + sub < t1 ? t0 + sub : t1 - 1;  // (the last one again, not written)
   const bool there = t0 + sub < t1;
-  s_cand += 33 * sub;
+  uint64_t* const word = scratch->word[sub];
+  int* const cand = scratch->expert[sub];
   s_expert += a.k * sub;
   float l[V];
-  uint32_t key[V];
   const int64_t row = t * a.G;
   load_row<DT, V, VL, LPT>(a.logits, row, a.G, sl, l);
   float m = -INFINITY, z = 0.0f;
@@ -205,47 +257,43 @@ __device__ __forceinline__ int choose_and_write(const RouteArgs& a, int64_t t0, 
     for (int i = 0; i < V; ++i) z += soft_exp(l[i], m);  // (0 past the end)
     z = group_sum<LPT>(z);
   }
-  uint32_t best = 0;
+  if (a.bias) add_bias<V, LPT>(s_bias, sl, l);
+  float floor_key;
+  if constexpr (LPT == 8) {
+    float b0 = -INFINITY, b1 = -INFINITY;
 #pragma unroll
-  for (int i = 0; i < V; i += VL) {
-    // 0: not there (a whole load is, or is not)
-    const bool in = expert_at<VL, LPT>(i, sl) < a.G;
+    for (int i = 0; i < V / 2; ++i) b0 = fmaxf(b0, l[i]), b1 = fmaxf(b1, l[V / 2 + i]);
+    sort_lanes_two<LPT>(b0, b1, sl);
+    floor_key = __shfl_sync(0xFFFFFFFFu, a.k & 1 ? b0 : b1, (a.k - 1) >> 1, LPT);
+  } else {
+    float best = -INFINITY;
 #pragma unroll
-    for (int c = i; c < i + VL; ++c) {
-      // (the bias is +0 without one, so a sum is never -0)
-      key[c] = in ? sort_key(l[c] + bias[c]) : 0u;
-      best = key[c] > best ? key[c] : best;
-    }
+    for (int i = 0; i < V; ++i) best = fmaxf(best, l[i]);
+    floor_key = __shfl_sync(0xFFFFFFFFu, sort_lanes<LPT>(best, sl), a.k - 1, LPT);
   }
-  // the k-th largest of the lanes' maxima (0: fewer lanes than k hold anything, so all that is
-  // there is looked at)
-  uint32_t floor_key =
-      __shfl_sync(0xFFFFFFFFu, sort_lanes<LPT>(best, sl), a.k - 1, LPT);
-  if (floor_key == 0) floor_key = 1;
-  int mine = 0;  // candidates of this lane, then of the lanes up to it
+  uint32_t mask = 0;  // this lane's candidates
 #pragma unroll
-  for (int i = 0; i < V; ++i) mine += key[i] >= floor_key ? 1 : 0;
-  int upto = mine;
+  for (int i = 0; i < V; ++i) mask |= l[i] >= floor_key ? 1u << i : 0u;
+  if (floor_key == -INFINITY) mask = 0;
+  int upto = __popc(mask);
+  int at = -upto;
 #pragma unroll
   for (int d = 1; d < LPT; d <<= 1) {
     const int y = __shfl_up_sync(0xFFFFFFFFu, upto, d, LPT);
     if (sl >= d) upto += y;
   }
+  at += upto;
   const int n = __shfl_sync(0xFFFFFFFFu, upto, LPT - 1, LPT);
-  {
-    // key above, the index's complement below: a larger number comes first. What is no candidate, or
-    // past the 32nd, goes to the last word, so that no lane branches.
-    int at = upto - mine;
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const bool in = key[i] >= floor_key;
-      s_cand[in && at < 32 ? at : 32] = static_cast<uint64_t>(key[i]) << 32 |
-                                        static_cast<uint32_t>(~expert_at<VL, LPT>(i, sl));
-      at += in ? 1 : 0;
-    }
+  const bool few = n > 0 && n <= kCand;
+  if (few) {
+    for (; mask; mask &= mask - 1) cand[at++] = expert_at<VL, LPT>(__ffs(mask) - 1, sl);
   }
   __syncwarp();
-  if (__any_sync(0xFFFFFFFFu, n > 32)) {
+  if (!__all_sync(0xFFFFFFFFu, few)) {
+    uint32_t key[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      key[i] = expert_at<VL, LPT>(i, sl) < a.G ? sort_key(l[i] + 0.0f) : 0u;  // 0: not there
     for (int j = 0; j < a.k; ++j) {
       uint32_t top = 0, where = 0;
 #pragma unroll
@@ -260,18 +308,41 @@ __device__ __forceinline__ int choose_and_write(const RouteArgs& a, int64_t t0, 
 #pragma unroll
       for (int i = 0; i < V; ++i)
         if (static_cast<uint32_t>(expert_at<VL, LPT>(i, sl)) == where) key[i] = 0;
-      if (n > 32 && sl == 0) s_expert[j] = static_cast<int>(where);
+      if (!few && sl == 0) s_expert[j] = static_cast<int>(where);
     }
   }
-  for (int c0 = 0; c0 < 32; c0 += LPT) {
-    if (!__any_sync(0xFFFFFFFFu, n <= 32 && c0 < n)) break;
-    if (n <= 32 && c0 + sl < n) {
-      const uint64_t own = s_cand[c0 + sl];
-      int before = 0;
-#pragma unroll 4
-      for (int j = 0; j < n; ++j) before += s_cand[j] > own ? 1 : 0;
-      if (before < a.k) s_expert[before] = static_cast<int>(~static_cast<uint32_t>(own));
+  const int most = few ? n : 0;
+  for (int c = sl; c < most + (most & 1); c += LPT) {  // (an even number: one of 0 is never before)
+    uint64_t w = 0;
+    if (c < most) {
+      const int e = cand[c];
+      const float b = a.bias ? a.bias[e] : 0.0f;  // (the sums of +0 are never -0)
+      w = static_cast<uint64_t>(sort_key(load_logit<DT>(a.logits, row + e) + b + 0.0f)) << 32 |
+          static_cast<uint32_t>(~e);
     }
+    word[c] = w;
+  }
+  __syncwarp();
+  constexpr int kPass = LPT < 16 ? 16 : LPT, kOwn = kPass / LPT;
+  for (int c0 = 0; c0 < kCand; c0 += kPass) {
+    if (!__any_sync(0xFFFFFFFFu, c0 < most)) break;
+    uint64_t own[kOwn];
+    int before[kOwn];
+#pragma unroll
+    for (int q = 0; q < kOwn; ++q) {
+      const int c = c0 + q * LPT + sl;
+      own[q] = c < most ? word[c] : 0;
+      before[q] = c < most ? 0 : a.k;
+    }
+#pragma unroll 2
+    for (int j = 0; j < most; j += 2) {
+      const ulonglong2 w = *reinterpret_cast<const ulonglong2*>(word + j);
+#pragma unroll
+      for (int q = 0; q < kOwn; ++q) before[q] += (w.x > own[q] ? 1 : 0) + (w.y > own[q] ? 1 : 0);
+    }
+#pragma unroll
+    for (int q = 0; q < kOwn; ++q)
+      if (before[q] < a.k) s_expert[before[q]] = static_cast<int>(~static_cast<uint32_t>(own[q]));
   }
   __syncwarp();
   const bool on = sl < a.k;
@@ -312,16 +383,19 @@ template <int DT, int V, int VL, int LPT>
 __global__ void __launch_bounds__(kSmallThreads) route_small_kernel(const RouteArgs a) {
   extern __shared__ uint32_t s_cnt[];  // [warps][G], the entries' experts, [G] bases
   __shared__ uint32_t s_scan[33];
-  __shared__ uint64_t s_cand[kSmallThreads / 32][66];
+  __shared__ ChoiceScratch<LPT> s_cand[kSmallThreads / 32];
   ptx::griddep_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   int* s_expert = reinterpret_cast<int*>(s_cnt + warps * a.G);
   const int T = static_cast<int>(a.T), n = T * a.k;
-  float bias[V];
-  load_bias<V, VL, LPT>(a.bias, a.G, lane % LPT, bias);
+  __shared__ alignas(16) float s_bias[V * LPT];
+  if (a.bias) {
+    stage_bias<V, VL, LPT>(a, s_bias);
+    __syncthreads();
+  }
   constexpr int kTok = 32 / LPT;  // tokens of a warp at a time
   for (int t = kTok * warp; t < T; t += kTok * warps)
-    choose_and_write<DT, V, VL, LPT>(a, t, T, lane, bias, s_cand[warp], s_expert + t * a.k);
+    choose_and_write<DT, V, VL, LPT>(a, t, T, lane, s_bias, &s_cand[warp], s_expert + t * a.k);
   __syncthreads();
   const int run = ((n + warps - 1) / warps + 31) / 32 * 32;
   auto key = [&](int e) { return s_expert[e]; };
@@ -350,27 +424,28 @@ __global__ void __launch_bounds__(kSmallThreads) route_small_kernel(const RouteA
 // counter per warp and expert gives the ranks in order, without atomics; the warps' counts are then
 // added up in their order.
 template <int DT, int V, int VL, int LPT>
-__global__ void __launch_bounds__(32 * kWarps, V <= 16 ? 4 : 2) route_choose_kernel(const RouteArgs a) {
+__global__ void __launch_bounds__(32 * kWarps, LPT < 32 ? 4 : 2) route_choose_kernel(const RouteArgs a) {
   extern __shared__ uint32_t s_cnt[];  // [warps][G]
-  __shared__ uint64_t s_cand[kWarps][66];
-  __shared__ int s_expert[kWarps][kMaxRouteTopK];  // (two tokens of at most 16 or one)
+  __shared__ ChoiceScratch<LPT> s_cand[kWarps];
+  __shared__ int s_expert[kWarps][kMaxRouteTopK];  // (four tokens of at most 8, two of 16, one)
   ptx::griddep_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  __shared__ alignas(16) float s_bias[V * LPT];
   for (int i = threadIdx.x; i < kWarps * a.G; i += blockDim.x) s_cnt[i] = 0;
+  if (a.bias) stage_bias<V, VL, LPT>(a, s_bias);
   if (blockIdx.x == 0 && threadIdx.x == 0) a.hdr->status = 0;
   __syncthreads();
   constexpr int kTok = 32 / LPT;  // tokens of a warp at a time
   const int64_t b0 = static_cast<int64_t>(blockIdx.x) * a.tokens_per_block;
   const int64_t b1 = b0 + a.tokens_per_block < a.T ? b0 + a.tokens_per_block : a.T;
-  const int64_t run = a.tokens_per_block / kWarps;  // (a multiple of the warps, see route_blocks)
-  const int64_t t0 = b0 + warp * run < b1 ? b0 + warp * run : b1;
-  const int64_t t1 = t0 + run < b1 ? t0 + run : b1;
+  // whole steps of a warp, shared out evenly
+  const int steps = (a.tokens_per_block + kTok - 1) / kTok;
+  const int64_t w0 = b0 + steps * warp / kWarps * kTok, w1 = b0 + steps * (warp + 1) / kWarps * kTok;
+  const int64_t t0 = w0 < b1 ? w0 : b1, t1 = w1 < b1 ? w1 : b1;
   uint32_t* mine = s_cnt + warp * a.G;
-  float bias[V];
-  load_bias<V, VL, LPT>(a.bias, a.G, lane % LPT, bias);
   for (int64_t t = t0; t < t1; t += kTok) {
     const int e =
-        choose_and_write<DT, V, VL, LPT>(a, t, t1, lane, bias, s_cand[warp], s_expert[warp]);
+        choose_and_write<DT, V, VL, LPT>(a, t, t1, lane, s_bias, &s_cand[warp], s_expert[warp]);
     uint32_t r = 0;
 #pragma unroll
     for (int s = 0; s < kTok; ++s) {
@@ -564,9 +639,13 @@ cudaError_t launch_route_v(const RouteArgs& a, cudaStream_t stream) {
     // threads for the tokens, no more: fewer counters to clear
     const int64_t warps = (a.T * LPT + 31) / 32;
     const int threads = static_cast<int>(warps < kSmallThreads / 32 ? warps : kSmallThreads / 32) * 32;
-    const size_t smem = (static_cast<size_t>(threads / 32 + 1) * a.G + a.T * a.k) * 4;
+    // (the last step of a warp may leave choices for tokens past the last)
+    const size_t smem =
+        (static_cast<size_t>(threads / 32 + 1) * a.G + (a.T + 32 / LPT - 1) * a.k) * 4;
     auto kern = route_small_kernel<DT, V, VL, LPT>;
-    if (smem > 32 * 1024) {
+    constexpr size_t kStatic =
+        kSmallThreads / 32 * sizeof(ChoiceScratch<LPT>) + V * LPT * 4 + 33 * 4 + 60;
+    if (smem + kStatic > 48 * 1024) {
       cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              static_cast<int>(smem));
       if (err != cudaSuccess) return err;
@@ -593,7 +672,14 @@ cudaError_t launch_route_t(const RouteArgs& a, cudaStream_t stream) {
 
 template <int DT>
 cudaError_t launch_route_d(const RouteArgs& a, cudaStream_t stream) {
-  // two tokens a warp where a half's lanes are enough for the choices and the logits
+  // four or two tokens a warp where a quarter's or half's lanes are enough for the choices and the
+  // logits
+  if (a.k <= 8 && a.G <= 256) {
+    if (a.G <= 32) return launch_route_t<DT, 4, 8>(a, stream);
+    if (a.G <= 64) return launch_route_t<DT, 8, 8>(a, stream);
+    if (a.G <= 128) return launch_route_t<DT, 16, 8>(a, stream);
+    return launch_route_t<DT, 32, 8>(a, stream);
+  }
   if (a.k <= 16 && a.G <= 512) {
     if (a.G <= 32) return launch_route_t<DT, 2, 16>(a, stream);
     if (a.G <= 64) return launch_route_t<DT, 4, 16>(a, stream);
@@ -621,8 +707,7 @@ void route_blocks(int64_t T, int64_t G, int64_t k, int* blocks, int* tokens_per_
     return;
   }
   int64_t per = (T + kMaxBlocks - 1) / kMaxBlocks;
-  // whole warps of two tokens each
-  per = (per + 2 * kWarps - 1) / (2 * kWarps) * (2 * kWarps);
+  per = (per + 3) / 4 * 4;  // whole steps of a warp
   *tokens_per_block = static_cast<int>(per);
   *blocks = static_cast<int>((T + per - 1) / per);
 }
