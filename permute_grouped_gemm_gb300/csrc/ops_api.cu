@@ -221,9 +221,10 @@ int run_adapter_prep(const AdapterPlan& p, const AdapterTables& t, bool by_first
 }
 
 // u = scale * x f[adapter] for f [A, K, R], into rows of `u`, in the adapters' order.
-int run_shrink(const AdapterPlan& p, const AdapterTables& t, const HostEnv& env, const void* x,
-               const void* f, const float* scale, void* u, int64_t T, int64_t K, int64_t R,
-               int64_t A, int dtype, cudaStream_t stream) {
+// (early, late: see launch_order in pgg_ops_mma.cuh)
+int run_shrink(const AdapterPlan& p, const AdapterTables& t, const HostEnv& env, bool early,
+               bool late, const void* x, const void* f, const float* scale, void* u, int64_t T,
+               int64_t K, int64_t R, int64_t A, int dtype, cudaStream_t stream) {
   RowsArgs a;
   std::memset(&a, 0, sizeof(a));
   a.x = x;
@@ -241,6 +242,8 @@ int run_shrink(const AdapterPlan& p, const AdapterTables& t, const HostEnv& env,
   a.max_row_blocks = p.max_row_blocks;
   a.padded = p.padded;
   a.range = t.range;
+  a.early = early ? 1 : 0;
+  a.late = late ? 1 : 0;
   a.hold_release = env.hold_release;
   a.wait_limit_ns = env.wait_limit_ns;
   if (p.variant != kVariantSimt && aligned(x, 16) && aligned(f, 16)) {
@@ -272,8 +275,9 @@ int run_few_shrink(const AdapterTables& t, const void* x, const void* f, const i
 // y = x W + u f[adapter]^T for W [K, N] (transposed: [N, K]) and f [A, N, R]. by_token: the
 // adapter ids when u is fp32 in the tokens' order, else null.
 int run_adapt(const AdapterPlan& p, const AdapterTables& t, const HostEnv& env, bool transposed,
-              const int64_t* by_token, const void* x, const void* w, const void* u, const void* f, void* y, int64_t T,
-              int64_t K, int64_t N, int64_t R, int64_t A, int dtype, cudaStream_t stream) {
+              bool early, const int64_t* by_token, const void* x, const void* w, const void* u,
+              const void* f, void* y, int64_t T, int64_t K, int64_t N, int64_t R, int64_t A,
+              int dtype, cudaStream_t stream) {
   RowsArgs a;
   std::memset(&a, 0, sizeof(a));
   a.x = x;
@@ -294,6 +298,7 @@ int run_adapt(const AdapterPlan& p, const AdapterTables& t, const HostEnv& env, 
   a.R = static_cast<int32_t>(R);
   a.batch = T;
   a.max_row_blocks = p.max_row_blocks;
+  a.early = early ? 1 : 0;
   a.hold_release = env.hold_release;
   a.wait_limit_ns = env.wait_limit_ns;
   const RowsMode mode = transposed ? kAdaptT : kAdapt;
@@ -591,13 +596,13 @@ int pgg_adapters_execute(const void* x, const void* weight, const void* a, const
       aligned(b, 16)) {
     rc = run_few_shrink(t, x, a, adapter, scale, u, T, K, R, A, dtype, s);
     if (rc != PGG_OK) return rc;
-    return run_adapt(p, t, env, false, adapter, x, weight, u, b, y, T, K, N, R, A, dtype, s);
+    return run_adapt(p, t, env, false, false, adapter, x, weight, u, b, y, T, K, N, R, A, dtype, s);
   }
   rc = run_adapter_prep(p, t, true, adapter, T, A, s);
   if (rc != PGG_OK) return rc;
-  rc = run_shrink(p, t, env, x, a, scale, u, T, K, R, A, dtype, s);
+  rc = run_shrink(p, t, env, false, false, x, a, scale, u, T, K, R, A, dtype, s);
   if (rc != PGG_OK) return rc;
-  return run_adapt(p, t, env, false, nullptr, x, weight, u, b, y, T, K, N, R, A, dtype, s);
+  return run_adapt(p, t, env, false, false, nullptr, x, weight, u, b, y, T, K, N, R, A, dtype, s);
 }
 
 int pgg_adapters_grad_workspace_size(int64_t T, int64_t K, int64_t N, int64_t R, int64_t A,
@@ -644,12 +649,15 @@ int pgg_adapters_grad(const void* d_y, const void* x, const void* weight, const 
                           kInt32Max / 4;
   rc = run_adapter_prep(p, t, tensor, adapter, T, A, s);
   if (rc != PGG_OK) return rc;
-  rc = run_shrink(p, t, env, x, a, scale, u, T, K, R, A, dtype, s);
+  // u and v need the tables alone, and the factors' gradients u and v alone: each runs beside the
+  // launch before it. 8192 tokens, K 4096, N 2048, R 32: XX us against XX one after another.
+  rc = run_shrink(p, t, env, tensor, false, x, a, scale, u, T, K, R, A, dtype, s);
   if (rc != PGG_OK) return rc;
-  rc = run_shrink(p, t, env, d_y, b, scale, v, T, N, R, A, dtype, s);
+  rc = run_shrink(p, t, env, false, tensor, d_y, b, scale, v, T, N, R, A, dtype, s);
   if (rc != PGG_OK) return rc;
   if (d_x) {
-    rc = run_adapt(p, t, env, true, nullptr, d_y, weight, v, a, d_x, T, N, K, R, A, dtype, s);
+    rc = run_adapt(p, t, env, true, tensor, nullptr, d_y, weight, v, a, d_x, T, N, K, R, A, dtype,
+                   s);
     if (rc != PGG_OK) return rc;
   }
   if (tensor) {
@@ -671,6 +679,7 @@ int pgg_adapters_grad(const void* d_y, const void* x, const void* weight, const 
     o.right_rows = p.rows_u;
     o.A = static_cast<int32_t>(A);
     o.R = static_cast<int32_t>(R);
+    o.late = d_x ? 1 : 0;  // (else the launch before it writes v)
     o.hold_release = env.hold_release;
     o.wait_limit_ns = env.wait_limit_ns;
     return status_of(launch_rows_outer(dtype, o, env.num_sms, s));

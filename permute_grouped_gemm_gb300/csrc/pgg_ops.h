@@ -157,6 +157,7 @@ struct RowsArgs {
   int32_t n_blocks;
   int32_t padded;          // kShrink: fill up an adapter's rows with zeros to a multiple of kRowPad
   const int64_t* adapter;  // few tokens: [T]; u is fp32 in token order then
+  int32_t early, late;     // see launch_order in pgg_ops_mma.cuh
   int32_t hold_release;
   uint64_t wait_limit_ns;
 };
@@ -200,6 +201,7 @@ struct OuterArgs {
   int32_t A, R;
   int32_t blocks0, blocks1;  // 128-column blocks of each (set by the launch)
   uint32_t r_blocks;
+  int32_t late;            // see launch_order in pgg_ops_mma.cuh
   int32_t hold_release;
   uint64_t wait_limit_ns;
 };

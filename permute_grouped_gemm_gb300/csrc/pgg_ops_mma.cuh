@@ -79,6 +79,21 @@ __device__ __forceinline__ void launch_dependents() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
+// A launch and the one behind it that does not read what it writes may run side by side, so that the
+// second fills the multiprocessors that the first leaves idle. The first (early) waits for all
+// before it and then lets the second start; the second (late) starts at once: what it reads was
+// complete when the first let it. It waits for the first before it ends, so that the launch behind
+// both finds both complete.
+__device__ __forceinline__ void launch_order(bool early, bool late) {
+  if (late) return;
+  ptx::griddep_wait();
+  if (early) launch_dependents();
+}
+
+__device__ __forceinline__ void launch_end(bool late) {
+  if (late && blockIdx.x == 0) ptx::griddep_wait();
+}
+
 // p * silu(g) * u for a 16-bit output: the fast exponential and reciprocal, whose error (a few
 // 2^-21) is far below the one rounding of the result.
 __device__ __forceinline__ float gate(float g, float u, float p) {

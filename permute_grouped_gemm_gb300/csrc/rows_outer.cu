@@ -353,7 +353,7 @@ struct OuterMaps {
 template <int DT>
 __global__ void __launch_bounds__(kThreads, 1)
     rows_outer_kernel(const __grid_constant__ OuterMaps maps, const OuterArgs a) {
-  ptx::griddep_wait();
+  launch_order(false, a.late);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
@@ -369,6 +369,7 @@ __global__ void __launch_bounds__(kThreads, 1)
            q += static_cast<int64_t>(gridDim.x) * blockDim.x)
         static_cast<uint16_t*>(a.out[w])[q] = 0;
     }
+    launch_end(a.late);
     return;
   }
   const uint32_t total =
@@ -418,6 +419,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::tc_fence_after_sync();
     ptx::tmem_dealloc(tmem_base, kTmemCols);
   }
+  launch_end(a.late);
 }
 
 }  // namespace

@@ -578,7 +578,7 @@ __global__ void __launch_bounds__(Cfg<NR, PANELS>::kThreads, 1)
     rows_skinny_kernel(const __grid_constant__ CUtensorMap tm_w,
                        const __grid_constant__ CUtensorMap tm_x, const RowsArgs a) {
   using C = Cfg<NR, PANELS>;
-  if (MODE != kAdapt) ptx::griddep_wait();
+  if (MODE != kAdapt) launch_order(a.early, a.late);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
@@ -589,6 +589,7 @@ __global__ void __launch_bounds__(Cfg<NR, PANELS>::kThreads, 1)
 
   if (MODE != kAdapt && routing_failed(a.hdr)) {
     if (MODE == kGated) zero_rows16(a);
+    launch_end(a.late);
     return;
   }
   Walk k;
@@ -647,6 +648,7 @@ __global__ void __launch_bounds__(Cfg<NR, PANELS>::kThreads, 1)
     ptx::tc_fence_after_sync();
     ptx::tmem_dealloc(tmem_base, C::kTmemCols);
   }
+  launch_end(a.late);
 }
 
 // CTAs per tile: the split of K that leaves the fewest steps on the critical path for about

@@ -66,8 +66,9 @@ struct Cfg {
   static constexpr int kStageBytes = kABytes + kBBytes;
   static constexpr int kStages = H == 1 ? 7 : 4;
   static constexpr int kGatherWarps = kStages;
-  // Eight epilogue warps an MMA: two share its lanes' quarter, each half of the columns. (They wait
-  // for their own loads most of the time; with four, the drain of a tile took 19,000 cycles.)
+  // Eight epilogue warps an MMA: two share its lanes' quarter, each half of the columns. (A tile's
+  // drain is bound by its stores, and takes 13,000 cycles with gate_up with four warps as with
+  // eight; eight leave fewer columns a thread to unroll.)
   static constexpr int kEpiWarps = 8 * H;
   static constexpr int kEpiWarp0 = 2 + kGatherWarps;
   static constexpr int kThreads = 32 * (kEpiWarp0 + kEpiWarps);
@@ -606,7 +607,7 @@ __global__ void __launch_bounds__(Cfg<H>::kThreads, 1)
                      const __grid_constant__ CUtensorMap tm_b,
                      const __grid_constant__ CUtensorMap tm_x, const RowsArgs a) {
   using C = Cfg<H>;
-  ptx::griddep_wait();  // launched with programmatic serialization: predecessors done
+  launch_order(a.early, false);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
