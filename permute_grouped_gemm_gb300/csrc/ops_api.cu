@@ -275,9 +275,9 @@ int run_few_shrink(const AdapterTables& t, const void* x, const void* f, const i
 // y = x W + u f[adapter]^T for W [K, N] (transposed: [N, K]) and f [A, N, R]. by_token: the
 // adapter ids when u is fp32 in the tokens' order, else null.
 int run_adapt(const AdapterPlan& p, const AdapterTables& t, const HostEnv& env, bool transposed,
-              bool early, const int64_t* by_token, const void* x, const void* w, const void* u,
-              const void* f, void* y, int64_t T, int64_t K, int64_t N, int64_t R, int64_t A,
-              int dtype, cudaStream_t stream) {
+              bool early, bool late, const int64_t* by_token, const void* x, const void* w,
+              const void* u, const void* f, void* y, int64_t T, int64_t K, int64_t N, int64_t R,
+              int64_t A, int dtype, cudaStream_t stream) {
   RowsArgs a;
   std::memset(&a, 0, sizeof(a));
   a.x = x;
@@ -299,6 +299,7 @@ int run_adapt(const AdapterPlan& p, const AdapterTables& t, const HostEnv& env, 
   a.batch = T;
   a.max_row_blocks = p.max_row_blocks;
   a.early = early ? 1 : 0;
+  a.late = late ? 1 : 0;
   a.hold_release = env.hold_release;
   a.wait_limit_ns = env.wait_limit_ns;
   const RowsMode mode = transposed ? kAdaptT : kAdapt;
@@ -596,13 +597,15 @@ int pgg_adapters_execute(const void* x, const void* weight, const void* a, const
       aligned(b, 16)) {
     rc = run_few_shrink(t, x, a, adapter, scale, u, T, K, R, A, dtype, s);
     if (rc != PGG_OK) return rc;
-    return run_adapt(p, t, env, false, false, adapter, x, weight, u, b, y, T, K, N, R, A, dtype, s);
+    return run_adapt(p, t, env, false, false, false, adapter, x, weight, u, b, y, T, K, N, R, A,
+                     dtype, s);
   }
   rc = run_adapter_prep(p, t, true, adapter, T, A, s);
   if (rc != PGG_OK) return rc;
-  rc = run_shrink(p, t, env, false, false, x, a, scale, u, T, K, R, A, dtype, s);
+  rc = run_shrink(p, t, env, true, false, x, a, scale, u, T, K, R, A, dtype, s);
   if (rc != PGG_OK) return rc;
-  return run_adapt(p, t, env, false, false, nullptr, x, weight, u, b, y, T, K, N, R, A, dtype, s);
+  return run_adapt(p, t, env, false, false, true, nullptr, x, weight, u, b, y, T, K, N, R, A,
+                   dtype, s);
 }
 
 int pgg_adapters_grad_workspace_size(int64_t T, int64_t K, int64_t N, int64_t R, int64_t A,
@@ -653,10 +656,10 @@ int pgg_adapters_grad(const void* d_y, const void* x, const void* weight, const 
   // launch before it. 8192 tokens, K 4096, N 2048, R 32: XX us against XX one after another.
   rc = run_shrink(p, t, env, tensor, false, x, a, scale, u, T, K, R, A, dtype, s);
   if (rc != PGG_OK) return rc;
-  rc = run_shrink(p, t, env, false, tensor, d_y, b, scale, v, T, N, R, A, dtype, s);
+  rc = run_shrink(p, t, env, tensor, tensor, d_y, b, scale, v, T, N, R, A, dtype, s);
   if (rc != PGG_OK) return rc;
   if (d_x) {
-    rc = run_adapt(p, t, env, true, tensor, nullptr, d_y, weight, v, a, d_x, T, N, K, R, A, dtype,
+    rc = run_adapt(p, t, env, true, tensor, true, nullptr, d_y, weight, v, a, d_x, T, N, K, R, A, dtype,
                    s);
     if (rc != PGG_OK) return rc;
   }

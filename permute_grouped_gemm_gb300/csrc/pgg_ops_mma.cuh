@@ -85,8 +85,7 @@ __device__ __forceinline__ void launch_dependents() {
 // complete when the first let it. It waits for the first before it ends, so that the launch behind
 // both finds both complete.
 __device__ __forceinline__ void launch_order(bool early, bool late) {
-  if (late) return;
-  ptx::griddep_wait();
+  if (!late) ptx::griddep_wait();
   if (early) launch_dependents();
 }
 

@@ -294,6 +294,7 @@ __device__ void x_gatherer(uint8_t* smem, WideCtl* ctl, const RowsArgs& a, const
   const int nks = main_steps(a);
   uint32_t phase = 0;
   bool failed = false;
+  bool u_there = a.late == 0;
   int kb = w;  // the warp's next step, counted from the start of tile t
   // this lane's rows (lane >> 3) + 4 q of the tile: the x row's offset in
   // 16-byte units, or kNoRow past the block
@@ -346,6 +347,10 @@ __device__ void x_gatherer(uint8_t* smem, WideCtl* ctl, const RowsArgs& a, const
         }
       } else {
         // rows of u that belong to the step's adapter; zeros elsewhere
+        if (!u_there) {
+          ptx::griddep_wait();
+          u_there = true;
+        }
         int r0;
         const int4 seg = segment_of(a, x, kb - nks, &r0);
         const int64_t r = r0 + c * 8;
@@ -607,7 +612,9 @@ __global__ void __launch_bounds__(Cfg<H>::kThreads, 1)
                      const __grid_constant__ CUtensorMap tm_b,
                      const __grid_constant__ CUtensorMap tm_x, const RowsArgs a) {
   using C = Cfg<H>;
-  launch_order(a.early, false);
+  // late: u alone is not there yet. The gather warps wait before they read it, and the first
+  // epilogue warp before it lets the next launch start.
+  if (!a.late) launch_order(a.early, false);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
@@ -617,6 +624,7 @@ __global__ void __launch_bounds__(Cfg<H>::kThreads, 1)
 
   if (routing_failed(a.hdr)) {  // the result is defined as zeros
     zero_rows16(a);
+    if (a.late) ptx::griddep_wait();
     return;
   }
   const uint32_t row_blocks = MODE == kGated
@@ -659,6 +667,7 @@ __global__ void __launch_bounds__(Cfg<H>::kThreads, 1)
   } else if (warp < 2 + C::kGatherWarps) {
     x_gatherer<MODE, H>(smem, ctl, a, sc, rank);
   } else if (warp >= C::kEpiWarp0) {
+    if (a.late && warp == C::kEpiWarp0) launch_order(a.early, false);
     epilogue<DT, MODE, H>(ctl, tmem_base, a, sc, rank);
   }
 
