@@ -27,13 +27,16 @@ constexpr int kVariantSimt = 3;  // FP32 pipes: any dtype, size and alignment
 constexpr double kSkinnyRows = 104.0;
 
 // Adapters: whether the shared weight is streamed for blocks of 64 tokens in the caller's order,
-// with the low-rank part on the FP32 pipes (its cost grows with T R). (64 adapters mixed; K 7168,
-// N 4096, R 16: 256 tokens take 52 us this way and 111 in sorted blocks of 256; K = N = 4096, R 64:
-// 128 tokens 62 and 86, 192 tokens 95 and 90.) Beyond one block of tokens only while the tiles of 64
-// tokens x 128 columns fit the 152 SMs at once (K 2048, N 5120: 192 tokens 35 and 36, 256 53 and 37).
+// with the low-rank part on the FP32 pipes (its cost grows with T R), or the tokens are sorted and
+// the low-rank part is more steps of the product (0.4 to 0.7 us an adapter). Both sides: K 7168,
+// N 4096, R 16, 256 tokens: 4 adapters 48 us and 53, 64 adapters 52 and 109; K = N = 4096, R 32,
+// 32 adapters, 256 tokens: 56 and 64; R 64, 16 adapters: 64 tokens 32 and 44, 96 tokens 51 and 45;
+// K 2048, N 5120, R 64: 128 tokens 79 and 40. Beyond one block of tokens only while the tiles of 64
+// tokens x 128 columns fit the 152 SMs at once (K 2048, N 5120, R 32: 192 tokens 42 and 51, 256 67
+// and 50).
 bool few_tokens(int64_t T, int64_t N, int64_t R) {
-  return T <= 256 && T * R <= 8192 &&
-         (T <= 64 || (T + 63) / 64 * ((N + 127) / 128) <= 152);
+  if (T <= 64) return T * R <= 8192;
+  return T <= 256 && R <= 32 && (T + 63) / 64 * ((N + 127) / 128) <= 152;
 }
 
 int few_token_block(int64_t T) { return T <= 16 ? 16 : T <= 32 ? 32 : 64; }
@@ -653,7 +656,7 @@ int pgg_adapters_grad(const void* d_y, const void* x, const void* weight, const 
   rc = run_adapter_prep(p, t, tensor, adapter, T, A, s);
   if (rc != PGG_OK) return rc;
   // u and v need the tables alone, and the factors' gradients u and v alone: each runs beside the
-  // launch before it. 8192 tokens, K 4096, N 2048, R 32: XX us against XX one after another.
+  // launch before it. 8192 tokens, K 4096, N 2048, R 32: 149 us against 172 one after another.
   rc = run_shrink(p, t, env, tensor, false, x, a, scale, u, T, K, R, A, dtype, s);
   if (rc != PGG_OK) return rc;
   rc = run_shrink(p, t, env, tensor, tensor, d_y, b, scale, v, T, N, R, A, dtype, s);
