@@ -595,7 +595,7 @@ int pgg_swiglu_grad(const void* d_h, const void* gate_up, const float* probs,
  *   y        device, [T, N] of `dtype`
  *
  * Tokens may be in any order. What one adapter's weights hold (infinities, NaN)
- * does not reach the tokens of another.
+ * does not reach the tokens of another. No output may overlap an input.
  */
 int pgg_adapters_workspace_size(int64_t T, int64_t K, int64_t N, int64_t R, int64_t A,
                                 pgg_dtype dtype, size_t* workspace_bytes);
@@ -623,7 +623,8 @@ int pgg_adapters_plan(int64_t T, int64_t K, int64_t N, int64_t R, int64_t A, pgg
  *     d_b[ad] = sum over its tokens of d_y^T (scale x a[ad])  [A, N, R]
  *
  * all of `dtype`; an adapter without tokens gets zeros. Sums are fp32; v and
- * scale x a[ad] are rounded once to `dtype` before the second product.
+ * scale x a[ad] are rounded once to `dtype` before the second product. No output
+ * may overlap an input: d_x, d_a and d_b are written side by side.
  */
 int pgg_adapters_grad_workspace_size(int64_t T, int64_t K, int64_t N, int64_t R, int64_t A,
                                      pgg_dtype dtype, size_t* workspace_bytes);

@@ -285,3 +285,68 @@ def test_neighbouring_and_scattered_rows_in_one_call(dtype):
     check_grad(s)
     s["adapter"] = ad.flip(0).contiguous()
     check(s)
+
+
+# ---------------------------------------------------------------- launches that run side by side
+
+BESIDE = [
+    (300, 1024, 2048, 16, 9),
+    (700, 4096, 512, 64, 33),
+    (2500, 512, 1024, 32, 3),
+]
+
+
+@pytest.mark.parametrize("size", BESIDE)
+def test_calls_in_a_row_with_one_workspace(size):
+    """Forward and gradient of three inputs (one with an unknown adapter, one without any) again and
+    again into one workspace without a synchronisation: each call finds its own tables, u and v."""
+    T, K, N, R, A = size
+    sets = [inputs(T, K, N, R, A, "bf16", ids, i) for i, ids in enumerate(["mixed", "runs", "-1"])]
+    sets.append(dict(sets[0], adapter=sets[0]["adapter"].clone().fill_(A)))
+    dys = [torch.randn(T, N, device="cuda").bfloat16() for _ in sets]
+    forward = torch.empty(pgg.pgg_adapters_workspace_size(T, K, N, R, A, 2), dtype=torch.uint8,
+                          device="cuda")
+    backward = torch.empty(pgg.pgg_adapters_grad_workspace_size(T, K, N, R, A, 2),
+                           dtype=torch.uint8, device="cuda")
+    want = []
+    for s, dy in zip(sets, dys):
+        y, _ = pgg.adapters(**s)
+        torch.cuda.synchronize()
+        dx, da, db, _ = pgg.adapters_grad(dy, **s)
+        torch.cuda.synchronize()
+        want.append((y, dx, da, db))
+    assert not want[3][0].any() and not want[3][1].any() and not want[3][2].any()
+    for rep in range(4):
+        got = []
+        for s, dy in zip(sets, dys):
+            y, _ = pgg.adapters(**s, workspace=forward)
+            dx, da, db, _ = pgg.adapters_grad(dy, **s, workspace=backward)
+            _, da2, db2, _ = pgg.adapters_grad(dy, **s, need_x=False, workspace=backward)
+            got.append((y, dx, da, db, da2, db2))
+        torch.cuda.synchronize()
+        for g, w in zip(got, want):
+            for a, b in zip(g, w + w[2:]):
+                assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("size", BESIDE[:2])
+def test_in_a_graph(size):
+    T, K, N, R, A = size
+    s = inputs(T, K, N, R, A, "fp16", "mixed", 4)
+    dy = torch.randn(T, N, device="cuda").half()
+    y, fw = pgg.adapters(**s)
+    dx, da, db, bw = pgg.adapters_grad(dy, **s)
+    torch.cuda.synchronize()
+    want = [t.clone() for t in (y, dx, da, db)]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for _ in range(2):
+            pgg.adapters(**s, out=y, workspace=fw)
+            pgg.adapters_grad(dy, **s, d_x=dx, d_a=da, d_b=db, workspace=bw)
+    for _ in range(3):
+        for t in (y, dx, da, db):
+            t.fill_(7)
+        graph.replay()
+    torch.cuda.synchronize()
+    for got, ref in zip((y, dx, da, db), want):
+        assert torch.equal(got, ref)
