@@ -394,13 +394,13 @@ def adapters(x, weight, a, b, adapter, scale=None, out=None, workspace=None, str
     _dense(x, weight, a, b, adapter, scale, out)
     T, K, N, R, A = _adapter_sizes("adapters", x, weight, a, b, adapter, scale)
     _is("out", out, (T, N), x.dtype)
-    dt = dtype_code(x.dtype)
+    dt, dev = dtype_code(x.dtype), x.device
     if workspace is None:
         workspace = torch.empty(pgg_adapters_workspace_size(T, K, N, R, A, dt),
-                                dtype=torch.uint8, device=x.device)
+                                dtype=torch.uint8, device=dev)
     if out is None:
-        out = torch.empty(T, N, dtype=x.dtype, device=x.device)
-    stream = _stream_of(stream, x.device)
+        out = torch.empty(T, N, dtype=x.dtype, device=dev)
+    stream = _stream_of(stream, dev)
     rc = pgg_adapters_execute(x.data_ptr(), weight.data_ptr(), a.data_ptr(), b.data_ptr(),
                               adapter.data_ptr(), scale.data_ptr() if scale is not None else 0,
                               T, K, N, R, A, dt, workspace.data_ptr(),

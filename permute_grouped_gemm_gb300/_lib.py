@@ -6,6 +6,7 @@ fails loudly when the library has not been built."""
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -284,6 +285,18 @@ def pgg_unpermute_grad_apply(permuted, d_out, probs, expandedRowIdx, M, H, batch
                                            perm_grad, probs_grad or None, stream)
 
 
+_sized = []  # the functions below that keep the bytes of the sizes asked for lately
+
+
+def _by_sizes(f):
+    """Keeps a workspace's size by the sizes it belongs to (the call costs more than the rest of
+    a small operator's checks: 1.4 us)."""
+    f = functools.lru_cache(maxsize=512)(f)
+    _sized.append(f)
+    return f
+
+
+@_by_sizes
 def pgg_route_workspace_size(batch, G, topK) -> int:
     out = ctypes.c_size_t(0)
     _check(load().pgg_route_workspace_size(batch, G, topK, ctypes.byref(out)),
@@ -306,6 +319,7 @@ def pgg_route_grad(d_probs, logits, experts, batch, G, topK, dtype, score, renor
                                  renormalize, scale, d_logits, stream)
 
 
+@_by_sizes
 def pgg_swiglu_workspace_size(M, F, K, G, L, batch, topK, rowIdxType, dtype) -> int:
     out = ctypes.c_size_t(0)
     _check(load().pgg_swiglu_workspace_size(M, F, K, G, L, batch, topK, rowIdxType, dtype,
@@ -328,6 +342,7 @@ def pgg_swiglu_execute(x, weight, expandedRowIdx, groupList, probs, M, F, K, G, 
                                      workspace_bytes, h, gate_up or None, stream)
 
 
+@_by_sizes
 def pgg_swiglu_grad_workspace_size(M, batch, topK) -> int:
     out = ctypes.c_size_t(0)
     _check(load().pgg_swiglu_grad_workspace_size(M, batch, topK, ctypes.byref(out)),
@@ -343,6 +358,7 @@ def pgg_swiglu_grad(d_h, gate_up, probs, expandedRowIdx, M, F, batch, topK, rowI
                                   d_probs or None, h or None, stream)
 
 
+@_by_sizes
 def pgg_adapters_workspace_size(T, K, N, R, A, dtype) -> int:
     out = ctypes.c_size_t(0)
     _check(load().pgg_adapters_workspace_size(T, K, N, R, A, dtype, ctypes.byref(out)),
@@ -364,6 +380,7 @@ def pgg_adapters_execute(x, weight, a, b, adapter, scale, T, K, N, R, A, dtype, 
                                        dtype, workspace, workspace_bytes, y, stream)
 
 
+@_by_sizes
 def pgg_adapters_grad_workspace_size(T, K, N, R, A, dtype) -> int:
     out = ctypes.c_size_t(0)
     _check(load().pgg_adapters_grad_workspace_size(T, K, N, R, A, dtype, ctypes.byref(out)),
@@ -393,6 +410,8 @@ def pgg_debug_set_ticket_bias(bias: int):
 
 def pgg_debug_force_variant(variant: int):
     load().pgg_debug_force_variant(variant)
+    for f in _sized:
+        f.cache_clear()
 
 
 def pgg_debug_set_band_k_blocks(k_blocks: int):
