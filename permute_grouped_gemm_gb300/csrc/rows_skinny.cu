@@ -16,7 +16,7 @@
 // A stage is 128 of k (64 for NR = 128): two 64-column panels of the weight by
 // TMA (32 KB) and NR x rows, gathered by token with cp.async or, where they are
 // neighbours, as TMA boxes. With NR = 16 six stages are in flight per SM, 192 KB
-// of weight. The one thread that issues the MMAs is the limit otherwise: a wait,
+// of weight (adapt: four). The one thread that issues the MMAs is the limit otherwise: a wait,
 // four MMAs and a commit took it 0.33 us a 64 of k, everything present; with
 // eight MMAs to a wait and a commit it is 0.2.
 //
@@ -48,7 +48,7 @@ constexpr int kFK = 64;            // reduction of one 128-byte row of x
 constexpr int kEpiWarps = 4;
 constexpr int kMaxSplit = 8;
 
-template <int NR, int PANELS>
+template <int MODE, int NR, int PANELS>
 struct Cfg {
   static constexpr int kSub = NR <= 64 ? 2 : 1;       // 64s of k per stage
   static constexpr int kPanel = kSub * kFK * 128;     // k rows x 128 bytes (64 columns)
@@ -57,7 +57,11 @@ struct Cfg {
   static constexpr int kBBytes = kSub * kSubBytes;
   static constexpr int kStageBytes = kABytes + kBBytes;
   static constexpr int kRedBytes = NR * kM * 4;  // S slots of NR / S rows x 128 lanes
-  static constexpr int kFit = (226 * 1024 - 2048 - kRedBytes) / kStageBytes;
+  // adapt: a block of the launch before it (the low-rank rows: 17 KB, 256 threads of 64 registers)
+  // fits beside, so that the weight streams while that one runs: 48 tokens, 64 adapters, K 7168,
+  // N 4096 24.4 -> 24.0 us, 32 tokens of rank 32 28.1 -> 25.9.
+  static constexpr int kRoom = MODE == kAdapt ? 182 * 1024 : 226 * 1024;
+  static constexpr int kFit = (kRoom - 2048 - kRedBytes) / kStageBytes;
   static constexpr int kStages = kFit < 12 ? kFit : 12;
   static constexpr int kThreads = 32 * (2 + kStages + kEpiWarps);
   static constexpr int kTmemCols = 2 * NR < 32 ? 32 : 2 * NR;
@@ -75,9 +79,9 @@ struct Ctl {
   int abort;
 };
 
-template <int NR, int PANELS>
+template <int MODE, int NR, int PANELS>
 constexpr int smem_bytes() {
-  using C = Cfg<NR, PANELS>;
+  using C = Cfg<MODE, NR, PANELS>;
   return C::kStages * C::kStageBytes + C::kRedBytes +
          static_cast<int>(sizeof(Ctl<C::kStages>)) + 1024;
 }
@@ -140,10 +144,10 @@ __device__ __forceinline__ bool skipped(const RowsArgs& a, const Tile& x) {
 }
 
 template <int MODE, int NR, int PANELS>
-__device__ void w_producer(uint8_t* smem, Ctl<Cfg<NR, PANELS>::kStages>* ctl,
+__device__ void w_producer(uint8_t* smem, Ctl<Cfg<MODE, NR, PANELS>::kStages>* ctl,
                            const CUtensorMap* tm_w, const CUtensorMap* tm_x, const RowsArgs& a,
                            const Walk& k) {
-  using C = Cfg<NR, PANELS>;
+  using C = Cfg<MODE, NR, PANELS>;
   const uint64_t lim = a.wait_limit_ns;
   volatile int* abort = &ctl->abort;
   int stage = 0;
@@ -194,9 +198,9 @@ __device__ void w_producer(uint8_t* smem, Ctl<Cfg<NR, PANELS>::kStages>* ctl,
 
 // Gather warp w fills stage slot w: rows (lane >> 3) + 4 q, 16-byte chunk lane & 7.
 template <int MODE, int NR, int PANELS>
-__device__ void x_gatherer(uint8_t* smem, Ctl<Cfg<NR, PANELS>::kStages>* ctl, const RowsArgs& a,
+__device__ void x_gatherer(uint8_t* smem, Ctl<Cfg<MODE, NR, PANELS>::kStages>* ctl, const RowsArgs& a,
                            const Walk& k) {
-  using C = Cfg<NR, PANELS>;
+  using C = Cfg<MODE, NR, PANELS>;
   const uint64_t lim = a.wait_limit_ns;
   volatile int* abort = &ctl->abort;
   const int w = (threadIdx.x >> 5) - 2;
@@ -267,9 +271,9 @@ __device__ void x_gatherer(uint8_t* smem, Ctl<Cfg<NR, PANELS>::kStages>* ctl, co
 }
 
 template <int DT, int MODE, int NR, int PANELS>
-__device__ void mma_issuer(uint8_t* smem, Ctl<Cfg<NR, PANELS>::kStages>* ctl, uint32_t tmem_base,
+__device__ void mma_issuer(uint8_t* smem, Ctl<Cfg<MODE, NR, PANELS>::kStages>* ctl, uint32_t tmem_base,
                            const RowsArgs& a, const Walk& k) {
-  using C = Cfg<NR, PANELS>;
+  using C = Cfg<MODE, NR, PANELS>;
   constexpr uint32_t kFmt = DT == PGG_BF16 ? 1u : 0u;
   constexpr uint32_t idesc = ptx::idesc_make(kFmt, kM, NR) | (1u << 15);  // A MN-major
   const uint64_t lim = a.wait_limit_ns;
@@ -463,7 +467,7 @@ __device__ __forceinline__ void low_rank(const RowsArgs& a, const Tile& x, int j
 }
 
 template <int DT, int MODE, int NR, int PANELS>
-__device__ void epilogue(Ctl<Cfg<NR, PANELS>::kStages>* ctl, float* red, uint32_t tmem_base,
+__device__ void epilogue(Ctl<Cfg<MODE, NR, PANELS>::kStages>* ctl, float* red, uint32_t tmem_base,
                          const RowsArgs& a, const Walk& k, uint32_t rank, uint32_t S) {
   const uint64_t lim = a.wait_limit_ns;
   volatile int* abort = &ctl->abort;
@@ -574,10 +578,10 @@ __device__ void epilogue(Ctl<Cfg<NR, PANELS>::kStages>* ctl, float* red, uint32_
 }
 
 template <int DT, int MODE, int NR, int PANELS>
-__global__ void __launch_bounds__(Cfg<NR, PANELS>::kThreads, 1)
+__global__ void __launch_bounds__(Cfg<MODE, NR, PANELS>::kThreads, 1)
     rows_skinny_kernel(const __grid_constant__ CUtensorMap tm_w,
                        const __grid_constant__ CUtensorMap tm_x, const RowsArgs a) {
-  using C = Cfg<NR, PANELS>;
+  using C = Cfg<MODE, NR, PANELS>;
   if (MODE != kAdapt) launch_order(a.early, a.late);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -672,8 +676,8 @@ int choose_split(int64_t tiles, int nks, int NR, int num_sms) {
 template <int DT, int MODE, int NR, int PANELS>
 cudaError_t launch_t(const CUtensorMap (&tm)[2], const RowsArgs& a, int64_t tiles, int num_sms,
                      cudaStream_t stream) {
-  using C = Cfg<NR, PANELS>;
-  constexpr int smem = smem_bytes<NR, PANELS>();
+  using C = Cfg<MODE, NR, PANELS>;
+  constexpr int smem = smem_bytes<MODE, NR, PANELS>();
   static_assert(smem <= 227 * 1024, "shared memory per CTA");
   auto kern = rows_skinny_kernel<DT, MODE, NR, PANELS>;
   const int nks = static_cast<int>((a.K + C::kSub * kFK - 1) / (C::kSub * kFK));
