@@ -16,9 +16,9 @@
 // A stage is 128 of k (64 for NR = 128): two 64-column panels of the weight by
 // TMA (32 KB) and NR x rows, gathered by token with cp.async or, where they are
 // neighbours, as TMA boxes. With NR = 16 six stages are in flight per SM, 192 KB
-// of weight (adapt: four). The one thread that issues the MMAs is the limit otherwise: a wait,
-// four MMAs and a commit took it 0.33 us a 64 of k, everything present; with
-// eight MMAs to a wait and a commit it is 0.2.
+// of weight (adapt: four). The one thread that issues the MMAs is the limit
+// otherwise: a wait, four MMAs and a commit took it 0.33 us a 64 of k, everything
+// present; with eight MMAs to a wait and a commit it is 0.2.
 //
 // adapt with few tokens: rows stay in the caller's order, and the low-rank part
 // is added in fp32 by the epilogue warps, which work it out from a row's u and

@@ -206,8 +206,8 @@ __device__ __forceinline__ uint32_t w_bytes(const RowsArgs& a, const Tile& x, ui
 
 template <int MODE, int H>
 __device__ void w_producer(uint8_t* smem, WideCtl* ctl, const CUtensorMap* tm_w,
-                           const CUtensorMap* tm_b, const CUtensorMap* tm_x, const RowsArgs& a, const Schedule& sc,
-                           uint32_t rank) {
+                           const CUtensorMap* tm_b, const CUtensorMap* tm_x, const RowsArgs& a,
+                           const Schedule& sc, uint32_t rank) {
   using C = Cfg<H>;
   const uint64_t lim = a.wait_limit_ns;
   volatile int* abort = &ctl->abort;
