@@ -596,8 +596,9 @@ int pgg_adapters_execute(const void* x, const void* weight, const void* a, const
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const AdapterTables t = tables_of(p, workspace);
   void* u = static_cast<char*>(workspace) + p.u;
+  // (the few-token form writes y eight bytes at a time)
   if (p.variant == kVariantSkinny && aligned(x, 16) && aligned(weight, 16) && aligned(a, 16) &&
-      aligned(b, 16)) {
+      aligned(b, 16) && aligned(y, 8)) {
     rc = run_few_shrink(t, x, a, adapter, scale, u, T, K, R, A, dtype, s);
     if (rc != PGG_OK) return rc;
     return run_adapt(p, t, env, false, false, false, adapter, x, weight, u, b, y, T, K, N, R, A,
