@@ -20,6 +20,7 @@
 #include <cstdint>
 
 #include "pgg_ops.h"
+#include "pgg_ops_cluster.cuh"
 #include "pgg_ops_mma.cuh"
 #include "pgg_ptx.cuh"
 
@@ -32,6 +33,7 @@ constexpr int kMaxR = static_cast<int>(kMaxRank);
 
 template <int DT>
 __global__ void __launch_bounds__(kThreads, 4) few_shrink_kernel(const RowsArgs a) {
+  cluster_started();
   ptx::griddep_wait();
   // all that came before has completed; the launch behind this one reads only the caller's x and
   // weight until its own wait
@@ -109,6 +111,7 @@ __global__ void __launch_bounds__(kThreads, 4) few_shrink_kernel(const RowsArgs 
   __syncthreads();
   if (part < parts) s_mem[part * R + r] = v;
   __syncthreads();
+  cluster_all_started();
   if (tid < R) {
     v = 0.0f;
     for (int i = 0; i < parts; ++i) v += s_mem[i * R + tid];

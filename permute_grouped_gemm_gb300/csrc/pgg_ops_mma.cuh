@@ -7,6 +7,7 @@
 #include <cstdint>
 
 #include "pgg_ops.h"
+#include "pgg_ops_cluster.cuh"
 #include "pgg_ptx.cuh"
 
 namespace pgg {
@@ -67,11 +68,6 @@ __device__ __forceinline__ uint32_t mapa_addr(uint32_t addr, uint32_t rank) {
   uint32_t r;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
   return r;
-}
-
-// A float into the shared memory of a CTA of the cluster (address from ptx::mapa).
-__device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
-  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 
 // Programmatic dependent launch: the launch behind this one may start.
