@@ -22,6 +22,7 @@
 #include <cstdint>
 
 #include "pgg_ops.h"
+#include "pgg_ops_cluster.cuh"
 #include "pgg_ptx.cuh"
 #include "pgg_sort.cuh"
 
@@ -32,11 +33,6 @@ constexpr int kSmallRows = 8192;     // gated product: one block up to here
 constexpr int kSmallGroups = 4096;
 constexpr int64_t kSmallTokens = 65536;  // adapters: one cluster up to here
 constexpr int kCluster = 8;
-
-// A word into the shared memory of a block of the cluster (address from ptx::mapa).
-__device__ __forceinline__ void st_cluster_u32(uint32_t addr, uint32_t v) {
-  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
-}
 
 __device__ __forceinline__ RowInfo row_info(int64_t p, int top_k) {
   RowInfo r;
@@ -283,6 +279,7 @@ __global__ void __launch_bounds__(1024) adapter_prep_small_kernel(const AdapterP
   extern __shared__ uint32_t s_cnt[];
   __shared__ uint32_t s_scan[33];
   __shared__ int s_bad[kCluster];
+  cluster_started();
   ptx::griddep_wait();
   const int G = a.A + 1, warps = blockDim.x >> 5;
   const int C = static_cast<int>(gridDim.x), rank = static_cast<int>(blockIdx.x);  // one cluster
@@ -313,6 +310,7 @@ __global__ void __launch_bounds__(1024) adapter_prep_small_kernel(const AdapterP
   sort_count(s_cnt, G, n, run, key);
   const int g = threadIdx.x;
   // every block's counts to every block
+  cluster_all_started();
   if (g < G) {
     uint32_t c = 0;
     for (int w = 0; w < warps; ++w) c += s_cnt[w * G + g];

@@ -32,6 +32,7 @@ def first(pattern, body):
 
 @pytest.mark.parametrize("source,kernel,through", [
     ("adapters_few.cu", "few_shrink_kernel", None),
+    ("ops_prep.cu", "adapter_prep_small_kernel", None),
     ("rows_skinny.cu", "rows_skinny_kernel", "epilogue<"),
     ("rows_outer.cu", "rows_outer_kernel", "epilogue<"),
     ("rows_wide.cu", "rows_wide_kernel", "w_producer<"),
