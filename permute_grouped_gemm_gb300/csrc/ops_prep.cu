@@ -23,6 +23,7 @@
 
 #include "pgg_ops.h"
 #include "pgg_ops_cluster.cuh"
+#include "pgg_ops_launch.h"
 #include "pgg_ptx.cuh"
 #include "pgg_sort.cuh"
 
@@ -462,12 +463,13 @@ cudaError_t launch_adapter_prep(const AdapterPrepArgs& a, cudaStream_t stream) {
     const size_t smem =
         static_cast<size_t>(threads / 32 + (q.by_first ? 2 : 1) * kCluster + 6) * G * 4 +
         static_cast<size_t>(a.tokens_per_block) * 2;
-    if (smem > 32 * 1024) {
-      cudaError_t err = cudaFuncSetAttribute(
-          adapter_prep_small_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-          static_cast<int>(smem));
-      if (err != cudaSuccess) return err;
-    }
+    // the most of it: 1024 threads and groups (by id), and the keys of kSmallTokens / kCluster tokens
+    constexpr int kMost =
+        (1024 / 32 + kCluster + 6) * static_cast<int>(kMaxAdapters + 1) * 4 +
+        static_cast<int>(kSmallTokens / kCluster) * 2;
+    static SmemLimit limit;
+    const cudaError_t err = allow_smem(&limit, adapter_prep_small_kernel, kMost);
+    if (err != cudaSuccess) return err;
     return launch_pdl(adapter_prep_small_kernel, dim3(a.blocks), dim3(threads), smem, stream,
                       static_cast<unsigned>(a.blocks), q);
   }

@@ -1,6 +1,8 @@
-// Launch shape of a kernel with clusters: how many of its clusters fit the
-// device is asked once per device and cluster size and kept, as device
-// attributes are (the query and the attribute call cost microseconds).
+// What a launch needs of the device, asked or set once per device and kept, as
+// device attributes are (the calls cost microseconds): how many clusters of a
+// kernel fit, and how much dynamic shared memory it may take. That limit is the
+// kernel's, not a launch's: it is set to the most that any call takes, so that
+// calls of several threads do not lower it for each other.
 #pragma once
 
 #include <atomic>
@@ -9,6 +11,23 @@
 #include <cuda_runtime.h>
 
 namespace pgg {
+
+struct SmemLimit {
+  std::atomic<int> set[64] = {};  // by device
+};
+
+// Lets `kern` take up to `most` bytes of dynamic shared memory (one value per kernel).
+template <typename Kern>
+cudaError_t allow_smem(SmemLimit* limit, Kern kern, int most) {
+  int dev = 0;
+  cudaError_t err = cudaGetDevice(&dev);
+  if (err != cudaSuccess) return err;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (limit->set[dev].load()) return cudaSuccess;
+  err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+  if (err == cudaSuccess) limit->set[dev].store(1);
+  return err;
+}
 
 struct ClusterLimits {
   std::atomic<int> fit[64][4] = {};  // [device][log2 of the cluster size], 0 = not asked yet

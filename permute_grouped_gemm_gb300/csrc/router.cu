@@ -27,6 +27,7 @@
 #include <cstdint>
 
 #include "pgg_ops.h"
+#include "pgg_ops_launch.h"
 #include "pgg_ptx.cuh"
 #include "pgg_sort.cuh"
 
@@ -670,13 +671,11 @@ cudaError_t launch_route_v(const RouteArgs& a, cudaStream_t stream) {
     const size_t smem =
         (static_cast<size_t>(threads / 32 + 1) * a.G + (a.T + 32 / LPT - 1) * a.k) * 4;
     auto kern = route_small_kernel<DT, V, VL, LPT>;
-    constexpr size_t kStatic =
-        kSmallThreads / 32 * sizeof(ChoiceScratch<LPT>) + V * LPT * 4 + 33 * 4 + 60;
-    if (smem + kStatic > 48 * 1024) {
-      cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             static_cast<int>(smem));
-      if (err != cudaSuccess) return err;
-    }
+    // (G is at most V LPT, the pairs are at most kSmallEntries, a token's at most LPT)
+    constexpr int kMost = ((kSmallThreads / 32 + 1) * V * LPT + kSmallEntries + 32) * 4;
+    static SmemLimit limit;
+    const cudaError_t err = allow_smem(&limit, kern, kMost);
+    if (err != cudaSuccess) return err;
     return launch_pdl(kern, dim3(1), dim3(threads), smem, stream, 1, a);
   }
   cudaError_t err = launch_pdl(route_choose_kernel<DT, V, VL, LPT>, dim3(a.blocks), dim3(32 * kWarps),
