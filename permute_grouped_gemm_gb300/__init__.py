@@ -207,10 +207,12 @@ def _stream_of(stream, device) -> int:
     return torch._C._cuda_getCurrentRawStream(device.index)
 
 
-def _dense(*tensors):
-    for t in tensors:
-        if t is not None and not (t.is_cuda and t.is_contiguous()):
-            raise ValueError("inputs must be contiguous CUDA tensors")
+def _dense(first, *others):
+    """Every given tensor is contiguous and on the first one's GPU (a kernel takes addresses)."""
+    device = first.get_device()  # -1 on the host
+    for t in (first, *others):
+        if t is not None and (t.get_device() != device or device < 0 or not t.is_contiguous()):
+            raise ValueError("tensors must be contiguous CUDA tensors of one device")
 
 
 def _is(what: str, t, shape, dtype):
@@ -230,7 +232,7 @@ def route(logits, top_k: int, row_idx_type: int = 0, bias=None, score: str = "so
     by their sum with ``renormalize``, times ``scale``. Outputs are allocated when not given.
     """
     import torch
-    _dense(logits, bias, probs, experts, expanded_row_idx, group_list)
+    _dense(logits, bias, probs, experts, expanded_row_idx, group_list, workspace)
     batch, G = logits.shape
     M, dev = batch * top_k, logits.device
     _is("bias", bias, (G,), torch.float32)
@@ -292,7 +294,7 @@ def swiglu(x, weight, expanded_row_idx, group_list, batch: int, top_k: int, row_
     also returns the pre-activations, which ``swiglu_grad`` reads.
     """
     import torch
-    _dense(x, weight, expanded_row_idx, group_list, probs, out, gate_up)
+    _dense(x, weight, expanded_row_idx, group_list, probs, out, gate_up, workspace)
     if expanded_row_idx.dtype != torch.int64 or group_list.dtype != torch.int64:
         raise ValueError("expandedRowIdx and groupList must be int64")
     if x.dtype != weight.dtype:
@@ -330,7 +332,7 @@ def swiglu_grad(d_h, gate_up, expanded_row_idx, top_k: int, row_idx_type: int, p
     ``dx`` and ``dw`` for the gated weight; h (weighted) is the grad_y of ``dw`` for the down
     projection."""
     import torch
-    _dense(d_h, gate_up, expanded_row_idx, probs, d_gate_up, d_probs, h)
+    _dense(d_h, gate_up, expanded_row_idx, probs, d_gate_up, d_probs, h, workspace)
     if expanded_row_idx.dtype != torch.int64:
         raise ValueError("expandedRowIdx must be int64")
     if d_h.dtype != gate_up.dtype:
@@ -391,7 +393,7 @@ def adapters(x, weight, a, b, adapter, scale=None, out=None, workspace=None, str
     scale [A] fp32 (1 when None). Tokens may be in any order.
     """
     import torch
-    _dense(x, weight, a, b, adapter, scale, out)
+    _dense(x, weight, a, b, adapter, scale, out, workspace)
     T, K, N, R, A = _adapter_sizes("adapters", x, weight, a, b, adapter, scale)
     _is("out", out, (T, N), x.dtype)
     dt, dev = dtype_code(x.dtype), x.device
@@ -416,7 +418,7 @@ def adapters_grad(d_y, x, weight, a, b, adapter, scale=None, need_x: bool = True
     """(d_x [T, K] or None, d_a [A, K, R], d_b [A, N, R], workspace) of ``adapters`` from d_y
     [T, N], with the projection frozen. ``need_x`` False leaves d_x out."""
     import torch
-    _dense(d_y, x, weight, a, b, adapter, scale, d_x, d_a, d_b)
+    _dense(d_y, x, weight, a, b, adapter, scale, d_x, d_a, d_b, workspace)
     T, K, N, R, A = _adapter_sizes("adapters_grad", x, weight, a, b, adapter, scale)
     _is("d_y", d_y, (T, N), x.dtype)
     _is("d_x", d_x, (T, K), x.dtype)
