@@ -465,16 +465,22 @@ int pgg_unpermute_grad_apply(const void* permuted, const void* d_out, const void
  * Router: the top-k choice of experts from router logits, the routing weights,
  * and the expanded order that the grouped products of this file read.
  *
- *     key[b, e]  = logits[b, e] + bias[e]        (bias takes part in the choice only)
+ *     s          = softmax(logits[b]) over all G experts, or sigmoid(logits[b])
+ *     key[b, e]  = logits[b, e] + bias[e], or with PGG_BIAS_ON_SCORE s[e] + bias[e]
+ *                  (bias takes part in the choice only)
  *     experts[b] = the topK largest keys in decreasing order, the lowest index
  *                  first among equals
- *     s          = softmax(logits[b]) over all G experts, or sigmoid(logits[b])
  *     probs[b,j] = scale * s[experts[b,j]], or with `renormalize`
  *                  scale * s[experts[b,j]] / sum over the chosen of s
  *     expandedRowIdx, groupList: the pairs p = b * topK + j sorted by
  *                  (experts[b,j], p), in the rowIdxType form, and the experts' counts
  *
- *   logits   device, [batch, G] of `dtype`; -inf masks an expert (weight 0). A
+ *   score    pgg_score, with PGG_BIAS_ON_SCORE added where the bias was learnt
+ *            for the scores (a selection bias that balances the experts' load
+ *            without an auxiliary loss is). Without a bias the choice goes by
+ *            the logits either way.
+ *   logits   device, [batch, G] of `dtype`; -inf masks an expert (weight 0, its key
+ *            -inf whatever the bias). A
  *            token whose experts are all masked takes the lowest indices with
  *            weights 0. A NaN key sorts below every other; a NaN or +inf logit
  *            gives NaN weights, as IEEE arithmetic does; the order stays valid.
@@ -487,7 +493,11 @@ int pgg_unpermute_grad_apply(const void* permuted, const void* d_out, const void
  *
  * Weights are computed in fp32; the order depends on no atomic's order.
  */
-typedef enum { PGG_SCORE_SOFTMAX = 0, PGG_SCORE_SIGMOID = 1 } pgg_score;
+typedef enum {
+  PGG_SCORE_SOFTMAX = 0,
+  PGG_SCORE_SIGMOID = 1,
+  PGG_BIAS_ON_SCORE = 16 /* added to one of them, pgg_route_execute only */
+} pgg_score;
 
 int pgg_route_workspace_size(int64_t batch, int64_t G, int64_t topK, size_t* workspace_bytes);
 

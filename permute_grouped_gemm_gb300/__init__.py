@@ -10,7 +10,7 @@ supplies device memory and the current stream only.
 from __future__ import annotations
 
 from ._lib import (  # noqa: F401
-    CODES, PGG_BF16, PGG_F16, PGG_F32, PGG_SCORE_SIGMOID, PGG_SCORE_SOFTMAX, STATUS, PggError,
+    CODES, PGG_BF16, PGG_BIAS_ON_SCORE, PGG_F16, PGG_F32, PGG_SCORE_SIGMOID, PGG_SCORE_SOFTMAX, STATUS, PggError,
     load, pgg_adapters_execute, pgg_adapters_grad, pgg_adapters_grad_workspace_size,
     pgg_adapters_plan, pgg_adapters_workspace_size, pgg_route_execute, pgg_route_grad, pgg_route_workspace_size,
     pgg_swiglu_execute, pgg_swiglu_grad, pgg_swiglu_grad_workspace_size,
@@ -199,6 +199,9 @@ def _score_code(score: str) -> int:
     return _SCORES[score]
 
 
+_BIAS_ON = {"logits": 0, "scores": PGG_BIAS_ON_SCORE}
+
+
 def _stream_of(stream, device) -> int:
     """Address of ``stream``, or of torch's current stream on ``device``."""
     if stream is not None:
@@ -223,18 +226,23 @@ def _is(what: str, t, shape, dtype):
 
 def route(logits, top_k: int, row_idx_type: int = 0, bias=None, score: str = "softmax",
           renormalize: bool = True, scale: float = 1.0, probs=None, experts=None,
-          expanded_row_idx=None, group_list=None, workspace=None, stream=None):
+          expanded_row_idx=None, group_list=None, workspace=None, stream=None,
+          bias_on: str = "logits"):
     """Top-k routing of logits [batch, G]: (probs [batch, top_k] fp32, experts [batch, top_k]
     int64, expanded_row_idx [batch * top_k] int64, group_list [G] int64, workspace).
 
-    The choice goes by logits + bias (fp32 [G], optional), the lowest index first among
-    equals; probs are the chosen experts' softmax or sigmoid scores without the bias, divided
-    by their sum with ``renormalize``, times ``scale``. Outputs are allocated when not given.
+    The choice goes by logits + bias (fp32 [G], optional), or with ``bias_on="scores"`` by
+    scores + bias, which is what a selection bias learnt for the scores needs (routers that
+    balance their experts' load by a bias have such); the lowest index first among equals.
+    probs are the chosen experts' softmax or sigmoid scores without the bias, divided by their
+    sum with ``renormalize``, times ``scale``. Outputs are allocated when not given.
     """
     import torch
     _dense(logits, bias, probs, experts, expanded_row_idx, group_list, workspace)
     batch, G = logits.shape
     M, dev = batch * top_k, logits.device
+    if bias_on not in _BIAS_ON:
+        raise ValueError("bias_on must be 'logits' or 'scores'")
     _is("bias", bias, (G,), torch.float32)
     _is("probs", probs, (batch, top_k), torch.float32)
     _is("experts", experts, (batch, top_k), torch.int64)
@@ -253,11 +261,11 @@ def route(logits, top_k: int, row_idx_type: int = 0, bias=None, score: str = "so
         group_list = torch.empty(G, dtype=torch.int64, device=dev)
     stream = _stream_of(stream, dev)
     rc = pgg_route_execute(logits.data_ptr(), bias.data_ptr() if bias is not None else 0, batch, G,
-                           top_k, row_idx_type, dtype_code(logits.dtype), _score_code(score),
-                           int(renormalize), scale, workspace.data_ptr(),
-                           workspace.numel() * workspace.element_size(), probs.data_ptr(),
-                           experts.data_ptr(), expanded_row_idx.data_ptr(), group_list.data_ptr(),
-                           stream)
+                           top_k, row_idx_type, dtype_code(logits.dtype),
+                           _score_code(score) + _BIAS_ON[bias_on], int(renormalize), scale,
+                           workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                           probs.data_ptr(), experts.data_ptr(), expanded_row_idx.data_ptr(),
+                           group_list.data_ptr(), stream)
     if rc != 0:
         raise PggError(rc, "pgg_route_execute")
     return probs, experts, expanded_row_idx, group_list, workspace

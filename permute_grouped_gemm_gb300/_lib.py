@@ -13,7 +13,7 @@ import threading
 from . import build as _build
 
 PGG_F32, PGG_F16, PGG_BF16 = 0, 1, 2
-PGG_SCORE_SOFTMAX, PGG_SCORE_SIGMOID = 0, 1
+PGG_SCORE_SOFTMAX, PGG_SCORE_SIGMOID, PGG_BIAS_ON_SCORE = 0, 1, 16
 
 STATUS = {
     0: "PGG_OK", 1: "PGG_ERR_NULL", 2: "PGG_ERR_SHAPE", 3: "PGG_ERR_ATTR", 4: "PGG_ERR_DTYPE",

@@ -1,6 +1,6 @@
 """Builds libpgg.so (the C-ABI library) in-tree with nvcc for sm_103a.
 
-Nineteen translation units compiled in parallel, then linked as a shared
+Twenty translation units compiled in parallel, then linked as a shared
 library with the CUDA runtime linked statically; the driver API is reached at
 run time through cudaGetDriverEntryPointByVersion, so loading the library
 needs no libcuda.
@@ -29,7 +29,8 @@ CHECKS_DIR = os.path.join(OUT_DIR, "checks")
 LIB_CHECKS = os.path.join(CHECKS_DIR, "libpgg_checks.so")
 SOURCES = ["pgg_api.cu", "route_prep.cu", "gmm_dx.cu", "gmm_dx_simt.cu", "gmm_dw.cu",
            "gmm_dw_simt.cu", "gmm_fwd.cu", "gmm_fwd_simt.cu", "unpermute_grad.cu",
-           "gmm_dx_owner.cu", "ops_api.cu", "router.cu", "ops_prep.cu", "ops_simt.cu",
+           "gmm_dx_owner.cu", "ops_api.cu", "router.cu", "router_scores.cu", "ops_prep.cu",
+           "ops_simt.cu",
            "gated_grad.cu", "rows_wide.cu",
            "rows_skinny.cu", "adapters_few.cu", "rows_outer.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -343,7 +343,8 @@ int pgg_route_execute(const void* logits, const float* bias, int64_t batch, int6
     return PGG_ERR_NULL;
   if (!known_dtype(dtype)) return PGG_ERR_DTYPE;
   if (rowIdxType != 0 && rowIdxType != 1) return PGG_ERR_ATTR;
-  if (score != PGG_SCORE_SOFTMAX && score != PGG_SCORE_SIGMOID) return PGG_ERR_ATTR;
+  const int kind = score & ~PGG_BIAS_ON_SCORE;
+  if (kind != PGG_SCORE_SOFTMAX && kind != PGG_SCORE_SIGMOID) return PGG_ERR_ATTR;
   const int rc = check_route(batch, G, topK);
   if (rc != PGG_OK) return rc;
   if (!aligned(logits, static_cast<uintptr_t>(elem_size(dtype))) || !aligned(bias, 4) ||
@@ -366,7 +367,8 @@ int pgg_route_execute(const void* logits, const float* bias, int64_t batch, int6
   a.G = static_cast<int32_t>(G);
   a.k = static_cast<int32_t>(topK);
   a.row_idx_type = rowIdxType;
-  a.sigmoid = score == PGG_SCORE_SIGMOID ? 1 : 0;
+  a.sigmoid = kind == PGG_SCORE_SIGMOID ? 1 : 0;
+  a.bias_on_score = bias && (score & PGG_BIAS_ON_SCORE) ? 1 : 0;
   a.renormalize = renormalize != 0 ? 1 : 0;
   a.hdr = static_cast<WsHeader*>(workspace);
   route_blocks(batch, G, topK, &a.blocks, &a.tokens_per_block);

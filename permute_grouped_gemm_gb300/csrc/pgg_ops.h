@@ -55,6 +55,7 @@ struct RouteArgs {
   int32_t G, k;
   int32_t row_idx_type;
   int32_t sigmoid, renormalize;
+  int32_t bias_on_score;     // (with a bias) the choice goes by score + bias, not logit + bias
   int32_t blocks;            // blocks of the choice and placement launches
   int32_t tokens_per_block;  // tokens of each
 };
@@ -75,6 +76,8 @@ cudaError_t launch_count_scan(uint32_t* counts, int G, int blocks, int64_t* grou
                               cudaStream_t stream);
 void route_blocks(int64_t T, int64_t G, int64_t k, int* blocks, int* tokens_per_block);
 cudaError_t launch_route(int dtype, const RouteArgs& a, cudaStream_t stream);
+cudaError_t launch_route_scores(int dtype, const RouteArgs& a, cudaStream_t stream);  // (bias_on_score)
+cudaError_t launch_route_place(const RouteArgs& a, cudaStream_t stream);
 cudaError_t launch_route_grad(int dtype, const RouteGradArgs& a, int num_sms, cudaStream_t stream);
 
 // ------------------------------------------------------------ tables of the gated product
