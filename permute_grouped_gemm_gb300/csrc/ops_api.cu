@@ -143,7 +143,7 @@ struct AdapterPlan {
   int padded;
   int64_t max_row_blocks, rows_u;
   int blocks, tokens_per_block;
-  size_t off, range, order, padrow, rblist, segs, blkseg, box, counts, u, v, total;
+  size_t off, range, order, rblist, segs, blkseg, box, counts, u, v, total;
 };
 
 int check_adapters(int64_t T, int64_t K, int64_t N, int64_t R, int64_t A, int dtype) {
@@ -169,7 +169,7 @@ int adapter_plan(int64_t T, int64_t K, int64_t N, int64_t R, int64_t A, int dtyp
     // low-rank rows: blocks of 16 when adapters have about that many tokens
     p->rb = !grad && T <= 16 * groups ? 16 : 64;
   }
-  p->padded = grad ? 1 : 0;
+  p->padded = 0;
   p->max_row_blocks = (T + p->rb - 1) / p->rb + groups;
   p->rows_u = grad ? T + (kRowPad - 1) * groups : T;
   const int64_t widest = N > K ? N : K;
@@ -180,7 +180,6 @@ int adapter_plan(int64_t T, int64_t K, int64_t N, int64_t R, int64_t A, int dtyp
   p->off = c.take(8 * (A + 1));
   p->range = c.take(static_cast<int64_t>(sizeof(int4)) * (A + 1));
   p->order = c.take(static_cast<int64_t>(sizeof(RowInfo)) * T);
-  p->padrow = c.take(grad ? static_cast<int64_t>(sizeof(RowInfo)) * p->rows_u : 0);
   p->rblist = c.take(static_cast<int64_t>(sizeof(int4)) * p->max_row_blocks);
   p->segs = c.take(static_cast<int64_t>(sizeof(int4)) * A);
   p->blkseg = c.take(static_cast<int64_t>(sizeof(int2)) * ((T + 255) / 256));
@@ -199,7 +198,6 @@ AdapterTables tables_of(const AdapterPlan& p, void* ws) {
   t.off = reinterpret_cast<int64_t*>(w + p.off);
   t.range = reinterpret_cast<int4*>(w + p.range);
   t.order = reinterpret_cast<RowInfo*>(w + p.order);
-  t.padrow = reinterpret_cast<RowInfo*>(w + p.padrow);
   t.rblist = reinterpret_cast<int4*>(w + p.rblist);
   t.segs = reinterpret_cast<int4*>(w + p.segs);
   t.blkseg = reinterpret_cast<int2*>(w + p.blkseg);
@@ -651,11 +649,12 @@ int pgg_adapters_grad(const void* d_y, const void* x, const void* weight, const 
   void* u = static_cast<char*>(workspace) + p.u;
   void* v = static_cast<char*>(workspace) + p.v;
   // on the tensor cores throughout, or, for what they cannot take, on the FP32 pipes and with the
-  // weight-gradient kernels (which want the groups by id)
+  // weight-gradient kernels (which want the groups by id, one behind the other)
   const bool tensor = p.variant != kVariantSimt && aligned(x, 16) && aligned(d_y, 16) &&
                       aligned(a, 16) && aligned(b, 16) && aligned(d_a, 16) && aligned(d_b, 16) &&
                       static_cast<int64_t>(A) * ((K + 127) / 128 + (N + 127) / 128) <
                           kInt32Max / 4;
+  p.padded = tensor ? 1 : 0;
   rc = run_adapter_prep(p, t, tensor, adapter, T, A, s);
   if (rc != PGG_OK) return rc;
   // u and v need the tables alone, and the factors' gradients u and v alone: each runs beside the
@@ -680,7 +679,6 @@ int pgg_adapters_grad(const void* d_y, const void* x, const void* weight, const 
     o.out[1] = d_b;
     o.range = t.range;
     o.order = t.order;
-    o.padrow = t.padrow;
     o.hdr = t.hdr;
     o.cols[0] = K;
     o.cols[1] = N;
@@ -693,9 +691,9 @@ int pgg_adapters_grad(const void* d_y, const void* x, const void* weight, const 
     o.wait_limit_ns = env.wait_limit_ns;
     return status_of(launch_rows_outer(dtype, o, env.num_sms, s));
   }
-  rc = run_dw_tables(x, v, t.off, t.padrow, t.hdr, p.rows_u, R, K, A, T, dtype, d_a, s);
+  rc = run_dw_tables(x, v, t.off, t.order, t.hdr, T, R, K, A, T, dtype, d_a, s);
   if (rc != PGG_OK) return rc;
-  return run_dw_tables(d_y, u, t.off, t.padrow, t.hdr, p.rows_u, R, N, A, T, dtype, d_b, s);
+  return run_dw_tables(d_y, u, t.off, t.order, t.hdr, T, R, N, A, T, dtype, d_b, s);
 }
 
 }  // extern "C"

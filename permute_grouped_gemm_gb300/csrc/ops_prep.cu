@@ -162,11 +162,11 @@ __device__ __forceinline__ int adapter_key(int64_t id, int A) {
 }
 
 // Block-wide, blockDim.x > A (one thread per adapter and one for the group without): the lists
-// from the groups' sizes, into memory if `write`, and s_start, s_ustart (by id) in any case.
+// from the groups' sizes, into memory if `write`, and s_start (by id) in any case.
 // Thread g holds group g's count and first token; s_work is 3 x [A + 1].
 __device__ void build_adapter_lists(const AdapterPrepArgs& a, bool write, uint32_t count,
                                     uint32_t first, uint32_t* s_scan, uint32_t* s_start,
-                                    uint32_t* s_ustart, uint32_t* s_work) {
+                                    uint32_t* s_work) {
   const int G = a.A + 1, g = threadIdx.x;
   const bool group = g < G;
   uint32_t *s_first = s_work, *s_by = s_work + G, *s_end = s_work + 2 * G;
@@ -196,10 +196,7 @@ __device__ void build_adapter_lists(const AdapterPrepArgs& a, bool write, uint32
   const uint32_t seg = block_scan_u32(live ? 1u : 0u, s_scan, &n_seg);
   const uint32_t nb = (n + a.rb - 1) / a.rb;
   const uint32_t rb0 = block_scan_u32(nb, s_scan, &n_rb);
-  if (group) {
-    s_start[id] = start;
-    s_ustart[id] = ustart;
-  }
+  if (group) s_start[id] = start;
   if (write) {
     if (group) {
       a.t.off[id] = ustart;
@@ -241,20 +238,13 @@ __device__ void build_adapter_lists(const AdapterPrepArgs& a, bool write, uint32
   }
 }
 
-// Records of one sorted token; the last token of a padded adapter also fills up its last rows.
+// Record of one sorted token.
 __device__ __forceinline__ void put_token(const AdapterPrepArgs& a, int64_t token, int g,
-                                          uint32_t where, uint32_t start, uint32_t ustart,
-                                          uint32_t count) {
+                                          uint32_t where) {
   RowInfo r;
   r.token = static_cast<int32_t>(token);
   r.rank = g;
   a.t.order[where] = r;
-  if (!a.padded) return;
-  const uint32_t i = where - start;
-  r.rank = 0;
-  a.t.padrow[ustart + i] = r;
-  if (i + 1 == count)
-    for (uint32_t j = count; j < (count + kRowPad - 1) / kRowPad * kRowPad; ++j) a.t.padrow[ustart + j] = r;
 }
 
 // Warps w, w + warps, ...: whether each 128 compact rows are neighbours in token order.
@@ -276,7 +266,7 @@ __device__ __forceinline__ void find_boxes(const AdapterPrepArgs& a, int64_t w, 
 
 __global__ void __launch_bounds__(1024) adapter_prep_small_kernel(const AdapterPrepArgs a) {
   // [warps][A + 1] counters, [kCluster][A + 1] counts of every block and their first tokens,
-  // 6 x [A + 1], the block's keys
+  // 4 x [A + 1], the block's keys
   extern __shared__ uint32_t s_cnt[];
   __shared__ uint32_t s_scan[33];
   __shared__ int s_bad[kCluster];
@@ -287,7 +277,7 @@ __global__ void __launch_bounds__(1024) adapter_prep_small_kernel(const AdapterP
   uint32_t* s_all = s_cnt + warps * G;
   uint32_t* s_allf = s_all + kCluster * G;
   uint32_t* s_start = s_all + (a.by_first ? 2 : 1) * kCluster * G;  // (no s_allf otherwise)
-  uint32_t *s_ustart = s_start + G, *s_count = s_ustart + G, *s_work = s_count + G;
+  uint32_t* s_work = s_start + G;
   uint16_t* s_key = reinterpret_cast<uint16_t*>(s_work + 3 * G);
   const int64_t t0 = static_cast<int64_t>(rank) * a.tokens_per_block;
   const int64_t left = a.T - t0;
@@ -329,16 +319,12 @@ __global__ void __launch_bounds__(1024) adapter_prep_small_kernel(const AdapterP
       c += s_all[d * G + g];
       if (a.by_first && s_allf[d * G + g] < first) first = s_allf[d * G + g];
     }
-    s_count[g] = c;
   }
-  build_adapter_lists(a, rank == 0, c, first, s_scan, s_start, s_ustart, s_work);
+  build_adapter_lists(a, rank == 0, c, first, s_scan, s_start, s_work);
   __syncthreads();
   sort_place(
       s_cnt, G, n, run, key, [&](int k) { return s_start[k] + mine; },
-      [&](int e, uint32_t where) {
-        const int k = key(e);
-        put_token(a, t0 + e, k, where, s_start[k], s_ustart[k], s_count[k]);
-      });
+      [&](int e, uint32_t where) { put_token(a, t0 + e, key(e), where); });
   ptx::cluster_sync();  // every block's part of the order is there
   find_boxes(a, rank * warps + (threadIdx.x >> 5), static_cast<int64_t>(C) * warps);
   if (rank == 0 && threadIdx.x == 0) {
@@ -371,13 +357,13 @@ __global__ void __launch_bounds__(kSortThreads) adapter_count_kernel(const Adapt
 
 // Third launch (one block), after the prefix sums: the lists. The totals arrive in off.
 __global__ void __launch_bounds__(1024) adapter_lists_kernel(const AdapterPrepArgs a) {
-  extern __shared__ uint32_t s_lists[];  // 5 x [A + 1]
+  extern __shared__ uint32_t s_lists[];  // 4 x [A + 1]
   __shared__ uint32_t s_scan[33];
   ptx::griddep_wait();
   const int G = a.A + 1, g = threadIdx.x;
   const uint32_t c = g < G ? static_cast<uint32_t>(a.t.off[g]) : 0u;
   // (groups by id: the first tokens would be one more launch's work)
-  build_adapter_lists(a, true, c, 0, s_scan, s_lists, s_lists + G, s_lists + 2 * G);
+  build_adapter_lists(a, true, c, 0, s_scan, s_lists, s_lists + G);
   if (g == 0) {
     a.t.hdr->status = 0;
     a.t.hdr->sched_next = 0;
@@ -408,11 +394,7 @@ __global__ void __launch_bounds__(kSortThreads) adapter_place_kernel(const Adapt
         return static_cast<uint32_t>(a.t.range[g].x) +
                a.t.counts[static_cast<int64_t>(g) * a.blocks + blockIdx.x];
       },
-      [&](int e, uint32_t where) {
-        const int k = key(e);
-        const int4 r = a.t.range[k];
-        put_token(a, t0 + e, k, where, r.x, r.z, r.y);
-      });
+      [&](int e, uint32_t where) { put_token(a, t0 + e, key(e), where); });
 }
 
 // Fifth launch.
@@ -461,11 +443,11 @@ cudaError_t launch_adapter_prep(const AdapterPrepArgs& a, cudaStream_t stream) {
     AdapterPrepArgs q = a;
     if (G > 512) q.by_first = 0;  // (their tables would not fit beside the counters)
     const size_t smem =
-        static_cast<size_t>(threads / 32 + (q.by_first ? 2 : 1) * kCluster + 6) * G * 4 +
+        static_cast<size_t>(threads / 32 + (q.by_first ? 2 : 1) * kCluster + 4) * G * 4 +
         static_cast<size_t>(a.tokens_per_block) * 2;
     // the most of it: 1024 threads and groups (by id), and the keys of kSmallTokens / kCluster tokens
     constexpr int kMost =
-        (1024 / 32 + kCluster + 6) * static_cast<int>(kMaxAdapters + 1) * 4 +
+        (1024 / 32 + kCluster + 4) * static_cast<int>(kMaxAdapters + 1) * 4 +
         static_cast<int>(kSmallTokens / kCluster) * 2;
     static SmemLimit limit;
     const cudaError_t err = allow_smem(&limit, adapter_prep_small_kernel, kMost);
@@ -480,7 +462,7 @@ cudaError_t launch_adapter_prep(const AdapterPrepArgs& a, cudaStream_t stream) {
   if (err != cudaSuccess) return err;
   AdapterPrepArgs by_id = a;
   by_id.by_first = 0;
-  err = launch_pdl(adapter_lists_kernel, dim3(1), dim3(1024), static_cast<size_t>(5) * G * 4,
+  err = launch_pdl(adapter_lists_kernel, dim3(1), dim3(1024), static_cast<size_t>(4) * G * 4,
                    stream, 1, by_id);
   if (err != cudaSuccess) return err;
   err = launch_pdl(adapter_place_kernel, dim3(a.blocks), dim3(kSortThreads),

@@ -275,14 +275,6 @@ __global__ void __launch_bounds__(kThr, 3) rows_simt_kernel(const RowsArgs a) {
         }
       }
     }
-    if (MODE == kShrink && a.padded) {
-      // the adapter's last block: rows that fill it up
-      const int fill = rows_to_fill(a, e);
-      for (int q = tid; q < fill * kTileN; q += kThr) {
-        const int64_t n = n0 + q % kTileN;
-        if (n < a.N) st<DT>(a.out, (static_cast<int64_t>(e.w) + e.z + q / kTileN) * a.N + n, 0.0f);
-      }
-    }
   }
 }
 

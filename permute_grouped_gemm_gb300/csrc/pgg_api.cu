@@ -514,8 +514,10 @@ int check_dw(const void* x, const void* gradY, const int64_t* idx, const int64_t
   return PGG_OK;
 }
 
+// own_rows: the sums may read no rows but their own (copied by the gather warps then, not by TMA in
+// boxes that reach into the next expert's).
 int run_dw(const Plan& plan, const void* x, const void* gradY, void* ws, void* dweight,
-           int out_dtype, cudaStream_t stream) {
+           int out_dtype, cudaStream_t stream, bool own_rows = false) {
   DeviceInfo di;
   if (device_info(&di) != PGG_OK) return PGG_ERR_CUDA;
   char* w = static_cast<char*>(ws);
@@ -536,8 +538,9 @@ int run_dw(const Plan& plan, const void* x, const void* gradY, void* ws, void* d
   a.gather_dy = 0;
   a.hold_release = g_hold_release.load() != 0 ? 1 : 0;
   a.wait_limit_ns = g_wait_limit_ns.load();
-  if (!dw_tensor_path(plan.dtype, plan.N, plan.K, x, gradY, dweight) &&
-      dw_gather_path(plan.dtype, plan.N, plan.K, x, gradY, dweight)) {
+  const bool tensor =
+      !own_rows && dw_tensor_path(plan.dtype, plan.N, plan.K, x, gradY, dweight);
+  if (!tensor && dw_gather_path(plan.dtype, plan.N, plan.K, x, gradY, dweight)) {
     dw_tiles(plan.K, plan.N, &a.k_blocks, &a.n_blocks);
     a.gather_dy = 1;
     CUtensorMap none;
@@ -545,7 +548,7 @@ int run_dw(const Plan& plan, const void* x, const void* gradY, void* ws, void* d
     return launch_dw(plan.dtype, none, none, a, di.num_sms, stream) == cudaSuccess ? PGG_OK
                                                                                    : PGG_ERR_CUDA;
   }
-  if (dw_tensor_path(plan.dtype, plan.N, plan.K, x, gradY, dweight)) {
+  if (tensor) {
     dw_tiles(plan.K, plan.N, &a.k_blocks, &a.n_blocks);
     EncodeTiledFn enc = encode_fn();
     if (!enc) return PGG_ERR_CUDA;
@@ -782,7 +785,7 @@ int run_dw_tables(const void* x, const void* dy, const int64_t* off, const RowIn
   p.layout.hdr = 0;
   p.layout.off = static_cast<size_t>(reinterpret_cast<const char*>(off) - base);
   p.layout.rowinfo = static_cast<size_t>(reinterpret_cast<const char*>(rowinfo) - base);
-  return run_dw(p, x, dy, base, out, dtype, stream);
+  return run_dw(p, x, dy, base, out, dtype, stream, true);
 }
 
 }  // namespace pgg

@@ -25,7 +25,8 @@ bool encode_map_3d(CUtensorMap* m, int dtype, const void* base, int64_t d0, int6
 bool encode_map_rows(CUtensorMap* m, int dtype, const void* base, int64_t d0, int64_t d1,
                      int box1);
 // The weight-gradient kernels on tables already in memory: out[g] = sum over rows i in
-// [off[g], off[g + 1]) of x[token(i)]^T dy[i], g < G. dy has `rows` rows.
+// [off[g], off[g + 1]) of x[token(i)]^T dy[i], g < G. dy has `rows` rows; no group's sum reads a row
+// of another's, whatever it holds (the form with TMA copies does, against zeros of x).
 int run_dw_tables(const void* x, const void* dy, const int64_t* off, const RowInfo* rowinfo,
                   WsHeader* hdr, int64_t rows, int64_t N, int64_t K, int64_t G, int64_t batch,
                   int dtype, void* out, cudaStream_t stream);
@@ -102,14 +103,13 @@ cudaError_t launch_rows_prep(const RowsPrepArgs& a, int num_sms, cudaStream_t st
 // weight-gradient kernels that take off[] need that). That compact order of T rows is what the
 // projection walks. The low-rank factors u and v are stored in a second order, in which
 // (padded = 1) every group starts at a multiple of kRowPad rows and is filled up with zero rows: the
-// reduction over an adapter's rows reads that many at a time, and what it reads past them must not be
-// another adapter's.
+// reduction over an adapter's rows (rows_outer.cu) reads that many at a time, and what it reads past
+// them must not be another adapter's. (The rows of x and d_y that meet them there read as zeros.)
 struct AdapterTables {
   WsHeader* hdr;
   int64_t* off;       // [A + 1] first row of each group in the order of u and v, groups by id
   int4* range;        // [A + 1] {first compact row, rows, first row of u, 0} by id
   RowInfo* order;     // [T] compact order: {token, adapter}
-  RowInfo* padrow;    // [P] order of u and v: {token, 0}; a filled-up row repeats a token
   int4* rblist;       // {adapter, first compact row, rows, first row of u}: at most rb rows each
   int4* segs;         // {adapter, first compact row, end, first row of u} of each live adapter
   int32_t* box;       // [2 ceil(T / 256)] first token of each 128 compact rows if they are neighbours
@@ -197,7 +197,6 @@ struct OuterArgs {
   void* out[2];
   const int4* range;     // [A + 1]
   const RowInfo* order;
-  const RowInfo* padrow;
   WsHeader* hdr;
   int64_t cols[2];
   int64_t T, right_rows;

@@ -10,9 +10,8 @@
 // operands are MN-major. A stage is 128 rows: 128 columns of x, by TMA where
 // the 128 rows are neighbouring tokens, else gathered by token with cp.async
 // (one warp per stage slot), and the rows' ranks of v by TMA. v is stored so
-// that an adapter's rows end on a multiple of 128 with rows of zeros, whose x row
-// repeats the adapter's last: another adapter's rows, whatever they hold, never
-// take part.
+// that an adapter's rows end on a multiple of 128 with rows of zeros, and their
+// x rows read as zeros: nobody's rows, whatever they hold, take part there.
 //
 // A cluster of S CTAs shares a tile: each reduces its part of the adapter's
 // rows, the partial sums meet through distributed shared memory, 128 / S
@@ -170,12 +169,13 @@ __device__ void gatherer(uint8_t* smem, Ctl* ctl, const OuterArgs& a, uint32_t t
     for (; kb < steps; kb += kStages) {
       const int s = x.s0 + kb;
       const int32_t box = box_of(a, x, s);
-      int32_t tok[2];  // rows 64 half + lane + 32 h of the step
+      int32_t tok[2];  // rows 64 half + lane + 32 h of the step; -1 past the adapter's
       if (box < 0) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-          tok[h] = a.padrow[static_cast<int64_t>(x.range.z) + kRows * s + 64 * half + lane + 32 * h]
-                       .token;
+        for (int h = 0; h < 2; ++h) {
+          const int row = kRows * s + 64 * half + lane + 32 * h;
+          tok[h] = row < x.range.y ? a.order[static_cast<int64_t>(x.range.x) + row].token : -1;
+        }
       }
       if (!ptx::mbar_wait(&ctl->empty[w], phase ^ 1u, lim, abort)) {
         failed = true;
@@ -186,10 +186,11 @@ __device__ void gatherer(uint8_t* smem, Ctl* ctl, const OuterArgs& a, uint32_t t
         for (int q = 0; q < kRows / 4; ++q) {
           const int rq = (lane >> 4) + 2 * q, rr = 64 * half + rq;
           const int32_t tk = __shfl_sync(0xFFFFFFFFu, tok[q / 16], rq & 31);
-          const void* src = in ? static_cast<const void*>(
+          const bool ok = in && tk >= 0;
+          const void* src = ok ? static_cast<const void*>(
                                      base + (static_cast<int64_t>(tk) * C + col) * 2)
                                : static_cast<const void*>(base);
-          ptx::cp_async_16(sa + rr * 128 + (((c & 7) ^ (rr & 7)) << 4), src, in ? 16u : 0u);
+          ptx::cp_async_16(sa + rr * 128 + (((c & 7) ^ (rr & 7)) << 4), src, ok ? 16u : 0u);
         }
         ptx::cp_async_commit();
         ptx::cp_async_wait<0>();

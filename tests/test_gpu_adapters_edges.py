@@ -64,3 +64,67 @@ def test_a_gradient_at_any_element(T, name):
         # each side rounds the sum and the low-rank row once
         for g, w in zip(got[:3], want.values()):
             assert (g.double() - w.double()).abs().max() <= 3 * 2.0 ** -8 * w.double().abs().max()
+
+
+# ------------------------------------------------------- infinities at an adapter's last token
+
+COUNTS = (1, 127, 128, 129, 300)
+
+
+def with_counts(order, dtype, K=64, N=72, R=16):
+    """Inputs whose adapters have COUNTS tokens, in runs or mixed, and each one's last token."""
+    T = sum(COUNTS)
+    s = inputs(T, K, N, R, len(COUNTS), dtype=dtype, seed=91)
+    ids = torch.repeat_interleave(torch.arange(len(COUNTS)), torch.tensor(COUNTS))
+    if order == "mixed":
+        ids = ids[torch.randperm(T, generator=torch.Generator().manual_seed(3))]
+    s["adapter"] = ids.cuda()
+    last = [int((ids == i).nonzero().max()) for i in range(len(COUNTS))]
+    return s, last
+
+
+# on the tensor cores; with an odd rank (the weight-gradient kernel that gathers both operands); with
+# an output off a 16-byte boundary; on the FP32 pipes
+@pytest.mark.parametrize("form", ["tensor", "rank 10", "unaligned", "pipes", "fp32"])
+@pytest.mark.parametrize("order", ["runs", "mixed"])
+def test_an_infinity_at_an_adapters_last_token_stays_one(order, form):
+    dtype = {"tensor": "bf16", "fp32": "fp32"}.get(form, "fp16")
+    s, last = with_counts(order, dtype, R=10 if form == "rank 10" else 16)
+    T, N, R = s["x"].shape[0], s["weight"].shape[1], s["a"].shape[2]
+    d_y = torch.randn(T, N, device="cuda").to(s["x"].dtype)
+    out = {}
+    if form == "unaligned":
+        out = dict(d_a=shifted(tuple(s["a"].shape), s["a"].dtype, 4)[1],
+                   d_b=shifted(tuple(s["b"].shape), s["b"].dtype, 4)[1])
+
+    def grads(s, d_y):
+        if form == "pipes":
+            pgg.pgg_debug_force_variant(3)
+        try:
+            got = pgg.adapters_grad(d_y, **s, **out)
+        finally:
+            pgg.pgg_debug_force_variant(-1)
+        torch.cuda.synchronize()
+        assert pgg.status(got[3]) == 0
+        return got[0], got[1].clone(), got[2].clone()
+
+    _, d_a, d_b = grads(s, d_y)
+    assert torch.isfinite(d_a).all() and torch.isfinite(d_b).all()
+    v = low_rank(d_y, s["b"], s["adapter"], s["scale"])
+    u = low_rank(s["x"], s["a"], s["adapter"], s["scale"])
+    for i, t in enumerate(last):
+        x2, dy2 = s["x"].clone(), d_y.clone()
+        x2[t, 5] = float("inf")
+        dy2[t, 7] = float("-inf")
+        # x^T v: the column of the infinity is infinite with v's signs, the others are as before
+        _, got, _ = grads(dict(s, x=x2), d_y)
+        assert torch.equal(got[i, 5].double(), torch.sign(v[t]) * float("inf"))
+        rest = torch.ones_like(got, dtype=torch.bool)
+        rest[i, 5] = False
+        assert torch.equal(got[rest], d_a[rest])
+        # d_y^T u alike
+        _, _, got = grads(s, dy2)
+        assert torch.equal(got[i, 7].double(), torch.sign(u[t]) * float("-inf"))
+        rest = torch.ones_like(got, dtype=torch.bool)
+        rest[i, 7] = False
+        assert torch.equal(got[rest], d_b[rest])
