@@ -480,10 +480,12 @@ int pgg_unpermute_grad_apply(const void* permuted, const void* d_out, const void
  *            without an auxiliary loss is). Without a bias the choice goes by
  *            the logits either way.
  *   logits   device, [batch, G] of `dtype`; -inf masks an expert (weight 0, its key
- *            -inf whatever the bias). A
- *            token whose experts are all masked takes the lowest indices with
- *            weights 0. A NaN key sorts below every other; a NaN or +inf logit
- *            gives NaN weights, as IEEE arithmetic does; the order stays valid.
+ *            -inf with any finite bias). A token whose experts are all masked takes
+ *            the lowest indices; where the chosen scores are all 0 in fp32 the
+ *            weights are 0. A NaN key sorts below every other, so that the order
+ *            stays valid. Scores follow IEEE arithmetic: a softmax over a NaN or a
+ *            +inf is NaN, so are all of the token's weights; a sigmoid is NaN for a
+ *            NaN alone (renormalised: all weights, if that one is chosen).
  *   bias     device, fp32 [G], or NULL
  *   G <= 1024, topK <= min(G, 32), else PGG_ERR_SHAPE
  *   workspace at least pgg_route_workspace_size bytes, 256-byte aligned; the
@@ -511,7 +513,8 @@ int pgg_route_execute(const void* logits, const float* bias, int64_t batch, int6
  * Gradient of probs for the logits (bias gets none: the choice is piecewise
  * constant). d_logits [batch, G] of `dtype` is written whole; needs no
  * workspace. A token whose `experts` hold an index outside [0, G) or one
- * twice gets NaN. Aliasing d_logits with logits is not allowed.
+ * twice gets NaN. Only the plain softmax reads more than the chosen logits.
+ * Aliasing d_logits with logits is not allowed.
  */
 int pgg_route_grad(const float* d_probs, const void* logits, const int64_t* experts,
                    int64_t batch, int64_t G, int64_t topK, pgg_dtype dtype, pgg_score score,

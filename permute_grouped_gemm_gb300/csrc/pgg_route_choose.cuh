@@ -117,6 +117,13 @@ __device__ __forceinline__ float soft_exp(float l, float m) {
   return l == -INFINITY ? 0.0f : expf(l - m);
 }
 
+// Maximum that is NaN when one of the two is.
+__device__ __forceinline__ float max_or_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
 __device__ __forceinline__ float sigmoid(float l) { return 1.0f / (1.0f + expf(-l)); }
 
 // What the bias is added to when it belongs to the scores: the score in fp32, -inf for a masked
@@ -250,6 +257,16 @@ __device__ __forceinline__ int choose_and_write(const RouteArgs& a, int64_t t0, 
     for (int i = 0; i < V; ++i) z += soft_exp(l[i], m);  // (0 past the end)
     z = group_sum<LPT>(z);
   }
+  // a softmax over all with a NaN or +inf in it is NaN, which the sum over the chosen alone would
+  // not show when that one is not chosen
+  bool no_softmax = false;
+  if (!a.sigmoid && a.renormalize) {
+    float w = l[0];
+#pragma unroll
+    for (int i = 1; i < V; ++i) w = max_or_nan(w, l[i]);
+    const uint32_t lanes = __ballot_sync(0xFFFFFFFFu, !(w < INFINITY));
+    no_softmax = ((lanes >> (LPT * sub)) & (0xFFFFFFFFu >> (32 - LPT))) != 0;
+  }
   if constexpr (ON_SCORE) {
 #pragma unroll
     for (int i = 0; i < V; ++i) l[i] = score_of(l[i], a.sigmoid, m, z);
@@ -360,6 +377,7 @@ __device__ __forceinline__ int choose_and_write(const RouteArgs& a, int64_t t0, 
     p = on ? soft_exp(my_l, m) : 0.0f;
     z = group_sum<LPT>(p);
     p = m == -INFINITY && z == 0.0f ? 0.0f : p / z;
+    if (no_softmax) p = NAN;
   } else {
     p = m == -INFINITY && z == 0.0f ? 0.0f : soft_exp(my_l, m) / z;
   }

@@ -11,9 +11,10 @@
 // A warp takes four tokens (or two, or one): the logits sit in registers, G / 8
 // a lane; see choose_and_write (65536 tokens, 256 experts, k 8, bf16: 25 us). A
 // NaN key sorts below everything (the choice stays a valid one); scores follow IEEE
-// arithmetic, so a NaN or +inf logit gives NaN weights. A masked expert
-// (-inf) has weight 0; a token whose experts are all masked takes the lowest
-// indices with weights 0. Everything is computed in 32 bits.
+// arithmetic, so a softmax over a NaN or +inf logit gives NaN weights, whether that
+// one is chosen or not. A masked expert (-inf) has weight 0; a token whose experts
+// are all masked takes the lowest indices with weights 0. Everything is computed in
+// 32 bits.
 //
 // Few tokens: one block does everything in one launch. Many: (1) choice, ranks
 // and the block's count of every expert, (2) prefix sums of the counts over the

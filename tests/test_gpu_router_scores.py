@@ -172,3 +172,37 @@ def test_in_a_graph_and_on_unaligned_logits():
     torch.cuda.synchronize()
     for p, q in zip(first[:4], out[:4]):
         assert torch.equal(p, q)
+
+
+# ------------------------------------------------------------------ NaN and +inf in a softmax
+
+# every form: four tokens a warp, two, one; in one block and in several; loads of one value
+@pytest.mark.parametrize("bias_on", ["logits", "scores"])
+@pytest.mark.parametrize("t,g,k", [(9, 16, 4), (200, 60, 8), (600, 256, 8), (300, 255, 6),
+                                   (40, 500, 12), (700, 96, 16), (30, 1024, 20), (500, 700, 32)])
+def test_a_softmax_with_a_nan_gives_nan_weights(t, g, k, bias_on):
+    l = logits_of(t, g, "fp32", t)
+    low = l.argmin(1)  # an expert that is not chosen
+    l[1, low[1]] = float("nan")
+    l[4, g - 1] = l[4, 0] = float("nan")
+    l[6, low[6]] = float("inf")
+    l[7, low[7]] = float("-inf")
+    # the +inf is not chosen: its key is NaN
+    bias = torch.zeros(g, device="cuda")
+    bias[low[6]] = float("-inf")
+    for renormalize in (False, True):
+        p, e, idx, _, _ = pgg.route(l, k, bias=bias, renormalize=renormalize, bias_on=bias_on)
+        assert not (e[1] == low[1]).any() and not (e[7] == low[7]).any()
+        if bias_on == "logits":
+            assert not (e[6] == low[6]).any()
+        assert torch.equal(torch.sort(idx).values.cpu(), torch.arange(t * k))
+        odd = torch.zeros(t, dtype=torch.bool, device="cuda")
+        odd[[1, 4, 6]] = True
+        assert torch.isnan(p[odd]).all()
+        assert torch.isfinite(p[~odd]).all()
+        # without a bias too, where the +inf is chosen
+        p = pgg.route(l, k, renormalize=renormalize)[0]
+        assert torch.isnan(p[odd]).all() and torch.isfinite(p[~odd]).all()
+    # a sigmoid of an expert that is not chosen does not matter
+    p = pgg.route(l, k, score="sigmoid")[0]
+    assert torch.isfinite(p).all()
