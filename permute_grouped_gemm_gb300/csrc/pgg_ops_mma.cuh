@@ -89,8 +89,10 @@ __device__ __forceinline__ void launch_end(bool late) {
   if (late && blockIdx.x == 0) ptx::griddep_wait();
 }
 
-// p * silu(g) * u for a 16-bit output: the fast exponential and reciprocal, whose error (a few
-// 2^-21) is far below the one rounding of the result.
+// p * silu(g) * u for a 16-bit output: the fast exponential, within 2 + |1.2 g| units of 2^-23 (2^-19
+// of the result at g = -8, 2^-16 at -85; where g is positive it hardly counts), and a quotient
+// within two (0 below g = -87.3). That stays well below the one rounding of the result, 2^-9 in
+// bf16 and 2^-12 in fp16.
 __device__ __forceinline__ float gate(float g, float u, float p) {
   return p * (g * __fdividef(1.0f, 1.0f + __expf(-g)) * u);
 }
