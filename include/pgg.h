@@ -514,7 +514,7 @@ int pgg_route_execute(const void* logits, const float* bias, int64_t batch, int6
  * constant). d_logits [batch, G] of `dtype` is written whole; needs no
  * workspace. A token whose `experts` hold an index outside [0, G) or one
  * twice gets NaN. Only the plain softmax reads more than the chosen logits.
- * Aliasing d_logits with logits is not allowed.
+ * d_logits may be logits itself; another overlap is not allowed.
  */
 int pgg_route_grad(const float* d_probs, const void* logits, const int64_t* experts,
                    int64_t batch, int64_t G, int64_t topK, pgg_dtype dtype, pgg_score score,

@@ -274,7 +274,8 @@ def route(logits, top_k: int, row_idx_type: int = 0, bias=None, score: str = "so
 def route_grad(d_probs, logits, experts, score: str = "softmax", renormalize: bool = True,
                scale: float = 1.0, out=None, stream=None):
     """d_logits [batch, G] (logits' dtype) from d_probs [batch, top_k] fp32 and the ``experts``
-    that ``route`` chose from ``logits`` with the same score, renormalize and scale."""
+    that ``route`` chose from ``logits`` with the same score, renormalize and scale. ``out`` may
+    be ``logits``."""
     import torch
     _dense(d_probs, logits, experts, out)
     batch, G = logits.shape

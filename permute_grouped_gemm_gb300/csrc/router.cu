@@ -149,7 +149,7 @@ __global__ void __launch_bounds__(32 * kWarps) route_grad_kernel(const RouteGrad
     const bool bad = __any_sync(0xFFFFFFFFu, on && (!in || __popc(same) > 1));
     const float lj = sparse && on ? load_logit<DT>(a.logits, row + e) : -INFINITY;
     if (sparse) {
-      __syncwarp();  // (d_logits may be logits)
+      __syncwarp();  // (d_logits may be logits: all of the warp have read theirs)
       zero_row(static_cast<char*>(a.d_logits) + row * kSize, a.G * kSize, lane);
     }
     __syncwarp();

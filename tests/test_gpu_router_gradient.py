@@ -81,3 +81,15 @@ def test_gradient(t, g, k, dtype, score, renormalize):
     elif k > 1:
         chosen = want.gather(1, experts).abs() > 2 * bound.gather(1, experts)
         assert chosen.double().mean() > (0.5 if dtype == "fp16" else 0.99)
+
+
+@pytest.mark.parametrize("score,renormalize", KINDS)
+@pytest.mark.parametrize("dtype,g", [("fp32", 60), ("bf16", 256), ("fp16", 77)])
+def test_in_place(dtype, g, score, renormalize):
+    l = logits_of(400, g, dtype, 31)
+    experts = pgg.route(l, 6, score=score)[1]
+    dp = torch.randn(400, 6, device="cuda")
+    want = pgg.route_grad(dp, l, experts, score=score, renormalize=renormalize)
+    got = pgg.route_grad(dp, l, experts, score=score, renormalize=renormalize, out=l)
+    assert got.data_ptr() == l.data_ptr()
+    assert torch.equal(got, want)
