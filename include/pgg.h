@@ -607,8 +607,11 @@ int pgg_swiglu_grad(const void* d_h, const void* gate_up, const float* probs,
  *            word at offset 0
  *   y        device, [T, N] of `dtype`
  *
- * Tokens may be in any order. What one adapter's weights hold (infinities, NaN)
- * does not reach the tokens of another. No output may overlap an input.
+ * Tokens may be in any order. Sums are fp32, the low-rank row scale x a among them:
+ * it enters the second product in fp32, or as the sum of two values of `dtype`
+ * (2^-16 of it is lost in bf16, 2^-21 in fp16, where it may reach 131008), and y is
+ * rounded once. What one adapter's weights hold (infinities, NaN) does not reach
+ * the tokens of another. No output may overlap an input.
  */
 int pgg_adapters_workspace_size(int64_t T, int64_t K, int64_t N, int64_t R, int64_t A,
                                 pgg_dtype dtype, size_t* workspace_bytes);
@@ -635,9 +638,11 @@ int pgg_adapters_plan(int64_t T, int64_t K, int64_t N, int64_t R, int64_t A, pgg
  *     d_a[ad] = sum over its tokens of x^T v                  [A, K, R]
  *     d_b[ad] = sum over its tokens of d_y^T (scale x a[ad])  [A, N, R]
  *
- * all of `dtype`; an adapter without tokens gets zeros. Sums are fp32; v and
- * scale x a[ad] are rounded once to `dtype` before the second product. No output
- * may overlap an input: d_x, d_a and d_b are written side by side.
+ * all of `dtype`; an adapter without tokens gets zeros. Sums are fp32. v and
+ * u = scale x a[ad] enter the second products as the sums of two values of `dtype`
+ * (as in the forward) where 16-bit tensors have widths that are multiples of 8 and
+ * are 16-byte aligned, else rounded once to `dtype`. No output may overlap an
+ * input: d_x, d_a and d_b are written side by side.
  */
 int pgg_adapters_grad_workspace_size(int64_t T, int64_t K, int64_t N, int64_t R, int64_t A,
                                      pgg_dtype dtype, size_t* workspace_bytes);

@@ -185,8 +185,10 @@ int adapter_plan(int64_t T, int64_t K, int64_t N, int64_t R, int64_t A, int dtyp
   p->blkseg = c.take(static_cast<int64_t>(sizeof(int2)) * ((T + 255) / 256));
   p->box = c.take(8 * ((T + 255) / 256));
   p->counts = c.take(p->blocks > 8 ? 4 * (A + 1) * p->blocks : 0);
-  p->u = c.take(p->rows_u * R * (p->variant == kVariantSkinny ? 4 : elem_size(dtype)));
-  p->v = c.take(grad ? p->rows_u * R * elem_size(dtype) : 0);
+  // (16-bit: room for each of the forms, of which the split one is the largest)
+  const int64_t low_bytes = dtype == PGG_F32 ? R * 4 : low_width(R) * 2;
+  p->u = c.take(p->rows_u * low_bytes);
+  p->v = c.take(grad ? p->rows_u * low_bytes : 0);
   p->total = c.used;
   return PGG_OK;
 }
@@ -223,9 +225,9 @@ int run_adapter_prep(const AdapterPlan& p, const AdapterTables& t, bool by_first
 
 // u = scale * x f[adapter] for f [A, K, R], into rows of `u`, in the adapters' order.
 // (early, late: see launch_order in pgg_ops_mma.cuh)
-int run_shrink(const AdapterPlan& p, const AdapterTables& t, const HostEnv& env, bool early,
-               bool late, const void* x, const void* f, const float* scale, void* u, int64_t T,
-               int64_t K, int64_t R, int64_t A, int dtype, cudaStream_t stream) {
+int run_shrink(const AdapterPlan& p, const AdapterTables& t, const HostEnv& env, LowRankForm form,
+               bool early, bool late, const void* x, const void* f, const float* scale, void* u,
+               int64_t T, int64_t K, int64_t R, int64_t A, int dtype, cudaStream_t stream) {
   RowsArgs a;
   std::memset(&a, 0, sizeof(a));
   a.x = x;
@@ -241,6 +243,7 @@ int run_shrink(const AdapterPlan& p, const AdapterTables& t, const HostEnv& env,
   a.G = A;
   a.batch = T;
   a.max_row_blocks = p.max_row_blocks;
+  a.low_form = form;
   a.padded = p.padded;
   a.range = t.range;
   a.early = early ? 1 : 0;
@@ -273,12 +276,18 @@ int run_few_shrink(const AdapterTables& t, const void* x, const void* f, const i
   return status_of(launch_few_shrink(dtype, a, stream));
 }
 
+// Whether the tensor cores take a projection of these tensors (the FP32 pipes do otherwise).
+bool wide_takes(const AdapterPlan& p, const void* x, const void* w, const void* f, const void* y) {
+  return p.variant != kVariantSimt && aligned(x, 16) && aligned(w, 16) && aligned(f, 16) &&
+         aligned(y, 16);
+}
+
 // y = x W + u f[adapter]^T for W [K, N] (transposed: [N, K]) and f [A, N, R]. by_token: the
 // adapter ids when u is fp32 in the tokens' order, else null.
-int run_adapt(const AdapterPlan& p, const AdapterTables& t, const HostEnv& env, bool transposed,
-              bool early, bool late, const int64_t* by_token, const void* x, const void* w,
-              const void* u, const void* f, void* y, int64_t T, int64_t K, int64_t N, int64_t R,
-              int64_t A, int dtype, cudaStream_t stream) {
+int run_adapt(const AdapterPlan& p, const AdapterTables& t, const HostEnv& env, LowRankForm form,
+              bool transposed, bool early, bool late, const int64_t* by_token, const void* x,
+              const void* w, const void* u, const void* f, void* y, int64_t T, int64_t K, int64_t N,
+              int64_t R, int64_t A, int dtype, cudaStream_t stream) {
   RowsArgs a;
   std::memset(&a, 0, sizeof(a));
   a.x = x;
@@ -297,6 +306,7 @@ int run_adapt(const AdapterPlan& p, const AdapterTables& t, const HostEnv& env, 
   a.K = K;
   a.G = A;
   a.R = static_cast<int32_t>(R);
+  a.low_form = form;
   a.batch = T;
   a.max_row_blocks = p.max_row_blocks;
   a.early = early ? 1 : 0;
@@ -310,8 +320,7 @@ int run_adapt(const AdapterPlan& p, const AdapterTables& t, const HostEnv& env, 
     return status_of(launch_rows_skinny(dtype, mode, nr, a, (T + nr - 1) / nr, env.num_sms,
                                         stream));
   }
-  if (p.variant != kVariantSimt && aligned(x, 16) && aligned(w, 16) && aligned(f, 16) &&
-      aligned(y, 16))
+  if (wide_takes(p, x, w, f, y))
     return status_of(launch_rows_wide(dtype, mode, a, (T + 255) / 256, env.num_sms, stream));
   return status_of(launch_rows_simt(dtype, mode, a, env.num_sms, stream));
 }
@@ -601,14 +610,17 @@ int pgg_adapters_execute(const void* x, const void* weight, const void* a, const
       aligned(b, 16) && aligned(y, 8)) {
     rc = run_few_shrink(t, x, a, adapter, scale, u, T, K, R, A, dtype, s);
     if (rc != PGG_OK) return rc;
-    return run_adapt(p, t, env, false, false, false, adapter, x, weight, u, b, y, T, K, N, R, A,
-                     dtype, s);
+    return run_adapt(p, t, env, kLowFloat, false, false, false, adapter, x, weight, u, b, y, T, K, N,
+                     R, A, dtype, s);
   }
   rc = run_adapter_prep(p, t, true, adapter, T, A, s);
   if (rc != PGG_OK) return rc;
-  rc = run_shrink(p, t, env, true, false, x, a, scale, u, T, K, R, A, dtype, s);
+  const LowRankForm form = dtype == PGG_F32                   ? kLowRounded
+                           : wide_takes(p, x, weight, b, y) ? kLowSplit
+                                                            : kLowFloat;
+  rc = run_shrink(p, t, env, form, true, false, x, a, scale, u, T, K, R, A, dtype, s);
   if (rc != PGG_OK) return rc;
-  return run_adapt(p, t, env, false, false, true, nullptr, x, weight, u, b, y, T, K, N, R, A,
+  return run_adapt(p, t, env, form, false, false, true, nullptr, x, weight, u, b, y, T, K, N, R, A,
                    dtype, s);
 }
 
@@ -652,20 +664,22 @@ int pgg_adapters_grad(const void* d_y, const void* x, const void* weight, const 
   // weight-gradient kernels (which want the groups by id, one behind the other)
   const bool tensor = p.variant != kVariantSimt && aligned(x, 16) && aligned(d_y, 16) &&
                       aligned(a, 16) && aligned(b, 16) && aligned(d_a, 16) && aligned(d_b, 16) &&
+                      (!d_x || wide_takes(p, d_y, weight, a, d_x)) &&
                       static_cast<int64_t>(A) * ((K + 127) / 128 + (N + 127) / 128) <
                           kInt32Max / 4;
+  const LowRankForm form = tensor ? kLowSplit : kLowRounded;
   p.padded = tensor ? 1 : 0;
   rc = run_adapter_prep(p, t, tensor, adapter, T, A, s);
   if (rc != PGG_OK) return rc;
   // u and v need the tables alone, and the factors' gradients u and v alone: each runs beside the
   // launch before it. 8192 tokens, K 4096, N 2048, R 32: 149 us against 172 one after another.
-  rc = run_shrink(p, t, env, tensor, false, x, a, scale, u, T, K, R, A, dtype, s);
+  rc = run_shrink(p, t, env, form, tensor, false, x, a, scale, u, T, K, R, A, dtype, s);
   if (rc != PGG_OK) return rc;
-  rc = run_shrink(p, t, env, tensor, tensor, d_y, b, scale, v, T, N, R, A, dtype, s);
+  rc = run_shrink(p, t, env, form, tensor, tensor, d_y, b, scale, v, T, N, R, A, dtype, s);
   if (rc != PGG_OK) return rc;
   if (d_x) {
-    rc = run_adapt(p, t, env, true, tensor, true, nullptr, d_y, weight, v, a, d_x, T, N, K, R, A, dtype,
-                   s);
+    rc = run_adapt(p, t, env, form, true, tensor, true, nullptr, d_y, weight, v, a, d_x, T, N, K, R,
+                   A, dtype, s);
     if (rc != PGG_OK) return rc;
   }
   if (tensor) {

@@ -21,6 +21,7 @@
 #include <cstdint>
 
 #include "pgg_ops.h"
+#include "pgg_ops_mma.cuh"
 #include "pgg_ptx.cuh"
 
 namespace pgg {
@@ -53,6 +54,19 @@ __device__ __forceinline__ void st(void* p, int64_t i, float v) {
   if constexpr (DT == PGG_BF16) static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
 }
 
+// Rank n of a low-rank row (a.N ranks).
+template <int DT>
+__device__ __forceinline__ void store_low(const RowsArgs& a, int64_t row, int64_t n, float v) {
+  if (a.low_form == kLowFloat) {
+    static_cast<float*>(a.out)[row * a.N + n] = v;
+  } else if (a.low_form == kLowRounded) {
+    st<DT>(a.out, row * a.N + n, v);
+  } else if constexpr (DT != PGG_F32) {
+    uint16_t* p = static_cast<uint16_t*>(a.out) + row * low_width(a.N) + n / 32 * 64 + n % 32;
+    split16<DT>(v, p, p + 32);
+  }
+}
+
 // A [row][k] and B by element: column c of the tile at bcol[c-part] + k * kstride.
 struct Operand {
   const void* a;
@@ -64,7 +78,7 @@ struct Operand {
   int64_t half;     // gated: offset of the second half's columns; else 0
 };
 
-template <int DT, bool HALVES, bool KMAJOR>
+template <int DA, int DT, bool HALVES, bool KMAJOR>
 __device__ __forceinline__ void load_step(const Operand& o, const int32_t (&arow)[4], int64_t k0,
                                           int warp, int lane, float (&ra)[16], float (&rb)[32]) {
   const int l_k = lane & 7, l_r = lane >> 3;
@@ -73,7 +87,7 @@ __device__ __forceinline__ void load_step(const Operand& o, const int32_t (&arow
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       const int64_t k = k0 + 8 * q + l_k;
-      ra[4 * it + q] = arow[it] >= 0 && k < o.K ? ld<DT>(o.a, arow[it] * o.lda + k) : 0.0f;
+      ra[4 * it + q] = arow[it] >= 0 && k < o.K ? ld<DA>(o.a, arow[it] * o.lda + k) : 0.0f;
     }
   if constexpr (KMAJOR) {  // 8 k x 4 columns an instruction
 #pragma unroll
@@ -121,21 +135,21 @@ __device__ __forceinline__ void store_step(float* sa, float* sb, int warp, int l
   }
 }
 
-// acc += A B over the operand's whole reduction.
-template <int DT, bool HALVES, bool KMAJOR>
+// acc += A B over the operand's whole reduction (A of dtype DA, B of DT).
+template <int DA, int DT, bool HALVES, bool KMAJOR>
 __device__ __forceinline__ void product(Smem& sm, const Operand& o, const int32_t (&arow)[4],
                                         float (&acc)[8][8]) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int tx = tid & 15, ty = tid >> 4;
   float ra[16], rb[32];
-  load_step<DT, HALVES, KMAJOR>(o, arow, 0, warp, lane, ra, rb);
+  load_step<DA, DT, HALVES, KMAJOR>(o, arow, 0, warp, lane, ra, rb);
   __syncthreads();  // earlier reads of buffer 0 are done
   store_step<KMAJOR>(sm.a[0], sm.b[0], warp, lane, ra, rb);
   __syncthreads();
   int buf = 0;
   for (int64_t k0 = 0; k0 < o.K; k0 += kKc) {
     const bool more = k0 + kKc < o.K;
-    if (more) load_step<DT, HALVES, KMAJOR>(o, arow, k0 + kKc, warp, lane, ra, rb);
+    if (more) load_step<DA, DT, HALVES, KMAJOR>(o, arow, k0 + kKc, warp, lane, ra, rb);
     const float* pa = sm.a[buf];
     const float* pb = sm.b[buf];
 #pragma unroll 4
@@ -227,7 +241,7 @@ __global__ void __launch_bounds__(kThr, 3) rows_simt_kernel(const RowsArgs a) {
         o.bn = 1;
         o.b0 = (MODE == kShrink ? g * a.K * a.N : 0) + n0;
       }
-      product<DT, kHalves, MODE == kAdaptT>(sm, o, tok, acc);
+      product<DT, DT, kHalves, MODE == kAdaptT>(sm, o, tok, acc);
       if ((MODE == kAdapt || MODE == kAdaptT) && !none) {
         // the low-rank part: rows of u are in order, b [A, N, R] has the rank innermost
         int32_t urow[4];
@@ -243,7 +257,10 @@ __global__ void __launch_bounds__(kThr, 3) rows_simt_kernel(const RowsArgs a) {
         o.bk = 1;
         o.bn = a.R;
         o.b0 = (g * a.N + n0) * a.R;
-        product<DT, false, true>(sm, o, urow, acc);
+        if (a.low_form == kLowFloat)
+          product<PGG_F32, DT, false, true>(sm, o, urow, acc);
+        else
+          product<DT, DT, false, true>(sm, o, urow, acc);
       }
       const float sc = MODE == kShrink && a.scale ? a.scale[g] : 1.0f;
 #pragma unroll
@@ -270,7 +287,11 @@ __global__ void __launch_bounds__(kThr, 3) rows_simt_kernel(const RowsArgs a) {
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             const int64_t n = n0 + (j < 4 ? 4 * tx + j : 64 + 4 * tx + j - 4);
-            if (n < a.N) st<DT>(a.out, orow * a.N + n, acc[i][j] * sc);
+            if (n >= a.N) continue;
+            if (MODE == kShrink)
+              store_low<DT>(a, orow, n, acc[i][j] * sc);
+            else
+              st<DT>(a.out, orow * a.N + n, acc[i][j]);
           }
         }
       }

@@ -731,7 +731,6 @@ int host_env(HostEnv* env) {
   const int rc = device_info(&di);
   if (rc != PGG_OK) return rc;
   env->num_sms = di.num_sms;
-  env->force_variant = g_force_variant.load();
   env->hold_release = g_hold_release.load() != 0 ? 1 : 0;
   env->wait_limit_ns = g_wait_limit_ns.load();
   return PGG_OK;

@@ -11,7 +11,6 @@ namespace pgg {
 
 struct HostEnv {
   int num_sms;             // of the current device
-  int force_variant;       // test hook, -1 = automatic
   int hold_release;        // test hook
   uint64_t wait_limit_ns;  // bound of every wait inside a kernel
 };
@@ -139,10 +138,29 @@ enum RowsMode {
   kAdaptT = 3,   // the same with W given as [N, K]: the gradient of x
 };
 
+// How the low-rank rows u and v are stored between the product that writes them and the one that
+// reads them. They are sums, and the tensor cores read 16-bit operands: one rounding to 16 bits there
+// would be as large as the output's own (the factors' gradients of 8192 tokens lay 1.4 times as far
+// from the 64-bit values). So a 16-bit call on the tensor cores keeps each value as the sum of two
+// (split16 in pgg_ops_mma.cuh) and multiplies with both: at most 2^-16 of u is lost in bf16, 2^-21
+// of it or 2^-25 in fp16. It costs 1.5% at rank 32 (8191 tokens, 24 adapters, K = N = 4096: 191 -> 195
+// us), 5 to 8% at ranks of 64 and more, where it takes more low-rank steps.
+enum LowRankForm {
+  kLowRounded = 0,  // [rows, R] of the dtype (fp32 calls; the weight-gradient kernels' operand)
+  kLowSplit = 1,    // [rows, low_width(R)]: for each 32 ranks 32 hi, then 32 lo
+  kLowFloat = 2,    // [rows, R] fp32, for the FP32 pipes
+};
+#ifdef __CUDACC__
+#define PGG_HOST_DEVICE __host__ __device__
+#else
+#define PGG_HOST_DEVICE
+#endif
+PGG_HOST_DEVICE constexpr int64_t low_width(int64_t R) { return (R + 31) / 32 * 64; }
+
 struct RowsArgs {
   const void* x;           // rows gathered by token, K elements each
   const void* w;           // kGated [G, K, 2 N]; kShrink [G, K, N]; kAdapt [K, N]; kAdaptT [N, K]
-  const void* u;           // kAdapt*: [*, R] low-rank rows, scale applied
+  const void* u;           // kAdapt*: low-rank rows, scale applied, stored as low_form says
   const void* b;           // kAdapt*: [A, N, R]
   const float* probs;      // kGated: [M] weight of each original position, or null
   const float* scale;      // kShrink: [A] or null
@@ -153,12 +171,13 @@ struct RowsArgs {
   const int4* range;       // kShrink, padded: see AdapterTables
   const int32_t* box;      // kAdapt*
   WsHeader* hdr;
-  void* out;               // h [M, N], u [*, N], y [T, N] (rows in token order)
+  void* out;               // h [M, N], u (as low_form says), y [T, N] (rows in token order)
   void* gate_up;           // kGated: [M, 2 N] or null
   int64_t M, N, K, G, batch, max_row_blocks;
   int32_t R;
   int32_t n_blocks;
-  int32_t padded;          // kShrink: fill up an adapter's rows with zeros to a multiple of kRowPad
+  int32_t low_form;        // LowRankForm of u: kShrink writes it, kAdapt* reads it
+  int32_t padded;          // kShrink, split: fill up an adapter's rows with zeros to a multiple of kRowPad
   const int64_t* adapter;  // few tokens: [T]; u is fp32 in token order then
   int32_t early, late;     // see launch_order in pgg_ops_mma.cuh
   int32_t hold_release;
@@ -189,11 +208,11 @@ cudaError_t launch_rows_skinny(int dtype, RowsMode mode, int NR, RowsArgs a, int
 // Few tokens: u [T, R] fp32 in token order (R and K multiples of 8), and the ids' check.
 cudaError_t launch_few_shrink(int dtype, const RowsArgs& a, cudaStream_t stream);
 
-// Both factors' gradients, for tables in the padded order (16-bit, widths multiples of 8, 16-byte
-// aligned): out[w] [A, cols[w], R] = sum over an adapter's rows of left[w]^T right[w].
+// Both factors' gradients, for tables in the padded order (16-bit, u and v split, widths multiples
+// of 8, 16-byte aligned): out[w] [A, cols[w], R] = sum over an adapter's rows of left[w]^T right[w].
 struct OuterArgs {
   const void* left[2];   // x [T, cols[0]], d_y [T, cols[1]]: rows by token
-  const void* right[2];  // v, u [right_rows, R]: rows in the padded order
+  const void* right[2];  // v, u [right_rows, low_width(R)]: rows in the padded order
   void* out[2];
   const int4* range;     // [A + 1]
   const RowInfo* order;

@@ -63,6 +63,33 @@ __device__ __forceinline__ float2 unpack2(uint32_t w) {
     return __half22float2(*reinterpret_cast<const __half2*>(&w));
 }
 
+// v as the sum of two 16-bit values (see LowRankForm): hi is v cut off, lo the rounded rest. Both have
+// v's sign and (but for the smallest numbers) neither is 0, so that times an infinity they are the
+// same infinity, and their sum is what v times it is; where nothing is left, hi gives one unit to lo.
+template <int DT>
+__device__ __forceinline__ void split16(float v, uint16_t* hi, uint16_t* lo) {
+  const bool finite = fabsf(v) < INFINITY;
+  uint32_t h;
+  float left;
+  if constexpr (DT == PGG_BF16) {
+    const uint32_t b = __float_as_uint(v);
+    h = b >> 16;
+    if (finite && (b & 0xFFFFu) == 0 && (h & 0x7FFFu) != 0) --h;
+    left = v - __uint_as_float(h << 16);
+    *lo = __bfloat16_as_ushort(__float2bfloat16_rn(left));
+  } else {
+    h = __half_as_ushort(__float2half_rz(v));
+    left = v - __half2float(__ushort_as_half(static_cast<uint16_t>(h)));
+    if (finite && fabsf(left) <= 0x1p-25f && (h & 0x7FFFu) != 0) {  // (would round to 0)
+      --h;
+      left = v - __half2float(__ushort_as_half(static_cast<uint16_t>(h)));
+    }
+    *lo = __half_as_ushort(__float2half_rn(left));
+  }
+  if (!finite) *lo = static_cast<uint16_t>(h);
+  *hi = static_cast<uint16_t>(h);
+}
+
 // ptx::mapa of a shared-memory address.
 __device__ __forceinline__ uint32_t mapa_addr(uint32_t addr, uint32_t rank) {
   uint32_t r;

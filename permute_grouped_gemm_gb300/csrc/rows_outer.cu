@@ -6,8 +6,10 @@
 // Both in one launch: tall, R-wide products whose reduction runs over the rows
 // of one adapter, so what they cost is reading x and d_y once (R multiply-adds
 // a byte). Tile: one adapter, 128 of the K (N) columns as accumulator lanes and
-// 64 ranks as accumulator columns, fp32 in tensor memory (two buffers); both
-// operands are MN-major. A stage is 128 rows: 128 columns of x, by TMA where
+// 32 or 64 ranks (P of 32) as accumulator columns, fp32 in tensor memory (two
+// buffers): u and v come as the sums of two values (see LowRankForm), so 32 ranks
+// take 64 columns, 32 for the hi and 32 for the lo parts, which the epilogue adds.
+// Both operands are MN-major. A stage is 128 rows: 128 columns of x, by TMA where
 // the 128 rows are neighbouring tokens, else gathered by token with cp.async
 // (one warp per stage slot), and the rows' ranks of v by TMA. v is stored so
 // that an adapter's rows end on a multiple of 128 with rows of zeros, and their
@@ -33,23 +35,32 @@ namespace pgg {
 namespace {
 
 constexpr int kM = 128;            // columns of x (d_y) per tile: accumulator lanes
-constexpr int kNR = 64;            // ranks per tile: accumulator columns
 constexpr int kRows = 128;         // reduction per stage
 constexpr int kPanel = kRows * 128;
 constexpr int kABytes = 2 * kPanel;
-constexpr int kBBytes = kPanel;
-constexpr int kStageBytes = kABytes + kBBytes;
-constexpr int kStages = 4;
-constexpr int kRedBytes = kM * kNR * 4;
 constexpr int kEpiWarps = 4;
-constexpr int kGatherWarps = 2 * kStages;  // two per stage slot
-constexpr int kEpiWarp0 = 12;              // (a multiple of four: tensor-memory lanes)
-constexpr int kThreads = 32 * (kEpiWarp0 + kEpiWarps);
-constexpr int kTmemCols = 2 * kNR;
+
+// P: panels of 32 ranks a tile. One where the rank is at most 32, else two, so that x and d_y are
+// not read more often than ranks beyond 64 need.
+template <int P>
+struct Cfg {
+  static constexpr int kNR = 32 * P;       // ranks per tile
+  static constexpr int kCols = 64 * P;     // accumulator columns
+  static constexpr int kBBytes = P * kPanel;
+  static constexpr int kStageBytes = kABytes + kBBytes;
+  static constexpr int kStages = P == 1 ? 4 : 3;
+  static constexpr int kRedBytes = kM * kNR * 4;
+  static constexpr int kGatherWarps = 2 * kStages;  // two per stage slot
+  static constexpr int kEpiWarp0 = P == 1 ? 12 : 8;  // (a multiple of four: tensor-memory lanes)
+  static constexpr int kThreads = 32 * (kEpiWarp0 + kEpiWarps);
+  static constexpr int kTmemCols = 2 * kCols;
+  static_assert(2 + kGatherWarps <= kEpiWarp0, "warp roles");
+};
+constexpr int kMaxStages = 4;
 
 struct Ctl {
-  uint64_t full[kStages];   // bytes + the two gather warps' arrivals
-  uint64_t empty[kStages];  // MMAs of the stage done
+  uint64_t full[kMaxStages];   // bytes + the two gather warps' arrivals
+  uint64_t empty[kMaxStages];  // MMAs of the stage done
   uint64_t tfull[2], tempty[2];
   uint64_t rfull, rempty;   // partial sums of all CTAs received here / mine read by all CTAs
   uint64_t drain;
@@ -57,9 +68,13 @@ struct Ctl {
   int abort;
 };
 
-constexpr int kSmemBytes =
-    kStages * kStageBytes + kRedBytes + static_cast<int>(sizeof(Ctl)) + 1024;
-static_assert(kSmemBytes <= 227 * 1024, "shared memory per CTA");
+template <int P>
+constexpr int smem_bytes() {
+  return Cfg<P>::kStages * Cfg<P>::kStageBytes + Cfg<P>::kRedBytes +
+         static_cast<int>(sizeof(Ctl)) + 1024;
+}
+static_assert(smem_bytes<1>() <= 227 * 1024 && smem_bytes<2>() <= 227 * 1024,
+              "shared memory per CTA");
 
 __device__ __forceinline__ uint32_t cluster_size() {
   uint32_t r;
@@ -77,13 +92,14 @@ struct Tile {
 };
 
 // Tiles run over the adapters first, so that neighbouring clusters share the work of a large one.
+template <int P>
 __device__ __forceinline__ Tile tile_of(uint32_t t, const OuterArgs& a, uint32_t rank,
                                         uint32_t S) {
   Tile x;
   const uint32_t A = static_cast<uint32_t>(a.A);
   x.ad = static_cast<int>(t % A);
   uint32_t q = t / A;
-  x.r0 = static_cast<int>(q % a.r_blocks) * kNR;
+  x.r0 = static_cast<int>(q % a.r_blocks) * Cfg<P>::kNR;
   q /= a.r_blocks;
   x.which = q >= static_cast<uint32_t>(a.blocks0) ? 1 : 0;
   x.c0 = static_cast<int64_t>(x.which ? q - a.blocks0 : q) * kM;
@@ -100,29 +116,32 @@ __device__ __forceinline__ int32_t box_of(const OuterArgs& a, const Tile& x, int
   return box_of_rows(a.order, static_cast<int64_t>(x.range.x) + kRows * s, kRows);
 }
 
+template <int P>
 __device__ void producer(uint8_t* smem, Ctl* ctl, const CUtensorMap* tm, const OuterArgs& a,
                          uint32_t total, uint32_t first, uint32_t step, uint32_t rank,
                          uint32_t S) {
+  using C = Cfg<P>;
   const uint64_t lim = a.wait_limit_ns;
   volatile int* abort = &ctl->abort;
   int stage = 0;
   uint32_t phase = 0, outstanding = 0, last_parity = 0;
   bool failed = false;
   for (uint32_t t = first; t < total && !failed; t += step) {
-    const Tile x = tile_of(t, a, rank, S);
-    const int64_t C = a.cols[x.which];
+    const Tile x = tile_of<P>(t, a, rank, S);
     const CUtensorMap* tm_x = tm + 2 * x.which;
-    const bool second = x.c0 + 64 < C;
+    const bool second = x.c0 + 64 < a.cols[x.which];
     for (int s = x.s0; s < x.s1; ++s) {
       const int32_t box = box_of(a, x, s);
       if (!ptx::mbar_wait(&ctl->empty[stage], phase ^ 1u, lim, abort)) {
         failed = true;
         break;
       }
-      uint8_t* sa = smem + stage * kStageBytes;
+      uint8_t* sa = smem + stage * C::kStageBytes;
       ptx::mbar_arrive_expect_tx(&ctl->full[stage],
-                                 kBBytes + (box >= 0 ? (second ? 2 * kPanel : kPanel) : 0));
-      ptx::tma_load_2d(sa + kABytes, tm_x + 1, &ctl->full[stage], x.r0, x.range.z + kRows * s);
+                                 C::kBBytes + (box >= 0 ? (second ? 2 * kPanel : kPanel) : 0));
+      for (int p = 0; p < P; ++p)  // (32 ranks are 64 columns of v)
+        ptx::tma_load_2d(sa + kABytes + p * kPanel, tm_x + 1, &ctl->full[stage],
+                         2 * x.r0 + 64 * p, x.range.z + kRows * s);
       if (box >= 0) {
         ptx::tma_load_2d(sa, tm_x, &ctl->full[stage], static_cast<int32_t>(x.c0), box);
         if (second)
@@ -131,7 +150,7 @@ __device__ void producer(uint8_t* smem, Ctl* ctl, const CUtensorMap* tm, const O
       }
       outstanding |= 1u << stage;
       last_parity = (last_parity & ~(1u << stage)) | (phase << stage);
-      if (++stage == kStages) {
+      if (++stage == C::kStages) {
         stage = 0;
         phase ^= 1u;
       }
@@ -142,31 +161,32 @@ __device__ void producer(uint8_t* smem, Ctl* ctl, const CUtensorMap* tm, const O
     raise_status(a.hdr, kStTimeout, 52);
   }
   int no_abort = 0;
-  for (int s = 0; s < kStages; ++s)
+  for (int s = 0; s < C::kStages; ++s)
     if (outstanding & (1u << s))
       ptx::mbar_wait(&ctl->full[s], (last_parity >> s) & 1u, lim, &no_abort);
 }
 
 // Gather warps 2 w and 2 w + 1 fill half of stage slot w each where its rows are not neighbours:
 // row (lane >> 4) + 2 q, 16-byte chunk lane & 15 of its 256 bytes.
+template <int P>
 __device__ void gatherer(uint8_t* smem, Ctl* ctl, const OuterArgs& a, uint32_t total,
                          uint32_t first, uint32_t step, uint32_t rank, uint32_t S) {
   const uint64_t lim = a.wait_limit_ns;
   volatile int* abort = &ctl->abort;
   const int w = ((threadIdx.x >> 5) - 2) >> 1, half = ((threadIdx.x >> 5) - 2) & 1;
   const int lane = threadIdx.x & 31, c = lane & 15;
-  const uint32_t sa = ptx::smem_addr(smem + w * kStageBytes + (c >> 3) * kPanel);
+  const uint32_t sa = ptx::smem_addr(smem + w * Cfg<P>::kStageBytes + (c >> 3) * kPanel);
   uint32_t phase = 0;
   bool failed = false;
   int kb = w;  // the warp's next step, counted from the start of tile t
   for (uint32_t t = first; t < total && !failed; t += step) {
-    const Tile x = tile_of(t, a, rank, S);
+    const Tile x = tile_of<P>(t, a, rank, S);
     const int64_t C = a.cols[x.which];
     const char* base = static_cast<const char*>(a.left[x.which]);
     const int64_t col = x.c0 + 8 * c;
     const bool in = col < C;
     const int steps = x.s1 - x.s0;
-    for (; kb < steps; kb += kStages) {
+    for (; kb < steps; kb += Cfg<P>::kStages) {
       const int s = x.s0 + kb;
       const int32_t box = box_of(a, x, s);
       int32_t tok[2];  // rows 64 half + lane + 32 h of the step; -1 past the adapter's
@@ -209,31 +229,32 @@ __device__ void gatherer(uint8_t* smem, Ctl* ctl, const OuterArgs& a, uint32_t t
   }
 }
 
-template <int DT>
+template <int DT, int P>
 __device__ void mma_issuer(uint8_t* smem, Ctl* ctl, uint32_t tmem_base, const OuterArgs& a,
                            uint32_t total, uint32_t first, uint32_t step, uint32_t rank,
                            uint32_t S) {
-  constexpr uint32_t idesc = ptx::idesc_make_mn(DT == PGG_BF16 ? 1u : 0u, kM, kNR);
+  using C = Cfg<P>;
+  constexpr uint32_t idesc = ptx::idesc_make_mn(DT == PGG_BF16 ? 1u : 0u, kM, C::kCols);
   const uint64_t lim = a.wait_limit_ns;
   volatile int* abort = &ctl->abort;
   int stage = 0, acc = 0;
   uint32_t phase = 0, aph = 0;
   bool issued = false, failed = false;
   for (uint32_t t = first; t < total && !failed; t += step) {
-    const Tile x = tile_of(t, a, rank, S);
+    const Tile x = tile_of<P>(t, a, rank, S);
     if (!ptx::mbar_wait(&ctl->tempty[acc], aph ^ 1u, lim, abort)) {
       failed = true;
       break;
     }
     ptx::tc_fence_after_sync();
-    const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * kNR);
+    const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * C::kCols);
     for (int s = x.s0; s < x.s1; ++s) {
       if (!ptx::mbar_wait(&ctl->full[stage], phase, lim, abort)) {
         failed = true;
         break;
       }
       ptx::tc_fence_after_sync();
-      const uint32_t sa = ptx::smem_addr(smem + stage * kStageBytes);
+      const uint32_t sa = ptx::smem_addr(smem + stage * C::kStageBytes);
       const uint64_t da = ptx::sdesc_sw128_mn(sa, kPanel);
       const uint64_t db = ptx::sdesc_sw128_mn(sa + kABytes, kPanel);
 #pragma unroll
@@ -243,7 +264,7 @@ __device__ void mma_issuer(uint8_t* smem, Ctl* ctl, uint32_t tmem_base, const Ou
       }
       issued = true;
       ptx::mma_commit(&ctl->empty[stage]);
-      if (++stage == kStages) {
+      if (++stage == C::kStages) {
         stage = 0;
         phase ^= 1u;
       }
@@ -264,10 +285,11 @@ __device__ void mma_issuer(uint8_t* smem, Ctl* ctl, uint32_t tmem_base, const Ou
   }
 }
 
-template <int DT>
+template <int DT, int P>
 __device__ void epilogue(Ctl* ctl, float* red, uint32_t tmem_base, const OuterArgs& a,
                          uint32_t total, uint32_t first, uint32_t step, uint32_t rank,
                          uint32_t S) {
+  constexpr int kNR = Cfg<P>::kNR;
   const uint64_t lim = a.wait_limit_ns;
   volatile int* abort = &ctl->abort;
   const int lane = threadIdx.x & 31;
@@ -279,7 +301,7 @@ __device__ void epilogue(Ctl* ctl, float* red, uint32_t tmem_base, const OuterAr
   uint32_t aph = 0, rph = 0;
   bool held = a.hold_release != 0;
   for (uint32_t t = first; t < total; t += step) {
-    const Tile x = tile_of(t, a, rank, S);
+    const Tile x = tile_of<P>(t, a, rank, S);
     const int nr = a.R - x.r0 < kNR ? a.R - x.r0 : kNR;  // (a multiple of 8)
     bool ok = ptx::mbar_wait(&ctl->tfull[acc], aph, lim, abort);
     ok = ok && ptx::mbar_wait_cluster(&ctl->rempty, rph ^ 1u, lim, abort);
@@ -293,18 +315,21 @@ __device__ void epilogue(Ctl* ctl, float* red, uint32_t tmem_base, const OuterAr
     ptx::tc_fence_after_sync();
     if (x.s1 > x.s0) {  // (a CTA without a step has nothing to send, and is not read)
       const uint32_t t_lane = tmem_base + (static_cast<uint32_t>(32 * quarter) << 16) +
-                              static_cast<uint32_t>(acc * kNR);
+                              static_cast<uint32_t>(acc * Cfg<P>::kCols);
       const int dst = tid >> shift;  // the CTA that finishes this lane's column
       float* mine = red + static_cast<int>(rank) * kNR * lanes + (tid & (lanes - 1));
       const uint32_t to = ptx::mapa(mine, static_cast<uint32_t>(dst));
 #pragma unroll 1
       for (int c0 = 0; c0 < nr; c0 += 16) {
-        uint32_t v[16];
-        ptx::tmem_ld_32x32b_x16(t_lane + static_cast<uint32_t>(c0), v);
+        uint32_t hi[16], lo[16];  // ranks c0 .. c0 + 15
+        const uint32_t at = t_lane + static_cast<uint32_t>(c0 / 32 * 64 + c0 % 32);
+        ptx::tmem_ld_32x32b_x16(at, hi);
+        ptx::tmem_ld_32x32b_x16(at + 32u, lo);
         ptx::tmem_ld_wait();
 #pragma unroll
         for (int i = 0; i < 16; ++i)
-          st_cluster_f32(to + static_cast<uint32_t>((c0 + i) * lanes * 4), __uint_as_float(v[i]));
+          st_cluster_f32(to + static_cast<uint32_t>((c0 + i) * lanes * 4),
+                         __uint_as_float(hi[i]) + __uint_as_float(lo[i]));
       }
     }
     ptx::tc_fence_before_sync();
@@ -351,15 +376,16 @@ struct OuterMaps {
   CUtensorMap m[4];  // x, v, d_y, u
 };
 
-template <int DT>
-__global__ void __launch_bounds__(kThreads, 1)
+template <int DT, int P>
+__global__ void __launch_bounds__(Cfg<P>::kThreads, 1)
     rows_outer_kernel(const __grid_constant__ OuterMaps maps, const OuterArgs a) {
+  using C = Cfg<P>;
   launch_order(false, a.late);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
-  float* red = reinterpret_cast<float*>(smem + kStages * kStageBytes);
-  auto* ctl = reinterpret_cast<Ctl*>(smem + kStages * kStageBytes + kRedBytes);
+  float* red = reinterpret_cast<float*>(smem + C::kStages * C::kStageBytes);
+  auto* ctl = reinterpret_cast<Ctl*>(smem + C::kStages * C::kStageBytes + C::kRedBytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = ptx::cluster_ctarank(), S = cluster_size();
 
@@ -378,7 +404,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t first = blockIdx.x / S, step = gridDim.x / S;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kStages; ++s) {
+    for (int s = 0; s < C::kStages; ++s) {
       ptx::mbar_init(&ctl->full[s], 3);
       ptx::mbar_init(&ctl->empty[s], 1);
     }
@@ -394,7 +420,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (warp == 0 && lane < 4) ptx::tma_prefetch_desc(&maps.m[lane]);
   if (warp == 1) {
-    ptx::tmem_alloc(&ctl->tmem_base, kTmemCols);
+    ptx::tmem_alloc(&ctl->tmem_base, C::kTmemCols);
     ptx::tmem_relinquish();
   }
   ptx::tc_fence_before_sync();
@@ -404,13 +430,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem_base = ctl->tmem_base;
 
   if (warp == 0) {
-    if (lane == 0) producer(smem, ctl, maps.m, a, total, first, step, rank, S);
+    if (lane == 0) producer<P>(smem, ctl, maps.m, a, total, first, step, rank, S);
   } else if (warp == 1) {
-    if (lane == 0) mma_issuer<DT>(smem, ctl, tmem_base, a, total, first, step, rank, S);
-  } else if (warp < 2 + kGatherWarps) {
-    gatherer(smem, ctl, a, total, first, step, rank, S);
-  } else if (warp >= kEpiWarp0) {
-    epilogue<DT>(ctl, red, tmem_base, a, total, first, step, rank, S);
+    if (lane == 0) mma_issuer<DT, P>(smem, ctl, tmem_base, a, total, first, step, rank, S);
+  } else if (warp < 2 + C::kGatherWarps) {
+    gatherer<P>(smem, ctl, a, total, first, step, rank, S);
+  } else if (warp >= C::kEpiWarp0) {
+    epilogue<DT, P>(ctl, red, tmem_base, a, total, first, step, rank, S);
   }
 
   ptx::tc_fence_before_sync();
@@ -418,9 +444,30 @@ __global__ void __launch_bounds__(kThreads, 1)
   ptx::cluster_sync();  // no CTA leaves while another may still write to it
   if (warp == 1) {
     ptx::tc_fence_after_sync();
-    ptx::tmem_dealloc(tmem_base, kTmemCols);
+    ptx::tmem_dealloc(tmem_base, C::kTmemCols);
   }
   launch_end(a.late);
+}
+
+template <int DT, int P>
+cudaError_t launch_t(const OuterMaps& maps, OuterArgs a, int num_sms, cudaStream_t stream) {
+  using C = Cfg<P>;
+  a.r_blocks = static_cast<uint32_t>((a.R + C::kNR - 1) / C::kNR);
+  // Two CTAs a tile while there are few tiles for the SMs, so that one long adapter does not hold up
+  // the rest; with many the exchange costs more than it evens out (8192 tokens, K 4096, N 2048, of
+  // one adapter: 204 us alone, 190 in two; of 48: 227 alone, 264 in two).
+  const int64_t all_tiles =
+      static_cast<int64_t>(a.A) * a.r_blocks * (a.blocks0 + a.blocks1);
+  const int S = all_tiles < 4 * num_sms ? 2 : 1;
+  static ClusterLimits limits;
+  const auto kern = rows_outer_kernel<DT, P>;
+  int clusters = 0;
+  const cudaError_t err = clusters_that_fit(&limits, kern, C::kThreads, smem_bytes<P>(), S, num_sms,
+                                            &clusters);
+  if (err != cudaSuccess) return err;
+  if (all_tiles < clusters) clusters = static_cast<int>(all_tiles);
+  return launch_pdl(kern, dim3(static_cast<unsigned>(S * clusters)), dim3(C::kThreads),
+                    static_cast<size_t>(smem_bytes<P>()), stream, static_cast<unsigned>(S), maps, a);
 }
 
 }  // namespace
@@ -428,27 +475,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 cudaError_t launch_rows_outer(int dtype, OuterArgs a, int num_sms, cudaStream_t stream) {
   a.blocks0 = static_cast<int32_t>((a.cols[0] + kM - 1) / kM);
   a.blocks1 = static_cast<int32_t>((a.cols[1] + kM - 1) / kM);
-  a.r_blocks = static_cast<uint32_t>((a.R + kNR - 1) / kNR);
   OuterMaps maps;
   for (int w = 0; w < 2; ++w)
     if (!encode_map_rows(&maps.m[2 * w], dtype, a.left[w], a.cols[w], a.T, kRows) ||
-        !encode_map_rows(&maps.m[2 * w + 1], dtype, a.right[w], a.R, a.right_rows, kRows))
+        !encode_map_rows(&maps.m[2 * w + 1], dtype, a.right[w], low_width(a.R), a.right_rows, kRows))
       return cudaErrorInvalidValue;
-  const auto kern = dtype == PGG_BF16 ? rows_outer_kernel<PGG_BF16> : rows_outer_kernel<PGG_F16>;
-  // Two CTAs a tile while there are few tiles for the SMs, so that one long adapter does not hold up
-  // the rest; with many the exchange costs more than it evens out (8192 tokens, K 4096, N 2048, of
-  // one adapter: 204 us alone, 190 in two; of 48: 227 alone, 264 in two).
-  const int64_t all_tiles =
-      static_cast<int64_t>(a.A) * a.r_blocks * (a.blocks0 + a.blocks1);
-  const int S = all_tiles < 4 * num_sms ? 2 : 1;
-  static ClusterLimits limits[2];
-  int clusters = 0;
-  const cudaError_t err = clusters_that_fit(&limits[dtype == PGG_BF16 ? 0 : 1], kern, kThreads,
-                                            kSmemBytes, S, num_sms, &clusters);
-  if (err != cudaSuccess) return err;
-  if (all_tiles < clusters) clusters = static_cast<int>(all_tiles);
-  return launch_pdl(kern, dim3(static_cast<unsigned>(S * clusters)), dim3(kThreads),
-                    static_cast<size_t>(kSmemBytes), stream, static_cast<unsigned>(S), maps, a);
+  if (dtype == PGG_BF16)
+    return a.R <= 32 ? launch_t<PGG_BF16, 1>(maps, a, num_sms, stream)
+                     : launch_t<PGG_BF16, 2>(maps, a, num_sms, stream);
+  return a.R <= 32 ? launch_t<PGG_F16, 1>(maps, a, num_sms, stream)
+                   : launch_t<PGG_F16, 2>(maps, a, num_sms, stream);
 }
 
 }  // namespace pgg

@@ -379,14 +379,30 @@ __device__ __forceinline__ void write_rows(const float* red, int slot, uint32_t 
   } else if constexpr (MODE == kShrink) {
     const int left = static_cast<int>(a.N - x.n0 < kM ? a.N - x.n0 : kM);
     const int groups = left / 4;  // of four columns
+    const int64_t width = a.low_form == kLowSplit ? low_width(a.N) : a.N;
 #pragma unroll 2
     for (int i = 32 * warp + lane; i < n * groups; i += 32 * kEpiWarps) {
       const int j = i / groups, c = 4 * (i - j * groups);
       float4 v = sum4(red, slot, S, j * kM + c);
       v = make_float4(v.x * row_scale, v.y * row_scale, v.z * row_scale, v.w * row_scale);
-      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) +
-                                (static_cast<int64_t>(x.urow) + j0 + j) * a.N + x.n0 + c) =
-          pack4<DT>(v);
+      const int64_t row = (static_cast<int64_t>(x.urow) + j0 + j) * width, r = x.n0 + c;
+      if (a.low_form == kLowFloat) {
+        *reinterpret_cast<float4*>(static_cast<float*>(a.out) + row + r) = v;
+        continue;
+      }
+      uint16_t* p = static_cast<uint16_t*>(a.out) + row;
+      if (a.low_form == kLowRounded) {
+        *reinterpret_cast<uint2*>(p + r) = pack4<DT>(v);
+        continue;
+      }
+      ushort4 hi, lo;
+      split16<DT>(v.x, &hi.x, &lo.x);
+      split16<DT>(v.y, &hi.y, &lo.y);
+      split16<DT>(v.z, &hi.z, &lo.z);
+      split16<DT>(v.w, &hi.w, &lo.w);
+      p += r / 32 * 64 + r % 32;
+      *reinterpret_cast<ushort4*>(p) = hi;
+      *reinterpret_cast<ushort4*>(p + 32) = lo;
     }
   } else {
     const int64_t c = x.n0 + 4 * lane;
@@ -565,8 +581,12 @@ __device__ void epilogue(Ctl<Cfg<MODE, NR, PANELS>::kStages>* ctl, float* red, u
                                                            x.urow));
         for (int j = x.rows + static_cast<int>(rank) * kEpiWarps + quarter; j < end;
              j += static_cast<int>(S) * kEpiWarps)
-          for (int64_t c = x.n0 + lane; c < a.N && c < x.n0 + kM; c += 32)
-            static_cast<uint16_t*>(a.out)[(static_cast<int64_t>(x.urow) + j) * a.N + c] = 0;
+          for (int64_t c = x.n0 + lane; c < a.N && c < x.n0 + kM; c += 32) {
+            uint16_t* p = static_cast<uint16_t*>(a.out) +
+                          (static_cast<int64_t>(x.urow) + j) * low_width(a.N) + c / 32 * 64 + c % 32;
+            p[0] = 0;
+            p[32] = 0;
+          }
       }
     }
     __syncwarp();

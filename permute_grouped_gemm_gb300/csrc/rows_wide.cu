@@ -26,8 +26,11 @@
 // meets, the A operand is u and the B operand b[ad], and the MMA writes only
 // that adapter's accumulator lanes (disable-output-lane). Masking the output
 // and not the operand keeps what another adapter's weights hold (infinities,
-// NaN) out of the row: 0 * inf never happens. u is rounded to the dtype once
-// (it is an operand of the tensor cores), its sums are fp32.
+// NaN) out of the row: 0 * inf never happens. u is an operand of the tensor
+// cores, so it comes as the sum of two values of the dtype (see LowRankForm): a
+// low-rank step covers 32 ranks, their 32 hi and 32 lo parts fill the step's 64
+// columns of A, and both meet the same rows of b. Two more MMAs a 32 ranks are
+// hidden behind the step's copies; ranks above 32 take a step per 32.
 //
 // Warp roles per CTA: 0 TMA; 1 tensor-memory allocation and (even CTA) MMA
 // issue; one gather warp per stage slot; eight epilogue warps an MMA. Tiles are
@@ -113,7 +116,12 @@ struct Shape {
 __device__ __forceinline__ int main_steps(const RowsArgs& a) {
   return static_cast<int>((a.K + kFK - 1) / kFK);
 }
-__device__ __forceinline__ int rank_steps(const RowsArgs& a) { return (a.R + kFK - 1) / kFK; }
+__device__ __forceinline__ int rank_span(const RowsArgs& a) {
+  return a.low_form == kLowSplit ? kFK / 2 : kFK;
+}
+__device__ __forceinline__ int rank_steps(const RowsArgs& a) {
+  return (a.R + rank_span(a) - 1) / rank_span(a);
+}
 
 // The tiles' numbers: `full` whole ones, then (H == 2) the two halves of each of the others, so that
 // a last round that would leave most pairs of CTAs idle takes half the time.
@@ -173,7 +181,7 @@ __device__ __forceinline__ Tile tile_of(uint32_t t, const Schedule& s, const Row
 __device__ __forceinline__ int4 segment_of(const RowsArgs& a, const Tile& x, int e, int* r0) {
   const int rs = rank_steps(a);
   const int s = e / rs;
-  *r0 = (e - s * rs) * kFK;
+  *r0 = (e - s * rs) * rank_span(a);
   return a.segs[x.seg0 + s];
 }
 
@@ -353,15 +361,19 @@ __device__ void x_gatherer(uint8_t* smem, WideCtl* ctl, const RowsArgs& a, const
         }
         int r0;
         const int4 seg = segment_of(a, x, kb - nks, &r0);
-        const int64_t r = r0 + c * 8;
+        // chunk c: ranks 8 c, or the hi or lo parts of ranks 8 (c % 4), of the step's
+        const bool split = a.low_form == kLowSplit;
+        const bool in = r0 + 8 * (split ? c & 3 : c) < a.R;
+        const int64_t width = split ? low_width(a.R) : a.R;
+        const int64_t col = (split ? 2 * r0 : r0) + 8 * c;
         const char* ub = static_cast<const char*>(a.u);
 #pragma unroll 4
         for (int q = 0; q < kFM / 4; ++q) {
           const int rr = (lane >> 3) + 4 * q;
           const int64_t row = x.row0 + rr;
-          const bool ok = r < a.R && rr < x.rows && row >= seg.y && row < seg.z;
+          const bool ok = in && rr < x.rows && row >= seg.y && row < seg.z;
           const void* src = ok ? static_cast<const void*>(
-                                     ub + ((seg.w + (row - seg.y)) * a.R + r) * 2)
+                                     ub + ((seg.w + (row - seg.y)) * width + col) * 2)
                                : static_cast<const void*>(ub);
           ptx::cp_async_16(sa_slot + rr * 128 + ((c ^ (rr & 7)) << 4), src, ok ? 16u : 0u);
         }
@@ -441,12 +453,16 @@ __device__ void mma_issuer(uint8_t* smem, WideCtl* ctl, uint32_t tmem_base, cons
         const uint32_t sb = sa + kABytes + h * kHalfBytes;
         if (low) {
           const uint64_t db = ptx::sdesc_sw128(sb);
+          const bool split = a.low_form == kLowSplit;
 #pragma unroll
-          for (int kk = 0; kk < kFK / 16; ++kk)
-            if (r0 + 16 * kk < a.R) {
+          for (int kk = 0; kk < kFK / 16; ++kk) {
+            const int kb = split ? kk & 1 : kk;  // 16 ranks of b; kk 2 and 3 of a split are lo parts
+            if (r0 + 16 * kb < a.R) {
               const uint64_t off = static_cast<uint64_t>((kk * 32) >> 4);
-              mma_f16_pair_lanes(d_tmem, da + off, db + off, idesc_k, m, 1u);
+              const uint64_t b_off = static_cast<uint64_t>((kb * 32) >> 4);
+              mma_f16_pair_lanes(d_tmem, da + off, db + b_off, idesc_k, m, 1u);
             }
+          }
         } else if constexpr (MODE == kAdaptT) {
           const uint64_t db = ptx::sdesc_sw128(sb);
 #pragma unroll
