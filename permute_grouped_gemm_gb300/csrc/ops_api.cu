@@ -32,11 +32,13 @@ constexpr double kSkinnyRows = 104.0;
 // N 4096, R 16, 256 tokens: 4 adapters 48 us and 53, 64 adapters 52 and 109; K = N = 4096, R 32,
 // 32 adapters, 256 tokens: 56 and 64; R 64, 16 adapters: 64 tokens 32 and 44, 96 tokens 51 and 45;
 // K 2048, N 5120, R 64: 128 tokens 79 and 40. Beyond one block of tokens only while the tiles of 64
-// tokens x 128 columns fit the 152 SMs at once (K 2048, N 5120, R 32: 192 tokens 42 and 51, 256 67
-// and 50).
+// tokens x 128 columns fit the SMs at once (K 2048, N 5120, R 32: 192 tokens 42 and 51, 256 67 and
+// 50). Their number is written here: the plan and the workspace's size go by this rule, and no
+// device is asked for them.
+constexpr int64_t kSms = 152;
 bool few_tokens(int64_t T, int64_t N, int64_t R) {
   if (T <= 64) return T * R <= 8192;
-  return T <= 256 && R <= 32 && (T + 63) / 64 * ((N + 127) / 128) <= 152;
+  return T <= 256 && R <= 32 && (T + 63) / 64 * ((N + 127) / 128) <= kSms;
 }
 
 int few_token_block(int64_t T) { return T <= 16 ? 16 : T <= 32 ? 32 : 64; }

@@ -468,7 +468,10 @@ cudaError_t launch_adapter_prep(const AdapterPrepArgs& a, cudaStream_t stream) {
   err = launch_pdl(adapter_place_kernel, dim3(a.blocks), dim3(kSortThreads),
                    static_cast<size_t>(kSortThreads / 32) * G * 4, stream, 1, a);
   if (err != cudaSuccess) return err;
-  return launch_pdl(adapter_boxes_kernel, dim3(152), dim3(kSortThreads), 0, stream, 1, a);
+  const int64_t per = kSortThreads / 32;  // boxes of a block at a time, a warp each
+  const int64_t boxes = (2 * ((a.T + 255) / 256) + per - 1) / per;
+  return launch_pdl(adapter_boxes_kernel, dim3(static_cast<unsigned>(boxes < 1024 ? boxes : 1024)),
+                    dim3(kSortThreads), 0, stream, 1, a);
 }
 
 }  // namespace pgg
