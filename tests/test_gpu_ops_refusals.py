@@ -29,7 +29,7 @@ I64, F32 = torch.int64, torch.float32
 def calls():
     idx = torch.arange(T * TOPK, device="cuda")
     groups = torch.full((G,), T * TOPK // G, device="cuda")
-    size = 1 << 16  # of every workspace here
+    size = 1 << 20  # of every workspace here
     ws = on(size, torch.uint8)
     yield pgg.route, dict(logits=on((T, G), F32), top_k=TOPK, bias=on(G, F32),
                           probs=on((T, TOPK), F32), experts=on((T, TOPK), I64),
