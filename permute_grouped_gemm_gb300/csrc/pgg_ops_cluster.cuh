@@ -1,5 +1,5 @@
-// Writes into the shared memory of the other blocks of a cluster by the kernels that exchange counts
-// and sums there.
+// Writes into the shared memory of a cluster's other blocks by the kernels that exchange counts and
+// sums there.
 //
 // A block may be touched only once it has started, and that the blocks of a cluster run side by
 // side does not say that all of them have. So such a kernel arrives at the cluster's barrier first
@@ -11,9 +11,11 @@
 
 namespace pgg {
 
-// First half of the cluster's barrier: this thread has started. Every thread, once.
+// First half of the cluster's barrier: this thread has started. Every thread, once. (Nothing that it
+// wrote has to be seen by the others, so it orders nothing: 200 tokens of the few-token form 34.0 ->
+// 32.7 us against an arrival that releases.)
 __device__ __forceinline__ void cluster_started() {
-  asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+  asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
 }
 
 // Second half: all blocks of the cluster have started. Every thread, before its first remote store.
