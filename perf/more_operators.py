@@ -172,7 +172,7 @@ def _prepare_norm(gen, case):
     s = dict(case=case, residual_scale=0.75)
     s["x"] = _normal(gen, (t, h), dt, 2.0)
     s["y"] = _normal(gen, (t, h), DTYPES[case["y"]], 0.7)
-    shape = {"none": None, "channel": (h,), "token": (t,), "full": (t, h)}[case["gate"]]
+    shape = {"none": None, "channel": (h,), "token": (t, 1), "full": (t, h)}[case["gate"]]
     s["gate"] = _normal(gen, shape, pt, 0.5) if shape else None
     for side in ("post", "pre"):
         s[side + "_weight"] = None if case[side] == "none" else (
@@ -276,9 +276,8 @@ def _plain_norm_of(s, side, v):
 
 
 def _gate_of(s):
-    """The gate in a shape that broadcasts over [tokens, hidden]."""
-    g = s["gate"]
-    return 1.0 if g is None else (g[:, None] if s["case"]["gate"] == "token" else g).float()
+    """The gate, in a shape that broadcasts over [tokens, hidden]."""
+    return 1.0 if s["gate"] is None else s["gate"].float()
 
 
 def _plain_block_norm(s):
@@ -309,7 +308,7 @@ def _plain_block_norm_grad(s):
     kind = s["case"]["gate"]
     if kind != "none":
         d_gate = g * _plain_norm_of(s, "post", y)
-        got["d_gate"] = (d_gate.sum(0) if kind == "channel" else d_gate.sum(1) if kind == "token"
+        got["d_gate"] = (d_gate.sum(0) if kind == "channel" else d_gate.sum(1, keepdim=True) if kind == "token"
                          else d_gate.to(s["gate"].dtype))
     got["d_y"] = _plain_norm_back(s, "post", y, g * _gate_of(s), got).to(dt)
     return got
@@ -458,7 +457,7 @@ def _exact_forward(s, p):
 
     n = norm("post", p["y"])
     if "gate" in p:
-        n = (p["gate"].unsqueeze(1) if c["gate"] == "token" else p["gate"]) * n
+        n = p["gate"] * n
     r = s["residual_scale"] * p["x"] + n
     return r, norm("pre", r)
 
