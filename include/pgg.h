@@ -653,6 +653,159 @@ int pgg_adapters_grad(const void* d_y, const void* x, const void* weight, const 
                       void* workspace, size_t workspace_bytes, void* d_x, void* d_a, void* d_b,
                       pgg_stream_t stream);
 
+/*
+ * ---------------------------------------------------------------------------
+ * Products with 4-bit expert weights (serving): the forward, the gated product
+ * and the down projection with the combination, with weights
+ *
+ *     w[g, n, k] = scale[g, n, k / groupSize] (code[g, n, k] - zero[g, n, k / groupSize])
+ *
+ *     PGG_W4_ROWS      out[i, n] = sum_k x[batch(i), k] w[g(i), n, k]          [M, N]
+ *     PGG_W4_GATED     out[i, f] = prob silu(gate) up, gate = column f, up = column N + f of
+ *                      the same product                                        [M, N]
+ *     PGG_W4_COMBINED  out[b, n] = sum over the rows i of token b of
+ *                      sum_k x[i, k] w[g(i), n, k], as pgg_dx_execute          [batch, N]
+ *
+ *   x        device, of `dtype`: [batch, K] in token order; combined: [M, K] in
+ *            expanded order
+ *   codes    device, uint8 [G, C, ceil(K / 2)], C = N (gated: 2 N): byte j of a
+ *            column holds code k = 2 j in its lower half and k = 2 j + 1 in its
+ *            upper (which is not used where K is odd and ends there)
+ *   scales   device, [G, C, ceil(K / groupSize)] of scale_dtype, `dtype` or PGG_F32
+ *   zeros    device, uint8 of the same shape (0 .. 255; codes are 0 .. 15), or NULL: 8
+ *   expandedRowIdx, groupList, M, G, L, batch, topK, rowIdxType: as for
+ *            pgg_dx_execute
+ *   probs    gated: device, fp32 [batch, topK], or NULL (1); else NULL
+ *   groupSize at least 1; the last group of a column may be shorter
+ *   out_dtype rows: `dtype` or PGG_F32; gated: `dtype`; combined: PGG_F32
+ *   workspace at least pgg_w4_workspace_size bytes, 256-byte aligned; status word
+ *            at offset 0. When the routing is not valid the output is zero-filled.
+ *
+ * The weights are not rounded: a group's sum of x (code - zero) is taken in fp32
+ * and then scaled (or each weight is formed in fp32), all sums are fp32, each
+ * output is rounded once. Bitwise repeatable.
+ */
+typedef enum { PGG_W4_ROWS = 0, PGG_W4_GATED = 1, PGG_W4_COMBINED = 2 } pgg_w4_product;
+
+int pgg_w4_workspace_size(pgg_w4_product product, int64_t M, int64_t N, int64_t K, int64_t G,
+                          int64_t L, int64_t batch, int64_t topK, int rowIdxType,
+                          int64_t groupSize, pgg_dtype dtype, size_t* workspace_bytes);
+
+int pgg_w4_execute(pgg_w4_product product, const void* x, const uint8_t* codes,
+                   const void* scales, const uint8_t* zeros, const int64_t* expandedRowIdx,
+                   const int64_t* groupList, const float* probs, int64_t M, int64_t N, int64_t K,
+                   int64_t G, int64_t L, int64_t batch, int64_t topK, int rowIdxType,
+                   int64_t groupSize, pgg_dtype dtype, pgg_dtype scale_dtype, pgg_dtype out_dtype,
+                   void* workspace, size_t workspace_bytes, void* out, pgg_stream_t stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * The norms before and after a block, with its gate and residual scale, in one
+ * pass: what stands between the block's output y and the next block's input h.
+ *
+ *     n = N_post(y),  r = residual_scale x + gate n,  h = N_pre(r)
+ *     N(v) = (v - mean) / sqrt(var + eps) (weight_offset + weight) + bias    PGG_NORM_LAYER
+ *     N(v) = v / sqrt(mean of v^2 + eps) (weight_offset + weight)            PGG_NORM_RMS
+ *     N(v) = v                                                               PGG_NORM_NONE
+ *
+ *   x        device, [T, H] of `dtype`: the residual stream before the block
+ *   y        device, [T, H] of y_dtype, `dtype` or PGG_F32 (what pgg_dx_execute
+ *            leaves), or NULL: r = residual_scale x (then post and gate_kind are none)
+ *   gate     device, of param_dtype, as gate_kind says; NULL for PGG_GATE_NONE
+ *   post_weight, post_bias, pre_weight, pre_bias
+ *            device, [H] of param_dtype, each may be NULL (the factor is then 1, the
+ *            bias 0); none without a norm, no bias with PGG_NORM_RMS: PGG_ERR_ATTR
+ *   param_dtype `dtype` or PGG_F32
+ *   r, h     device, [T, H] of `dtype`; r may be NULL, h is NULL exactly if pre is
+ *            PGG_NORM_NONE, one of them is written
+ *
+ * All in fp32, the pre norm on r before r is rounded. No device-detected errors.
+ * r may be x; another overlap of outputs and inputs is not allowed.
+ */
+typedef enum { PGG_NORM_NONE = 0, PGG_NORM_RMS = 1, PGG_NORM_LAYER = 2 } pgg_norm;
+
+/* Shape of the gate: [H], [T] or [T, H]. */
+typedef enum {
+  PGG_GATE_NONE = 0,
+  PGG_GATE_CHANNEL = 1,
+  PGG_GATE_TOKEN = 2,
+  PGG_GATE_FULL = 3
+} pgg_gate;
+
+int pgg_block_norm(const void* x, const void* y, const void* gate, const void* post_weight,
+                   const void* post_bias, const void* pre_weight, const void* pre_bias, int64_t T,
+                   int64_t H, pgg_dtype dtype, pgg_dtype y_dtype, pgg_dtype param_dtype,
+                   pgg_norm post, pgg_norm pre, pgg_gate gate_kind, float residual_scale,
+                   float weight_offset, float eps, void* r, void* h, pgg_stream_t stream);
+
+/*
+ * Its gradient, from d_r (the gradient of r by its later uses) and d_h, the kept
+ * r and y:
+ *
+ *     g = d_r + N_pre'(d_h at r),  d_x = residual_scale g
+ *     d_gate = g n, summed over what the gate was broadcast over
+ *     d_y = N_post'(g gate at y), and the sums over rows for weights and biases
+ *
+ *   d_r      device, [T, H] of `dtype`, or NULL (0); d_h: [T, H] of dh_dtype,
+ *            `dtype` or PGG_F32; NULL exactly if pre is PGG_NORM_NONE
+ *   r        device, [T, H] of `dtype`, NULL exactly if pre is PGG_NORM_NONE
+ *   d_x      device, [T, H] of `dtype`;  d_y the same, NULL exactly if y is
+ *   d_gate   fp32 [H] or [T]; for PGG_GATE_FULL [T, H] of param_dtype; NULL
+ *            exactly if gate is
+ *   d_post_weight, d_post_bias, d_pre_weight, d_pre_bias
+ *            device, fp32 [H], each may be NULL; not without its parameter
+ *   workspace at least pgg_block_norm_grad_workspace_size bytes, 256-byte aligned;
+ *            the status word at offset 0 is 0 after the call
+ *
+ * Sums over rows are fp32, in an order that depends on the sizes alone. d_x may
+ * be d_r; another overlap of outputs and inputs is not allowed.
+ */
+int pgg_block_norm_grad_workspace_size(int64_t T, int64_t H, size_t* workspace_bytes);
+
+int pgg_block_norm_grad(const void* d_r, const void* d_h, const void* r, const void* y,
+                        const void* gate, const void* post_weight, const void* post_bias,
+                        const void* pre_weight, const void* pre_bias, int64_t T, int64_t H,
+                        pgg_dtype dtype, pgg_dtype y_dtype, pgg_dtype dh_dtype,
+                        pgg_dtype param_dtype, pgg_norm post, pgg_norm pre, pgg_gate gate_kind,
+                        float residual_scale, float weight_offset, float eps, void* workspace,
+                        size_t workspace_bytes, void* d_x, void* d_y, void* d_gate,
+                        float* d_post_weight, float* d_post_bias, float* d_pre_weight,
+                        float* d_pre_bias, pgg_stream_t stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * The global norm of a list of gradients, and the gradients clipped to it:
+ *
+ *     norm = |scale| sqrt(sum over all tensors of g^2)
+ *     out  = g c,  c = scale min(1, max_norm / (norm + eps))
+ *
+ *   count    number of tensors, 0 or more
+ *   grads    host array of count device pointers (NULL where a size is 0)
+ *   sizes    host array: elements of each, 0 or more;  dtypes: host array
+ *   scale    multiplies every gradient (1 / the loss scale, 1 / accumulated steps)
+ *   max_norm 0 or more (may be infinite); eps 0 or more
+ *   norm     device, fp32
+ *   out      host array of device pointers; out[i] has the dtype of grads[i], is
+ *            grads[i] itself or overlaps no gradient
+ *   workspace at least pgg_clip_workspace_size bytes, 256-byte aligned; the status
+ *            word at offset 0 is 0 after the call
+ *
+ * The host arrays are read during the call only. A norm that is not finite clips
+ * nothing: c = scale, and the caller sees it in `norm`. Where c is 1 a gradient
+ * that is its own output is not written. Squares are summed in fp32 and fp64;
+ * neither their sum nor a small gradient's square leaves the range.
+ */
+int pgg_clip_workspace_size(int64_t count, size_t* workspace_bytes);
+
+int pgg_grad_norm(int64_t count, const void* const* grads, const int64_t* sizes,
+                  const pgg_dtype* dtypes, float scale, void* workspace, size_t workspace_bytes,
+                  float* norm, pgg_stream_t stream);
+
+int pgg_clip_grads(int64_t count, const void* const* grads, const int64_t* sizes,
+                   const pgg_dtype* dtypes, float max_norm, float eps, float scale,
+                   void* workspace, size_t workspace_bytes, float* norm, void* const* out,
+                   pgg_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

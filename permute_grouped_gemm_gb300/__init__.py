@@ -11,6 +11,10 @@ from __future__ import annotations
 
 from ._lib import (  # noqa: F401
     CODES, PGG_BF16, PGG_BIAS_ON_SCORE, PGG_F16, PGG_F32, PGG_SCORE_SIGMOID, PGG_SCORE_SOFTMAX, STATUS, PggError,
+    PGG_GATE_CHANNEL, PGG_GATE_FULL, PGG_GATE_NONE, PGG_GATE_TOKEN, PGG_NORM_LAYER, PGG_NORM_NONE,
+    PGG_NORM_RMS, PGG_W4_COMBINED, PGG_W4_GATED, PGG_W4_ROWS, pgg_block_norm, pgg_block_norm_grad,
+    pgg_block_norm_grad_workspace_size, pgg_clip_grads, pgg_clip_workspace_size, pgg_grad_norm,
+    pgg_w4_execute, pgg_w4_workspace_size,
     load, pgg_adapters_execute, pgg_adapters_grad, pgg_adapters_grad_workspace_size,
     pgg_adapters_plan, pgg_adapters_workspace_size, pgg_route_execute, pgg_route_grad, pgg_route_workspace_size,
     pgg_swiglu_execute, pgg_swiglu_grad, pgg_swiglu_grad_workspace_size,
@@ -453,6 +457,267 @@ def adapters_grad(d_y, x, weight, a, b, adapter, scale=None, need_x: bool = True
     if rc != 0:
         raise PggError(rc, "pgg_adapters_grad")
     return (d_x if need_x else None), d_a, d_b, workspace
+
+
+def _w4(where, product, x, codes, scales, expanded_row_idx, group_list, batch, top_k, row_idx_type,
+        group, zeros, probs, out_dtype, out, workspace, stream):
+    """One of the products with 4-bit weights: (out, workspace)."""
+    import torch
+    _dense(x, codes, scales, expanded_row_idx, group_list, zeros, probs, out, workspace)
+    if expanded_row_idx.dtype != torch.int64 or group_list.dtype != torch.int64:
+        raise ValueError("expandedRowIdx and groupList must be int64")
+    if codes.dtype != torch.uint8:
+        raise ValueError("codes must be uint8")
+    if group <= 0:
+        raise PggError(CODES["PGG_ERR_ATTR"], where)
+    G, C, row_bytes = codes.shape
+    rows, K = x.shape
+    M, dev = expanded_row_idx.shape[0], x.device
+    combined, gated = product == PGG_W4_COMBINED, product == PGG_W4_GATED
+    if rows != (M if combined else batch) or group_list.shape != (G,) or (gated and C % 2) \
+            or row_bytes != (K + 1) // 2:
+        raise PggError(CODES["PGG_ERR_SHAPE"], where)
+    if scales.dtype not in (x.dtype, torch.float32):
+        raise PggError(CODES["PGG_ERR_DTYPE"], where)
+    N = C // 2 if gated else C
+    shape = (G, C, (K + group - 1) // group)
+    _is("scales", scales, shape, scales.dtype)
+    _is("zeros", zeros, shape, torch.uint8)
+    _is("probs", probs, (batch, top_k), torch.float32)
+    out_shape = (batch if combined else M, N)
+    _is("out", out, out_shape, out_dtype)
+    dt = dtype_code(x.dtype)
+    if workspace is None:
+        need = pgg_w4_workspace_size(product, M, N, K, G, M, batch, top_k, row_idx_type, group, dt)
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    if out is None:
+        out = torch.empty(out_shape, dtype=out_dtype, device=dev)
+    stream = _stream_of(stream, dev)
+    rc = pgg_w4_execute(product, x.data_ptr(), codes.data_ptr(), scales.data_ptr(),
+                        zeros.data_ptr() if zeros is not None else 0, expanded_row_idx.data_ptr(),
+                        group_list.data_ptr(), probs.data_ptr() if probs is not None else 0, M, N,
+                        K, G, M, batch, top_k, row_idx_type, group, dt, dtype_code(scales.dtype),
+                        dtype_code(out_dtype), workspace.data_ptr(),
+                        workspace.numel() * workspace.element_size(), out.data_ptr(), stream)
+    if rc != 0:
+        raise PggError(rc, "pgg_w4_execute")
+    return out, workspace
+
+
+def fwd_w4(x, codes, scales, expanded_row_idx, group_list, batch: int, top_k: int,
+           row_idx_type: int, group: int = 128, zeros=None, out_dtype=None, out=None,
+           workspace=None, stream=None):
+    """Forward with 4-bit expert weights: (y [M, N] in expanded order, workspace).
+
+    y[i] = sum_k x[token, k] w[expert, :, k], w = scale (code - zero), for x [batch, K], codes
+    uint8 [G, N, ceil(K / 2)] (two codes a byte along K, the lower half first), scales
+    [G, N, ceil(K / group)] (x's dtype or fp32) and zeros uint8 of the same shape (8 when None).
+    ``out_dtype``: x's dtype by default, or torch.float32.
+    """
+    return _w4("fwd_w4", PGG_W4_ROWS, x, codes, scales, expanded_row_idx, group_list, batch, top_k,
+               row_idx_type, group, zeros, None, x.dtype if out_dtype is None else out_dtype, out,
+               workspace, stream)
+
+
+def swiglu_w4(x, codes, scales, expanded_row_idx, group_list, batch: int, top_k: int,
+              row_idx_type: int, group: int = 128, zeros=None, probs=None, out=None,
+              workspace=None, stream=None):
+    """``swiglu`` with 4-bit expert weights: (h [M, F], workspace). codes [G, 2F, ceil(K / 2)]
+    hold F gate columns, then F up columns; scales and zeros as for ``fwd_w4``."""
+    return _w4("swiglu_w4", PGG_W4_GATED, x, codes, scales, expanded_row_idx, group_list, batch,
+               top_k, row_idx_type, group, zeros, probs, x.dtype, out, workspace, stream)
+
+
+def down_w4(h, codes, scales, expanded_row_idx, group_list, batch: int, top_k: int,
+            row_idx_type: int, group: int = 128, zeros=None, out=None, workspace=None,
+            stream=None):
+    """Down projection with 4-bit expert weights, summed over each token's experts:
+    (out [batch, N] fp32, workspace), for h [M, K] in expanded order and codes
+    [G, N, ceil(K / 2)]; what ``dx`` computes with 16-bit weights [G, N, K]."""
+    import torch
+    return _w4("down_w4", PGG_W4_COMBINED, h, codes, scales, expanded_row_idx, group_list, batch,
+               top_k, row_idx_type, group, zeros, None, torch.float32, out, workspace, stream)
+
+
+_NORMS = {None: PGG_NORM_NONE, "rms": PGG_NORM_RMS, "layer": PGG_NORM_LAYER}
+
+
+def _ptr(t) -> int:
+    return t.data_ptr() if t is not None else 0
+
+
+def _norm_setup(where, T, H, dtype, y, gate, post, post_weight, post_bias, pre, pre_weight,
+                pre_bias):
+    """Codes (y_dtype, param_dtype, post, pre, gate_kind) of a norm call whose tensors agree."""
+    if post not in _NORMS or pre not in _NORMS:
+        raise ValueError("post and pre must be None, 'rms' or 'layer'")
+    params = {"post_weight": post_weight, "post_bias": post_bias, "pre_weight": pre_weight,
+              "pre_bias": pre_bias}
+    given = [t for t in (gate, *params.values()) if t is not None]
+    pdt = given[0].dtype if given else dtype
+    code = dtype_code(dtype)
+    if dtype_code(pdt) not in (code, PGG_F32):
+        raise PggError(CODES["PGG_ERR_DTYPE"], where)
+    for name, t in params.items():
+        _is(name, t, (H,), pdt)
+    kind = PGG_GATE_NONE
+    if gate is not None:
+        shape = tuple(gate.shape)
+        if shape == (T, H):
+            kind = PGG_GATE_FULL
+        elif shape == (T, 1):
+            kind = PGG_GATE_TOKEN
+        elif shape == (H,):
+            kind = PGG_GATE_CHANNEL
+        else:
+            raise ValueError(f"gate must be [{H}], [{T}, 1] or [{T}, {H}], got {list(shape)}")
+        _is("gate", gate, shape, pdt)
+    ydt = code
+    if y is not None:
+        ydt = dtype_code(y.dtype)
+        if y.shape != (T, H):
+            raise PggError(CODES["PGG_ERR_SHAPE"], where)
+        if ydt not in (code, PGG_F32):
+            raise PggError(CODES["PGG_ERR_DTYPE"], where)
+    return ydt, dtype_code(pdt), _NORMS[post], _NORMS[pre], kind
+
+
+def block_norm(x, y=None, gate=None, post=None, post_weight=None, post_bias=None, pre="rms",
+               pre_weight=None, pre_bias=None, residual_scale: float = 1.0,
+               weight_offset: float = 0.0, eps: float = 1e-6, r=None, h=None, stream=None):
+    """What stands between two blocks, in one pass: (r [T, H], h [T, H] or None without ``pre``).
+
+        r = residual_scale x + gate N_post(y),  h = N_pre(r)
+
+    x [T, H]: the residual stream; y [T, H] (x's dtype or fp32): the block's output, or None.
+    ``post`` and ``pre`` are None, "rms" or "layer"; a norm's factor is weight_offset + weight (1
+    without a weight), a layer norm may have a bias. gate: [H], [T, 1] or [T, H]. All parameters
+    and the gate are of one dtype, x's or fp32. h is taken from r before r is rounded. ``r`` may
+    be ``x``.
+    """
+    import torch
+    _dense(x, y, gate, post_weight, post_bias, pre_weight, pre_bias, r, h)
+    T, H = x.shape
+    codes = _norm_setup("block_norm", T, H, x.dtype, y, gate, post, post_weight, post_bias, pre,
+                        pre_weight, pre_bias)
+    _is("r", r, (T, H), x.dtype)
+    _is("h", h, (T, H), x.dtype)
+    if r is None:
+        r = torch.empty_like(x)
+    if pre is not None and h is None:
+        h = torch.empty_like(x)
+    rc = pgg_block_norm(x.data_ptr(), _ptr(y), _ptr(gate), _ptr(post_weight), _ptr(post_bias),
+                        _ptr(pre_weight), _ptr(pre_bias), T, H, dtype_code(x.dtype), *codes,
+                        residual_scale, weight_offset, eps, r.data_ptr(), _ptr(h),
+                        _stream_of(stream, x.device))
+    if rc != 0:
+        raise PggError(rc, "pgg_block_norm")
+    return r, h
+
+
+def block_norm_grad(d_r, d_h, r, y=None, gate=None, post=None, post_weight=None, post_bias=None,
+                    pre="rms", pre_weight=None, pre_bias=None, residual_scale: float = 1.0,
+                    weight_offset: float = 0.0, eps: float = 1e-6, d_x=None, d_y=None,
+                    workspace=None, stream=None):
+    """Gradients of ``block_norm`` from d_r (r's later uses; None: 0) and d_h (r's dtype or fp32),
+    the r that it returned and its y: (a dict, workspace). The dict holds d_x, d_y [T, H] in r's
+    dtype, d_gate (the gate's shape; fp32, a [T, H] gate's in its dtype) and fp32 d_post_weight,
+    d_post_bias, d_pre_weight, d_pre_bias [H], None for what is not there. ``d_x`` may be ``d_r``.
+    Without ``pre``, d_h is None and r is not read.
+    """
+    import torch
+    base = r if r is not None else d_r
+    if base is None:
+        raise PggError(CODES["PGG_ERR_NULL"], "block_norm_grad")
+    _dense(base, d_r, d_h, y, gate, post_weight, post_bias, pre_weight, pre_bias, d_x, d_y,
+           workspace)
+    T, H = base.shape
+    dtype, dev = base.dtype, base.device
+    ydt, pdt, post_code, pre_code, kind = _norm_setup(
+        "block_norm_grad", T, H, dtype, y, gate, post, post_weight, post_bias, pre, pre_weight,
+        pre_bias)
+    _is("d_r", d_r, (T, H), dtype)
+    for name, t in (("d_x", d_x), ("d_y", d_y)):
+        _is(name, t, (T, H), dtype)
+    dhdt = dtype_code(dtype)
+    if d_h is not None:
+        dhdt = dtype_code(d_h.dtype)
+        _is("d_h", d_h, (T, H), d_h.dtype)
+    if d_x is None:
+        d_x = torch.empty_like(base)
+    if y is not None and d_y is None:
+        d_y = torch.empty(T, H, dtype=dtype, device=dev)
+    d_gate = None if gate is None else torch.empty(
+        gate.shape, dtype=gate.dtype if kind == PGG_GATE_FULL else torch.float32, device=dev)
+    d_params = [None if p is None else torch.empty(H, dtype=torch.float32, device=dev)
+                for p in (post_weight, post_bias, pre_weight, pre_bias)]
+    if workspace is None:
+        workspace = torch.empty(pgg_block_norm_grad_workspace_size(T, H), dtype=torch.uint8,
+                                device=dev)
+    rc = pgg_block_norm_grad(
+        _ptr(d_r), _ptr(d_h), _ptr(r) if pre is not None else 0, _ptr(y), _ptr(gate),
+        _ptr(post_weight), _ptr(post_bias), _ptr(pre_weight), _ptr(pre_bias), T, H,
+        dtype_code(dtype), ydt, dhdt, pdt, post_code, pre_code, kind, residual_scale,
+        weight_offset, eps, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+        d_x.data_ptr(), _ptr(d_y), _ptr(d_gate), *(_ptr(p) for p in d_params),
+        _stream_of(stream, dev))
+    if rc != 0:
+        raise PggError(rc, "pgg_block_norm_grad")
+    names = ("d_post_weight", "d_post_bias", "d_pre_weight", "d_pre_bias")
+    return dict(zip(names, d_params), d_x=d_x, d_y=d_y, d_gate=d_gate), workspace
+
+
+def _grad_list(grads, workspace, norm):
+    """(addresses, sizes, dtype codes, device, workspace, norm) of a list of gradients."""
+    import torch
+    if not grads and workspace is None and norm is None:
+        raise ValueError("an empty list needs a workspace or norm to tell the device")
+    dev = (grads[0] if grads else workspace if workspace is not None else norm).device
+    _dense(*(t for t in (*grads, workspace, norm) if t is not None))
+    _is("norm", norm, (), torch.float32)
+    if workspace is None:
+        workspace = torch.empty(pgg_clip_workspace_size(len(grads)), dtype=torch.uint8, device=dev)
+    if norm is None:
+        norm = torch.empty((), dtype=torch.float32, device=dev)
+    return ([t.data_ptr() for t in grads], [t.numel() for t in grads],
+            [dtype_code(t.dtype) for t in grads], dev, workspace, norm)
+
+
+def grad_norm(grads, scale: float = 1.0, norm=None, workspace=None, stream=None):
+    """(norm, workspace): the fp32 scalar |scale| sqrt(sum of all squares) over the tensors."""
+    ptrs, sizes, dtypes, dev, workspace, norm = _grad_list(grads, workspace, norm)
+    rc = pgg_grad_norm(ptrs, sizes, dtypes, scale, workspace.data_ptr(),
+                       workspace.numel() * workspace.element_size(), norm.data_ptr(),
+                       _stream_of(stream, dev))
+    if rc != 0:
+        raise PggError(rc, "pgg_grad_norm")
+    return norm, workspace
+
+
+def clip_grads(grads, max_norm: float, eps: float = 1e-6, scale: float = 1.0, out=None, norm=None,
+               workspace=None, stream=None):
+    """Clips gradients by their global norm: (norm, out, workspace).
+
+    norm = |scale| sqrt(sum of all squares); out[i] = grads[i] scale min(1, max_norm / (norm +
+    eps)), in place when ``out`` (a list of like tensors) is None. A norm that is not finite clips
+    nothing (out = grads scale): look at it before the step.
+    """
+    out = grads if out is None else out
+    ptrs, sizes, dtypes, dev, workspace, norm = _grad_list(grads, workspace, norm)
+    if out is not grads:
+        if len(out) != len(grads):
+            raise PggError(CODES["PGG_ERR_SHAPE"], "clip_grads")
+        if grads:
+            _dense(grads[0], *out)
+        for g, o in zip(grads, out):
+            _is("out", o, g.shape, g.dtype)
+    rc = pgg_clip_grads(ptrs, sizes, dtypes, max_norm, eps, scale, workspace.data_ptr(),
+                        workspace.numel() * workspace.element_size(), norm.data_ptr(),
+                        ptrs if out is grads else [t.data_ptr() for t in out],
+                        _stream_of(stream, dev))
+    if rc != 0:
+        raise PggError(rc, "pgg_clip_grads")
+    return norm, out, workspace
 
 
 def status(workspace) -> int:

@@ -14,6 +14,9 @@ from . import build as _build
 
 PGG_F32, PGG_F16, PGG_BF16 = 0, 1, 2
 PGG_SCORE_SOFTMAX, PGG_SCORE_SIGMOID, PGG_BIAS_ON_SCORE = 0, 1, 16
+PGG_W4_ROWS, PGG_W4_GATED, PGG_W4_COMBINED = 0, 1, 2
+PGG_NORM_NONE, PGG_NORM_RMS, PGG_NORM_LAYER = 0, 1, 2
+PGG_GATE_NONE, PGG_GATE_CHANNEL, PGG_GATE_TOKEN, PGG_GATE_FULL = 0, 1, 2, 3
 
 STATUS = {
     0: "PGG_OK", 1: "PGG_ERR_NULL", 2: "PGG_ERR_SHAPE", 3: "PGG_ERR_ATTR", 4: "PGG_ERR_DTYPE",
@@ -119,6 +122,20 @@ def load(path: str | None = None):
                       "pgg_swiglu_grad_workspace_size", "pgg_swiglu_grad",
                       "pgg_adapters_workspace_size", "pgg_adapters_plan", "pgg_adapters_execute",
                       "pgg_adapters_grad_workspace_size", "pgg_adapters_grad"):
+                getattr(lib, f).restype = ctypes.c_int
+            lib.pgg_w4_workspace_size.argtypes = [i32, *_SIZES, i32, i64, i32, ctypes.POINTER(sz)]
+            lib.pgg_w4_execute.argtypes = [i32] + [vp] * 7 + [*_SIZES, i32, i64, i32, i32, i32, vp,
+                                                              sz, vp, vp]
+            lib.pgg_block_norm.argtypes = [vp] * 7 + [i64] * 2 + [i32] * 6 + [f32] * 3 + [vp] * 3
+            lib.pgg_block_norm_grad_workspace_size.argtypes = [i64] * 2 + [ctypes.POINTER(sz)]
+            lib.pgg_block_norm_grad.argtypes = [vp] * 9 + [i64] * 2 + [i32] * 7 + [f32] * 3 + [
+                vp, sz] + [vp] * 8
+            lib.pgg_clip_workspace_size.argtypes = [i64, ctypes.POINTER(sz)]
+            lib.pgg_grad_norm.argtypes = [i64, vp, vp, vp, f32, vp, sz, vp, vp]
+            lib.pgg_clip_grads.argtypes = [i64, vp, vp, vp, f32, f32, f32, vp, sz, vp, vp, vp]
+            for f in ("pgg_w4_workspace_size", "pgg_w4_execute", "pgg_block_norm",
+                      "pgg_block_norm_grad_workspace_size", "pgg_block_norm_grad",
+                      "pgg_clip_workspace_size", "pgg_grad_norm", "pgg_clip_grads"):
                 getattr(lib, f).restype = ctypes.c_int
             lib.pgg_status_string.argtypes = [ctypes.c_int]
             lib.pgg_status_string.restype = ctypes.c_char_p
@@ -394,6 +411,85 @@ def pgg_adapters_grad(d_y, x, weight, a, b, adapter, scale, T, K, N, R, A, dtype
     return load().pgg_adapters_grad(d_y, x, weight, a, b, adapter, scale or None, T, K, N, R, A,
                                     dtype, workspace, workspace_bytes, d_x or None, d_a, d_b,
                                     stream)
+
+
+@_by_sizes
+def pgg_w4_workspace_size(product, M, N, K, G, L, batch, topK, rowIdxType, groupSize,
+                          dtype) -> int:
+    out = ctypes.c_size_t(0)
+    _check(load().pgg_w4_workspace_size(product, M, N, K, G, L, batch, topK, rowIdxType, groupSize,
+                                        dtype, ctypes.byref(out)), "pgg_w4_workspace_size")
+    return out.value
+
+
+def pgg_w4_execute(product, x, codes, scales, zeros, expandedRowIdx, groupList, probs, M, N, K, G,
+                   L, batch, topK, rowIdxType, groupSize, dtype, scale_dtype, out_dtype, workspace,
+                   workspace_bytes, out, stream) -> int:
+    """Raw call with integer device addresses (0 for absent zeros or probs)."""
+    return load().pgg_w4_execute(product, x, codes, scales, zeros or None, expandedRowIdx,
+                                 groupList, probs or None, M, N, K, G, L, batch, topK, rowIdxType,
+                                 groupSize, dtype, scale_dtype, out_dtype, workspace,
+                                 workspace_bytes, out, stream)
+
+
+def pgg_block_norm(x, y, gate, post_weight, post_bias, pre_weight, pre_bias, T, H, dtype, y_dtype,
+                   param_dtype, post, pre, gate_kind, residual_scale, weight_offset, eps, r, h,
+                   stream) -> int:
+    """Raw call with integer device addresses (0 for absent tensors)."""
+    return load().pgg_block_norm(x, y or None, gate or None, post_weight or None,
+                                 post_bias or None, pre_weight or None, pre_bias or None, T, H,
+                                 dtype, y_dtype, param_dtype, post, pre, gate_kind,
+                                 residual_scale, weight_offset, eps, r or None, h or None, stream)
+
+
+@_by_sizes
+def pgg_block_norm_grad_workspace_size(T, H) -> int:
+    out = ctypes.c_size_t(0)
+    _check(load().pgg_block_norm_grad_workspace_size(T, H, ctypes.byref(out)),
+           "pgg_block_norm_grad_workspace_size")
+    return out.value
+
+
+def pgg_block_norm_grad(d_r, d_h, r, y, gate, post_weight, post_bias, pre_weight, pre_bias, T, H,
+                        dtype, y_dtype, dh_dtype, param_dtype, post, pre, gate_kind,
+                        residual_scale, weight_offset, eps, workspace, workspace_bytes, d_x, d_y,
+                        d_gate, d_post_weight, d_post_bias, d_pre_weight, d_pre_bias,
+                        stream) -> int:
+    """Raw call with integer device addresses (0 for absent tensors)."""
+    return load().pgg_block_norm_grad(
+        d_r or None, d_h or None, r or None, y or None, gate or None, post_weight or None,
+        post_bias or None, pre_weight or None, pre_bias or None, T, H, dtype, y_dtype, dh_dtype,
+        param_dtype, post, pre, gate_kind, residual_scale, weight_offset, eps, workspace,
+        workspace_bytes, d_x, d_y or None, d_gate or None, d_post_weight or None,
+        d_post_bias or None, d_pre_weight or None, d_pre_bias or None, stream)
+
+
+@_by_sizes
+def pgg_clip_workspace_size(count) -> int:
+    out = ctypes.c_size_t(0)
+    _check(load().pgg_clip_workspace_size(count, ctypes.byref(out)), "pgg_clip_workspace_size")
+    return out.value
+
+
+def _tensor_list(grads, sizes, dtypes, out=()):
+    n = len(grads)
+    return ((ctypes.c_void_p * n)(*grads), (ctypes.c_int64 * n)(*sizes),
+            (ctypes.c_int * n)(*dtypes), (ctypes.c_void_p * n)(*out))
+
+
+def pgg_grad_norm(grads, sizes, dtypes, scale, workspace, workspace_bytes, norm, stream) -> int:
+    """Raw call with sequences of integer device addresses, sizes and dtype codes."""
+    g, n, d, _ = _tensor_list(grads, sizes, dtypes)
+    return load().pgg_grad_norm(len(grads), g, n, d, scale, workspace, workspace_bytes, norm,
+                                stream)
+
+
+def pgg_clip_grads(grads, sizes, dtypes, max_norm, eps, scale, workspace, workspace_bytes, norm,
+                   out, stream) -> int:
+    """Raw call with sequences of integer device addresses, sizes and dtype codes."""
+    g, n, d, o = _tensor_list(grads, sizes, dtypes, out)
+    return load().pgg_clip_grads(len(grads), g, n, d, max_norm, eps, scale, workspace,
+                                 workspace_bytes, norm, o, stream)
 
 
 def pgg_status_string(code: int) -> str:

@@ -1,6 +1,6 @@
 """Builds libpgg.so (the C-ABI library) in-tree with nvcc for sm_103a.
 
-Twenty translation units compiled in parallel, then linked as a shared
+The translation units are compiled in parallel, then linked as a shared
 library with the CUDA runtime linked statically; the driver API is reached at
 run time through cudaGetDriverEntryPointByVersion, so loading the library
 needs no libcuda.
@@ -32,7 +32,8 @@ SOURCES = ["pgg_api.cu", "route_prep.cu", "gmm_dx.cu", "gmm_dx_simt.cu", "gmm_dw
            "gmm_dx_owner.cu", "ops_api.cu", "router.cu", "router_scores.cu", "ops_prep.cu",
            "ops_simt.cu",
            "gated_grad.cu", "rows_wide.cu",
-           "rows_skinny.cu", "adapters_few.cu", "rows_outer.cu"]
+           "rows_skinny.cu", "adapters_few.cu", "rows_outer.cu", "block_api.cu", "w4_simt.cu",
+           "block_norm.cu", "grad_clip.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

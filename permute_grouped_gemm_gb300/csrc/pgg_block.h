@@ -1,0 +1,93 @@
+// Internal definitions of what surrounds the experts' products in a block:
+// products with 4-bit weights, the norms before and after the block, and the
+// gradients' global norm.
+#pragma once
+
+#include "pgg_ops.h"
+
+namespace pgg {
+
+// ------------------------------------------------------------ 4-bit experts
+
+struct W4Args {
+  const void* x;         // [batch, K] by token, or (combined) [M, K] in expanded order
+  const uint8_t* codes;  // [G, C, ceil(K / 2)], C = N, gated: 2 N columns
+  const void* scales;    // [G, C, groups]
+  const uint8_t* zeros;  // [G, C, groups] or null (8)
+  const float* probs;    // gated: [M] weight of each original position, or null
+  const int4* rblist;    // {expert, first row, rows, 0}
+  const RowInfo* rowinfo;  // {token, original position}
+  WsHeader* hdr;
+  void* out;             // [M, N], expanded order; combined: fp32 [M, N] by original position
+  int64_t M, N, K, G, batch, max_row_blocks;
+  int64_t row_bytes;     // ceil(K / 2)
+  int32_t group, groups;  // codes of a scale, scales of a row
+  int32_t product;       // pgg_w4_product
+  int32_t scale_f32;     // scales are fp32 (else the dtype)
+  int32_t out_f32;       // out is fp32 (else the dtype)
+};
+
+cudaError_t launch_w4_simt(int dtype, const W4Args& a, int num_sms, cudaStream_t stream);
+// out[b] = sum over j of rows[b * top_k + j] in fp32, zeros when the status word is set.
+cudaError_t launch_w4_combine(const float* rows, const WsHeader* hdr, int64_t batch, int64_t top_k,
+                              int64_t N, float* out, int num_sms, cudaStream_t stream);
+
+// ------------------------------------------------------------ norms around a block
+
+struct NormArgs {
+  const void* x;     // [T, H]; backward: r, the forward's output, or null without a pre norm
+  const void* y;     // [T, H] or null
+  const void* gate;  // as gate_kind says
+  const void* w_post;
+  const void* b_post;
+  const void* w_pre;
+  const void* b_pre;
+  void* r;           // forward: [T, H] or null;  backward: d_x
+  void* h;           // forward: [T, H] or null;  backward: d_y or null
+  // backward
+  const void* d_r;   // [T, H] or null
+  const void* d_h;   // [T, H] or null
+  void* d_gate;      // full: [T, H] of the parameters' dtype; token: fp32 [T]; channel: fp32 [H]
+  float* d_cols[5];  // fp32 [H] or null: gate (channel), w_post, b_post, w_pre, b_pre
+  float* partial;    // [blocks][5][H]
+  WsHeader* hdr;
+  int64_t T, H;
+  int32_t post, pre;       // pgg_norm
+  int32_t gate_kind;       // pgg_gate
+  int32_t y_f32, p_f32, dh_f32;  // fp32 (else the dtype)
+  float residual_scale, weight_offset, eps;
+};
+
+// Blocks whose column sums the backward keeps apart.
+int64_t norm_grad_blocks(int64_t T);
+cudaError_t launch_block_norm(int dtype, const NormArgs& a, bool rows16, int num_sms,
+                              cudaStream_t stream);
+cudaError_t launch_block_norm_grad(int dtype, const NormArgs& a, bool rows16, int num_sms,
+                                   cudaStream_t stream);
+
+// ------------------------------------------------------------ the gradients' norm
+
+constexpr int kClipTensors = 512;    // tensors of one launch
+constexpr int kClipBlocks = 1024;    // most blocks, and partial sums, of one
+
+struct ClipTable {
+  const void* in[kClipTensors];
+  void* out[kClipTensors];
+  int64_t n[kClipTensors];
+  uint32_t first[kClipTensors + 1];  // first chunk of each; behind the last, all chunks
+  uint8_t dtype[kClipTensors];
+  int32_t tensors;
+};
+
+// One partial sum of squares a block into partial[0, blocks).
+int64_t clip_chunks(int64_t n);  // chunks of a tensor of n elements
+cudaError_t launch_clip_squares(const ClipTable& t, WsHeader* hdr, double* partial, int blocks,
+                                cudaStream_t stream);
+// norm = |scale| sqrt(sum of partial), in fp32.
+cudaError_t launch_clip_norm(const double* partial, int64_t count, float scale, float* norm,
+                             cudaStream_t stream);
+// out = in * c, c = scale min(1, max_norm / (norm + eps)) (scale alone if norm is not finite).
+cudaError_t launch_clip_apply(const ClipTable& t, const float* norm, float max_norm, float eps,
+                              float scale, int blocks, cudaStream_t stream);
+
+}  // namespace pgg
