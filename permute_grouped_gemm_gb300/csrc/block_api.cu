@@ -2,6 +2,7 @@
 // (include/pgg.h): argument validation, workspace layouts, the choice of kernel
 // and the launches.
 
+#include <cmath>
 #include <cstdint>
 #include <cstring>
 
@@ -24,11 +25,14 @@ int status_of(cudaError_t e) { return e == cudaSuccess ? PGG_OK : PGG_ERR_CUDA; 
 // ---------------------------------------------------------------- 4-bit experts
 
 constexpr int kSimtRows = 32;
+constexpr int kVariantStream = 1;  // tensor cores, the codes streamed for blocks of 8 to 32 rows
+constexpr int kVariantSimt = 3;    // FP32 pipes: any dtype, size and alignment
 
 struct W4Plan {
+  int variant;
   int rows_per_block;
   int64_t max_row_blocks;
-  size_t rblist, rowinfo, inv, rows, total;
+  size_t rblist, rowinfo, inv, rows, parts, arrived, total;
 };
 
 int w4_plan(int product, int64_t M, int64_t N, int64_t K, int64_t G, int64_t L, int64_t batch,
@@ -43,7 +47,18 @@ int w4_plan(int product, int64_t M, int64_t N, int64_t K, int64_t G, int64_t L, 
       groupSize > kInt32Max)
     return PGG_ERR_SHAPE;
   if (L != M || batch > M || topK > M || batch * topK != M) return PGG_ERR_SHAPE;
+  p->variant = kVariantSimt;
   p->rows_per_block = kSimtRows;
+  if (dtype != PGG_F32 && K % 32 == 0 && groupSize % 32 == 0 && forced_variant() != kVariantSimt) {
+    p->variant = kVariantStream;
+    // room for an even routing's rows and what a draw adds to them in all but a few experts (their
+    // rows take a second block), but an expert has at most one row of a token
+    const double miss = topK >= G ? 0.0 : 1.0 - static_cast<double>(topK) / G;
+    const double live = G * (1.0 - std::pow(miss, static_cast<double>(batch)));
+    const double rows = M / live, most = rows + 2.8 * std::sqrt(rows);
+    const double want = most < batch ? most : static_cast<double>(batch);
+    p->rows_per_block = want <= 8 ? 8 : want <= 16 ? 16 : 32;
+  }
   p->max_row_blocks = (M + p->rows_per_block - 1) / p->rows_per_block + (G < M ? G : M);
   if (p->max_row_blocks * ((N + 31) / 32) > kInt32Max) return PGG_ERR_SHAPE;  // 32-bit tile numbers
   size_t used = 256;
@@ -56,6 +71,9 @@ int w4_plan(int product, int64_t M, int64_t N, int64_t K, int64_t G, int64_t L, 
   p->rowinfo = take(static_cast<int64_t>(sizeof(RowInfo)) * M);
   p->inv = take(4 * M);
   p->rows = take(product == PGG_W4_COMBINED ? 4 * M * N : 0);
+  const bool stream = p->variant == kVariantStream;
+  p->parts = take(stream ? 2ll * kW4Grid * p->rows_per_block * 128 * 4 : 0);
+  p->arrived = take(stream ? kW4Grid * 4 : 0);
   p->total = used;
   return PGG_OK;
 }
@@ -263,6 +281,12 @@ int pgg_w4_execute(pgg_w4_product product, const void* x, const uint8_t* codes,
   pr.top_k = static_cast<int32_t>(topK);
   pr.row_idx_type = rowIdxType;
   pr.rows_per_block = p.rows_per_block;
+  // the tensor cores need 16-byte aligned rows; the FP32 pipes take any row blocks
+  const bool stream_rows = p.variant == kVariantStream && aligned(x, 16) && aligned(codes, 16);
+  if (stream_rows) {
+    pr.clear = reinterpret_cast<uint32_t*>(w + p.arrived);
+    pr.n_clear = kW4Grid;
+  }
   rc = status_of(launch_rows_prep(pr, env.num_sms, s));
   if (rc != PGG_OK) return rc;
   W4Args a;
@@ -288,7 +312,15 @@ int pgg_w4_execute(pgg_w4_product product, const void* x, const uint8_t* codes,
   a.product = product;
   a.scale_f32 = scale_dtype == PGG_F32;
   a.out_f32 = out_dtype == PGG_F32;
-  rc = status_of(launch_w4_simt(dtype, a, env.num_sms, s));
+  a.wait_limit_ns = env.wait_limit_ns;
+  if (stream_rows) {
+    a.parts = reinterpret_cast<float*>(w + p.parts);
+    a.arrived = reinterpret_cast<uint32_t*>(w + p.arrived);
+    a.pairs = N % 2 == 0 && aligned(a.out, 2 * elem_size(out_dtype));
+    rc = status_of(launch_w4_stream(dtype, p.rows_per_block, a, env.num_sms, s));
+  } else {
+    rc = status_of(launch_w4_simt(dtype, a, env.num_sms, s));
+  }
   if (rc != PGG_OK || product != PGG_W4_COMBINED) return rc;
   return status_of(launch_w4_combine(static_cast<const float*>(a.out), a.hdr, batch, topK, N,
                                      static_cast<float*>(out), env.num_sms, s));

@@ -80,6 +80,7 @@ __device__ bool build_row_blocks(const RowsPrepArgs& a) {
     rows += tot_c;
     blocks += tot_b;
   }
+  for (int i = threadIdx.x; i < a.n_clear; i += blockDim.x) a.clear[i] = 0;
   if (threadIdx.x == 0) {
     a.hdr->n_row_blocks = blocks;
     a.hdr->sched_next = 0;

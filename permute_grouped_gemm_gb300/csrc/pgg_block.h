@@ -25,7 +25,19 @@ struct W4Args {
   int32_t product;       // pgg_w4_product
   int32_t scale_f32;     // scales are fp32 (else the dtype)
   int32_t out_f32;       // out is fp32 (else the dtype)
+  // of the streaming kernel
+  float* parts;          // [2 kW4Grid][rows of a block][128] sums of the tiles that CTAs share
+  uint32_t* arrived;     // [kW4Grid] parts of the tile that begins in a CTA; zeros at the start
+  int32_t n_blocks;      // blocks of columns (set by the launch)
+  int32_t pairs;         // two neighbouring outputs are one aligned word
+  uint64_t wait_limit_ns;
 };
+
+constexpr int kW4Grid = 152;  // most CTAs of the streaming kernel: one an SM
+
+// 16-bit, K and group multiples of 32, x and codes 16-byte aligned; blocks of 8, 16 or 32 rows.
+cudaError_t launch_w4_stream(int dtype, int rows_per_block, W4Args a, int num_sms,
+                             cudaStream_t stream);
 
 cudaError_t launch_w4_simt(int dtype, const W4Args& a, int num_sms, cudaStream_t stream);
 // out[b] = sum over j of rows[b * top_k + j] in fp32, zeros when the status word is set.

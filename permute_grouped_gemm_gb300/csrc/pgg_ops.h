@@ -91,6 +91,8 @@ struct RowsPrepArgs {
   int32_t* inv;      // [M]
   int64_t M, G;
   int32_t top_k, row_idx_type, rows_per_block;
+  uint32_t* clear = nullptr;  // words that the launch sets to 0
+  int32_t n_clear = 0;
 };
 cudaError_t launch_rows_prep(const RowsPrepArgs& a, int num_sms, cudaStream_t stream);
 
