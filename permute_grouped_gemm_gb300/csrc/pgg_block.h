@@ -26,6 +26,7 @@ struct W4Args {
   int32_t scale_f32;     // scales are fp32 (else the dtype)
   int32_t out_f32;       // out is fp32 (else the dtype)
   // of the streaming kernel
+  void* packed;          // the row blocks' rows of x in the products' order
   float* parts;          // [2 kW4Grid][rows of a block][128] sums of the tiles that CTAs share
   uint32_t* arrived;     // [kW4Grid] parts of the tile that begins in a CTA; zeros at the start
   int32_t n_blocks;      // blocks of columns (set by the launch)
@@ -35,6 +36,7 @@ struct W4Args {
 
 constexpr int kW4Grid = 152;  // most CTAs of the streaming kernel: one an SM
 
+int64_t w4_packed_bytes(int64_t row_blocks, int rows_per_block, int64_t K);
 // 16-bit, K and group multiples of 32, x and codes 16-byte aligned; blocks of 8, 16 or 32 rows.
 cudaError_t launch_w4_stream(int dtype, int rows_per_block, W4Args a, int num_sms,
                              cudaStream_t stream);

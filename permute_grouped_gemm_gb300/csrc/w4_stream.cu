@@ -2,26 +2,25 @@
 // streamed once per block of up to 32 rows, and that stream is the bound.
 //
 // Tile: 128 columns of one expert (gated: 64 gates and their 64 ups) x NR rows.
-// A stage is 256 of k: 128 columns x 128 bytes of codes by TMA, the rows of x,
-// and the columns' scales. Eight warps take 32 columns x half of k each: codes
-// are unpacked in registers, (v >> 4 j) & 0x000F000F | magic is the pair of
-// numbers 2^7 + code (bf16; 2^10 + code in fp16), from which 2^7 + zero is
-// subtracted exactly, and go as the A operand into mma.sync m16n8k16 with eight
-// rows of x as B. (A word holds codes k .. k + 7, so such a pair is k + j, k + 4 + j;
-// the warp that lays out x pairs it the same way.) A group's fp32 sum is then
-// multiplied by its scale: the weights are never rounded. The warp-wide product
-// is used because the operand is made in registers: for tcgen05 it would go
-// through shared memory once more (5 bytes a code, where 128 a cycle serve all)
-// or through tensor memory and two hand-overs a step; with eight to 32 rows the
-// product itself is far from a bound.
+// A stage is 512 of k (256 with 32 rows): the columns' codes by TMA, and the rows
+// of x, which a launch before this one has gathered and laid out in the order in
+// which the products read them. A warp takes 32 columns x 128 of k: codes are
+// unpacked in registers, (v >> 4 j) & 0x000F000F | magic is the pair of numbers
+// 2^7 + code (bf16; 2^10 + code in fp16), from which 2^7 + zero is subtracted
+// exactly, and go as the A operand into mma.sync m16n8k16 with eight rows of x as
+// B. (A word holds codes k .. k + 7, so such a pair is k + j, k + 4 + j; x is laid
+// out the same way.) A group's fp32 sum is then multiplied by its scale: the
+// weights are never rounded. The warp-wide product is used because the operand is
+// made in registers: for tcgen05 it would go through shared memory once more (5
+// bytes a code, where 128 a cycle serve all) or through tensor memory and two
+// hand-overs a step; with eight to 32 rows the product itself is far from a bound.
 //
 // The tiles' steps of k are dealt to the CTAs in equal runs. A tile that is
 // shared leaves fp32 parts in the workspace, and the CTA that comes last (a
 // counter) adds them in the order of k: no CTA waits for another, and the result
 // does not depend on who comes last.
 //
-// Warps: 0 TMA; one per stage slot for x and the scales; eight for the product.
-// Waits are bounded as everywhere.
+// Warp 0 copies, the others multiply. Waits are bounded as everywhere.
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -38,29 +37,33 @@ namespace pgg {
 namespace {
 
 constexpr int kTile = 128;       // columns of codes
-constexpr int kStep = 256;       // of k a stage
-constexpr int kMmaWarps = 8;     // 4 x 32 columns, 2 halves of a stage's k
-constexpr int kCodeBytes = kTile * kStep / 2;
+constexpr int kPart = 128;       // of k: what a warp takes of a stage
+constexpr int kPanelBytes = kTile * 128;  // codes of 256 of k
 constexpr int kRedStride = kTile + 4;
 
+// NT: eights of rows. U: of k that share a scale (a divisor of the group).
 template <int NT, int U, bool ZEROS>
 struct Cfg {
   static constexpr int kRows = 8 * NT;
-  static constexpr int kUnits = kStep / U;  // groups of a stage, U of k each
+  static constexpr int kParts = NT <= 2 ? 4 : 2;  // (more rows need more registers a warp)
+  static constexpr int kStep = kParts * kPart;
+  static constexpr int kMmaWarps = 4 * kParts;
+  static constexpr int kUnits = kPart / U;  // scales of a column and part
+  static constexpr int kCodeBytes = kParts / 2 * kPanelBytes;
   static constexpr int kXBytes = kRows * kStep * 2;
-  static constexpr int kScaleBytes = kUnits * kTile * 4;
-  static constexpr int kStageBytes = kCodeBytes + kXBytes + kScaleBytes * (ZEROS ? 2 : 1);
-  static constexpr int kRedBytes = kRows * kRedStride * 4;
+  static constexpr int kStageBytes = kCodeBytes + kXBytes;
+  static constexpr int kRedFloats = kRows * kRedStride;
+  static constexpr int kRedBytes = kParts / 2 * kRedFloats * 4;  // one for two parts
   static constexpr int kFit = (225 * 1024 - kRedBytes - 1024) / kStageBytes;
-  static constexpr int kStages = kFit < 7 ? kFit : 7;  // (16 warps: 128 registers a thread)
-  static constexpr int kThreads = 32 * (1 + kStages + kMmaWarps);
+  static constexpr int kStages = kFit < 8 ? kFit : 8;
+  static constexpr int kThreads = 32 * (1 + kMmaWarps);
   static constexpr int kSmem = kStages * kStageBytes + kRedBytes + 2048;
   static_assert(kStageBytes % 1024 == 0, "operand alignment");
 };
 
 struct Ctl {
-  uint64_t full[8];   // codes' bytes, and x and scales written
-  uint64_t empty[8];  // read by all eight warps
+  uint64_t full[8];   // the stage's bytes are there
+  uint64_t empty[8];  // read by all warps
   int abort;
   int last;           // this CTA is the one that adds the tile's parts
 };
@@ -73,6 +76,7 @@ struct Walk {
 
 struct Tile {
   int64_t g, row0, n0;
+  uint32_t rb;
   int rows;
 };
 
@@ -90,6 +94,7 @@ __device__ __forceinline__ Tile tile_of(uint32_t t, const W4Args& a) {
          (a.product == PGG_W4_GATED ? kTile / 2 : kTile);
   x.g = e.x;
   x.row0 = e.y;
+  x.rb = rb;
   x.rows = e.z;
   return x;
 }
@@ -103,8 +108,18 @@ __device__ __forceinline__ int64_t column_of(const W4Args& a, const Tile& x, int
   return x.n0 + r < a.N ? x.n0 + r : -1;
 }
 
+// `bytes` (a multiple of 16) from global to shared memory, both 16-byte aligned.
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes,
+                                          uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          ptx::smem_addr(dst)),
+      "l"(src), "r"(bytes), "r"(ptx::smem_addr(bar))
+      : "memory");
+}
+
 template <int NT, int U, bool ZEROS>
-__device__ void code_producer(uint8_t* smem, Ctl* ctl, const CUtensorMap* tm, const W4Args& a,
+__device__ void producer(uint8_t* smem, Ctl* ctl, const CUtensorMap* tm, const W4Args& a,
                               const Walk& k) {
   using C = Cfg<NT, U, ZEROS>;
   volatile int* abort = &ctl->abort;
@@ -119,17 +134,28 @@ __device__ void code_producer(uint8_t* smem, Ctl* ctl, const CUtensorMap* tm, co
     const int32_t c0 = static_cast<int32_t>(x.n0);
     const int32_t c1 = static_cast<int32_t>(x.n0 + (gated ? a.N : 64));
     const bool second = gated || x.n0 + 64 < a.N;
+    const char* xp = static_cast<const char*>(a.packed) +
+                     static_cast<int64_t>(x.rb) * k.nks * C::kXBytes;
     for (; ks < k.nks && s < k.end; ++ks, ++s) {
       if (!ptx::mbar_wait(&ctl->empty[stage], phase ^ 1u, a.wait_limit_ns, abort)) {
         failed = true;
         break;
       }
       uint8_t* p = smem + stage * C::kStageBytes;
-      ptx::mbar_arrive_expect_tx(&ctl->full[stage], second ? kCodeBytes : kCodeBytes / 2);
-      ptx::tma_load_3d(p, tm, &ctl->full[stage], ks * (kStep / 4), c0, static_cast<int32_t>(x.g));
-      if (second)
-        ptx::tma_load_3d(p + kCodeBytes / 2, tm, &ctl->full[stage], ks * (kStep / 4), c1,
+      // (panels behind the last column or code bring nothing or zeros; x is zero there)
+      ptx::mbar_arrive_expect_tx(&ctl->full[stage],
+                                 (second ? C::kCodeBytes : C::kCodeBytes / 2) + C::kXBytes);
+#pragma unroll
+      for (int j = 0; j < C::kParts / 2; ++j) {
+        const int32_t c = (ks * (C::kParts / 2) + j) * 64;
+        ptx::tma_load_3d(p + j * kPanelBytes, tm, &ctl->full[stage], c, c0,
                          static_cast<int32_t>(x.g));
+        if (second)
+          ptx::tma_load_3d(p + j * kPanelBytes + kPanelBytes / 2, tm, &ctl->full[stage], c, c1,
+                           static_cast<int32_t>(x.g));
+      }
+      bulk_load(p + C::kCodeBytes, xp + static_cast<int64_t>(ks) * C::kXBytes, C::kXBytes,
+                &ctl->full[stage]);
       outstanding |= 1u << stage;
       last_parity = (last_parity & ~(1u << stage)) | (phase << stage);
       if (++stage == C::kStages) {
@@ -142,7 +168,7 @@ __device__ void code_producer(uint8_t* smem, Ctl* ctl, const CUtensorMap* tm, co
     ctl->abort = 1;
     raise_status(a.hdr, kStTimeout, 172);
   }
-  // the copies in flight land before the CTA ends (the feeders arrive whatever happens)
+  // the copies in flight land before the CTA ends
   int no_abort = 0;
   for (int i = 0; i < C::kStages; ++i)
     if (outstanding & (1u << i))
@@ -150,12 +176,12 @@ __device__ void code_producer(uint8_t* smem, Ctl* ctl, const CUtensorMap* tm, co
 }
 
 // Where the eight values of x at k = 8 v of a stage, row n, stand: in the order in which the
-// product's lanes read them, 16 bytes each, mixed so that neither side meets in a bank.
-template <int U>
+// product's lanes read them, 16 bytes each.
+template <int PARTS, int U>
 __device__ __forceinline__ int x_place(int n, int v) {
   const int unit = v / (U / 8), rest = v % (U / 8), q = rest / (U / 32), i = rest % (U / 32);
-  const int s = unit * (U / 32) + i, p = (n & 7) * 4 + q;
-  return ((n >> 3) * 8 + s) * 512 + ((p ^ (s & 3) ^ ((p & 1) << 2)) << 4);
+  const int slot = unit * (U / 32) + i;  // of 32 k
+  return ((n >> 3) * (4 * PARTS) + slot) * 512 + (((n & 7) * 4 + q) << 4);
 }
 
 // (x0 x1)(x2 x3)(x4 x5)(x6 x7) -> (x0 x4)(x1 x5)(x2 x6)(x3 x7)
@@ -164,102 +190,39 @@ __device__ __forceinline__ uint4 pair_up(const uint4& x) {
                     __byte_perm(x.y, x.w, 0x5410), __byte_perm(x.y, x.w, 0x7632));
 }
 
-// Feeder warp w fills stage slot w: the rows of x, a row of 512 bytes at a time, and the columns'
-// scales (and zeros, as the pair that is subtracted).
-template <int DT, int NT, int U, bool ZEROS>
-__device__ void feeder(uint8_t* smem, Ctl* ctl, int w, const W4Args& a, const Walk& k) {
+// The rows of x of every row block, gathered and in the products' order. A warp takes eight rows of
+// a block and 32 of k: every 16 bytes of a lane are one of its 512 neighbouring bytes.
+template <int NT, int U, bool ZEROS>
+__global__ void __launch_bounds__(256) w4_pack_kernel(const W4Args a) {
   using C = Cfg<NT, U, ZEROS>;
-  volatile int* abort = &ctl->abort;
+  ptx::griddep_wait();
+  if (routing_failed(a.hdr)) return;
   const int lane = threadIdx.x & 31;
-  uint8_t* xs = smem + w * C::kStageBytes + kCodeBytes;
-  float* scales = reinterpret_cast<float*>(xs + C::kXBytes);
-  uint32_t* zeros = reinterpret_cast<uint32_t*>(xs + C::kXBytes + C::kScaleBytes);
-  const int64_t columns = a.product == PGG_W4_GATED ? 2 * a.N : a.N;
-  uint32_t phase = 0;
-  bool failed = false;
-  int64_t tile = -1;
-  Tile x = {};
-  int64_t xrow = 0;       // lane n: offset of row n of x
-  int64_t at[4] = {};     // first scale of columns lane + 32 i, or -1
-  for (int64_t s = k.begin + w; s < k.end; s += C::kStages) {
-    const int64_t t = s / k.nks;
-    const int ks = static_cast<int>(s - t * k.nks);
-    if (t != tile) {
-      tile = t;
-      x = tile_of<C::kRows>(static_cast<uint32_t>(t), a);
-      if (lane < x.rows) {
-        const int64_t row = check_index(a.hdr, x.row0 + lane, a.M, 173);
-        xrow = (a.product == PGG_W4_COMBINED
-                    ? row
-                    : check_index(a.hdr, a.rowinfo[row].token, a.batch, 174)) *
-               a.K;
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int64_t c = column_of(a, x, lane + 32 * i);
-        at[i] = c < 0 ? -1 : (x.g * columns + c) * a.groups;
-      }
-    }
-    const uint32_t k0 = static_cast<uint32_t>(ks) * kStep;
-    const uint32_t K = static_cast<uint32_t>(a.K);
-#pragma unroll
-    for (int n0 = 0; n0 < C::kRows; n0 += 8) {
-      uint4 v[8];  // (the first eight rows are loaded before the wait: they need no room yet)
-#pragma unroll
-      for (int n = 0; n < 8; ++n) {
-        const int64_t row = __shfl_sync(0xFFFFFFFFu, xrow, n0 + n);
-        v[n] = make_uint4(0, 0, 0, 0);
-        if (n0 + n < x.rows && k0 + 8 * lane < K)
-          v[n] = __ldg(
-              reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.x) + row + k0) + lane);
-      }
-      if (n0 == 0) {
-        if (!failed && !ptx::mbar_wait(&ctl->empty[w], phase ^ 1u, a.wait_limit_ns, abort))
-          failed = true;  // (from here on it only arrives, so that copies in flight are waited for)
-        failed = __any_sync(0xFFFFFFFFu, failed);
-      }
-      if (failed) break;
-#pragma unroll
-      for (int n = 0; n < 8; ++n)
-        if (n0 + n < x.rows)  // (what stands in the others reaches no row that is looked at)
-          *reinterpret_cast<uint4*>(xs + x_place<U>(n0 + n, lane)) = pair_up(v[n]);
-    }
-    if (!failed) {
-#pragma unroll
-      for (int u = 0; u < C::kUnits; ++u) {
-        const uint32_t kk = k0 + u * U;
-        const uint32_t group = kk < K ? kk / static_cast<uint32_t>(a.group) : 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float sc = 0.0f;
-          uint32_t z = 8;
-          if (at[i] >= 0 && kk < K) {
-            if (a.scale_f32)
-              sc = __ldg(static_cast<const float*>(a.scales) + at[i] + group);
-            else if (DT == PGG_BF16)
-              sc = __uint_as_float(static_cast<uint32_t>(__ldg(
-                       static_cast<const uint16_t*>(a.scales) + at[i] + group)) << 16);
-            else
-              sc = __half2float(__ldg(static_cast<const __half*>(a.scales) + at[i] + group));
-            if (ZEROS) z = __ldg(a.zeros + at[i] + group);
-          }
-          scales[u * kTile + lane + 32 * i] = sc;
-          if (ZEROS) {
-            const uint16_t h = DT == PGG_BF16
-                                   ? __bfloat16_as_ushort(__float2bfloat16_rn(128.0f + z))
-                                   : __half_as_ushort(__float2half_rn(1024.0f + z));
-            zeros[u * kTile + lane + 32 * i] = h * 0x10001u;
-          }
-        }
-      }
-    }
-    __syncwarp();
-    if (lane == 0) ptx::mbar_arrive(&ctl->full[w]);
-    phase ^= 1u;
-  }
-  if (failed && lane == 0) {
-    ctl->abort = 1;
-    raise_status(a.hdr, kStTimeout, 175);
+  const uint32_t K = static_cast<uint32_t>(a.K);
+  const uint32_t nks = (K + C::kStep - 1) / C::kStep;
+  constexpr uint32_t kSlots = 4 * C::kParts * NT;  // of 512 bytes, a stage
+  const uint64_t total = static_cast<uint64_t>(a.hdr->n_row_blocks) * nks * kSlots;
+  const uint64_t step = static_cast<uint64_t>(gridDim.x) * 8;
+  for (uint64_t i = blockIdx.x * 8ull + (threadIdx.x >> 5); i < total; i += step) {
+    const uint64_t stage = i / kSlots;
+    const uint32_t in_stage = static_cast<uint32_t>(i - stage * kSlots);
+    const uint32_t rb = static_cast<uint32_t>(stage / nks);
+    const uint32_t ks = static_cast<uint32_t>(stage - static_cast<uint64_t>(rb) * nks);
+    const uint32_t slot = in_stage % (4 * C::kParts);
+    const int n = 8 * static_cast<int>(in_stage / (4 * C::kParts)) + (lane >> 2);
+    const int4 e = a.rblist[rb];
+    if (n >= e.z) continue;  // (what stands there reaches no row that is looked at)
+    // the inverse of x_place: this lane's eight values of k
+    const uint32_t unit = slot / (U / 32), w = slot % (U / 32);
+    const uint32_t k = ks * C::kStep + unit * U + (lane & 3) * (U / 4) + w * 8;
+    const int64_t row = check_index(a.hdr, static_cast<int64_t>(e.y) + n, a.M, 173);
+    const int64_t xrow = a.product == PGG_W4_COMBINED
+                             ? row
+                             : check_index(a.hdr, a.rowinfo[row].token, a.batch, 174);
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (k < K)
+      v = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.x) + xrow * a.K + k));
+    *reinterpret_cast<uint4*>(static_cast<char*>(a.packed) + i * 512 + lane * 16) = pair_up(v);
   }
 }
 
@@ -280,11 +243,12 @@ __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uin
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Codes j and 4 + j of a word, less the zero (`z` is the pair 2^7 + zero, or 2^10 + zero).
+// Codes j and 4 + j of a word, less the zero (`z` is the pair 2^7 + zero, or 2^10 + zero; `magic` the
+// pair 2^7 or 2^10, from a register: an instruction holds one of the two constants only).
 template <int DT>
-__device__ __forceinline__ uint32_t unpack(uint32_t w, int j, uint32_t z) {
-  const uint32_t v = ((w >> (4 * j)) & 0x000F000Fu) | (DT == PGG_BF16 ? 0x43004300u : 0x64006400u);
-  uint32_t r;
+__device__ __forceinline__ uint32_t unpack(uint32_t w, int j, uint32_t magic, uint32_t z) {
+  uint32_t v, r;
+  asm("lop3.b32 %0, %1, 0x000F000F, %2, 0xEA;" : "=r"(v) : "r"(w >> (4 * j)), "r"(magic));
   if constexpr (DT == PGG_BF16)
     asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(z));
   else
@@ -297,30 +261,40 @@ struct Words {
   uint32_t v[W];
 };
 
+// W words of shared memory.
 template <int W>
-__device__ __forceinline__ Words<W> load_words(const uint8_t* p) {
+__device__ __forceinline__ Words<W> load_words(uint32_t addr) {
   Words<W> r;
-  if constexpr (W == 4) {
-    const uint4 q = *reinterpret_cast<const uint4*>(p);
-    r.v[0] = q.x;
-    r.v[1] = q.y;
-    r.v[2] = q.z;
-    r.v[3] = q.w;
-  } else if constexpr (W == 2) {
-    const uint2 q = *reinterpret_cast<const uint2*>(p);
-    r.v[0] = q.x;
-    r.v[1] = q.y;
-  } else {
-    r.v[0] = *reinterpret_cast<const uint32_t*>(p);
-  }
+  if constexpr (W == 4)
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r.v[0]), "=r"(r.v[1]), "=r"(r.v[2]), "=r"(r.v[3])
+                 : "r"(addr)
+                 : "memory");
+  else if constexpr (W == 2)
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];"
+                 : "=r"(r.v[0]), "=r"(r.v[1])
+                 : "r"(addr)
+                 : "memory");
+  else
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(r.v[0]) : "r"(addr) : "memory");
   return r;
+}
+
+// A sum over the stage's parts of k, of which each two have been added already.
+template <int PARTS, int STRIDE>
+__device__ __forceinline__ float sum_parts(const float* p) {
+  return PARTS == 4 ? p[0] + p[STRIDE] : p[0];
 }
 
 // The tile's results from `red` [row][column].
 template <int DT, int NT>
 __device__ __forceinline__ void write_tile(const float* red, const W4Args& a, const Tile& x,
                                            int thread) {
-  constexpr int kThr = 32 * kMmaWarps;
+  using C = Cfg<NT, 128, false>;
+  constexpr int kThr = C::kMmaWarps * 32;
+  auto at_red = [&](int j, int c) {
+    return sum_parts<C::kParts, C::kRedFloats>(red + j * kRedStride + c);
+  };
   const bool gated = a.product == PGG_W4_GATED;
   const int half = gated ? 32 : 64;  // pairs of a row
   for (int i = thread; i < x.rows * half; i += kThr) {
@@ -329,11 +303,11 @@ __device__ __forceinline__ void write_tile(const float* red, const W4Args& a, co
     if (n >= a.N) continue;
     const int64_t row = x.row0 + j;
     const int64_t pos = check_index(a.hdr, a.rowinfo[row].rank, a.M, 176);
-    float v0 = red[j * kRedStride + c], v1 = red[j * kRedStride + c + 1];
+    float v0 = at_red(j, c), v1 = at_red(j, c + 1);
     if (gated) {
       const float p = a.probs ? a.probs[pos] : 1.0f;
-      v0 = gate(v0, red[j * kRedStride + 64 + c], p);
-      v1 = gate(v1, red[j * kRedStride + 65 + c], p);
+      v0 = gate(v0, at_red(j, 64 + c), p);
+      v1 = gate(v1, at_red(j, 65 + c), p);
     }
     const int64_t at = (a.product == PGG_W4_COMBINED ? pos : row) * a.N + n;
     if (a.out_f32) {
@@ -357,12 +331,42 @@ __device__ __forceinline__ void write_tile(const float* red, const W4Args& a, co
   }
 }
 
+// Scales (and zeros) of this lane's column for one step, a part of the k.
+template <int DT, int NT, int U, bool ZEROS>
+struct Scales {
+  using C = Cfg<NT, U, ZEROS>;
+  uint32_t s[C::kUnits];  // as they stand in memory: what converts them would wait for them
+  uint32_t z[ZEROS ? C::kUnits : 1];
+
+  // `at`: the column's first scale or -1;  unit: the first of the step's units of U
+  __device__ __forceinline__ void load(const W4Args& a, int64_t at, uint32_t unit) {
+#pragma unroll
+    for (int u = 0; u < C::kUnits; ++u) {
+      uint32_t group = unit + u;
+      if (a.group != U) group = group * U / static_cast<uint32_t>(a.group);
+      s[u] = 0;
+      if (ZEROS) z[u] = 0;
+      if (at < 0 || group >= static_cast<uint32_t>(a.groups)) continue;
+      if (a.scale_f32)
+        s[u] = __ldg(static_cast<const uint32_t*>(a.scales) + at + group);
+      else
+        s[u] = __ldg(static_cast<const uint16_t*>(a.scales) + at + group);
+      if (ZEROS) z[u] = __ldg(a.zeros + at + group);
+    }
+  }
+  __device__ __forceinline__ float scale(const W4Args& a, int u) const {
+    if (a.scale_f32) return __uint_as_float(s[u]);
+    if (DT == PGG_BF16) return __uint_as_float(s[u] << 16);
+    return __half2float(__ushort_as_half(static_cast<uint16_t>(s[u])));
+  }
+};
+
 template <int DT, int NT, int U, bool ZEROS>
 __device__ void multiplier(uint8_t* smem, Ctl* ctl, float* red, int w, const W4Args& a,
                            const Walk& k) {
   using C = Cfg<NT, U, ZEROS>;
-  constexpr int W = U / 32;            // words of a lane and group
-  constexpr int kHalf = C::kUnits / 2;  // groups of this warp and stage
+  constexpr int W = U / 32;  // words of a lane and unit
+  constexpr int kThr = 32 * C::kMmaWarps;
   volatile int* abort = &ctl->abort;
   const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
   const int col0 = 32 * (w & 3), part = w >> 2;
@@ -370,7 +374,14 @@ __device__ void multiplier(uint8_t* smem, Ctl* ctl, float* red, int w, const W4A
   // (two g) lie in different halves of the swizzled 128 bytes
   const int perm = (g >> 1) + 4 * (g & 1);
   const int thread = 32 * w + lane;
-  constexpr uint32_t kZero8 = DT == PGG_BF16 ? 0x43084308u : 0x64086408u;
+  // bf16: 2^7 + z is 0x4300 | z, fp16: 2^10 + z is 0x6400 | z
+  constexpr uint32_t kMagic = DT == PGG_BF16 ? 0x43004300u : 0x64006400u;
+  const int64_t columns = a.product == PGG_W4_GATED ? 2 * a.N : a.N;
+  const uint32_t my_codes =
+      ptx::smem_addr(smem) + (part >> 1) * kPanelBytes + (col0 + perm) * 128;
+  const uint32_t my_x = ptx::smem_addr(smem) + C::kCodeBytes + part * 4 * 512 + lane * 16;
+  uint32_t magic;
+  asm volatile("mov.u32 %0, %1;" : "=r"(magic) : "n"(kMagic));
   int stage = 0;
   uint32_t phase = 0;
   bool failed = false;
@@ -380,8 +391,16 @@ __device__ void multiplier(uint8_t* smem, Ctl* ctl, float* red, int w, const W4A
     const int64_t left = k.end - s;
     const int n_steps = left < k.nks - ks0 ? static_cast<int>(left) : k.nks - ks0;
     const Tile x = tile_of<C::kRows>(t, a);
+    const int64_t column = column_of(a, x, col0 + lane);
+    const int64_t at = column < 0 ? -1 : (x.g * columns + column) * a.groups;
     float sum[2][NT][4] = {};
+    Scales<DT, NT, U, ZEROS> now, next;
+    uint32_t unit = static_cast<uint32_t>(ks0 * C::kParts + part) * C::kUnits;
+    next.load(a, at, unit);
     for (int i = 0; i < n_steps; ++i) {
+      now = next;
+      unit += C::kParts * C::kUnits;
+      if (i + 1 < n_steps) next.load(a, at, unit);  // (a step ahead)
       if (!failed && !__all_sync(0xFFFFFFFFu, ptx::mbar_wait(&ctl->full[stage], phase,
                                                              a.wait_limit_ns, abort))) {
         failed = true;
@@ -390,59 +409,60 @@ __device__ void multiplier(uint8_t* smem, Ctl* ctl, float* red, int w, const W4A
           raise_status(a.hdr, kStTimeout, 177);
         }
       }
-      if (failed) break;  // (the eight warps still meet at every barrier below)
-      const uint8_t* codes = smem + stage * C::kStageBytes;
-      const uint8_t* xs = codes + kCodeBytes;
-      const float* scales = reinterpret_cast<const float*>(xs + C::kXBytes);
-      const uint32_t* zeros = reinterpret_cast<const uint32_t*>(xs + C::kXBytes + C::kScaleBytes);
+      if (failed) break;  // (the warps still meet at every barrier below)
+      const uint32_t codes = my_codes + stage * C::kStageBytes;
+      const uint32_t xs = my_x + stage * C::kStageBytes;
 #pragma unroll
-      for (int h = 0; h < kHalf; ++h) {
-        const int u = part * kHalf + h;
-        const int byte = u * (U / 2) + q * (U / 8);
+      for (int u = 0; u < C::kUnits; ++u) {
+        const int byte = (part & 1) * 64 + u * (U / 2) + q * (U / 8);
+        const int in_row = (((byte >> 4) ^ perm) << 4) | (byte & 15);
         Words<W> word[2][2];
-        uint32_t z[2][2];
-        float sc[2][2];
 #pragma unroll
         for (int r = 0; r < 2; ++r)
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int col = col0 + 16 * r + 8 * e + perm;
-            word[r][e] = load_words<W>(codes + col * 128 + ((((byte >> 4) ^ perm) << 4) | (byte & 15)));
-            sc[r][e] = scales[u * kTile + col];
-            z[r][e] = ZEROS ? zeros[u * kTile + col] : kZero8;
-          }
+          for (int e = 0; e < 2; ++e)
+            word[r][e] = load_words<W>(codes + (16 * r + 8 * e) * 128 + in_row);
+        uint32_t z[2][2];
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            z[r][e] = kMagic + (ZEROS ? __shfl_sync(0xFFFFFFFFu, now.z[ZEROS ? u : 0],
+                                                    16 * r + 8 * e + perm) * 0x10001u
+                                      : 0x00080008u);
         float d[2][NT][4] = {};
 #pragma unroll
         for (int i8 = 0; i8 < W; ++i8) {
-          const int slot = u * W + i8;
-          uint4 b[NT];
+          Words<4> b[NT];
 #pragma unroll
           for (int n = 0; n < NT; ++n)
-            b[n] = *reinterpret_cast<const uint4*>(
-                xs + (n * 8 + slot) * 512 + ((lane ^ (slot & 3) ^ ((lane & 1) << 2)) << 4));
+            b[n] = load_words<4>(xs + (n * 4 * C::kParts + u * W + i8) * 512);
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
             uint32_t p[2][4];
 #pragma unroll
             for (int e = 0; e < 2; ++e)
 #pragma unroll
-              for (int j = 0; j < 4; ++j) p[e][j] = unpack<DT>(word[r][e].v[i8], j, z[r][e]);
+              for (int j = 0; j < 4; ++j) p[e][j] = unpack<DT>(word[r][e].v[i8], j, magic, z[r][e]);
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-              mma<DT>(d[r][n], p[0][0], p[1][0], p[0][1], p[1][1], b[n].x, b[n].y);
-              mma<DT>(d[r][n], p[0][2], p[1][2], p[0][3], p[1][3], b[n].z, b[n].w);
+              mma<DT>(d[r][n], p[0][0], p[1][0], p[0][1], p[1][1], b[n].v[0], b[n].v[1]);
+              mma<DT>(d[r][n], p[0][2], p[1][2], p[0][3], p[1][3], b[n].v[2], b[n].v[3]);
             }
           }
         }
 #pragma unroll
-        for (int r = 0; r < 2; ++r)
+        for (int r = 0; r < 2; ++r) {
+          const float s0 = __shfl_sync(0xFFFFFFFFu, now.scale(a, u), 16 * r + perm);
+          const float s1 = __shfl_sync(0xFFFFFFFFu, now.scale(a, u), 16 * r + 8 + perm);
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
-            sum[r][n][0] = fmaf(sc[r][0], d[r][n][0], sum[r][n][0]);
-            sum[r][n][1] = fmaf(sc[r][0], d[r][n][1], sum[r][n][1]);
-            sum[r][n][2] = fmaf(sc[r][1], d[r][n][2], sum[r][n][2]);
-            sum[r][n][3] = fmaf(sc[r][1], d[r][n][3], sum[r][n][3]);
+            sum[r][n][0] = fmaf(s0, d[r][n][0], sum[r][n][0]);
+            sum[r][n][1] = fmaf(s0, d[r][n][1], sum[r][n][1]);
+            sum[r][n][2] = fmaf(s1, d[r][n][2], sum[r][n][2]);
+            sum[r][n][3] = fmaf(s1, d[r][n][3], sum[r][n][3]);
           }
+        }
       }
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(&ctl->empty[stage]);
@@ -451,21 +471,24 @@ __device__ void multiplier(uint8_t* smem, Ctl* ctl, float* red, int w, const W4A
         phase ^= 1u;
       }
     }
-    // both halves of k into red [row][column]
+    // the parts of k into red [row][column], each two one after the other
+    if (s > k.begin) ptx::named_bar_sync(1, kThr);  // (the tile before is read)
+#pragma unroll
     for (int turn = 0; turn < 2; ++turn) {
-      if (part == turn) {
+      if ((part & 1) == turn) {
 #pragma unroll
         for (int r = 0; r < 2; ++r)
 #pragma unroll
           for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              float* p = red + (8 * n + 2 * q + (e & 1)) * kRedStride + col0 + 16 * r +
-                         8 * (e >> 1) + perm;
+              float* p = red + (part >> 1) * C::kRedFloats +
+                         (8 * n + 2 * q + (e & 1)) * kRedStride + col0 + 16 * r + 8 * (e >> 1) +
+                         perm;
               *p = turn == 0 ? sum[r][n][e] : *p + sum[r][n][e];
             }
       }
-      ptx::named_bar_sync(1, 32 * kMmaWarps);
+      ptx::named_bar_sync(1, kThr);
     }
     bool mine = true;
     if (n_steps < k.nks) {
@@ -473,31 +496,32 @@ __device__ void multiplier(uint8_t* smem, Ctl* ctl, float* red, int w, const W4A
       const int64_t s0 = static_cast<int64_t>(t) * k.nks;
       const int64_t first = ((s0 + 1) * k.ctas - 1) / k.total;
       const int64_t last = ((s0 + k.nks) * k.ctas - 1) / k.total;
-      constexpr int kPart = C::kRows * kTile;
-      float* own = a.parts + (2 * static_cast<int64_t>(blockIdx.x) + (ks0 == 0 ? 1 : 0)) * kPart;
-      for (int i = thread; i < x.rows * kTile; i += 32 * kMmaWarps)
-        own[i] = red[(i / kTile) * kRedStride + i % kTile];
+      constexpr int kShare = C::kRows * kTile;
+      float* own = a.parts + (2 * static_cast<int64_t>(blockIdx.x) + (ks0 == 0 ? 1 : 0)) * kShare;
+      for (int i = thread; i < x.rows * kTile; i += kThr)
+        own[i] = sum_parts<C::kParts, C::kRedFloats>(red + (i / kTile) * kRedStride + i % kTile);
       __threadfence();
-      ptx::named_bar_sync(1, 32 * kMmaWarps);
+      ptx::named_bar_sync(1, kThr);
       if (thread == 0) {
         const uint32_t before = atomicAdd(a.arrived + first, 1u);
         ctl->last = before == static_cast<uint32_t>(last - first) ? 1 : 0;
       }
-      ptx::named_bar_sync(1, 32 * kMmaWarps);
+      ptx::named_bar_sync(1, kThr);
       mine = *const_cast<volatile int*>(&ctl->last) != 0;
       if (mine) {
         __threadfence();
-        for (int i = thread; i < x.rows * kTile; i += 32 * kMmaWarps) {
+        for (int i = thread; i < x.rows * kTile; i += kThr) {
           float v = 0.0f;
           for (int64_t c = first; c <= last; ++c)
-            v += __ldcg(a.parts + (2 * c + (c == first ? 1 : 0)) * kPart + i);
-          red[(i / kTile) * kRedStride + i % kTile] = v;
+            v += __ldcg(a.parts + (2 * c + (c == first ? 1 : 0)) * kShare + i);
+          float* p = red + (i / kTile) * kRedStride + i % kTile;
+          p[0] = v;
+          if (C::kParts == 4) p[C::kRedFloats] = 0.0f;
         }
-        ptx::named_bar_sync(1, 32 * kMmaWarps);
+        ptx::named_bar_sync(1, kThr);
       }
     }
     if (mine) write_tile<DT, NT>(red, a, x, thread);
-    ptx::named_bar_sync(1, 32 * kMmaWarps);  // red is read before the next tile's sums go there
     s += n_steps;
   }
 }
@@ -514,8 +538,8 @@ __global__ void __launch_bounds__(Cfg<NT, U, ZEROS>::kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
-      ptx::mbar_init(&ctl.full[s], 2);
-      ptx::mbar_init(&ctl.empty[s], kMmaWarps);
+      ptx::mbar_init(&ctl.full[s], 1);
+      ptx::mbar_init(&ctl.empty[s], C::kMmaWarps);
     }
     ctl.abort = 0;
     ptx::fence_mbar_init();
@@ -535,7 +559,7 @@ __global__ void __launch_bounds__(Cfg<NT, U, ZEROS>::kThreads, 1)
     return;
   }
   Walk k;
-  k.nks = static_cast<int>((a.K + kStep - 1) / kStep);
+  k.nks = static_cast<int>((a.K + C::kStep - 1) / C::kStep);
   k.total = static_cast<int64_t>(a.hdr->n_row_blocks) * a.n_blocks * k.nks;
   // at least two steps a CTA, so that each has some
   k.ctas = k.total < 2 * static_cast<int64_t>(gridDim.x) ? (k.total + 1) / 2 : gridDim.x;
@@ -543,11 +567,9 @@ __global__ void __launch_bounds__(Cfg<NT, U, ZEROS>::kThreads, 1)
   k.begin = static_cast<int64_t>(blockIdx.x) * k.total / k.ctas;
   k.end = (static_cast<int64_t>(blockIdx.x) + 1) * k.total / k.ctas;
   if (warp == 0) {
-    if (lane == 0) code_producer<NT, U, ZEROS>(smem, &ctl, &tm, a, k);
-  } else if (warp <= C::kStages) {
-    feeder<DT, NT, U, ZEROS>(smem, &ctl, warp - 1, a, k);
+    if (lane == 0) producer<NT, U, ZEROS>(smem, &ctl, &tm, a, k);
   } else {
-    multiplier<DT, NT, U, ZEROS>(smem, &ctl, red, warp - 1 - C::kStages, a, k);
+    multiplier<DT, NT, U, ZEROS>(smem, &ctl, red, warp - 1, a, k);
   }
 }
 
@@ -559,6 +581,13 @@ cudaError_t launch_t(const CUtensorMap& tm, const W4Args& a, int num_sms, cudaSt
   static SmemLimit limit;
   const cudaError_t err = allow_smem(&limit, kern, C::kSmem);
   if (err != cudaSuccess) return err;
+  const int64_t slots = a.max_row_blocks * ((a.K + C::kStep - 1) / C::kStep) * 4 * C::kParts * NT;
+  int64_t blocks = (slots + 7) / 8;
+  if (blocks > num_sms * 8) blocks = num_sms * 8;
+  const cudaError_t packed = launch_pdl(w4_pack_kernel<NT, U, ZEROS>,
+                                        dim3(static_cast<unsigned>(blocks)), dim3(256), 0, stream,
+                                        1, a);
+  if (packed != cudaSuccess) return packed;
   return launch_pdl(kern, dim3(static_cast<unsigned>(num_sms < kW4Grid ? num_sms : kW4Grid)),
                     dim3(C::kThreads), static_cast<size_t>(C::kSmem), stream, 1, tm, a);
 }
@@ -586,6 +615,11 @@ cudaError_t launch_nt(const CUtensorMap& tm, int rows, const W4Args& a, int num_
 }
 
 }  // namespace
+
+int64_t w4_packed_bytes(int64_t row_blocks, int rows_per_block, int64_t K) {
+  const int64_t step = rows_per_block <= 16 ? 4 * kPart : 2 * kPart;
+  return row_blocks * rows_per_block * ((K + step - 1) / step) * step * 2;
+}
 
 cudaError_t launch_w4_stream(int dtype, int rows_per_block, W4Args a, int num_sms,
                              cudaStream_t stream) {
