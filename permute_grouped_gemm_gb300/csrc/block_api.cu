@@ -32,7 +32,7 @@ struct W4Plan {
   int variant;
   int rows_per_block;
   int64_t max_row_blocks;
-  size_t rblist, rowinfo, inv, rows, packed, parts, arrived, total;
+  size_t rblist, rowinfo, inv, rows, packed, exponent, parts, arrived, total;
 };
 
 int w4_plan(int product, int64_t M, int64_t N, int64_t K, int64_t G, int64_t L, int64_t batch,
@@ -73,6 +73,7 @@ int w4_plan(int product, int64_t M, int64_t N, int64_t K, int64_t G, int64_t L, 
   p->rows = take(product == PGG_W4_COMBINED ? 4 * M * N : 0);
   const bool stream = p->variant == kVariantStream;
   p->packed = take(stream ? w4_packed_bytes(p->max_row_blocks, p->rows_per_block, K) : 0);
+  p->exponent = take(stream ? p->max_row_blocks * p->rows_per_block * 4 : 0);
   p->parts = take(stream ? 2ll * kW4Grid * p->rows_per_block * 128 * 4 : 0);
   p->arrived = take(stream ? kW4Grid * 4 : 0);
   p->total = used;
@@ -316,6 +317,7 @@ int pgg_w4_execute(pgg_w4_product product, const void* x, const uint8_t* codes,
   a.wait_limit_ns = env.wait_limit_ns;
   if (stream_rows) {
     a.packed = w + p.packed;
+    a.exponent = reinterpret_cast<int32_t*>(w + p.exponent);
     a.parts = reinterpret_cast<float*>(w + p.parts);
     a.arrived = reinterpret_cast<uint32_t*>(w + p.arrived);
     a.pairs = N % 2 == 0 && aligned(a.out, 2 * elem_size(out_dtype));

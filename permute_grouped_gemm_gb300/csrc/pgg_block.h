@@ -27,14 +27,16 @@ struct W4Args {
   int32_t out_f32;       // out is fp32 (else the dtype)
   // of the streaming kernel
   void* packed;          // the row blocks' rows of x in the products' order
+  int32_t* exponent;     // [row blocks][rows of a block] their powers of two
   float* parts;          // [2 kW4Grid][rows of a block][128] sums of the tiles that CTAs share
   uint32_t* arrived;     // [kW4Grid] parts of the tile that begins in a CTA; zeros at the start
   int32_t n_blocks;      // blocks of columns (set by the launch)
+  int32_t bf16;          // the dtype is bf16 (set by the launch)
   int32_t pairs;         // two neighbouring outputs are one aligned word
   uint64_t wait_limit_ns;
 };
 
-constexpr int kW4Grid = 152;  // most CTAs of the streaming kernel: one an SM
+constexpr int kW4Grid = 304;  // most CTAs of the streaming kernel: two an SM
 
 int64_t w4_packed_bytes(int64_t row_blocks, int rows_per_block, int64_t K);
 // 16-bit, K and group multiples of 32, x and codes 16-byte aligned; blocks of 8, 16 or 32 rows.

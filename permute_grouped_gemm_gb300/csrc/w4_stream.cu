@@ -2,25 +2,36 @@
 // streamed once per block of up to 32 rows, and that stream is the bound.
 //
 // Tile: 128 columns of one expert (gated: 64 gates and their 64 ups) x NR rows.
-// A stage is 512 of k (256 with 32 rows): the columns' codes by TMA, and the rows
-// of x, which a launch before this one has gathered and laid out in the order in
-// which the products read them. A warp takes 32 columns x 128 of k: codes are
-// unpacked in registers, (v >> 4 j) & 0x000F000F | magic is the pair of numbers
-// 2^7 + code (bf16; 2^10 + code in fp16), from which 2^7 + zero is subtracted
-// exactly, and go as the A operand into mma.sync m16n8k16 with eight rows of x as
-// B. (A word holds codes k .. k + 7, so such a pair is k + j, k + 4 + j; x is laid
-// out the same way.) A group's fp32 sum is then multiplied by its scale: the
-// weights are never rounded. The warp-wide product is used because the operand is
-// made in registers: for tcgen05 it would go through shared memory once more (5
-// bytes a code, where 128 a cycle serve all) or through tensor memory and two
-// hand-overs a step; with eight to 32 rows the product itself is far from a bound.
+// A stage is 256 of k. A warp takes 32 columns x 128 of k of it and multiplies
+// with mma.sync m16n8k16 in fp16: the codes, unpacked in registers, are the A
+// operand, eight rows of x the B operand. What the loop is made for is few
+// instructions a code (logic runs at half rate: two an eight codes' word took
+// 250 us, where this takes 150: 64 experts, 512 rows, K 7168, F 2048):
 //
-// The tiles' steps of k are dealt to the CTAs in equal runs. A tile that is
-// shared leaves fp32 parts in the workspace, and the CTA that comes last (a
-// counter) adds them in the order of k: no CTA waits for another, and the result
-// does not depend on who comes last.
+//   - A code needs no conversion: the four bits alone, (w & 0x000F000F), are two
+//     fp16 subnormals of code 2^-24, and (w & 0x00F000F0) two of code 2^-20, so a
+//     word of eight codes costs four ANDs and one shift. Products with x and
+//     their fp32 sums are exact or rounded as in any fp32 sum.
+//   - x is brought to fp16 by a power of two a row, so that its largest value lies
+//     in [2^14, 2^15): bf16 keeps its eight bits, and what is lost is below 2^-35
+//     of the row's largest value. A launch before this one does that, gathers the
+//     rows, and lays them out in the order in which the products read them (a
+//     pair is k + j, k + 4 + j, as in the codes' word; those that meet code 2^-20
+//     divided by 16), with every group's sum of x.
+//   - The zero is taken off a group's sum, zero times the sum of x, and then the
+//     scale multiplies it: the weights are never rounded.
 //
-// Warp 0 copies, the others multiply. Waits are bounded as everywhere.
+// The warp-wide product is used because the operand is made in registers: for
+// tcgen05 it would go through shared memory once more or through tensor memory
+// and two hand-overs a step; with 8 to 32 rows the product is not the bound.
+//
+// The tiles' steps of k are dealt to the CTAs (two an SM, so that one multiplies
+// while the other ends a tile) in equal runs. A tile that is shared leaves fp32
+// parts in the workspace, and the CTA that comes last (a counter) adds them in
+// the order of k: no CTA waits for another, and the result does not depend on
+// who comes last.
+//
+// Warp 0 copies, eight multiply. Waits are bounded as everywhere.
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -32,40 +43,46 @@
 #include "pgg_ops_launch.h"
 #include "pgg_ops_mma.cuh"
 #include "pgg_ptx.cuh"
+#include "pgg_vec.cuh"
 
 namespace pgg {
 namespace {
 
 constexpr int kTile = 128;       // columns of codes
+constexpr int kStep = 256;       // of k a stage
 constexpr int kPart = 128;       // of k: what a warp takes of a stage
-constexpr int kPanelBytes = kTile * 128;  // codes of 256 of k
+constexpr int kMmaWarps = 8;     // 4 x 32 columns, two parts of k
+constexpr int kThreads = 32 * (1 + kMmaWarps);
+constexpr int kCodeBytes = kTile * kStep / 2;
 constexpr int kRedStride = kTile + 4;
+constexpr int kMaxStages = 8;
 
 // NT: eights of rows. U: of k that share a scale (a divisor of the group).
-template <int NT, int U, bool ZEROS>
+template <int NT, int U>
 struct Cfg {
+  static constexpr int kCtas = NT <= 2 ? 2 : 1;  // (32 rows need the registers)
   static constexpr int kRows = 8 * NT;
-  static constexpr int kParts = NT <= 2 ? 4 : 2;  // (more rows need more registers a warp)
-  static constexpr int kStep = kParts * kPart;
-  static constexpr int kMmaWarps = 4 * kParts;
-  static constexpr int kUnits = kPart / U;  // scales of a column and part
-  static constexpr int kCodeBytes = kParts / 2 * kPanelBytes;
-  static constexpr int kXBytes = kRows * kStep * 2;
-  static constexpr int kStageBytes = kCodeBytes + kXBytes;
-  static constexpr int kRedFloats = kRows * kRedStride;
-  static constexpr int kRedBytes = kParts / 2 * kRedFloats * 4;  // one for two parts
-  static constexpr int kFit = (225 * 1024 - kRedBytes - 1024) / kStageBytes;
-  static constexpr int kStages = kFit < 8 ? kFit : 8;
-  static constexpr int kThreads = 32 * (1 + kMmaWarps);
-  static constexpr int kSmem = kStages * kStageBytes + kRedBytes + 2048;
-  static_assert(kStageBytes % 1024 == 0, "operand alignment");
+  static constexpr int kUnits = kPart / U;       // groups of a part
+  static constexpr int kStageUnits = kStep / U;
+  // x of a stage, then its groups' sums [unit][row]
+  static constexpr int kXBytes = kRows * kStep * 2 + kStageUnits * kRows * 4;
+  // a column's scales of a stage (room for fp32), then its zeros
+  static constexpr int kScaleBytes = kTile * kStageUnits * 4;
+  static constexpr int kZeroBytes = kTile * kStageUnits;
+  static constexpr int kStageBytes =
+      (kCodeBytes + kXBytes + kScaleBytes + kZeroBytes + 1023) / 1024 * 1024;
+  static constexpr int kRedBytes = kRows * kRedStride * 4;
+  static constexpr int kFit = (226 * 1024 / kCtas - kRedBytes - 2560) / kStageBytes;
+  static constexpr int kStages = kFit < kMaxStages ? kFit : kMaxStages;
+  static constexpr int kSmem = kStages * kStageBytes + kRedBytes + 1024;
+  static_assert(kSmem * kCtas <= 225 * 1024 && kStages >= 3, "shared memory");
 };
 
 struct Ctl {
-  uint64_t full[8];   // the stage's bytes are there
-  uint64_t empty[8];  // read by all warps
+  uint64_t full[kMaxStages];   // bytes by TMA, the copying warp's cp.async and its stores
+  uint64_t empty[kMaxStages];  // read by all eight warps
   int abort;
-  int last;           // this CTA is the one that adds the tile's parts
+  int last;                    // this CTA is the one that adds the tile's parts
 };
 
 // The steps [begin, end) of this CTA among `total`, dealt to `ctas` of them; nks steps a tile.
@@ -108,6 +125,88 @@ __device__ __forceinline__ int64_t column_of(const W4Args& a, const Tile& x, int
   return x.n0 + r < a.N ? x.n0 + r : -1;
 }
 
+// ------------------------------------------------------------------ x
+
+// Sum of one value a thread over 128 threads, and the largest.
+__device__ __forceinline__ float block_max(float v, float* s) {
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, d));
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = v;
+  __syncthreads();
+  return fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3]));
+}
+
+// A row of a row block: its power of two, its values in the products' order, and its groups' sums.
+// 128 threads a row, eight of k a thread and turn.
+template <int DT, int NT, int U>
+__global__ void __launch_bounds__(128) w4_pack_kernel(const W4Args a) {
+  using C = Cfg<NT, U>;
+  __shared__ float s_max[4];
+  ptx::griddep_wait();
+  if (routing_failed(a.hdr)) return;
+  const int tid = threadIdx.x;
+  const int64_t nks = (a.K + kStep - 1) / kStep;
+  const int64_t total = static_cast<int64_t>(a.hdr->n_row_blocks) * C::kRows;
+  for (int64_t i = blockIdx.x; i < total; i += gridDim.x) {
+    const int64_t rb = i / C::kRows;
+    const int n = static_cast<int>(i - rb * C::kRows);
+    const int4 e = a.rblist[check_index(a.hdr, rb, a.max_row_blocks, 172)];
+    if (n >= e.z) continue;  // (what stands there reaches no row that is looked at)
+    const int64_t row = check_index(a.hdr, static_cast<int64_t>(e.y) + n, a.M, 173);
+    const int64_t xrow = a.product == PGG_W4_COMBINED
+                             ? row
+                             : check_index(a.hdr, a.rowinfo[row].token, a.batch, 174);
+    const uint16_t* x = static_cast<const uint16_t*>(a.x) + xrow * a.K;
+    float most = 0.0f;
+    for (int64_t k = 8 * tid; k < a.K; k += 8 * 128) {
+      float v[8];
+      vec::load<DT, 8>(x, k, v);
+#pragma unroll
+      for (int j = 0; j < 8; ++j)  // (infinities and NaN stay what they are under any power)
+        most = fmaxf(most, fabsf(v[j]) < INFINITY ? fabsf(v[j]) : 0.0f);
+    }
+    most = block_max(most, s_max);
+    int exponent = 0;  // of two: most = m 2^exponent, m in [0.5, 1)
+    if (most > 0.0f) frexpf(most, &exponent);
+    exponent -= 15;
+    // 2^-exponent in two factors (it may lie outside fp32)
+    const float by0 = ldexpf(1.0f, -(exponent / 2)), by1 = ldexpf(1.0f, -(exponent - exponent / 2));
+    if (tid == 0) a.exponent[i] = exponent;
+    char* out = static_cast<char*>(a.packed) + rb * nks * C::kXBytes;
+    const int64_t end = nks * kStep;
+    for (int64_t k = 8 * tid; k < end; k += 8 * 128) {
+      float v[8] = {};
+      if (k < a.K) vec::load<DT, 8>(x, k, v);
+      float sum = 0.0f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        v[j] = __half2float(__float2half_rn(v[j] * by0 * by1));
+        sum += v[j];
+      }
+      // lanes of a group (U / 8 neighbours)
+#pragma unroll
+      for (int d = 1; d < U / 8; d *= 2) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
+      uint4 w;
+      w.x = vec::pack2<PGG_F16>(v[0], v[4]);
+      w.y = vec::pack2<PGG_F16>(v[1] * 0.0625f, v[5] * 0.0625f);
+      w.z = vec::pack2<PGG_F16>(v[2], v[6]);
+      w.w = vec::pack2<PGG_F16>(v[3] * 0.0625f, v[7] * 0.0625f);
+      const int64_t ks = k / kStep;
+      const int in = static_cast<int>(k - ks * kStep) / 8;  // eight of the stage
+      const int unit = in / (U / 8), rest = in % (U / 8), q = rest / (U / 32);
+      const int slot = unit * (U / 32) + rest % (U / 32);  // of 32 k
+      char* stage = out + ks * C::kXBytes;
+      *reinterpret_cast<uint4*>(stage + ((n >> 3) * 8 + slot) * 512 + (((n & 7) * 4 + q) << 4)) = w;
+      if (rest == 0)
+        reinterpret_cast<float*>(stage + C::kRows * kStep * 2)[unit * C::kRows + n] =
+            sum * 0x1p-24f;
+    }
+  }
+}
+
+// ------------------------------------------------------------------ the copying warp
+
 // `bytes` (a multiple of 16) from global to shared memory, both 16-byte aligned.
 __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes,
                                           uint64_t* bar) {
@@ -118,11 +217,36 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
       : "memory");
 }
 
-template <int NT, int U, bool ZEROS>
-__device__ void producer(uint8_t* smem, Ctl* ctl, const CUtensorMap* tm, const W4Args& a,
-                              const Walk& k) {
-  using C = Cfg<NT, U, ZEROS>;
+// Completion of this thread's cp.async so far arrives at `bar`.
+__device__ __forceinline__ void arrive_when_copied(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(ptx::smem_addr(bar))
+               : "memory");
+}
+
+template <int B>
+__device__ __forceinline__ void cp_async(uint32_t dst, const void* src) {
+  if constexpr (B == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(B) : "memory");
+}
+
+// Codes by TMA, x as one piece, the columns' scales and zeros as they stand in memory: by cp.async
+// where a stage's scales of a column are one aligned piece, else one by one.
+template <int NT, int U>
+__device__ void copier(uint8_t* smem, Ctl* ctl, const CUtensorMap* tm, const W4Args& a,
+                       const Walk& k) {
+  using C = Cfg<NT, U>;
+  constexpr int kS = C::kStageUnits;
   volatile int* abort = &ctl->abort;
+  const int lane = threadIdx.x & 31;
+  const bool gated = a.product == PGG_W4_GATED;
+  const int64_t columns = gated ? 2 * a.N : a.N;
+  const int es = a.scale_f32 ? 4 : 2;
+  const uint32_t groups = static_cast<uint32_t>(a.groups);
+  constexpr int kPiece2 = kS * 2 < 16 ? kS * 2 : 16, kPiece4 = kS * 4 < 16 ? kS * 4 : 16;
+  const bool whole = a.group == U && groups % kS == 0 &&
+                     reinterpret_cast<uintptr_t>(a.scales) % (es == 4 ? kPiece4 : kPiece2) == 0;
   int stage = 0;
   uint32_t phase = 0, outstanding = 0, last_parity = 0;
   bool failed = false;
@@ -130,43 +254,107 @@ __device__ void producer(uint8_t* smem, Ctl* ctl, const CUtensorMap* tm, const W
     const uint32_t t = static_cast<uint32_t>(s / k.nks);
     int ks = static_cast<int>(s - static_cast<int64_t>(t) * k.nks);
     const Tile x = tile_of<C::kRows>(t, a);
-    const bool gated = a.product == PGG_W4_GATED;
     const int32_t c0 = static_cast<int32_t>(x.n0);
     const int32_t c1 = static_cast<int32_t>(x.n0 + (gated ? a.N : 64));
     const bool second = gated || x.n0 + 64 < a.N;
     const char* xp = static_cast<const char*>(a.packed) +
                      static_cast<int64_t>(x.rb) * k.nks * C::kXBytes;
+    int64_t at[4];  // first scale of columns lane + 32 i (one that is not there: any)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int64_t c = column_of(a, x, lane + 32 * i);
+      at[i] = (x.g * columns + (c < 0 ? 0 : c)) * a.groups;
+    }
     for (; ks < k.nks && s < k.end; ++ks, ++s) {
-      if (!ptx::mbar_wait(&ctl->empty[stage], phase ^ 1u, a.wait_limit_ns, abort)) {
+      const uint32_t unit = static_cast<uint32_t>(ks) * kS;
+      uint32_t z[4] = {};  // (up to four bytes each; loaded before the wait)
+      if (a.zeros && kS <= 4) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int u = 0; u < kS; ++u) {
+            uint32_t group = unit + u;
+            if (a.group != U) group = group * U / static_cast<uint32_t>(a.group);
+            if (group < groups) z[i] |= static_cast<uint32_t>(__ldg(a.zeros + at[i] + group)) << (8 * u);
+          }
+      }
+      if (!__all_sync(0xFFFFFFFFu, ptx::mbar_wait(&ctl->empty[stage], phase ^ 1u, a.wait_limit_ns,
+                                                  abort))) {
         failed = true;
         break;
       }
       uint8_t* p = smem + stage * C::kStageBytes;
-      // (panels behind the last column or code bring nothing or zeros; x is zero there)
-      ptx::mbar_arrive_expect_tx(&ctl->full[stage],
-                                 (second ? C::kCodeBytes : C::kCodeBytes / 2) + C::kXBytes);
-#pragma unroll
-      for (int j = 0; j < C::kParts / 2; ++j) {
-        const int32_t c = (ks * (C::kParts / 2) + j) * 64;
-        ptx::tma_load_3d(p + j * kPanelBytes, tm, &ctl->full[stage], c, c0,
-                         static_cast<int32_t>(x.g));
+      uint64_t* full = &ctl->full[stage];
+      if (lane == 0) {
+        ptx::mbar_arrive_expect_tx(full, (second ? kCodeBytes : kCodeBytes / 2) + C::kXBytes);
+        ptx::tma_load_3d(p, tm, full, ks * (kStep / 4), c0, static_cast<int32_t>(x.g));
         if (second)
-          ptx::tma_load_3d(p + j * kPanelBytes + kPanelBytes / 2, tm, &ctl->full[stage], c, c1,
+          ptx::tma_load_3d(p + kCodeBytes / 2, tm, full, ks * (kStep / 4), c1,
                            static_cast<int32_t>(x.g));
+        bulk_load(p + kCodeBytes, xp + static_cast<int64_t>(ks) * C::kXBytes, C::kXBytes, full);
       }
-      bulk_load(p + C::kCodeBytes, xp + static_cast<int64_t>(ks) * C::kXBytes, C::kXBytes,
-                &ctl->full[stage]);
       outstanding |= 1u << stage;
       last_parity = (last_parity & ~(1u << stage)) | (phase << stage);
+      uint8_t* sc = p + kCodeBytes + C::kXBytes;
+      uint8_t* zs = sc + C::kScaleBytes;
+      if (whole && unit < groups) {  // (groups end with a stage, so all of its are there)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const char* src = static_cast<const char*>(a.scales) + (at[i] + unit) * es;
+          const uint32_t dst = ptx::smem_addr(sc) + (lane + 32 * i) * kS * es;
+          if (a.scale_f32) {
+            cp_async<kPiece4>(dst, src);
+            if (kS == 8) cp_async<16>(dst + 16, src + 16);
+          } else {
+            cp_async<kPiece2>(dst, src);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int u = 0; u < kS; ++u) {
+            uint32_t group = unit + u;
+            if (a.group != U) group = group * U / static_cast<uint32_t>(a.group);
+            const bool in = group < groups;  // (x is 0 behind, but 0 inf is not)
+            const int to = (lane + 32 * i) * kS + u;
+            if (a.scale_f32)
+              reinterpret_cast<uint32_t*>(sc)[to] =
+                  in ? __ldg(static_cast<const uint32_t*>(a.scales) + at[i] + group) : 0;
+            else
+              reinterpret_cast<uint16_t*>(sc)[to] =
+                  in ? __ldg(static_cast<const uint16_t*>(a.scales) + at[i] + group) : 0;
+          }
+      }
+      if (a.zeros) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if constexpr (kS == 2) {
+            reinterpret_cast<uint16_t*>(zs)[lane + 32 * i] = static_cast<uint16_t>(z[i]);
+          } else if constexpr (kS == 4) {
+            reinterpret_cast<uint32_t*>(zs)[lane + 32 * i] = z[i];
+          } else {
+#pragma unroll
+            for (int u = 0; u < kS; ++u) {
+              uint32_t group = unit + u;
+              if (a.group != U) group = group * U / static_cast<uint32_t>(a.group);
+              zs[(lane + 32 * i) * kS + u] = group < groups ? __ldg(a.zeros + at[i] + group) : 0;
+            }
+          }
+        }
+      }
+      arrive_when_copied(full);
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(full);
       if (++stage == C::kStages) {
         stage = 0;
         phase ^= 1u;
       }
     }
   }
-  if (failed) {
+  if (failed && lane == 0) {
     ctl->abort = 1;
-    raise_status(a.hdr, kStTimeout, 172);
+    raise_status(a.hdr, kStTimeout, 175);
   }
   // the copies in flight land before the CTA ends
   int no_abort = 0;
@@ -175,85 +363,19 @@ __device__ void producer(uint8_t* smem, Ctl* ctl, const CUtensorMap* tm, const W
       ptx::mbar_wait(&ctl->full[i], (last_parity >> i) & 1u, a.wait_limit_ns, &no_abort);
 }
 
-// Where the eight values of x at k = 8 v of a stage, row n, stand: in the order in which the
-// product's lanes read them, 16 bytes each.
-template <int PARTS, int U>
-__device__ __forceinline__ int x_place(int n, int v) {
-  const int unit = v / (U / 8), rest = v % (U / 8), q = rest / (U / 32), i = rest % (U / 32);
-  const int slot = unit * (U / 32) + i;  // of 32 k
-  return ((n >> 3) * (4 * PARTS) + slot) * 512 + (((n & 7) * 4 + q) << 4);
-}
+// ------------------------------------------------------------------ the multiplying warps
 
-// (x0 x1)(x2 x3)(x4 x5)(x6 x7) -> (x0 x4)(x1 x5)(x2 x6)(x3 x7)
-__device__ __forceinline__ uint4 pair_up(const uint4& x) {
-  return make_uint4(__byte_perm(x.x, x.z, 0x5410), __byte_perm(x.x, x.z, 0x7632),
-                    __byte_perm(x.y, x.w, 0x5410), __byte_perm(x.y, x.w, 0x7632));
-}
-
-// The rows of x of every row block, gathered and in the products' order. A warp takes eight rows of
-// a block and 32 of k: every 16 bytes of a lane are one of its 512 neighbouring bytes.
-template <int NT, int U, bool ZEROS>
-__global__ void __launch_bounds__(256) w4_pack_kernel(const W4Args a) {
-  using C = Cfg<NT, U, ZEROS>;
-  ptx::griddep_wait();
-  if (routing_failed(a.hdr)) return;
-  const int lane = threadIdx.x & 31;
-  const uint32_t K = static_cast<uint32_t>(a.K);
-  const uint32_t nks = (K + C::kStep - 1) / C::kStep;
-  constexpr uint32_t kSlots = 4 * C::kParts * NT;  // of 512 bytes, a stage
-  const uint64_t total = static_cast<uint64_t>(a.hdr->n_row_blocks) * nks * kSlots;
-  const uint64_t step = static_cast<uint64_t>(gridDim.x) * 8;
-  for (uint64_t i = blockIdx.x * 8ull + (threadIdx.x >> 5); i < total; i += step) {
-    const uint64_t stage = i / kSlots;
-    const uint32_t in_stage = static_cast<uint32_t>(i - stage * kSlots);
-    const uint32_t rb = static_cast<uint32_t>(stage / nks);
-    const uint32_t ks = static_cast<uint32_t>(stage - static_cast<uint64_t>(rb) * nks);
-    const uint32_t slot = in_stage % (4 * C::kParts);
-    const int n = 8 * static_cast<int>(in_stage / (4 * C::kParts)) + (lane >> 2);
-    const int4 e = a.rblist[rb];
-    if (n >= e.z) continue;  // (what stands there reaches no row that is looked at)
-    // the inverse of x_place: this lane's eight values of k
-    const uint32_t unit = slot / (U / 32), w = slot % (U / 32);
-    const uint32_t k = ks * C::kStep + unit * U + (lane & 3) * (U / 4) + w * 8;
-    const int64_t row = check_index(a.hdr, static_cast<int64_t>(e.y) + n, a.M, 173);
-    const int64_t xrow = a.product == PGG_W4_COMBINED
-                             ? row
-                             : check_index(a.hdr, a.rowinfo[row].token, a.batch, 174);
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (k < K)
-      v = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.x) + xrow * a.K + k));
-    *reinterpret_cast<uint4*>(static_cast<char*>(a.packed) + i * 512 + lane * 16) = pair_up(v);
-  }
-}
-
-template <int DT>
+// d = a b, or d += a b.
+template <bool FIRST>
 __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                     uint32_t a3, uint32_t b0, uint32_t b1) {
-  if constexpr (DT == PGG_BF16)
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3},"
-        " {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-  else
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3},"
-        " {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-// Codes j and 4 + j of a word, less the zero (`z` is the pair 2^7 + zero, or 2^10 + zero; `magic` the
-// pair 2^7 or 2^10, from a register: an instruction holds one of the two constants only).
-template <int DT>
-__device__ __forceinline__ uint32_t unpack(uint32_t w, int j, uint32_t magic, uint32_t z) {
-  uint32_t v, r;
-  asm("lop3.b32 %0, %1, 0x000F000F, %2, 0xEA;" : "=r"(v) : "r"(w >> (4 * j)), "r"(magic));
-  if constexpr (DT == PGG_BF16)
-    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(z));
-  else
-    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(z));
-  return r;
+  const float c0 = FIRST ? 0.0f : d[0], c1 = FIRST ? 0.0f : d[1], c2 = FIRST ? 0.0f : d[2],
+              c3 = FIRST ? 0.0f : d[3];
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3},"
+      " {%4, %5, %6, %7}, {%8, %9}, {%10, %11, %12, %13};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
 }
 
 template <int W>
@@ -280,34 +402,37 @@ __device__ __forceinline__ Words<W> load_words(uint32_t addr) {
   return r;
 }
 
-// A sum over the stage's parts of k, of which each two have been added already.
-template <int PARTS, int STRIDE>
-__device__ __forceinline__ float sum_parts(const float* p) {
-  return PARTS == 4 ? p[0] + p[STRIDE] : p[0];
+__device__ __forceinline__ uint32_t load_half(uint32_t addr) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr) : "memory");
+  return v;
 }
 
-// The tile's results from `red` [row][column].
-template <int DT, int NT>
+__device__ __forceinline__ uint32_t load_byte(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+// Results of the tile from `red` [row][column], which lack the rows' powers of two and 2^24.
+template <int NT>
 __device__ __forceinline__ void write_tile(const float* red, const W4Args& a, const Tile& x,
                                            int thread) {
-  using C = Cfg<NT, 128, false>;
-  constexpr int kThr = C::kMmaWarps * 32;
-  auto at_red = [&](int j, int c) {
-    return sum_parts<C::kParts, C::kRedFloats>(red + j * kRedStride + c);
-  };
   const bool gated = a.product == PGG_W4_GATED;
   const int half = gated ? 32 : 64;  // pairs of a row
-  for (int i = thread; i < x.rows * half; i += kThr) {
+  for (int i = thread; i < x.rows * half; i += 32 * kMmaWarps) {
     const int j = i / half, c = 2 * (i - j * half);
     const int64_t n = x.n0 + c;
     if (n >= a.N) continue;
     const int64_t row = x.row0 + j;
     const int64_t pos = check_index(a.hdr, a.rowinfo[row].rank, a.M, 176);
-    float v0 = at_red(j, c), v1 = at_red(j, c + 1);
+    const int e = a.exponent[static_cast<int64_t>(x.rb) * (8 * NT) + j] + 24;
+    const float* r = red + j * kRedStride + c;
+    float v0 = ldexpf(r[0], e), v1 = ldexpf(r[1], e);
     if (gated) {
       const float p = a.probs ? a.probs[pos] : 1.0f;
-      v0 = gate(v0, at_red(j, 64 + c), p);
-      v1 = gate(v1, at_red(j, 65 + c), p);
+      v0 = gate(v0, ldexpf(r[64], e), p);
+      v1 = gate(v1, ldexpf(r[65], e), p);
     }
     const int64_t at = (a.product == PGG_W4_COMBINED ? pos : row) * a.N + n;
     if (a.out_f32) {
@@ -320,7 +445,7 @@ __device__ __forceinline__ void write_tile(const float* red, const W4Args& a, co
       }
     } else {
       uint16_t* o = static_cast<uint16_t*>(a.out) + at;
-      const uint32_t p = pack2<DT>(v0, v1);
+      const uint32_t p = a.bf16 ? pack2<PGG_BF16>(v0, v1) : pack2<PGG_F16>(v0, v1);
       if (a.pairs) {
         *reinterpret_cast<uint32_t*>(o) = p;
       } else {
@@ -331,42 +456,12 @@ __device__ __forceinline__ void write_tile(const float* red, const W4Args& a, co
   }
 }
 
-// Scales (and zeros) of this lane's column for one step, a part of the k.
-template <int DT, int NT, int U, bool ZEROS>
-struct Scales {
-  using C = Cfg<NT, U, ZEROS>;
-  uint32_t s[C::kUnits];  // as they stand in memory: what converts them would wait for them
-  uint32_t z[ZEROS ? C::kUnits : 1];
-
-  // `at`: the column's first scale or -1;  unit: the first of the step's units of U
-  __device__ __forceinline__ void load(const W4Args& a, int64_t at, uint32_t unit) {
-#pragma unroll
-    for (int u = 0; u < C::kUnits; ++u) {
-      uint32_t group = unit + u;
-      if (a.group != U) group = group * U / static_cast<uint32_t>(a.group);
-      s[u] = 0;
-      if (ZEROS) z[u] = 0;
-      if (at < 0 || group >= static_cast<uint32_t>(a.groups)) continue;
-      if (a.scale_f32)
-        s[u] = __ldg(static_cast<const uint32_t*>(a.scales) + at + group);
-      else
-        s[u] = __ldg(static_cast<const uint16_t*>(a.scales) + at + group);
-      if (ZEROS) z[u] = __ldg(a.zeros + at + group);
-    }
-  }
-  __device__ __forceinline__ float scale(const W4Args& a, int u) const {
-    if (a.scale_f32) return __uint_as_float(s[u]);
-    if (DT == PGG_BF16) return __uint_as_float(s[u] << 16);
-    return __half2float(__ushort_as_half(static_cast<uint16_t>(s[u])));
-  }
-};
-
-template <int DT, int NT, int U, bool ZEROS>
+template <int NT, int U>
 __device__ void multiplier(uint8_t* smem, Ctl* ctl, float* red, int w, const W4Args& a,
                            const Walk& k) {
-  using C = Cfg<NT, U, ZEROS>;
+  using C = Cfg<NT, U>;
   constexpr int W = U / 32;  // words of a lane and unit
-  constexpr int kThr = 32 * C::kMmaWarps;
+  constexpr int kThr = 32 * kMmaWarps;
   volatile int* abort = &ctl->abort;
   const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
   const int col0 = 32 * (w & 3), part = w >> 2;
@@ -374,14 +469,11 @@ __device__ void multiplier(uint8_t* smem, Ctl* ctl, float* red, int w, const W4A
   // (two g) lie in different halves of the swizzled 128 bytes
   const int perm = (g >> 1) + 4 * (g & 1);
   const int thread = 32 * w + lane;
-  // bf16: 2^7 + z is 0x4300 | z, fp16: 2^10 + z is 0x6400 | z
-  constexpr uint32_t kMagic = DT == PGG_BF16 ? 0x43004300u : 0x64006400u;
-  const int64_t columns = a.product == PGG_W4_GATED ? 2 * a.N : a.N;
-  const uint32_t my_codes =
-      ptx::smem_addr(smem) + (part >> 1) * kPanelBytes + (col0 + perm) * 128;
-  const uint32_t my_x = ptx::smem_addr(smem) + C::kCodeBytes + part * 4 * 512 + lane * 16;
-  uint32_t magic;
-  asm volatile("mov.u32 %0, %1;" : "=r"(magic) : "n"(kMagic));
+  const bool f32 = a.scale_f32 != 0, zeros = a.zeros != nullptr, bf16 = a.bf16 != 0;
+  const uint32_t my_codes = ptx::smem_addr(smem) + (col0 + perm) * 128;
+  const uint32_t my_x = ptx::smem_addr(smem) + kCodeBytes + part * 4 * 512 + lane * 16;
+  const uint32_t my_sums =
+      ptx::smem_addr(smem) + kCodeBytes + C::kRows * kStep * 2 + part * C::kUnits * C::kRows * 4 + q * 8;
   int stage = 0;
   uint32_t phase = 0;
   bool failed = false;
@@ -391,16 +483,8 @@ __device__ void multiplier(uint8_t* smem, Ctl* ctl, float* red, int w, const W4A
     const int64_t left = k.end - s;
     const int n_steps = left < k.nks - ks0 ? static_cast<int>(left) : k.nks - ks0;
     const Tile x = tile_of<C::kRows>(t, a);
-    const int64_t column = column_of(a, x, col0 + lane);
-    const int64_t at = column < 0 ? -1 : (x.g * columns + column) * a.groups;
     float sum[2][NT][4] = {};
-    Scales<DT, NT, U, ZEROS> now, next;
-    uint32_t unit = static_cast<uint32_t>(ks0 * C::kParts + part) * C::kUnits;
-    next.load(a, at, unit);
     for (int i = 0; i < n_steps; ++i) {
-      now = next;
-      unit += C::kParts * C::kUnits;
-      if (i + 1 < n_steps) next.load(a, at, unit);  // (a step ahead)
       if (!failed && !__all_sync(0xFFFFFFFFu, ptx::mbar_wait(&ctl->full[stage], phase,
                                                              a.wait_limit_ns, abort))) {
         failed = true;
@@ -410,57 +494,84 @@ __device__ void multiplier(uint8_t* smem, Ctl* ctl, float* red, int w, const W4A
         }
       }
       if (failed) break;  // (the warps still meet at every barrier below)
-      const uint32_t codes = my_codes + stage * C::kStageBytes;
-      const uint32_t xs = my_x + stage * C::kStageBytes;
+      const uint32_t base = stage * C::kStageBytes;
+      const uint32_t scales = ptx::smem_addr(smem) + base + kCodeBytes + C::kXBytes;
 #pragma unroll
       for (int u = 0; u < C::kUnits; ++u) {
-        const int byte = (part & 1) * 64 + u * (U / 2) + q * (U / 8);
+        const int byte = part * 64 + u * (U / 2) + q * (U / 8);
         const int in_row = (((byte >> 4) ^ perm) << 4) | (byte & 15);
         Words<W> word[2][2];
 #pragma unroll
         for (int r = 0; r < 2; ++r)
 #pragma unroll
           for (int e = 0; e < 2; ++e)
-            word[r][e] = load_words<W>(codes + (16 * r + 8 * e) * 128 + in_row);
-        uint32_t z[2][2];
-#pragma unroll
-        for (int r = 0; r < 2; ++r)
-#pragma unroll
-          for (int e = 0; e < 2; ++e)
-            z[r][e] = kMagic + (ZEROS ? __shfl_sync(0xFFFFFFFFu, now.z[ZEROS ? u : 0],
-                                                    16 * r + 8 * e + perm) * 0x10001u
-                                      : 0x00080008u);
-        float d[2][NT][4] = {};
+            word[r][e] = load_words<W>(my_codes + base + (16 * r + 8 * e) * 128 + in_row);
+        float d[2][NT][4];
 #pragma unroll
         for (int i8 = 0; i8 < W; ++i8) {
           Words<4> b[NT];
 #pragma unroll
           for (int n = 0; n < NT; ++n)
-            b[n] = load_words<4>(xs + (n * 4 * C::kParts + u * W + i8) * 512);
+            b[n] = load_words<4>(my_x + base + (n * 8 + u * W + i8) * 512);
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
-            uint32_t p[2][4];
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-#pragma unroll
-              for (int j = 0; j < 4; ++j) p[e][j] = unpack<DT>(word[r][e].v[i8], j, magic, z[r][e]);
+            const uint32_t w0 = word[r][0].v[i8], w1 = word[r][1].v[i8];
+            const uint32_t h0 = w0 >> 8, h1 = w1 >> 8;
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-              mma<DT>(d[r][n], p[0][0], p[1][0], p[0][1], p[1][1], b[n].v[0], b[n].v[1]);
-              mma<DT>(d[r][n], p[0][2], p[1][2], p[0][3], p[1][3], b[n].v[2], b[n].v[3]);
+              if (i8 == 0)
+                mma<true>(d[r][n], w0 & 0x000F000Fu, w1 & 0x000F000Fu, w0 & 0x00F000F0u,
+                          w1 & 0x00F000F0u, b[n].v[0], b[n].v[1]);
+              else
+                mma<false>(d[r][n], w0 & 0x000F000Fu, w1 & 0x000F000Fu, w0 & 0x00F000F0u,
+                           w1 & 0x00F000F0u, b[n].v[0], b[n].v[1]);
+              mma<false>(d[r][n], h0 & 0x000F000Fu, h1 & 0x000F000Fu, h0 & 0x00F000F0u,
+                         h1 & 0x00F000F0u, b[n].v[2], b[n].v[3]);
             }
           }
         }
+        float sc[2][2], z[2][2];
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const float s0 = __shfl_sync(0xFFFFFFFFu, now.scale(a, u), 16 * r + perm);
-          const float s1 = __shfl_sync(0xFFFFFFFFu, now.scale(a, u), 16 * r + 8 + perm);
+        for (int r = 0; r < 2; ++r)
 #pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            sum[r][n][0] = fmaf(s0, d[r][n][0], sum[r][n][0]);
-            sum[r][n][1] = fmaf(s0, d[r][n][1], sum[r][n][1]);
-            sum[r][n][2] = fmaf(s1, d[r][n][2], sum[r][n][2]);
-            sum[r][n][3] = fmaf(s1, d[r][n][3], sum[r][n][3]);
+          for (int e = 0; e < 2; ++e) z[r][e] = -8.0f;
+        const int at = (col0 + perm) * C::kStageUnits + part * C::kUnits + u;
+        if (f32) {
+#pragma unroll
+          for (int r = 0; r < 2; ++r)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              sc[r][e] = __uint_as_float(
+                  load_words<1>(scales + (at + (16 * r + 8 * e) * C::kStageUnits) * 4).v[0]);
+        } else {
+#pragma unroll
+          for (int r = 0; r < 2; ++r)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const uint32_t v = load_half(scales + (at + (16 * r + 8 * e) * C::kStageUnits) * 2);
+              sc[r][e] = bf16 ? __uint_as_float(v << 16)
+                              : __half2float(__ushort_as_half(static_cast<uint16_t>(v)));
+            }
+        }
+        if (zeros) {
+#pragma unroll
+          for (int r = 0; r < 2; ++r)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)  // (2^23 + z, without its lowest bits' exponent)
+              z[r][e] = 8388608.0f -
+                        __uint_as_float(0x4B000000u | load_byte(scales + C::kScaleBytes + at +
+                                                                (16 * r + 8 * e) * C::kStageUnits));
+        }
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          const Words<2> xs = load_words<2>(my_sums + base + u * C::kRows * 4 + n * 32);
+          const float x0 = __uint_as_float(xs.v[0]), x1 = __uint_as_float(xs.v[1]);
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            sum[r][n][0] = fmaf(sc[r][0], fmaf(z[r][0], x0, d[r][n][0]), sum[r][n][0]);
+            sum[r][n][1] = fmaf(sc[r][0], fmaf(z[r][0], x1, d[r][n][1]), sum[r][n][1]);
+            sum[r][n][2] = fmaf(sc[r][1], fmaf(z[r][1], x0, d[r][n][2]), sum[r][n][2]);
+            sum[r][n][3] = fmaf(sc[r][1], fmaf(z[r][1], x1, d[r][n][3]), sum[r][n][3]);
           }
         }
       }
@@ -471,20 +582,19 @@ __device__ void multiplier(uint8_t* smem, Ctl* ctl, float* red, int w, const W4A
         phase ^= 1u;
       }
     }
-    // the parts of k into red [row][column], each two one after the other
+    // both parts of k into red [row][column], one after the other
     if (s > k.begin) ptx::named_bar_sync(1, kThr);  // (the tile before is read)
 #pragma unroll
     for (int turn = 0; turn < 2; ++turn) {
-      if ((part & 1) == turn) {
+      if (part == turn) {
 #pragma unroll
         for (int r = 0; r < 2; ++r)
 #pragma unroll
           for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              float* p = red + (part >> 1) * C::kRedFloats +
-                         (8 * n + 2 * q + (e & 1)) * kRedStride + col0 + 16 * r + 8 * (e >> 1) +
-                         perm;
+              float* p = red + (8 * n + 2 * q + (e & 1)) * kRedStride + col0 + 16 * r +
+                         8 * (e >> 1) + perm;
               *p = turn == 0 ? sum[r][n][e] : *p + sum[r][n][e];
             }
       }
@@ -499,7 +609,7 @@ __device__ void multiplier(uint8_t* smem, Ctl* ctl, float* red, int w, const W4A
       constexpr int kShare = C::kRows * kTile;
       float* own = a.parts + (2 * static_cast<int64_t>(blockIdx.x) + (ks0 == 0 ? 1 : 0)) * kShare;
       for (int i = thread; i < x.rows * kTile; i += kThr)
-        own[i] = sum_parts<C::kParts, C::kRedFloats>(red + (i / kTile) * kRedStride + i % kTile);
+        own[i] = red[(i / kTile) * kRedStride + i % kTile];
       __threadfence();
       ptx::named_bar_sync(1, kThr);
       if (thread == 0) {
@@ -514,32 +624,30 @@ __device__ void multiplier(uint8_t* smem, Ctl* ctl, float* red, int w, const W4A
           float v = 0.0f;
           for (int64_t c = first; c <= last; ++c)
             v += __ldcg(a.parts + (2 * c + (c == first ? 1 : 0)) * kShare + i);
-          float* p = red + (i / kTile) * kRedStride + i % kTile;
-          p[0] = v;
-          if (C::kParts == 4) p[C::kRedFloats] = 0.0f;
+          red[(i / kTile) * kRedStride + i % kTile] = v;
         }
         ptx::named_bar_sync(1, kThr);
       }
     }
-    if (mine) write_tile<DT, NT>(red, a, x, thread);
+    if (mine) write_tile<NT>(red, a, x, thread);
     s += n_steps;
   }
 }
 
-template <int DT, int NT, int U, bool ZEROS>
-__global__ void __launch_bounds__(Cfg<NT, U, ZEROS>::kThreads, 1)
+template <int NT, int U>
+__global__ void __launch_bounds__(kThreads, Cfg<NT, U>::kCtas)
     w4_stream_kernel(const __grid_constant__ CUtensorMap tm, const W4Args a) {
-  using C = Cfg<NT, U, ZEROS>;
+  using C = Cfg<NT, U>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   float* red = reinterpret_cast<float*>(smem + C::kStages * C::kStageBytes);
   __shared__ Ctl ctl;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
-      ptx::mbar_init(&ctl.full[s], 1);
-      ptx::mbar_init(&ctl.empty[s], C::kMmaWarps);
+      ptx::mbar_init(&ctl.full[s], 1 + 32 + 1);
+      ptx::mbar_init(&ctl.empty[s], kMmaWarps);
     }
     ctl.abort = 0;
     ptx::fence_mbar_init();
@@ -559,79 +667,66 @@ __global__ void __launch_bounds__(Cfg<NT, U, ZEROS>::kThreads, 1)
     return;
   }
   Walk k;
-  k.nks = static_cast<int>((a.K + C::kStep - 1) / C::kStep);
+  k.nks = static_cast<int>((a.K + kStep - 1) / kStep);
   k.total = static_cast<int64_t>(a.hdr->n_row_blocks) * a.n_blocks * k.nks;
   // at least two steps a CTA, so that each has some
   k.ctas = k.total < 2 * static_cast<int64_t>(gridDim.x) ? (k.total + 1) / 2 : gridDim.x;
   if (static_cast<int64_t>(blockIdx.x) >= k.ctas) return;
   k.begin = static_cast<int64_t>(blockIdx.x) * k.total / k.ctas;
   k.end = (static_cast<int64_t>(blockIdx.x) + 1) * k.total / k.ctas;
-  if (warp == 0) {
-    if (lane == 0) producer<NT, U, ZEROS>(smem, &ctl, &tm, a, k);
-  } else {
-    multiplier<DT, NT, U, ZEROS>(smem, &ctl, red, warp - 1, a, k);
-  }
+  if (warp == 0)
+    copier<NT, U>(smem, &ctl, &tm, a, k);
+  else
+    multiplier<NT, U>(smem, &ctl, red, warp - 1, a, k);
 }
 
-template <int DT, int NT, int U, bool ZEROS>
-cudaError_t launch_t(const CUtensorMap& tm, const W4Args& a, int num_sms, cudaStream_t stream) {
-  using C = Cfg<NT, U, ZEROS>;
-  static_assert(C::kSmem <= 227 * 1024 && C::kStages >= 3, "shared memory");
-  auto kern = w4_stream_kernel<DT, NT, U, ZEROS>;
+template <int NT, int U>
+cudaError_t launch_t(int dtype, const CUtensorMap& tm, const W4Args& a, int num_sms,
+                     cudaStream_t stream) {
+  using C = Cfg<NT, U>;
+  auto kern = w4_stream_kernel<NT, U>;
   static SmemLimit limit;
-  const cudaError_t err = allow_smem(&limit, kern, C::kSmem);
+  cudaError_t err = allow_smem(&limit, kern, C::kSmem);
   if (err != cudaSuccess) return err;
-  const int64_t slots = a.max_row_blocks * ((a.K + C::kStep - 1) / C::kStep) * 4 * C::kParts * NT;
-  int64_t blocks = (slots + 7) / 8;
-  if (blocks > num_sms * 8) blocks = num_sms * 8;
-  const cudaError_t packed = launch_pdl(w4_pack_kernel<NT, U, ZEROS>,
-                                        dim3(static_cast<unsigned>(blocks)), dim3(256), 0, stream,
-                                        1, a);
-  if (packed != cudaSuccess) return packed;
-  return launch_pdl(kern, dim3(static_cast<unsigned>(num_sms < kW4Grid ? num_sms : kW4Grid)),
-                    dim3(C::kThreads), static_cast<size_t>(C::kSmem), stream, 1, tm, a);
+  int64_t blocks = a.max_row_blocks * C::kRows;
+  if (blocks > num_sms * 16) blocks = num_sms * 16;
+  err = launch_pdl(dtype == PGG_BF16 ? w4_pack_kernel<PGG_BF16, NT, U>
+                                     : w4_pack_kernel<PGG_F16, NT, U>,
+                   dim3(static_cast<unsigned>(blocks)), dim3(128), 0, stream, 1, a);
+  if (err != cudaSuccess) return err;
+  const int grid = num_sms * C::kCtas < kW4Grid ? num_sms * C::kCtas : kW4Grid;
+  return launch_pdl(kern, dim3(static_cast<unsigned>(grid)), dim3(kThreads),
+                    static_cast<size_t>(C::kSmem), stream, 1, tm, a);
 }
 
-template <int DT, int NT>
-cudaError_t launch_u(const CUtensorMap& tm, const W4Args& a, int num_sms, cudaStream_t stream) {
-  const bool z = a.zeros != nullptr;
-  if (a.group % 128 == 0)
-    return z ? launch_t<DT, NT, 128, true>(tm, a, num_sms, stream)
-             : launch_t<DT, NT, 128, false>(tm, a, num_sms, stream);
-  if (a.group % 64 == 0)
-    return z ? launch_t<DT, NT, 64, true>(tm, a, num_sms, stream)
-             : launch_t<DT, NT, 64, false>(tm, a, num_sms, stream);
-  return z ? launch_t<DT, NT, 32, true>(tm, a, num_sms, stream)
-           : launch_t<DT, NT, 32, false>(tm, a, num_sms, stream);
-}
-
-template <int DT>
-cudaError_t launch_nt(const CUtensorMap& tm, int rows, const W4Args& a, int num_sms,
-                      cudaStream_t stream) {
-  if (rows == 8) return launch_u<DT, 1>(tm, a, num_sms, stream);
-  if (rows == 16) return launch_u<DT, 2>(tm, a, num_sms, stream);
-  if (rows == 32) return launch_u<DT, 4>(tm, a, num_sms, stream);
-  return cudaErrorInvalidValue;
+template <int NT>
+cudaError_t launch_u(int dtype, const CUtensorMap& tm, const W4Args& a, int num_sms,
+                     cudaStream_t stream) {
+  if (a.group % 128 == 0) return launch_t<NT, 128>(dtype, tm, a, num_sms, stream);
+  if (a.group % 64 == 0) return launch_t<NT, 64>(dtype, tm, a, num_sms, stream);
+  return launch_t<NT, 32>(dtype, tm, a, num_sms, stream);
 }
 
 }  // namespace
 
+// (groups' sums for groups of 32: the most there are)
 int64_t w4_packed_bytes(int64_t row_blocks, int rows_per_block, int64_t K) {
-  const int64_t step = rows_per_block <= 16 ? 4 * kPart : 2 * kPart;
-  return row_blocks * rows_per_block * ((K + step - 1) / step) * step * 2;
+  return row_blocks * rows_per_block * ((K + kStep - 1) / kStep) * (kStep * 2 + kStep / 32 * 4);
 }
 
 cudaError_t launch_w4_stream(int dtype, int rows_per_block, W4Args a, int num_sms,
                              cudaStream_t stream) {
   const int tile = a.product == PGG_W4_GATED ? kTile / 2 : kTile;
   a.n_blocks = static_cast<int32_t>((a.N + tile - 1) / tile);
+  a.bf16 = dtype == PGG_BF16;
   CUtensorMap tm;  // codes as words of 16 bits: boxes of 128 bytes x 64 columns
   std::memset(&tm, 0, sizeof(tm));
   if (!encode_map_3d(&tm, PGG_F16, a.codes, a.row_bytes / 2,
                      a.product == PGG_W4_GATED ? 2 * a.N : a.N, a.G, 64))
     return cudaErrorInvalidValue;
-  if (dtype == PGG_BF16) return launch_nt<PGG_BF16>(tm, rows_per_block, a, num_sms, stream);
-  if (dtype == PGG_F16) return launch_nt<PGG_F16>(tm, rows_per_block, a, num_sms, stream);
+  if (rows_per_block == 8) return launch_u<1>(dtype, tm, a, num_sms, stream);
+  if (rows_per_block == 16) return launch_u<2>(dtype, tm, a, num_sms, stream);
+  if (rows_per_block == 32) return launch_u<4>(dtype, tm, a, num_sms, stream);
   return cudaErrorInvalidValue;
 }
 
