@@ -69,13 +69,17 @@ struct Cfg {
   // a column's scales of a stage (room for fp32), then its zeros
   static constexpr int kScaleBytes = kTile * kStageUnits * 4;
   static constexpr int kZeroBytes = kTile * kStageUnits;
-  static constexpr int kStageBytes =
-      (kCodeBytes + kXBytes + kScaleBytes + kZeroBytes + 1023) / 1024 * 1024;
+  static constexpr int kExtraBytes = (kXBytes + kScaleBytes + kZeroBytes + 127) / 128 * 128;
   static constexpr int kRedBytes = kRows * kRedStride * 4;
-  static constexpr int kFit = (226 * 1024 / kCtas - kRedBytes - 2560) / kStageBytes;
+  // (a block may have 227 KB, an SM 228 KB with 1 KB of each block's kept back)
+  static constexpr int kRoom = kCtas == 2 ? 113 * 1024 : 227 * 1024;
+  static constexpr int kFit = (kRoom - kRedBytes - 1024 - 256) / (kCodeBytes + kExtraBytes);
   static constexpr int kStages = kFit < kMaxStages ? kFit : kMaxStages;
-  static constexpr int kSmem = kStages * kStageBytes + kRedBytes + 1024;
-  static_assert(kSmem * kCtas <= 225 * 1024 && kStages >= 3, "shared memory");
+  // codes of all stages (in pieces of 1 KB), then what else they have, then the tile's sums
+  static constexpr int kExtra = kStages * kCodeBytes;
+  static constexpr int kRed = kExtra + kStages * kExtraBytes;
+  static constexpr int kSmem = kRed + kRedBytes + 1024;
+  static_assert(kStages >= 3, "shared memory");
 };
 
 struct Ctl {
@@ -245,6 +249,9 @@ __device__ void copier(uint8_t* smem, Ctl* ctl, const CUtensorMap* tm, const W4A
   const int es = a.scale_f32 ? 4 : 2;
   const uint32_t groups = static_cast<uint32_t>(a.groups);
   constexpr int kPiece2 = kS * 2 < 16 ? kS * 2 : 16, kPiece4 = kS * 4 < 16 ? kS * 4 : 16;
+  // the same of zeros, for a load of one to eight bytes
+  const bool whole_z = a.group == U && groups % kS == 0 &&
+                       reinterpret_cast<uintptr_t>(a.zeros) % kS == 0;
   const bool whole = a.group == U && groups % kS == 0 &&
                      reinterpret_cast<uintptr_t>(a.scales) % (es == 4 ? kPiece4 : kPiece2) == 0;
   int stage = 0;
@@ -267,23 +274,33 @@ __device__ void copier(uint8_t* smem, Ctl* ctl, const CUtensorMap* tm, const W4A
     }
     for (; ks < k.nks && s < k.end; ++ks, ++s) {
       const uint32_t unit = static_cast<uint32_t>(ks) * kS;
-      uint32_t z[4] = {};  // (up to four bytes each; loaded before the wait)
-      if (a.zeros && kS <= 4) {
+      uint64_t z[4] = {};  // (loaded before the wait: they need no room yet)
+      if (a.zeros && unit * U < static_cast<uint64_t>(a.K)) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < 4; ++i) {
+          const uint8_t* p = a.zeros + at[i] + unit;
+          if (whole_z) {
+            if constexpr (kS == 2) z[i] = __ldg(reinterpret_cast<const uint16_t*>(p));
+            if constexpr (kS == 4) z[i] = __ldg(reinterpret_cast<const uint32_t*>(p));
+            if constexpr (kS == 8) z[i] = __ldg(reinterpret_cast<const unsigned long long*>(p));
+          } else {
 #pragma unroll
-          for (int u = 0; u < kS; ++u) {
-            uint32_t group = unit + u;
-            if (a.group != U) group = group * U / static_cast<uint32_t>(a.group);
-            if (group < groups) z[i] |= static_cast<uint32_t>(__ldg(a.zeros + at[i] + group)) << (8 * u);
+            for (int u = 0; u < kS; ++u) {
+              uint32_t group = unit + u;
+              if (a.group != U) group = group * U / static_cast<uint32_t>(a.group);
+              if (group < groups)
+                z[i] |= static_cast<uint64_t>(__ldg(a.zeros + at[i] + group)) << (8 * u);
+            }
           }
+        }
       }
       if (!__all_sync(0xFFFFFFFFu, ptx::mbar_wait(&ctl->empty[stage], phase ^ 1u, a.wait_limit_ns,
                                                   abort))) {
         failed = true;
         break;
       }
-      uint8_t* p = smem + stage * C::kStageBytes;
+      uint8_t* p = smem + stage * kCodeBytes;
+      uint8_t* px = smem + C::kExtra + stage * C::kExtraBytes;
       uint64_t* full = &ctl->full[stage];
       if (lane == 0) {
         ptx::mbar_arrive_expect_tx(full, (second ? kCodeBytes : kCodeBytes / 2) + C::kXBytes);
@@ -291,11 +308,11 @@ __device__ void copier(uint8_t* smem, Ctl* ctl, const CUtensorMap* tm, const W4A
         if (second)
           ptx::tma_load_3d(p + kCodeBytes / 2, tm, full, ks * (kStep / 4), c1,
                            static_cast<int32_t>(x.g));
-        bulk_load(p + kCodeBytes, xp + static_cast<int64_t>(ks) * C::kXBytes, C::kXBytes, full);
+        bulk_load(px, xp + static_cast<int64_t>(ks) * C::kXBytes, C::kXBytes, full);
       }
       outstanding |= 1u << stage;
       last_parity = (last_parity & ~(1u << stage)) | (phase << stage);
-      uint8_t* sc = p + kCodeBytes + C::kXBytes;
+      uint8_t* sc = px + C::kXBytes;
       uint8_t* zs = sc + C::kScaleBytes;
       if (whole && unit < groups) {  // (groups end with a stage, so all of its are there)
 #pragma unroll
@@ -329,18 +346,11 @@ __device__ void copier(uint8_t* smem, Ctl* ctl, const CUtensorMap* tm, const W4A
       if (a.zeros) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          if constexpr (kS == 2) {
+          if constexpr (kS == 2)
             reinterpret_cast<uint16_t*>(zs)[lane + 32 * i] = static_cast<uint16_t>(z[i]);
-          } else if constexpr (kS == 4) {
-            reinterpret_cast<uint32_t*>(zs)[lane + 32 * i] = z[i];
-          } else {
-#pragma unroll
-            for (int u = 0; u < kS; ++u) {
-              uint32_t group = unit + u;
-              if (a.group != U) group = group * U / static_cast<uint32_t>(a.group);
-              zs[(lane + 32 * i) * kS + u] = group < groups ? __ldg(a.zeros + at[i] + group) : 0;
-            }
-          }
+          if constexpr (kS == 4)
+            reinterpret_cast<uint32_t*>(zs)[lane + 32 * i] = static_cast<uint32_t>(z[i]);
+          if constexpr (kS == 8) reinterpret_cast<uint64_t*>(zs)[lane + 32 * i] = z[i];
         }
       }
       arrive_when_copied(full);
@@ -371,7 +381,7 @@ __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uin
                                     uint32_t a3, uint32_t b0, uint32_t b1) {
   const float c0 = FIRST ? 0.0f : d[0], c1 = FIRST ? 0.0f : d[1], c2 = FIRST ? 0.0f : d[2],
               c3 = FIRST ? 0.0f : d[3];
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3},"
       " {%4, %5, %6, %7}, {%8, %9}, {%10, %11, %12, %13};"
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
@@ -471,9 +481,9 @@ __device__ void multiplier(uint8_t* smem, Ctl* ctl, float* red, int w, const W4A
   const int thread = 32 * w + lane;
   const bool f32 = a.scale_f32 != 0, zeros = a.zeros != nullptr, bf16 = a.bf16 != 0;
   const uint32_t my_codes = ptx::smem_addr(smem) + (col0 + perm) * 128;
-  const uint32_t my_x = ptx::smem_addr(smem) + kCodeBytes + part * 4 * 512 + lane * 16;
-  const uint32_t my_sums =
-      ptx::smem_addr(smem) + kCodeBytes + C::kRows * kStep * 2 + part * C::kUnits * C::kRows * 4 + q * 8;
+  const uint32_t my_x = ptx::smem_addr(smem) + C::kExtra + part * 4 * 512 + lane * 16;
+  const uint32_t my_sums = ptx::smem_addr(smem) + C::kExtra + C::kRows * kStep * 2 +
+                           part * C::kUnits * C::kRows * 4 + q * 8;
   int stage = 0;
   uint32_t phase = 0;
   bool failed = false;
@@ -494,8 +504,8 @@ __device__ void multiplier(uint8_t* smem, Ctl* ctl, float* red, int w, const W4A
         }
       }
       if (failed) break;  // (the warps still meet at every barrier below)
-      const uint32_t base = stage * C::kStageBytes;
-      const uint32_t scales = ptx::smem_addr(smem) + base + kCodeBytes + C::kXBytes;
+      const uint32_t codes = my_codes + stage * kCodeBytes, extra = stage * C::kExtraBytes;
+      const uint32_t scales = ptx::smem_addr(smem) + C::kExtra + extra + C::kXBytes;
 #pragma unroll
       for (int u = 0; u < C::kUnits; ++u) {
         const int byte = part * 64 + u * (U / 2) + q * (U / 8);
@@ -505,30 +515,37 @@ __device__ void multiplier(uint8_t* smem, Ctl* ctl, float* red, int w, const W4A
         for (int r = 0; r < 2; ++r)
 #pragma unroll
           for (int e = 0; e < 2; ++e)
-            word[r][e] = load_words<W>(my_codes + base + (16 * r + 8 * e) * 128 + in_row);
-        float d[2][NT][4];
+            word[r][e] = load_words<W>(codes + (16 * r + 8 * e) * 128 + in_row);
+        // products that add to the same sums are at least four apart: one waits for the other
+        constexpr int kSums = NT == 1 ? 2 : 1;
+        float d[kSums][2][NT][4];
 #pragma unroll
         for (int i8 = 0; i8 < W; ++i8) {
           Words<4> b[NT];
 #pragma unroll
           for (int n = 0; n < NT; ++n)
-            b[n] = load_words<4>(my_x + base + (n * 8 + u * W + i8) * 512);
+            b[n] = load_words<4>(my_x + extra + (n * 8 + u * W + i8) * 512);
 #pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            const uint32_t w0 = word[r][0].v[i8], w1 = word[r][1].v[i8];
-            const uint32_t h0 = w0 >> 8, h1 = w1 >> 8;
+          for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-              if (i8 == 0)
-                mma<true>(d[r][n], w0 & 0x000F000Fu, w1 & 0x000F000Fu, w0 & 0x00F000F0u,
-                          w1 & 0x00F000F0u, b[n].v[0], b[n].v[1]);
-              else
-                mma<false>(d[r][n], w0 & 0x000F000Fu, w1 & 0x000F000Fu, w0 & 0x00F000F0u,
-                           w1 & 0x00F000F0u, b[n].v[0], b[n].v[1]);
-              mma<false>(d[r][n], h0 & 0x000F000Fu, h1 & 0x000F000Fu, h0 & 0x00F000F0u,
-                         h1 & 0x00F000F0u, b[n].v[2], b[n].v[3]);
+            for (int r = 0; r < 2; ++r) {
+              const uint32_t w0 = word[r][0].v[i8] >> (8 * h), w1 = word[r][1].v[i8] >> (8 * h);
+#pragma unroll
+              for (int n = 0; n < NT; ++n) {
+                if (i8 == 0 && h < kSums)
+                  mma<true>(d[h % kSums][r][n], w0 & 0x000F000Fu, w1 & 0x000F000Fu,
+                            w0 & 0x00F000F0u, w1 & 0x00F000F0u, b[n].v[2 * h], b[n].v[2 * h + 1]);
+                else
+                  mma<false>(d[h % kSums][r][n], w0 & 0x000F000Fu, w1 & 0x000F000Fu,
+                             w0 & 0x00F000F0u, w1 & 0x00F000F0u, b[n].v[2 * h], b[n].v[2 * h + 1]);
+              }
             }
-          }
+        }
+        if constexpr (kSums == 2) {
+#pragma unroll
+          for (int r = 0; r < 2; ++r)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) d[0][r][0][e] += d[1][r][0][e];
         }
         float sc[2][2], z[2][2];
 #pragma unroll
@@ -564,14 +581,14 @@ __device__ void multiplier(uint8_t* smem, Ctl* ctl, float* red, int w, const W4A
         }
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-          const Words<2> xs = load_words<2>(my_sums + base + u * C::kRows * 4 + n * 32);
+          const Words<2> xs = load_words<2>(my_sums + extra + u * C::kRows * 4 + n * 32);
           const float x0 = __uint_as_float(xs.v[0]), x1 = __uint_as_float(xs.v[1]);
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
-            sum[r][n][0] = fmaf(sc[r][0], fmaf(z[r][0], x0, d[r][n][0]), sum[r][n][0]);
-            sum[r][n][1] = fmaf(sc[r][0], fmaf(z[r][0], x1, d[r][n][1]), sum[r][n][1]);
-            sum[r][n][2] = fmaf(sc[r][1], fmaf(z[r][1], x0, d[r][n][2]), sum[r][n][2]);
-            sum[r][n][3] = fmaf(sc[r][1], fmaf(z[r][1], x1, d[r][n][3]), sum[r][n][3]);
+            sum[r][n][0] = fmaf(sc[r][0], fmaf(z[r][0], x0, d[0][r][n][0]), sum[r][n][0]);
+            sum[r][n][1] = fmaf(sc[r][0], fmaf(z[r][0], x1, d[0][r][n][1]), sum[r][n][1]);
+            sum[r][n][2] = fmaf(sc[r][1], fmaf(z[r][1], x0, d[0][r][n][2]), sum[r][n][2]);
+            sum[r][n][3] = fmaf(sc[r][1], fmaf(z[r][1], x1, d[0][r][n][3]), sum[r][n][3]);
           }
         }
       }
@@ -641,7 +658,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<NT, U>::kCtas)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
-  float* red = reinterpret_cast<float*>(smem + C::kStages * C::kStageBytes);
+  float* red = reinterpret_cast<float*>(smem + C::kRed);
   __shared__ Ctl ctl;
   const int warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) {
