@@ -5,6 +5,7 @@
 #include <cmath>
 #include <cstdint>
 #include <cstring>
+#include <initializer_list>
 
 #include <cuda_runtime.h>
 
@@ -109,6 +110,27 @@ int check_norm(const void* y, const void* gate, const void* post_weight, const v
   return PGG_OK;
 }
 
+// How the rows of a call can be read: vectors of 16 bytes of the dtype, pairs of 16-bit elements, or
+// (0) one by one. A vector of another dtype's tensor is 16-byte aligned, or to its own size.
+struct Tensor {
+  const void* p;
+  int dtype;
+};
+int row_words(int64_t H, int dtype, std::initializer_list<const void*> own,
+              std::initializer_list<Tensor> others) {
+  for (const int words : {16, 4}) {
+    const uintptr_t elems = words / elem_size(dtype);
+    bool ok = elems > 1 && H % static_cast<int64_t>(elems) == 0;
+    for (const void* p : own) ok = ok && aligned(p, words);
+    for (const Tensor& t : others) {
+      const uintptr_t bytes = elems * elem_size(t.dtype);
+      ok = ok && aligned(t.p, bytes < 16 ? bytes : 16);
+    }
+    if (ok) return words;
+  }
+  return 0;
+}
+
 NormArgs norm_args(const void* x, const void* y, const void* gate, const void* post_weight,
                    const void* post_bias, const void* pre_weight, const void* pre_bias, int64_t T,
                    int64_t H, int y_dtype, int param_dtype, int post, int pre, int gate_kind,
@@ -164,7 +186,7 @@ int check_clip(int64_t count, const void* const* grads, const int64_t* sizes,
     if (!aligned(grads[i], elem_size(dtypes[i])) ||
         (clip && !aligned(out[i], elem_size(dtypes[i]))))
       return PGG_ERR_ALIGN;
-    chunks += clip_chunks(sizes[i]);
+    chunks += clip_chunks(sizes[i], dtypes[i]);
     if (chunks > kInt32Max) return PGG_ERR_SHAPE;  // 32-bit chunk numbers
   }
   return PGG_OK;
@@ -182,7 +204,7 @@ int fill_table(ClipTable* t, int64_t begin, int64_t count, const void* const* gr
     t->n[i] = sizes[begin + i];
     t->dtype[i] = static_cast<uint8_t>(dtypes[begin + i]);
     t->first[i] = chunks;
-    chunks += static_cast<uint32_t>(clip_chunks(sizes[begin + i]));
+    chunks += static_cast<uint32_t>(clip_chunks(sizes[begin + i], dtypes[begin + i]));
   }
   t->first[t->tensors] = chunks;
   int blocks = num_sms * 4 < kClipBlocks ? num_sms * 4 : kClipBlocks;
@@ -216,12 +238,12 @@ int run_clip(int64_t count, const void* const* grads, const int64_t* sizes,
     if (rc != PGG_OK) return rc;
     partials += blocks;
   }
-  rc = status_of(launch_clip_norm(partial, partials, scale, norm, stream));
-  if (rc != PGG_OK || !clip) return rc;
-  for (int64_t i = 0; i < p.tables; ++i) {
+  if (!clip) return status_of(launch_clip_norm(partial, partials, scale, norm, stream));
+  for (int64_t i = p.tables - 1; i >= 0; --i) {
     const int blocks =
         fill_table(&t, i * kClipTensors, count, grads, sizes, dtypes, out, env.num_sms);
-    rc = status_of(launch_clip_apply(t, norm, max_norm, eps, scale, blocks, stream));
+    rc = status_of(launch_clip_apply(t, partial, partials, max_norm, eps, scale, norm, blocks,
+                                     stream));
     if (rc != PGG_OK) return rc;
   }
   return PGG_OK;
@@ -347,12 +369,12 @@ int pgg_block_norm(const void* x, const void* y, const void* gate, const void* p
                          param_dtype, post, pre, gate_kind, residual_scale, weight_offset, eps);
   a.r = r;
   a.h = h;
-  const bool rows16 = H % (16 / static_cast<int64_t>(es)) == 0 && aligned(x, 16) &&
-                      aligned(y, 16) && (gate_kind == PGG_GATE_TOKEN || aligned(gate, 16)) &&
-                      aligned(post_weight, 16) && aligned(post_bias, 16) &&
-                      aligned(pre_weight, 16) && aligned(pre_bias, 16) && aligned(r, 16) &&
-                      aligned(h, 16);
-  return status_of(launch_block_norm(dtype, a, rows16, env.num_sms,
+  const int words = row_words(
+      H, dtype, {x, r, h},
+      {{y, y_dtype}, {gate_kind == PGG_GATE_TOKEN ? nullptr : gate, param_dtype},
+       {post_weight, param_dtype}, {post_bias, param_dtype}, {pre_weight, param_dtype},
+       {pre_bias, param_dtype}});
+  return status_of(launch_block_norm(dtype, a, words, env.num_sms,
                                      reinterpret_cast<cudaStream_t>(stream)));
 }
 
@@ -360,7 +382,7 @@ int pgg_block_norm_grad_workspace_size(int64_t T, int64_t H, size_t* workspace_b
   if (!workspace_bytes) return PGG_ERR_NULL;
   if (T <= 0) return PGG_ERR_ATTR;
   if (H <= 0 || H > kInt32Max || T > kInt32Max) return PGG_ERR_SHAPE;
-  *workspace_bytes = align_up(256 + static_cast<size_t>(norm_grad_blocks(T)) * 5 * 4 *
+  *workspace_bytes = align_up(256 + static_cast<size_t>(norm_grad_blocks(T, H)) * 5 * 4 *
                                         static_cast<size_t>(H), 256);
   return PGG_OK;
 }
@@ -414,13 +436,13 @@ int pgg_block_norm_grad(const void* d_r, const void* d_h, const void* r, const v
   a.d_cols[4] = d_pre_bias;
   a.hdr = static_cast<WsHeader*>(workspace);
   a.partial = reinterpret_cast<float*>(static_cast<char*>(workspace) + 256);
-  const bool rows16 = H % (16 / static_cast<int64_t>(es)) == 0 && aligned(d_r, 16) &&
-                      aligned(d_h, 16) && aligned(r, 16) && aligned(y, 16) &&
-                      (gate_kind == PGG_GATE_TOKEN || aligned(gate, 16)) &&
-                      aligned(post_weight, 16) && aligned(post_bias, 16) &&
-                      aligned(pre_weight, 16) && aligned(d_x, 16) && aligned(d_y, 16) &&
-                      (gate_kind != PGG_GATE_FULL || aligned(d_gate, 16));
-  return status_of(launch_block_norm_grad(dtype, a, rows16, env.num_sms,
+  const int words = row_words(H, dtype, {d_r, r, d_x, d_y},
+                              {{y, y_dtype}, {d_h, dh_dtype},
+                               {gate_kind == PGG_GATE_TOKEN ? nullptr : gate, param_dtype},
+                               {gate_kind == PGG_GATE_FULL ? d_gate : nullptr, param_dtype},
+                               {post_weight, param_dtype}, {post_bias, param_dtype},
+                               {pre_weight, param_dtype}});
+  return status_of(launch_block_norm_grad(dtype, a, words,
                                           reinterpret_cast<cudaStream_t>(stream)));
 }
 

@@ -10,17 +10,24 @@
 //     N'(d) = rstd (u - v^ mean(u v^) - mean(u)),  u = d (offset + w)  (rms: no mean(u))
 //     d_w = sum over rows of d v^,  d_b = sum over rows of d
 //
-// A block of threads takes a row at a time and holds it in registers, so each
-// tensor is read once; sums are fp32 (variances of the centred values), and the
-// pre norm takes r before it is rounded. Memory bounds it. In the gradient a
-// thread keeps its columns' parts of the parameters' gradients in registers over
-// all rows of its block; the blocks' sums are added in their order by a second
-// launch: bitwise repeatable. Rows too long for registers are read again for each
-// pass over them.
+// A block of threads takes a row at a time; sums are fp32 (variances of the
+// centred values), and the pre norm takes r before it is rounded. Memory bounds
+// it, so while a row's sums go round the block the next rows are on their way:
+// every thread copies (cp.async) what it will read itself into shared memory and
+// waits for its own copies only, and reads them again for each pass over the row,
+// which leaves its registers to the parameters (forward) and to its columns'
+// parts of the parameters' gradients (backward), kept over all rows of the block;
+// the blocks' sums are added in their order by a second launch: bitwise
+// repeatable. Sums of one pass go round together: the gradient of an rms norm
+// needs sum r^2 and sum u r, and 1 / deviation can be multiplied in afterwards.
+// Rows that are no multiple of 16 bytes are read from memory each time (the first
+// level cache holds them), too long ones with one element a thread and turn.
 
+#include <atomic>
 #include <cstdint>
 
 #include "pgg_block.h"
+#include "pgg_ops_launch.h"
 #include "pgg_ptx.cuh"
 #include "pgg_vec.cuh"
 
@@ -28,7 +35,67 @@ namespace pgg {
 namespace {
 
 constexpr int kMaxThreads = 1024;
-constexpr int64_t kGradBlocks = 304;  // most blocks of the gradient: two an SM
+constexpr int kRingBytes = 168 * 1024;  // of shared memory: rows that are held or on their way
+
+// The rows of up to four tensors, a thread's vectors for itself. RING: on their way through shared
+// memory, vector q of a tensor at q * 16 (of 32 bytes: the second halves behind all first ones);
+// else in memory.
+template <int DT, int V, int NV, bool RING>
+struct Rows {
+  const char* base[4];
+  int bytes[4];       // of a vector; 0 = no tensor
+  uint32_t offset[4];
+  uint32_t slot_bytes;
+  int n;              // vectors of a row
+
+  __device__ __forceinline__ void add(int i, const void* p, bool f32) {
+    base[i] = static_cast<const char*>(p);
+    bytes[i] = p ? V * (f32 ? 4 : vec::elem_bytes(DT)) : 0;
+    offset[i] = slot_bytes;
+    slot_bytes += static_cast<uint32_t>(n) * bytes[i];
+  }
+  // Row t into `slot` (nothing behind the last row); one group of copies.
+  __device__ __forceinline__ void fetch(uint8_t* smem, int slot, int64_t t, int64_t T) const {
+    if (!RING) return;
+    if (t < T) {
+      const uint32_t to = ptx::smem_addr(smem) + slot * slot_bytes;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (bytes[i] == 0) continue;
+        const char* row = base[i] + t * (static_cast<int64_t>(n) * bytes[i]);
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+          const int q = j * blockDim.x + threadIdx.x;
+          if (q >= n) continue;
+          const uint32_t at = to + offset[i] + q * 16;
+          const char* src = row + q * bytes[i];
+          ptx::cp_async_16(at, src, 16);
+          if (bytes[i] == 32) ptx::cp_async_16(at + n * 16, src + 16, 16);
+        }
+      }
+    }
+    ptx::cp_async_commit();
+  }
+  // Vector q of row t of tensor i.
+  __device__ __forceinline__ void read(const uint8_t* smem, int slot, int64_t t, int i, int q,
+                                       bool f32, float (&v)[V]) const {
+    if constexpr (RING) {
+      const uint8_t* p = smem + slot * slot_bytes + offset[i] + q * 16;
+      if (DT != PGG_F32 && f32) {
+        float lo[4], hi[4];
+        vec::load<PGG_F32, 4>(p, 0, lo);
+        vec::load<PGG_F32, 4>(p + n * 16, 0, hi);
+#pragma unroll
+        for (int c = 0; c < V; ++c) v[c] = c < 4 ? lo[c & 3] : hi[c & 3];
+      } else {
+        vec::load<DT, V>(p, 0, v);
+      }
+    } else {
+      const char* row = base[i] + t * (static_cast<int64_t>(n) * bytes[i]);
+      vec::load_or_f32<DT, V>(row, f32, q * V, v);
+    }
+  }
+};
 
 // Sums of K values over the block, the same bits in every thread. Two buffers in turn, so that one
 // barrier a call is enough.
@@ -57,37 +124,6 @@ __device__ __forceinline__ void block_sum(BlockSum<M>* s, int* turn, float (&v)[
     for (int d = 16; d > 0; d >>= 1) v[i] += __shfl_xor_sync(0xFFFFFFFFu, v[i], d);
   }
   *turn ^= 1;
-}
-
-// ------------------------------------------------------------------ rows in registers
-
-// Mean and 1 / deviation of up to two rows of values held by the block.
-template <int V, int NV, int M>
-__device__ __forceinline__ void stats(BlockSum<M>* s, int* turn, int kind, const float (&v)[NV][V],
-                                      int64_t H, float eps, float* mean, float* rstd) {
-  const int64_t n = H / V;
-  float sum[1] = {0.0f};
-  *mean = 0.0f;
-  if (kind == PGG_NORM_LAYER) {
-#pragma unroll
-    for (int j = 0; j < NV; ++j)
-#pragma unroll
-      for (int c = 0; c < V; ++c) sum[0] += v[j][c];  // (0 outside the row)
-    block_sum(s, turn, sum);
-    *mean = sum[0] / static_cast<float>(H);
-    sum[0] = 0.0f;
-  }
-#pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    const bool in = j * static_cast<int64_t>(blockDim.x) + threadIdx.x < n;
-#pragma unroll
-    for (int c = 0; c < V; ++c) {
-      const float d = v[j][c] - *mean;
-      if (in) sum[0] = fmaf(d, d, sum[0]);
-    }
-  }
-  block_sum(s, turn, sum);
-  *rstd = 1.0f / sqrtf(sum[0] / static_cast<float>(H) + eps);
 }
 
 // The weight's factor and the bias of V columns.
@@ -125,55 +161,138 @@ __device__ __forceinline__ void gate_at(const NormArgs& a, int64_t t, int64_t i,
   }
 }
 
-template <int DT, int V, int NV>
-__global__ void __launch_bounds__(kMaxThreads) block_norm_kernel(const NormArgs a) {
+// ------------------------------------------------------------------ rows held by a block
+
+// (BIAS: some norm has one)
+template <int DT, int V, int NV, bool RING, bool BIAS, int THREADS>
+__global__ void __launch_bounds__(THREADS, 1) block_norm_kernel(const NormArgs a, const int ring) {
+  extern __shared__ __align__(16) uint8_t smem[];
   __shared__ BlockSum<1> s;
-  int turn = 0;
+  int turn = 0, slot = 0;
   ptx::griddep_wait();
-  const int64_t n = a.H / V;
-  for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
-    float r[NV][V], y[NV][V];
+  const float inv_h = 1.0f / static_cast<float>(a.H);
+  Rows<DT, V, NV, RING> rows = {};
+  rows.n = static_cast<int>(a.H / V);
+  const int n = rows.n, tid = threadIdx.x;
+  const bool y_f32 = DT == PGG_F32 || a.y_f32, have_y = a.y != nullptr;
+  rows.add(0, a.x, DT == PGG_F32);
+  rows.add(1, a.y, y_f32);
+  for (int i = 0; RING && i < ring; ++i)
+    rows.fetch(smem, i, blockIdx.x + static_cast<int64_t>(i) * gridDim.x, a.T);
+  // the post norm's factor and bias with a channel's gate, and the pre norm's
+  const bool by_row = a.gate_kind == PGG_GATE_FULL || a.gate_kind == PGG_GATE_TOKEN;
+  float f0[NV][V], b0[NV][V], f1[NV][V], b1[NV][V];
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int64_t q = j * static_cast<int64_t>(blockDim.x) + threadIdx.x;
+  for (int j = 0; j < NV; ++j) {
+    const int q = j * blockDim.x + tid;
+    if (q >= n) continue;
+    affine<DT, V>(a.w_post, a.b_post, a.p_f32, a.weight_offset, q * V, f0[j], b0[j]);
+    affine<DT, V>(a.w_pre, a.b_pre, a.p_f32, a.weight_offset, q * V, f1[j], b1[j]);
+    if (a.gate_kind == PGG_GATE_CHANNEL) {
+      float g[V];
+      vec::load_or_f32<DT, V>(a.gate, a.p_f32, q * V, g);
 #pragma unroll
-      for (int c = 0; c < V; ++c) r[j][c] = y[j][c] = 0.0f;
-      if (q < n) {
-        vec::load<DT, V>(a.x, t * a.H + q * V, r[j]);
-        if (a.y) vec::load_or_f32<DT, V>(a.y, a.y_f32, t * a.H + q * V, y[j]);
+      for (int c = 0; c < V; ++c) {
+        f0[j][c] *= g[c];
+        b0[j][c] *= g[c];
       }
+    }
+  }
+  for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
+    if (RING) {  // (a group of copies a row: those of the `ring` - 1 rows behind may be pending)
+      if (ring > 2) ptx::cp_async_wait<2>(); else if (ring == 2) ptx::cp_async_wait<1>(); else ptx::cp_async_wait<0>();
     }
     float mean = 0.0f, rstd = 1.0f;
-    if (a.post != PGG_NORM_NONE) stats(&s, &turn, a.post, y, a.H, a.eps, &mean, &rstd);
+    if (a.post != PGG_NORM_NONE) {
+      float sum[1];
+      if (a.post == PGG_NORM_LAYER) {
+        sum[0] = 0.0f;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+          const int q = j * blockDim.x + tid;
+          if (q >= n) continue;
+          float y[V];
+          rows.read(smem, slot, t, 1, q, y_f32, y);
+#pragma unroll
+          for (int c = 0; c < V; ++c) sum[0] += y[c];
+        }
+        block_sum(&s, &turn, sum);
+        mean = sum[0] * inv_h;
+      }
+      sum[0] = 0.0f;
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const int q = j * blockDim.x + tid;
+        if (q >= n) continue;
+        float y[V];
+        rows.read(smem, slot, t, 1, q, y_f32, y);
+#pragma unroll
+        for (int c = 0; c < V; ++c) sum[0] = fmaf(y[c] - mean, y[c] - mean, sum[0]);
+      }
+      block_sum(&s, &turn, sum);
+      rstd = 1.0f / sqrtf(sum[0] * inv_h + a.eps);
+    }
+    float r[NV][V], sum[1] = {0.0f};
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int64_t q = j * static_cast<int64_t>(blockDim.x) + threadIdx.x;
+      const int q = j * blockDim.x + tid;
       if (q >= n) continue;
-      if (a.y) {
-        float f[V], b[V], g[V];
-        affine<DT, V>(a.w_post, a.b_post, a.p_f32, a.weight_offset, q * V, f, b);
-        gate_at<DT, V>(a, t, q * V, g);
+      rows.read(smem, slot, t, 0, q, DT == PGG_F32, r[j]);
 #pragma unroll
-        for (int c = 0; c < V; ++c) {
-          const float u = fmaf((y[j][c] - mean) * rstd, f[c], b[c]);
-          r[j][c] = fmaf(g[c], u, a.residual_scale * r[j][c]);
+      for (int c = 0; c < V; ++c) r[j][c] *= a.residual_scale;
+      if (have_y) {
+        float y[V];
+        rows.read(smem, slot, t, 1, q, y_f32, y);
+        if (by_row) {
+          float g[V];
+          gate_at<DT, V>(a, t, q * V, g);
+#pragma unroll
+          for (int c = 0; c < V; ++c) {
+            const float u = (y[c] - mean) * rstd;
+            r[j][c] = fmaf(g[c], BIAS ? fmaf(u, f0[j][c], b0[j][c]) : u * f0[j][c], r[j][c]);
+          }
+        } else {
+#pragma unroll
+          for (int c = 0; c < V; ++c) {
+            r[j][c] = fmaf((y[c] - mean) * rstd, f0[j][c], r[j][c]);
+            if (BIAS) r[j][c] += b0[j][c];
+          }
         }
-      } else {
-#pragma unroll
-        for (int c = 0; c < V; ++c) r[j][c] *= a.residual_scale;
       }
       if (a.r) vec::store<DT, V>(a.r, t * a.H + q * V, r[j]);
+#pragma unroll
+      for (int c = 0; c < V; ++c)
+        sum[0] = a.pre == PGG_NORM_LAYER ? sum[0] + r[j][c] : fmaf(r[j][c], r[j][c], sum[0]);
+    }
+    if (RING) {  // (a thread's copies go where it alone has read)
+      rows.fetch(smem, slot, t + static_cast<int64_t>(ring) * gridDim.x, a.T);
+      slot = slot + 1 == ring ? 0 : slot + 1;
     }
     if (a.pre == PGG_NORM_NONE) continue;
-    stats(&s, &turn, a.pre, r, a.H, a.eps, &mean, &rstd);
+    block_sum(&s, &turn, sum);
+    mean = 0.0f;
+    if (a.pre == PGG_NORM_LAYER) {
+      mean = sum[0] * inv_h;
+      sum[0] = 0.0f;
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const int q = j * blockDim.x + tid;
+        if (q >= n) continue;
+#pragma unroll
+        for (int c = 0; c < V; ++c) sum[0] = fmaf(r[j][c] - mean, r[j][c] - mean, sum[0]);
+      }
+      block_sum(&s, &turn, sum);
+    }
+    rstd = 1.0f / sqrtf(sum[0] * inv_h + a.eps);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int64_t q = j * static_cast<int64_t>(blockDim.x) + threadIdx.x;
+      const int q = j * blockDim.x + tid;
       if (q >= n) continue;
-      float f[V], b[V];
-      affine<DT, V>(a.w_pre, a.b_pre, a.p_f32, a.weight_offset, q * V, f, b);
 #pragma unroll
-      for (int c = 0; c < V; ++c) r[j][c] = fmaf((r[j][c] - mean) * rstd, f[c], b[c]);
+      for (int c = 0; c < V; ++c) {
+        const float u = (r[j][c] - mean) * rstd;
+        r[j][c] = BIAS ? fmaf(u, f1[j][c], b1[j][c]) : u * f1[j][c];
+      }
       vec::store<DT, V>(a.h, t * a.H + q * V, r[j]);
     }
   }
@@ -182,117 +301,174 @@ __global__ void __launch_bounds__(kMaxThreads) block_norm_kernel(const NormArgs 
 // Columns' sums that a block keeps: gate (channel), w_post, b_post, w_pre, b_pre.
 enum { kColGate, kColWPost, kColBPost, kColWPre, kColBPre, kCols };
 
-// (BIAS: some norm has a mean, so there may be sums for a bias)
-template <int DT, int V, int NV, bool BIAS>
-__global__ void __launch_bounds__(kMaxThreads) block_norm_grad_kernel(const NormArgs a) {
-  __shared__ BlockSum<3> s;
-  int turn = 0;
+// (BIAS: there are sums for a bias)
+template <int DT, int V, int NV, bool RING, bool BIAS, int THREADS>
+__global__ void __launch_bounds__(THREADS, 1)
+    block_norm_grad_kernel(const NormArgs a, const int ring) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ BlockSum<4> s;
+  int turn = 0, slot = 0;
   ptx::griddep_wait();
   if (blockIdx.x == 0 && threadIdx.x == 0) a.hdr->status = 0;
-  const int64_t n = a.H / V;
   const float inv_h = 1.0f / static_cast<float>(a.H);
+  Rows<DT, V, NV, RING> rows = {};
+  rows.n = static_cast<int>(a.H / V);
+  const int n = rows.n, tid = threadIdx.x;
+  const bool y_f32 = DT == PGG_F32 || a.y_f32, dh_f32 = DT == PGG_F32 || a.dh_f32;
+  const bool have_y = a.y != nullptr, pre = a.pre != PGG_NORM_NONE, token = a.gate_kind == PGG_GATE_TOKEN;
+  rows.add(0, a.d_r, DT == PGG_F32);
+  rows.add(1, a.y, y_f32);
+  rows.add(2, pre ? a.d_h : nullptr, dh_f32);
+  rows.add(3, pre ? a.x : nullptr, DT == PGG_F32);
+  for (int i = 0; RING && i < ring; ++i)
+    rows.fetch(smem, i, blockIdx.x + static_cast<int64_t>(i) * gridDim.x, a.T);
   float col[BIAS ? kCols : 3][NV][V] = {};  // without BIAS: gate, w_post, w_pre
   constexpr int kWPre = BIAS ? kColWPre : 2;
+  // the factor of a column's norm (its bias: b)
+  auto factor = [&](const void* w, const void* bias, int q, float (&f)[V], float (&b)[V]) {
+    affine<DT, V>(w, bias, a.p_f32, a.weight_offset, q * V, f, b);
+  };
   for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
-    // g: the gradient of r;  dh, then what it gives;  r and y, then normalised
-    float g[NV][V], dh[NV][V], r[NV][V], y[NV][V];
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int64_t q = j * static_cast<int64_t>(blockDim.x) + threadIdx.x;
-#pragma unroll
-      for (int c = 0; c < V; ++c) g[j][c] = dh[j][c] = r[j][c] = y[j][c] = 0.0f;
-      if (q < n) {
-        const int64_t i = t * a.H + q * V;
-        if (a.d_r) vec::load<DT, V>(a.d_r, i, g[j]);
-        if (a.y) vec::load_or_f32<DT, V>(a.y, a.y_f32, i, y[j]);
-        if (a.pre != PGG_NORM_NONE) {
-          vec::load_or_f32<DT, V>(a.d_h, a.dh_f32, i, dh[j]);
-          vec::load<DT, V>(a.x, i, r[j]);
-        }
-      }
+    if (RING) {
+      if (ring > 2) ptx::cp_async_wait<2>(); else if (ring == 2) ptx::cp_async_wait<1>(); else ptx::cp_async_wait<0>();
     }
-    float mean, rstd;
-    if (a.pre != PGG_NORM_NONE) {
-      stats(&s, &turn, a.pre, r, a.H, a.eps, &mean, &rstd);
-      float sum[2] = {0.0f, 0.0f};
+    float mean = 0.0f, rstd = 1.0f, along = 0.0f, centre = 0.0f;
+    if (pre) {
+      if (a.pre == PGG_NORM_LAYER) {
+        float sum[1] = {0.0f};
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+          const int q = j * blockDim.x + tid;
+          if (q >= n) continue;
+          float r[V];
+          rows.read(smem, slot, t, 3, q, DT == PGG_F32, r);
+#pragma unroll
+          for (int c = 0; c < V; ++c) sum[0] += r[c];
+        }
+        block_sum(&s, &turn, sum);
+        mean = sum[0] * inv_h;
+      }
+      float sum[3] = {0.0f, 0.0f, 0.0f};  // of v^2, u v, u with v = r - mean
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
-        const int64_t q = j * static_cast<int64_t>(blockDim.x) + threadIdx.x;
+        const int q = j * blockDim.x + tid;
         if (q >= n) continue;
-        float f[V], b[V];
-        affine<DT, V>(a.w_pre, nullptr, a.p_f32, a.weight_offset, q * V, f, b);
+        float r[V], dh[V], f[V], b[V];
+        rows.read(smem, slot, t, 3, q, DT == PGG_F32, r);
+        rows.read(smem, slot, t, 2, q, dh_f32, dh);
+        factor(a.w_pre, nullptr, q, f, b);
 #pragma unroll
         for (int c = 0; c < V; ++c) {
-          r[j][c] = (r[j][c] - mean) * rstd;
-          col[kWPre][j][c] = fmaf(dh[j][c], r[j][c], col[kWPre][j][c]);
-          if constexpr (BIAS) col[kColBPre][j][c] += dh[j][c];
-          dh[j][c] *= f[c];
-          sum[0] = fmaf(dh[j][c], r[j][c], sum[0]);
-          sum[1] += dh[j][c];
+          const float v = r[c] - mean, u = dh[c] * f[c];
+          sum[0] = fmaf(v, v, sum[0]);
+          sum[1] = fmaf(u, v, sum[1]);
+          sum[2] += u;
         }
       }
       block_sum(&s, &turn, sum);
-      const float along = sum[0] * inv_h;
-      const float centre = a.pre == PGG_NORM_LAYER ? sum[1] * inv_h : 0.0f;
-#pragma unroll
-      for (int j = 0; j < NV; ++j)
-#pragma unroll
-        for (int c = 0; c < V; ++c)
-          g[j][c] = fmaf(rstd, dh[j][c] - fmaf(r[j][c], along, centre), g[j][c]);
+      rstd = 1.0f / sqrtf(sum[0] * inv_h + a.eps);
+      along = sum[1] * rstd * inv_h;
+      centre = a.pre == PGG_NORM_LAYER ? sum[2] * inv_h : 0.0f;
     }
-    // (r is done with: it holds d_x)
+    float mean_y = 0.0f;
+    if (a.post == PGG_NORM_LAYER) {
+      float sum[1] = {0.0f};
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int64_t q = j * static_cast<int64_t>(blockDim.x) + threadIdx.x;
-      if (q >= n) continue;
+      for (int j = 0; j < NV; ++j) {
+        const int q = j * blockDim.x + tid;
+        if (q >= n) continue;
+        float y[V];
+        rows.read(smem, slot, t, 1, q, y_f32, y);
 #pragma unroll
-      for (int c = 0; c < V; ++c) r[j][c] = a.residual_scale * g[j][c];
-      vec::store<DT, V>(a.r, t * a.H + q * V, r[j]);
-    }
-    if (!a.y) continue;
-    mean = 0.0f;
-    rstd = 1.0f;
-    if (a.post != PGG_NORM_NONE) stats(&s, &turn, a.post, y, a.H, a.eps, &mean, &rstd);
-    float sum[3] = {0.0f, 0.0f, 0.0f};
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int64_t q = j * static_cast<int64_t>(blockDim.x) + threadIdx.x;
-      if (q >= n) continue;
-      float f[V], b[V], gate[V], whole[V];
-      affine<DT, V>(a.w_post, a.b_post, a.p_f32, a.weight_offset, q * V, f, b);
-      gate_at<DT, V>(a, t, q * V, gate);
-#pragma unroll
-      for (int c = 0; c < V; ++c) {
-        y[j][c] = (y[j][c] - mean) * rstd;
-        whole[c] = g[j][c] * fmaf(y[j][c], f[c], b[c]);
-        col[kColGate][j][c] += whole[c];
-        sum[2] += whole[c];
-        g[j][c] *= gate[c];
-        col[kColWPost][j][c] = fmaf(g[j][c], y[j][c], col[kColWPost][j][c]);
-        if constexpr (BIAS) col[kColBPost][j][c] += g[j][c];
-        g[j][c] *= f[c];
-        sum[0] = fmaf(g[j][c], y[j][c], sum[0]);
-        sum[1] += g[j][c];
+        for (int c = 0; c < V; ++c) sum[0] += y[c];
       }
-      if (a.gate_kind == PGG_GATE_FULL) {
-        if (DT == PGG_F32 || a.p_f32)
-          vec::store<PGG_F32, V>(a.d_gate, t * a.H + q * V, whole);
-        else
-          vec::store<DT, V>(a.d_gate, t * a.H + q * V, whole);
-      }
+      block_sum(&s, &turn, sum);
+      mean_y = sum[0] * inv_h;
     }
-    if (a.post != PGG_NORM_NONE || a.gate_kind == PGG_GATE_TOKEN) block_sum(&s, &turn, sum);
-    if (a.gate_kind == PGG_GATE_TOKEN && threadIdx.x == 0)
-      static_cast<float*>(a.d_gate)[t] = sum[2];
-    const float along = a.post != PGG_NORM_NONE ? sum[0] * inv_h : 0.0f;
-    const float centre = a.post == PGG_NORM_LAYER ? sum[1] * inv_h : 0.0f;
+    // g, d_x, and the sums of v^2, w v, w and g b with v = y - mean, w = g gate f (and, for a
+    // token's gate, g f v is w v / gate: it is taken by itself)
+    float g[NV][V], sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int64_t q = j * static_cast<int64_t>(blockDim.x) + threadIdx.x;
+      const int q = j * blockDim.x + tid;
       if (q >= n) continue;
 #pragma unroll
-      for (int c = 0; c < V; ++c) y[j][c] = rstd * (g[j][c] - fmaf(y[j][c], along, centre));
-      vec::store<DT, V>(a.h, t * a.H + q * V, y[j]);
+      for (int c = 0; c < V; ++c) g[j][c] = 0.0f;
+      if (a.d_r) rows.read(smem, slot, t, 0, q, DT == PGG_F32, g[j]);
+      if (pre) {
+        float r[V], dh[V], f[V], b[V];
+        rows.read(smem, slot, t, 3, q, DT == PGG_F32, r);
+        rows.read(smem, slot, t, 2, q, dh_f32, dh);
+        factor(a.w_pre, nullptr, q, f, b);
+#pragma unroll
+        for (int c = 0; c < V; ++c) {
+          const float v = (r[c] - mean) * rstd;
+          col[kWPre][j][c] = fmaf(dh[c], v, col[kWPre][j][c]);
+          if constexpr (BIAS) col[kColBPre][j][c] += dh[c];
+          g[j][c] = fmaf(rstd, fmaf(dh[c], f[c], -fmaf(v, along, centre)), g[j][c]);
+        }
+      }
+      float d[V];
+#pragma unroll
+      for (int c = 0; c < V; ++c) d[c] = a.residual_scale * g[j][c];
+      vec::store<DT, V>(a.r, t * a.H + q * V, d);
+      if (have_y && (a.post != PGG_NORM_NONE || token)) {
+        float y[V], f[V], b[V], gate[V];
+        rows.read(smem, slot, t, 1, q, y_f32, y);
+        factor(a.w_post, a.b_post, q, f, b);
+        gate_at<DT, V>(a, t, q * V, gate);
+#pragma unroll
+        for (int c = 0; c < V; ++c) {
+          const float v = y[c] - mean_y, w = g[j][c] * f[c];
+          sum[0] = fmaf(v, v, sum[0]);
+          sum[1] = fmaf(token ? w : w * gate[c], v, sum[1]);
+          sum[2] = fmaf(w, gate[c], sum[2]);
+          if constexpr (BIAS) sum[3] = fmaf(g[j][c], b[c], sum[3]);
+        }
+      }
+    }
+    if (have_y) {
+      float rstd_y = 1.0f, along_y = 0.0f, centre_y = 0.0f;
+      if (a.post != PGG_NORM_NONE || token) {
+        block_sum(&s, &turn, sum);
+        if (a.post != PGG_NORM_NONE) rstd_y = 1.0f / sqrtf(sum[0] * inv_h + a.eps);
+        float tg[1] = {1.0f};
+        if (token) {
+          vec::load_or_f32<DT, 1>(a.gate, a.p_f32, t, tg);
+          if (tid == 0) static_cast<float*>(a.d_gate)[t] = fmaf(sum[1], rstd_y, sum[3]);
+        }
+        if (a.post != PGG_NORM_NONE) along_y = sum[1] * tg[0] * rstd_y * inv_h;
+        if (a.post == PGG_NORM_LAYER) centre_y = sum[2] * inv_h;
+      }
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const int q = j * blockDim.x + tid;
+        if (q >= n) continue;
+        float y[V], f[V], b[V], gate[V], whole[V];
+        rows.read(smem, slot, t, 1, q, y_f32, y);
+        factor(a.w_post, a.b_post, q, f, b);
+        gate_at<DT, V>(a, t, q * V, gate);
+#pragma unroll
+        for (int c = 0; c < V; ++c) {
+          const float v = (y[c] - mean_y) * rstd_y, d = g[j][c] * gate[c];
+          whole[c] = g[j][c] * (BIAS ? fmaf(v, f[c], b[c]) : v * f[c]);
+          col[kColGate][j][c] += whole[c];
+          col[kColWPost][j][c] = fmaf(d, v, col[kColWPost][j][c]);
+          if constexpr (BIAS) col[kColBPost][j][c] += d;
+          y[c] = rstd_y * fmaf(d, f[c], -fmaf(v, along_y, centre_y));
+        }
+        vec::store<DT, V>(a.h, t * a.H + q * V, y);
+        if (a.gate_kind == PGG_GATE_FULL) {
+          if (DT == PGG_F32 || a.p_f32)
+            vec::store<PGG_F32, V>(a.d_gate, t * a.H + q * V, whole);
+          else
+            vec::store<DT, V>(a.d_gate, t * a.H + q * V, whole);
+        }
+      }
+    }
+    if (RING) {  // (a thread's copies go where it alone has read)
+      rows.fetch(smem, slot, t + static_cast<int64_t>(ring) * gridDim.x, a.T);
+      slot = slot + 1 == ring ? 0 : slot + 1;
     }
   }
 #pragma unroll
@@ -301,7 +477,7 @@ __global__ void __launch_bounds__(kMaxThreads) block_norm_grad_kernel(const Norm
     if (!a.d_cols[which]) continue;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int64_t q = j * static_cast<int64_t>(blockDim.x) + threadIdx.x;
+      const int q = j * blockDim.x + tid;
       if (q < n)
         vec::store<PGG_F32, V>(a.partial, (static_cast<int64_t>(blockIdx.x) * kCols + which) * a.H
                                               + q * V, col[k][j]);
@@ -487,87 +663,178 @@ __global__ void __launch_bounds__(256) block_norm_cols_kernel(const NormArgs a, 
   out[i] = sum;
 }
 
-// Vectors of a thread and threads for rows of n vectors: as few vectors as `most` threads allow.
-bool shape(int64_t n, int most, int max_nv, int* nv, int* threads) {
-  for (*nv = 1; *nv <= max_nv; *nv *= 2) {
+// Rows of n vectors: vectors a thread (1, 2 or 4) and threads, at most 512; false: too long.
+bool shape(int64_t n, int* nv, int* threads) {
+  for (*nv = 1; *nv <= 4; *nv *= 2) {
     const int64_t need = ((n + *nv - 1) / *nv + 31) / 32 * 32;
-    if (need <= (*nv == max_nv ? kMaxThreads : most)) {
-      *threads = static_cast<int>(need);
-      return true;
-    }
+    *threads = static_cast<int>(need);
+    if (need <= (*nv == 1 ? 256 : 512)) return true;
   }
   return false;
 }
 
+// Blocks of a kernel that an SM holds at once, by its registers and shared memory; asked once.
+struct Fit {
+  std::atomic<int> registers{0};
+};
+
+template <typename K>
+cudaError_t blocks_that_fit(Fit* fit, K kern, int threads, int64_t smem, int* blocks) {
+  int regs = fit->registers.load();
+  if (regs == 0) {
+    cudaFuncAttributes attr;
+    const cudaError_t err = cudaFuncGetAttributes(&attr, kern);
+    if (err != cudaSuccess) return err;
+    regs = (attr.numRegs + 7) / 8 * 8;
+    fit->registers.store(regs);
+  }
+  int64_t n = 65536 / (static_cast<int64_t>(regs) * threads);
+  if (n > 226 * 1024 / (smem + 2048)) n = 226 * 1024 / (smem + 2048);
+  *blocks = static_cast<int>(n < 1 ? 1 : n > 16 ? 16 : n);
+  return cudaSuccess;
+}
+
+// Rows that a block keeps on their way: one to three, with `blocks` of them on an SM.
+int ring_rows(int64_t row_bytes, int blocks) {
+  const int64_t n = kRingBytes / blocks / row_bytes;
+  return n < 1 ? 1 : n > 3 ? 3 : static_cast<int>(n);
+}
+
+// Bytes of a row of what the kernel reads.
+template <int DT>
+int64_t forward_bytes(const NormArgs& a) {
+  constexpr int es = vec::elem_bytes(DT);
+  return a.H * (es + (a.y ? (a.y_f32 ? 4 : es) : 0));
+}
+template <int DT>
+int64_t backward_bytes(const NormArgs& a) {
+  constexpr int es = vec::elem_bytes(DT);
+  return a.H * ((a.d_r ? es : 0) + (a.y ? (a.y_f32 ? 4 : es) : 0) +
+                (a.pre != PGG_NORM_NONE ? (a.dh_f32 ? 4 : es) + es : 0));
+}
+
+template <typename K>
+cudaError_t launch_rows(SmemLimit* limit, K kern, int64_t grid, int threads, int64_t smem,
+                        cudaStream_t stream, const NormArgs& a, int ring) {
+  if (smem > 40 * 1024) {  // (beside what is static)
+    const cudaError_t err = allow_smem(limit, kern, kRingBytes + 1024);
+    if (err != cudaSuccess) return err;
+  }
+  return launch_pdl(kern, dim3(static_cast<unsigned>(grid)), dim3(static_cast<unsigned>(threads)),
+                    static_cast<size_t>(smem), stream, 1, a, ring);
+}
+
+template <int DT, int V, int NV, bool BIAS, int THREADS>
+cudaError_t launch_forward_t(const NormArgs& a, int threads, int num_sms, cudaStream_t stream) {
+  constexpr bool kHeld = V >= 4;
+  auto kern = block_norm_kernel<DT, V, NV, kHeld, BIAS, THREADS>;
+  static Fit fit;
+  static SmemLimit limit;
+  int blocks;
+  cudaError_t err = blocks_that_fit(&fit, kern, threads, 0, &blocks);
+  if (err != cudaSuccess) return err;
+  const int64_t row = forward_bytes<DT>(a);
+  const int ring = kHeld ? ring_rows(row, blocks) : 0;
+  err = blocks_that_fit(&fit, kern, threads, ring * row, &blocks);
+  if (err != cudaSuccess) return err;
+  const int64_t most = static_cast<int64_t>(num_sms) * blocks;
+  return launch_rows(&limit, kern, a.T < most ? a.T : most, threads, ring * row, stream, a, ring);
+}
+
 template <int DT, int V>
 cudaError_t launch_forward(const NormArgs& a, int num_sms, cudaStream_t stream) {
-  using K = void (*)(const NormArgs);
-  static const K kern[4] = {block_norm_kernel<DT, V, 1>, block_norm_kernel<DT, V, 2>,
-                            block_norm_kernel<DT, V, 4>, block_norm_kernel<DT, V, 8>};
   int nv, threads;
-  K k = block_norm_long_kernel<DT>;
-  if (shape(a.H / V, 512, V == 1 ? 8 : 4, &nv, &threads))
-    k = kern[nv == 1 ? 0 : nv == 2 ? 1 : nv == 4 ? 2 : 3];
-  else
-    threads = kMaxThreads;
-  int64_t grid = static_cast<int64_t>(num_sms) * (2048 / threads);
-  if (grid > a.T) grid = a.T;
-  return launch_pdl(k, dim3(static_cast<unsigned>(grid)), dim3(static_cast<unsigned>(threads)), 0,
-                    stream, 1, a);
+  const bool bias = a.b_post || a.b_pre;
+  if (shape(a.H / V, &nv, &threads) && (V < 4 || forward_bytes<DT>(a) <= kRingBytes)) {
+    if (nv == 1)
+      return bias ? launch_forward_t<DT, V, 1, true, 256>(a, threads, num_sms, stream)
+                  : launch_forward_t<DT, V, 1, false, 256>(a, threads, num_sms, stream);
+    if (nv == 2)
+      return bias ? launch_forward_t<DT, V, 2, true, 512>(a, threads, num_sms, stream)
+                  : launch_forward_t<DT, V, 2, false, 512>(a, threads, num_sms, stream);
+    return bias ? launch_forward_t<DT, V, 4, true, 512>(a, threads, num_sms, stream)
+                : launch_forward_t<DT, V, 4, false, 512>(a, threads, num_sms, stream);
+  }
+  const int64_t grid = a.T < 2 * num_sms ? a.T : 2 * num_sms;
+  return launch_pdl(block_norm_long_kernel<DT>, dim3(static_cast<unsigned>(grid)),
+                    dim3(kMaxThreads), 0, stream, 1, a);
+}
+
+template <int DT, int V, int NV, bool BIAS, int THREADS>
+cudaError_t launch_backward_t(const NormArgs& a, int threads, cudaStream_t stream) {
+  constexpr bool kHeld = V >= 4;
+  static SmemLimit limit;
+  const int64_t row = backward_bytes<DT>(a), blocks = norm_grad_blocks(a.T, a.H);
+  const int ring = kHeld ? ring_rows(row, static_cast<int>((blocks + 151) / 152)) : 0;
+  return launch_rows(&limit, block_norm_grad_kernel<DT, V, NV, kHeld, BIAS, THREADS>, blocks,
+                     threads, ring * row, stream, a, ring);
 }
 
 template <int DT, int V>
 cudaError_t launch_backward(const NormArgs& a, cudaStream_t stream) {
-  using K = void (*)(const NormArgs);
-  static const K kern[2][2] = {
-      {block_norm_grad_kernel<DT, V, 1, false>, block_norm_grad_kernel<DT, V, 2, false>},
-      {block_norm_grad_kernel<DT, V, 1, true>, block_norm_grad_kernel<DT, V, 2, true>}};
+  const bool bias = a.b_post || a.b_pre;
   int nv, threads;
-  K k = block_norm_grad_long_kernel<DT>;
-  const bool bias = a.d_cols[kColBPost] || a.d_cols[kColBPre];
-  if (shape(a.H / V, kMaxThreads, 2, &nv, &threads))
-    k = kern[bias ? 1 : 0][nv - 1];
-  else
-    threads = kMaxThreads;
-  const int64_t blocks = norm_grad_blocks(a.T);
-  cudaError_t err = launch_pdl(k, dim3(static_cast<unsigned>(blocks)),
-                               dim3(static_cast<unsigned>(threads)), 0, stream, 1, a);
+  cudaError_t err;
+  if (shape(a.H / V, &nv, &threads) && (V < 4 || backward_bytes<DT>(a) <= kRingBytes)) {
+    if (nv == 1)
+      err = bias ? launch_backward_t<DT, V, 1, true, 256>(a, threads, stream)
+                 : launch_backward_t<DT, V, 1, false, 256>(a, threads, stream);
+    else if (nv == 2)
+      err = bias ? launch_backward_t<DT, V, 2, true, 512>(a, threads, stream)
+                 : launch_backward_t<DT, V, 2, false, 512>(a, threads, stream);
+    else
+      err = bias ? launch_backward_t<DT, V, 4, true, 512>(a, threads, stream)
+                 : launch_backward_t<DT, V, 4, false, 512>(a, threads, stream);
+  } else {
+    err = launch_pdl(block_norm_grad_long_kernel<DT>,
+                     dim3(static_cast<unsigned>(norm_grad_blocks(a.T, a.H))), dim3(kMaxThreads), 0,
+                     stream, 1, a);
+  }
   if (err != cudaSuccess) return err;
   for (int i = 0; i < kCols; ++i)
     if (a.d_cols[i])
       return launch_pdl(block_norm_cols_kernel, dim3(static_cast<unsigned>((a.H + 31) / 32), kCols),
-                        dim3(256), 0, stream, 1, a, blocks);
+                        dim3(256), 0, stream, 1, a, norm_grad_blocks(a.T, a.H));
   return cudaSuccess;
 }
 
 }  // namespace
 
-int64_t norm_grad_blocks(int64_t T) { return T < kGradBlocks ? T : kGradBlocks; }
+// One block an SM holds long rows; of short ones several do, and hide each other's sums.
+int64_t norm_grad_blocks(int64_t T, int64_t H) {
+  const int64_t most = 152 * (H > 4096 ? 1 : H > 2048 ? 2 : H > 1024 ? 3 : 6);
+  return T < most ? T : most;
+}
 
-cudaError_t launch_block_norm(int dtype, const NormArgs& a, bool rows16, int num_sms,
+// words: 16, 4 (two 16-bit elements, or one fp32) or 0 for rows that are read element by element.
+cudaError_t launch_block_norm(int dtype, const NormArgs& a, int words, int num_sms,
                               cudaStream_t stream) {
   if (dtype == PGG_F32)
-    return rows16 ? launch_forward<PGG_F32, 4>(a, num_sms, stream)
-                  : launch_forward<PGG_F32, 1>(a, num_sms, stream);
+    return words == 16 ? launch_forward<PGG_F32, 4>(a, num_sms, stream)
+                       : launch_forward<PGG_F32, 1>(a, num_sms, stream);
   if (dtype == PGG_F16)
-    return rows16 ? launch_forward<PGG_F16, 8>(a, num_sms, stream)
-                  : launch_forward<PGG_F16, 1>(a, num_sms, stream);
+    return words == 16  ? launch_forward<PGG_F16, 8>(a, num_sms, stream)
+           : words == 4 ? launch_forward<PGG_F16, 2>(a, num_sms, stream)
+                        : launch_forward<PGG_F16, 1>(a, num_sms, stream);
   if (dtype == PGG_BF16)
-    return rows16 ? launch_forward<PGG_BF16, 8>(a, num_sms, stream)
-                  : launch_forward<PGG_BF16, 1>(a, num_sms, stream);
+    return words == 16  ? launch_forward<PGG_BF16, 8>(a, num_sms, stream)
+           : words == 4 ? launch_forward<PGG_BF16, 2>(a, num_sms, stream)
+                        : launch_forward<PGG_BF16, 1>(a, num_sms, stream);
   return cudaErrorInvalidValue;
 }
 
-cudaError_t launch_block_norm_grad(int dtype, const NormArgs& a, bool rows16, int num_sms,
-                                   cudaStream_t stream) {
-  (void)num_sms;
+cudaError_t launch_block_norm_grad(int dtype, const NormArgs& a, int words, cudaStream_t stream) {
   if (dtype == PGG_F32)
-    return rows16 ? launch_backward<PGG_F32, 4>(a, stream) : launch_backward<PGG_F32, 1>(a, stream);
+    return words == 16 ? launch_backward<PGG_F32, 4>(a, stream)
+                       : launch_backward<PGG_F32, 1>(a, stream);
   if (dtype == PGG_F16)
-    return rows16 ? launch_backward<PGG_F16, 8>(a, stream) : launch_backward<PGG_F16, 1>(a, stream);
+    return words == 16  ? launch_backward<PGG_F16, 8>(a, stream)
+           : words == 4 ? launch_backward<PGG_F16, 2>(a, stream)
+                        : launch_backward<PGG_F16, 1>(a, stream);
   if (dtype == PGG_BF16)
-    return rows16 ? launch_backward<PGG_BF16, 8>(a, stream)
-                  : launch_backward<PGG_BF16, 1>(a, stream);
+    return words == 16  ? launch_backward<PGG_BF16, 8>(a, stream)
+           : words == 4 ? launch_backward<PGG_BF16, 2>(a, stream)
+                        : launch_backward<PGG_BF16, 1>(a, stream);
   return cudaErrorInvalidValue;
 }
 

@@ -75,11 +75,11 @@ struct NormArgs {
 };
 
 // Blocks whose column sums the backward keeps apart.
-int64_t norm_grad_blocks(int64_t T);
-cudaError_t launch_block_norm(int dtype, const NormArgs& a, bool rows16, int num_sms,
+int64_t norm_grad_blocks(int64_t T, int64_t H);
+// words: bytes of a vector of the dtype that all rows allow: 16, 4, or 0 (element by element).
+cudaError_t launch_block_norm(int dtype, const NormArgs& a, int words, int num_sms,
                               cudaStream_t stream);
-cudaError_t launch_block_norm_grad(int dtype, const NormArgs& a, bool rows16, int num_sms,
-                                   cudaStream_t stream);
+cudaError_t launch_block_norm_grad(int dtype, const NormArgs& a, int words, cudaStream_t stream);
 
 // ------------------------------------------------------------ the gradients' norm
 
@@ -96,14 +96,16 @@ struct ClipTable {
 };
 
 // One partial sum of squares a block into partial[0, blocks).
-int64_t clip_chunks(int64_t n);  // chunks of a tensor of n elements
+int64_t clip_chunks(int64_t n, int dtype);  // chunks of a tensor of n elements
 cudaError_t launch_clip_squares(const ClipTable& t, WsHeader* hdr, double* partial, int blocks,
                                 cudaStream_t stream);
 // norm = |scale| sqrt(sum of partial), in fp32.
 cudaError_t launch_clip_norm(const double* partial, int64_t count, float scale, float* norm,
                              cudaStream_t stream);
-// out = in * c, c = scale min(1, max_norm / (norm + eps)) (scale alone if norm is not finite).
-cudaError_t launch_clip_apply(const ClipTable& t, const float* norm, float max_norm, float eps,
-                              float scale, int blocks, cudaStream_t stream);
+// The norm as above, and out = in * c, c = scale min(1, max_norm / (norm + eps)) (scale alone if norm
+// is not finite).
+cudaError_t launch_clip_apply(const ClipTable& t, const double* partial, int64_t count,
+                              float max_norm, float eps, float scale, float* norm, int blocks,
+                              cudaStream_t stream);
 
 }  // namespace pgg

@@ -52,12 +52,17 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
   }
 }
 
-// V consecutive elements from element i on; V > 1 needs them 16-byte aligned (V elements of the
-// dtype are one or two 16-byte words).
+// V (1, 2, 4 or 8) consecutive elements from element i on, aligned to their size or to 16 bytes.
 template <int DT, int V>
 __device__ __forceinline__ void load(const void* p, int64_t i, float (&v)[V]) {
   if constexpr (V == 1) {
     v[0] = load1<DT>(p, i);
+  } else if constexpr (DT == PGG_F32 && V == 2) {
+    const float2 f = *reinterpret_cast<const float2*>(static_cast<const float*>(p) + i);
+    v[0] = f.x;
+    v[1] = f.y;
+  } else if constexpr (V == 2) {
+    unpack2<DT>(*reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(p) + i), v[0], v[1]);
   } else if constexpr (DT == PGG_F32) {
     const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
 #pragma unroll
@@ -85,6 +90,10 @@ template <int DT, int V>
 __device__ __forceinline__ void store(void* p, int64_t i, const float (&v)[V]) {
   if constexpr (V == 1) {
     store1<DT>(p, i, v[0]);
+  } else if constexpr (DT == PGG_F32 && V == 2) {
+    *reinterpret_cast<float2*>(static_cast<float*>(p) + i) = make_float2(v[0], v[1]);
+  } else if constexpr (V == 2) {
+    *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p) + i) = pack2<DT>(v[0], v[1]);
   } else if constexpr (DT == PGG_F32) {
     float4* q = reinterpret_cast<float4*>(static_cast<float*>(p) + i);
 #pragma unroll
