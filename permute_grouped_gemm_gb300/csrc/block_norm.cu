@@ -97,31 +97,50 @@ struct Rows {
   }
 };
 
-// Sums of K values over the block, the same bits in every thread. Two buffers in turn, so that one
-// barrier a call is enough.
+// Sums of K values (1, or up to 4) over the block, the same bits in every thread. Two buffers in
+// turn, so that one barrier a call is enough. Four values are added together: after two exchanges a
+// lane goes on with one of them, so that it takes 6 shuffles, not 20, before the barrier and 7 after.
 template <int K>
 struct BlockSum {
-  float part[2][32][K];
+  float part[2][32][K == 1 ? 1 : 4];
 };
 
 template <int K, int M>
 __device__ __forceinline__ void block_sum(BlockSum<M>* s, int* turn, float (&v)[K]) {
-  static_assert(K <= M, "room");
+  static_assert(K <= M && K != 2, "room, and values by one or three");
+  constexpr uint32_t kAll = 0xFFFFFFFFu;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  if constexpr (K == 1) {
 #pragma unroll
-  for (int i = 0; i < K; ++i)
+    for (int d = 16; d > 0; d >>= 1) v[0] += __shfl_xor_sync(kAll, v[0], d);
+    if (warps == 1) return;
+    if (lane == 0) s->part[*turn][warp][0] = v[0];
+    __syncthreads();
+    v[0] = lane < warps ? s->part[*turn][lane][0] : 0.0f;
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) v[i] += __shfl_xor_sync(0xFFFFFFFFu, v[i], d);
-  if (warps == 1) return;
-  if (lane == 0)
+    for (int d = 16; d > 0; d >>= 1) v[0] += __shfl_xor_sync(kAll, v[0], d);
+  } else {
+    // lane bit 0 picks values {0, 1} or {2, 3}, bit 1 one of the two
+    const float v2 = v[2], v3 = K > 3 ? v[K - 1] : 0.0f;
+    const bool b0 = lane & 1, b1 = lane & 2;
+    float x = (b0 ? v2 : v[0]) + __shfl_xor_sync(kAll, b0 ? v[0] : v2, 1);
+    float y = (b0 ? v3 : v[1]) + __shfl_xor_sync(kAll, b0 ? v[1] : v3, 1);
+    x = (b1 ? y : x) + __shfl_xor_sync(kAll, b1 ? x : y, 2);
 #pragma unroll
-    for (int i = 0; i < K; ++i) s->part[*turn][warp][i] = v[i];
-  __syncthreads();
+    for (int d = 4; d < 32; d *= 2) x += __shfl_xor_sync(kAll, x, d);
+    if (warps > 1) {
+      if (lane < 4) s->part[*turn][warp][lane] = x;
+      __syncthreads();
+      x = 0.0f;
+      for (int w = lane >> 2; w < warps; w += 8) x += s->part[*turn][w][lane & 3];
 #pragma unroll
-  for (int i = 0; i < K; ++i) {
-    v[i] = lane < warps ? s->part[*turn][lane][i] : 0.0f;
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) v[i] += __shfl_xor_sync(0xFFFFFFFFu, v[i], d);
+      for (int d = 4; d < 32; d *= 2) x += __shfl_xor_sync(kAll, x, d);
+    }
+    // lane 0: value 0, lane 2: value 1, lane 1: value 2, lane 3: value 3
+    v[0] = __shfl_sync(kAll, x, 0);
+    v[1] = __shfl_sync(kAll, x, 2);
+    v[2] = __shfl_sync(kAll, x, 1);
+    if constexpr (K > 3) v[K - 1] = __shfl_sync(kAll, x, 3);
   }
   *turn ^= 1;
 }
@@ -146,6 +165,55 @@ __device__ __forceinline__ void affine(const void* w, const void* b, bool f32, f
   }
 }
 
+// One parameter (a weight with its offset, or a channel's gate) of this thread's columns: P16: of the
+// rows' 16-bit dtype, kept packed in registers; else read each time. 1 where there is none.
+template <int DT, int V, int NV, bool P16>
+struct Param {
+  uint32_t raw[P16 ? NV : 1][P16 ? V / 2 : 1];
+  const void* p;
+  float offset;
+  bool f32;
+
+  __device__ __forceinline__ void init(const NormArgs& a, const void* param, float add, int n) {
+    p = param;
+    offset = add;
+    f32 = a.p_f32;
+    if constexpr (P16) {
+      if (!param) offset = 1.0f;
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const int q = j * blockDim.x + threadIdx.x;
+#pragma unroll
+        for (int c = 0; c < V / 2; ++c) raw[j][c] = 0;
+        if (param && q < n) {
+          const uint4 w = __ldg(static_cast<const uint4*>(param) + q);
+          raw[j][0] = w.x;
+          raw[j][1] = w.y;
+          raw[j][2] = w.z;
+          raw[j][3] = w.w;
+        }
+      }
+    }
+  }
+  __device__ __forceinline__ void get(int j, int q, float (&v)[V]) const {
+    if constexpr (P16) {
+#pragma unroll
+      for (int c = 0; c < V / 2; ++c) {
+        vec::unpack2<DT>(raw[j][c], v[2 * c], v[2 * c + 1]);
+        v[2 * c] += offset;
+        v[2 * c + 1] += offset;
+      }
+    } else if (p) {
+      vec::load_or_f32<DT, V>(p, f32, q * V, v);
+#pragma unroll
+      for (int c = 0; c < V; ++c) v[c] += offset;
+    } else {
+#pragma unroll
+      for (int c = 0; c < V; ++c) v[c] = 1.0f;
+    }
+  }
+};
+
 // The gate of V columns of a row.
 template <int DT, int V>
 __device__ __forceinline__ void gate_at(const NormArgs& a, int64_t t, int64_t i, float (&g)[V]) {
@@ -163,9 +231,9 @@ __device__ __forceinline__ void gate_at(const NormArgs& a, int64_t t, int64_t i,
 
 // ------------------------------------------------------------------ rows held by a block
 
-// (BIAS: some norm has one)
-template <int DT, int V, int NV, bool RING, bool BIAS, int THREADS>
-__global__ void __launch_bounds__(THREADS, 1) block_norm_kernel(const NormArgs a, const int ring) {
+// LEAN: rms norms or none, a gate of one number a channel or none.
+template <int DT, int V, int NV, bool RING, bool LEAN, bool P16, int THREADS>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS) block_norm_kernel(const NormArgs a, const int ring) {
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ BlockSum<1> s;
   int turn = 0, slot = 0;
@@ -179,33 +247,21 @@ __global__ void __launch_bounds__(THREADS, 1) block_norm_kernel(const NormArgs a
   rows.add(1, a.y, y_f32);
   for (int i = 0; RING && i < ring; ++i)
     rows.fetch(smem, i, blockIdx.x + static_cast<int64_t>(i) * gridDim.x, a.T);
-  // the post norm's factor and bias with a channel's gate, and the pre norm's
-  const bool by_row = a.gate_kind == PGG_GATE_FULL || a.gate_kind == PGG_GATE_TOKEN;
-  float f0[NV][V], b0[NV][V], f1[NV][V], b1[NV][V];
-#pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    const int q = j * blockDim.x + tid;
-    if (q >= n) continue;
-    affine<DT, V>(a.w_post, a.b_post, a.p_f32, a.weight_offset, q * V, f0[j], b0[j]);
-    affine<DT, V>(a.w_pre, a.b_pre, a.p_f32, a.weight_offset, q * V, f1[j], b1[j]);
-    if (a.gate_kind == PGG_GATE_CHANNEL) {
-      float g[V];
-      vec::load_or_f32<DT, V>(a.gate, a.p_f32, q * V, g);
-#pragma unroll
-      for (int c = 0; c < V; ++c) {
-        f0[j][c] *= g[c];
-        b0[j][c] *= g[c];
-      }
-    }
-  }
+  const bool by_row = !LEAN && (a.gate_kind == PGG_GATE_FULL || a.gate_kind == PGG_GATE_TOKEN);
+  const int post = LEAN && a.post != PGG_NORM_NONE ? PGG_NORM_RMS : a.post;
+  const bool layer = !LEAN && a.pre == PGG_NORM_LAYER;
+  Param<DT, V, NV, P16> f_post, f_pre, channel;
+  f_post.init(a, a.w_post, a.weight_offset, n);
+  f_pre.init(a, a.w_pre, a.weight_offset, n);
+  channel.init(a, a.gate_kind == PGG_GATE_CHANNEL ? a.gate : nullptr, 0.0f, n);
   for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
     if (RING) {  // (a group of copies a row: those of the `ring` - 1 rows behind may be pending)
       if (ring > 2) ptx::cp_async_wait<2>(); else if (ring == 2) ptx::cp_async_wait<1>(); else ptx::cp_async_wait<0>();
     }
     float mean = 0.0f, rstd = 1.0f;
-    if (a.post != PGG_NORM_NONE) {
+    if (post != PGG_NORM_NONE) {
       float sum[1];
-      if (a.post == PGG_NORM_LAYER) {
+      if (!LEAN && post == PGG_NORM_LAYER) {
         sum[0] = 0.0f;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
@@ -227,7 +283,10 @@ __global__ void __launch_bounds__(THREADS, 1) block_norm_kernel(const NormArgs a
         float y[V];
         rows.read(smem, slot, t, 1, q, y_f32, y);
 #pragma unroll
-        for (int c = 0; c < V; ++c) sum[0] = fmaf(y[c] - mean, y[c] - mean, sum[0]);
+        for (int c = 0; c < V; ++c) {
+          const float v = LEAN ? y[c] : y[c] - mean;
+          sum[0] = fmaf(v, v, sum[0]);
+        }
       }
       block_sum(&s, &turn, sum);
       rstd = 1.0f / sqrtf(sum[0] * inv_h + a.eps);
@@ -243,26 +302,27 @@ __global__ void __launch_bounds__(THREADS, 1) block_norm_kernel(const NormArgs a
       if (have_y) {
         float y[V];
         rows.read(smem, slot, t, 1, q, y_f32, y);
-        if (by_row) {
-          float g[V];
+        float f[V], g[V];
+        f_post.get(j, q, f);
+        if (by_row)
           gate_at<DT, V>(a, t, q * V, g);
+        else
+          channel.get(j, q, g);
+        if constexpr (LEAN) {
 #pragma unroll
-          for (int c = 0; c < V; ++c) {
-            const float u = (y[c] - mean) * rstd;
-            r[j][c] = fmaf(g[c], BIAS ? fmaf(u, f0[j][c], b0[j][c]) : u * f0[j][c], r[j][c]);
-          }
+          for (int c = 0; c < V; ++c) r[j][c] = fmaf(y[c] * rstd, f[c] * g[c], r[j][c]);
         } else {
+          float one[V], b[V];
+          affine<DT, V>(nullptr, a.b_post, a.p_f32, 0.0f, q * V, one, b);
 #pragma unroll
-          for (int c = 0; c < V; ++c) {
-            r[j][c] = fmaf((y[c] - mean) * rstd, f0[j][c], r[j][c]);
-            if (BIAS) r[j][c] += b0[j][c];
-          }
+          for (int c = 0; c < V; ++c)
+            r[j][c] = fmaf(g[c], fmaf((y[c] - mean) * rstd, f[c], b[c]), r[j][c]);
         }
       }
       if (a.r) vec::store<DT, V>(a.r, t * a.H + q * V, r[j]);
 #pragma unroll
       for (int c = 0; c < V; ++c)
-        sum[0] = a.pre == PGG_NORM_LAYER ? sum[0] + r[j][c] : fmaf(r[j][c], r[j][c], sum[0]);
+        sum[0] = layer ? sum[0] + r[j][c] : fmaf(r[j][c], r[j][c], sum[0]);
     }
     if (RING) {  // (a thread's copies go where it alone has read)
       rows.fetch(smem, slot, t + static_cast<int64_t>(ring) * gridDim.x, a.T);
@@ -271,7 +331,7 @@ __global__ void __launch_bounds__(THREADS, 1) block_norm_kernel(const NormArgs a
     if (a.pre == PGG_NORM_NONE) continue;
     block_sum(&s, &turn, sum);
     mean = 0.0f;
-    if (a.pre == PGG_NORM_LAYER) {
+    if (layer) {
       mean = sum[0] * inv_h;
       sum[0] = 0.0f;
 #pragma unroll
@@ -288,10 +348,16 @@ __global__ void __launch_bounds__(THREADS, 1) block_norm_kernel(const NormArgs a
     for (int j = 0; j < NV; ++j) {
       const int q = j * blockDim.x + tid;
       if (q >= n) continue;
+      float f[V];
+      f_pre.get(j, q, f);
+      if constexpr (LEAN) {
 #pragma unroll
-      for (int c = 0; c < V; ++c) {
-        const float u = (r[j][c] - mean) * rstd;
-        r[j][c] = BIAS ? fmaf(u, f1[j][c], b1[j][c]) : u * f1[j][c];
+        for (int c = 0; c < V; ++c) r[j][c] = r[j][c] * rstd * f[c];
+      } else {
+        float one[V], b[V];
+        affine<DT, V>(nullptr, a.b_pre, a.p_f32, 0.0f, q * V, one, b);
+#pragma unroll
+        for (int c = 0; c < V; ++c) r[j][c] = fmaf((r[j][c] - mean) * rstd, f[c], b[c]);
       }
       vec::store<DT, V>(a.h, t * a.H + q * V, r[j]);
     }
@@ -301,11 +367,12 @@ __global__ void __launch_bounds__(THREADS, 1) block_norm_kernel(const NormArgs a
 // Columns' sums that a block keeps: gate (channel), w_post, b_post, w_pre, b_pre.
 enum { kColGate, kColWPost, kColBPost, kColWPre, kColBPre, kCols };
 
-// (BIAS: there are sums for a bias)
-template <int DT, int V, int NV, bool RING, bool BIAS, int THREADS>
+// LEAN as above: no sums for a bias either.
+template <int DT, int V, int NV, bool RING, bool LEAN, bool P16, int THREADS>
 __global__ void __launch_bounds__(THREADS, 1)
     block_norm_grad_kernel(const NormArgs a, const int ring) {
   extern __shared__ __align__(16) uint8_t smem[];
+  constexpr bool BIAS = !LEAN;
   __shared__ BlockSum<4> s;
   int turn = 0, slot = 0;
   ptx::griddep_wait();
@@ -315,7 +382,9 @@ __global__ void __launch_bounds__(THREADS, 1)
   rows.n = static_cast<int>(a.H / V);
   const int n = rows.n, tid = threadIdx.x;
   const bool y_f32 = DT == PGG_F32 || a.y_f32, dh_f32 = DT == PGG_F32 || a.dh_f32;
-  const bool have_y = a.y != nullptr, pre = a.pre != PGG_NORM_NONE, token = a.gate_kind == PGG_GATE_TOKEN;
+  const bool have_y = a.y != nullptr, pre = a.pre != PGG_NORM_NONE;
+  const bool token = !LEAN && a.gate_kind == PGG_GATE_TOKEN;
+  const bool by_row = token || (!LEAN && a.gate_kind == PGG_GATE_FULL);
   rows.add(0, a.d_r, DT == PGG_F32);
   rows.add(1, a.y, y_f32);
   rows.add(2, pre ? a.d_h : nullptr, dh_f32);
@@ -324,9 +393,19 @@ __global__ void __launch_bounds__(THREADS, 1)
     rows.fetch(smem, i, blockIdx.x + static_cast<int64_t>(i) * gridDim.x, a.T);
   float col[BIAS ? kCols : 3][NV][V] = {};  // without BIAS: gate, w_post, w_pre
   constexpr int kWPre = BIAS ? kColWPre : 2;
-  // the factor of a column's norm (its bias: b)
-  auto factor = [&](const void* w, const void* bias, int q, float (&f)[V], float (&b)[V]) {
-    affine<DT, V>(w, bias, a.p_f32, a.weight_offset, q * V, f, b);
+  Param<DT, V, NV, P16> f_post, f_pre, channel;
+  f_post.init(a, a.w_post, a.weight_offset, n);
+  f_pre.init(a, a.w_pre, a.weight_offset, n);
+  channel.init(a, a.gate_kind == PGG_GATE_CHANNEL ? a.gate : nullptr, 0.0f, n);
+  auto bias_at = [&](int q, float (&b)[V]) {
+    float one[V];
+    affine<DT, V>(nullptr, BIAS ? a.b_post : nullptr, a.p_f32, 0.0f, q * V, one, b);
+  };
+  auto gate_of = [&](int64_t t, int j, int q, float (&g)[V]) {
+    if (by_row)
+      gate_at<DT, V>(a, t, q * V, g);
+    else
+      channel.get(j, q, g);
   };
   for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
     if (RING) {
@@ -334,7 +413,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     float mean = 0.0f, rstd = 1.0f, along = 0.0f, centre = 0.0f;
     if (pre) {
-      if (a.pre == PGG_NORM_LAYER) {
+      if (!LEAN && a.pre == PGG_NORM_LAYER) {
         float sum[1] = {0.0f};
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
@@ -353,25 +432,25 @@ __global__ void __launch_bounds__(THREADS, 1)
       for (int j = 0; j < NV; ++j) {
         const int q = j * blockDim.x + tid;
         if (q >= n) continue;
-        float r[V], dh[V], f[V], b[V];
+        float r[V], dh[V], f[V];
         rows.read(smem, slot, t, 3, q, DT == PGG_F32, r);
         rows.read(smem, slot, t, 2, q, dh_f32, dh);
-        factor(a.w_pre, nullptr, q, f, b);
+        f_pre.get(j, q, f);
 #pragma unroll
         for (int c = 0; c < V; ++c) {
-          const float v = r[c] - mean, u = dh[c] * f[c];
+          const float v = LEAN ? r[c] : r[c] - mean, u = dh[c] * f[c];
           sum[0] = fmaf(v, v, sum[0]);
           sum[1] = fmaf(u, v, sum[1]);
-          sum[2] += u;
+          if (!LEAN) sum[2] += u;
         }
       }
       block_sum(&s, &turn, sum);
       rstd = 1.0f / sqrtf(sum[0] * inv_h + a.eps);
       along = sum[1] * rstd * inv_h;
-      centre = a.pre == PGG_NORM_LAYER ? sum[2] * inv_h : 0.0f;
+      centre = !LEAN && a.pre == PGG_NORM_LAYER ? sum[2] * inv_h : 0.0f;
     }
     float mean_y = 0.0f;
-    if (a.post == PGG_NORM_LAYER) {
+    if (!LEAN && a.post == PGG_NORM_LAYER) {
       float sum[1] = {0.0f};
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
@@ -396,16 +475,17 @@ __global__ void __launch_bounds__(THREADS, 1)
       for (int c = 0; c < V; ++c) g[j][c] = 0.0f;
       if (a.d_r) rows.read(smem, slot, t, 0, q, DT == PGG_F32, g[j]);
       if (pre) {
-        float r[V], dh[V], f[V], b[V];
+        float r[V], dh[V], f[V];
         rows.read(smem, slot, t, 3, q, DT == PGG_F32, r);
         rows.read(smem, slot, t, 2, q, dh_f32, dh);
-        factor(a.w_pre, nullptr, q, f, b);
+        f_pre.get(j, q, f);
 #pragma unroll
         for (int c = 0; c < V; ++c) {
-          const float v = (r[c] - mean) * rstd;
+          const float v = (LEAN ? r[c] : r[c] - mean) * rstd;
           col[kWPre][j][c] = fmaf(dh[c], v, col[kWPre][j][c]);
           if constexpr (BIAS) col[kColBPre][j][c] += dh[c];
-          g[j][c] = fmaf(rstd, fmaf(dh[c], f[c], -fmaf(v, along, centre)), g[j][c]);
+          const float u = dh[c] * f[c];
+          g[j][c] = fmaf(rstd, LEAN ? fmaf(-v, along, u) : u - fmaf(v, along, centre), g[j][c]);
         }
       }
       float d[V];
@@ -415,15 +495,20 @@ __global__ void __launch_bounds__(THREADS, 1)
       if (have_y && (a.post != PGG_NORM_NONE || token)) {
         float y[V], f[V], b[V], gate[V];
         rows.read(smem, slot, t, 1, q, y_f32, y);
-        factor(a.w_post, a.b_post, q, f, b);
-        gate_at<DT, V>(a, t, q * V, gate);
+        f_post.get(j, q, f);
+        if (BIAS) bias_at(q, b);
+        gate_of(t, j, q, gate);
 #pragma unroll
         for (int c = 0; c < V; ++c) {
-          const float v = y[c] - mean_y, w = g[j][c] * f[c];
+          const float v = LEAN ? y[c] : y[c] - mean_y, w = g[j][c] * f[c];
           sum[0] = fmaf(v, v, sum[0]);
-          sum[1] = fmaf(token ? w : w * gate[c], v, sum[1]);
-          sum[2] = fmaf(w, gate[c], sum[2]);
-          if constexpr (BIAS) sum[3] = fmaf(g[j][c], b[c], sum[3]);
+          if constexpr (LEAN) {
+            sum[1] = fmaf(w * gate[c], v, sum[1]);
+          } else {
+            sum[1] = fmaf(token ? w : w * gate[c], v, sum[1]);
+            sum[2] = fmaf(w, gate[c], sum[2]);
+            sum[3] = fmaf(g[j][c], b[c], sum[3]);
+          }
         }
       }
     }
@@ -438,7 +523,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           if (tid == 0) static_cast<float*>(a.d_gate)[t] = fmaf(sum[1], rstd_y, sum[3]);
         }
         if (a.post != PGG_NORM_NONE) along_y = sum[1] * tg[0] * rstd_y * inv_h;
-        if (a.post == PGG_NORM_LAYER) centre_y = sum[2] * inv_h;
+        if (!LEAN && a.post == PGG_NORM_LAYER) centre_y = sum[2] * inv_h;
       }
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
@@ -446,19 +531,21 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (q >= n) continue;
         float y[V], f[V], b[V], gate[V], whole[V];
         rows.read(smem, slot, t, 1, q, y_f32, y);
-        factor(a.w_post, a.b_post, q, f, b);
-        gate_at<DT, V>(a, t, q * V, gate);
+        f_post.get(j, q, f);
+        if (BIAS) bias_at(q, b);
+        gate_of(t, j, q, gate);
 #pragma unroll
         for (int c = 0; c < V; ++c) {
-          const float v = (y[c] - mean_y) * rstd_y, d = g[j][c] * gate[c];
+          const float v = (LEAN ? y[c] : y[c] - mean_y) * rstd_y, d = g[j][c] * gate[c];
           whole[c] = g[j][c] * (BIAS ? fmaf(v, f[c], b[c]) : v * f[c]);
           col[kColGate][j][c] += whole[c];
           col[kColWPost][j][c] = fmaf(d, v, col[kColWPost][j][c]);
           if constexpr (BIAS) col[kColBPost][j][c] += d;
-          y[c] = rstd_y * fmaf(d, f[c], -fmaf(v, along_y, centre_y));
+          const float u = d * f[c];
+          y[c] = rstd_y * (LEAN ? fmaf(-v, along_y, u) : u - fmaf(v, along_y, centre_y));
         }
         vec::store<DT, V>(a.h, t * a.H + q * V, y);
-        if (a.gate_kind == PGG_GATE_FULL) {
+        if (!LEAN && a.gate_kind == PGG_GATE_FULL) {
           if (DT == PGG_F32 || a.p_f32)
             vec::store<PGG_F32, V>(a.d_gate, t * a.H + q * V, whole);
           else
@@ -575,7 +662,7 @@ __global__ void __launch_bounds__(kMaxThreads) block_norm_grad_long_kernel(const
     const Stat pre = stats_of(&s, &turn, a.pre, a.H, a.eps, r);
     float along = 0.0f, centre = 0.0f;
     if (a.pre != PGG_NORM_NONE) {
-      float sum[2] = {0.0f, 0.0f};
+      float sum[3] = {0.0f, 0.0f, 0.0f};
       for (int64_t i = threadIdx.x; i < a.H; i += blockDim.x) {
         const float d = at<DT>(a.d_h, a.dh_f32, t0 + i), v = (r(i) - pre.mean) * pre.rstd;
         keep(kColWPre, i, d * v);
@@ -724,10 +811,16 @@ cudaError_t launch_rows(SmemLimit* limit, K kern, int64_t grid, int threads, int
                     static_cast<size_t>(smem), stream, 1, a, ring);
 }
 
-template <int DT, int V, int NV, bool BIAS, int THREADS>
+// Rms norms or none, a channel's gate or none: the kernels' short form.
+bool lean(const NormArgs& a) {
+  return a.post != PGG_NORM_LAYER && a.pre != PGG_NORM_LAYER &&
+         (a.gate_kind == PGG_GATE_NONE || a.gate_kind == PGG_GATE_CHANNEL);
+}
+
+template <int DT, int V, int NV, bool LEAN, bool P16, int THREADS>
 cudaError_t launch_forward_t(const NormArgs& a, int threads, int num_sms, cudaStream_t stream) {
   constexpr bool kHeld = V >= 4;
-  auto kern = block_norm_kernel<DT, V, NV, kHeld, BIAS, THREADS>;
+  auto kern = block_norm_kernel<DT, V, NV, kHeld, LEAN, P16, THREADS>;
   static Fit fit;
   static SmemLimit limit;
   int blocks;
@@ -741,50 +834,65 @@ cudaError_t launch_forward_t(const NormArgs& a, int threads, int num_sms, cudaSt
   return launch_rows(&limit, kern, a.T < most ? a.T : most, threads, ring * row, stream, a, ring);
 }
 
+template <int DT, int V, int NV, int THREADS>
+cudaError_t launch_forward_f(const NormArgs& a, int threads, int num_sms, cudaStream_t stream) {
+  if constexpr (V == 8 && NV <= 2) {  // (more would not leave four blocks an SM)
+    if (lean(a) && !a.p_f32)
+      return launch_forward_t<DT, V, NV, true, true, THREADS>(a, threads, num_sms, stream);
+  }
+  if (V >= 4 && lean(a))
+    return launch_forward_t<DT, V, NV, V >= 4, false, THREADS>(a, threads, num_sms, stream);
+  return launch_forward_t<DT, V, NV, false, false, THREADS>(a, threads, num_sms, stream);
+}
+
 template <int DT, int V>
 cudaError_t launch_forward(const NormArgs& a, int num_sms, cudaStream_t stream) {
   int nv, threads;
-  const bool bias = a.b_post || a.b_pre;
   if (shape(a.H / V, &nv, &threads) && (V < 4 || forward_bytes<DT>(a) <= kRingBytes)) {
-    if (nv == 1)
-      return bias ? launch_forward_t<DT, V, 1, true, 256>(a, threads, num_sms, stream)
-                  : launch_forward_t<DT, V, 1, false, 256>(a, threads, num_sms, stream);
-    if (nv == 2)
-      return bias ? launch_forward_t<DT, V, 2, true, 512>(a, threads, num_sms, stream)
-                  : launch_forward_t<DT, V, 2, false, 512>(a, threads, num_sms, stream);
-    return bias ? launch_forward_t<DT, V, 4, true, 512>(a, threads, num_sms, stream)
-                : launch_forward_t<DT, V, 4, false, 512>(a, threads, num_sms, stream);
+    if (nv == 1) return launch_forward_f<DT, V, 1, 256>(a, threads, num_sms, stream);
+    if (nv == 2) return launch_forward_f<DT, V, 2, 512>(a, threads, num_sms, stream);
+    return launch_forward_f<DT, V, 4, 512>(a, threads, num_sms, stream);
   }
   const int64_t grid = a.T < 2 * num_sms ? a.T : 2 * num_sms;
   return launch_pdl(block_norm_long_kernel<DT>, dim3(static_cast<unsigned>(grid)),
                     dim3(kMaxThreads), 0, stream, 1, a);
 }
 
-template <int DT, int V, int NV, bool BIAS, int THREADS>
+template <int DT, int V, int NV, bool LEAN, bool P16, int THREADS>
 cudaError_t launch_backward_t(const NormArgs& a, int threads, cudaStream_t stream) {
   constexpr bool kHeld = V >= 4;
   static SmemLimit limit;
   const int64_t row = backward_bytes<DT>(a), blocks = norm_grad_blocks(a.T, a.H);
   const int ring = kHeld ? ring_rows(row, static_cast<int>((blocks + 151) / 152)) : 0;
-  return launch_rows(&limit, block_norm_grad_kernel<DT, V, NV, kHeld, BIAS, THREADS>, blocks,
+  return launch_rows(&limit, block_norm_grad_kernel<DT, V, NV, kHeld, LEAN, P16, THREADS>, blocks,
                      threads, ring * row, stream, a, ring);
+}
+
+template <int DT, int V, int NV, int THREADS>
+cudaError_t launch_backward_f(const NormArgs& a, int threads, cudaStream_t stream) {
+  if constexpr (V == 8) {
+    if (lean(a) && !a.p_f32)
+      return launch_backward_t<DT, V, NV, true, true, THREADS>(a, threads, stream);
+  }
+  if (V >= 4 && lean(a))
+    return launch_backward_t<DT, V, NV, V >= 4, false, THREADS>(a, threads, stream);
+  return launch_backward_t<DT, V, NV, false, false, THREADS>(a, threads, stream);
 }
 
 template <int DT, int V>
 cudaError_t launch_backward(const NormArgs& a, cudaStream_t stream) {
-  const bool bias = a.b_post || a.b_pre;
-  int nv, threads;
+  const int64_t n = a.H / V;
   cudaError_t err;
-  if (shape(a.H / V, &nv, &threads) && (V < 4 || backward_bytes<DT>(a) <= kRingBytes)) {
+  // two vectors a thread (four: the columns' sums no longer fit the registers)
+  const int nv = n <= 256 ? 1 : n <= 1024 ? 2 : 4;
+  const int threads = static_cast<int>(((n + nv - 1) / nv + 31) / 32 * 32);
+  if (threads <= 512 && (V < 4 || backward_bytes<DT>(a) <= kRingBytes)) {
     if (nv == 1)
-      err = bias ? launch_backward_t<DT, V, 1, true, 256>(a, threads, stream)
-                 : launch_backward_t<DT, V, 1, false, 256>(a, threads, stream);
+      err = launch_backward_f<DT, V, 1, 256>(a, threads, stream);
     else if (nv == 2)
-      err = bias ? launch_backward_t<DT, V, 2, true, 512>(a, threads, stream)
-                 : launch_backward_t<DT, V, 2, false, 512>(a, threads, stream);
+      err = launch_backward_f<DT, V, 2, 512>(a, threads, stream);
     else
-      err = bias ? launch_backward_t<DT, V, 4, true, 512>(a, threads, stream)
-                 : launch_backward_t<DT, V, 4, false, 512>(a, threads, stream);
+      err = launch_backward_f<DT, V, 4, 512>(a, threads, stream);
   } else {
     err = launch_pdl(block_norm_grad_long_kernel<DT>,
                      dim3(static_cast<unsigned>(norm_grad_blocks(a.T, a.H))), dim3(kMaxThreads), 0,
