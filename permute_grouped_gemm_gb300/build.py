@@ -32,7 +32,7 @@ SOURCES = ["pgg_api.cu", "route_prep.cu", "gmm_dx.cu", "gmm_dx_simt.cu", "gmm_dw
            "gmm_dx_owner.cu", "ops_api.cu", "router.cu", "router_scores.cu", "ops_prep.cu",
            "ops_simt.cu",
            "gated_grad.cu", "rows_wide.cu",
-           "rows_skinny.cu", "adapters_few.cu", "rows_outer.cu", "block_api.cu", "w4_simt.cu", "w4_stream.cu",
+           "rows_skinny.cu", "adapters_few.cu", "rows_outer.cu", "block_api.cu", "w4_simt.cu", "w4_stream.cu", "w4_wide.cu",
            "block_norm.cu", "grad_clip.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

@@ -26,8 +26,12 @@ int status_of(cudaError_t e) { return e == cudaSuccess ? PGG_OK : PGG_ERR_CUDA; 
 // ---------------------------------------------------------------- 4-bit experts
 
 constexpr int kSimtRows = 32;
+constexpr int kVariantWide = 0;    // tensor cores, row blocks of up to 256 rows
 constexpr int kVariantStream = 1;  // tensor cores, the codes streamed for blocks of 8 to 32 rows
 constexpr int kVariantSimt = 3;    // FP32 pipes: any dtype, size and alignment
+
+// Up to this many rows per live expert the codes are streamed.
+constexpr double kStreamRows = 32.0;
 
 struct W4Plan {
   int variant;
@@ -59,6 +63,11 @@ int w4_plan(int product, int64_t M, int64_t N, int64_t K, int64_t G, int64_t L, 
     const double rows = M / live, most = rows + 2.8 * std::sqrt(rows);
     const double want = most < batch ? most : static_cast<double>(batch);
     p->rows_per_block = want <= 8 ? 8 : want <= 16 ? 16 : 32;
+    const int forced = forced_variant();
+    if (forced == kVariantWide || (forced != kVariantStream && rows > kStreamRows)) {
+      p->variant = kVariantWide;
+      p->rows_per_block = kW4WideRows;
+    }
   }
   p->max_row_blocks = (M + p->rows_per_block - 1) / p->rows_per_block + (G < M ? G : M);
   if (p->max_row_blocks * ((N + 31) / 32) > kInt32Max) return PGG_ERR_SHAPE;  // 32-bit tile numbers
@@ -72,9 +81,13 @@ int w4_plan(int product, int64_t M, int64_t N, int64_t K, int64_t G, int64_t L, 
   p->rowinfo = take(static_cast<int64_t>(sizeof(RowInfo)) * M);
   p->inv = take(4 * M);
   p->rows = take(product == PGG_W4_COMBINED ? 4 * M * N : 0);
-  const bool stream = p->variant == kVariantStream;
-  p->packed = take(stream ? w4_packed_bytes(p->max_row_blocks, p->rows_per_block, K) : 0);
-  p->exponent = take(stream ? p->max_row_blocks * p->rows_per_block * 4 : 0);
+  const bool stream = p->variant == kVariantStream, wide = p->variant == kVariantWide;
+  p->packed = take(stream ? w4_packed_bytes(p->max_row_blocks, p->rows_per_block, K)
+                   : wide ? w4_packed_wide_bytes(M, p->max_row_blocks, K)
+                          : 0);
+  p->exponent = take(stream ? p->max_row_blocks * p->rows_per_block * 4
+                     : wide ? w4_packed_wide_rows(M, p->max_row_blocks) * 4
+                            : 0);
   p->parts = take(stream ? 2ll * kW4Grid * p->rows_per_block * 128 * 4 : 0);
   p->arrived = take(stream ? kW4Grid * 4 : 0);
   p->total = used;
@@ -306,7 +319,9 @@ int pgg_w4_execute(pgg_w4_product product, const void* x, const uint8_t* codes,
   pr.row_idx_type = rowIdxType;
   pr.rows_per_block = p.rows_per_block;
   // the tensor cores need 16-byte aligned rows; the FP32 pipes take any row blocks
-  const bool stream_rows = p.variant == kVariantStream && aligned(x, 16) && aligned(codes, 16);
+  const bool tensor = p.variant != kVariantSimt && aligned(x, 16) && aligned(codes, 16);
+  const bool stream_rows = tensor && p.variant == kVariantStream;
+  pr.even = tensor && p.variant == kVariantWide;
   if (stream_rows) {
     pr.clear = reinterpret_cast<uint32_t*>(w + p.arrived);
     pr.n_clear = kW4Grid;
@@ -337,9 +352,11 @@ int pgg_w4_execute(pgg_w4_product product, const void* x, const uint8_t* codes,
   a.scale_f32 = scale_dtype == PGG_F32;
   a.out_f32 = out_dtype == PGG_F32;
   a.wait_limit_ns = env.wait_limit_ns;
-  if (stream_rows) {
-    a.packed = w + p.packed;
-    a.exponent = reinterpret_cast<int32_t*>(w + p.exponent);
+  a.packed = w + p.packed;
+  a.exponent = reinterpret_cast<int32_t*>(w + p.exponent);
+  if (tensor && !stream_rows) {
+    rc = status_of(launch_w4_wide(dtype, a, env.num_sms, s));
+  } else if (stream_rows) {
     a.parts = reinterpret_cast<float*>(w + p.parts);
     a.arrived = reinterpret_cast<uint32_t*>(w + p.arrived);
     a.pairs = N % 2 == 0 && aligned(a.out, 2 * elem_size(out_dtype));

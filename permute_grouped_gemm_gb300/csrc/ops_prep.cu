@@ -67,8 +67,12 @@ __device__ bool build_row_blocks(const RowsPrepArgs& a) {
   for (int64_t g0 = 0; ok && g0 < a.G; g0 += blockDim.x) {
     const int64_t g = g0 + threadIdx.x;
     const uint32_t c = g < a.G ? static_cast<uint32_t>(a.groups[g]) : 0u;
-    const uint32_t rpb = static_cast<uint32_t>(a.rows_per_block);
-    const uint32_t nb = (c + rpb - 1) / rpb;
+    uint32_t rpb = static_cast<uint32_t>(a.rows_per_block);
+    uint32_t nb = (c + rpb - 1) / rpb;
+    if (a.even && nb > 1) {  // (never more blocks than of full size)
+      rpb = ((c + nb - 1) / nb + 15) / 16 * 16;
+      nb = (c + rpb - 1) / rpb;
+    }
     uint32_t tot_c, tot_b;
     const uint32_t row0 = rows + block_scan_u32(c, s_scan, &tot_c);
     const uint32_t b0 = blocks + block_scan_u32(nb, s_scan, &tot_b);

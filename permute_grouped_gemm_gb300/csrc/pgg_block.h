@@ -48,6 +48,12 @@ cudaError_t launch_w4_simt(int dtype, const W4Args& a, int num_sms, cudaStream_t
 cudaError_t launch_w4_combine(const float* rows, const WsHeader* hdr, int64_t batch, int64_t top_k,
                               int64_t N, float* out, int num_sms, cudaStream_t stream);
 
+constexpr int kW4WideRows = 192;  // most rows of a block of the tensor-core kernel
+int64_t w4_packed_wide_rows(int64_t M, int64_t row_blocks);
+int64_t w4_packed_wide_bytes(int64_t M, int64_t row_blocks, int64_t K);
+// The same tensors, many rows an expert: row blocks of up to kW4WideRows rows.
+cudaError_t launch_w4_wide(int dtype, W4Args a, int num_sms, cudaStream_t stream);
+
 // ------------------------------------------------------------ norms around a block
 
 struct NormArgs {

@@ -91,6 +91,7 @@ struct RowsPrepArgs {
   int32_t* inv;      // [M]
   int64_t M, G;
   int32_t top_k, row_idx_type, rows_per_block;
+  int32_t even = 0;  // 1: a group's rows in blocks of like size, a multiple of 16 rows
   uint32_t* clear = nullptr;  // words that the launch sets to 0
   int32_t n_clear = 0;
 };
