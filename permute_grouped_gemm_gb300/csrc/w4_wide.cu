@@ -14,13 +14,12 @@
 // (panels of 64 k, 128-byte swizzle, pairs k + j, k + 4 + j) by a launch before
 // this one, so it arrives in plain pieces.
 //
-// The rows of a tile are two halves with an accumulator each: while one half's
-// sums are added up the other's products run. Tensor memory: two accumulators of
-// 128 columns, four A buffers (128 of k: 64 columns). Eight worker warps: four
-// lane quarters x two (half of a group's k when unpacking, half of the rows when
-// adding); they unpack two groups ahead, also across the tile's end, so that the
-// products go on while results are written. One warp copies, one issues the MMAs.
-// Waits are bounded as everywhere.
+// Tensor memory: two accumulators of up to 192 columns, two A buffers (128 of k:
+// 64 columns). While a group's products run, the sixteen worker warps (four lane
+// quarters x four) add up the sums of the group before and unpack the codes of
+// the group behind, also across a tile's end, so that the products go on while
+// results are written. One warp copies, one issues the MMAs. Waits are bounded as
+// everywhere.
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -42,17 +41,18 @@ constexpr int kRows = kW4WideRows;    // most rows of a tile
 constexpr int kGroup = 128;           // of k: one A buffer, one stage of x
 constexpr int kSlotBytes = kTile * 128;           // codes of 256 of k
 constexpr int kStageBytes = kRows * kGroup * 2;   // x of 128 of k
-constexpr int kHalf = kRows / 2;       // most rows of a half: sums of a thread
-constexpr int kSlots = 2, kStages = 4, kBufs = 4;
-constexpr int kWorkers = 8;
+constexpr int kSlots = 2, kStages = 4;
+constexpr int kParts = 4;             // worker warps of a lane quarter
+constexpr int kChunks = kRows / 16 / kParts;  // of 16 rows, that a worker adds up
+constexpr int kWorkers = 4 * kParts;
 constexpr int kThreads = 32 * (2 + kWorkers);
-constexpr int kACols = 256;           // first tensor-memory column of the A buffers
+constexpr int kACols = 2 * kRows;     // first tensor-memory column of the A buffers
 
 struct Ctl {
   uint64_t cfull[kSlots], cempty[kSlots];  // codes
   uint64_t xfull[kStages], xempty[kStages];
-  uint64_t afull[kBufs], aempty[kBufs];
-  uint64_t dfull[2], dempty[2];
+  uint64_t afull[2];             // codes of a group are in tensor memory
+  uint64_t dfull[2], dempty[2];  // (a full accumulator also frees the A buffer of its group)
   uint64_t drain;
   uint32_t tmem_base;
   int abort;
@@ -64,7 +64,7 @@ static_assert(kSmem <= 227 * 1024, "shared memory");
 
 struct Tile {
   int64_t g, row0, n0, prow;  // prow: its first row in the packed x
-  int rows, rows16, n[2];     // rows of the halves, multiples of 16
+  int rows, rows16;
 };
 
 __device__ __forceinline__ int64_t packed_row(const int4& e, int64_t rb) {
@@ -87,8 +87,6 @@ __device__ __forceinline__ Tile tile_of(uint32_t t, const W4Args& a) {
   x.prow = packed_row(e, rb);
   x.rows = e.z;
   x.rows16 = (e.z + 15) / 16 * 16;
-  x.n[0] = (x.rows16 / 2 + 15) / 16 * 16;
-  x.n[1] = x.rows16 - x.n[0];
   return x;
 }
 
@@ -256,13 +254,13 @@ template <int U>
 __device__ void issuer(uint8_t* smem, Ctl* ctl, uint32_t tmem, const W4Args& a, const Walk& k) {
   volatile int* abort = &ctl->abort;
   uint8_t* xs = smem + kSlots * kSlotBytes;
-  int stage = 0, buf = 0;
-  uint32_t xphase = 0, aphase = 0, dphase[2] = {0, 0};
+  int stage = 0, buf = 0, acc = 0;
+  uint32_t xphase = 0, aphase = 0, dphase = 0;
   bool issued = false, failed = false;
   for (uint32_t t = k.first; t < k.total && !failed; t += k.step) {
     const Tile x = tile_of(t, a);
     const uint32_t panel = static_cast<uint32_t>(x.rows16) * 128;
-    const uint32_t idesc[2] = {ptx::idesc_make(0, kTile, x.n[0]), ptx::idesc_make(0, kTile, x.n[1])};
+    const uint32_t idesc = ptx::idesc_make(0, kTile, x.rows16);
     for (int g = 0; g < k.groups && !failed; ++g) {
       if (!ptx::mbar_wait(&ctl->xfull[stage], xphase, a.wait_limit_ns, abort) ||
           !ptx::mbar_wait(&ctl->afull[buf], aphase, a.wait_limit_ns, abort)) {
@@ -271,38 +269,33 @@ __device__ void issuer(uint8_t* smem, Ctl* ctl, uint32_t tmem, const W4Args& a, 
       }
       ptx::tc_fence_after_sync();
       const uint32_t xb = ptx::smem_addr(xs + stage * kStageBytes);
-      for (int u = 0; u < kGroup / U && !failed; ++u)
-        for (int h = 0; h < 2; ++h) {
-          if (x.n[h] == 0) continue;
-          if (!ptx::mbar_wait(&ctl->dempty[h], dphase[h] ^ 1u, a.wait_limit_ns, abort)) {
-            failed = true;
-            break;
-          }
-          dphase[h] ^= 1u;
-          ptx::tc_fence_after_sync();
-          const uint32_t half = xb + (h ? x.n[0] * 128 : 0);
-#pragma unroll
-          for (int kk = 0; kk < U / 16; ++kk) {
-            const int s = u * (U / 16) + kk;  // of 16 k
-            mma_tmem(tmem + 128 * h, tmem + kACols + 64 * buf + 8 * s,
-                     ptx::sdesc_sw128(half + (s >> 2) * panel) +
-                         static_cast<uint64_t>(((s & 3) * 32) >> 4),
-                     idesc[h], kk > 0 ? 1u : 0u);
-          }
-          issued = true;
-          ptx::mma_commit(&ctl->dfull[h]);
+      for (int u = 0; u < kGroup / U; ++u) {
+        if (!ptx::mbar_wait(&ctl->dempty[acc], dphase ^ 1u, a.wait_limit_ns, abort)) {
+          failed = true;
+          break;
         }
+        ptx::tc_fence_after_sync();
+#pragma unroll
+        for (int kk = 0; kk < U / 16; ++kk) {
+          const int s = u * (U / 16) + kk;  // of 16 k
+          mma_tmem(tmem + kRows * acc, tmem + kACols + 64 * buf + 8 * s,
+                   ptx::sdesc_sw128(xb + (s >> 2) * panel) +
+                       static_cast<uint64_t>(((s & 3) * 32) >> 4),
+                   idesc, kk > 0 ? 1u : 0u);
+        }
+        issued = true;
+        ptx::mma_commit(&ctl->dfull[acc]);
+        acc ^= 1;
+        if (acc == 0) dphase ^= 1u;
+      }
       if (failed) break;
-      ptx::mma_commit(&ctl->aempty[buf]);
       ptx::mma_commit(&ctl->xempty[stage]);
       if (++stage == kStages) {
         stage = 0;
         xphase ^= 1u;
       }
-      if (++buf == kBufs) {
-        buf = 0;
-        aphase ^= 1u;
-      }
+      buf ^= 1;
+      if (buf == 0) aphase ^= 1u;
     }
   }
   if (failed) {
@@ -357,10 +350,15 @@ __device__ __forceinline__ int64_t column_of(const W4Args& a, const Tile& x, int
   return x.n0 + l < a.N ? x.n0 + l : -1;
 }
 
-__device__ __forceinline__ float scale_at(const W4Args& a, int64_t i) {
-  if (a.scale_f32) return __ldg(static_cast<const float*>(a.scales) + i);
-  const uint16_t v = __ldg(static_cast<const uint16_t*>(a.scales) + i);
-  return a.bf16 ? __uint_as_float(static_cast<uint32_t>(v) << 16) : __half2float(__ushort_as_half(v));
+// A scale as it stands in memory (what converts it would wait for it), and as a number.
+__device__ __forceinline__ uint32_t raw_scale(const W4Args& a, int64_t i) {
+  return a.scale_f32 ? __ldg(static_cast<const uint32_t*>(a.scales) + i)
+                     : __ldg(static_cast<const uint16_t*>(a.scales) + i);
+}
+__device__ __forceinline__ float scale_of(const W4Args& a, uint32_t v) {
+  if (a.scale_f32) return __uint_as_float(v);
+  return a.bf16 ? __uint_as_float(v << 16)
+                : __half2float(__ushort_as_half(static_cast<uint16_t>(v)));
 }
 
 template <int U>
@@ -373,11 +371,12 @@ struct Worker {
   int lane, quarter, part, l;  // l: lane of the tile
   bool gated;
   int64_t columns;
-  // unpacking, two groups ahead of the sums
+  // unpacking, a group ahead of the sums
   uint32_t t_next;
   int g_next, slot, buf;
-  uint32_t cphase, aphase;
+  uint32_t cphase;
   int64_t at_next;
+  uint32_t zero;    // of the next group's part of the k
   bool failed;
 
   __device__ __forceinline__ int64_t first_scale(const Tile& x) const {
@@ -394,50 +393,50 @@ struct Worker {
       raise_status(a.hdr, kStTimeout, site);
     }
   }
+  // What the next unpack_next() needs from memory.
+  __device__ __forceinline__ void look_ahead() {
+    if (t_next >= k.total || failed) return;
+    if (g_next == 0 && a.zeros) at_next = first_scale(tile_of(t_next, a));
+    zero = 8;
+    if (a.zeros) {
+      const uint32_t group = group_of((g_next * kGroup + part * 32) / U);
+      zero = group < static_cast<uint32_t>(a.groups) ? __ldg(a.zeros + at_next + group) : 0;
+    }
+  }
 
-  // 64 of k of this thread's column into the next A buffer.
+  // 32 of k of this thread's column into the next A buffer: four words, 16 columns of tensor memory.
+  // (The buffer is free: the sums of the group before the last have been added up.)
   __device__ __forceinline__ void unpack_next() {
     if (t_next >= k.total || failed) return;
-    if (g_next == 0) at_next = first_scale(tile_of(t_next, a));
-    uint32_t z0[2], z1[2];  // zero 2^-24 and 2^-20, of the two halves of the 64 of k
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      uint32_t z = 8;
-      if (a.zeros) {
-        const uint32_t group = group_of((g_next * kGroup + part * 64 + i * 32) / U);
-        z = group < static_cast<uint32_t>(a.groups) ? __ldg(a.zeros + at_next + group) : 0;
-      }
-      z0[i] = __half_as_ushort(__float2half_rn(z * 0x1p-24f)) * 0x10001u;
-      z1[i] = __half_as_ushort(__float2half_rn(z * 0x1p-20f)) * 0x10001u;
-    }
     volatile int* abort = &ctl->abort;
-    const bool ok = ptx::mbar_wait(&ctl->cfull[slot], cphase, a.wait_limit_ns, abort) &&
-                    ptx::mbar_wait(&ctl->aempty[buf], aphase ^ 1u, a.wait_limit_ns, abort);
-    if (!__all_sync(0xFFFFFFFFu, ok)) return give_up(187);
-    ptx::tc_fence_after_sync();
-    const int row = code_row(gated, l), chunk = (g_next & 1) * 4 + part * 2;
-    const uint32_t base = codes + slot * kSlotBytes + row * 128;
+    if (!__all_sync(0xFFFFFFFFu, ptx::mbar_wait(&ctl->cfull[slot], cphase, a.wait_limit_ns, abort)))
+      return give_up(187);
+    const int row = code_row(gated, l), chunk = (g_next & 1) * 4 + part;
+    const uint4 q = lds128(codes + slot * kSlotBytes + row * 128 + ((chunk ^ (row & 7)) << 4));
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+    // zero 2^-24 and 2^-20
+    const uint32_t z0 = __half_as_ushort(__float2half_rn(zero * 0x1p-24f)) * 0x10001u;
+    const uint32_t z1 = __half_as_ushort(__float2half_rn(zero * 0x1p-20f)) * 0x10001u;
+    uint32_t v[16];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {  // 32 of k: four words, 16 columns of tensor memory
-      const uint4 q = lds128(base + (((chunk + i) ^ (row & 7)) << 4));
-      const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-      uint32_t v[16];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint32_t hi = w[j] >> 8;
-        v[4 * j] = sub2(w[j] & 0x000F000Fu, z0[i]);
-        v[4 * j + 1] = sub2(w[j] & 0x00F000F0u, z1[i]);
-        v[4 * j + 2] = sub2(hi & 0x000F000Fu, z0[i]);
-        v[4 * j + 3] = sub2(hi & 0x00F000F0u, z1[i]);
-      }
-      tmem_st_x16(tmem + (static_cast<uint32_t>(32 * quarter) << 16) + kACols + 64 * buf +
-                      32 * part + 16 * i,
-                  v);
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t hi = w[j] >> 8;
+      v[4 * j] = sub2(w[j] & 0x000F000Fu, z0);
+      v[4 * j + 1] = sub2(w[j] & 0x00F000F0u, z1);
+      v[4 * j + 2] = sub2(hi & 0x000F000Fu, z0);
+      v[4 * j + 3] = sub2(hi & 0x00F000F0u, z1);
     }
+    tmem_st_x16(tmem + (static_cast<uint32_t>(32 * quarter) << 16) + kACols + 64 * buf + 16 * part,
+                v);
+    const bool slot_done = (g_next & 1) || g_next + 1 == k.groups;
+    if (++g_next == k.groups) {
+      g_next = 0;
+      t_next += k.step;
+    }
+    look_ahead();
     ptx::tmem_st_wait();
     ptx::tc_fence_before_sync();
     __syncwarp();
-    const bool slot_done = (g_next & 1) || g_next + 1 == k.groups;
     if (lane == 0) {
       ptx::mbar_arrive(&ctl->afull[buf]);
       if (slot_done) ptx::mbar_arrive(&ctl->cempty[slot]);
@@ -446,14 +445,7 @@ struct Worker {
       slot = 0;
       cphase ^= 1u;
     }
-    if (++buf == kBufs) {
-      buf = 0;
-      aphase ^= 1u;
-    }
-    if (++g_next == k.groups) {
-      g_next = 0;
-      t_next += k.step;
-    }
+    buf ^= 1;
   }
 };
 
@@ -465,76 +457,79 @@ __device__ void worker(uint8_t* smem, Ctl* ctl, uint32_t tmem, int w, const W4Ar
   const int quarter = (threadIdx.x >> 5) & 3, part = w >> 2;
   const bool gated = a.product == PGG_W4_GATED;
   Worker<U> wk = {a, k, ctl, ptx::smem_addr(smem), tmem, lane, quarter, part, 32 * quarter + lane,
-                  gated, gated ? 2 * a.N : a.N, k.first, 0, 0, 0, 0u, 0u, 0, false};
+                  gated, gated ? 2 * a.N : a.N, k.first, 0, 0, 0, 0u, 0, 8u, false};
   volatile int* abort = &ctl->abort;
-  const uint32_t d_tmem = tmem + (static_cast<uint32_t>(32 * quarter) << 16) + 128 * part;
+  const uint32_t d_tmem = tmem + (static_cast<uint32_t>(32 * quarter) << 16) + 16 * part;
+  int acc = 0;
   uint32_t dphase = 0;
-  wk.unpack_next();
+  wk.look_ahead();
   wk.unpack_next();
   for (uint32_t t = k.first; t < k.total && !wk.failed; t += k.step) {
     const Tile x = tile_of(t, a);
-    const int mine = x.n[part];
     const int64_t at = wk.first_scale(x);
-    float sum[kHalf];
+    uint32_t s_next = raw_scale(a, at);
+    float sum[kChunks][16];
 #pragma unroll
-    for (int i = 0; i < kHalf; ++i) sum[i] = 0.0f;
+    for (int c = 0; c < kChunks; ++c)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) sum[c][i] = 0.0f;
     for (int g = 0; g < k.groups; ++g) {
       wk.unpack_next();
 #pragma unroll
       for (int u = 0; u < kGroup / U; ++u) {
-        if (mine == 0) continue;
-        const uint32_t group = wk.group_of(g * (kGroup / U) + u);
+        const uint32_t unit = g * (kGroup / U) + u;
         // (x is 0 behind the last group, but 0 inf is not)
-        const float s = group < static_cast<uint32_t>(a.groups) ? scale_at(a, at + group) : 0.0f;
-        if (!wk.failed && !__all_sync(0xFFFFFFFFu, ptx::mbar_wait(&ctl->dfull[part], dphase,
+        const bool in = wk.group_of(unit) < static_cast<uint32_t>(a.groups);
+        const float s = in ? scale_of(a, s_next) : 0.0f;
+        const uint32_t next = wk.group_of(unit + 1);
+        if (next < static_cast<uint32_t>(a.groups)) s_next = raw_scale(a, at + next);
+        if (!wk.failed && !__all_sync(0xFFFFFFFFu, ptx::mbar_wait(&ctl->dfull[acc], dphase,
                                                                   a.wait_limit_ns, abort)))
           wk.give_up(188);
         if (wk.failed) break;
-        dphase ^= 1u;
         ptx::tc_fence_after_sync();
 #pragma unroll
-        for (int c = 0; c < kHalf / 32; ++c) {
-          if (32 * c >= mine) continue;
-          uint32_t v[32];
-          ptx::tmem_ld_32x32b_x32(d_tmem + 32 * c, v);
-          ptx::tmem_ld_wait_regs(v);
+        for (int c = 0; c < kChunks; ++c) {  // rows 64 c + 16 part ..
+          if (64 * c + 16 * part >= x.rows16) continue;
+          uint32_t v[16];
+          ptx::tmem_ld_32x32b_x16(d_tmem + kRows * acc + 64 * c, v);
+          ptx::tmem_ld_wait();
 #pragma unroll
-          for (int i = 0; i < 32; ++i)
-            sum[32 * c + i] = fmaf(s, __uint_as_float(v[i]), sum[32 * c + i]);
+          for (int i = 0; i < 16; ++i) sum[c][i] = fmaf(s, __uint_as_float(v[i]), sum[c][i]);
         }
         ptx::tc_fence_before_sync();
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(&ctl->dempty[part]);
+        if (lane == 0) ptx::mbar_arrive(&ctl->dempty[acc]);
+        acc ^= 1;
+        if (acc == 0) dphase ^= 1u;
       }
       if (wk.failed) break;
     }
     if (wk.failed) break;
-    // results: this thread's column of the rows of its half
+    // results: this thread's column of its rows
     const int64_t f = x.n0 + (gated ? wk.l >> 1 : wk.l);
     const bool writes = f < a.N && (!gated || (lane & 1) == 0);
-    const int j0 = part ? x.n[0] : 0;
 #pragma unroll
-    for (int c = 0; c < kHalf / 32; ++c) {
-      const int left = (part ? x.rows - j0 : (x.rows < x.n[0] ? x.rows : x.n[0])) - 32 * c;
+    for (int c = 0; c < kChunks; ++c) {
+      const int j0 = 64 * c + 16 * part, left = x.rows - j0;
       if (left <= 0) continue;
       // lane i holds what belongs to the chunk's row i
       int64_t out_row = 0;
       int e = 0;
       float p = 1.0f;
-      if (lane < left) {
-        const int64_t row = x.row0 + j0 + 32 * c + lane;
+      if (lane < 16 && lane < left) {
+        const int64_t row = x.row0 + j0 + lane;
         const int64_t pos = check_index(a.hdr, a.rowinfo[row].rank, a.M, 189);
         out_row = a.product == PGG_W4_COMBINED ? pos : row;
-        e = a.exponent[x.prow + j0 + 32 * c + lane] + 24;
+        e = a.exponent[x.prow + j0 + lane] + 24;
         if (gated && a.probs) p = a.probs[pos];
       }
       // 2^e in two factors (it may lie outside fp32)
       const float by0 = ldexpf(1.0f, e / 2), by1 = ldexpf(1.0f, e - e / 2);
 #pragma unroll
-      for (int i = 0; i < 32; ++i) {
+      for (int i = 0; i < 16; ++i) {
         if (i >= left) continue;
-        float v = sum[32 * c + i] * __shfl_sync(0xFFFFFFFFu, by0, i) *
-                  __shfl_sync(0xFFFFFFFFu, by1, i);
+        float v = sum[c][i] * __shfl_sync(0xFFFFFFFFu, by0, i) * __shfl_sync(0xFFFFFFFFu, by1, i);
         if (gated) {
           const float up = __shfl_xor_sync(0xFFFFFFFFu, v, 1);
           v = gate(v, up, __shfl_sync(0xFFFFFFFFu, p, i));
@@ -586,13 +581,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       ptx::mbar_init(&ctl->xfull[i], 1);
       ptx::mbar_init(&ctl->xempty[i], 1);
     }
-    for (int i = 0; i < kBufs; ++i) {
-      ptx::mbar_init(&ctl->afull[i], kWorkers);
-      ptx::mbar_init(&ctl->aempty[i], 1);
-    }
     for (int i = 0; i < 2; ++i) {
+      ptx::mbar_init(&ctl->afull[i], kWorkers);
       ptx::mbar_init(&ctl->dfull[i], 1);
-      ptx::mbar_init(&ctl->dempty[i], kWorkers / 2);
+      ptx::mbar_init(&ctl->dempty[i], kWorkers);
     }
     ptx::mbar_init(&ctl->drain, 1);
     ctl->abort = 0;
