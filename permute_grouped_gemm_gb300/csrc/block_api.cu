@@ -86,7 +86,7 @@ int w4_plan(int product, int64_t M, int64_t N, int64_t K, int64_t G, int64_t L, 
                    : wide ? w4_packed_wide_bytes(M, p->max_row_blocks, K)
                           : 0);
   p->exponent = take(stream ? p->max_row_blocks * p->rows_per_block * 4
-                     : wide ? w4_packed_wide_rows(M, p->max_row_blocks) * 4
+                     : wide ? w4_packed_wide_rows(M, p->max_row_blocks) * 16
                             : 0);
   p->parts = take(stream ? 2ll * kW4Grid * p->rows_per_block * 128 * 4 : 0);
   p->arrived = take(stream ? kW4Grid * 4 : 0);
@@ -354,6 +354,7 @@ int pgg_w4_execute(pgg_w4_product product, const void* x, const uint8_t* codes,
   a.wait_limit_ns = env.wait_limit_ns;
   a.packed = w + p.packed;
   a.exponent = reinterpret_cast<int32_t*>(w + p.exponent);
+  a.meta = reinterpret_cast<int4*>(w + p.exponent);
   if (tensor && !stream_rows) {
     rc = status_of(launch_w4_wide(dtype, a, env.num_sms, s));
   } else if (stream_rows) {

@@ -28,6 +28,7 @@ struct W4Args {
   // of the streaming kernel
   void* packed;          // the row blocks' rows of x in the products' order
   int32_t* exponent;     // [row blocks][rows of a block] their powers of two
+  int4* meta;            // (wide) of each packed row: {output row, power of two, weight, 0}
   float* parts;          // [2 kW4Grid][rows of a block][128] sums of the tiles that CTAs share
   uint32_t* arrived;     // [kW4Grid] parts of the tile that begins in a CTA; zeros at the start
   int32_t n_blocks;      // blocks of columns (set by the launch)

@@ -15,11 +15,13 @@
 // this one, so it arrives in plain pieces.
 //
 // Tensor memory: two accumulators of up to 192 columns, two A buffers (128 of k:
-// 64 columns). While a group's products run, the sixteen worker warps (four lane
-// quarters x four) add up the sums of the group before and unpack the codes of
-// the group behind, also across a tile's end, so that the products go on while
-// results are written. One warp copies, one issues the MMAs. Waits are bounded as
-// everywhere.
+// 64 columns). Roles: one warp copies, one issues the MMAs; eight unpack (four
+// lane quarters x even and odd groups, so that the latencies of a group's waits and
+// stores hide behind the other's); eight add up (four quarters x two halves of the
+// rows, up to 96 sums a thread, for which the warpgroups' registers are split
+// unevenly) and write the results, while the products of the next tile begin.
+// Unpacking and adding up in the same warps, one after the other, took 2100
+// cycles a group where this takes XX. Waits are bounded as everywhere.
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -42,17 +44,20 @@ constexpr int kGroup = 128;           // of k: one A buffer, one stage of x
 constexpr int kSlotBytes = kTile * 128;           // codes of 256 of k
 constexpr int kStageBytes = kRows * kGroup * 2;   // x of 128 of k
 constexpr int kSlots = 2, kStages = 4;
-constexpr int kParts = 4;             // worker warps of a lane quarter
-constexpr int kChunks = kRows / 16 / kParts;  // of 16 rows, that a worker adds up
-constexpr int kWorkers = 4 * kParts;
-constexpr int kThreads = 32 * (2 + kWorkers);
+constexpr int kChunks = kRows / 32;   // of 16 rows, that an adding warp takes
 constexpr int kACols = 2 * kRows;     // first tensor-memory column of the A buffers
+// Warpgroups: copies and MMAs; two that unpack; two that add. Registers a thread of each, which
+// draw on what the block is launched with.
+constexpr int kThreads = 5 * 128;
+constexpr int kLaunchRegs = 96, kFewRegs = 40, kUnpackRegs = 56, kAddRegs = 160;
+static_assert(128 * kFewRegs + 256 * kUnpackRegs + 256 * kAddRegs <= kThreads * kLaunchRegs,
+              "registers");
 
 struct Ctl {
   uint64_t cfull[kSlots], cempty[kSlots];  // codes
   uint64_t xfull[kStages], xempty[kStages];
-  uint64_t afull[2];             // codes of a group are in tensor memory
-  uint64_t dfull[2], dempty[2];  // (a full accumulator also frees the A buffer of its group)
+  uint64_t afull[2], aempty[2];  // codes of a group in tensor memory
+  uint64_t dfull[2], dempty[2];  // accumulators
   uint64_t drain;
   uint32_t tmem_base;
   int abort;
@@ -134,7 +139,12 @@ __global__ void __launch_bounds__(128) w4_pack_wide_kernel(const W4Args a) {
     exponent -= 15;
     const float by0 = ldexpf(1.0f, -(exponent / 2)), by1 = ldexpf(1.0f, -(exponent - exponent / 2));
     const int64_t prow = packed_row(e, rb);
-    if (tid == 0) a.exponent[prow + n] = exponent;
+    if (tid == 0) {  // what the results need to know of the row
+      const int64_t pos = check_index(a.hdr, a.rowinfo[row].rank, a.M, 189);
+      const float p = a.probs ? a.probs[pos] : 1.0f;
+      a.meta[prow + n] = make_int4(static_cast<int>(a.product == PGG_W4_COMBINED ? pos : row),
+                                   exponent + 24, __float_as_int(p), 0);
+    }
     char* out = static_cast<char*>(a.packed) + prow * width * 2;
     const int64_t panel = static_cast<int64_t>((e.z + 15) / 16 * 16) * 128;
     for (int64_t k = 8 * tid; k < width; k += 8 * 128) {
@@ -289,6 +299,7 @@ __device__ void issuer(uint8_t* smem, Ctl* ctl, uint32_t tmem, const W4Args& a, 
         if (acc == 0) dphase ^= 1u;
       }
       if (failed) break;
+      ptx::mma_commit(&ctl->aempty[buf]);
       ptx::mma_commit(&ctl->xempty[stage]);
       if (++stage == kStages) {
         stage = 0;
@@ -361,180 +372,181 @@ __device__ __forceinline__ float scale_of(const W4Args& a, uint32_t v) {
                 : __half2float(__ushort_as_half(static_cast<uint16_t>(v)));
 }
 
-template <int U>
-struct Worker {
-  const W4Args& a;
-  const Walk& k;
-  Ctl* ctl;
-  uint32_t codes;   // shared memory
-  uint32_t tmem;
-  int lane, quarter, part, l;  // l: lane of the tile
-  bool gated;
-  int64_t columns;
-  // unpacking, a group ahead of the sums
-  uint32_t t_next;
-  int g_next, slot, buf;
-  uint32_t cphase;
-  int64_t at_next;
-  uint32_t zero;    // of the next group's part of the k
-  bool failed;
-
-  __device__ __forceinline__ int64_t first_scale(const Tile& x) const {
-    const int64_t c = column_of(a, x, l);  // (a column that is not there: any scales)
-    return (x.g * columns + (c < 0 ? 0 : c)) * a.groups;
-  }
-  __device__ __forceinline__ uint32_t group_of(uint32_t unit) const {
-    return a.group == U ? unit : unit * U / static_cast<uint32_t>(a.group);
-  }
-  __device__ __forceinline__ void give_up(uint32_t site) {
-    failed = true;
-    if (lane == 0) {
-      ctl->abort = 1;
-      raise_status(a.hdr, kStTimeout, site);
-    }
-  }
-  // What the next unpack_next() needs from memory.
-  __device__ __forceinline__ void look_ahead() {
-    if (t_next >= k.total || failed) return;
-    if (g_next == 0 && a.zeros) at_next = first_scale(tile_of(t_next, a));
-    zero = 8;
-    if (a.zeros) {
-      const uint32_t group = group_of((g_next * kGroup + part * 32) / U);
-      zero = group < static_cast<uint32_t>(a.groups) ? __ldg(a.zeros + at_next + group) : 0;
-    }
-  }
-
-  // 32 of k of this thread's column into the next A buffer: four words, 16 columns of tensor memory.
-  // (The buffer is free: the sums of the group before the last have been added up.)
-  __device__ __forceinline__ void unpack_next() {
-    if (t_next >= k.total || failed) return;
-    volatile int* abort = &ctl->abort;
-    if (!__all_sync(0xFFFFFFFFu, ptx::mbar_wait(&ctl->cfull[slot], cphase, a.wait_limit_ns, abort)))
-      return give_up(187);
-    const int row = code_row(gated, l), chunk = (g_next & 1) * 4 + part;
-    const uint4 q = lds128(codes + slot * kSlotBytes + row * 128 + ((chunk ^ (row & 7)) << 4));
-    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-    // zero 2^-24 and 2^-20
-    const uint32_t z0 = __half_as_ushort(__float2half_rn(zero * 0x1p-24f)) * 0x10001u;
-    const uint32_t z1 = __half_as_ushort(__float2half_rn(zero * 0x1p-20f)) * 0x10001u;
-    uint32_t v[16];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint32_t hi = w[j] >> 8;
-      v[4 * j] = sub2(w[j] & 0x000F000Fu, z0);
-      v[4 * j + 1] = sub2(w[j] & 0x00F000F0u, z1);
-      v[4 * j + 2] = sub2(hi & 0x000F000Fu, z0);
-      v[4 * j + 3] = sub2(hi & 0x00F000F0u, z1);
-    }
-    tmem_st_x16(tmem + (static_cast<uint32_t>(32 * quarter) << 16) + kACols + 64 * buf + 16 * part,
-                v);
-    const bool slot_done = (g_next & 1) || g_next + 1 == k.groups;
-    if (++g_next == k.groups) {
-      g_next = 0;
-      t_next += k.step;
-    }
-    look_ahead();
-    ptx::tmem_st_wait();
-    ptx::tc_fence_before_sync();
-    __syncwarp();
-    if (lane == 0) {
-      ptx::mbar_arrive(&ctl->afull[buf]);
-      if (slot_done) ptx::mbar_arrive(&ctl->cempty[slot]);
-    }
-    if (slot_done && ++slot == kSlots) {
-      slot = 0;
-      cphase ^= 1u;
-    }
-    buf ^= 1;
-  }
-};
+// A lane's first scale in its column (a column that is not there: any scales).
+__device__ __forceinline__ int64_t first_scale(const W4Args& a, const Tile& x, int l) {
+  const int64_t c = column_of(a, x, l);
+  return (x.g * (a.product == PGG_W4_GATED ? 2 * a.N : a.N) + (c < 0 ? 0 : c)) * a.groups;
+}
 
 template <int U>
-__device__ void worker(uint8_t* smem, Ctl* ctl, uint32_t tmem, int w, const W4Args& a,
-                       const Walk& k) {
-  const int lane = threadIdx.x & 31;
-  // (a warp reaches the lanes of tensor memory of its place among four)
-  const int quarter = (threadIdx.x >> 5) & 3, part = w >> 2;
-  const bool gated = a.product == PGG_W4_GATED;
-  Worker<U> wk = {a, k, ctl, ptx::smem_addr(smem), tmem, lane, quarter, part, 32 * quarter + lane,
-                  gated, gated ? 2 * a.N : a.N, k.first, 0, 0, 0, 0u, 0, 8u, false};
+__device__ __forceinline__ uint32_t group_of(const W4Args& a, uint32_t unit) {
+  return a.group == U ? unit : unit * U / static_cast<uint32_t>(a.group);
+}
+
+// Groups `par`, par + 2, ... of this CTA's sequence of groups: the thread's column, 128 of k, into A
+// buffer par.
+template <int U>
+__device__ void unpacker(uint8_t* smem, Ctl* ctl, uint32_t tmem, int par, const W4Args& a,
+                         const Walk& k) {
+  constexpr int kZeros = U < kGroup ? kGroup / U : 1;  // of a column and group
   volatile int* abort = &ctl->abort;
-  const uint32_t d_tmem = tmem + (static_cast<uint32_t>(32 * quarter) << 16) + 16 * part;
+  const int lane = threadIdx.x & 31, quarter = (threadIdx.x >> 5) & 3, l = 32 * quarter + lane;
+  const int row = code_row(a.product == PGG_W4_GATED, l);
+  const uint32_t codes = ptx::smem_addr(smem) + row * 128;
+  const uint32_t a_tmem = tmem + (static_cast<uint32_t>(32 * quarter) << 16) + kACols + 64 * par;
+  // slots of codes: one for two groups of a tile
+  int slot = 0;
+  uint32_t cphase = 0, aphase = 0;
+  uint32_t turn = 0;  // of all groups
+  for (uint32_t t = k.first; t < k.total; t += k.step) {
+    const int64_t at = a.zeros ? first_scale(a, tile_of(t, a), l) : 0;
+    for (int g = 0; g < k.groups; ++g, ++turn) {
+      const bool slot_done = (g & 1) || g + 1 == k.groups;
+      if ((turn & 1) == static_cast<uint32_t>(par)) {
+        uint32_t zero[kZeros];
+#pragma unroll
+        for (int i = 0; i < kZeros; ++i) {
+          zero[i] = 8;
+          if (a.zeros) {
+            const uint32_t group = group_of<U>(a, g * (kGroup / U) + i);
+            zero[i] = group < static_cast<uint32_t>(a.groups) ? __ldg(a.zeros + at + group) : 0;
+          }
+        }
+        const bool ok = ptx::mbar_wait(&ctl->cfull[slot], cphase, a.wait_limit_ns, abort) &&
+                        ptx::mbar_wait(&ctl->aempty[par], aphase ^ 1u, a.wait_limit_ns, abort);
+        if (!__all_sync(0xFFFFFFFFu, ok)) {
+          if (lane == 0) {
+            ctl->abort = 1;
+            raise_status(a.hdr, kStTimeout, 187);
+          }
+          return;
+        }
+        ptx::tc_fence_after_sync();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {  // 32 of k: four words, 16 columns of tensor memory
+          const int chunk = (g & 1) * 4 + i;
+          const uint4 q = lds128(codes + slot * kSlotBytes + ((chunk ^ (row & 7)) << 4));
+          const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+          const uint32_t z = zero[i * 32 / U < kZeros ? i * 32 / U : 0];
+          // zero 2^-24 and 2^-20
+          const uint32_t z0 = __half_as_ushort(__float2half_rn(z * 0x1p-24f)) * 0x10001u;
+          const uint32_t z1 = __half_as_ushort(__float2half_rn(z * 0x1p-20f)) * 0x10001u;
+          uint32_t v[16];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t hi = w[j] >> 8;
+            v[4 * j] = sub2(w[j] & 0x000F000Fu, z0);
+            v[4 * j + 1] = sub2(w[j] & 0x00F000F0u, z1);
+            v[4 * j + 2] = sub2(hi & 0x000F000Fu, z0);
+            v[4 * j + 3] = sub2(hi & 0x00F000F0u, z1);
+          }
+          tmem_st_x16(a_tmem + 16 * i, v);
+        }
+        ptx::tmem_st_wait();
+        ptx::tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) {
+          ptx::mbar_arrive(&ctl->afull[par]);
+          ptx::mbar_arrive(&ctl->cempty[slot]);
+        }
+        aphase ^= 1u;
+      } else if (slot_done && (g & 1) == 0) {
+        // a slot with one group: the other warps have nothing to read of it (but it has to be this
+        // use of the slot that they let go)
+        if (!__all_sync(0xFFFFFFFFu, ptx::mbar_wait(&ctl->cfull[slot], cphase, a.wait_limit_ns,
+                                                    abort))) {
+          if (lane == 0) {
+            ctl->abort = 1;
+            raise_status(a.hdr, kStTimeout, 190);
+          }
+          return;
+        }
+        if (lane == 0) ptx::mbar_arrive(&ctl->cempty[slot]);
+      }
+      if (slot_done && ++slot == kSlots) {
+        slot = 0;
+        cphase ^= 1u;
+      }
+    }
+  }
+}
+
+// Sums of the thread's column: 16-row chunks half, half + 2, ... of the tile's rows.
+template <int U>
+__device__ void adder(Ctl* ctl, uint32_t tmem, int half, const W4Args& a, const Walk& k) {
+  volatile int* abort = &ctl->abort;
+  const int lane = threadIdx.x & 31, quarter = (threadIdx.x >> 5) & 3, l = 32 * quarter + lane;
+  const bool gated = a.product == PGG_W4_GATED;
+  const uint32_t d_tmem = tmem + (static_cast<uint32_t>(32 * quarter) << 16) + 16 * half;
   int acc = 0;
   uint32_t dphase = 0;
-  wk.look_ahead();
-  wk.unpack_next();
-  for (uint32_t t = k.first; t < k.total && !wk.failed; t += k.step) {
+  for (uint32_t t = k.first; t < k.total; t += k.step) {
     const Tile x = tile_of(t, a);
-    const int64_t at = wk.first_scale(x);
+    const int64_t at = first_scale(a, x, l);
     uint32_t s_next = raw_scale(a, at);
     float sum[kChunks][16];
 #pragma unroll
     for (int c = 0; c < kChunks; ++c)
 #pragma unroll
       for (int i = 0; i < 16; ++i) sum[c][i] = 0.0f;
-    for (int g = 0; g < k.groups; ++g) {
-      wk.unpack_next();
-#pragma unroll
-      for (int u = 0; u < kGroup / U; ++u) {
-        const uint32_t unit = g * (kGroup / U) + u;
-        // (x is 0 behind the last group, but 0 inf is not)
-        const bool in = wk.group_of(unit) < static_cast<uint32_t>(a.groups);
-        const float s = in ? scale_of(a, s_next) : 0.0f;
-        const uint32_t next = wk.group_of(unit + 1);
-        if (next < static_cast<uint32_t>(a.groups)) s_next = raw_scale(a, at + next);
-        if (!wk.failed && !__all_sync(0xFFFFFFFFu, ptx::mbar_wait(&ctl->dfull[acc], dphase,
-                                                                  a.wait_limit_ns, abort)))
-          wk.give_up(188);
-        if (wk.failed) break;
-        ptx::tc_fence_after_sync();
-#pragma unroll
-        for (int c = 0; c < kChunks; ++c) {  // rows 64 c + 16 part ..
-          if (64 * c + 16 * part >= x.rows16) continue;
-          uint32_t v[16];
-          ptx::tmem_ld_32x32b_x16(d_tmem + kRows * acc + 64 * c, v);
-          ptx::tmem_ld_wait();
-#pragma unroll
-          for (int i = 0; i < 16; ++i) sum[c][i] = fmaf(s, __uint_as_float(v[i]), sum[c][i]);
+    const uint32_t units = k.groups * (kGroup / U);
+    for (uint32_t unit = 0; unit < units; ++unit) {
+      // (x is 0 behind the last group, but 0 inf is not)
+      const bool in = group_of<U>(a, unit) < static_cast<uint32_t>(a.groups);
+      const float s = in ? scale_of(a, s_next) : 0.0f;
+      const uint32_t next = group_of<U>(a, unit + 1);
+      if (next < static_cast<uint32_t>(a.groups)) s_next = raw_scale(a, at + next);
+      if (!__all_sync(0xFFFFFFFFu, ptx::mbar_wait(&ctl->dfull[acc], dphase, a.wait_limit_ns,
+                                                  abort))) {
+        if (lane == 0) {
+          ctl->abort = 1;
+          raise_status(a.hdr, kStTimeout, 188);
         }
-        ptx::tc_fence_before_sync();
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(&ctl->dempty[acc]);
-        acc ^= 1;
-        if (acc == 0) dphase ^= 1u;
+        return;
       }
-      if (wk.failed) break;
+      ptx::tc_fence_after_sync();
+      const uint32_t d = d_tmem + kRows * acc;
+#pragma unroll
+      for (int c = 0; c < kChunks; c += 2) {  // rows 32 c + 16 half ..
+        if (32 * c + 16 * half >= x.rows16) continue;
+        uint32_t v[2][16];
+        const bool two = 32 * (c + 1) + 16 * half < x.rows16;
+        ptx::tmem_ld_32x32b_x16(d + 32 * c, v[0]);
+        if (two) ptx::tmem_ld_32x32b_x16(d + 32 * (c + 1), v[1]);
+        ptx::tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < 16; ++i) sum[c][i] = fmaf(s, __uint_as_float(v[0][i]), sum[c][i]);
+        if (two)
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            sum[c + 1][i] = fmaf(s, __uint_as_float(v[1][i]), sum[c + 1][i]);
+      }
+      ptx::tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(&ctl->dempty[acc]);
+      acc ^= 1;
+      if (acc == 0) dphase ^= 1u;
     }
-    if (wk.failed) break;
     // results: this thread's column of its rows
-    const int64_t f = x.n0 + (gated ? wk.l >> 1 : wk.l);
+    const int64_t f = x.n0 + (gated ? l >> 1 : l);
     const bool writes = f < a.N && (!gated || (lane & 1) == 0);
 #pragma unroll
     for (int c = 0; c < kChunks; ++c) {
-      const int j0 = 64 * c + 16 * part, left = x.rows - j0;
+      const int j0 = 32 * c + 16 * half, left = x.rows - j0;
       if (left <= 0) continue;
-      // lane i holds what belongs to the chunk's row i
-      int64_t out_row = 0;
-      int e = 0;
-      float p = 1.0f;
-      if (lane < 16 && lane < left) {
-        const int64_t row = x.row0 + j0 + lane;
-        const int64_t pos = check_index(a.hdr, a.rowinfo[row].rank, a.M, 189);
-        out_row = a.product == PGG_W4_COMBINED ? pos : row;
-        e = a.exponent[x.prow + j0 + lane] + 24;
-        if (gated && a.probs) p = a.probs[pos];
-      }
+      int4 m = make_int4(0, 0, 0, 0);  // lane i holds what belongs to the chunk's row i
+      if (lane < 16 && lane < left) m = a.meta[x.prow + j0 + lane];
       // 2^e in two factors (it may lie outside fp32)
-      const float by0 = ldexpf(1.0f, e / 2), by1 = ldexpf(1.0f, e - e / 2);
+      const float by0 = ldexpf(1.0f, m.y / 2), by1 = ldexpf(1.0f, m.y - m.y / 2);
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         if (i >= left) continue;
         float v = sum[c][i] * __shfl_sync(0xFFFFFFFFu, by0, i) * __shfl_sync(0xFFFFFFFFu, by1, i);
         if (gated) {
           const float up = __shfl_xor_sync(0xFFFFFFFFu, v, 1);
-          v = gate(v, up, __shfl_sync(0xFFFFFFFFu, p, i));
+          v = gate(v, up, __int_as_float(__shfl_sync(0xFFFFFFFFu, m.z, i)));
         }
-        const int64_t to = __shfl_sync(0xFFFFFFFFu, out_row, i) * a.N + f;
+        const int64_t to = static_cast<int64_t>(__shfl_sync(0xFFFFFFFFu, m.x, i)) * a.N + f;
         if (!writes) continue;
         if (a.out_f32)
           static_cast<float*>(a.out)[to] = v;
@@ -545,6 +557,15 @@ __device__ void worker(uint8_t* smem, Ctl* ctl, uint32_t tmem, int w, const W4Ar
       }
     }
   }
+}
+
+template <int N>
+__device__ __forceinline__ void fewer_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void more_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
 
 template <int U>
@@ -575,16 +596,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < kSlots; ++i) {
       ptx::mbar_init(&ctl->cfull[i], 1);
-      ptx::mbar_init(&ctl->cempty[i], kWorkers);
+      ptx::mbar_init(&ctl->cempty[i], 8);
     }
     for (int i = 0; i < kStages; ++i) {
       ptx::mbar_init(&ctl->xfull[i], 1);
       ptx::mbar_init(&ctl->xempty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
-      ptx::mbar_init(&ctl->afull[i], kWorkers);
+      ptx::mbar_init(&ctl->afull[i], 4);
+      ptx::mbar_init(&ctl->aempty[i], 1);
       ptx::mbar_init(&ctl->dfull[i], 1);
-      ptx::mbar_init(&ctl->dempty[i], kWorkers);
+      ptx::mbar_init(&ctl->dempty[i], 8);
     }
     ptx::mbar_init(&ctl->drain, 1);
     ctl->abort = 0;
@@ -599,12 +621,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   ptx::tc_fence_after_sync();
   const uint32_t tmem = ctl->tmem_base;
-  if (warp == 0) {
-    if (lane == 0) copier(smem, ctl, &tm, a, k);
-  } else if (warp == 1) {
-    if (lane == 0) issuer<U>(smem, ctl, tmem, a, k);
+  const int wg = warp >> 2;
+  if (wg == 0) {
+    fewer_registers<kFewRegs>();
+    if (warp == 0 && lane == 0) copier(smem, ctl, &tm, a, k);
+    if (warp == 1 && lane == 0) issuer<U>(smem, ctl, tmem, a, k);
+  } else if (wg <= 2) {
+    fewer_registers<kUnpackRegs>();
+    unpacker<U>(smem, ctl, tmem, wg - 1, a, k);
   } else {
-    worker<U>(smem, ctl, tmem, warp - 2, a, k);
+    more_registers<kAddRegs>();
+    adder<U>(ctl, tmem, wg - 3, a, k);
   }
   ptx::tc_fence_before_sync();
   __syncthreads();
