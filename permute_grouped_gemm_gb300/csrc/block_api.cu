@@ -37,7 +37,7 @@ struct W4Plan {
   int variant;
   int rows_per_block;
   int64_t max_row_blocks;
-  size_t rblist, rowinfo, inv, rows, packed, exponent, parts, arrived, total;
+  size_t rblist, rowinfo, inv, rows, packed, exponent, col_exponent, parts, arrived, total;
 };
 
 int w4_plan(int product, int64_t M, int64_t N, int64_t K, int64_t G, int64_t L, int64_t batch,
@@ -66,7 +66,7 @@ int w4_plan(int product, int64_t M, int64_t N, int64_t K, int64_t G, int64_t L, 
     const int forced = forced_variant();
     if (forced == kVariantWide || (forced != kVariantStream && rows > kStreamRows)) {
       p->variant = kVariantWide;
-      p->rows_per_block = kW4WideRows;
+      p->rows_per_block = kW4SplitRows;  // (the smaller one, for the tables' sizes)
     }
   }
   p->max_row_blocks = (M + p->rows_per_block - 1) / p->rows_per_block + (G < M ? G : M);
@@ -88,6 +88,7 @@ int w4_plan(int product, int64_t M, int64_t N, int64_t K, int64_t G, int64_t L, 
   p->exponent = take(stream ? p->max_row_blocks * p->rows_per_block * 4
                      : wide ? w4_packed_wide_rows(M, p->max_row_blocks) * 16
                             : 0);
+  p->col_exponent = take(wide ? 4 * G * N * (product == PGG_W4_GATED ? 2 : 1) : 0);
   p->parts = take(stream ? 2ll * kW4Grid * p->rows_per_block * 128 * 4 : 0);
   p->arrived = take(stream ? kW4Grid * 4 : 0);
   p->total = used;
@@ -321,7 +322,10 @@ int pgg_w4_execute(pgg_w4_product product, const void* x, const uint8_t* codes,
   // the tensor cores need 16-byte aligned rows; the FP32 pipes take any row blocks
   const bool tensor = p.variant != kVariantSimt && aligned(x, 16) && aligned(codes, 16);
   const bool stream_rows = tensor && p.variant == kVariantStream;
-  pr.even = tensor && p.variant == kVariantWide;
+  if (tensor && !stream_rows) {
+    pr.rows_per_block = w4_wide_rows(dtype, scale_dtype == PGG_F32, zeros != nullptr);
+    pr.even = 1;
+  }
   if (stream_rows) {
     pr.clear = reinterpret_cast<uint32_t*>(w + p.arrived);
     pr.n_clear = kW4Grid;
@@ -355,8 +359,9 @@ int pgg_w4_execute(pgg_w4_product product, const void* x, const uint8_t* codes,
   a.packed = w + p.packed;
   a.exponent = reinterpret_cast<int32_t*>(w + p.exponent);
   a.meta = reinterpret_cast<int4*>(w + p.exponent);
+  a.col_exponent = reinterpret_cast<int32_t*>(w + p.col_exponent);
   if (tensor && !stream_rows) {
-    rc = status_of(launch_w4_wide(dtype, a, env.num_sms, s));
+    rc = status_of(launch_w4_wide(dtype, a, groupList, env.num_sms, s));
   } else if (stream_rows) {
     a.parts = reinterpret_cast<float*>(w + p.parts);
     a.arrived = reinterpret_cast<uint32_t*>(w + p.arrived);

@@ -28,6 +28,8 @@ struct W4Args {
   // of the streaming kernel
   void* packed;          // the row blocks' rows of x in the products' order
   int32_t* exponent;     // [row blocks][rows of a block] their powers of two
+  int32_t* col_exponent; // (wide) [G][C] the columns' powers of two
+  int32_t block_rows;    // (wide) most rows of a block (set by the launch)
   int4* meta;            // (wide) of each packed row: {output row, power of two, weight, 0}
   float* parts;          // [2 kW4Grid][rows of a block][128] sums of the tiles that CTAs share
   uint32_t* arrived;     // [kW4Grid] parts of the tile that begins in a CTA; zeros at the start
@@ -49,11 +51,14 @@ cudaError_t launch_w4_simt(int dtype, const W4Args& a, int num_sms, cudaStream_t
 cudaError_t launch_w4_combine(const float* rows, const WsHeader* hdr, int64_t batch, int64_t top_k,
                               int64_t N, float* out, int num_sms, cudaStream_t stream);
 
-constexpr int kW4WideRows = 192;  // most rows of a block of the tensor-core kernel
+// Most rows of a block of the tensor-core kernel; where its weights are the sum of two.
+constexpr int kW4WideRows = 192, kW4SplitRows = 128;
+int w4_wide_rows(int dtype, bool scale_f32, bool zeros);  // which
 int64_t w4_packed_wide_rows(int64_t M, int64_t row_blocks);
 int64_t w4_packed_wide_bytes(int64_t M, int64_t row_blocks, int64_t K);
-// The same tensors, many rows an expert: row blocks of up to kW4WideRows rows.
-cudaError_t launch_w4_wide(int dtype, W4Args a, int num_sms, cudaStream_t stream);
+// The same tensors, many rows an expert: row blocks of up to w4_wide_rows rows.
+cudaError_t launch_w4_wide(int dtype, W4Args a, const int64_t* group_list, int num_sms,
+                           cudaStream_t stream);
 
 // ------------------------------------------------------------ norms around a block
 

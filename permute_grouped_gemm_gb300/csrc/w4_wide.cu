@@ -1,27 +1,33 @@
 // Products with 4-bit expert weights, many rows an expert: the tensor cores are
 // the bound (tcgen05, 128 columns x up to 192 rows a tile).
 //
-//     D[column, row] = sum over a group of (code - zero) x,  sum += scale[column] D
+//     y[column, row] = sum over k of scale (code - zero) x
 //
 // The columns are the MMA's M operand, so a column is a lane of tensor memory: a
-// thread unpacks its own column's codes, four ANDs, a shift and four exact
-// subtractions a word of eight (codes and zeros as fp16 subnormals, see
-// w4_stream.cu), and writes them to tensor memory, from where the MMA takes them
-// (tcgen05.st, A operand in tensor memory): through shared memory they would cost
-// it as much as x does. A group's fp32 sums come back to the same thread, which
-// multiplies its column's scale and adds: the weights are never rounded. x is
-// brought to fp16 by a power of two a row and laid out as the MMA's other operand
-// (panels of 64 k, 128-byte swizzle, pairs k + j, k + 4 + j) by a launch before
-// this one, so it arrives in plain pieces.
+// thread unpacks its own column's codes, multiplies its group's scale in and
+// writes them to tensor memory, from where the MMA takes them (tcgen05.st, A
+// operand in tensor memory): through shared memory they would cost it as much as
+// x does. The other operand is x, brought to fp16 by a power of two a row (its
+// largest value in [2^14, 2^15): bf16 keeps its eight bits, what is lost is below
+// 2^-39 of the row's largest) and laid out as the MMA reads it (panels of 64 k,
+// 128-byte swizzle, pairs k + j, k + 4 + j as in a word of codes) by a launch
+// before this one, so that it arrives in plain pieces.
 //
-// Tensor memory: two accumulators of up to 192 columns, two A buffers (128 of k:
-// 64 columns). Roles: one warp copies, one issues the MMAs; eight unpack (four
-// lane quarters x even and odd groups, so that the latencies of a group's waits and
-// stores hide behind the other's); eight add up (four quarters x two halves of the
-// rows, up to 96 sums a thread, for which the warpgroups' registers are split
-// unevenly) and write the results, while the products of the next tile begin.
-// Unpacking and adding up in the same warps, one after the other, took 2100
-// cycles a group where this takes XX. Waits are bounded as everywhere.
+// The weight is not rounded. Brought to fp16 by a power of two a column (found by
+// the launch before), a bf16 scale has eight bits and code - 8 at most three, so
+// the product is an fp16 number. With zeros or other scales it is the sum of two
+// (hi and what is left), and the MMAs run twice. Scaling each group's fp32 sums
+// instead costs more: tensor memory is read at about 20 bytes a cycle and
+// quarter, so bringing back 128 x 144 sums took 880 cycles, the products of a
+// group of 128 are 580 (2048 tokens, 60 experts: 1432 us, now XX).
+//
+// Tensor memory: two accumulators and two A buffers (128 of k: 64 columns, split
+// 128). Roles: one warp copies, one issues the MMAs; eight unpack (four lane
+// quarters x even and odd groups, so that the latencies of a group's waits and
+// stores hide behind the other's); eight write the results (four quarters x two
+// halves of the rows, up to 96 sums a thread, for which the warpgroups' registers
+// are split unevenly) while the next tile's products run. Waits are bounded as
+// everywhere.
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -39,18 +45,25 @@ namespace pgg {
 namespace {
 
 constexpr int kTile = 128;            // columns of codes
-constexpr int kRows = kW4WideRows;    // most rows of a tile
 constexpr int kGroup = 128;           // of k: one A buffer, one stage of x
 constexpr int kSlotBytes = kTile * 128;           // codes of 256 of k
-constexpr int kStageBytes = kRows * kGroup * 2;   // x of 128 of k
+constexpr int kStageBytes = kW4WideRows * kGroup * 2;  // x of 128 of k
 constexpr int kSlots = 2, kStages = 4;
-constexpr int kChunks = kRows / 32;   // of 16 rows, that an adding warp takes
-constexpr int kACols = 2 * kRows;     // first tensor-memory column of the A buffers
-// Warpgroups: copies and MMAs; two that unpack; two that add. Registers a thread of each, which
+
+// Most rows of a tile, first tensor-memory column of the A buffers, columns of one.
+template <bool SPLIT>
+struct Cfg {
+  static constexpr int kRows = SPLIT ? kW4SplitRows : kW4WideRows;
+  static constexpr int kChunks = kRows / 32;  // of 16 rows, that a writing warp takes
+  static constexpr int kACols = 2 * kRows;
+  static constexpr int kABuf = SPLIT ? 128 : 64;
+  static_assert(kACols + 2 * kABuf <= 512, "tensor memory");
+};
+// Warpgroups: copies and MMAs; two that unpack; two that write. Registers a thread of each, which
 // draw on what the block is launched with.
 constexpr int kThreads = 5 * 128;
-constexpr int kLaunchRegs = 96, kFewRegs = 40, kUnpackRegs = 56, kAddRegs = 160;
-static_assert(128 * kFewRegs + 256 * kUnpackRegs + 256 * kAddRegs <= kThreads * kLaunchRegs,
+constexpr int kLaunchRegs = 96, kFewRegs = 40, kUnpackRegs = 56, kWriteRegs = 160;
+static_assert(128 * kFewRegs + 256 * kUnpackRegs + 256 * kWriteRegs <= kThreads * kLaunchRegs,
               "registers");
 
 struct Ctl {
@@ -80,7 +93,7 @@ __device__ __forceinline__ Tile tile_of(uint32_t t, const W4Args& a) {
   const uint32_t rb = t / static_cast<uint32_t>(a.n_blocks);
   int4 e = a.rblist[check_index(a.hdr, rb, a.max_row_blocks, 180)];
   if (!check_ok(a.hdr,
-                e.x >= 0 && e.x < a.G && e.y >= 0 && e.z > 0 && e.z <= kRows &&
+                e.x >= 0 && e.x < a.G && e.y >= 0 && e.z > 0 && e.z <= kW4WideRows &&
                     static_cast<int64_t>(e.y) + e.z <= a.M,
                 181))
     e = make_int4(0, 0, 1, 0);
@@ -106,18 +119,55 @@ __device__ __forceinline__ float block_max(float v, float* s) {
   return fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3]));
 }
 
-// A row of a row block: its power of two and its values as the MMA reads them. 128 threads a row.
+__device__ __forceinline__ float scale_at(const W4Args& a, int64_t i) {
+  if (a.scale_f32) return __ldg(static_cast<const float*>(a.scales) + i);
+  const uint16_t v = __ldg(static_cast<const uint16_t*>(a.scales) + i);
+  return a.bf16 ? __uint_as_float(static_cast<uint32_t>(v) << 16) : __half2float(__ushort_as_half(v));
+}
+
+// The power of two of a number that is to become m 2^e with m in [0.5, 1).
+__device__ __forceinline__ int exponent_of(float most) {
+  int e = 0;
+  if (most > 0.0f) frexpf(most, &e);
+  return e;
+}
+
+// The first `row_blocks` blocks: a row of a row block, its power of two and its values as the MMA
+// reads them, 128 threads a row. The others: the columns' powers of two, eight lanes a column of an
+// expert with rows: its largest scale comes to lie in [2^8, 2^9).
 template <int DT>
-__global__ void __launch_bounds__(128) w4_pack_wide_kernel(const W4Args a) {
+__global__ void __launch_bounds__(128)
+    w4_pack_wide_kernel(const W4Args a, const int64_t* group_list, const int row_blocks) {
   __shared__ float s_max[4];
   ptx::griddep_wait();
   if (routing_failed(a.hdr)) return;
   const int tid = threadIdx.x;
+  if (static_cast<int>(blockIdx.x) >= row_blocks) {
+    const int64_t columns = a.product == PGG_W4_GATED ? 2 * a.N : a.N;
+    const int64_t step = static_cast<int64_t>(gridDim.x - row_blocks) * 16;
+    const int lane = tid & 7;
+    // (whole warps walk together: the exchange below needs them)
+    const int64_t end = (a.G * columns + 3) / 4 * 4;
+    for (int64_t c = (static_cast<int64_t>(blockIdx.x) - row_blocks) * 16 + (tid >> 3); c < end;
+         c += step) {
+      float most = 0.0f;
+      const bool live = c < a.G * columns && group_list[c / columns] > 0;
+      if (live)
+        for (int64_t i = lane; i < a.groups; i += 8) {
+          const float v = fabsf(scale_at(a, c * a.groups + i));
+          if (v < INFINITY) most = fmaxf(most, v);
+        }
+#pragma unroll
+      for (int d = 1; d < 8; d *= 2) most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, d));
+      if (live && lane == 0) a.col_exponent[c] = exponent_of(most) - 9;
+    }
+    return;
+  }
   const int64_t width = (a.K + kGroup - 1) / kGroup * kGroup;
-  const int64_t total = static_cast<int64_t>(a.hdr->n_row_blocks) * kRows;
-  for (int64_t i = blockIdx.x; i < total; i += gridDim.x) {
-    const int64_t rb = i / kRows;
-    const int n = static_cast<int>(i - rb * kRows);
+  const int64_t total = static_cast<int64_t>(a.hdr->n_row_blocks) * a.block_rows;
+  for (int64_t i = blockIdx.x; i < total; i += row_blocks) {
+    const int64_t rb = i / a.block_rows;
+    const int n = static_cast<int>(i - rb * a.block_rows);
     const int4 e = a.rblist[check_index(a.hdr, rb, a.max_row_blocks, 182)];
     if (n >= e.z) continue;  // (what stands there reaches no row that is looked at)
     const int64_t row = check_index(a.hdr, static_cast<int64_t>(e.y) + n, a.M, 183);
@@ -134,16 +184,14 @@ __global__ void __launch_bounds__(128) w4_pack_wide_kernel(const W4Args a) {
         most = fmaxf(most, fabsf(v[j]) < INFINITY ? fabsf(v[j]) : 0.0f);
     }
     most = block_max(most, s_max);
-    int exponent = 0;  // of two: most = m 2^exponent, m in [0.5, 1)
-    if (most > 0.0f) frexpf(most, &exponent);
-    exponent -= 15;
+    const int exponent = exponent_of(most) - 15;
     const float by0 = ldexpf(1.0f, -(exponent / 2)), by1 = ldexpf(1.0f, -(exponent - exponent / 2));
     const int64_t prow = packed_row(e, rb);
     if (tid == 0) {  // what the results need to know of the row
       const int64_t pos = check_index(a.hdr, a.rowinfo[row].rank, a.M, 189);
       const float p = a.probs ? a.probs[pos] : 1.0f;
       a.meta[prow + n] = make_int4(static_cast<int>(a.product == PGG_W4_COMBINED ? pos : row),
-                                   exponent + 24, __float_as_int(p), 0);
+                                   exponent, __float_as_int(p), 0);
     }
     char* out = static_cast<char*>(a.packed) + prow * width * 2;
     const int64_t panel = static_cast<int64_t>((e.z + 15) / 16 * 16) * 128;
@@ -151,12 +199,12 @@ __global__ void __launch_bounds__(128) w4_pack_wide_kernel(const W4Args a) {
       float v[8] = {};
       if (k < a.K) vec::load<DT, 8>(x, k, v);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = __half2float(__float2half_rn(v[j] * by0 * by1));
+      for (int j = 0; j < 8; ++j) v[j] = v[j] * by0 * by1;
       uint4 w;
       w.x = vec::pack2<PGG_F16>(v[0], v[4]);
-      w.y = vec::pack2<PGG_F16>(v[1] * 0.0625f, v[5] * 0.0625f);
+      w.y = vec::pack2<PGG_F16>(v[1], v[5]);
       w.z = vec::pack2<PGG_F16>(v[2], v[6]);
-      w.w = vec::pack2<PGG_F16>(v[3] * 0.0625f, v[7] * 0.0625f);
+      w.w = vec::pack2<PGG_F16>(v[3], v[7]);
       const int chunk = static_cast<int>(k / 8) & 7;
       *reinterpret_cast<uint4*>(out + k / 64 * panel + n * 128 + ((chunk ^ (n & 7)) << 4)) = w;
     }
@@ -259,9 +307,10 @@ __device__ __forceinline__ void mma_tmem(uint32_t d_tmem, uint32_t a_tmem, uint6
       : "memory");
 }
 
-// One thread. U: of k that share a scale.
-template <int U>
+// One thread.
+template <bool SPLIT>
 __device__ void issuer(uint8_t* smem, Ctl* ctl, uint32_t tmem, const W4Args& a, const Walk& k) {
+  using C = Cfg<SPLIT>;
   volatile int* abort = &ctl->abort;
   uint8_t* xs = smem + kSlots * kSlotBytes;
   int stage = 0, buf = 0, acc = 0;
@@ -271,7 +320,12 @@ __device__ void issuer(uint8_t* smem, Ctl* ctl, uint32_t tmem, const W4Args& a, 
     const Tile x = tile_of(t, a);
     const uint32_t panel = static_cast<uint32_t>(x.rows16) * 128;
     const uint32_t idesc = ptx::idesc_make(0, kTile, x.rows16);
-    for (int g = 0; g < k.groups && !failed; ++g) {
+    const uint32_t d = tmem + C::kRows * acc;
+    if (!ptx::mbar_wait(&ctl->dempty[acc], dphase ^ 1u, a.wait_limit_ns, abort)) {
+      failed = true;
+      break;
+    }
+    for (int g = 0; g < k.groups; ++g) {
       if (!ptx::mbar_wait(&ctl->xfull[stage], xphase, a.wait_limit_ns, abort) ||
           !ptx::mbar_wait(&ctl->afull[buf], aphase, a.wait_limit_ns, abort)) {
         failed = true;
@@ -279,26 +333,15 @@ __device__ void issuer(uint8_t* smem, Ctl* ctl, uint32_t tmem, const W4Args& a, 
       }
       ptx::tc_fence_after_sync();
       const uint32_t xb = ptx::smem_addr(xs + stage * kStageBytes);
-      for (int u = 0; u < kGroup / U; ++u) {
-        if (!ptx::mbar_wait(&ctl->dempty[acc], dphase ^ 1u, a.wait_limit_ns, abort)) {
-          failed = true;
-          break;
-        }
-        ptx::tc_fence_after_sync();
+      const uint32_t ab = tmem + C::kACols + C::kABuf * buf;
 #pragma unroll
-        for (int kk = 0; kk < U / 16; ++kk) {
-          const int s = u * (U / 16) + kk;  // of 16 k
-          mma_tmem(tmem + kRows * acc, tmem + kACols + 64 * buf + 8 * s,
-                   ptx::sdesc_sw128(xb + (s >> 2) * panel) +
-                       static_cast<uint64_t>(((s & 3) * 32) >> 4),
-                   idesc, kk > 0 ? 1u : 0u);
-        }
-        issued = true;
-        ptx::mma_commit(&ctl->dfull[acc]);
-        acc ^= 1;
-        if (acc == 0) dphase ^= 1u;
+      for (int s = 0; s < kGroup / 16; ++s) {  // of 16 k
+        const uint64_t desc = ptx::sdesc_sw128(xb + (s >> 2) * panel) +
+                              static_cast<uint64_t>(((s & 3) * 32) >> 4);
+        mma_tmem(d, ab + 8 * s, desc, idesc, (g | s) > 0 ? 1u : 0u);
+        if (SPLIT) mma_tmem(d, ab + 64 + 8 * s, desc, idesc, 1u);
       }
-      if (failed) break;
+      issued = true;
       ptx::mma_commit(&ctl->aempty[buf]);
       ptx::mma_commit(&ctl->xempty[stage]);
       if (++stage == kStages) {
@@ -308,6 +351,10 @@ __device__ void issuer(uint8_t* smem, Ctl* ctl, uint32_t tmem, const W4Args& a, 
       buf ^= 1;
       if (buf == 0) aphase ^= 1u;
     }
+    if (failed) break;
+    ptx::mma_commit(&ctl->dfull[acc]);
+    acc ^= 1;
+    if (acc == 0) dphase ^= 1u;
   }
   if (failed) {
     ctl->abort = 1;
@@ -331,10 +378,24 @@ __device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&v)[
       : "memory");
 }
 
+// Pairs of fp16.
 __device__ __forceinline__ uint32_t sub2(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
+}
+__device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t fma2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t r;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+  return r;
+}
+__device__ __forceinline__ uint32_t twice(float v) {
+  return __half_as_ushort(__float2half_rn(v)) * 0x10001u;
 }
 
 __device__ __forceinline__ uint4 lds128(uint32_t addr) {
@@ -361,86 +422,123 @@ __device__ __forceinline__ int64_t column_of(const W4Args& a, const Tile& x, int
   return x.n0 + l < a.N ? x.n0 + l : -1;
 }
 
-// A scale as it stands in memory (what converts it would wait for it), and as a number.
-__device__ __forceinline__ uint32_t raw_scale(const W4Args& a, int64_t i) {
-  return a.scale_f32 ? __ldg(static_cast<const uint32_t*>(a.scales) + i)
-                     : __ldg(static_cast<const uint16_t*>(a.scales) + i);
-}
-__device__ __forceinline__ float scale_of(const W4Args& a, uint32_t v) {
-  if (a.scale_f32) return __uint_as_float(v);
-  return a.bf16 ? __uint_as_float(v << 16)
-                : __half2float(__ushort_as_half(static_cast<uint16_t>(v)));
-}
-
-// A lane's first scale in its column (a column that is not there: any scales).
-__device__ __forceinline__ int64_t first_scale(const W4Args& a, const Tile& x, int l) {
+// A lane's column among all experts' (one that is not there: any).
+__device__ __forceinline__ int64_t column_index(const W4Args& a, const Tile& x, int l) {
   const int64_t c = column_of(a, x, l);
-  return (x.g * (a.product == PGG_W4_GATED ? 2 * a.N : a.N) + (c < 0 ? 0 : c)) * a.groups;
+  return x.g * (a.product == PGG_W4_GATED ? 2 * a.N : a.N) + (c < 0 ? 0 : c);
 }
 
+// What a thread needs from memory for a group, loaded ahead: its column's scales and zeros.
 template <int U>
-__device__ __forceinline__ uint32_t group_of(const W4Args& a, uint32_t unit) {
-  return a.group == U ? unit : unit * U / static_cast<uint32_t>(a.group);
-}
+struct Ahead {
+  static constexpr int kN = kGroup / U;
+  float s[kN];
+  uint32_t z[kN];
+
+  __device__ __forceinline__ void load(const W4Args& a, int64_t at, int g) {
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      uint32_t group = g * kN + i;
+      if (a.group != U) group = group * U / static_cast<uint32_t>(a.group);
+      const bool in = group < static_cast<uint32_t>(a.groups);  // (x is 0 behind, but 0 inf is not)
+      s[i] = in ? scale_at(a, at + group) : 0.0f;
+      z[i] = in && a.zeros ? __ldg(a.zeros + at + group) : 8;
+    }
+  }
+};
 
 // Groups `par`, par + 2, ... of this CTA's sequence of groups: the thread's column, 128 of k, into A
-// buffer par.
-template <int U>
+// buffer par. U: of k that share a scale.
+template <int U, bool SPLIT>
 __device__ void unpacker(uint8_t* smem, Ctl* ctl, uint32_t tmem, int par, const W4Args& a,
                          const Walk& k) {
-  constexpr int kZeros = U < kGroup ? kGroup / U : 1;  // of a column and group
+  using C = Cfg<SPLIT>;
   volatile int* abort = &ctl->abort;
   const int lane = threadIdx.x & 31, quarter = (threadIdx.x >> 5) & 3, l = 32 * quarter + lane;
   const int row = code_row(a.product == PGG_W4_GATED, l);
   const uint32_t codes = ptx::smem_addr(smem) + row * 128;
-  const uint32_t a_tmem = tmem + (static_cast<uint32_t>(32 * quarter) << 16) + kACols + 64 * par;
-  // slots of codes: one for two groups of a tile
-  int slot = 0;
+  const uint32_t a_tmem =
+      tmem + (static_cast<uint32_t>(32 * quarter) << 16) + C::kACols + C::kABuf * par;
+  uint32_t magic;  // the pair 2^10, from a register: an instruction holds one of two constants only
+  asm volatile("mov.u32 %0, 0x64006400;" : "=r"(magic));
+  int slot = 0;  // of codes: two groups of a tile
   uint32_t cphase = 0, aphase = 0;
   uint32_t turn = 0;  // of all groups
+  // a tile ahead: the column, and its power of two
+  int64_t next = k.first < k.total ? column_index(a, tile_of(k.first, a), l) : 0;
+  int next_exponent = k.first < k.total ? a.col_exponent[next] : 0;
+  Ahead<U> now;
+  bool loaded = false;
   for (uint32_t t = k.first; t < k.total; t += k.step) {
-    const int64_t at = a.zeros ? first_scale(a, tile_of(t, a), l) : 0;
+    const int64_t at = next * a.groups;
+    const int exponent = next_exponent;
+    if (!loaded) now.load(a, at, static_cast<int>((turn ^ par) & 1u));
+    loaded = false;
+    const bool more = t + k.step < k.total;
+    if (more) {
+      next = column_index(a, tile_of(t + k.step, a), l);
+      next_exponent = a.col_exponent[next];
+    }
     for (int g = 0; g < k.groups; ++g, ++turn) {
       const bool slot_done = (g & 1) || g + 1 == k.groups;
-      if ((turn & 1) == static_cast<uint32_t>(par)) {
-        uint32_t zero[kZeros];
-#pragma unroll
-        for (int i = 0; i < kZeros; ++i) {
-          zero[i] = 8;
-          if (a.zeros) {
-            const uint32_t group = group_of<U>(a, g * (kGroup / U) + i);
-            zero[i] = group < static_cast<uint32_t>(a.groups) ? __ldg(a.zeros + at + group) : 0;
-          }
+      const bool mine = (turn & 1) == static_cast<uint32_t>(par);
+      if (!mine && !(slot_done && (g & 1) == 0)) {
+        if (slot_done && ++slot == kSlots) {
+          slot = 0;
+          cphase ^= 1u;
         }
-        const bool ok = ptx::mbar_wait(&ctl->cfull[slot], cphase, a.wait_limit_ns, abort) &&
-                        ptx::mbar_wait(&ctl->aempty[par], aphase ^ 1u, a.wait_limit_ns, abort);
-        if (!__all_sync(0xFFFFFFFFu, ok)) {
-          if (lane == 0) {
-            ctl->abort = 1;
-            raise_status(a.hdr, kStTimeout, 187);
-          }
-          return;
+        continue;
+      }
+      bool ok = ptx::mbar_wait(&ctl->cfull[slot], cphase, a.wait_limit_ns, abort);
+      if (mine) ok = ok && ptx::mbar_wait(&ctl->aempty[par], aphase ^ 1u, a.wait_limit_ns, abort);
+      if (!__all_sync(0xFFFFFFFFu, ok)) {
+        if (lane == 0) {
+          ctl->abort = 1;
+          raise_status(a.hdr, kStTimeout, 187);
         }
+        return;
+      }
+      if (mine) {
         ptx::tc_fence_after_sync();
 #pragma unroll
         for (int i = 0; i < 4; ++i) {  // 32 of k: four words, 16 columns of tensor memory
           const int chunk = (g & 1) * 4 + i;
           const uint4 q = lds128(codes + slot * kSlotBytes + ((chunk ^ (row & 7)) << 4));
           const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-          const uint32_t z = zero[i * 32 / U < kZeros ? i * 32 / U : 0];
-          // zero 2^-24 and 2^-20
-          const uint32_t z0 = __half_as_ushort(__float2half_rn(z * 0x1p-24f)) * 0x10001u;
-          const uint32_t z1 = __half_as_ushort(__float2half_rn(z * 0x1p-20f)) * 0x10001u;
-          uint32_t v[16];
+          const float zero = static_cast<float>(now.z[32 * i / U]);
+          const uint32_t z0 = twice(1024.0f + zero), z1 = twice(-64.0f - zero);
+          const float sf = ldexpf(now.s[32 * i / U], -exponent);
+          const uint32_t s_hi = twice(sf);
+          const uint32_t s_lo =
+              SPLIT ? twice(sf - __half2float(__ushort_as_half(static_cast<uint16_t>(s_hi)))) : 0;
+          uint32_t v[16], left[SPLIT ? 16 : 1];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const uint32_t hi = w[j] >> 8;
-            v[4 * j] = sub2(w[j] & 0x000F000Fu, z0);
-            v[4 * j + 1] = sub2(w[j] & 0x00F000F0u, z1);
-            v[4 * j + 2] = sub2(hi & 0x000F000Fu, z0);
-            v[4 * j + 3] = sub2(hi & 0x00F000F0u, z1);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const uint32_t b = w[j] >> (8 * h);
+              uint32_t t0, t1;  // 2^10 + code, 2^10 + 16 code
+              asm("lop3.b32 %0, %1, 0x000F000F, %2, 0xEA;" : "=r"(t0) : "r"(b), "r"(magic));
+              asm("lop3.b32 %0, %1, 0x00F000F0, %2, 0xEA;" : "=r"(t1) : "r"(b), "r"(magic));
+              t0 = sub2(t0, z0);
+              t1 = fma2(t1, 0x2C002C00u, z1);  // times 2^-4, less 64 + zero: exact
+              const int to = 4 * j + 2 * h;
+              v[to] = mul2(t0, s_hi);
+              v[to + 1] = mul2(t1, s_hi);
+              if constexpr (SPLIT) {
+                left[to] = fma2(t0, s_lo, fma2(t0, s_hi, v[to] ^ 0x80008000u));
+                left[to + 1] = fma2(t1, s_lo, fma2(t1, s_hi, v[to + 1] ^ 0x80008000u));
+              }
+            }
           }
           tmem_st_x16(a_tmem + 16 * i, v);
+          if constexpr (SPLIT) tmem_st_x16(a_tmem + 64 + 16 * i, left);
+        }
+        if (g + 2 < k.groups) {
+          now.load(a, at, g + 2);
+        } else if (more && k.groups > 1) {
+          now.load(a, next * a.groups, g + 2 - k.groups);
+          loaded = true;
         }
         ptx::tmem_st_wait();
         ptx::tc_fence_before_sync();
@@ -450,18 +548,10 @@ __device__ void unpacker(uint8_t* smem, Ctl* ctl, uint32_t tmem, int par, const 
           ptx::mbar_arrive(&ctl->cempty[slot]);
         }
         aphase ^= 1u;
-      } else if (slot_done && (g & 1) == 0) {
-        // a slot with one group: the other warps have nothing to read of it (but it has to be this
-        // use of the slot that they let go)
-        if (!__all_sync(0xFFFFFFFFu, ptx::mbar_wait(&ctl->cfull[slot], cphase, a.wait_limit_ns,
-                                                    abort))) {
-          if (lane == 0) {
-            ctl->abort = 1;
-            raise_status(a.hdr, kStTimeout, 190);
-          }
-          return;
-        }
-        if (lane == 0) ptx::mbar_arrive(&ctl->cempty[slot]);
+      } else if (lane == 0) {
+        // a slot with one group: these warps have nothing to read of it (but it has to be this use
+        // of the slot that they let go)
+        ptx::mbar_arrive(&ctl->cempty[slot]);
       }
       if (slot_done && ++slot == kSlots) {
         slot = 0;
@@ -471,9 +561,17 @@ __device__ void unpacker(uint8_t* smem, Ctl* ctl, uint32_t tmem, int par, const 
   }
 }
 
-// Sums of the thread's column: 16-row chunks half, half + 2, ... of the tile's rows.
-template <int U>
-__device__ void adder(Ctl* ctl, uint32_t tmem, int half, const W4Args& a, const Walk& k) {
+// v 2^e, e in (-400, 250): in two factors, since 2^e may lie outside fp32.
+__device__ __forceinline__ float times_power(float v, int e) {
+  const int half = e >> 1, rest = e - half;
+  return v * __int_as_float((max(half, -126) + 127) << 23) *
+         __int_as_float((max(rest, -126) + 127) << 23);
+}
+
+// Results of the thread's column: 16-row chunks half, half + 2, ... of the tile's rows.
+template <bool SPLIT>
+__device__ void writer(Ctl* ctl, uint32_t tmem, int half, const W4Args& a, const Walk& k) {
+  using C = Cfg<SPLIT>;
   volatile int* abort = &ctl->abort;
   const int lane = threadIdx.x & 31, quarter = (threadIdx.x >> 5) & 3, l = 32 * quarter + lane;
   const bool gated = a.product == PGG_W4_GATED;
@@ -482,71 +580,50 @@ __device__ void adder(Ctl* ctl, uint32_t tmem, int half, const W4Args& a, const 
   uint32_t dphase = 0;
   for (uint32_t t = k.first; t < k.total; t += k.step) {
     const Tile x = tile_of(t, a);
-    const int64_t at = first_scale(a, x, l);
-    uint32_t s_next = raw_scale(a, at);
-    float sum[kChunks][16];
+    const int exponent = a.col_exponent[column_index(a, x, l)];
+    int4 m[C::kChunks];  // lane i holds what belongs to a chunk's row i
 #pragma unroll
-    for (int c = 0; c < kChunks; ++c)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) sum[c][i] = 0.0f;
-    const uint32_t units = k.groups * (kGroup / U);
-    for (uint32_t unit = 0; unit < units; ++unit) {
-      // (x is 0 behind the last group, but 0 inf is not)
-      const bool in = group_of<U>(a, unit) < static_cast<uint32_t>(a.groups);
-      const float s = in ? scale_of(a, s_next) : 0.0f;
-      const uint32_t next = group_of<U>(a, unit + 1);
-      if (next < static_cast<uint32_t>(a.groups)) s_next = raw_scale(a, at + next);
-      if (!__all_sync(0xFFFFFFFFu, ptx::mbar_wait(&ctl->dfull[acc], dphase, a.wait_limit_ns,
-                                                  abort))) {
-        if (lane == 0) {
-          ctl->abort = 1;
-          raise_status(a.hdr, kStTimeout, 188);
-        }
-        return;
-      }
-      ptx::tc_fence_after_sync();
-      const uint32_t d = d_tmem + kRows * acc;
-#pragma unroll
-      for (int c = 0; c < kChunks; c += 2) {  // rows 32 c + 16 half ..
-        if (32 * c + 16 * half >= x.rows16) continue;
-        uint32_t v[2][16];
-        const bool two = 32 * (c + 1) + 16 * half < x.rows16;
-        ptx::tmem_ld_32x32b_x16(d + 32 * c, v[0]);
-        if (two) ptx::tmem_ld_32x32b_x16(d + 32 * (c + 1), v[1]);
-        ptx::tmem_ld_wait();
-#pragma unroll
-        for (int i = 0; i < 16; ++i) sum[c][i] = fmaf(s, __uint_as_float(v[0][i]), sum[c][i]);
-        if (two)
-#pragma unroll
-          for (int i = 0; i < 16; ++i)
-            sum[c + 1][i] = fmaf(s, __uint_as_float(v[1][i]), sum[c + 1][i]);
-      }
-      ptx::tc_fence_before_sync();
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(&ctl->dempty[acc]);
-      acc ^= 1;
-      if (acc == 0) dphase ^= 1u;
+    for (int c = 0; c < C::kChunks; ++c) {
+      const int j0 = 32 * c + 16 * half;
+      m[c] = make_int4(0, 0, 0, 0);
+      if (lane < 16 && j0 + lane < x.rows) m[c] = a.meta[x.prow + j0 + lane];
     }
-    // results: this thread's column of its rows
+    if (!__all_sync(0xFFFFFFFFu,
+                    ptx::mbar_wait(&ctl->dfull[acc], dphase, a.wait_limit_ns, abort))) {
+      if (lane == 0) {
+        ctl->abort = 1;
+        raise_status(a.hdr, kStTimeout, 188);
+      }
+      return;
+    }
+    ptx::tc_fence_after_sync();
+    uint32_t sum[C::kChunks][16];
+#pragma unroll
+    for (int c = 0; c < C::kChunks; ++c)
+      if (32 * c + 16 * half < x.rows16)
+        ptx::tmem_ld_32x32b_x16(d_tmem + C::kRows * acc + 32 * c, sum[c]);
+    ptx::tmem_ld_wait();
+    ptx::tc_fence_before_sync();
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive(&ctl->dempty[acc]);
+    acc ^= 1;
+    if (acc == 0) dphase ^= 1u;
     const int64_t f = x.n0 + (gated ? l >> 1 : l);
     const bool writes = f < a.N && (!gated || (lane & 1) == 0);
 #pragma unroll
-    for (int c = 0; c < kChunks; ++c) {
-      const int j0 = 32 * c + 16 * half, left = x.rows - j0;
+    for (int c = 0; c < C::kChunks; ++c) {
+      const int left = x.rows - 32 * c - 16 * half;
       if (left <= 0) continue;
-      int4 m = make_int4(0, 0, 0, 0);  // lane i holds what belongs to the chunk's row i
-      if (lane < 16 && lane < left) m = a.meta[x.prow + j0 + lane];
-      // 2^e in two factors (it may lie outside fp32)
-      const float by0 = ldexpf(1.0f, m.y / 2), by1 = ldexpf(1.0f, m.y - m.y / 2);
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         if (i >= left) continue;
-        float v = sum[c][i] * __shfl_sync(0xFFFFFFFFu, by0, i) * __shfl_sync(0xFFFFFFFFu, by1, i);
+        float v = times_power(__uint_as_float(sum[c][i]),
+                              __shfl_sync(0xFFFFFFFFu, m[c].y, i) + exponent);
         if (gated) {
           const float up = __shfl_xor_sync(0xFFFFFFFFu, v, 1);
-          v = gate(v, up, __int_as_float(__shfl_sync(0xFFFFFFFFu, m.z, i)));
+          v = gate(v, up, __int_as_float(__shfl_sync(0xFFFFFFFFu, m[c].z, i)));
         }
-        const int64_t to = static_cast<int64_t>(__shfl_sync(0xFFFFFFFFu, m.x, i)) * a.N + f;
+        const int64_t to = static_cast<int64_t>(__shfl_sync(0xFFFFFFFFu, m[c].x, i)) * a.N + f;
         if (!writes) continue;
         if (a.out_f32)
           static_cast<float*>(a.out)[to] = v;
@@ -568,7 +645,7 @@ __device__ __forceinline__ void more_registers() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
 
-template <int U>
+template <int U, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
     w4_wide_kernel(const __grid_constant__ CUtensorMap tm, const W4Args a) {
   extern __shared__ uint8_t smem_raw[];
@@ -625,13 +702,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (wg == 0) {
     fewer_registers<kFewRegs>();
     if (warp == 0 && lane == 0) copier(smem, ctl, &tm, a, k);
-    if (warp == 1 && lane == 0) issuer<U>(smem, ctl, tmem, a, k);
+    if (warp == 1 && lane == 0) issuer<SPLIT>(smem, ctl, tmem, a, k);
   } else if (wg <= 2) {
     fewer_registers<kUnpackRegs>();
-    unpacker<U>(smem, ctl, tmem, wg - 1, a, k);
+    unpacker<U, SPLIT>(smem, ctl, tmem, wg - 1, a, k);
   } else {
-    more_registers<kAddRegs>();
-    adder<U>(ctl, tmem, wg - 3, a, k);
+    more_registers<kWriteRegs>();
+    writer<SPLIT>(ctl, tmem, wg - 3, a, k);
   }
   ptx::tc_fence_before_sync();
   __syncthreads();
@@ -641,9 +718,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <int U>
+template <int U, bool SPLIT>
 cudaError_t launch_t(const CUtensorMap& tm, const W4Args& a, int num_sms, cudaStream_t stream) {
-  auto kern = w4_wide_kernel<U>;
+  auto kern = w4_wide_kernel<U, SPLIT>;
   static SmemLimit limit;
   const cudaError_t err = allow_smem(&limit, kern, kSmem);
   if (err != cudaSuccess) return err;
@@ -651,32 +728,44 @@ cudaError_t launch_t(const CUtensorMap& tm, const W4Args& a, int num_sms, cudaSt
                     static_cast<size_t>(kSmem), stream, 1, tm, a);
 }
 
+template <bool SPLIT>
+cudaError_t launch_u(const CUtensorMap& tm, const W4Args& a, int num_sms, cudaStream_t stream) {
+  if (a.group % 128 == 0) return launch_t<128, SPLIT>(tm, a, num_sms, stream);
+  if (a.group % 64 == 0) return launch_t<64, SPLIT>(tm, a, num_sms, stream);
+  return launch_t<32, SPLIT>(tm, a, num_sms, stream);
+}
+
 }  // namespace
 
+int w4_wide_rows(int dtype, bool scale_f32, bool zeros) {
+  return dtype == PGG_BF16 && !scale_f32 && !zeros ? kW4WideRows : kW4SplitRows;
+}
 int64_t w4_packed_wide_rows(int64_t M, int64_t row_blocks) { return M + 16 * row_blocks; }
 int64_t w4_packed_wide_bytes(int64_t M, int64_t row_blocks, int64_t K) {
   return w4_packed_wide_rows(M, row_blocks) * ((K + kGroup - 1) / kGroup * kGroup) * 2;
 }
 
-cudaError_t launch_w4_wide(int dtype, W4Args a, int num_sms, cudaStream_t stream) {
+cudaError_t launch_w4_wide(int dtype, W4Args a, const int64_t* group_list, int num_sms,
+                           cudaStream_t stream) {
   const int tile = a.product == PGG_W4_GATED ? kTile / 2 : kTile;
+  const int64_t columns = a.product == PGG_W4_GATED ? 2 * a.N : a.N;
   a.n_blocks = static_cast<int32_t>((a.N + tile - 1) / tile);
   a.bf16 = dtype == PGG_BF16;
+  a.block_rows = w4_wide_rows(dtype, a.scale_f32 != 0, a.zeros != nullptr);
   CUtensorMap tm;  // codes as words of 16 bits: boxes of 128 bytes x 64 columns
   std::memset(&tm, 0, sizeof(tm));
-  if (!encode_map_3d(&tm, PGG_F16, a.codes, a.row_bytes / 2,
-                     a.product == PGG_W4_GATED ? 2 * a.N : a.N, a.G, 64))
+  if (!encode_map_3d(&tm, PGG_F16, a.codes, a.row_bytes / 2, columns, a.G, 64))
     return cudaErrorInvalidValue;
-  const int64_t rows = a.max_row_blocks * kRows;
-  const int blocks = static_cast<int>(rows < num_sms * 16 ? rows : num_sms * 16);
-  const cudaError_t err = launch_pdl(dtype == PGG_BF16 ? w4_pack_wide_kernel<PGG_BF16>
-                                                       : w4_pack_wide_kernel<PGG_F16>,
-                                     dim3(static_cast<unsigned>(blocks)), dim3(128), 0, stream, 1,
-                                     a);
+  const int64_t rows = a.max_row_blocks * a.block_rows, cols = (a.G * columns + 15) / 16;
+  const int row_blocks = static_cast<int>(rows < num_sms * 12 ? rows : num_sms * 12);
+  const int col_blocks = static_cast<int>(cols < num_sms * 4 ? cols : num_sms * 4);
+  const cudaError_t err =
+      launch_pdl(dtype == PGG_BF16 ? w4_pack_wide_kernel<PGG_BF16> : w4_pack_wide_kernel<PGG_F16>,
+                 dim3(static_cast<unsigned>(row_blocks + col_blocks)), dim3(128), 0, stream, 1, a,
+                 group_list, row_blocks);
   if (err != cudaSuccess) return err;
-  if (a.group % 128 == 0) return launch_t<128>(tm, a, num_sms, stream);
-  if (a.group % 64 == 0) return launch_t<64>(tm, a, num_sms, stream);
-  return launch_t<32>(tm, a, num_sms, stream);
+  return a.block_rows == kW4WideRows ? launch_u<false>(tm, a, num_sms, stream)
+                                     : launch_u<true>(tm, a, num_sms, stream);
 }
 
 }  // namespace pgg
