@@ -62,7 +62,7 @@ struct Cfg {
 // Warpgroups: copies and MMAs; two that unpack; two that write. Registers a thread of each, which
 // draw on what the block is launched with.
 constexpr int kThreads = 5 * 128;
-constexpr int kLaunchRegs = 96, kFewRegs = 40, kUnpackRegs = 56, kWriteRegs = 160;
+constexpr int kLaunchRegs = 96, kFewRegs = 32, kUnpackRegs = 72, kWriteRegs = 152;
 static_assert(128 * kFewRegs + 256 * kUnpackRegs + 256 * kWriteRegs <= kThreads * kLaunchRegs,
               "registers");
 
@@ -422,6 +422,13 @@ __device__ __forceinline__ int64_t column_of(const W4Args& a, const Tile& x, int
   return x.n0 + l < a.N ? x.n0 + l : -1;
 }
 
+// v 2^e, e in (-400, 250): in two factors, since 2^e may lie outside fp32.
+__device__ __forceinline__ float times_power(float v, int e) {
+  const int half = e >> 1, rest = e - half;
+  return v * __int_as_float((max(half, -126) + 127) << 23) *
+         __int_as_float((max(rest, -126) + 127) << 23);
+}
+
 // A lane's column among all experts' (one that is not there: any).
 __device__ __forceinline__ int64_t column_index(const W4Args& a, const Tile& x, int l) {
   const int64_t c = column_of(a, x, l);
@@ -432,7 +439,7 @@ __device__ __forceinline__ int64_t column_index(const W4Args& a, const Tile& x, 
 template <int U>
 struct Ahead {
   static constexpr int kN = kGroup / U;
-  float s[kN];
+  uint32_t s[kN];  // as they stand in memory: what converts them would wait for them
   uint32_t z[kN];
 
   __device__ __forceinline__ void load(const W4Args& a, int64_t at, int g) {
@@ -441,9 +448,18 @@ struct Ahead {
       uint32_t group = g * kN + i;
       if (a.group != U) group = group * U / static_cast<uint32_t>(a.group);
       const bool in = group < static_cast<uint32_t>(a.groups);  // (x is 0 behind, but 0 inf is not)
-      s[i] = in ? scale_at(a, at + group) : 0.0f;
-      z[i] = in && a.zeros ? __ldg(a.zeros + at + group) : 8;
+      s[i] = 0;
+      z[i] = 8;
+      if (!in) continue;
+      s[i] = a.scale_f32 ? __ldg(static_cast<const uint32_t*>(a.scales) + at + group)
+                         : __ldg(static_cast<const uint16_t*>(a.scales) + at + group);
+      if (a.zeros) z[i] = __ldg(a.zeros + at + group);
     }
+  }
+  __device__ __forceinline__ float scale(const W4Args& a, int i) const {
+    if (a.scale_f32) return __uint_as_float(s[i]);
+    return a.bf16 ? __uint_as_float(s[i] << 16)
+                  : __half2float(__ushort_as_half(static_cast<uint16_t>(s[i])));
   }
 };
 
@@ -507,7 +523,7 @@ __device__ void unpacker(uint8_t* smem, Ctl* ctl, uint32_t tmem, int par, const 
           const uint32_t w[4] = {q.x, q.y, q.z, q.w};
           const float zero = static_cast<float>(now.z[32 * i / U]);
           const uint32_t z0 = twice(1024.0f + zero), z1 = twice(-64.0f - zero);
-          const float sf = ldexpf(now.s[32 * i / U], -exponent);
+          const float sf = times_power(now.scale(a, 32 * i / U), -exponent);
           const uint32_t s_hi = twice(sf);
           const uint32_t s_lo =
               SPLIT ? twice(sf - __half2float(__ushort_as_half(static_cast<uint16_t>(s_hi)))) : 0;
@@ -559,13 +575,6 @@ __device__ void unpacker(uint8_t* smem, Ctl* ctl, uint32_t tmem, int par, const 
       }
     }
   }
-}
-
-// v 2^e, e in (-400, 250): in two factors, since 2^e may lie outside fp32.
-__device__ __forceinline__ float times_power(float v, int e) {
-  const int half = e >> 1, rest = e - half;
-  return v * __int_as_float((max(half, -126) + 127) << 23) *
-         __int_as_float((max(rest, -126) + 127) << 23);
 }
 
 // Results of the thread's column: 16-row chunks half, half + 2, ... of the tile's rows.
