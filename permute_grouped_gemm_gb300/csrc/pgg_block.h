@@ -52,7 +52,7 @@ cudaError_t launch_w4_combine(const float* rows, const WsHeader* hdr, int64_t ba
                               int64_t N, float* out, int num_sms, cudaStream_t stream);
 
 // Most rows of a block of the tensor-core kernel; where its weights are the sum of two.
-constexpr int kW4WideRows = 192, kW4SplitRows = 128;
+constexpr int kW4WideRows = 160, kW4SplitRows = 128;
 int w4_wide_rows(int dtype, bool scale_f32, bool zeros);  // which
 int64_t w4_packed_wide_rows(int64_t M, int64_t row_blocks);
 int64_t w4_packed_wide_bytes(int64_t M, int64_t row_blocks, int64_t K);

@@ -1,5 +1,5 @@
 // Products with 4-bit expert weights, many rows an expert: the tensor cores are
-// the bound (tcgen05, 128 columns x up to 192 rows a tile).
+// the bound (tcgen05, 128 columns x up to 160 rows a tile).
 //
 //     y[column, row] = sum over k of scale (code - zero) x
 //
@@ -25,7 +25,7 @@
 // 128). Roles: one warp copies, one issues the MMAs; eight unpack (four lane
 // quarters x even and odd groups, so that the latencies of a group's waits and
 // stores hide behind the other's); eight write the results (four quarters x two
-// halves of the rows, up to 96 sums a thread, for which the warpgroups' registers
+// halves of the rows, up to 80 sums a thread, for which the warpgroups' registers
 // are split unevenly) while the next tile's products run. Waits are bounded as
 // everywhere.
 
@@ -48,7 +48,7 @@ constexpr int kTile = 128;            // columns of codes
 constexpr int kGroup = 128;           // of k: one A buffer, one stage of x
 constexpr int kSlotBytes = kTile * 128;           // codes of 256 of k
 constexpr int kStageBytes = kW4WideRows * kGroup * 2;  // x of 128 of k
-constexpr int kSlots = 2, kStages = 4;
+constexpr int kSlots = 4, kStages = 4;
 
 // Most rows of a tile, first tensor-memory column of the A buffers, columns of one.
 template <bool SPLIT>
@@ -68,8 +68,9 @@ static_assert(128 * kFewRegs + 256 * kUnpackRegs + 256 * kWriteRegs <= kThreads 
 
 struct Ctl {
   uint64_t cfull[kSlots], cempty[kSlots];  // codes
-  uint64_t xfull[kStages], xempty[kStages];
-  uint64_t afull[2], aempty[2];  // codes of a group in tensor memory
+  // of a group: its x has arrived and its codes are in tensor memory; its MMAs are done (one barrier
+  // each: what a wait and a commit cost the thread that issues, 100 cycles, is what bounds it)
+  uint64_t full[kStages], done[kStages];
   uint64_t dfull[2], dempty[2];  // accumulators
   uint64_t drain;
   uint32_t tmem_base;
@@ -264,13 +265,13 @@ __device__ void copier(uint8_t* smem, Ctl* ctl, const CUtensorMap* tm, const W4A
           cphase ^= 1u;
         }
       }
-      if (!ptx::mbar_wait(&ctl->xempty[stage], xphase ^ 1u, a.wait_limit_ns, abort)) {
+      if (!ptx::mbar_wait(&ctl->done[stage], xphase ^ 1u, a.wait_limit_ns, abort)) {
         failed = true;
         break;
       }
-      ptx::mbar_arrive_expect_tx(&ctl->xfull[stage], bytes);
+      ptx::mbar_arrive_expect_tx(&ctl->full[stage], bytes);
       bulk_load(xs + stage * kStageBytes, src + static_cast<int64_t>(g) * bytes, bytes,
-                &ctl->xfull[stage]);
+                &ctl->full[stage]);
       x_out |= 1u << stage;
       x_parity = (x_parity & ~(1u << stage)) | (xphase << stage);
       if (++stage == kStages) {
@@ -287,9 +288,13 @@ __device__ void copier(uint8_t* smem, Ctl* ctl, const CUtensorMap* tm, const W4A
   for (int i = 0; i < kSlots; ++i)
     if (c_out & (1u << i))
       ptx::mbar_wait(&ctl->cfull[i], (c_parity >> i) & 1u, a.wait_limit_ns, &no_abort);
-  for (int i = 0; i < kStages; ++i)
-    if (x_out & (1u << i))
-      ptx::mbar_wait(&ctl->xfull[i], (x_parity >> i) & 1u, a.wait_limit_ns, &no_abort);
+  for (int i = 0; i < kStages; ++i) {
+    if (!(x_out & (1u << i))) continue;
+    // (unpacking warps that gave up have not arrived: their arrivals are made up for)
+    for (int n = 0; ctl->abort && n < 4; ++n)
+      if (!ptx::mbar_try_wait(&ctl->full[i], (x_parity >> i) & 1u)) ptx::mbar_arrive(&ctl->full[i]);
+    ptx::mbar_wait(&ctl->full[i], (x_parity >> i) & 1u, a.wait_limit_ns, &no_abort);
+  }
 }
 
 // ------------------------------------------------------------------ MMAs
@@ -314,7 +319,7 @@ __device__ void issuer(uint8_t* smem, Ctl* ctl, uint32_t tmem, const W4Args& a, 
   volatile int* abort = &ctl->abort;
   uint8_t* xs = smem + kSlots * kSlotBytes;
   int stage = 0, buf = 0, acc = 0;
-  uint32_t xphase = 0, aphase = 0, dphase = 0;
+  uint32_t phase = 0, dphase = 0;
   bool issued = false, failed = false;
   for (uint32_t t = k.first; t < k.total && !failed; t += k.step) {
     const Tile x = tile_of(t, a);
@@ -326,8 +331,7 @@ __device__ void issuer(uint8_t* smem, Ctl* ctl, uint32_t tmem, const W4Args& a, 
       break;
     }
     for (int g = 0; g < k.groups; ++g) {
-      if (!ptx::mbar_wait(&ctl->xfull[stage], xphase, a.wait_limit_ns, abort) ||
-          !ptx::mbar_wait(&ctl->afull[buf], aphase, a.wait_limit_ns, abort)) {
+      if (!ptx::mbar_wait(&ctl->full[stage], phase, a.wait_limit_ns, abort)) {
         failed = true;
         break;
       }
@@ -342,14 +346,12 @@ __device__ void issuer(uint8_t* smem, Ctl* ctl, uint32_t tmem, const W4Args& a, 
         if (SPLIT) mma_tmem(d, ab + 64 + 8 * s, desc, idesc, 1u);
       }
       issued = true;
-      ptx::mma_commit(&ctl->aempty[buf]);
-      ptx::mma_commit(&ctl->xempty[stage]);
+      ptx::mma_commit(&ctl->done[stage]);
       if (++stage == kStages) {
         stage = 0;
-        xphase ^= 1u;
+        phase ^= 1u;
       }
       buf ^= 1;
-      if (buf == 0) aphase ^= 1u;
     }
     if (failed) break;
     ptx::mma_commit(&ctl->dfull[acc]);
@@ -478,7 +480,7 @@ __device__ void unpacker(uint8_t* smem, Ctl* ctl, uint32_t tmem, int par, const 
   uint32_t magic;  // the pair 2^10, from a register: an instruction holds one of two constants only
   asm volatile("mov.u32 %0, 0x64006400;" : "=r"(magic));
   int slot = 0;  // of codes: two groups of a tile
-  uint32_t cphase = 0, aphase = 0;
+  uint32_t cphase = 0;
   uint32_t turn = 0;  // of all groups
   // a tile ahead: the column, and its power of two
   int64_t next = k.first < k.total ? column_index(a, tile_of(k.first, a), l) : 0;
@@ -506,7 +508,9 @@ __device__ void unpacker(uint8_t* smem, Ctl* ctl, uint32_t tmem, int par, const 
         continue;
       }
       bool ok = ptx::mbar_wait(&ctl->cfull[slot], cphase, a.wait_limit_ns, abort);
-      if (mine) ok = ok && ptx::mbar_wait(&ctl->aempty[par], aphase ^ 1u, a.wait_limit_ns, abort);
+      if (mine && turn >= 2)  // the buffer's last group
+        ok = ok && ptx::mbar_wait(&ctl->done[(turn - 2) % kStages], ((turn - 2) / kStages) & 1u,
+                                  a.wait_limit_ns, abort);
       if (!__all_sync(0xFFFFFFFFu, ok)) {
         if (lane == 0) {
           ctl->abort = 1;
@@ -560,10 +564,9 @@ __device__ void unpacker(uint8_t* smem, Ctl* ctl, uint32_t tmem, int par, const 
         ptx::tc_fence_before_sync();
         __syncwarp();
         if (lane == 0) {
-          ptx::mbar_arrive(&ctl->afull[par]);
+          ptx::mbar_arrive(&ctl->full[turn % kStages]);
           ptx::mbar_arrive(&ctl->cempty[slot]);
         }
-        aphase ^= 1u;
       } else if (lane == 0) {
         // a slot with one group: these warps have nothing to read of it (but it has to be this use
         // of the slot that they let go)
@@ -685,12 +688,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       ptx::mbar_init(&ctl->cempty[i], 8);
     }
     for (int i = 0; i < kStages; ++i) {
-      ptx::mbar_init(&ctl->xfull[i], 1);
-      ptx::mbar_init(&ctl->xempty[i], 1);
+      ptx::mbar_init(&ctl->full[i], 1 + 4);
+      ptx::mbar_init(&ctl->done[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
-      ptx::mbar_init(&ctl->afull[i], 4);
-      ptx::mbar_init(&ctl->aempty[i], 1);
       ptx::mbar_init(&ctl->dfull[i], 1);
       ptx::mbar_init(&ctl->dempty[i], 8);
     }
