@@ -21,8 +21,8 @@
 // quarter, so bringing back 128 x 144 sums took 880 cycles, the products of a
 // group of 128 are 580 (2048 tokens, 60 experts: 1432 us, now XX).
 //
-// Tensor memory: two accumulators and two A buffers (128 of k: 64 columns, split
-// 128). Roles: one warp copies, one issues the MMAs; eight unpack (four lane
+// Tensor memory: two accumulators and three A buffers (128 of k: 64 columns; split
+// two of 128). Roles: one warp copies, one issues the MMAs; eight unpack (four lane
 // quarters x even and odd groups, so that the latencies of a group's waits and
 // stores hide behind the other's); eight write the results (four quarters x two
 // halves of the rows, up to 80 sums a thread, for which the warpgroups' registers
@@ -57,7 +57,8 @@ struct Cfg {
   static constexpr int kChunks = kRows / 32;  // of 16 rows, that a writing warp takes
   static constexpr int kACols = 2 * kRows;
   static constexpr int kABuf = SPLIT ? 128 : 64;
-  static_assert(kACols + 2 * kABuf <= 512, "tensor memory");
+  static constexpr int kBufs = SPLIT ? 2 : 3;
+  static_assert(kACols + kBufs * kABuf <= 512 && kBufs < kStages, "tensor memory");
 };
 // Warpgroups: copies and MMAs; two that unpack; two that write. Registers a thread of each, which
 // draw on what the block is launched with.
@@ -351,7 +352,7 @@ __device__ void issuer(uint8_t* smem, Ctl* ctl, uint32_t tmem, const W4Args& a, 
         stage = 0;
         phase ^= 1u;
       }
-      buf ^= 1;
+      buf = buf + 1 == C::kBufs ? 0 : buf + 1;
     }
     if (failed) break;
     ptx::mma_commit(&ctl->dfull[acc]);
@@ -465,8 +466,8 @@ struct Ahead {
   }
 };
 
-// Groups `par`, par + 2, ... of this CTA's sequence of groups: the thread's column, 128 of k, into A
-// buffer par. U: of k that share a scale.
+// Groups `par`, par + 2, ... of this CTA's sequence of groups: the thread's column, 128 of k, into an
+// A buffer. U: of k that share a scale.
 template <int U, bool SPLIT>
 __device__ void unpacker(uint8_t* smem, Ctl* ctl, uint32_t tmem, int par, const W4Args& a,
                          const Walk& k) {
@@ -475,8 +476,7 @@ __device__ void unpacker(uint8_t* smem, Ctl* ctl, uint32_t tmem, int par, const 
   const int lane = threadIdx.x & 31, quarter = (threadIdx.x >> 5) & 3, l = 32 * quarter + lane;
   const int row = code_row(a.product == PGG_W4_GATED, l);
   const uint32_t codes = ptx::smem_addr(smem) + row * 128;
-  const uint32_t a_tmem =
-      tmem + (static_cast<uint32_t>(32 * quarter) << 16) + C::kACols + C::kABuf * par;
+  const uint32_t a_lanes = tmem + (static_cast<uint32_t>(32 * quarter) << 16) + C::kACols;
   uint32_t magic;  // the pair 2^10, from a register: an instruction holds one of two constants only
   asm volatile("mov.u32 %0, 0x64006400;" : "=r"(magic));
   int slot = 0;  // of codes: two groups of a tile
@@ -508,9 +508,11 @@ __device__ void unpacker(uint8_t* smem, Ctl* ctl, uint32_t tmem, int par, const 
         continue;
       }
       bool ok = ptx::mbar_wait(&ctl->cfull[slot], cphase, a.wait_limit_ns, abort);
-      if (mine && turn >= 2)  // the buffer's last group
-        ok = ok && ptx::mbar_wait(&ctl->done[(turn - 2) % kStages], ((turn - 2) / kStages) & 1u,
+      if (mine && turn >= C::kBufs) {  // the buffer's last group
+        const uint32_t last = turn - C::kBufs;
+        ok = ok && ptx::mbar_wait(&ctl->done[last % kStages], (last / kStages) & 1u,
                                   a.wait_limit_ns, abort);
+      }
       if (!__all_sync(0xFFFFFFFFu, ok)) {
         if (lane == 0) {
           ctl->abort = 1;
@@ -520,6 +522,7 @@ __device__ void unpacker(uint8_t* smem, Ctl* ctl, uint32_t tmem, int par, const 
       }
       if (mine) {
         ptx::tc_fence_after_sync();
+        const uint32_t a_tmem = a_lanes + C::kABuf * (turn % C::kBufs);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {  // 32 of k: four words, 16 columns of tensor memory
           const int chunk = (g & 1) * 4 + i;
