@@ -300,6 +300,19 @@ __device__ void copier(uint8_t* smem, Ctl* ctl, const CUtensorMap* tm, const W4A
 
 // ------------------------------------------------------------------ MMAs
 
+// One lane of a converged warp.
+__device__ __forceinline__ bool elected() {
+  uint32_t r;
+  asm volatile(
+      "{\n"
+      ".reg .pred p;\n"
+      "elect.sync _|p, 0xFFFFFFFF;\n"
+      "selp.u32 %0, 1, 0, p;\n"
+      "}\n"
+      : "=r"(r));
+  return r != 0;
+}
+
 // D[tmem] (+)= A[tmem] * B[smem]^T, fp16, fp32 accumulator.
 __device__ __forceinline__ void mma_tmem(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
                                          uint32_t idesc, uint32_t accumulate) {
@@ -313,7 +326,8 @@ __device__ __forceinline__ void mma_tmem(uint32_t d_tmem, uint32_t a_tmem, uint6
       : "memory");
 }
 
-// One thread.
+// One warp, of which one lane issues: the others keep it converged, so that what the MMAs take (all of
+// it the same in every lane) stays in uniform registers.
 template <bool SPLIT>
 __device__ void issuer(uint8_t* smem, Ctl* ctl, uint32_t tmem, const W4Args& a, const Walk& k) {
   using C = Cfg<SPLIT>;
@@ -327,27 +341,32 @@ __device__ void issuer(uint8_t* smem, Ctl* ctl, uint32_t tmem, const W4Args& a, 
     const uint32_t panel = static_cast<uint32_t>(x.rows16) * 128;
     const uint32_t idesc = ptx::idesc_make(0, kTile, x.rows16);
     const uint32_t d = tmem + C::kRows * acc;
-    if (!ptx::mbar_wait(&ctl->dempty[acc], dphase ^ 1u, a.wait_limit_ns, abort)) {
+    if (!__all_sync(0xFFFFFFFFu, ptx::mbar_wait(&ctl->dempty[acc], dphase ^ 1u, a.wait_limit_ns,
+                                                abort))) {
       failed = true;
       break;
     }
     for (int g = 0; g < k.groups; ++g) {
-      if (!ptx::mbar_wait(&ctl->full[stage], phase, a.wait_limit_ns, abort)) {
+      if (!__all_sync(0xFFFFFFFFu, ptx::mbar_wait(&ctl->full[stage], phase, a.wait_limit_ns,
+                                                  abort))) {
         failed = true;
         break;
       }
       ptx::tc_fence_after_sync();
       const uint32_t xb = ptx::smem_addr(xs + stage * kStageBytes);
       const uint32_t ab = tmem + C::kACols + C::kABuf * buf;
+      const uint64_t desc0 = ptx::sdesc_sw128(xb), desc1 = ptx::sdesc_sw128(xb + panel);
+      if (elected()) {
 #pragma unroll
-      for (int s = 0; s < kGroup / 16; ++s) {  // of 16 k
-        const uint64_t desc = ptx::sdesc_sw128(xb + (s >> 2) * panel) +
-                              static_cast<uint64_t>(((s & 3) * 32) >> 4);
-        mma_tmem(d, ab + 8 * s, desc, idesc, (g | s) > 0 ? 1u : 0u);
-        if (SPLIT) mma_tmem(d, ab + 64 + 8 * s, desc, idesc, 1u);
+        for (int s = 0; s < kGroup / 16; ++s) {  // of 16 k: 32 bytes of a panel's rows
+          const uint64_t desc = (s < 4 ? desc0 : desc1) + 2 * (s & 3);
+          mma_tmem(d, ab + 8 * s, desc, idesc, (g | s) > 0 ? 1u : 0u);
+          if (SPLIT) mma_tmem(d, ab + 64 + 8 * s, desc, idesc, 1u);
+        }
+        ptx::mma_commit(&ctl->done[stage]);
       }
+      __syncwarp();
       issued = true;
-      ptx::mma_commit(&ctl->done[stage]);
       if (++stage == kStages) {
         stage = 0;
         phase ^= 1u;
@@ -355,7 +374,8 @@ __device__ void issuer(uint8_t* smem, Ctl* ctl, uint32_t tmem, const W4Args& a, 
       buf = buf + 1 == C::kBufs ? 0 : buf + 1;
     }
     if (failed) break;
-    ptx::mma_commit(&ctl->dfull[acc]);
+    if (elected()) ptx::mma_commit(&ctl->dfull[acc]);
+    __syncwarp();
     acc ^= 1;
     if (acc == 0) dphase ^= 1u;
   }
@@ -365,7 +385,8 @@ __device__ void issuer(uint8_t* smem, Ctl* ctl, uint32_t tmem, const W4Args& a, 
   }
   if (issued) {
     int no_abort = 0;
-    ptx::mma_commit(&ctl->drain);
+    if (elected()) ptx::mma_commit(&ctl->drain);
+    __syncwarp();
     ptx::mbar_wait(&ctl->drain, 0u, a.wait_limit_ns, &no_abort);
   }
 }
@@ -715,7 +736,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (wg == 0) {
     fewer_registers<kFewRegs>();
     if (warp == 0 && lane == 0) copier(smem, ctl, &tm, a, k);
-    if (warp == 1 && lane == 0) issuer<SPLIT>(smem, ctl, tmem, a, k);
+    if (warp == 1) issuer<SPLIT>(smem, ctl, __shfl_sync(0xFFFFFFFFu, tmem, 0), a, k);
   } else if (wg <= 2) {
     fewer_registers<kUnpackRegs>();
     unpacker<U, SPLIT>(smem, ctl, tmem, wg - 1, a, k);
