@@ -667,20 +667,33 @@ def block_norm_grad(d_r, d_h, r, y=None, gate=None, post=None, post_weight=None,
     return dict(zip(names, d_params), d_x=d_x, d_y=d_y, d_gate=d_gate), workspace
 
 
+def _addresses(tensors, device):
+    """Addresses of dense tensors on the GPU of that index."""
+    for t in tensors:
+        if t.get_device() != device or not t.is_contiguous():
+            raise ValueError("tensors must be contiguous CUDA tensors of one device")
+    return [t.data_ptr() for t in tensors]
+
+
 def _grad_list(grads, workspace, norm):
     """(addresses, sizes, dtype codes, device, workspace, norm) of a list of gradients."""
     import torch
-    if not grads and workspace is None and norm is None:
+    given = [t for t in (workspace, norm) if t is not None]
+    if not grads and not given:
         raise ValueError("an empty list needs a workspace or norm to tell the device")
-    dev = (grads[0] if grads else workspace if workspace is not None else norm).device
-    _dense(*(t for t in (*grads, workspace, norm) if t is not None))
+    dev = (grads[0] if grads else given[0]).device
+    if dev.type != "cuda":
+        raise ValueError("tensors must be contiguous CUDA tensors of one device")
+    _addresses(given, dev.index)
     _is("norm", norm, (), torch.float32)
     if workspace is None:
         workspace = torch.empty(pgg_clip_workspace_size(len(grads)), dtype=torch.uint8, device=dev)
     if norm is None:
         norm = torch.empty((), dtype=torch.float32, device=dev)
-    return ([t.data_ptr() for t in grads], [t.numel() for t in grads],
-            [dtype_code(t.dtype) for t in grads], dev, workspace, norm)
+    dtypes = [t.dtype for t in grads]
+    codes = {d: dtype_code(d) for d in set(dtypes)}
+    return (_addresses(grads, dev.index), [t.numel() for t in grads], [codes[d] for d in dtypes],
+            dev, workspace, norm)
 
 
 def grad_norm(grads, scale: float = 1.0, norm=None, workspace=None, stream=None):
@@ -704,17 +717,17 @@ def clip_grads(grads, max_norm: float, eps: float = 1e-6, scale: float = 1.0, ou
     """
     out = grads if out is None else out
     ptrs, sizes, dtypes, dev, workspace, norm = _grad_list(grads, workspace, norm)
+    to = ptrs
     if out is not grads:
         if len(out) != len(grads):
             raise PggError(CODES["PGG_ERR_SHAPE"], "clip_grads")
-        if grads:
-            _dense(grads[0], *out)
+        to = _addresses(out, dev.index)
         for g, o in zip(grads, out):
-            _is("out", o, g.shape, g.dtype)
+            if g.dtype != o.dtype or g.shape != o.shape:
+                raise ValueError("out must hold tensors like the gradients")
     rc = pgg_clip_grads(ptrs, sizes, dtypes, max_norm, eps, scale, workspace.data_ptr(),
                         workspace.numel() * workspace.element_size(), norm.data_ptr(),
-                        ptrs if out is grads else [t.data_ptr() for t in out],
-                        _stream_of(stream, dev))
+                        to, _stream_of(stream, dev))
     if rc != 0:
         raise PggError(rc, "pgg_clip_grads")
     return norm, out, workspace

@@ -9,6 +9,7 @@ import ctypes
 import functools
 import os
 import threading
+from array import array
 
 from . import build as _build
 
@@ -471,25 +472,25 @@ def pgg_clip_workspace_size(count) -> int:
     return out.value
 
 
-def _tensor_list(grads, sizes, dtypes, out=()):
-    n = len(grads)
-    return ((ctypes.c_void_p * n)(*grads), (ctypes.c_int64 * n)(*sizes),
-            (ctypes.c_int * n)(*dtypes), (ctypes.c_void_p * n)(*out))
-
-
 def pgg_grad_norm(grads, sizes, dtypes, scale, workspace, workspace_bytes, norm, stream) -> int:
     """Raw call with sequences of integer device addresses, sizes and dtype codes."""
-    g, n, d, _ = _tensor_list(grads, sizes, dtypes)
-    return load().pgg_grad_norm(len(grads), g, n, d, scale, workspace, workspace_bytes, norm,
+    g, n, d = array("Q", grads), array("q", sizes), array("i", dtypes)
+    if not len(g) == len(n) == len(d):
+        raise PggError(CODES["PGG_ERR_SHAPE"], "pgg_grad_norm")
+    return load().pgg_grad_norm(len(g), g.buffer_info()[0], n.buffer_info()[0],
+                                d.buffer_info()[0], scale, workspace, workspace_bytes, norm,
                                 stream)
 
 
 def pgg_clip_grads(grads, sizes, dtypes, max_norm, eps, scale, workspace, workspace_bytes, norm,
                    out, stream) -> int:
     """Raw call with sequences of integer device addresses, sizes and dtype codes."""
-    g, n, d, o = _tensor_list(grads, sizes, dtypes, out)
-    return load().pgg_clip_grads(len(grads), g, n, d, max_norm, eps, scale, workspace,
-                                 workspace_bytes, norm, o, stream)
+    g, n, d, o = array("Q", grads), array("q", sizes), array("i", dtypes), array("Q", out)
+    if not len(g) == len(n) == len(d) == len(o):
+        raise PggError(CODES["PGG_ERR_SHAPE"], "pgg_clip_grads")
+    return load().pgg_clip_grads(len(g), g.buffer_info()[0], n.buffer_info()[0],
+                                 d.buffer_info()[0], max_norm, eps, scale, workspace,
+                                 workspace_bytes, norm, o.buffer_info()[0], stream)
 
 
 def pgg_status_string(code: int) -> str:

@@ -127,6 +127,16 @@ __device__ __forceinline__ float scale_at(const W4Args& a, int64_t i) {
   return a.bf16 ? __uint_as_float(static_cast<uint32_t>(v) << 16) : __half2float(__ushort_as_half(v));
 }
 
+// A number's size, 0 where it is not finite; the largest of a word of scales.
+__device__ __forceinline__ float finite(float v) { return fabsf(v) < INFINITY ? fabsf(v) : 0.0f; }
+template <int DT>
+__device__ __forceinline__ float largest(const W4Args& a, uint32_t w) {
+  if (a.scale_f32) return finite(__uint_as_float(w));
+  float lo, hi;
+  vec::unpack2<DT>(w, lo, hi);
+  return fmaxf(finite(lo), finite(hi));
+}
+
 // The power of two of a number that is to become m 2^e with m in [0.5, 1).
 __device__ __forceinline__ int exponent_of(float most) {
   int e = 0;
@@ -147,18 +157,28 @@ __global__ void __launch_bounds__(128)
   if (static_cast<int>(blockIdx.x) >= row_blocks) {
     const int64_t columns = a.product == PGG_W4_GATED ? 2 * a.N : a.N;
     const int64_t step = static_cast<int64_t>(gridDim.x - row_blocks) * 16;
-    const int lane = tid & 7;
+    const int lane = tid & 7, es = a.scale_f32 ? 4 : 2;
+    // a column's scales are whole words of 16 bytes
+    const bool words =
+        a.groups * es % 16 == 0 && reinterpret_cast<uintptr_t>(a.scales) % 16 == 0;
     // (whole warps walk together: the exchange below needs them)
     const int64_t end = (a.G * columns + 3) / 4 * 4;
     for (int64_t c = (static_cast<int64_t>(blockIdx.x) - row_blocks) * 16 + (tid >> 3); c < end;
          c += step) {
       float most = 0.0f;
       const bool live = c < a.G * columns && group_list[c / columns] > 0;
-      if (live)
-        for (int64_t i = lane; i < a.groups; i += 8) {
-          const float v = fabsf(scale_at(a, c * a.groups + i));
-          if (v < INFINITY) most = fmaxf(most, v);
+      if (live && words) {
+        const uint4* p = reinterpret_cast<const uint4*>(static_cast<const char*>(a.scales) +
+                                                        c * a.groups * es);
+        for (int i = lane; i < a.groups * es / 16; i += 8) {
+          const uint4 q = __ldg(p + i);
+          most = fmaxf(fmaxf(most, largest<DT>(a, q.x)), largest<DT>(a, q.y));
+          most = fmaxf(fmaxf(most, largest<DT>(a, q.z)), largest<DT>(a, q.w));
         }
+      } else if (live) {
+        for (int64_t i = lane; i < a.groups; i += 8)
+          most = fmaxf(most, finite(scale_at(a, c * a.groups + i)));
+      }
 #pragma unroll
       for (int d = 1; d < 8; d *= 2) most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, d));
       if (live && lane == 0) a.col_exponent[c] = exponent_of(most) - 9;
@@ -183,7 +203,7 @@ __global__ void __launch_bounds__(128)
       vec::load<DT, 8>(x, k, v);
 #pragma unroll
       for (int j = 0; j < 8; ++j)  // (infinities and NaN stay what they are under any power)
-        most = fmaxf(most, fabsf(v[j]) < INFINITY ? fabsf(v[j]) : 0.0f);
+        most = fmaxf(most, finite(v[j]));
     }
     most = block_max(most, s_max);
     const int exponent = exponent_of(most) - 15;
