@@ -33,7 +33,7 @@ SOURCES = ["pgg_api.cu", "route_prep.cu", "gmm_dx.cu", "gmm_dx_simt.cu", "gmm_dw
            "ops_simt.cu",
            "gated_grad.cu", "rows_wide.cu",
            "rows_skinny.cu", "adapters_few.cu", "rows_outer.cu", "block_api.cu", "w4_simt.cu", "w4_stream.cu", "w4_wide.cu",
-           "block_norm.cu", "grad_clip.cu"]
+           "block_norm.cu", "block_norm_rows.cu", "grad_clip.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -10,23 +10,23 @@
 //     N'(d) = rstd (u - v^ mean(u v^) - mean(u)),  u = d (offset + w)  (rms: no mean(u))
 //     d_w = sum over rows of d v^,  d_b = sum over rows of d
 //
-// A block of threads takes a row at a time; sums are fp32 (variances of the
-// centred values), and the pre norm takes r before it is rounded. Memory bounds
-// it, so while a row's sums go round the block the next rows are on their way:
-// every thread copies (cp.async) what it will read itself into shared memory and
-// waits for its own copies only, and reads them again for each pass over the row,
-// which leaves its registers to the parameters (forward) and to its columns'
-// parts of the parameters' gradients (backward), kept over all rows of the block;
-// the blocks' sums are added in their order by a second launch: bitwise
-// repeatable. Sums of one pass go round together: the gradient of an rms norm
-// needs sum r^2 and sum u r, and 1 / deviation can be multiplied in afterwards.
-// Rows that are no multiple of 16 bytes are read from memory each time (the first
-// level cache holds them), too long ones with one element a thread and turn.
+// Here are the rows that block_norm_rows.cu does not take: no multiple of 16 bytes,
+// or too long for a block's threads with 16 elements each. A block takes a row at a
+// time; sums are fp32 (variances of the centred values), and the pre norm takes r
+// before it is rounded. Rows of 16-byte vectors go through shared memory: every
+// thread copies (cp.async) what it will read itself, while the row before is worked
+// on, and reads it again for each pass; others are read from memory each time (the
+// first level cache holds them); ones that are longer still with one element a
+// thread and turn. Columns' parts of the parameters' gradients are kept over all
+// rows of a block, and the blocks' sums are added in their order by a second
+// launch: bitwise repeatable. Instructions bound it: 4000 x 6999 takes 301 us, its
+// gradient 711, 4000 x 8704 (as rms norms, 16-bit) 99 and 348.
 
 #include <atomic>
 #include <cstdint>
 
 #include "pgg_block.h"
+#include "pgg_block_sum.cuh"
 #include "pgg_ops_launch.h"
 #include "pgg_ptx.cuh"
 #include "pgg_vec.cuh"
@@ -97,54 +97,6 @@ struct Rows {
   }
 };
 
-// Sums of K values (1, or up to 4) over the block, the same bits in every thread. Two buffers in
-// turn, so that one barrier a call is enough. Four values are added together: after two exchanges a
-// lane goes on with one of them, so that it takes 6 shuffles, not 20, before the barrier and 7 after.
-template <int K>
-struct BlockSum {
-  float part[2][32][K == 1 ? 1 : 4];
-};
-
-template <int K, int M>
-__device__ __forceinline__ void block_sum(BlockSum<M>* s, int* turn, float (&v)[K]) {
-  static_assert(K <= M && K != 2, "room, and values by one or three");
-  constexpr uint32_t kAll = 0xFFFFFFFFu;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-  if constexpr (K == 1) {
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) v[0] += __shfl_xor_sync(kAll, v[0], d);
-    if (warps == 1) return;
-    if (lane == 0) s->part[*turn][warp][0] = v[0];
-    __syncthreads();
-    v[0] = lane < warps ? s->part[*turn][lane][0] : 0.0f;
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) v[0] += __shfl_xor_sync(kAll, v[0], d);
-  } else {
-    // lane bit 0 picks values {0, 1} or {2, 3}, bit 1 one of the two
-    const float v2 = v[2], v3 = K > 3 ? v[K - 1] : 0.0f;
-    const bool b0 = lane & 1, b1 = lane & 2;
-    float x = (b0 ? v2 : v[0]) + __shfl_xor_sync(kAll, b0 ? v[0] : v2, 1);
-    float y = (b0 ? v3 : v[1]) + __shfl_xor_sync(kAll, b0 ? v[1] : v3, 1);
-    x = (b1 ? y : x) + __shfl_xor_sync(kAll, b1 ? x : y, 2);
-#pragma unroll
-    for (int d = 4; d < 32; d *= 2) x += __shfl_xor_sync(kAll, x, d);
-    if (warps > 1) {
-      if (lane < 4) s->part[*turn][warp][lane] = x;
-      __syncthreads();
-      x = 0.0f;
-      for (int w = lane >> 2; w < warps; w += 8) x += s->part[*turn][w][lane & 3];
-#pragma unroll
-      for (int d = 4; d < 32; d *= 2) x += __shfl_xor_sync(kAll, x, d);
-    }
-    // lane 0: value 0, lane 2: value 1, lane 1: value 2, lane 3: value 3
-    v[0] = __shfl_sync(kAll, x, 0);
-    v[1] = __shfl_sync(kAll, x, 2);
-    v[2] = __shfl_sync(kAll, x, 1);
-    if constexpr (K > 3) v[K - 1] = __shfl_sync(kAll, x, 3);
-  }
-  *turn ^= 1;
-}
-
 // The weight's factor and the bias of V columns.
 template <int DT, int V>
 __device__ __forceinline__ void affine(const void* w, const void* b, bool f32, float offset,
@@ -165,45 +117,15 @@ __device__ __forceinline__ void affine(const void* w, const void* b, bool f32, f
   }
 }
 
-// One parameter (a weight with its offset, or a channel's gate) of this thread's columns: P16: of the
-// rows' 16-bit dtype, kept packed in registers; else read each time. 1 where there is none.
-template <int DT, int V, int NV, bool P16>
+// One parameter (a weight with its offset, or a channel's gate); 1 where there is none.
+template <int DT, int V>
 struct Param {
-  uint32_t raw[P16 ? NV : 1][P16 ? V / 2 : 1];
   const void* p;
   float offset;
   bool f32;
 
-  __device__ __forceinline__ void init(const NormArgs& a, const void* param, float add, int n) {
-    p = param;
-    offset = add;
-    f32 = a.p_f32;
-    if constexpr (P16) {
-      if (!param) offset = 1.0f;
-#pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        const int q = j * blockDim.x + threadIdx.x;
-#pragma unroll
-        for (int c = 0; c < V / 2; ++c) raw[j][c] = 0;
-        if (param && q < n) {
-          const uint4 w = __ldg(static_cast<const uint4*>(param) + q);
-          raw[j][0] = w.x;
-          raw[j][1] = w.y;
-          raw[j][2] = w.z;
-          raw[j][3] = w.w;
-        }
-      }
-    }
-  }
-  __device__ __forceinline__ void get(int j, int q, float (&v)[V]) const {
-    if constexpr (P16) {
-#pragma unroll
-      for (int c = 0; c < V / 2; ++c) {
-        vec::unpack2<DT>(raw[j][c], v[2 * c], v[2 * c + 1]);
-        v[2 * c] += offset;
-        v[2 * c + 1] += offset;
-      }
-    } else if (p) {
+  __device__ __forceinline__ void get(int q, float (&v)[V]) const {
+    if (p) {
       vec::load_or_f32<DT, V>(p, f32, q * V, v);
 #pragma unroll
       for (int c = 0; c < V; ++c) v[c] += offset;
@@ -232,7 +154,7 @@ __device__ __forceinline__ void gate_at(const NormArgs& a, int64_t t, int64_t i,
 // ------------------------------------------------------------------ rows held by a block
 
 // LEAN: rms norms or none, a gate of one number a channel or none.
-template <int DT, int V, int NV, bool RING, bool LEAN, bool P16, int THREADS>
+template <int DT, int V, int NV, bool RING, bool LEAN, int THREADS>
 __global__ void __launch_bounds__(THREADS, 1024 / THREADS) block_norm_kernel(const NormArgs a, const int ring) {
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ BlockSum<1> s;
@@ -250,10 +172,10 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) block_norm_kernel(con
   const bool by_row = !LEAN && (a.gate_kind == PGG_GATE_FULL || a.gate_kind == PGG_GATE_TOKEN);
   const int post = LEAN && a.post != PGG_NORM_NONE ? PGG_NORM_RMS : a.post;
   const bool layer = !LEAN && a.pre == PGG_NORM_LAYER;
-  Param<DT, V, NV, P16> f_post, f_pre, channel;
-  f_post.init(a, a.w_post, a.weight_offset, n);
-  f_pre.init(a, a.w_pre, a.weight_offset, n);
-  channel.init(a, a.gate_kind == PGG_GATE_CHANNEL ? a.gate : nullptr, 0.0f, n);
+  const Param<DT, V> f_post = {a.w_post, a.weight_offset, a.p_f32 != 0},
+                     f_pre = {a.w_pre, a.weight_offset, a.p_f32 != 0},
+                     channel = {a.gate_kind == PGG_GATE_CHANNEL ? a.gate : nullptr, 0.0f,
+                                a.p_f32 != 0};
   for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
     if (RING) {  // (a group of copies a row: those of the `ring` - 1 rows behind may be pending)
       if (ring > 2) ptx::cp_async_wait<2>(); else if (ring == 2) ptx::cp_async_wait<1>(); else ptx::cp_async_wait<0>();
@@ -303,11 +225,11 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) block_norm_kernel(con
         float y[V];
         rows.read(smem, slot, t, 1, q, y_f32, y);
         float f[V], g[V];
-        f_post.get(j, q, f);
+        f_post.get(q, f);
         if (by_row)
           gate_at<DT, V>(a, t, q * V, g);
         else
-          channel.get(j, q, g);
+          channel.get(q, g);
         if constexpr (LEAN) {
 #pragma unroll
           for (int c = 0; c < V; ++c) r[j][c] = fmaf(y[c] * rstd, f[c] * g[c], r[j][c]);
@@ -349,7 +271,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) block_norm_kernel(con
       const int q = j * blockDim.x + tid;
       if (q >= n) continue;
       float f[V];
-      f_pre.get(j, q, f);
+      f_pre.get(q, f);
       if constexpr (LEAN) {
 #pragma unroll
         for (int c = 0; c < V; ++c) r[j][c] = r[j][c] * rstd * f[c];
@@ -364,11 +286,8 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) block_norm_kernel(con
   }
 }
 
-// Columns' sums that a block keeps: gate (channel), w_post, b_post, w_pre, b_pre.
-enum { kColGate, kColWPost, kColBPost, kColWPre, kColBPre, kCols };
-
 // LEAN as above: no sums for a bias either.
-template <int DT, int V, int NV, bool RING, bool LEAN, bool P16, int THREADS>
+template <int DT, int V, int NV, bool RING, bool LEAN, int THREADS>
 __global__ void __launch_bounds__(THREADS, 1)
     block_norm_grad_kernel(const NormArgs a, const int ring) {
   extern __shared__ __align__(16) uint8_t smem[];
@@ -391,12 +310,12 @@ __global__ void __launch_bounds__(THREADS, 1)
   rows.add(3, pre ? a.x : nullptr, DT == PGG_F32);
   for (int i = 0; RING && i < ring; ++i)
     rows.fetch(smem, i, blockIdx.x + static_cast<int64_t>(i) * gridDim.x, a.T);
-  float col[BIAS ? kCols : 3][NV][V] = {};  // without BIAS: gate, w_post, w_pre
+  float col[BIAS ? kNormCols : 3][NV][V] = {};  // without BIAS: gate, w_post, w_pre
   constexpr int kWPre = BIAS ? kColWPre : 2;
-  Param<DT, V, NV, P16> f_post, f_pre, channel;
-  f_post.init(a, a.w_post, a.weight_offset, n);
-  f_pre.init(a, a.w_pre, a.weight_offset, n);
-  channel.init(a, a.gate_kind == PGG_GATE_CHANNEL ? a.gate : nullptr, 0.0f, n);
+  const Param<DT, V> f_post = {a.w_post, a.weight_offset, a.p_f32 != 0},
+                     f_pre = {a.w_pre, a.weight_offset, a.p_f32 != 0},
+                     channel = {a.gate_kind == PGG_GATE_CHANNEL ? a.gate : nullptr, 0.0f,
+                                a.p_f32 != 0};
   auto bias_at = [&](int q, float (&b)[V]) {
     float one[V];
     affine<DT, V>(nullptr, BIAS ? a.b_post : nullptr, a.p_f32, 0.0f, q * V, one, b);
@@ -405,7 +324,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (by_row)
       gate_at<DT, V>(a, t, q * V, g);
     else
-      channel.get(j, q, g);
+      channel.get(q, g);
   };
   for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
     if (RING) {
@@ -435,7 +354,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         float r[V], dh[V], f[V];
         rows.read(smem, slot, t, 3, q, DT == PGG_F32, r);
         rows.read(smem, slot, t, 2, q, dh_f32, dh);
-        f_pre.get(j, q, f);
+        f_pre.get(q, f);
 #pragma unroll
         for (int c = 0; c < V; ++c) {
           const float v = LEAN ? r[c] : r[c] - mean, u = dh[c] * f[c];
@@ -478,7 +397,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         float r[V], dh[V], f[V];
         rows.read(smem, slot, t, 3, q, DT == PGG_F32, r);
         rows.read(smem, slot, t, 2, q, dh_f32, dh);
-        f_pre.get(j, q, f);
+        f_pre.get(q, f);
 #pragma unroll
         for (int c = 0; c < V; ++c) {
           const float v = (LEAN ? r[c] : r[c] - mean) * rstd;
@@ -495,7 +414,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       if (have_y && (a.post != PGG_NORM_NONE || token)) {
         float y[V], f[V], b[V], gate[V];
         rows.read(smem, slot, t, 1, q, y_f32, y);
-        f_post.get(j, q, f);
+        f_post.get(q, f);
         if (BIAS) bias_at(q, b);
         gate_of(t, j, q, gate);
 #pragma unroll
@@ -531,7 +450,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (q >= n) continue;
         float y[V], f[V], b[V], gate[V], whole[V];
         rows.read(smem, slot, t, 1, q, y_f32, y);
-        f_post.get(j, q, f);
+        f_post.get(q, f);
         if (BIAS) bias_at(q, b);
         gate_of(t, j, q, gate);
 #pragma unroll
@@ -559,14 +478,14 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
   }
 #pragma unroll
-  for (int k = 0; k < (BIAS ? kCols : 3); ++k) {
+  for (int k = 0; k < (BIAS ? kNormCols : 3); ++k) {
     const int which = BIAS ? k : (k == 2 ? static_cast<int>(kColWPre) : k);
     if (!a.d_cols[which]) continue;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int q = j * blockDim.x + tid;
       if (q < n)
-        vec::store<PGG_F32, V>(a.partial, (static_cast<int64_t>(blockIdx.x) * kCols + which) * a.H
+        vec::store<PGG_F32, V>(a.partial, (static_cast<int64_t>(blockIdx.x) * kNormCols + which) * a.H
                                               + q * V, col[k][j]);
     }
   }
@@ -645,7 +564,7 @@ __global__ void __launch_bounds__(kMaxThreads) block_norm_grad_long_kernel(const
   ptx::griddep_wait();
   if (blockIdx.x == 0 && threadIdx.x == 0) a.hdr->status = 0;
   const float inv_h = 1.0f / static_cast<float>(a.H);
-  float* mine = a.partial + static_cast<int64_t>(blockIdx.x) * kCols * a.H;
+  float* mine = a.partial + static_cast<int64_t>(blockIdx.x) * kNormCols * a.H;
   for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
     const int64_t t0 = t * a.H;
     const bool first = t == blockIdx.x;
@@ -739,7 +658,7 @@ __global__ void __launch_bounds__(256) block_norm_cols_kernel(const NormArgs a, 
   float sum = 0.0f;
   if (i < a.H) {
 #pragma unroll 8
-    for (int64_t b = share * per; b < b1; ++b) sum += a.partial[(b * kCols + blockIdx.y) * a.H + i];
+    for (int64_t b = share * per; b < b1; ++b) sum += a.partial[(b * kNormCols + blockIdx.y) * a.H + i];
   }
   s_sum[share][lane] = sum;
   __syncthreads();
@@ -817,10 +736,10 @@ bool lean(const NormArgs& a) {
          (a.gate_kind == PGG_GATE_NONE || a.gate_kind == PGG_GATE_CHANNEL);
 }
 
-template <int DT, int V, int NV, bool LEAN, bool P16, int THREADS>
+template <int DT, int V, int NV, bool LEAN, int THREADS>
 cudaError_t launch_forward_t(const NormArgs& a, int threads, int num_sms, cudaStream_t stream) {
   constexpr bool kHeld = V >= 4;
-  auto kern = block_norm_kernel<DT, V, NV, kHeld, LEAN, P16, THREADS>;
+  auto kern = block_norm_kernel<DT, V, NV, kHeld, LEAN, THREADS>;
   static Fit fit;
   static SmemLimit limit;
   int blocks;
@@ -836,21 +755,19 @@ cudaError_t launch_forward_t(const NormArgs& a, int threads, int num_sms, cudaSt
 
 template <int DT, int V, int NV, int THREADS>
 cudaError_t launch_forward_f(const NormArgs& a, int threads, int num_sms, cudaStream_t stream) {
-  if constexpr (V == 8 && NV <= 2) {  // (more would not leave four blocks an SM)
-    if (lean(a) && !a.p_f32)
-      return launch_forward_t<DT, V, NV, true, true, THREADS>(a, threads, num_sms, stream);
-  }
   if (V >= 4 && lean(a))
-    return launch_forward_t<DT, V, NV, V >= 4, false, THREADS>(a, threads, num_sms, stream);
-  return launch_forward_t<DT, V, NV, false, false, THREADS>(a, threads, num_sms, stream);
+    return launch_forward_t<DT, V, NV, V >= 4, THREADS>(a, threads, num_sms, stream);
+  return launch_forward_t<DT, V, NV, false, THREADS>(a, threads, num_sms, stream);
 }
 
 template <int DT, int V>
 cudaError_t launch_forward(const NormArgs& a, int num_sms, cudaStream_t stream) {
   int nv, threads;
   if (shape(a.H / V, &nv, &threads) && (V < 4 || forward_bytes<DT>(a) <= kRingBytes)) {
-    if (nv == 1) return launch_forward_f<DT, V, 1, 256>(a, threads, num_sms, stream);
-    if (nv == 2) return launch_forward_f<DT, V, 2, 512>(a, threads, num_sms, stream);
+    if constexpr (V < 4) {
+      if (nv == 1) return launch_forward_f<DT, V, 1, 256>(a, threads, num_sms, stream);
+      if (nv == 2) return launch_forward_f<DT, V, 2, 512>(a, threads, num_sms, stream);
+    }
     return launch_forward_f<DT, V, 4, 512>(a, threads, num_sms, stream);
   }
   const int64_t grid = a.T < 2 * num_sms ? a.T : 2 * num_sms;
@@ -858,65 +775,54 @@ cudaError_t launch_forward(const NormArgs& a, int num_sms, cudaStream_t stream) 
                     dim3(kMaxThreads), 0, stream, 1, a);
 }
 
-template <int DT, int V, int NV, bool LEAN, bool P16, int THREADS>
+template <int DT, int V, int NV, bool LEAN, int THREADS>
 cudaError_t launch_backward_t(const NormArgs& a, int threads, cudaStream_t stream) {
   constexpr bool kHeld = V >= 4;
   static SmemLimit limit;
   const int64_t row = backward_bytes<DT>(a), blocks = norm_grad_blocks(a.T, a.H);
   const int ring = kHeld ? ring_rows(row, static_cast<int>((blocks + 151) / 152)) : 0;
-  return launch_rows(&limit, block_norm_grad_kernel<DT, V, NV, kHeld, LEAN, P16, THREADS>, blocks,
+  return launch_rows(&limit, block_norm_grad_kernel<DT, V, NV, kHeld, LEAN, THREADS>, blocks,
                      threads, ring * row, stream, a, ring);
 }
 
 template <int DT, int V, int NV, int THREADS>
 cudaError_t launch_backward_f(const NormArgs& a, int threads, cudaStream_t stream) {
-  if constexpr (V == 8) {
-    if (lean(a) && !a.p_f32)
-      return launch_backward_t<DT, V, NV, true, true, THREADS>(a, threads, stream);
-  }
   if (V >= 4 && lean(a))
-    return launch_backward_t<DT, V, NV, V >= 4, false, THREADS>(a, threads, stream);
-  return launch_backward_t<DT, V, NV, false, false, THREADS>(a, threads, stream);
+    return launch_backward_t<DT, V, NV, V >= 4, THREADS>(a, threads, stream);
+  return launch_backward_t<DT, V, NV, false, THREADS>(a, threads, stream);
 }
 
 template <int DT, int V>
 cudaError_t launch_backward(const NormArgs& a, cudaStream_t stream) {
   const int64_t n = a.H / V;
-  cudaError_t err;
   // two vectors a thread (four: the columns' sums no longer fit the registers)
   const int nv = n <= 256 ? 1 : n <= 1024 ? 2 : 4;
   const int threads = static_cast<int>(((n + nv - 1) / nv + 31) / 32 * 32);
   if (threads <= 512 && (V < 4 || backward_bytes<DT>(a) <= kRingBytes)) {
-    if (nv == 1)
-      err = launch_backward_f<DT, V, 1, 256>(a, threads, stream);
-    else if (nv == 2)
-      err = launch_backward_f<DT, V, 2, 512>(a, threads, stream);
-    else
-      err = launch_backward_f<DT, V, 4, 512>(a, threads, stream);
-  } else {
-    err = launch_pdl(block_norm_grad_long_kernel<DT>,
-                     dim3(static_cast<unsigned>(norm_grad_blocks(a.T, a.H))), dim3(kMaxThreads), 0,
-                     stream, 1, a);
+    if constexpr (V < 4) {
+      if (nv == 1) return launch_backward_f<DT, V, 1, 256>(a, threads, stream);
+      if (nv == 2) return launch_backward_f<DT, V, 2, 512>(a, threads, stream);
+    }
+    return launch_backward_f<DT, V, 4, 512>(a, threads, stream);
   }
-  if (err != cudaSuccess) return err;
-  for (int i = 0; i < kCols; ++i)
-    if (a.d_cols[i])
-      return launch_pdl(block_norm_cols_kernel, dim3(static_cast<unsigned>((a.H + 31) / 32), kCols),
-                        dim3(256), 0, stream, 1, a, norm_grad_blocks(a.T, a.H));
-  return cudaSuccess;
+  return launch_pdl(block_norm_grad_long_kernel<DT>,
+                    dim3(static_cast<unsigned>(norm_grad_blocks(a.T, a.H))), dim3(kMaxThreads), 0,
+                    stream, 1, a);
 }
 
 }  // namespace
 
 // One block an SM holds long rows; of short ones several do, and hide each other's sums.
 int64_t norm_grad_blocks(int64_t T, int64_t H) {
-  const int64_t most = 152 * (H > 4096 ? 1 : H > 2048 ? 2 : H > 1024 ? 3 : 6);
+  const int64_t most = 152 * (H > 4096 ? 1 : H > 1024 ? 2 : H > 512 ? 4 : 8);
   return T < most ? T : most;
 }
 
 // words: 16, 4 (two 16-bit elements, or one fp32) or 0 for rows that are read element by element.
 cudaError_t launch_block_norm(int dtype, const NormArgs& a, int words, int num_sms,
                               cudaStream_t stream) {
+  cudaError_t err;
+  if (launch_block_norm_rows(dtype, a, words, num_sms, stream, &err)) return err;
   if (dtype == PGG_F32)
     return words == 16 ? launch_forward<PGG_F32, 4>(a, num_sms, stream)
                        : launch_forward<PGG_F32, 1>(a, num_sms, stream);
@@ -932,18 +838,28 @@ cudaError_t launch_block_norm(int dtype, const NormArgs& a, int words, int num_s
 }
 
 cudaError_t launch_block_norm_grad(int dtype, const NormArgs& a, int words, cudaStream_t stream) {
-  if (dtype == PGG_F32)
-    return words == 16 ? launch_backward<PGG_F32, 4>(a, stream)
-                       : launch_backward<PGG_F32, 1>(a, stream);
-  if (dtype == PGG_F16)
-    return words == 16  ? launch_backward<PGG_F16, 8>(a, stream)
-           : words == 4 ? launch_backward<PGG_F16, 2>(a, stream)
-                        : launch_backward<PGG_F16, 1>(a, stream);
-  if (dtype == PGG_BF16)
-    return words == 16  ? launch_backward<PGG_BF16, 8>(a, stream)
-           : words == 4 ? launch_backward<PGG_BF16, 2>(a, stream)
-                        : launch_backward<PGG_BF16, 1>(a, stream);
-  return cudaErrorInvalidValue;
+  cudaError_t err;
+  if (!launch_block_norm_rows_grad(dtype, a, words, stream, &err)) {
+    if (dtype == PGG_F32)
+      err = words == 16 ? launch_backward<PGG_F32, 4>(a, stream)
+                        : launch_backward<PGG_F32, 1>(a, stream);
+    else if (dtype == PGG_F16)
+      err = words == 16  ? launch_backward<PGG_F16, 8>(a, stream)
+            : words == 4 ? launch_backward<PGG_F16, 2>(a, stream)
+                         : launch_backward<PGG_F16, 1>(a, stream);
+    else if (dtype == PGG_BF16)
+      err = words == 16  ? launch_backward<PGG_BF16, 8>(a, stream)
+            : words == 4 ? launch_backward<PGG_BF16, 2>(a, stream)
+                         : launch_backward<PGG_BF16, 1>(a, stream);
+    else
+      err = cudaErrorInvalidValue;
+  }
+  if (err != cudaSuccess) return err;
+  for (int i = 0; i < kNormCols; ++i)
+    if (a.d_cols[i])
+      return launch_pdl(block_norm_cols_kernel, dim3(static_cast<unsigned>((a.H + 31) / 32), kNormCols),
+                        dim3(256), 0, stream, 1, a, norm_grad_blocks(a.T, a.H));
+  return cudaSuccess;
 }
 
 }  // namespace pgg

@@ -86,12 +86,20 @@ struct NormArgs {
   float residual_scale, weight_offset, eps;
 };
 
+// Columns' sums that a block of the backward keeps, in the order of d_cols.
+enum { kColGate, kColWPost, kColBPost, kColWPre, kColBPre, kNormCols };
+
 // Blocks whose column sums the backward keeps apart.
 int64_t norm_grad_blocks(int64_t T, int64_t H);
 // words: bytes of a vector of the dtype that all rows allow: 16, 4, or 0 (element by element).
 cudaError_t launch_block_norm(int dtype, const NormArgs& a, int words, int num_sms,
                               cudaStream_t stream);
 cudaError_t launch_block_norm_grad(int dtype, const NormArgs& a, int words, cudaStream_t stream);
+// Rows of 16-byte vectors that fit a block's threads: false, and nothing launched, where they do not.
+bool launch_block_norm_rows(int dtype, const NormArgs& a, int words, int num_sms,
+                           cudaStream_t stream, cudaError_t* err);
+bool launch_block_norm_rows_grad(int dtype, const NormArgs& a, int words, cudaStream_t stream,
+                                cudaError_t* err);
 
 // ------------------------------------------------------------ the gradients' norm
 
