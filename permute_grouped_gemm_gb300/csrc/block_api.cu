@@ -30,8 +30,11 @@ constexpr int kVariantWide = 0;    // tensor cores, row blocks of up to 256 rows
 constexpr int kVariantStream = 1;  // tensor cores, the codes streamed for blocks of 8 to 32 rows
 constexpr int kVariantSimt = 3;    // FP32 pipes: any dtype, size and alignment
 
-// Up to this many rows per live expert the codes are streamed.
-constexpr double kStreamRows = 32.0;
+// Up to this many rows per live expert the codes are streamed: 64 experts, K 7168, F 2048, gated, us
+// streamed / wide: 16 rows 375 / 414, 24 rows 409 / 418, 32 rows 568 / 423; with zero points 386 / 555,
+// 422 / 561 and 582 / 572; groups of 32 537 / 593, 570 / 598, 794 / 604. (The wide form reads and
+// unpacks a weight once whatever the rows are; streamed blocks have at most 32 rows.)
+constexpr double kStreamRows = 24.0;
 
 struct W4Plan {
   int variant;

@@ -5,8 +5,9 @@
 // A stage is 256 of k. A warp takes 32 columns x 128 of k of it and multiplies
 // with mma.sync m16n8k16 in fp16: the codes, unpacked in registers, are the A
 // operand, eight rows of x the B operand. What the loop is made for is few
-// instructions a code (logic runs at half rate: two an eight codes' word took
-// 250 us, where this takes 150: 64 experts, 512 rows, K 7168, F 2048):
+// instructions a code (64 experts, 512 rows, K 7168, F 2048: 227 us, with codes
+// made to halves by an OR and a subtraction of halves 248; the bytes alone, copied
+// and not multiplied, take some 180):
 //
 //   - A code needs no conversion: the four bits alone, (w & 0x000F000F), are two
 //     fp16 subnormals of code 2^-24, and (w & 0x00F000F0) two of code 2^-20, so a
@@ -83,7 +84,7 @@ struct Cfg {
 };
 
 struct Ctl {
-  uint64_t full[kMaxStages];   // bytes by TMA, the copying warp's cp.async and its stores
+  uint64_t full[kMaxStages];   // bytes by TMA, and the copying warp's stores
   uint64_t empty[kMaxStages];  // read by all eight warps
   int abort;
   int last;                    // this CTA is the one that adds the tile's parts
@@ -221,22 +222,38 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
       : "memory");
 }
 
-// Completion of this thread's cp.async so far arrives at `bar`.
-__device__ __forceinline__ void arrive_when_copied(uint64_t* bar) {
-  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(ptx::smem_addr(bar))
-               : "memory");
-}
-
+// B bytes (4, 8, 16 or 32) from memory into words, and from words to shared memory.
 template <int B>
-__device__ __forceinline__ void cp_async(uint32_t dst, const void* src) {
-  if constexpr (B == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-  else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(B) : "memory");
+__device__ __forceinline__ void load_bytes(const void* p, uint32_t* w) {
+  if constexpr (B == 4) {
+    w[0] = __ldg(static_cast<const uint32_t*>(p));
+  } else if constexpr (B == 8) {
+    const uint2 v = __ldg(static_cast<const uint2*>(p));
+    w[0] = v.x, w[1] = v.y;
+  } else {
+#pragma unroll
+    for (int i = 0; i < B / 16; ++i) {
+      const uint4 v = __ldg(static_cast<const uint4*>(p) + i);
+      w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
+    }
+  }
+}
+template <int B>
+__device__ __forceinline__ void store_bytes(uint8_t* p, const uint32_t* w) {
+  if constexpr (B == 4) {
+    *reinterpret_cast<uint32_t*>(p) = w[0];
+  } else if constexpr (B == 8) {
+    *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < B / 16; ++i)
+      reinterpret_cast<uint4*>(p)[i] =
+          make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+  }
 }
 
-// Codes by TMA, x as one piece, the columns' scales and zeros as they stand in memory: by cp.async
-// where a stage's scales of a column are one aligned piece, else one by one.
+// Codes by TMA, x as one piece, the columns' scales and zeros as they stand in memory, through
+// registers: a stage's of a column in one load where they are one aligned piece, else one by one.
 template <int NT, int U>
 __device__ void copier(uint8_t* smem, Ctl* ctl, const CUtensorMap* tm, const W4Args& a,
                        const Walk& k) {
@@ -248,12 +265,12 @@ __device__ void copier(uint8_t* smem, Ctl* ctl, const CUtensorMap* tm, const W4A
   const int64_t columns = gated ? 2 * a.N : a.N;
   const int es = a.scale_f32 ? 4 : 2;
   const uint32_t groups = static_cast<uint32_t>(a.groups);
-  constexpr int kPiece2 = kS * 2 < 16 ? kS * 2 : 16, kPiece4 = kS * 4 < 16 ? kS * 4 : 16;
+  const int piece = kS * es < 16 ? kS * es : 16;
   // the same of zeros, for a load of one to eight bytes
   const bool whole_z = a.group == U && groups % kS == 0 &&
                        reinterpret_cast<uintptr_t>(a.zeros) % kS == 0;
   const bool whole = a.group == U && groups % kS == 0 &&
-                     reinterpret_cast<uintptr_t>(a.scales) % (es == 4 ? kPiece4 : kPiece2) == 0;
+                     reinterpret_cast<uintptr_t>(a.scales) % piece == 0;
   int stage = 0;
   uint32_t phase = 0, outstanding = 0, last_parity = 0;
   bool failed = false;
@@ -274,7 +291,33 @@ __device__ void copier(uint8_t* smem, Ctl* ctl, const CUtensorMap* tm, const W4A
     }
     for (; ks < k.nks && s < k.end; ++ks, ++s) {
       const uint32_t unit = static_cast<uint32_t>(ks) * kS;
-      uint64_t z[4] = {};  // (loaded before the wait: they need no room yet)
+      // scales and zeros are loaded before the wait: they need no room yet
+      uint32_t raw[4][kS];  // 16 bits: kS / 2 words each
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const char* src = static_cast<const char*>(a.scales) + (at[i] + unit) * es;
+        if (whole && unit < groups) {  // (groups end with a stage, so all of its are there)
+          if (a.scale_f32)
+            load_bytes<4 * kS>(src, raw[i]);
+          else
+            load_bytes<2 * kS>(src, raw[i]);
+        } else {
+#pragma unroll
+          for (int u = 0; u < kS; ++u) {
+            uint32_t group = unit + u;
+            if (a.group != U) group = group * U / static_cast<uint32_t>(a.group);
+            const bool in = group < groups;  // (x is 0 behind, but 0 inf is not)
+            if (a.scale_f32) {
+              raw[i][u] = in ? __ldg(static_cast<const uint32_t*>(a.scales) + at[i] + group) : 0;
+            } else {
+              const uint32_t v =
+                  in ? __ldg(static_cast<const uint16_t*>(a.scales) + at[i] + group) : 0;
+              raw[i][u / 2] = u & 1 ? raw[i][u / 2] | v << 16 : v;
+            }
+          }
+        }
+      }
+      uint64_t z[4] = {};
       if (a.zeros && unit * U < static_cast<uint64_t>(a.K)) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -314,34 +357,12 @@ __device__ void copier(uint8_t* smem, Ctl* ctl, const CUtensorMap* tm, const W4A
       last_parity = (last_parity & ~(1u << stage)) | (phase << stage);
       uint8_t* sc = px + C::kXBytes;
       uint8_t* zs = sc + C::kScaleBytes;
-      if (whole && unit < groups) {  // (groups end with a stage, so all of its are there)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const char* src = static_cast<const char*>(a.scales) + (at[i] + unit) * es;
-          const uint32_t dst = ptx::smem_addr(sc) + (lane + 32 * i) * kS * es;
-          if (a.scale_f32) {
-            cp_async<kPiece4>(dst, src);
-            if (kS == 8) cp_async<16>(dst + 16, src + 16);
-          } else {
-            cp_async<kPiece2>(dst, src);
-          }
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int u = 0; u < kS; ++u) {
-            uint32_t group = unit + u;
-            if (a.group != U) group = group * U / static_cast<uint32_t>(a.group);
-            const bool in = group < groups;  // (x is 0 behind, but 0 inf is not)
-            const int to = (lane + 32 * i) * kS + u;
-            if (a.scale_f32)
-              reinterpret_cast<uint32_t*>(sc)[to] =
-                  in ? __ldg(static_cast<const uint32_t*>(a.scales) + at[i] + group) : 0;
-            else
-              reinterpret_cast<uint16_t*>(sc)[to] =
-                  in ? __ldg(static_cast<const uint16_t*>(a.scales) + at[i] + group) : 0;
-          }
+      for (int i = 0; i < 4; ++i) {
+        if (a.scale_f32)
+          store_bytes<4 * kS>(sc + (lane + 32 * i) * 4 * kS, raw[i]);
+        else
+          store_bytes<2 * kS>(sc + (lane + 32 * i) * 2 * kS, raw[i]);
       }
       if (a.zeros) {
 #pragma unroll
@@ -353,7 +374,6 @@ __device__ void copier(uint8_t* smem, Ctl* ctl, const CUtensorMap* tm, const W4A
           if constexpr (kS == 8) reinterpret_cast<uint64_t*>(zs)[lane + 32 * i] = z[i];
         }
       }
-      arrive_when_copied(full);
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(full);
       if (++stage == C::kStages) {
@@ -592,6 +612,9 @@ __device__ void multiplier(uint8_t* smem, Ctl* ctl, float* red, int w, const W4A
           }
         }
       }
+      // (the stage's next bytes are the asynchronous proxy's: without the fence they have overtaken the
+      // last of these loads)
+      ptx::fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(&ctl->empty[stage]);
       if (++stage == C::kStages) {
@@ -663,7 +686,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<NT, U>::kCtas)
   const int warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
-      ptx::mbar_init(&ctl.full[s], 1 + 32 + 1);
+      ptx::mbar_init(&ctl.full[s], 2);
       ptx::mbar_init(&ctl.empty[s], kMmaWarps);
     }
     ctl.abort = 0;

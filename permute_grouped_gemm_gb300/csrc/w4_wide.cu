@@ -19,7 +19,8 @@
 // (hi and what is left), and the MMAs run twice. Scaling each group's fp32 sums
 // instead costs more: tensor memory is read at about 20 bytes a cycle and
 // quarter, so bringing back 128 x 144 sums took 880 cycles, the products of a
-// group of 128 are 580 (2048 tokens, 60 experts: 1432 us, now XX).
+// group of 128 are 580 (2048 tokens, 60 experts, K 7168, F 2048: 1432 us, now 818;
+// with zeros 1610).
 //
 // Tensor memory: two accumulators and three A buffers (128 of k: 64 columns; split
 // two of 128). Roles: one warp copies, one issues the MMAs; eight unpack (four lane
@@ -146,7 +147,8 @@ __device__ __forceinline__ int exponent_of(float most) {
 
 // The first `row_blocks` blocks: a row of a row block, its power of two and its values as the MMA
 // reads them, 128 threads a row. The others: the columns' powers of two, eight lanes a column of an
-// expert with rows: its largest scale comes to lie in [2^8, 2^9).
+// expert with rows: its largest scale comes to lie in [2^8, 2^9), and lower by the bits that a zero
+// above 16 has over four, so that scale (code - zero) stays below 2^13.
 template <int DT>
 __global__ void __launch_bounds__(128)
     w4_pack_wide_kernel(const W4Args a, const int64_t* group_list, const int row_blocks) {
@@ -161,6 +163,7 @@ __global__ void __launch_bounds__(128)
     // a column's scales are whole words of 16 bytes
     const bool words =
         a.groups * es % 16 == 0 && reinterpret_cast<uintptr_t>(a.scales) % 16 == 0;
+    const bool zero_words = a.groups % 4 == 0 && reinterpret_cast<uintptr_t>(a.zeros) % 4 == 0;
     // (whole warps walk together: the exchange below needs them)
     const int64_t end = (a.G * columns + 3) / 4 * 4;
     for (int64_t c = (static_cast<int64_t>(blockIdx.x) - row_blocks) * 16 + (tid >> 3); c < end;
@@ -179,9 +182,26 @@ __global__ void __launch_bounds__(128)
         for (int64_t i = lane; i < a.groups; i += 8)
           most = fmaxf(most, finite(scale_at(a, c * a.groups + i)));
       }
+      uint32_t zero = 16;  // the column's largest, at least this
+      if (live && a.zeros) {
+        const uint8_t* z = a.zeros + c * a.groups;
+        if (zero_words) {
+          for (int i = lane; i < a.groups / 4; i += 8) {
+            const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(z) + i);
+            zero = max(max(max(zero, w & 255u), w >> 8 & 255u), max(w >> 16 & 255u, w >> 24));
+          }
+        } else {
+          for (int64_t i = lane; i < a.groups; i += 8)
+            zero = max(zero, static_cast<uint32_t>(__ldg(z + i)));
+        }
+      }
 #pragma unroll
-      for (int d = 1; d < 8; d *= 2) most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, d));
-      if (live && lane == 0) a.col_exponent[c] = exponent_of(most) - 9;
+      for (int d = 1; d < 8; d *= 2) {
+        most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, d));
+        zero = max(zero, __shfl_xor_sync(0xFFFFFFFFu, zero, d));
+      }
+      if (live && lane == 0)
+        a.col_exponent[c] = exponent_of(most) - 9 + (32 - __clz(static_cast<int>(zero - 1)) - 4);
     }
     return;
   }
@@ -604,7 +624,7 @@ __device__ void unpacker(uint8_t* smem, Ctl* ctl, uint32_t tmem, int par, const 
           now.load(a, next * a.groups, g + 2 - k.groups);
           loaded = true;
         }
-        ptx::tmem_st_wait();
+        ptx::tmem_st_wait();  // (so the codes have been read: TMA may write their slot)
         ptx::tc_fence_before_sync();
         __syncwarp();
         if (lane == 0) {
