@@ -204,7 +204,8 @@ const char* pgg_status_string(int status);
  * pgg_debug_force_variant: -1 = automatic (default), 0 .. 5 = force the
  *   variant reported by pgg_dx_plan (2, 4 and 5 exist for the 16-bit dtypes
  *   only, 5 for an even N only; rows that are not a multiple of 16 bytes
- *   take variant 5 when they can, else 3).
+ *   take variant 5 when they can, else 3). The 4-bit products take 0 (many
+ *   rows an expert), 1 (codes streamed) and 3 where their sizes allow them.
  * pgg_debug_set_band_k_blocks: k-blocks per band of the tile order (0 =
  *   automatic). The result does not depend on it, bit for bit: only the time
  *   order of the tiles changes, never the order of the additions.
@@ -681,9 +682,14 @@ int pgg_adapters_grad(const void* d_y, const void* x, const void* weight, const 
  *   workspace at least pgg_w4_workspace_size bytes, 256-byte aligned; status word
  *            at offset 0. When the routing is not valid the output is zero-filled.
  *
- * The weights are not rounded: a group's sum of x (code - zero) is taken in fp32
- * and then scaled (or each weight is formed in fp32), all sums are fp32, each
- * output is rounded once. Bitwise repeatable.
+ * Sums are fp32, each output is rounded once, and the weights are not rounded to
+ * 16 bits: few rows an expert multiply x with the codes and then a group's fp32 sum
+ * with its scale; many rows multiply with the weight as one fp16 number where that
+ * is exact (bf16 scales, no zeros) and as the sum of two (22 bits) otherwise; fp32
+ * x, and K or groupSize that is no multiple of 32, form each weight in fp32. x, a row
+ * at a time, and the weights, a column at a time, are brought to fp16's range by a
+ * power of two: a 16-bit x keeps its bits but for what lies below 2^-35 of its row's
+ * largest finite value, a weight likewise in its column. Bitwise repeatable.
  */
 typedef enum { PGG_W4_ROWS = 0, PGG_W4_GATED = 1, PGG_W4_COMBINED = 2 } pgg_w4_product;
 
