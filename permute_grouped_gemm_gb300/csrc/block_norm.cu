@@ -775,39 +775,45 @@ cudaError_t launch_forward(const NormArgs& a, int num_sms, cudaStream_t stream) 
                     dim3(kMaxThreads), 0, stream, 1, a);
 }
 
+// Most blocks: one an SM of the longest rows (1500 x 1021, fp32: 45 us, with two 49, with four 51: each
+// leaves columns' sums to add), of short ones as many as 1024 threads are (10000 x 333: 143 us, with
+// half of them 170).
+constexpr int64_t held_blocks(int threads) { return 152 * (threads >= 512 ? 1 : 1024 / threads); }
+
 template <int DT, int V, int NV, bool LEAN, int THREADS>
-cudaError_t launch_backward_t(const NormArgs& a, int threads, cudaStream_t stream) {
+cudaError_t launch_backward_t(const NormArgs& a, int threads, int64_t* grid, cudaStream_t stream) {
   constexpr bool kHeld = V >= 4;
   static SmemLimit limit;
-  const int64_t row = backward_bytes<DT>(a), blocks = norm_grad_blocks(a.T, a.H);
+  const int64_t row = backward_bytes<DT>(a), most = held_blocks(threads);
+  const int64_t blocks = *grid < most ? *grid : most;
+  *grid = blocks;
   const int ring = kHeld ? ring_rows(row, static_cast<int>((blocks + 151) / 152)) : 0;
   return launch_rows(&limit, block_norm_grad_kernel<DT, V, NV, kHeld, LEAN, THREADS>, blocks,
                      threads, ring * row, stream, a, ring);
 }
 
 template <int DT, int V, int NV, int THREADS>
-cudaError_t launch_backward_f(const NormArgs& a, int threads, cudaStream_t stream) {
+cudaError_t launch_backward_f(const NormArgs& a, int threads, int64_t* grid, cudaStream_t stream) {
   if (V >= 4 && lean(a))
-    return launch_backward_t<DT, V, NV, V >= 4, THREADS>(a, threads, stream);
-  return launch_backward_t<DT, V, NV, false, THREADS>(a, threads, stream);
+    return launch_backward_t<DT, V, NV, V >= 4, THREADS>(a, threads, grid, stream);
+  return launch_backward_t<DT, V, NV, false, THREADS>(a, threads, grid, stream);
 }
 
 template <int DT, int V>
-cudaError_t launch_backward(const NormArgs& a, cudaStream_t stream) {
+cudaError_t launch_backward(const NormArgs& a, int64_t* grid, cudaStream_t stream) {
   const int64_t n = a.H / V;
   // two vectors a thread (four: the columns' sums no longer fit the registers)
   const int nv = n <= 256 ? 1 : n <= 1024 ? 2 : 4;
   const int threads = static_cast<int>(((n + nv - 1) / nv + 31) / 32 * 32);
   if (threads <= 512 && (V < 4 || backward_bytes<DT>(a) <= kRingBytes)) {
     if constexpr (V < 4) {
-      if (nv == 1) return launch_backward_f<DT, V, 1, 256>(a, threads, stream);
-      if (nv == 2) return launch_backward_f<DT, V, 2, 512>(a, threads, stream);
+      if (nv == 1) return launch_backward_f<DT, V, 1, 256>(a, threads, grid, stream);
+      if (nv == 2) return launch_backward_f<DT, V, 2, 512>(a, threads, grid, stream);
     }
-    return launch_backward_f<DT, V, 4, 512>(a, threads, stream);
+    return launch_backward_f<DT, V, 4, 512>(a, threads, grid, stream);
   }
   return launch_pdl(block_norm_grad_long_kernel<DT>,
-                    dim3(static_cast<unsigned>(norm_grad_blocks(a.T, a.H))), dim3(kMaxThreads), 0,
-                    stream, 1, a);
+                    dim3(static_cast<unsigned>(*grid)), dim3(kMaxThreads), 0, stream, 1, a);
 }
 
 }  // namespace
@@ -839,18 +845,19 @@ cudaError_t launch_block_norm(int dtype, const NormArgs& a, int words, int num_s
 
 cudaError_t launch_block_norm_grad(int dtype, const NormArgs& a, int words, cudaStream_t stream) {
   cudaError_t err;
+  int64_t grid = norm_grad_blocks(a.T, a.H);  // (a launch may take fewer)
   if (!launch_block_norm_rows_grad(dtype, a, words, stream, &err)) {
     if (dtype == PGG_F32)
-      err = words == 16 ? launch_backward<PGG_F32, 4>(a, stream)
-                        : launch_backward<PGG_F32, 1>(a, stream);
+      err = words == 16 ? launch_backward<PGG_F32, 4>(a, &grid, stream)
+                        : launch_backward<PGG_F32, 1>(a, &grid, stream);
     else if (dtype == PGG_F16)
-      err = words == 16  ? launch_backward<PGG_F16, 8>(a, stream)
-            : words == 4 ? launch_backward<PGG_F16, 2>(a, stream)
-                         : launch_backward<PGG_F16, 1>(a, stream);
+      err = words == 16  ? launch_backward<PGG_F16, 8>(a, &grid, stream)
+            : words == 4 ? launch_backward<PGG_F16, 2>(a, &grid, stream)
+                         : launch_backward<PGG_F16, 1>(a, &grid, stream);
     else if (dtype == PGG_BF16)
-      err = words == 16  ? launch_backward<PGG_BF16, 8>(a, stream)
-            : words == 4 ? launch_backward<PGG_BF16, 2>(a, stream)
-                         : launch_backward<PGG_BF16, 1>(a, stream);
+      err = words == 16  ? launch_backward<PGG_BF16, 8>(a, &grid, stream)
+            : words == 4 ? launch_backward<PGG_BF16, 2>(a, &grid, stream)
+                         : launch_backward<PGG_BF16, 1>(a, &grid, stream);
     else
       err = cudaErrorInvalidValue;
   }
@@ -858,7 +865,7 @@ cudaError_t launch_block_norm_grad(int dtype, const NormArgs& a, int words, cuda
   for (int i = 0; i < kNormCols; ++i)
     if (a.d_cols[i])
       return launch_pdl(block_norm_cols_kernel, dim3(static_cast<unsigned>((a.H + 31) / 32), kNormCols),
-                        dim3(256), 0, stream, 1, a, norm_grad_blocks(a.T, a.H));
+                        dim3(256), 0, stream, 1, a, grid);
   return cudaSuccess;
 }
 
