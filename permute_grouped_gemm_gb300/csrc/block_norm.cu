@@ -19,8 +19,9 @@
 // first level cache holds them); ones that are longer still with one element a
 // thread and turn. Columns' parts of the parameters' gradients are kept over all
 // rows of a block, and the blocks' sums are added in their order by a second
-// launch: bitwise repeatable. Instructions bound it: 4000 x 6999 takes 301 us, its
-// gradient 711, 4000 x 8704 (as rms norms, 16-bit) 99 and 348.
+// launch: bitwise repeatable. Instructions bound it: 4000 x 6999 takes 273 us, its
+// gradient 629 (one element a thread and turn: 301 and 708; up to eight vectors a
+// thread are the rule where they fit), 4000 x 8704 (as rms norms, 16-bit) 99 and 346.
 
 #include <atomic>
 #include <cstdint>
@@ -669,12 +670,13 @@ __global__ void __launch_bounds__(256) block_norm_cols_kernel(const NormArgs a, 
   out[i] = sum;
 }
 
-// Rows of n vectors: vectors a thread (1, 2 or 4) and threads, at most 512; false: too long.
-bool shape(int64_t n, int* nv, int* threads) {
-  for (*nv = 1; *nv <= 4; *nv *= 2) {
+// Rows of n vectors: vectors a thread (1, 2, 4 or, where rows are read from memory, 8) and threads;
+// false: too long.
+bool shape(int64_t n, bool eight, int* nv, int* threads) {
+  for (*nv = 1; *nv <= (eight ? 8 : 4); *nv *= 2) {
     const int64_t need = ((n + *nv - 1) / *nv + 31) / 32 * 32;
     *threads = static_cast<int>(need);
-    if (need <= (*nv == 1 ? 256 : 512)) return true;
+    if (need <= (*nv == 1 ? 256 : *nv == 8 ? kMaxThreads : 512)) return true;
   }
   return false;
 }
@@ -763,10 +765,11 @@ cudaError_t launch_forward_f(const NormArgs& a, int threads, int num_sms, cudaSt
 template <int DT, int V>
 cudaError_t launch_forward(const NormArgs& a, int num_sms, cudaStream_t stream) {
   int nv, threads;
-  if (shape(a.H / V, &nv, &threads) && (V < 4 || forward_bytes<DT>(a) <= kRingBytes)) {
+  if (shape(a.H / V, V < 4, &nv, &threads) && (V < 4 || forward_bytes<DT>(a) <= kRingBytes)) {
     if constexpr (V < 4) {
       if (nv == 1) return launch_forward_f<DT, V, 1, 256>(a, threads, num_sms, stream);
       if (nv == 2) return launch_forward_f<DT, V, 2, 512>(a, threads, num_sms, stream);
+      if (nv == 8) return launch_forward_f<DT, V, 8, kMaxThreads>(a, threads, num_sms, stream);
     }
     return launch_forward_f<DT, V, 4, 512>(a, threads, num_sms, stream);
   }
@@ -803,12 +806,13 @@ template <int DT, int V>
 cudaError_t launch_backward(const NormArgs& a, int64_t* grid, cudaStream_t stream) {
   const int64_t n = a.H / V;
   // two vectors a thread (four: the columns' sums no longer fit the registers)
-  const int nv = n <= 256 ? 1 : n <= 1024 ? 2 : 4;
+  const int nv = n <= 256 ? 1 : n <= 1024 ? 2 : n <= 2048 || V >= 4 ? 4 : 8;
   const int threads = static_cast<int>(((n + nv - 1) / nv + 31) / 32 * 32);
-  if (threads <= 512 && (V < 4 || backward_bytes<DT>(a) <= kRingBytes)) {
+  if (threads <= (nv == 8 ? kMaxThreads : 512) && (V < 4 || backward_bytes<DT>(a) <= kRingBytes)) {
     if constexpr (V < 4) {
       if (nv == 1) return launch_backward_f<DT, V, 1, 256>(a, threads, grid, stream);
       if (nv == 2) return launch_backward_f<DT, V, 2, 512>(a, threads, grid, stream);
+      if (nv == 8) return launch_backward_f<DT, V, 8, kMaxThreads>(a, threads, grid, stream);
     }
     return launch_backward_f<DT, V, 4, 512>(a, threads, grid, stream);
   }

@@ -90,3 +90,17 @@ def test_in_place(gate):
     got = pgg.block_norm_grad(d, s["d_h"], r, s["y"], d_x=d, **kwargs(s))[0]
     for name, g in want.items():
         assert g is None or torch.equal(g, got[name]), name
+
+
+@pytest.mark.parametrize("post,pre,gate,bias", [("rms", "rms", "channel", False),
+                                                ("layer", "layer", "full", True),
+                                                ("layer", "rms", "token", True)])
+@pytest.mark.parametrize("dtype,y,H", [("bf16", "fp32", 3001), ("bf16", "bf16", 6998),
+                                       ("fp16", "fp32", 8191), ("fp32", "fp32", 5003),
+                                       ("bf16", "fp32", 8193), ("fp16", "fp16", 16382),
+                                       ("bf16", "bf16", 16386)])
+def test_long_rows_of_odd_lengths(dtype, y, H, post, pre, gate, bias):
+    s = case(T=170, H=H, dtype=dtype, y=y, params=dtype, post=post, pre=pre, gate=gate, bias=bias,
+             seed=H)
+    check_forward(s)
+    check_backward(s)
