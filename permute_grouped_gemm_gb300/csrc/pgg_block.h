@@ -30,7 +30,7 @@ struct W4Args {
   int32_t* exponent;     // [row blocks][rows of a block] their powers of two
   int32_t* col_exponent; // (wide) [G][C] the columns' powers of two
   int32_t block_rows;    // (wide) most rows of a block (set by the launch)
-  int4* meta;            // (wide) of each packed row: {output row, power of two, weight, 0}
+  int4* meta;            // (wide) of each packed row: {output row or -1, power of two, weight, 0}
   float* parts;          // [2 kW4Grid][rows of a block][128] sums of the tiles that CTAs share
   uint32_t* arrived;     // [kW4Grid] parts of the tile that begins in a CTA; zeros at the start
   int32_t n_blocks;      // blocks of columns (set by the launch)

@@ -45,6 +45,7 @@
 #include "pgg_ops_mma.cuh"
 #include "pgg_ptx.cuh"
 #include "pgg_vec.cuh"
+#include "pgg_w4_rows.cuh"
 
 namespace pgg {
 namespace {
@@ -57,6 +58,7 @@ constexpr int kThreads = 32 * (1 + kMmaWarps);
 constexpr int kCodeBytes = kTile * kStep / 2;
 constexpr int kRedStride = kTile + 4;
 constexpr int kMaxStages = 8;
+constexpr int32_t kWritten = INT32_MIN;  // as a row's power of two: its results are there already
 
 // NT: eights of rows. U: of k that share a scale (a divisor of the group).
 template <int NT, int U>
@@ -164,20 +166,29 @@ __global__ void __launch_bounds__(128) w4_pack_kernel(const W4Args a) {
                              : check_index(a.hdr, a.rowinfo[row].token, a.batch, 174);
     const uint16_t* x = static_cast<const uint16_t*>(a.x) + xrow * a.K;
     float most = 0.0f;
+    bool infinite = false;
     for (int64_t k = 8 * tid; k < a.K; k += 8 * 128) {
       float v[8];
       vec::load<DT, 8>(x, k, v);
 #pragma unroll
-      for (int j = 0; j < 8; ++j)  // (infinities and NaN stay what they are under any power)
-        most = fmaxf(most, fabsf(v[j]) < INFINITY ? fabsf(v[j]) : 0.0f);
+      for (int j = 0; j < 8; ++j) {
+        const bool is = fabsf(v[j]) < INFINITY;
+        most = fmaxf(most, is ? fabsf(v[j]) : 0.0f);
+        infinite = infinite || !is;
+      }
     }
     most = block_max(most, s_max);
+    infinite = __syncthreads_or(infinite) != 0;
     int exponent = 0;  // of two: most = m 2^exponent, m in [0.5, 1)
     if (most > 0.0f) frexpf(most, &exponent);
     exponent -= 15;
     // 2^-exponent in two factors (it may lie outside fp32)
     const float by0 = ldexpf(1.0f, -(exponent / 2)), by1 = ldexpf(1.0f, -(exponent - exponent / 2));
-    if (tid == 0) a.exponent[i] = exponent;
+    if (tid == 0) a.exponent[i] = infinite ? kWritten : exponent;
+    if (infinite) {
+      const int64_t pos = check_index(a.hdr, a.rowinfo[row].rank, a.M, 178);
+      write_infinite_row<DT>(a, x, check_index(a.hdr, e.x, a.G, 179), row, pos);
+    }
     char* out = static_cast<char*>(a.packed) + rb * nks * C::kXBytes;
     const int64_t end = nks * kStep;
     for (int64_t k = 8 * tid; k < end; k += 8 * 128) {
@@ -456,7 +467,8 @@ __device__ __forceinline__ void write_tile(const float* red, const W4Args& a, co
     if (n >= a.N) continue;
     const int64_t row = x.row0 + j;
     const int64_t pos = check_index(a.hdr, a.rowinfo[row].rank, a.M, 176);
-    const int e = a.exponent[static_cast<int64_t>(x.rb) * (8 * NT) + j] + 24;
+    const int power = a.exponent[static_cast<int64_t>(x.rb) * (8 * NT) + j], e = power + 24;
+    if (power == kWritten) continue;
     const float* r = red + j * kRedStride + c;
     float v0 = ldexpf(r[0], e), v1 = ldexpf(r[1], e);
     if (gated) {

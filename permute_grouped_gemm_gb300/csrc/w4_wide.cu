@@ -41,6 +41,7 @@
 #include "pgg_ops_mma.cuh"
 #include "pgg_ptx.cuh"
 #include "pgg_vec.cuh"
+#include "pgg_w4_rows.cuh"
 
 namespace pgg {
 namespace {
@@ -218,23 +219,28 @@ __global__ void __launch_bounds__(128)
                              : check_index(a.hdr, a.rowinfo[row].token, a.batch, 184);
     const uint16_t* x = static_cast<const uint16_t*>(a.x) + xrow * a.K;
     float most = 0.0f;
+    bool infinite = false;
     for (int64_t k = 8 * tid; k < a.K; k += 8 * 128) {
       float v[8];
       vec::load<DT, 8>(x, k, v);
 #pragma unroll
-      for (int j = 0; j < 8; ++j)  // (infinities and NaN stay what they are under any power)
+      for (int j = 0; j < 8; ++j) {
         most = fmaxf(most, finite(v[j]));
+        infinite = infinite || !(fabsf(v[j]) < INFINITY);
+      }
     }
     most = block_max(most, s_max);
+    infinite = __syncthreads_or(infinite) != 0;
     const int exponent = exponent_of(most) - 15;
     const float by0 = ldexpf(1.0f, -(exponent / 2)), by1 = ldexpf(1.0f, -(exponent - exponent / 2));
     const int64_t prow = packed_row(e, rb);
-    if (tid == 0) {  // what the results need to know of the row
-      const int64_t pos = check_index(a.hdr, a.rowinfo[row].rank, a.M, 189);
+    const int64_t pos = check_index(a.hdr, a.rowinfo[row].rank, a.M, 189);
+    if (tid == 0) {  // what the results need to know of the row (-1: they are there already)
       const float p = a.probs ? a.probs[pos] : 1.0f;
-      a.meta[prow + n] = make_int4(static_cast<int>(a.product == PGG_W4_COMBINED ? pos : row),
-                                   exponent, __float_as_int(p), 0);
+      const int to = static_cast<int>(a.product == PGG_W4_COMBINED ? pos : row);
+      a.meta[prow + n] = make_int4(infinite ? -1 : to, exponent, __float_as_int(p), 0);
     }
+    if (infinite) write_infinite_row<DT>(a, x, check_index(a.hdr, e.x, a.G, 190), row, pos);
     char* out = static_cast<char*>(a.packed) + prow * width * 2;
     const int64_t panel = static_cast<int64_t>((e.z + 15) / 16 * 16) * 128;
     for (int64_t k = 8 * tid; k < width; k += 8 * 128) {
@@ -699,8 +705,9 @@ __device__ void writer(Ctl* ctl, uint32_t tmem, int half, const W4Args& a, const
           const float up = __shfl_xor_sync(0xFFFFFFFFu, v, 1);
           v = gate(v, up, __int_as_float(__shfl_sync(0xFFFFFFFFu, m[c].z, i)));
         }
-        const int64_t to = static_cast<int64_t>(__shfl_sync(0xFFFFFFFFu, m[c].x, i)) * a.N + f;
-        if (!writes) continue;
+        const int row = __shfl_sync(0xFFFFFFFFu, m[c].x, i);
+        const int64_t to = static_cast<int64_t>(row) * a.N + f;
+        if (!writes || row < 0) continue;
         if (a.out_f32)
           static_cast<float*>(a.out)[to] = v;
         else if (a.bf16)
