@@ -8,6 +8,19 @@
 
 namespace pgg {
 
+// The largest |x| of a row over its 128 threads, and (rest, 0 for each thread whose values are finite)
+// whether it holds an infinity or NaN; the largest is then 1.
+__device__ __forceinline__ float row_max(float v, float rest, float* s, bool* infinite) {
+  const bool bad = __any_sync(0xFFFFFFFFu, rest != 0.0f);
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, d));
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = bad ? -1.0f : v;
+  __syncthreads();
+  *infinite = fminf(fminf(s[0], s[1]), fminf(s[2], s[3])) < 0.0f;
+  return *infinite ? 1.0f : fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3]));
+}
+
 constexpr int kListed = 512;  // positions of infinities that a block keeps
 
 // The results of a row of x that holds infinities or NaN, by the definition: each element that is not

@@ -134,16 +134,6 @@ __device__ __forceinline__ int64_t column_of(const W4Args& a, const Tile& x, int
 
 // ------------------------------------------------------------------ x
 
-// Sum of one value a thread over 128 threads, and the largest.
-__device__ __forceinline__ float block_max(float v, float* s) {
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, d));
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = v;
-  __syncthreads();
-  return fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3]));
-}
-
 // A row of a row block: its power of two, its values in the products' order, and its groups' sums.
 // 128 threads a row, eight of k a thread and turn.
 template <int DT, int NT, int U>
@@ -165,20 +155,18 @@ __global__ void __launch_bounds__(128) w4_pack_kernel(const W4Args a) {
                              ? row
                              : check_index(a.hdr, a.rowinfo[row].token, a.batch, 174);
     const uint16_t* x = static_cast<const uint16_t*>(a.x) + xrow * a.K;
-    float most = 0.0f;
-    bool infinite = false;
+    float most = 0.0f, rest = 0.0f;  // rest: 0 times the values, NaN where one is not finite
     for (int64_t k = 8 * tid; k < a.K; k += 8 * 128) {
       float v[8];
       vec::load<DT, 8>(x, k, v);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const bool is = fabsf(v[j]) < INFINITY;
-        most = fmaxf(most, is ? fabsf(v[j]) : 0.0f);
-        infinite = infinite || !is;
+        most = fmaxf(most, fabsf(v[j]));
+        rest = fmaf(v[j], 0.0f, rest);
       }
     }
-    most = block_max(most, s_max);
-    infinite = __syncthreads_or(infinite) != 0;
+    bool infinite;
+    most = row_max(most, rest, s_max, &infinite);
     int exponent = 0;  // of two: most = m 2^exponent, m in [0.5, 1)
     if (most > 0.0f) frexpf(most, &exponent);
     exponent -= 15;

@@ -114,15 +114,6 @@ __device__ __forceinline__ Tile tile_of(uint32_t t, const W4Args& a) {
 
 // ------------------------------------------------------------------ x
 
-__device__ __forceinline__ float block_max(float v, float* s) {
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, d));
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = v;
-  __syncthreads();
-  return fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3]));
-}
-
 __device__ __forceinline__ float scale_at(const W4Args& a, int64_t i) {
   if (a.scale_f32) return __ldg(static_cast<const float*>(a.scales) + i);
   const uint16_t v = __ldg(static_cast<const uint16_t*>(a.scales) + i);
@@ -218,29 +209,31 @@ __global__ void __launch_bounds__(128)
                              ? row
                              : check_index(a.hdr, a.rowinfo[row].token, a.batch, 184);
     const uint16_t* x = static_cast<const uint16_t*>(a.x) + xrow * a.K;
-    float most = 0.0f;
-    bool infinite = false;
+    float most = 0.0f, rest = 0.0f;  // rest: 0 times the values, NaN where one is not finite
     for (int64_t k = 8 * tid; k < a.K; k += 8 * 128) {
       float v[8];
       vec::load<DT, 8>(x, k, v);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        most = fmaxf(most, finite(v[j]));
-        infinite = infinite || !(fabsf(v[j]) < INFINITY);
+        most = fmaxf(most, fabsf(v[j]));
+        rest = fmaf(v[j], 0.0f, rest);
       }
     }
-    most = block_max(most, s_max);
-    infinite = __syncthreads_or(infinite) != 0;
+    bool infinite;
+    most = row_max(most, rest, s_max, &infinite);
     const int exponent = exponent_of(most) - 15;
     const float by0 = ldexpf(1.0f, -(exponent / 2)), by1 = ldexpf(1.0f, -(exponent - exponent / 2));
     const int64_t prow = packed_row(e, rb);
-    const int64_t pos = check_index(a.hdr, a.rowinfo[row].rank, a.M, 189);
     if (tid == 0) {  // what the results need to know of the row (-1: they are there already)
+      const int64_t pos = check_index(a.hdr, a.rowinfo[row].rank, a.M, 189);
       const float p = a.probs ? a.probs[pos] : 1.0f;
       const int to = static_cast<int>(a.product == PGG_W4_COMBINED ? pos : row);
       a.meta[prow + n] = make_int4(infinite ? -1 : to, exponent, __float_as_int(p), 0);
     }
-    if (infinite) write_infinite_row<DT>(a, x, check_index(a.hdr, e.x, a.G, 190), row, pos);
+    if (infinite) {
+      const int64_t pos = check_index(a.hdr, a.rowinfo[row].rank, a.M, 190);
+      write_infinite_row<DT>(a, x, check_index(a.hdr, e.x, a.G, 191), row, pos);
+    }
     char* out = static_cast<char*>(a.packed) + prow * width * 2;
     const int64_t panel = static_cast<int64_t>((e.z + 15) / 16 * 16) * 128;
     for (int64_t k = 8 * tid; k < width; k += 8 * 128) {
