@@ -21,18 +21,18 @@
 // of sums over the block, one after the other; here row t's second round and row
 // t+1's first go together, one barrier a row, so a layer norm's mean and variance
 // are of one round: sums of v - k and (v - k)^2, k the mean of the row's first
-// eight (four) elements. k is within deviation * sqrt(H / 8) of the row's mean whatever
-// the row holds, so the rounding of the difference is at most H / 8 steps of 2^-24
-// of the variance, and a few for rows without such an outlier in front.
+// eight (four) elements. Where outliers among these have moved k by more than two
+// deviations, the round is gone once more about the mean that it gave, so whatever the
+// row holds, at most a factor of five is lost of the squares' precision.
 //
 // Memory bounds the short form (13500 x 7168, y fp32: forward 165 us, gradient 270,
 // with floors of 142 and 228; y bf16 125 and 214). Two barriers a row, the sums of
 // gate and weight apart and one element an instruction (now two, fma.f32x2) took
 // 181 and 511. The general form, whose parameters come from the first level cache
-// for each row, is bound by instructions: layer norms with biases 330 and 624, a
-// gate of every element 253 and 630. It keeps fewer rows on their way (3 and 2), as
-// shared memory is taken from that cache: with 4 and 3 it took 390 and 624 (y bf16:
-// 332 and 659, now 314 and 529).
+// for each row, is bound by instructions: layer norms with biases 336 and 662, a
+// gate of every element 256 and 660 (324 and 624, 252 and 627 without the second look
+// at k, whose loop is written once: a round of its own for y took 806). It keeps fewer
+// rows on their way (3 and 2), as shared memory is taken from that cache.
 
 #include "pgg_block.h"
 #include "pgg_block_sum.cuh"
@@ -183,6 +183,12 @@ __device__ __forceinline__ Stat stat_of(int kind, float k, float sum, float squa
   return s;
 }
 
+// k lies so far from the mean that the variance has lost bits: the sums are of v - k and (v - k)^2.
+__device__ __forceinline__ bool too_far(float sum, float squares, float inv_h) {
+  const float from_k = sum * inv_h;
+  return from_k * from_k > 4.0f * fmaf(-from_k, from_k, squares * inv_h);
+}
+
 // The copies of all rows but the `behind` last ones have landed, for the warp.
 __device__ __forceinline__ void wait_rows(int behind) {
   if (behind >= 3)
@@ -275,9 +281,12 @@ __global__ void __launch_bounds__(THREADS, 1) block_norm_rows_kernel(const NormA
     sums[1] = added(squares);
   };
   wait_rows(ring - 1);
-  if (post) {
+#pragma unroll 1
+  for (bool again = false; post; again = true) {
     first_pass(0, k);
     block_sum(&s, &turn, sums);
+    if (!GEN || again || !post_mean || !too_far(sums[0], sums[1], inv_h)) break;
+    k = fmaf(sums[0], inv_h, k);
   }
   uint32_t slot = 0;
   for (; t < a.T; t += gridDim.x, e += step) {
@@ -326,8 +335,16 @@ __global__ void __launch_bounds__(THREADS, 1) block_norm_rows_kernel(const NormA
     sums[3] = added(squares);
     fetch_row(slot, t + ring * gridDim.x);
     wait_rows(ring - 1);
-    if (post && t + gridDim.x < a.T) first_pass(next, k_next);
-    if (post || pre) block_sum(&s, &turn, sums);
+    const bool more = post && t + gridDim.x < a.T;
+#pragma unroll 1
+    for (bool again = false;; again = true) {
+      if (more) first_pass(next, k_next);
+      if (post || pre) block_sum(&s, &turn, sums);
+      // (the same bits in every thread, so all of them go again or none)
+      if (!GEN || again || !post_mean || !more || !too_far(sums[0], sums[1], inv_h)) break;
+      k_next = fmaf(sums[0], inv_h, k_next);
+      if (tid != 0) sums[2] = sums[3] = 0.0f;  // (r's are there already, once)
+    }
     if (pre) {
       float mean = 0.0f, var = sums[3] * inv_h;
       if (pre_mean) {
@@ -440,8 +457,10 @@ __global__ void __launch_bounds__(THREADS, THREADS > 256 ? 1 : 2)
     load_p(j, q);
     load_f(j, q);
   }
-  // of the next row r^2 (of r - k), d_h f r; r - k, d_h f; of the row y^2 (of y - k), g p y; y - k, g p
-  constexpr int kY = GEN ? 4 : 2;
+  // of the next row r^2, d_h f r; of the row y^2, g p y. GEN: of the next row (r - k)^2, d_h f (r - k),
+  // r - k, d_h f, (y - k)^2, y - k; of the row g p (y - mean), g p
+  constexpr int kYY = GEN ? 4 : 2, kY1 = GEN ? 5 : 0, kWY = GEN ? 6 : 3, kW1 = GEN ? 7 : 0;
+  constexpr int kR1 = GEN ? 2 : 0, kU1 = GEN ? 3 : 0;
   float sums[kSums] = {};
   // of row t: r's k, y's k, and its token's gate
   struct Scalars {
@@ -454,51 +473,81 @@ __global__ void __launch_bounds__(THREADS, THREADS > 256 ? 1 : 2)
                    post_mean ? first_mean<DT, V>(a.y, y32, t * a.H) : 0.0f, one[0]};
   };
   Scalars now = scalars(t), later = {0.0f, 0.0f, 1.0f};
-  // the former of the row in `slot`
-  auto first_pass = [&](uint32_t slot, float k) {
+  // those of the next row, in `slot`
+  auto first_pass = [&](uint32_t slot, const Scalars& of) {
     F2 rr = both(0.0f), ur = both(0.0f), r1 = both(0.0f), u1 = both(0.0f);
+    F2 yy = both(0.0f), y1 = both(0.0f);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const uint32_t q = j * blockDim.x + tid;
       if (static_cast<int>(q) >= n) continue;
-      F2 r[P], dh[P];
-      read<DT, V>(base + slot, q, false, r);
-      read<DT, V>(base + slot + h_at, q, h32, dh);
-      if constexpr (GEN) load_f(j, q);
+      if (pre) {
+        F2 r[P], dh[P];
+        read<DT, V>(base + slot, q, false, r);
+        read<DT, V>(base + slot + h_at, q, h32, dh);
+        if constexpr (GEN) load_f(j, q);
 #pragma unroll
-      for (int c = 0; c < P; ++c) {
-        const F2 u = mul2(dh[c], f[j][c]);
-        if constexpr (GEN) {
-          r[c] = add2(r[c], both(-k));
-          r1 = add2(r1, r[c]);
-          u1 = add2(u1, u);
+        for (int c = 0; c < P; ++c) {
+          const F2 u = mul2(dh[c], f[j][c]);
+          if constexpr (GEN) {
+            r[c] = add2(r[c], both(-of.r));
+            r1 = add2(r1, r[c]);
+            u1 = add2(u1, u);
+          }
+          rr = fma2(r[c], r[c], rr);
+          ur = fma2(u, r[c], ur);
         }
-        rr = fma2(r[c], r[c], rr);
-        ur = fma2(u, r[c], ur);
+      }
+      if (GEN && post) {
+        F2 y[P];
+        read<DT, V>(base + slot + y_at, q, y32, y);
+#pragma unroll
+        for (int c = 0; c < P; ++c) {
+          y[c] = add2(y[c], both(-of.y));
+          y1 = add2(y1, y[c]);
+          yy = fma2(y[c], y[c], yy);
+        }
       }
     }
     sums[0] = added(rr);
     sums[1] = added(ur);
     if constexpr (GEN) {
-      sums[2] = added(r1);
-      sums[3] = added(u1);
+      sums[kR1] = added(r1);
+      sums[kU1] = added(u1);
+      sums[kYY] = added(yy);
+      sums[kY1] = added(y1);
+    }
+  };
+  // The block's sums, with the next row's (in `slot`, where there is one) gone over once more about
+  // the means where k was too far from one of them: the same bits in every thread, so all go or none.
+  auto sum_up = [&](uint32_t slot, bool there, Scalars& of) {
+#pragma unroll 1
+    for (bool again = false;; again = true) {
+      if (there) first_pass(slot, of);
+      block_sum(&s, &turn, sums);
+      if (!GEN || again || !there) break;
+      const bool far_r = pre_mean && too_far(sums[kR1], sums[0], inv_h);
+      const bool far_y = post_mean && too_far(sums[kY1], sums[kYY], inv_h);
+      if (!far_r && !far_y) break;
+      if (far_r) of.r = fmaf(sums[kR1], inv_h, of.r);
+      if (far_y) of.y = fmaf(sums[kY1], inv_h, of.y);
+      if (tid != 0) sums[kWY] = sums[kW1] = 0.0f;  // (the row's are there already, once)
     }
   };
   wait_rows(ring - 1);
-  if (pre) {
-    first_pass(0, now.r);
-    block_sum(&s, &turn, sums);
-  }
+  if (pre || (GEN && post)) sum_up(0, true, now);
   uint32_t slot = 0;
   for (; t < a.T; t += gridDim.x, e += step) {
-    const Stat of_r = stat_of(a.pre, now.r, GEN ? sums[2] : 0.0f, sums[0], inv_h, a.eps);
-    const float u_r = GEN ? sums[3] : 0.0f, uv = fmaf(-of_r.from_k, u_r, sums[1]);
+    const Stat of_r = stat_of(a.pre, now.r, GEN ? sums[kR1] : 0.0f, sums[0], inv_h, a.eps);
+    Stat of_y = {};
+    if constexpr (GEN) of_y = stat_of(a.post, now.y, sums[kY1], sums[kYY], inv_h, a.eps);
+    const float u_r = GEN ? sums[kU1] : 0.0f, uv = fmaf(-of_r.from_k, u_r, sums[1]);
     const F2 rstd_r = both(of_r.rstd), mean_r = both(-of_r.mean),
              along_r = both(-(uv * of_r.rstd * inv_h) * of_r.rstd),
              centre_r = both(pre_mean ? -u_r * inv_h * of_r.rstd : 0.0f);
     const uint32_t next = slot + slot_bytes == ring * slot_bytes ? 0 : slot + slot_bytes;
     if (GEN && t + gridDim.x < a.T) later = scalars(t + gridDim.x);
-    F2 g[NV][P], yy = both(0.0f), wy = both(0.0f), y1 = both(0.0f), w1 = both(0.0f), gb = both(0.0f);
+    F2 g[NV][P], yy = both(0.0f), wy = both(0.0f), w1 = both(0.0f), gb = both(0.0f);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const uint32_t q = j * blockDim.x + tid;
@@ -550,27 +599,23 @@ __global__ void __launch_bounds__(THREADS, THREADS > 256 ? 1 : 2)
         for (int c = 0; c < P; ++c) {
           const F2 w = mul2(g[j][c], p[j][c]);
           if constexpr (GEN) {
-            y[c] = add2(y[c], both(-now.y));
-            y1 = add2(y1, y[c]);
+            y[c] = add2(y[c], both(-of_y.mean));
             w1 = add2(w1, w);
+          } else {
+            yy = fma2(y[c], y[c], yy);
           }
-          yy = fma2(y[c], y[c], yy);
           wy = fma2(w, y[c], wy);
         }
       }
     }
-    sums[kY] = added(yy);
-    sums[kY + 1] = added(wy);
-    if constexpr (GEN) {
-      sums[6] = added(y1);
-      sums[7] = added(w1);
-    }
+    if constexpr (!GEN) sums[kYY] = added(yy);
+    sums[kWY] = added(wy);
+    if constexpr (GEN) sums[kW1] = added(w1);
     wait_rows(ring - 2);
-    if (pre && t + gridDim.x < a.T) first_pass(next, later.r);
-    if (post || pre || token) block_sum(&s, &turn, sums);
+    if (post || pre || token) sum_up(next, (pre || GEN) && t + gridDim.x < a.T, later);
     if (have_y) {
-      const Stat of_y = stat_of(a.post, now.y, GEN ? sums[kSums - 2] : 0.0f, sums[kY], inv_h, a.eps);
-      const float w_sum = GEN ? sums[kSums - 1] : 0.0f, wv = fmaf(-of_y.from_k, w_sum, sums[kY + 1]);
+      if constexpr (!GEN) of_y = stat_of(a.post, 0.0f, 0.0f, sums[kYY], inv_h, a.eps);
+      const float w_sum = GEN ? sums[kW1] : 0.0f, wv = sums[kWY];
       if (token) {
         float b[1] = {added(gb)};
         if (a.b_post) block_sum(&s, &turn, b);
