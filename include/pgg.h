@@ -682,14 +682,20 @@ int pgg_adapters_grad(const void* d_y, const void* x, const void* weight, const 
  *   workspace at least pgg_w4_workspace_size bytes, 256-byte aligned; status word
  *            at offset 0. When the routing is not valid the output is zero-filled.
  *
- * Sums are fp32, each output is rounded once, and the weights are not rounded to
- * 16 bits: few rows an expert multiply x with the codes and then a group's fp32 sum
- * with its scale; many rows multiply with the weight as one fp16 number where that
- * is exact (bf16 scales, no zeros) and as the sum of two (22 bits) otherwise; fp32
- * x, and K or groupSize that is no multiple of 32, form each weight in fp32. x, a row
- * at a time, and the weights, a column at a time, are brought to fp16's range by a
- * power of two: a 16-bit x keeps its bits but for what lies below 2^-35 of its row's
- * largest finite value, a weight likewise in its column. Bitwise repeatable.
+ * Sums are fp32, and each output is rounded once. The weights are not rounded to
+ * 16 bits. Few rows an expert multiply x with the codes and then a group's fp32 sum
+ * with its scale. fp32 x, and K or groupSize that is no multiple of 32, form each
+ * weight in fp32. Many rows an expert multiply with the weight as one fp16 number
+ * where that is exact (bf16 scales, no zeros) and as the sum of two (22 bits)
+ * otherwise, and bring the weights of a column to fp16's range by a power of two: a
+ * weight there is off by up to (|code - zero| + 1) 2^-35 of its column's largest
+ * scale (with zeros above 16 up to 2^-31). In all of them a 16-bit x is brought to
+ * fp16's range a row at a time and keeps its bits but for what lies below 2^-35 of
+ * the row's largest value. Bitwise repeatable.
+ *
+ * A row of x with infinities or NaN gives what the sums of its weights times these
+ * give, +-inf or NaN. A scale that is not finite leaves no result of its
+ * column finite, whether +-inf or NaN.
  */
 typedef enum { PGG_W4_ROWS = 0, PGG_W4_GATED = 1, PGG_W4_COMBINED = 2 } pgg_w4_product;
 

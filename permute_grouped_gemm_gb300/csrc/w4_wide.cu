@@ -13,10 +13,11 @@
 // 128-byte swizzle, pairs k + j, k + 4 + j as in a word of codes) by a launch
 // before this one, so that it arrives in plain pieces.
 //
-// The weight is not rounded. Brought to fp16 by a power of two a column (found by
-// the launch before), a bf16 scale has eight bits and code - 8 at most three, so
-// the product is an fp16 number. With zeros or other scales it is the sum of two
-// (hi and what is left), and the MMAs run twice. Scaling each group's fp32 sums
+// Brought to fp16 by a power of two a column (found by the launch before), a bf16
+// scale has eight bits and code - 8 at most three, so the product is an fp16 number
+// and the weight is not rounded. With zeros or other scales it is the sum of two (hi
+// and what is left, 22 bits), and the MMAs run twice. Either way bits are lost that lie
+// below 2^-35 of the column's largest scale. Scaling each group's fp32 sums
 // instead costs more: tensor memory is read at about 20 bytes a cycle and
 // quarter, so bringing back 128 x 144 sums took 880 cycles, the products of a
 // group of 128 are 580 (2048 tokens, 60 experts, K 7168, F 2048: 1432 us, now 818;
@@ -139,8 +140,9 @@ __device__ __forceinline__ int exponent_of(float most) {
 
 // The first `row_blocks` blocks: a row of a row block, its power of two and its values as the MMA
 // reads them, 128 threads a row. The others: the columns' powers of two, eight lanes a column of an
-// expert with rows: its largest scale comes to lie in [2^8, 2^9), and lower by the bits that a zero
-// above 16 has over four, so that scale (code - zero) stays below 2^13.
+// expert with rows: its largest scale comes to lie in [2^10, 2^11), and lower by the bits that a zero
+// above 16 has over four, so that scale (code - zero) stays at 2^15 or below, in fp16's range, whose
+// smallest step is then 2^-34 of that scale or less (with zeros near 255 2^-30).
 template <int DT>
 __global__ void __launch_bounds__(128)
     w4_pack_wide_kernel(const W4Args a, const int64_t* group_list, const int row_blocks) {
@@ -193,7 +195,7 @@ __global__ void __launch_bounds__(128)
         zero = max(zero, __shfl_xor_sync(0xFFFFFFFFu, zero, d));
       }
       if (live && lane == 0)
-        a.col_exponent[c] = exponent_of(most) - 9 + (32 - __clz(static_cast<int>(zero - 1)) - 4);
+        a.col_exponent[c] = exponent_of(most) - 11 + (32 - __clz(static_cast<int>(zero - 1)) - 4);
     }
     return;
   }
