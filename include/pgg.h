@@ -797,8 +797,9 @@ int pgg_block_norm_grad(const void* d_r, const void* d_h, const void* r, const v
  *   scale    multiplies every gradient (1 / the loss scale, 1 / accumulated steps)
  *   max_norm 0 or more (may be infinite); eps 0 or more
  *   norm     device, fp32
- *   out      host array of device pointers; out[i] has the dtype of grads[i], is
- *            grads[i] itself or overlaps no gradient
+ *   out      host array of device pointers; out[i] has the dtype of grads[i]. It is
+ *            grads[i] itself or overlaps no gradient, and overlaps no other output
+ *            (one tensor twice in the list, say): else PGG_ERR_ATTR
  *   workspace at least pgg_clip_workspace_size bytes, 256-byte aligned; the status
  *            word at offset 0 is 0 after the call
  *

@@ -712,7 +712,8 @@ def clip_grads(grads, max_norm: float, eps: float = 1e-6, scale: float = 1.0, ou
     """Clips gradients by their global norm: (norm, out, workspace).
 
     norm = |scale| sqrt(sum of all squares); out[i] = grads[i] scale min(1, max_norm / (norm +
-    eps)), in place when ``out`` (a list of like tensors) is None. A norm that is not finite clips
+    eps)), in place when ``out`` (a list of like tensors) is None. No output may overlap another, or
+    another's gradient: a tensor that is shared is listed once. A norm that is not finite clips
     nothing (out = grads scale): look at it before the step.
     """
     out = grads if out is None else out

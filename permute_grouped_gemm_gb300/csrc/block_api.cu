@@ -2,8 +2,10 @@
 // (include/pgg.h): argument validation, workspace layouts, the choice of kernel
 // and the launches.
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <cstdlib>
 #include <cstring>
 #include <initializer_list>
 
@@ -209,6 +211,38 @@ int check_clip(int64_t count, const void* const* grads, const int64_t* sizes,
   return PGG_OK;
 }
 
+// No output may reach into another output, or into a gradient but its own (blocks of one read what
+// those of the other write): the ranges in the order of their addresses.
+int check_clip_ranges(int64_t count, const void* const* grads, const int64_t* sizes,
+                      const pgg_dtype* dtypes, void* const* out) {
+  struct Range {
+    uintptr_t begin, end;
+    bool written;
+  };
+  if (count == 0) return PGG_OK;
+  Range* ranges = static_cast<Range*>(std::malloc(sizeof(Range) * 2 * static_cast<size_t>(count)));
+  if (!ranges) return PGG_ERR_CUDA;
+  int64_t n = 0;
+  for (int64_t i = 0; i < count; ++i) {
+    const uintptr_t bytes = static_cast<uintptr_t>(sizes[i]) * elem_size(dtypes[i]);
+    if (bytes == 0) continue;
+    const uintptr_t to = reinterpret_cast<uintptr_t>(out[i]);
+    const uintptr_t from = reinterpret_cast<uintptr_t>(grads[i]);
+    ranges[n++] = {to, to + bytes, true};
+    if (from != to) ranges[n++] = {from, from + bytes, false};
+  }
+  std::sort(ranges, ranges + n, [](const Range& a, const Range& b) { return a.begin < b.begin; });
+  uintptr_t written = 0, read = 0;  // ends of those before
+  bool ok = true;
+  for (int64_t i = 0; ok && i < n; ++i) {
+    ok = ranges[i].begin >= written && !(ranges[i].written && ranges[i].begin < read);
+    uintptr_t& end = ranges[i].written ? written : read;
+    end = std::max(end, ranges[i].end);
+  }
+  std::free(ranges);
+  return ok ? PGG_OK : PGG_ERR_ATTR;
+}
+
 // The tensors of one launch; returns its blocks.
 int fill_table(ClipTable* t, int64_t begin, int64_t count, const void* const* grads,
                const int64_t* sizes, const pgg_dtype* dtypes, void* const* out, int num_sms) {
@@ -242,6 +276,10 @@ int run_clip(int64_t count, const void* const* grads, const int64_t* sizes,
   if (rc != PGG_OK) return rc;
   if (!aligned(workspace, 256) || !aligned(norm, 4)) return PGG_ERR_ALIGN;
   if (workspace_bytes < p.total) return PGG_ERR_WORKSPACE;
+  if (clip) {
+    rc = check_clip_ranges(count, grads, sizes, dtypes, out);
+    if (rc != PGG_OK) return rc;
+  }
   HostEnv env;
   if (host_env(&env) != PGG_OK) return PGG_ERR_CUDA;
   WsHeader* hdr = static_cast<WsHeader*>(workspace);
