@@ -28,7 +28,7 @@ int status_of(cudaError_t e) { return e == cudaSuccess ? PGG_OK : PGG_ERR_CUDA; 
 // ---------------------------------------------------------------- 4-bit experts
 
 constexpr int kSimtRows = 32;
-constexpr int kVariantWide = 0;    // tensor cores, row blocks of up to 256 rows
+constexpr int kVariantWide = 0;    // tensor cores, row blocks of up to 160 rows (two-part weights: 128)
 constexpr int kVariantStream = 1;  // tensor cores, the codes streamed for blocks of 8 to 32 rows
 constexpr int kVariantSimt = 3;    // FP32 pipes: any dtype, size and alignment
 

@@ -833,9 +833,8 @@ cudaError_t launch_block_norm(int dtype, const NormArgs& a, int words, int num_s
                               cudaStream_t stream) {
   cudaError_t err;
   if (launch_block_norm_rows(dtype, a, words, num_sms, stream, &err)) return err;
-  if (dtype == PGG_F32)
-    return words == 16 ? launch_forward<PGG_F32, 4>(a, num_sms, stream)
-                       : launch_forward<PGG_F32, 1>(a, num_sms, stream);
+  // (fp32 rows of 16-byte vectors come here with more than 8192 elements only: they are read one by one)
+  if (dtype == PGG_F32) return launch_forward<PGG_F32, 1>(a, num_sms, stream);
   if (dtype == PGG_F16)
     return words == 16  ? launch_forward<PGG_F16, 8>(a, num_sms, stream)
            : words == 4 ? launch_forward<PGG_F16, 2>(a, num_sms, stream)
