@@ -1,9 +1,10 @@
-// What the kernels that lay out rows of x for the 4-bit products share.
+// What the tensor-core kernels of the 4-bit products share: how rows of x are laid out and fetched.
 #pragma once
 
 #include <cstdint>
 
 #include "pgg_block.h"
+#include "pgg_ptx.cuh"
 #include "pgg_vec.cuh"
 
 namespace pgg {
@@ -73,6 +74,16 @@ __device__ __noinline__ void write_infinite_row(const W4Args& a, const uint16_t*
       vec::store1<DT>(a.out, out + c, v);
   }
   __syncthreads();  // (s_at and s_count are the next such row's)
+}
+
+// `bytes` (a multiple of 16) from global to shared memory, both 16-byte aligned.
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes,
+                                          uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          ptx::smem_addr(dst)),
+      "l"(src), "r"(bytes), "r"(ptx::smem_addr(bar))
+      : "memory");
 }
 
 }  // namespace pgg

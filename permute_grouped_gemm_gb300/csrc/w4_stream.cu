@@ -211,16 +211,6 @@ __global__ void __launch_bounds__(128) w4_pack_kernel(const W4Args a) {
 
 // ------------------------------------------------------------------ the copying warp
 
-// `bytes` (a multiple of 16) from global to shared memory, both 16-byte aligned.
-__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes,
-                                          uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-          ptx::smem_addr(dst)),
-      "l"(src), "r"(bytes), "r"(ptx::smem_addr(bar))
-      : "memory");
-}
-
 // B bytes (4, 8, 16 or 32) from memory into words, and from words to shared memory.
 template <int B>
 __device__ __forceinline__ void load_bytes(const void* p, uint32_t* w) {

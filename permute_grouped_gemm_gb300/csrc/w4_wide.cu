@@ -256,15 +256,6 @@ __global__ void __launch_bounds__(128)
 
 // ------------------------------------------------------------------ copies
 
-__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes,
-                                          uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-          ptx::smem_addr(dst)),
-      "l"(src), "r"(bytes), "r"(ptx::smem_addr(bar))
-      : "memory");
-}
-
 struct Walk {
   uint32_t first, step, total;
   int groups;  // of 128 of k
@@ -539,6 +530,9 @@ __device__ void unpacker(uint8_t* smem, Ctl* ctl, uint32_t tmem, int par, const 
   const int row = code_row(a.product == PGG_W4_GATED, l);
   const uint32_t codes = ptx::smem_addr(smem) + row * 128;
   const uint32_t a_lanes = tmem + (static_cast<uint32_t>(32 * quarter) << 16) + C::kACols;
+  // A code becomes a half as the low bits of 2^10, or 16 times as high, which are ones there (a published
+  // way: Kim et al., "Who Says Elephants Can't Run: Bringing Large Scale MoE Models into Cloud Scale
+  // Production", 2022).
   uint32_t magic;  // the pair 2^10, from a register: an instruction holds one of two constants only
   asm volatile("mov.u32 %0, 0x64006400;" : "=r"(magic));
   int slot = 0;  // of codes: two groups of a tile
