@@ -34,6 +34,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <atomic>
 #include <cstdint>
 #include <cstring>
 
@@ -792,8 +793,18 @@ template <int U, bool SPLIT>
 cudaError_t launch_t(const CUtensorMap& tm, const W4Args& a, int num_sms, cudaStream_t stream) {
   auto kern = w4_wide_kernel<U, SPLIT>;
   static SmemLimit limit;
-  const cudaError_t err = allow_smem(&limit, kern, kSmem);
+  cudaError_t err = allow_smem(&limit, kern, kSmem);
   if (err != cudaSuccess) return err;
+  // The warpgroups' shares are those of kLaunchRegs a thread: with fewer (flags that ask the compiler for
+  // it) the writers would wait for theirs without end.
+  static std::atomic<bool> enough{false};
+  if (!enough.load()) {
+    cudaFuncAttributes attr;
+    err = cudaFuncGetAttributes(&attr, kern);
+    if (err != cudaSuccess) return err;
+    if (attr.numRegs < kLaunchRegs) return cudaErrorInvalidConfiguration;
+    enough.store(true);
+  }
   return launch_pdl(kern, dim3(static_cast<unsigned>(num_sms)), dim3(kThreads),
                     static_cast<size_t>(kSmem), stream, 1, tm, a);
 }
