@@ -35,7 +35,10 @@ constexpr int kVariantSimt = 3;    // FP32 pipes: any dtype, size and alignment
 // Up to this many rows per live expert the codes are streamed: 64 experts, K 7168, F 2048, gated, us
 // streamed / wide: 16 rows 375 / 414, 24 rows 409 / 418, 32 rows 568 / 423; with zero points 386 / 555,
 // 422 / 561 and 582 / 572; groups of 32 537 / 593, 570 / 598, 794 / 604. (The wide form reads and
-// unpacks a weight once whatever the rows are; streamed blocks have at most 32 rows.)
+// unpacks a weight once whatever the rows are; streamed blocks have at most 32 rows.) The rows are those
+// of an even routing, as the host knows no other; an uneven one pays for it, since an expert's codes are
+// streamed once for each of its blocks: 60 tokens on the same 8 of 256 experts 202 us, wide 120 (on 209
+// experts 609 and 1265), 256 tokens 433, wide 185 (on 256 experts 894 and 1544).
 constexpr double kStreamRows = 24.0;
 
 struct W4Plan {

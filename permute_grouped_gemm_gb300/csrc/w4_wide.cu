@@ -20,8 +20,8 @@
 // below 2^-35 of the column's largest scale. Scaling each group's fp32 sums
 // instead costs more: tensor memory is read at about 20 bytes a cycle and
 // quarter, so bringing back 128 x 144 sums took 880 cycles, the products of a
-// group of 128 are 580 (2048 tokens, 60 experts, K 7168, F 2048: 1432 us, now 818;
-// with zeros 1610).
+// group of 128 are 580 (2048 tokens, 60 experts, K 7168, F 2048: 1432 us, now 825
+// to 875; with zeros 1660).
 //
 // Tensor memory: two accumulators and three A buffers (128 of k: 64 columns; split
 // two of 128). Roles: one warp copies, one issues the MMAs; eight unpack (four lane
