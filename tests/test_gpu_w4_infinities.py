@@ -84,9 +84,10 @@ def test_fp16(form):  # noqa: F811
     check(dict(s, x=x), clean)
 
 
+@pytest.mark.parametrize("zeros,scales", [(True, "bf16"), (False, "bf16"), (False, "fp32")])
 @pytest.mark.parametrize("product", PRODUCTS)
-def test_a_scale_that_is_not_finite_stays_with_its_column(form, product):  # noqa: F811
-    s = case(product, T=20, G=3, K=256, N=48, group=64, zeros=True)
+def test_a_scale_that_is_not_finite_stays_with_its_column(form, product, zeros, scales):  # noqa: F811
+    s = case(product, T=20, G=3, K=256, N=48, group=64, zeros=zeros, scales=scales)
     clean = call(s)[0]
     bad = s["scales"].clone()
     bad[1, 7, 2], bad[1, 20, 0] = INF, NAN
@@ -100,10 +101,12 @@ def test_a_scale_that_is_not_finite_stays_with_its_column(form, product):  # noq
     assert torch.equal(got[keep], clean[keep]) and not bool(torch.isfinite(got[~keep]).any())
 
 
-@pytest.mark.parametrize("name", ["idx", "groups"])
+@pytest.mark.parametrize("name,zeros,out", [("idx", True, None), ("groups", False, None),
+                                            ("idx", False, "fp32")])
 @pytest.mark.parametrize("product", PRODUCTS)
-def test_bad_routing_gives_zeros_in_every_form(form, product, name):  # noqa: F811
-    s = case(product, T=30, G=3, K=256, N=72, group=128)
+def test_bad_routing_gives_zeros_in_every_form(form, product, name, zeros, out):  # noqa: F811
+    out = None if product == "gated" else out
+    s = case(product, T=30, G=3, K=256, N=72, group=128, zeros=zeros, out=out)
     clean, _ = call(s)
     s[name] = s[name].clone()
     s[name][0] = s[name][1] if name == "idx" else s[name][0] + 1
