@@ -21,7 +21,14 @@
 // instead costs more: tensor memory is read at about 20 bytes a cycle and
 // quarter, so bringing back 128 x 144 sums took 880 cycles, the products of a
 // group of 128 are 580 (2048 tokens, 60 experts, K 7168, F 2048: 1432 us, now 825
-// to 875; with zeros 1660).
+// to 875; with zeros 1605).
+//
+// An accumulator cuts off at every step what falls out of its 24 bits, which adds up
+// over a long k (K 7168: 7.3e-6 of the results' size, with two-part weights 1.7e-5; fp32
+// products, rounded, 1.0e-6 and 1.5e-6). The rounding of 16-bit results hides it. For fp32
+// results an accumulator adds up eight groups (two-part weights: three), and the writing
+// warps add these sums: 0.9e-6 (2048 tokens' down projection, K 2048, N 7168: 685 us, 655 with
+// one sum; four groups 740).
 //
 // Tensor memory: two accumulators and three A buffers (128 of k: 64 columns; split
 // two of 128). Roles: one warp copies, one issues the MMAs; eight unpack (four lane
@@ -62,6 +69,7 @@ struct Cfg {
   static constexpr int kACols = 2 * kRows;
   static constexpr int kABuf = SPLIT ? 128 : 64;
   static constexpr int kBufs = SPLIT ? 2 : 3;
+  static constexpr int kChain = SPLIT ? 3 : 8;  // groups that an accumulator adds up for fp32 results
   static_assert(kACols + kBufs * kABuf <= 512 && kBufs < kStages, "tensor memory");
 };
 // Warpgroups: copies and MMAs; two that unpack; two that write. Registers a thread of each, which
@@ -260,6 +268,7 @@ __global__ void __launch_bounds__(128)
 struct Walk {
   uint32_t first, step, total;
   int groups;  // of 128 of k
+  int chain;   // of them, that an accumulator adds up
 };
 
 // One thread.
@@ -373,44 +382,47 @@ __device__ void issuer(uint8_t* smem, Ctl* ctl, uint32_t tmem, const W4Args& a, 
     const Tile x = tile_of(t, a);
     const uint32_t panel = static_cast<uint32_t>(x.rows16) * 128;
     const uint32_t idesc = ptx::idesc_make(0, kTile, x.rows16);
-    const uint32_t d = tmem + C::kRows * acc;
-    if (!__all_sync(0xFFFFFFFFu, ptx::mbar_wait(&ctl->dempty[acc], dphase ^ 1u, a.wait_limit_ns,
-                                                abort))) {
-      failed = true;
-      break;
-    }
-    for (int g = 0; g < k.groups; ++g) {
-      if (!__all_sync(0xFFFFFFFFu, ptx::mbar_wait(&ctl->full[stage], phase, a.wait_limit_ns,
+    for (int g0 = 0; g0 < k.groups && !failed; g0 += k.chain) {
+      const uint32_t d = tmem + C::kRows * acc;
+      if (!__all_sync(0xFFFFFFFFu, ptx::mbar_wait(&ctl->dempty[acc], dphase ^ 1u, a.wait_limit_ns,
                                                   abort))) {
         failed = true;
         break;
       }
-      ptx::tc_fence_after_sync();
-      const uint32_t xb = ptx::smem_addr(xs + stage * kStageBytes);
-      const uint32_t ab = tmem + C::kACols + C::kABuf * buf;
-      const uint64_t desc0 = ptx::sdesc_sw128(xb), desc1 = ptx::sdesc_sw128(xb + panel);
-      if (elected()) {
-#pragma unroll
-        for (int s = 0; s < kGroup / 16; ++s) {  // of 16 k: 32 bytes of a panel's rows
-          const uint64_t desc = (s < 4 ? desc0 : desc1) + 2 * (s & 3);
-          mma_tmem(d, ab + 8 * s, desc, idesc, (g | s) > 0 ? 1u : 0u);
-          if (SPLIT) mma_tmem(d, ab + 64 + 8 * s, desc, idesc, 1u);
+      const int end = g0 + k.chain < k.groups ? g0 + k.chain : k.groups;
+      for (int g = g0; g < end; ++g) {
+        if (!__all_sync(0xFFFFFFFFu, ptx::mbar_wait(&ctl->full[stage], phase, a.wait_limit_ns,
+                                                    abort))) {
+          failed = true;
+          break;
         }
-        ptx::mma_commit(&ctl->done[stage]);
+        ptx::tc_fence_after_sync();
+        const uint32_t xb = ptx::smem_addr(xs + stage * kStageBytes);
+        const uint32_t ab = tmem + C::kACols + C::kABuf * buf;
+        const uint64_t desc0 = ptx::sdesc_sw128(xb), desc1 = ptx::sdesc_sw128(xb + panel);
+        if (elected()) {
+#pragma unroll
+          for (int s = 0; s < kGroup / 16; ++s) {  // of 16 k: 32 bytes of a panel's rows
+            const uint64_t desc = (s < 4 ? desc0 : desc1) + 2 * (s & 3);
+            mma_tmem(d, ab + 8 * s, desc, idesc, ((g - g0) | s) > 0 ? 1u : 0u);
+            if (SPLIT) mma_tmem(d, ab + 64 + 8 * s, desc, idesc, 1u);
+          }
+          ptx::mma_commit(&ctl->done[stage]);
+        }
+        __syncwarp();
+        issued = true;
+        if (++stage == kStages) {
+          stage = 0;
+          phase ^= 1u;
+        }
+        buf = buf + 1 == C::kBufs ? 0 : buf + 1;
       }
+      if (failed) break;
+      if (elected()) ptx::mma_commit(&ctl->dfull[acc]);
       __syncwarp();
-      issued = true;
-      if (++stage == kStages) {
-        stage = 0;
-        phase ^= 1u;
-      }
-      buf = buf + 1 == C::kBufs ? 0 : buf + 1;
+      acc ^= 1;
+      if (acc == 0) dphase ^= 1u;
     }
-    if (failed) break;
-    if (elected()) ptx::mma_commit(&ctl->dfull[acc]);
-    __syncwarp();
-    acc ^= 1;
-    if (acc == 0) dphase ^= 1u;
   }
   if (failed) {
     ctl->abort = 1;
@@ -640,7 +652,7 @@ __device__ void unpacker(uint8_t* smem, Ctl* ctl, uint32_t tmem, int par, const 
   }
 }
 
-// Results of the thread's column: 16-row chunks half, half + 2, ... of the tile's rows.
+// 16-bit results of the thread's column: 16-row chunks half, half + 2, ... of the tile's rows.
 template <bool SPLIT>
 __device__ void writer(Ctl* ctl, uint32_t tmem, int half, const W4Args& a, const Walk& k) {
   using C = Cfg<SPLIT>;
@@ -698,12 +710,72 @@ __device__ void writer(Ctl* ctl, uint32_t tmem, int half, const W4Args& a, const
         const int row = __shfl_sync(0xFFFFFFFFu, m[c].x, i);
         const int64_t to = static_cast<int64_t>(row) * a.N + f;
         if (!writes || row < 0) continue;
-        if (a.out_f32)
-          static_cast<float*>(a.out)[to] = v;
-        else if (a.bf16)
+        if (a.bf16)
           static_cast<__nv_bfloat16*>(a.out)[to] = __float2bfloat16_rn(v);
         else
           static_cast<__half*>(a.out)[to] = __float2half_rn(v);
+      }
+    }
+  }
+}
+
+// fp32 results (not gated) of the same: an accumulator's sums are added to those before.
+template <bool SPLIT>
+__device__ void writer_f32(Ctl* ctl, uint32_t tmem, int half, const W4Args& a, const Walk& k) {
+  using C = Cfg<SPLIT>;
+  volatile int* abort = &ctl->abort;
+  const int lane = threadIdx.x & 31, quarter = (threadIdx.x >> 5) & 3, l = 32 * quarter + lane;
+  const uint32_t d_tmem = tmem + (static_cast<uint32_t>(32 * quarter) << 16) + 16 * half;
+  int acc = 0;
+  uint32_t dphase = 0;
+  for (uint32_t t = k.first; t < k.total; t += k.step) {
+    const Tile x = tile_of(t, a);
+    float sum[C::kChunks][16];
+#pragma unroll
+    for (int c = 0; c < C::kChunks; ++c)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) sum[c][i] = 0.0f;
+#pragma unroll 1
+    for (int g = 0; g < k.groups; g += k.chain) {
+      if (!__all_sync(0xFFFFFFFFu,
+                      ptx::mbar_wait(&ctl->dfull[acc], dphase, a.wait_limit_ns, abort))) {
+        if (lane == 0) {
+          ctl->abort = 1;
+          raise_status(a.hdr, kStTimeout, 192);
+        }
+        return;
+      }
+      ptx::tc_fence_after_sync();
+#pragma unroll
+      for (int c = 0; c < C::kChunks; ++c) {
+        if (32 * c + 16 * half >= x.rows16) continue;
+        uint32_t part[16];
+        ptx::tmem_ld_32x32b_x16(d_tmem + C::kRows * acc + 32 * c, part);
+        ptx::tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < 16; ++i) sum[c][i] += __uint_as_float(part[i]);
+      }
+      ptx::tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(&ctl->dempty[acc]);
+      acc ^= 1;
+      if (acc == 0) dphase ^= 1u;
+    }
+    const int exponent = a.col_exponent[column_index(a, x, l)];
+    const bool writes = x.n0 + l < a.N;
+#pragma unroll
+    for (int c = 0; c < C::kChunks; ++c) {
+      const int j0 = 32 * c + 16 * half, left = x.rows - j0;
+      if (left <= 0) continue;
+      int4 m = make_int4(0, 0, 0, 0);  // lane i holds what belongs to row i
+      if (lane < 16 && lane < left) m = a.meta[x.prow + j0 + lane];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        if (i >= left) continue;
+        const float v = times_power(sum[c][i], __shfl_sync(0xFFFFFFFFu, m.y, i) + exponent);
+        const int row = __shfl_sync(0xFFFFFFFFu, m.x, i);
+        if (writes && row >= 0)
+          static_cast<float*>(a.out)[static_cast<int64_t>(row) * a.N + x.n0 + l] = v;
       }
     }
   }
@@ -743,6 +815,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   k.step = gridDim.x;
   k.total = a.hdr->n_row_blocks * static_cast<uint32_t>(a.n_blocks);
   k.groups = static_cast<int>((a.K + kGroup - 1) / kGroup);
+  k.chain = a.out_f32 ? Cfg<SPLIT>::kChain : k.groups;
   if (threadIdx.x == 0) {
     for (int i = 0; i < kSlots; ++i) {
       ptx::mbar_init(&ctl->cfull[i], 1);
@@ -779,7 +852,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     unpacker<U, SPLIT>(smem, ctl, tmem, wg - 1, a, k);
   } else {
     more_registers<kWriteRegs>();
-    writer<SPLIT>(ctl, tmem, wg - 3, a, k);
+    if (a.out_f32)
+      writer_f32<SPLIT>(ctl, tmem, wg - 3, a, k);
+    else
+      writer<SPLIT>(ctl, tmem, wg - 3, a, k);
   }
   ptx::tc_fence_before_sync();
   __syncthreads();

@@ -61,3 +61,21 @@ def test_a_group_of_small_scales_by_itself(form, dtype, scales, zeros, down):  #
     x = s["x"].double()[s["gather"]].abs()
     more = torch.stack([x[i] @ off[int(s["pick"][i])].T for i in range(x.shape[0])])
     assert bool(((got.double() - y).abs() <= bound + more).all())
+
+
+@pytest.mark.parametrize("zeros,dtype,scales", [(False, "bf16", "bf16"), (True, "bf16", "fp32"),
+                                                (False, "fp16", "fp32"), (True, "fp16", "fp16")])
+@pytest.mark.parametrize("product", ["rows", "combined"])
+@pytest.mark.parametrize("K", [2048, 7168])
+def test_fp32_results_keep_fp32_bits(form, product, zeros, dtype, scales, K):  # noqa: F811
+    """Sums that are cut off at every step would lose more the longer they are. Where at most 64 steps
+    go into one, each off by u of it on average towards zero (2/3 of its last size on average), that is
+    43 u of the result, K / 1024 sums to add K / 1024 u; sums that are rounded K times are off by
+    0.58 u at each, at random: 0.58 sqrt(K / 2) u, 35 u."""
+    s = case(product, T=60, G=2, top_k=1, K=K, N=128, group=128, zeros=zeros, dtype=dtype,
+             scales=scales, out="fp32", seed=K)
+    got, ws = call(s)
+    y, _ = want(s)
+    assert pgg.status(ws) == 0
+    off = float((got.double() - y).square().mean().sqrt() / y.square().mean().sqrt())
+    assert off <= 50 * U, off / U
