@@ -40,7 +40,7 @@ def test_overlapping_outputs(grads, out, sizes, dtypes):
     ([], [], [], None),
 ])
 def test_what_is_allowed_passes_this_check(grads, out, sizes, dtypes):
-    # (without a GPU the call ends at the first question to the driver)
+    # (without a GPU the call ends where it asks for the device)
     import torch
     if torch.cuda.is_available():
         pytest.skip("the addresses are no tensors")
